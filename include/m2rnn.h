@@ -332,6 +332,123 @@ m2rnn_status m2rnn_forward_conv_bf16(const uint16_t* xq, const uint16_t* xk, con
                                      float* y, float* H_T, int B, int T, int N, int Nqk, int K,
                                      int V, void* stream);
 
+/*
+ * The selective state space block: what lies between its projections.  The linear
+ * counterpart of the M²RNN recurrence on the same tensors (the gate of Eq. (13)/(17) with
+ * the step size d_t in front of the outer product, no tanh and no W), with the short causal
+ * convolution in front of it and the gated group norm behind it, each for prompts, single
+ * tokens and training.  Not part of the notes' block; hybrid stacks (the notes' Sec. 5.2)
+ * alternate such layers with M²RNN layers.
+ *
+ * Strides.  Where an entry takes strides they are in elements; a token's channels (heads
+ * and their width) are contiguous, so slices of a wider projection or conv output can be
+ * passed without a copy.  All other tensors are dense.
+ *
+ * m2rnn_conv_silu_window_bf16: m2rnn_conv_silu_bf16 continuing an earlier call.
+ *   out[b,t,c] = SiLU(bias[c] + sum_{j=0..3} w[c][j] * X[b, t-3+j, c])
+ *   with X[b, -3..-1] = window_in[b] (NULL: zeros) and X[b, t >= 0] = x[b, t].
+ *   x [B, T, C] bf16 with strides (x_batch, x_token); window_in, window_out [B, 3, C] bf16:
+ *   the last three inputs, oldest first (window_out NULL: not written; window_out ==
+ *   window_in updates in place); out [B, T, C] bf16 dense; w [C, 4], bias [C] (or NULL)
+ *   float32.  T = 1 is the single-token form.  T = 0 copies the window.  Any C >= 1; rows
+ *   of C % 8 == 0 channels with every bf16 pointer and stride 16-byte aligned run on
+ *   16-byte accesses.
+ * m2rnn_conv_silu_backward_bf16: its gradients, given dout [B, T, C] bf16 (dense):
+ *   dx [B, T, C] bf16 (dense), dw [C, 4], dbias [C] float32 (NULL: not written),
+ *   dwindow [B, 3, C] bf16 (NULL: not written).  The workspace (16-byte aligned, at least
+ *   m2rnn_conv_silu_backward_workspace_bytes) holds partial sums, added in a fixed order.
+ */
+m2rnn_status m2rnn_conv_silu_window_bf16(const uint16_t* x, const float* w, const float* bias,
+                                         const uint16_t* window_in, uint16_t* out,
+                                         uint16_t* window_out, int B, int T, int C,
+                                         long long x_batch, long long x_token, void* stream);
+size_t m2rnn_conv_silu_backward_workspace_bytes(int B, int T, int C);
+m2rnn_status m2rnn_conv_silu_backward_bf16(const uint16_t* x, const float* w, const float* bias,
+                                           const uint16_t* window_in, const uint16_t* dout,
+                                           uint16_t* dx, float* dw, float* dbias,
+                                           uint16_t* dwindow, int B, int T, int C,
+                                           long long x_batch, long long x_token, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
+ * The selective scan.  For every (batch b, head n), with x_t = a_{t,n} + beta_n:
+ *   d_t = softplus(x_t),  f_t = exp(-alpha_n d_t)
+ *   H_t = f_t H_{t-1} + d_t k_t v_t^T,   y_t = H_t^T q_t + w_r ⊙ v_t
+ *   q, k  [B, T, Nqk, K] bf16, Nqk >= 1 dividing N: head n reads head n Nqk / N of q and k
+ *   v     [B, T, N, V], a [B, T, N] bf16;  alpha, beta [N], w_r [N, V] float32
+ *   H0, H_T [B, N, K, V] float32 (NULL: zeros / not written; H_T == H0 is allowed)
+ *   y     [B, T, N, V] bf16, dense
+ *   strides: eight values, (batch, token) of q, k, v and a in turn, or NULL for dense.
+ * 1 <= K, V <= 128 (UNSUPPORTED above), B, N >= 1, T >= 0.  a = -infinity makes a token
+ * inert (d = 0, f = 1); a token with a large enough a resets the state (f = 0).
+ * The state and every sum are float32; the operands of the tensor-core products are bf16.
+ * m2rnn_ssm_forward_bf16 with Hs != NULL also keeps what the backward reads:
+ *   Hs    m2rnn_ssm_states_bytes(...) bytes, 16-byte aligned: the state before every chunk
+ *         of 64 tokens and the final one, each value as the sum of two bf16 values.
+ * The workspace (16-byte aligned, at least m2rnn_ssm_workspace_bytes(..., 0) for the
+ * forward and (..., 1) for the backward; NULL where that is 0) is overwritten: calls in
+ * flight at once need one each.
+ */
+size_t m2rnn_ssm_states_bytes(int B, int T, int N, int K, int V);
+size_t m2rnn_ssm_workspace_bytes(int B, int T, int N, int Nqk, int K, int V, int backward);
+m2rnn_status m2rnn_ssm_forward_bf16(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                    const uint16_t* a, const float* alpha, const float* beta,
+                                    const float* w_r, const float* H0, uint16_t* y, float* H_T,
+                                    void* Hs, const long long* strides, int B, int T, int N,
+                                    int Nqk, int K, int V, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+/*
+ * Gradients of a loss through y (dy [B, T, N, V] bf16, dense) and H_T (dH_T [B, N, K, V]
+ * float32, NULL: zero), from the forward's inputs and its Hs.  With G the gradient of H_t,
+ * G_t = f_{t+1} G_{t+1} + q_t dy_t^T, and g_t = f_t <G_t, H_{t-1}>:
+ *   dq_t = H_t dy_t, dk_t = d_t G_t v_t, dv_t = d_t G_t^T k_t + w_r ⊙ dy_t,
+ *   da_t = sigmoid(x_t) (k_t^T G_t v_t - alpha g_t),
+ *   dalpha = -sum d_t g_t, dbeta = sum da_t, dw_r = sum dy_t ⊙ v_t, dH0 = f_1 G_1.
+ * dq, dk [B, T, Nqk, K] (summed over the heads that share them), dv [B, T, N, V],
+ * da [B, T, N]: bf16, dense; dalpha, dbeta [N], dw_r [N, V], dH0 [B, N, K, V] (NULL: not
+ * written): float32.  Sums run in a fixed order.
+ */
+m2rnn_status m2rnn_ssm_backward_bf16(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                     const uint16_t* a, const float* alpha, const float* beta,
+                                     const float* w_r, const void* Hs, const uint16_t* dy,
+                                     const float* dH_T, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+                                     uint16_t* da, float* dalpha, float* dbeta, float* dw_r,
+                                     float* dH0, const long long* strides, int B, int T, int N,
+                                     int Nqk, int K, int V, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+/*
+ * One token (T = 1): q, k [B, Nqk, K], v [B, N, V], a [B, N] bf16 dense, H_in, H_out
+ * [B, N, K, V] float32 (H_in NULL: zeros; H_out == H_in updates in place), y [B, N, V] bf16.
+ * fp32 arithmetic throughout.
+ */
+m2rnn_status m2rnn_ssm_step_bf16(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                 const uint16_t* a, const float* alpha, const float* beta,
+                                 const float* w_r, const float* H_in, float* H_out, uint16_t* y,
+                                 int B, int N, int Nqk, int K, int V, void* stream);
+
+/*
+ * Gated group norm over the channels of one token: each of `rows` rows of D values is cut
+ * into `groups` groups of E = D / groups consecutive channels,
+ *   n = (y - mean) / sqrt(var + eps)  (mean and biased variance of the group),
+ *   p = w ⊙ n + bias,   out = p ⊙ SiLU(g_pre), or SiLU(p) where g_pre is NULL.
+ * y [rows, D] float32 (y_f32 != 0) or bf16; g_pre, out bf16; w, bias [D] float32 (bias
+ * NULL: none).  E <= 8192 (UNSUPPORTED above; INVALID_ARG where groups does not divide D
+ * or eps < 0).  A group is read once and kept in registers; E % 8 == 0 with 16-byte aligned
+ * pointers runs on 16-byte accesses.
+ * Backward: dout bf16 -> dy (of y's type), dg_pre bf16 (with g_pre), dw, dbias [D] float32
+ * (dbias NULL: not written), with a workspace for partial sums added in a fixed order.
+ */
+m2rnn_status m2rnn_gate_groupnorm(const void* y, int y_f32, const uint16_t* g_pre, const float* w,
+                                  const float* bias, float eps, uint16_t* out, long long rows,
+                                  int D, int groups, void* stream);
+size_t m2rnn_gate_groupnorm_backward_workspace_bytes(long long rows, int D, int groups);
+m2rnn_status m2rnn_gate_groupnorm_backward(const void* y, int y_f32, const uint16_t* g_pre,
+                                           const float* w, const float* bias, float eps,
+                                           const uint16_t* dout, void* dy, uint16_t* dg_pre,
+                                           float* dw, float* dbias, long long rows, int D,
+                                           int groups, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
 /* Name of a bf16 kernel variant (NULL for an unknown id).  Id 0 is "auto". */
 const char* m2rnn_variant_name(int variant);
 

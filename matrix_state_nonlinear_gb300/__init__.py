@@ -9,3 +9,6 @@ from .m2rnn import (M2RNNError, backward_workspace_bytes, conv_silu, gate_rmsnor
                     pick_variant,
                     status_string, stream_status, variant_name, variant_supports,
                     version)
+from .ssm import (conv_silu_backward, conv_silu_step, conv_silu_window, gate_groupnorm,  # noqa: F401
+                  gate_groupnorm_backward, ssm_backward, ssm_forward, ssm_forward_train,
+                  ssm_states_bytes, ssm_step, ssm_workspace_bytes)

@@ -1,0 +1,123 @@
+// m2rnn_ssm_step.cu — one token of the selective scan, state in and out.
+//
+//   H' = f H + d k v^T,  y = H'^T q + w_r ⊙ v
+//
+// Bound by the state's traffic, 8 K V bytes per (request, head), at about 5 operations for every
+// value.  One block per pair: a thread owns kVec neighbouring columns of every kRowsAt-th row
+// and loads all of its rows before it computes (kDepth 16-byte loads in flight per thread); the
+// readout is summed in registers, then over the row groups in shared memory in a fixed order.
+#include "m2rnn_ssm.h"
+#include "ptx_util.cuh"
+
+namespace m2rnn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxDim = 128;
+
+template <int VEC>
+struct Cols {
+  float c[VEC];
+};
+
+template <int VEC, int DEPTH>
+__global__ void __launch_bounds__(kThreads)
+    ssm_step_kernel(const uint16_t* __restrict__ q, const uint16_t* __restrict__ k,
+                    const uint16_t* __restrict__ v, const uint16_t* __restrict__ a,
+                    const float* __restrict__ alpha, const float* __restrict__ beta,
+                    const float* __restrict__ w_r, const float* H_in, float* H_out,
+                    uint16_t* __restrict__ y, int N, int Nqk, int K, int V, int lanes) {
+  __shared__ float sk[kMaxDim], sq[kMaxDim];
+  __shared__ float part[kThreads * VEC];
+  const long long pair = blockIdx.x;
+  const int n = (int)(pair % N);
+  const long long b = pair / N;
+  const long long qk = (b * Nqk + (long long)n * Nqk / N) * K;
+  const int col = (threadIdx.x % lanes) * VEC;  // lanes threads side by side cover the columns
+  const int row0 = threadIdx.x / lanes, rows_at = kThreads / lanes;
+  const bool live = col < V;
+  const float* hin = H_in ? H_in + pair * K * V + col : nullptr;
+  float* hout = H_out + pair * K * V + col;
+  Cols<VEC> h[DEPTH];
+#pragma unroll
+  for (int r = 0; r < DEPTH; ++r) {
+    const int i = row0 + r * rows_at;
+    if (live && i < K && hin) {
+      if constexpr (VEC == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(hin + (size_t)i * V);
+        h[r].c[0] = u.x, h[r].c[1] = u.y, h[r].c[2] = u.z, h[r].c[3] = u.w;
+      } else {
+        h[r].c[0] = hin[(size_t)i * V];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) h[r].c[j] = 0.f;
+    }
+  }
+  const float2 gate = ssm_gate(bf16_to_f(a[pair]), alpha[n], beta[n]);
+  const float d = gate.x, f = expf(gate.y);
+  for (int i = threadIdx.x; i < K; i += kThreads) {
+    sk[i] = d * bf16_to_f(k[qk + i]);
+    sq[i] = bf16_to_f(q[qk + i]);
+  }
+  float vv[VEC], acc[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    vv[j] = live ? bf16_to_f(v[pair * V + col + j]) : 0.f;
+    acc[j] = 0.f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < DEPTH; ++r) {
+    const int i = row0 + r * rows_at;
+    if (!live || i >= K) break;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      h[r].c[j] = fmaf(f, h[r].c[j], sk[i] * vv[j]);
+      acc[j] = fmaf(h[r].c[j], sq[i], acc[j]);
+    }
+    if constexpr (VEC == 4)
+      *reinterpret_cast<float4*>(hout + (size_t)i * V) =
+          make_float4(h[r].c[0], h[r].c[1], h[r].c[2], h[r].c[3]);
+    else
+      hout[(size_t)i * V] = h[r].c[0];
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) part[j * kThreads + threadIdx.x] = acc[j];
+  __syncthreads();
+  // Column c of the readout: thread c % VEC's share of the lane c / VEC, over the row groups.
+  for (int c = threadIdx.x; c < V; c += kThreads) {
+    const float* s = part + (c % VEC) * kThreads + c / VEC;
+    float sum = 0.f;
+    for (int g = 0; g < rows_at; ++g) sum += s[g * lanes];
+    y[pair * V + c] = f_to_bf16(fmaf(w_r[(size_t)n * V + c], bf16_to_f(v[pair * V + c]), sum));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_step(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                            const uint16_t* a, const float* alpha, const float* beta,
+                            const float* w_r, const float* H_in, float* H_out, uint16_t* y, int B,
+                            int N, int Nqk, int K, int V, cudaStream_t stream) {
+  const bool vec = V % 4 == 0 && aligned_to(H_in, 16) && aligned_to(H_out, 16);
+  const int chunks = vec ? V / 4 : V;
+  int lanes = 1;
+  while (lanes < chunks) lanes *= 2;
+  const int depth = (K * lanes + kThreads - 1) / kThreads;  // rows per thread
+  const unsigned blocks = (unsigned)((long long)B * N);
+  auto run = [&](auto kernel) {
+    kernel<<<blocks, kThreads, 0, stream>>>(q, k, v, a, alpha, beta, w_r, H_in, H_out, y, N, Nqk, K,
+                                            V, lanes);
+    return cudaGetLastError();
+  };
+  if (vec) {
+    if (depth <= 4) return run(ssm_step_kernel<4, 4>);
+    if (depth <= 8) return run(ssm_step_kernel<4, 8>);
+    return run(ssm_step_kernel<4, 16>);
+  }
+  if (depth <= 16) return run(ssm_step_kernel<1, 16>);
+  return run(ssm_step_kernel<1, 64>);
+}
+
+}  // namespace m2rnn

@@ -20,6 +20,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT = 0, 1, 2, 3, 4
 # Exported symbols of include/m2rnn.h, with (restype, argtypes).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
 SYMBOLS = {
     "m2rnn_forward_f32": (_I, [_P] * 11 + [_I] * 5 + [_P]),
     "m2rnn_forward_bf16": (_I, [_P] * 11 + [_I] * 5 + [_P]),
@@ -46,6 +47,19 @@ SYMBOLS = {
     "m2rnn_conv_silu_bf16": (_I, [_P] * 4 + [_I] * 3 + [_P]),
     "m2rnn_forward_conv_bf16": (_I, [_P] * 17 + [_I] * 6 + [_P]),
     "m2rnn_gate_rmsnorm_bf16": (_I, [_P] * 3 + [ctypes.c_float, _P, ctypes.c_longlong, _I, _P]),
+    "m2rnn_conv_silu_window_bf16": (_I, [_P] * 6 + [_I] * 3 + [_L] * 2 + [_P]),
+    "m2rnn_conv_silu_backward_workspace_bytes": (ctypes.c_size_t, [_I] * 3),
+    "m2rnn_conv_silu_backward_bf16": (_I, [_P] * 9 + [_I] * 3 + [_L] * 2
+                                      + [_P, ctypes.c_size_t, _P]),
+    "m2rnn_ssm_states_bytes": (ctypes.c_size_t, [_I] * 5),
+    "m2rnn_ssm_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
+    "m2rnn_ssm_forward_bf16": (_I, [_P] * 12 + [_I] * 6 + [_P, ctypes.c_size_t, _P]),
+    "m2rnn_ssm_backward_bf16": (_I, [_P] * 19 + [_I] * 6 + [_P, ctypes.c_size_t, _P]),
+    "m2rnn_ssm_step_bf16": (_I, [_P] * 10 + [_I] * 5 + [_P]),
+    "m2rnn_gate_groupnorm": (_I, [_P, _I] + [_P] * 3 + [ctypes.c_float, _P, _L, _I, _I, _P]),
+    "m2rnn_gate_groupnorm_backward_workspace_bytes": (ctypes.c_size_t, [_L, _I, _I]),
+    "m2rnn_gate_groupnorm_backward": (_I, [_P, _I] + [_P] * 3 + [ctypes.c_float] + [_P] * 5
+                                      + [_L, _I, _I, _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
