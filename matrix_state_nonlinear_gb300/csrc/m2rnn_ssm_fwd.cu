@@ -40,6 +40,9 @@ struct alignas(16) Gates {  // of one chunk, per token; read in pairs
   float wk[L];    // d times the decay from the token to the chunk's end
   float total;    // log2 of the whole chunk's decay
 };
+struct alignas(16) Row {
+  float w_r[VT];
+};
 
 template <int KP, bool STATES_ONLY>
 struct Smem {
@@ -50,7 +53,8 @@ struct Smem {
   static constexpr int kH = STATES_ONLY ? 0 : KP * VT * 2;  // the state as bf16, two buffers
   static constexpr int kY = STATES_ONLY || KP >= 64 ? 0 : L * VT * 2;  // y on its way out
   static constexpr int kGates = 2 * kStage + 2 * kH + kY;
-  static constexpr int kBytes = kGates + 2 * (int)sizeof(Gates);
+  static constexpr int kRow = kGates + 2 * (int)sizeof(Gates);
+  static constexpr int kBytes = kRow + (int)sizeof(Row);
   static_assert(kGates % 16 == 0 && sizeof(Gates) % 16 == 0, "pairs of gates are read at once");
 };
 
@@ -75,9 +79,6 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
   const int v0 = vt * VT, vw = min(VT, p.V - v0);  // this block's columns
   const int rb = (warp + blockIdx.x + blockIdx.y) & 3;  // this warp's 16 tokens of y
 
-  const uint16_t* qg = p.q + b * p.sq.batch + (long long)head * p.K;
-  const uint16_t* kg = p.k + b * p.sk.batch + (long long)head * p.K;
-  const uint16_t* vg = p.v + b * p.sv.batch + (long long)n * p.V + v0;
   const uint16_t* ag = p.a + b * p.sa.batch + n;
   const float alpha = p.alpha[n], beta = p.beta[n];
 
@@ -85,15 +86,23 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
   auto tile_k = [&](int s) { return base + s * S::kStage + S::kQ; };
   auto tile_v = [&](int s) { return base + s * S::kStage + S::kQ + S::kK; };
   auto tile_h = [&](int s) { return base + 2 * S::kStage + s * S::kH; };
+  TileLoader<KP, L, kThreads> load_q, load_k;
+  TileLoader<VT, L, kThreads> load_v;
+  if constexpr (!STATES_ONLY) load_q.init(p.q + b * p.sq.batch + (long long)head * p.K, p.sq.token, p.K, tid);
+  load_k.init(p.k + b * p.sk.batch + (long long)head * p.K, p.sk.token, p.K, tid);
+  load_v.init(p.v + b * p.sv.batch + (long long)n * p.V + v0, p.sv.token, vw, tid);
   auto load_chunk = [&](int chunk, int s) {
     const long long t0 = (long long)chunk * L;
     const int rows = min(L, p.T - chunk * L);
-    if constexpr (!STATES_ONLY)
-      load_tile<KP, L, kThreads>(tile_q(s), qg + t0 * p.sq.token, p.sq.token, rows, p.K, vec, tid);
-    load_tile<KP, L, kThreads>(tile_k(s), kg + t0 * p.sk.token, p.sk.token, rows, p.K, vec, tid);
-    load_tile<VT, L, kThreads>(tile_v(s), vg + t0 * p.sv.token, p.sv.token, rows, vw, vec, tid);
+    if constexpr (!STATES_ONLY) load_q.load(tile_q(s), t0, rows, vec, tid);
+    load_k.load(tile_k(s), t0, rows, vec, tid);
+    load_v.load(tile_v(s), t0, rows, vec, tid);
     cp_async_commit();
   };
+  const uint32_t part_k_down = lane_part<KP>(lane, true), part_k_across = lane_part<KP>(lane, false);
+  const uint32_t part_v_down = lane_part<VT>(lane, true);
+  float* wr = reinterpret_cast<Row*>(smem + S::kRow)->w_r;
+  if (!STATES_ONLY && tid < VT) wr[tid] = tid < vw ? p.w_r[(size_t)n * p.V + v0 + tid] : 0.f;
   // The gate logits of a chunk (tokens lane, lane + 32) and what the products need of them.
   auto load_logits = [&](int chunk) {
     const int t = chunk * L + lane;
@@ -146,11 +155,11 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = (m0 + m) * 16 + g + r * 8, chunk16 = nt0 + j;
-          uint32_t hi, lo;
-          split_bf16x2(H[m][j][2 * r], H[m][j][2 * r + 1], hi, lo);
+          const uint32_t hi = pack_bf16x2(H[m][j][2 * r], H[m][j][2 * r + 1]);
           st_shared_u32(Tile<VT>::at(tile_h(s), row, chunk16) + c2 * 2, hi);
           const int col = chunk16 * 8 + c2;
           if (kept && row < p.K && col < vw) {
+            const uint32_t lo = pack_bf16x2(H[m][j][2 * r] - bf16_lo(hi), H[m][j][2 * r + 1] - bf16_hi(hi));
             uint16_t* at = kept + (size_t)row * p.V + v0 + col;
             const size_t plane = (size_t)p.K * p.V;
             if ((p.V & 1) == 0) {
@@ -194,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
         for (int e = 0; e < 4; ++e) y[i][e] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < KP / 16; ++kk) {
-        frag_a<KP>(qa[kk], tile_q(s), rb * 16, kk * 2, lane);
+        ldsm_x4(qa[kk], frag_at<KP>(tile_q(s), part_k_down, rb * 16, kk * 2));
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
           uint32_t h[4];
-          frag_bk<VT>(h, tile_h(s), kk * 16, np * 2, lane);
+          ldsm_x4_trans(h, frag_at<VT>(tile_h(s), part_v_down, kk * 16, np * 2));
           mma_bf16_16816(y[2 * np], qa[kk], h[0], h[1]);
           mma_bf16_16816(y[2 * np + 1], qa[kk], h[2], h[3]);
         }
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
     for (int j = 0; j < 4; ++j) {  // 16 tokens s at a time
       uint32_t vf[4][4];
 #pragma unroll
-      for (int np = 0; np < 4; ++np) frag_bk<VT>(vf[np], tile_v(s), j * 16, np * 2, lane);
+      for (int np = 0; np < 4; ++np) ldsm_x4_trans(vf[np], frag_at<VT>(tile_v(s), part_v_down, j * 16, np * 2));
       if constexpr (!STATES_ONLY) {
         if (j <= rb) {
           float sc[2][4];
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
 #pragma unroll
           for (int kk = 0; kk < KP / 16; ++kk) {
             uint32_t kf[4];
-            frag_bn<KP>(kf, tile_k(s), j * 16, kk * 2, lane);
+            ldsm_x4(kf, frag_at<KP>(tile_k(s), part_k_across, j * 16, kk * 2));
             mma_bf16_16816(sc[0], qa[kk], kf[0], kf[1]);
             mma_bf16_16816(sc[1], qa[kk], kf[2], kf[3]);
           }
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         uint32_t kf[4], hi[4], lo[4];
-        frag_at<KP>(kf, tile_k(s), j * 16, (m0 + m) * 2, lane);
+        ldsm_x4_trans(kf, frag_at<KP>(tile_k(s), part_k_across, j * 16, (m0 + m) * 2));
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float2 w = r < 2 ? w0 : w1;
@@ -303,14 +312,12 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int col = i * 8 + c2;
-        float2 wr;
-        wr.x = col < vw ? p.w_r[(size_t)n * p.V + v0 + col] : 0.f;
-        wr.y = col + 1 < vw ? p.w_r[(size_t)n * p.V + v0 + col + 1] : 0.f;
+        const float2 w = *reinterpret_cast<const float2*>(wr + col);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t v = ld_shared_u32(Tile<VT>::at(tile_v(s), rb * 16 + g + r * 8, i) + c2 * 2);
           st_shared_u32(Tile<VT>::at(out, g + r * 8, i) + c2 * 2,
-                        pack_bf16x2(fmaf(wr.x, bf16_lo(v), y[i][2 * r]), fmaf(wr.y, bf16_hi(v), y[i][2 * r + 1])));
+                        pack_bf16x2(fmaf(w.x, bf16_lo(v), y[i][2 * r]), fmaf(w.y, bf16_hi(v), y[i][2 * r + 1])));
         }
       }
       __syncwarp();
@@ -363,24 +370,34 @@ __global__ void __launch_bounds__(256)
   if (i >= kv) return;
   float h = H0 ? H0[(size_t)pair * kv + i] : 0.f;
   float* s = seg_state + (size_t)pair * segments * kv + i;
-  for (int j = 0; j < segments; ++j) {
-    const float own = j + 1 < segments ? s[(size_t)j * kv] : 0.f;
-    s[(size_t)j * kv] = h;
-    if (j + 1 < segments) h = fmaf(exp2_approx(seg_decay[pair * segments + j]), h, own);
+  constexpr int kAhead = 8;  // segments loaded at once
+  for (int j = 0; j < segments; j += kAhead) {
+    float own[kAhead], decay[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (j + u + 1 < segments) {
+        own[u] = s[(size_t)(j + u) * kv];
+        decay[u] = seg_decay[pair * segments + j + u];
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (j + u < segments) s[(size_t)(j + u) * kv] = h;
+      if (j + u + 1 < segments) h = fmaf(exp2_approx(decay[u]), h, own[u]);
+    }
   }
 }
 
 int blocks_per_sm(int K) { return K <= 64 ? 3 : 2; }
 
-// Segments so that about two waves of blocks run where the pairs alone are fewer than a wave;
-// every segment of at least four chunks.
+// Segments so that at most two full waves of blocks run where the pairs alone are fewer than a
+// wave; every segment of at least four chunks.
 Cut cut_of(int B, int T, int N, int K, int V) {
   const long long units = (long long)B * N * ((V + VT - 1) / VT);
   const long long slots = 152LL * blocks_per_sm(K);
   const int chunks = ssm_chunks(T);
   Cut c{1, chunks > 0 ? chunks : 1};
   if (units >= slots || chunks < 8) return c;
-  long long want = (2 * slots + units - 1) / units;
+  long long want = 2 * slots / units;
   if (want > chunks / 4) want = chunks / 4;
   if (want > 1024) want = 1024;
   if (want < 2) return c;

@@ -54,53 +54,67 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Starts the load of `rows` rows (of ROWS; the rest become zeros) of `width` values each, row r
-// at src + r * stride, into a tile.  With `vec` (width % 8 == 0, 16-byte aligned rows) it is
-// asynchronous; otherwise value by value, complete at the next block barrier.
+// Loads tiles of ROWS rows of `width` values (the rest become zeros), row r at src + r * stride.
+// With `vec` (width % 8 == 0, 16-byte aligned rows) the load is asynchronous; otherwise value by
+// value, complete at the next block barrier.
 template <int COLS, int ROWS, int THREADS>
-__device__ __forceinline__ void load_tile(uint32_t tile, const uint16_t* src, long long stride, int rows,
-                                          int width, bool vec, int tid) {
-  constexpr int kChunks = Tile<COLS>::kChunks;
-  if (vec) {
+struct TileLoader {
+  static constexpr int kChunks = Tile<COLS>::kChunks;
+  static constexpr int kStep = THREADS / kChunks;  // rows between a thread's pieces
+  static constexpr int kPieces = (ROWS + kStep - 1) / kStep;
+  static_assert(THREADS % kChunks == 0 && (kStep % 8 == 0 || kPieces == 1), "the same place in every row");
+  const uint16_t *base, *src;  // row 0 of the sequence, and this thread's first piece
+  long long stride;
+  int row, width, col;
+  uint32_t place;
+  __device__ __forceinline__ void init(const uint16_t* base_, long long stride_, int width_, int tid) {
+    base = base_, stride = stride_, width = width_;
+    const int chunk = tid % kChunks;
+    row = tid / kChunks, col = chunk * 8;
+    place = Tile<COLS>::at(0, row, chunk);
+    src = base + row * stride + col;
+  }
+  // Rows [t0, t0 + rows) of the sequence.
+  __device__ __forceinline__ void load(uint32_t tile, long long t0, int rows, bool vec, int tid) const {
+    if (vec) {
+      const uint16_t* s = src + t0 * stride;
+      const int most = col < width ? rows : 0;
 #pragma unroll
-    for (int i = 0; i < (ROWS * kChunks + THREADS - 1) / THREADS; ++i) {
-      const int id = tid + i * THREADS;
-      if (ROWS * kChunks % THREADS != 0 && id >= ROWS * kChunks) break;
-      const int row = id / kChunks, chunk = id % kChunks;
-      const bool live = row < rows && chunk * 8 < width;
-      cp_async16(Tile<COLS>::at(tile, row, chunk), live ? src + row * stride + chunk * 8 : src, live);
-    }
-  } else {
-    for (int id = tid; id < ROWS * COLS; id += THREADS) {
-      const int row = id / COLS, col = id % COLS;
-      const uint16_t u = row < rows && col < width ? src[row * stride + col] : (uint16_t)0;
-      st_shared_u16(Tile<COLS>::at(tile, row, col >> 3) + (col & 7) * 2, u);
+      for (int i = 0; i < kPieces; ++i) {
+        if (ROWS % kStep != 0 && row + i * kStep >= ROWS) break;
+        const bool live = row + i * kStep < most;
+        cp_async16(tile + place + i * kStep * Tile<COLS>::kRowBytes, live ? s : base, live);
+        s += kStep * stride;
+      }
+    } else {
+      const uint16_t* s = base + t0 * stride;
+      for (int id = tid; id < ROWS * COLS; id += THREADS) {
+        const int r = id / COLS, c = id % COLS;
+        const uint16_t u = r < rows && c < width ? s[r * stride + c] : (uint16_t)0;
+        st_shared_u16(Tile<COLS>::at(tile, r, c >> 3) + (c & 7) * 2, u);
+      }
     }
   }
-}
+};
 
-// A operand (16 x 16): rows row0.., columns 8 chunk0.. of a tile.
+// A lane's part of the address of an ldmatrix of four 8 x 8 tiles, two down and two across a
+// tile: `down` orders them down first, else across first.  A fragment at row row0 (a multiple
+// of 8) and chunk chunk0 (even) is at tile + row0 * kRowBytes + (part ^ chunk0 * 16).
 template <int COLS>
-__device__ __forceinline__ void frag_a(uint32_t (&r)[4], uint32_t tile, int row0, int chunk0, int lane) {
-  ldsm_x4(r, Tile<COLS>::at(tile, row0 + (lane & 15), chunk0 + (lane >> 4)));
+__device__ __forceinline__ uint32_t lane_part(int lane, bool down) {
+  return down ? Tile<COLS>::at(0, lane & 15, lane >> 4)
+              : Tile<COLS>::at(0, (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
 }
-// A operand (16 x 16) of the transposed tile: A's rows are columns 8 chunk0.., its columns rows row0..
 template <int COLS>
-__device__ __forceinline__ void frag_at(uint32_t (&r)[4], uint32_t tile, int row0, int chunk0, int lane) {
-  ldsm_x4_trans(r, Tile<COLS>::at(tile, row0 + (lane & 7) + ((lane >> 4) << 3), chunk0 + ((lane >> 3) & 1)));
+__device__ __forceinline__ uint32_t frag_at(uint32_t tile, uint32_t part, int row0, int chunk0) {
+  return tile + row0 * Tile<COLS>::kRowBytes + (part ^ (chunk0 << 4));
 }
-// Two B operands (16 x 8 each) of X^T: B's columns are the tile's rows row0..+15 (n), its rows the
-// tile's columns 8 chunk0..+15 (k).  r[0], r[1]: the first 8 columns; r[2], r[3]: the next 8.
-template <int COLS>
-__device__ __forceinline__ void frag_bn(uint32_t (&r)[4], uint32_t tile, int row0, int chunk0, int lane) {
-  ldsm_x4(r, Tile<COLS>::at(tile, row0 + (lane & 7) + ((lane >> 4) << 3), chunk0 + ((lane >> 3) & 1)));
-}
-// Two B operands (16 x 8 each) of X: B's rows are the tile's rows row0..+15 (k), its columns the
-// tile's columns 8 chunk0..+15 (n).
-template <int COLS>
-__device__ __forceinline__ void frag_bk(uint32_t (&r)[4], uint32_t tile, int row0, int chunk0, int lane) {
-  ldsm_x4_trans(r, Tile<COLS>::at(tile, row0 + (lane & 15), chunk0 + (lane >> 4)));
-}
+// The fragments of m16n8k16 at such an address:
+//   A (16 x 16), rows by columns of the tile:                      ldsm_x4,       part down
+//   A of the transposed tile (A's rows are the tile's columns):    ldsm_x4_trans, part across
+//   two B (16 x 8) of the tile, k its rows, n its columns:         ldsm_x4_trans, part down
+//   two B of the transposed tile, k its columns, n its rows:       ldsm_x4,       part across
+// Of two B fragments r[0], r[1] are the first 8 columns (n), r[2], r[3] the next 8.
 
 // (x, y) as bf16 pairs hi + lo: hi is the rounding to bf16, lo that of the remainder, so that
 // hi + lo is within 2^-17 of each value (2^-18 of its binade) and two bf16 products give nearly
