@@ -9,7 +9,8 @@
 
 namespace m2rnn {
 
-constexpr int kSsmChunk = 64;  // tokens per chunk of the scan
+constexpr int kSsmChunk = 64;    // tokens per chunk of the scan
+constexpr int kSsmColumns = 64;  // value columns per block of the scan
 
 // Batch and token strides of one bf16 operand, in elements.
 struct Strides {
@@ -41,6 +42,28 @@ struct SsmBackwardProblem {
 };
 
 __host__ __device__ inline int ssm_chunks(int T) { return (T + kSsmChunk - 1) / kSsmChunk; }
+
+// How a pair's chunks are cut: `segments` of `per` chunks, side by side in the main launch, and
+// each into `fine` pieces of `piece` chunks for the launch that finds their starting states.
+struct SsmCut {
+  int segments, per, fine, piece;
+};
+SsmCut ssm_cut(int B, int T, int N, int V);
+int ssm_pieces(const SsmCut& c, int T);
+size_t ssm_segment_floats(const SsmCut& c, int B, int T, int N, int K, int V);
+struct SegmentProblem {
+  const uint16_t *x, *y;  // k and v, or q and dy
+  const uint16_t* a;
+  const float *alpha, *beta;
+  const float* start;  // the first state (the last state's gradient), or null
+  Strides sx, sy, sa;
+  int B, T, N, Nqk, K, V;
+  float* state;  // [pairs][pieces][K][V], then [pairs][pieces]: ssm_segment_floats
+  int pieces;    // set by the launch, as is decay
+  float* decay;
+};
+cudaError_t launch_ssm_segments(SegmentProblem p, const SsmCut& c, bool reverse, bool vec,
+                                cudaStream_t stream);
 
 size_t ssm_forward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V);
 size_t ssm_backward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V);
@@ -88,6 +111,10 @@ cudaError_t launch_sum_rows(const float* src, float* dst0, float* dst1, int coun
 
 inline bool aligned_to(const void* p, uintptr_t n) {
   return (reinterpret_cast<uintptr_t>(p) % n) == 0;
+}
+// Rows of `width` bf16 values that can be read 16 bytes at a time.
+inline bool rows_of_16(const void* p, const Strides& s, int width) {
+  return width % 8 == 0 && s.batch % 8 == 0 && s.token % 8 == 0 && aligned_to(p, 16);
 }
 
 #ifdef __CUDACC__

@@ -119,9 +119,10 @@ __device__ __forceinline__ uint32_t frag_at(uint32_t tile, uint32_t part, int ro
 // (x, y) as bf16 pairs hi + lo: hi is the rounding to bf16, lo that of the remainder, so that
 // hi + lo is within 2^-17 of each value (2^-18 of its binade) and two bf16 products give nearly
 // a float32 one.
-__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf16_lo(hi), y - bf16_hi(hi));
+__device__ __forceinline__ void split_bf16x2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  const float2 r = sub2(x, bf16x2_to_float2(hi));
+  lo = pack_bf16x2(r.x, r.y);
 }
 
 // The gates of a chunk's 64 tokens, by one warp (lane l has tokens l and l + 32), from their d
@@ -153,5 +154,60 @@ __device__ __forceinline__ ChunkSums chunk_sums(float l0, float l1, int lane) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// A state (or its gradient) of KP x VT float32 values over the accumulators of four warps: MT
+// tiles of 16 rows by NT tiles of 8 columns each.  A warp of a state with fewer than four row
+// tiles takes some of the columns.
+template <int KP, int VT>
+struct StateTiles {
+  static constexpr int kRowTiles = KP / 16;
+  static constexpr bool kSplit = kRowTiles < 4;
+  static constexpr int MT = kSplit ? 1 : kRowTiles / 4;
+  static constexpr int NT = kSplit ? VT / 8 * kRowTiles / 4 : VT / 8;
+  __device__ static int row_tile(int warp) { return kSplit ? warp % kRowTiles : warp * MT; }
+  __device__ static int col_tile(int warp) { return kSplit ? warp / kRowTiles * NT : 0; }
+};
+
+template <typename T>
+__device__ __forceinline__ void scale_state(float (&H)[T::MT][T::NT][4], float f) {
+  const float2 f2 = make_float2(f, f);
+#pragma unroll
+  for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+    for (int j = 0; j < T::NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 h = mul2(make_float2(H[m][j][2 * r], H[m][j][2 * r + 1]), f2);
+        H[m][j][2 * r] = h.x, H[m][j][2 * r + 1] = h.y;
+      }
+}
+
+// H += sum over the 16 tokens t of block j of (w[t] x_t) y_t^T: x from its tile [token][KP], y as
+// the B fragments of those tokens.  w x is split into two bf16 values.
+template <int KP, typename T>
+__device__ __forceinline__ void add_outer(float (&H)[T::MT][T::NT][4], uint32_t tile_x, uint32_t part_x,
+                                          const float* w, const uint32_t (&yf)[4][4], int j, int m0, int nt0,
+                                          int c2) {
+  const float2 w0 = *reinterpret_cast<const float2*>(w + j * 16 + c2);
+  const float2 w1 = *reinterpret_cast<const float2*>(w + j * 16 + 8 + c2);
+#pragma unroll
+  for (int m = 0; m < T::MT; ++m) {
+    uint32_t xf[4], hi[4], lo[4];
+    ldsm_x4_trans(xf, frag_at<KP>(tile_x, part_x, j * 16, (m0 + m) * 2));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) split_bf16x2(mul2(bf16x2_to_float2(xf[r]), r < 2 ? w0 : w1), hi[r], lo[r]);
+#pragma unroll
+    for (int i = 0; i < T::NT; ++i) {
+      uint32_t b0 = yf[i >> 1][(i & 1) * 2], b1 = yf[i >> 1][(i & 1) * 2 + 1];
+      if constexpr (T::kSplit) {  // column tile nt0 + i, chosen without indexing registers
+#pragma unroll
+        for (int o = 0; o < 8; ++o)
+          if (o == nt0 + i) b0 = yf[o >> 1][(o & 1) * 2], b1 = yf[o >> 1][(o & 1) * 2 + 1];
+      }
+      mma_bf16_16816(H[m][i], hi, b0, b1);
+      mma_bf16_16816(H[m][i], lo, b0, b1);
+    }
+  }
+}
 
 }  // namespace m2rnn
