@@ -384,7 +384,7 @@ m2rnn_status m2rnn_conv_silu_backward_bf16(const uint16_t* x, const float* w, co
  * The state and every sum are float32; the operands of the tensor-core products are bf16.
  * m2rnn_ssm_forward_bf16 with Hs != NULL also keeps what the backward reads:
  *   Hs    m2rnn_ssm_states_bytes(...) bytes, 16-byte aligned: the state before every chunk
- *         of 64 tokens and the final one, each value as the sum of two bf16 values.
+ *         of 128 tokens and the final one, each value as the sum of two bf16 values.
  * The workspace (16-byte aligned, at least m2rnn_ssm_workspace_bytes(..., 0) for the
  * forward and (..., 1) for the backward; NULL where that is 0) is overwritten: calls in
  * flight at once need one each.

@@ -5,6 +5,7 @@
 
 #include "../../include/m2rnn.h"
 #include "m2rnn_internal.h"
+#include "m2rnn_ssm.h"
 
 namespace m2rnn {
 
@@ -34,6 +35,15 @@ int* status_address(int dev) {
   if (have_id || current_context_id(&id)) cache[dev] = Entry{id, static_cast<int*>(p)};
   return static_cast<int*>(p);
 }
+
+}  // namespace
+
+int* device_status() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? status_address(dev) : nullptr;
+}
+
+namespace {
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;

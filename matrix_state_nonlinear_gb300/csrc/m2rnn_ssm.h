@@ -9,13 +9,16 @@
 
 namespace m2rnn {
 
-constexpr int kSsmChunk = 64;    // tokens per chunk of the scan
+constexpr int kSsmChunk = 128;   // tokens per chunk of the scan
 constexpr int kSsmColumns = 64;  // value columns per block of the scan
 
 // Batch and token strides of one bf16 operand, in elements.
 struct Strides {
   long long batch, token;
 };
+
+// Device address of the current device's status word (m2rnn_stream_status), or null.
+int* device_status();
 
 struct SsmProblem {
   const uint16_t *q, *k, *v, *a;
@@ -26,6 +29,7 @@ struct SsmProblem {
   Strides sq, sk, sv, sa;
   int B, T, N, Nqk, K, V;
   float* ws;
+  int* status;
 };
 
 struct SsmBackwardProblem {
@@ -39,6 +43,7 @@ struct SsmBackwardProblem {
   Strides sq, sk, sv, sa;
   int B, T, N, Nqk, K, V;
   float* ws;
+  int* status;
 };
 
 __host__ __device__ inline int ssm_chunks(int T) { return (T + kSsmChunk - 1) / kSsmChunk; }

@@ -95,8 +95,10 @@ m2rnn_status m2rnn_ssm_forward_bf16(const uint16_t* q, const uint16_t* k, const 
   if (!aligned_to(workspace, 16) || !aligned_to(Hs, 16) || !aligned_to(H0, 4) ||
       !aligned_to(H_T, 4))
     return M2RNN_ERR_INVALID_ARG;
+  int* status = device_status();
+  if (!status) return M2RNN_ERR_CUDA;
   const SsmProblem p{q,    k,    v,    a,    alpha, beta, w_r, H0,  y, H_T, static_cast<uint16_t*>(Hs),
-                     s[0], s[1], s[2], s[3], B,     T,    N,   Nqk, K, V,   static_cast<float*>(workspace)};
+                     s[0], s[1], s[2], s[3], B,     T,    N,   Nqk, K, V,   static_cast<float*>(workspace), status};
   return done(launch_ssm_forward(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -120,9 +122,11 @@ m2rnn_status m2rnn_ssm_backward_bf16(const uint16_t* q, const uint16_t* k, const
   if (!aligned_to(workspace, 16) || !aligned_to(Hs, 16) || !aligned_to(dH_T, 4) ||
       !aligned_to(dH0, 4))
     return M2RNN_ERR_INVALID_ARG;
+  int* status = device_status();
+  if (!status) return M2RNN_ERR_CUDA;
   const SsmBackwardProblem p{q,  k,  v,  a,  alpha,  beta,  w_r,  static_cast<const uint16_t*>(Hs),
                              dy, dH_T, dq, dk, dv, da, dalpha, dbeta, dw_r, dH0, s[0], s[1], s[2],
-                             s[3], B, T, N, Nqk, K, V, static_cast<float*>(workspace)};
+                             s[3], B, T, N, Nqk, K, V, static_cast<float*>(workspace), status};
   return done(launch_ssm_backward(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -19,7 +19,8 @@ namespace m2rnn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int L = kSsmChunk;
+constexpr int L = 64;  // tokens per step; pieces are whole chunks
+constexpr int kSteps = kSsmChunk / L;
 constexpr int VT = kSsmColumns;
 constexpr int kStages = 3;
 
@@ -53,8 +54,8 @@ __global__ void __launch_bounds__(kThreads, KP <= 64 ? 3 : 2)
   const int n = (int)(pair % p.N);
   const long long b = pair / p.N;
   const int head = (int)((long long)n * p.Nqk / p.N);
-  const int chunks = ssm_chunks(p.T);
-  const int first = piece * per, count = min(chunks, first + per) - first;
+  const int steps = (p.T + L - 1) / L;
+  const int first = piece * per * kSteps, count = min(steps, first + per * kSteps) - first;
   const int v0 = vt * VT, vw = min(VT, p.V - v0);
   const uint16_t* ag = p.a + b * p.sa.batch + n;
   const float alpha = p.alpha[n], beta = p.beta[n];
@@ -179,19 +180,19 @@ cudaError_t run(const SegmentProblem& p, int per, bool vec, cudaStream_t stream)
 
 }  // namespace
 
-// Whole segments for every SM at most; segments of at least eight chunks.  Pieces: three blocks
-// of the first launch per SM, of at least four chunks.
+// Whole segments for every SM at most; segments of at least four chunks.  Pieces: three blocks
+// of the first launch per SM, of at least two chunks.
 SsmCut ssm_cut(int B, int T, int N, int V) {
   constexpr int kSms = 152;
   const long long units = (long long)B * N * ((V + VT - 1) / VT);
   const int chunks = ssm_chunks(T);
   SsmCut c{1, chunks > 0 ? chunks : 1, 1, chunks > 0 ? chunks : 1};
   long long want = kSms / units;
-  if (want > chunks / 8) want = chunks / 8;
+  if (want > chunks / 4) want = chunks / 4;
   if (want < 2) return c;
   const int per = (int)((chunks + want - 1) / want);
   int fine = (int)(3 * kSms / (units * want));
-  if (fine > per / 4) fine = per / 4;
+  if (fine > per / 2) fine = per / 2;
   if (fine < 1) fine = 1;
   c.piece = (per + fine - 1) / fine;
   c.per = c.piece * fine;

@@ -109,7 +109,7 @@ def test_scan_refusals(lib):
     assert lib.m2rnn_ssm_backward_bf16(*args, ONE, need - 1, None) == bad
     assert lib.m2rnn_ssm_backward_bf16(*args, None, need, None) == bad
     assert lib.m2rnn_ssm_workspace_bytes(1, 4, 3, 2, 8, 8, 0) == 0
-    assert lib.m2rnn_ssm_states_bytes(2, 65, 3, 4, 5) == 4 * 2 * 3 * 3 * 4 * 5
+    assert lib.m2rnn_ssm_states_bytes(2, 129, 3, 4, 5) == 4 * 2 * 3 * 3 * 4 * 5
     assert lib.m2rnn_ssm_step_bf16(*[ONE] * 8, None, ONE, 1, 2, 1, 8, 8, None) == bad
     assert lib.m2rnn_ssm_step_bf16(*[ONE] * 10, 1, 2, 1, 8, 200, None) == wide
 
