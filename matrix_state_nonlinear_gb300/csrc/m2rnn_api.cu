@@ -59,6 +59,12 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+EncodeTiledFn tensor_map_encoder() { return encode_fn(); }
+
+namespace {
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 enum Variant : int {

@@ -17,13 +17,15 @@ m2rnn_status ssm_sizes(int B, int T, int N, int Nqk, int K, int V) {
   return M2RNN_OK;
 }
 
-// Given strides, or the dense ones.  A token's channels must not overlap the next token's
-// (unless every token is the same row, stride 0, which only reads).
-bool read_strides(const long long* s, int T, int N, int Nqk, int K, int V, Strides (&out)[4]) {
+// Given strides, or the dense ones.  The stride of a dimension of one is never used: it becomes
+// an aligned one.
+bool read_strides(const long long* s, int B, int T, int N, int Nqk, int K, int V, Strides (&out)[4]) {
   const long long width[4] = {(long long)Nqk * K, (long long)Nqk * K, (long long)N * V, N};
   for (int i = 0; i < 4; ++i) {
     out[i] = s ? Strides{s[2 * i], s[2 * i + 1]} : Strides{T * width[i], width[i]};
     if (out[i].batch < 0 || out[i].token < 0) return false;
+    if (T <= 1) out[i].token = (width[i] + 7) / 8 * 8;
+    if (B <= 1) out[i].batch = out[i].token * T;
   }
   return true;
 }
@@ -89,7 +91,7 @@ m2rnn_status m2rnn_ssm_forward_bf16(const uint16_t* q, const uint16_t* k, const 
   if (!alpha || !beta || !w_r) return M2RNN_ERR_INVALID_ARG;
   if (T > 0 && (!q || !k || !v || !a || !y)) return M2RNN_ERR_INVALID_ARG;
   Strides s[4];
-  if (!read_strides(strides, T, N, Nqk, K, V, s)) return M2RNN_ERR_INVALID_ARG;
+  if (!read_strides(strides, B, T, N, Nqk, K, V, s)) return M2RNN_ERR_INVALID_ARG;
   const size_t need = ssm_forward_workspace_bytes(B, T, N, Nqk, K, V);
   if (need > 0 && (!workspace || workspace_bytes < need)) return M2RNN_ERR_INVALID_ARG;
   if (!aligned_to(workspace, 16) || !aligned_to(Hs, 16) || !aligned_to(H0, 4) ||
@@ -116,7 +118,7 @@ m2rnn_status m2rnn_ssm_backward_bf16(const uint16_t* q, const uint16_t* k, const
   if (T > 0 && (!q || !k || !v || !a || !Hs || !dy || !dq || !dk || !dv || !da))
     return M2RNN_ERR_INVALID_ARG;
   Strides s[4];
-  if (!read_strides(strides, T, N, Nqk, K, V, s)) return M2RNN_ERR_INVALID_ARG;
+  if (!read_strides(strides, B, T, N, Nqk, K, V, s)) return M2RNN_ERR_INVALID_ARG;
   const size_t need = ssm_backward_workspace_bytes(B, T, N, Nqk, K, V);
   if (need > 0 && (!workspace || workspace_bytes < need)) return M2RNN_ERR_INVALID_ARG;
   if (!aligned_to(workspace, 16) || !aligned_to(Hs, 16) || !aligned_to(dH_T, 4) ||

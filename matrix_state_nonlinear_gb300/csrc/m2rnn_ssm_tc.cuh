@@ -13,22 +13,32 @@ namespace m2rnn {
 // Byte offset of panel `i` of a tile of `rows` rows.
 __device__ __forceinline__ constexpr int panel(int i, int rows) { return i * rows * 128; }
 
-// D (+)= A B, A and B in shared memory, `steps` of 16 along the summed index; a and b are the
-// descriptors of the first step, a_step and b_step their advance per step in 16-byte units, with
-// an extra a_panel, b_panel after every fourth step (K-major panels; 0: none).
+// D (+)= A B over STEPS (a multiple of four) steps of 16 along the summed index, issued where
+// `pred` holds; a and b describe the first step, A_STEP and B_STEP are their advance per step and
+// A_PANEL, B_PANEL the further advance after every fourth (16-byte units).
 template <int STEPS, int A_STEP, int B_STEP, int A_PANEL = 0, int B_PANEL = 0>
-__device__ __forceinline__ void umma_loop(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void umma_steps(bool pred, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
 #pragma unroll
-  for (int i = 0; i < STEPS; ++i)
-    umma_bf16(d, a + i * A_STEP + (i >> 2) * A_PANEL, b + i * B_STEP + (i >> 2) * B_PANEL, idesc,
-              i > 0 || accumulate ? 1u : 0u);
+  for (int i = 0; i < STEPS / 4; ++i)
+    umma4_if<A_STEP, B_STEP>(pred, d, a + i * (4 * A_STEP + A_PANEL), b + i * (4 * B_STEP + B_PANEL), idesc,
+                             i > 0 || accumulate ? 1u : 0u);
 }
-// The same with A in tensor memory (16 bf16 values of a row in 8 columns).
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Four steps with A in tensor memory (16 bf16 values of a row in 8 columns).
+template <int B_STEP>
+__device__ __forceinline__ void umma4_ta_if(bool pred, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate_first) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.ne.b32 t, %7, 0;\n\t"
+      "mov.b32 a, %1;\n\tmov.b64 b, %2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, a, 8;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, a, 8;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, a, 8;\n\tadd.s64 b, b, %6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate_first), "r"((int)pred), "n"(B_STEP), "r"(1)
       : "memory");
 }
 
@@ -37,26 +47,11 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b,
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return umma_desc(tile, 16, 1024, 2); }
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int rows) { return umma_desc(tile, rows * 128, 1024, 2); }
 
-// Thread i of a warp reads (writes) 32 or 16 consecutive columns of tensor-memory lane i of the
-// warp's quarter.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+// Thread i of a warp writes 8 consecutive columns of tensor-memory lane i of the warp's quarter.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -66,8 +61,39 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
                : "memory");
 }
 
-// A barrier of the whole block at which every thread learns whether any thread gave up.
-__device__ __forceinline__ bool sync_or(bool bad) { return __syncthreads_or(bad); }
+// A whole warp waits for the phase of `bar` with the given parity; false, for every lane, where the
+// wait ran out or another warp has given up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(~0u, wait_or_abort(bar, parity, kWaitLimitCycles, abort));
+}
+// One arrival for the warp, after its lanes' earlier work.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Tensor map of a bf16 operand [B][T][heads][width] with free token and batch strides, in boxes of
+// 128 tokens by 64 columns of one head, 128-byte swizzled; what lies outside is read as zero.
+inline bool token_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base, int width, int heads, int T, int B,
+                      const Strides& s) {
+  const cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)width * 2, (cuuint64_t)s.token * 2, (cuuint64_t)s.batch * 2};
+  const cuuint32_t box[4] = {64u, 1u, (cuuint32_t)kSsmChunk, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return s.token > 0 && s.batch > 0 &&
+         enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The same box by one warp, value by value, for operands that a tensor map cannot describe.
+__device__ __forceinline__ void copy_tokens(uint32_t tile, const uint16_t* src, long long stride, int rows, int width,
+                                            int lane) {
+  for (int id = lane; id < kSsmChunk * 64; id += 32) {
+    const int r = id >> 6, c = id & 63;
+    st_shared_u16(Tile<64>::at(tile, r, c >> 3) + (c & 7) * 2,
+                  r < rows && c < width ? src[r * stride + c] : (uint16_t)0);
+  }
+}
 
 constexpr int kTokens = kSsmChunk;  // 128: a chunk is one row of every product per token
 
@@ -80,47 +106,44 @@ struct alignas(16) ChunkGates {
   float total;          // log2 of the whole chunk's decay
 };
 
-// One warp fills a chunk's gates; lane l has tokens 4 l .. 4 l + 3, a their logits (-infinity past
-// the sequence).  Sums over later tokens run from the end, so that they are exact near zero.
-__device__ __forceinline__ void put_chunk_gates(ChunkGates& o, const float (&a)[4], float alpha, float beta, int lane) {
-  float d[4], c[4], r[4];
-#pragma unroll
+// One warp fills a chunk's gates; `logits` gives the logit of a token of the chunk (-infinity past
+// the sequence).  Each token's own values first (in o's arrays), then lane l sums over tokens
+// 4 l .. 4 l + 3 and the lanes before and after: sums over later tokens run from the end, so that
+// they are exact near zero.  The loop is kept short on purpose: the block's warps run different
+// code, and what does not fit the instruction cache stalls them all.
+template <typename Logits>
+__device__ __forceinline__ void put_chunk_gates(ChunkGates& o, Logits logits, float alpha, float beta, int lane) {
+#pragma unroll 1
   for (int i = 0; i < 4; ++i) {
-    const float2 g = ssm_gate(a[i], alpha, beta);
-    d[i] = g.x, c[i] = r[i] = g.y * kLog2e;
+    const int t = 32 * i + lane;
+    const float2 g = ssm_gate(logits(i), alpha, beta);
+    o.wd[t] = g.x;
+    o.cum[t] = g.y * kLog2e;
+    o.diag[t] = log2f(g.x);
   }
-  c[1] += c[0], c[2] += c[1], c[3] += c[2];
-  r[2] += r[3], r[1] += r[2], r[0] += r[1];
-  float before = c[3], after = r[0];
+  __syncwarp();
+  const float4 d = reinterpret_cast<const float4*>(o.wd)[lane], c = reinterpret_cast<const float4*>(o.cum)[lane];
+  float4 ld = reinterpret_cast<const float4*>(o.diag)[lane];
+  const float c1 = c.x + c.y, c2 = c1 + c.z, c3 = c2 + c.w, r2 = c.w, r1 = r2 + c.z, r0 = r1 + c.y;
+  float before = c3, after = r0 + c.x;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
     const float x = __shfl_up_sync(~0u, before, s), y = __shfl_down_sync(~0u, after, s);
     if (lane >= s) before += x;
     if (lane + s < 32) after += y;
   }
-  const float total = __shfl_sync(~0u, before, 31);
+  if (lane == 31) o.total = before;
   float pre = __shfl_up_sync(~0u, before, 1), post = __shfl_down_sync(~0u, after, 1);
   if (lane == 0) pre = 0.f;
   if (lane == 31) post = 0.f;
-  const float end = __shfl_sync(~0u, pre + c[3], lane | 7);
-  float4 cum, diag, wd, wk;
-  float* pc = &cum.x;
-  float* pd = &diag.x;
-  float* pw = &wd.x;
-  float* pk = &wk.x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = pre + c[i];
-    pc[i] = x;
-    pd[i] = x - log2f(d[i]);
-    pw[i] = d[i] * exp2_approx(end - x);
-    pk[i] = d[i] * exp2_approx((i < 3 ? r[i + 1] : 0.f) + post);
-  }
-  reinterpret_cast<float4*>(o.cum)[lane] = cum;
-  reinterpret_cast<float4*>(o.diag)[lane] = diag;
-  reinterpret_cast<float4*>(o.wd)[lane] = wd;
-  reinterpret_cast<float4*>(o.wk)[lane] = wk;
-  if (lane == 0) o.total = total;
+  const float4 x = make_float4(pre + c.x, pre + c1, pre + c2, pre + c3);
+  const float end = __shfl_sync(~0u, x.w, lane | 7);
+  reinterpret_cast<float4*>(o.cum)[lane] = x;
+  reinterpret_cast<float4*>(o.diag)[lane] = make_float4(x.x - ld.x, x.y - ld.y, x.z - ld.z, x.w - ld.w);
+  reinterpret_cast<float4*>(o.wd)[lane] = make_float4(d.x * exp2_approx(end - x.x), d.y * exp2_approx(end - x.y),
+                                                      d.z * exp2_approx(end - x.z), d.w * exp2_approx(end - x.w));
+  reinterpret_cast<float4*>(o.wk)[lane] = make_float4(d.x * exp2_approx(post + r0), d.y * exp2_approx(post + r1),
+                                                      d.z * exp2_approx(post + r2), d.w * exp2_approx(post));
 }
 
 // Eight bf16 values as four float2.
