@@ -10,7 +10,7 @@
 //   8 warps   P from S (a quarter of the tokens and half the columns each);
 //   4 warps   y from Y1, Y2 and v;
 //   8 warps   the state, float32 in registers, and the weighted v (half the columns each);
-//   1 warp    issues the products;  1 warp  the loads (TMA) and the gates.
+//   1 warp    issues the products;  1 warp  the loads (TMA);  2 warps  the gates, every other chunk.
 //  * S is decayed in float32 and rounded to bf16 in tensor memory, the first operand of P v; H is
 //    rounded to bf16 as an operand; y is bf16.  The state itself is float32 and takes U with float32
 //    weights: the weighted v enters as two bf16 values (17 bits), two products.
@@ -29,8 +29,9 @@ namespace {
 
 constexpr int L = kTokens;
 constexpr int VT = kSsmColumns;
-// Warps: P, y, state, then one for the products and one for loads and gates.
-constexpr int kWarpY = 8, kWarpState = 12, kWarpMma = 20, kWarps = 22;
+// First warp of each kind.
+constexpr int kWarpY = 8, kWarpState = 12, kWarpMma = 20, kWarpLoad = 21,
+              kWarpGate = 22, kWarps = 24;
 constexpr int kThreads = 32 * kWarps;
 
 // Tensor memory columns (S has two buffers).
@@ -373,17 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_if(leader, &bar.u);
       }
     }
-  } else {  // ---------------------------------------------------------- loads and gates
-    const uint16_t* ag = p.a + b * p.sa.batch + n;
-    const float alpha = p.alpha[n], beta = p.beta[n];
-    // Token 32 e + lane of a chunk, loaded a chunk ahead.
-    auto logit = [&](int i, int e) {
-      const long long t = (long long)(first + i) * L + 32 * e + lane;
-      return i < count && t < p.T ? bf16_to_f(ag[t * p.sa.token]) : -INFINITY;
-    };
-    float4 a = make_float4(logit(0, 0), logit(0, 1), logit(0, 2), logit(0, 3));
+  } else if (warp == kWarpLoad) {  // ----------------------------------- loads
     for (int i = 0; i < count; ++i) {
-      const float4 ahead = make_float4(logit(i + 1, 0), logit(i + 1, 1), logit(i + 1, 2), logit(i + 1, 3));
       if (i >= ST && !wait(bar.empty[i % ST], i / ST - 1)) break;
       const int t0 = (first + i) * L;
       if (tma) {
@@ -412,17 +404,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(&bar.full[i % ST], lane);
       }
-      if (i >= 4 && !wait(bar.gate_free[i & 3], (i >> 2) - 1)) break;
-      put_chunk_gates(
-          gates[i & 3], [&](int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }, alpha, beta, lane);
-      warp_arrive(&bar.gate[i & 3], lane);
-      a = ahead;
     }
     // Given up: whatever was started here arrives before the block ends (a stage's load that was
     // not started times out, one of an earlier chunk has long arrived).
     if (!ok && tma)
       for (int s = 0; s < ST; ++s)
         for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
+  } else {  // ---------------------------------------------------------- gates
+    const uint16_t* ag = p.a + b * p.sa.batch + n;
+    const float alpha = p.alpha[n], beta = p.beta[n];
+    // Token 32 e + lane of a chunk, loaded two chunks ahead.
+    auto logit = [&](int i, int e) {
+      const long long t = (long long)(first + i) * L + 32 * e + lane;
+      return i < count && t < p.T ? bf16_to_f(ag[t * p.sa.token]) : -INFINITY;
+    };
+    int i = warp - kWarpGate;
+    float4 a = make_float4(logit(i, 0), logit(i, 1), logit(i, 2), logit(i, 3));
+    for (; i < count; i += 2) {
+      const float4 ahead = make_float4(logit(i + 2, 0), logit(i + 2, 1), logit(i + 2, 2), logit(i + 2, 3));
+      if (i >= 4 && !wait(bar.gate_free[i & 3], (i >> 2) - 1)) break;
+      put_chunk_gates(
+          gates[i & 3], [&](int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }, alpha, beta, lane);
+      warp_arrive(&bar.gate[i & 3], lane);
+      a = ahead;
+    }
   }
   if (!ok && lane == 0) {
     *abort = 1;
