@@ -34,8 +34,10 @@ constexpr int kWarpY = 8, kWarpState = 12, kWarpMma = 20, kWarpLoad = 21,
               kWarpGate = 22, kWarps = 24;
 constexpr int kThreads = 32 * kWarps;
 
-// Tensor memory columns (S has two buffers).
-constexpr int kColS = 0, kColP = 256, kColY1 = 320, kColY2 = 384, kColU = 448, kTmemCols = 512;
+// Tensor memory columns.  S has two buffers, and P takes the place of its S: the 64 columns of
+// scores that a warp reads become 32 columns of bf16 pairs at their start.  U is in two halves, of
+// the high and the low parts of the weighted v.
+constexpr int kColS = 0, kColY1 = 256, kColY2 = 320, kColU = 384, kTmemCols = 512;
 
 template <int KP>
 struct Smem {
@@ -160,10 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (x == 0 && i > 0 && !wait(bar.y, i - 1)) break;  // P v of the chunk before still reads P
-        tmem_st8(t_lane + kColP + col / 2, out);
+        tmem_st8(ts + 64 * half + 8 * x, out);
       }
-      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&bar.p, lane);
@@ -315,11 +315,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 e2 = make_float2(e, e);
 #pragma unroll
       for (int x = 0; x < HC / 16; ++x) {
-        float u[16];
-        tmem_ld16_nowait(t_lane + kColU + hcol + 16 * x, u);
+        float hi[16], lo[16];
+        tmem_ld16_nowait(t_lane + kColU + hcol + 16 * x, hi);
+        tmem_ld16_nowait(t_lane + kColU + VT + hcol + 16 * x, lo);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) H[8 * x + c] = fma2(e2, H[8 * x + c], make_float2(u[2 * c], u[2 * c + 1]));
+        for (int c = 0; c < 8; ++c)
+          H[8 * x + c] = fma2(e2, H[8 * x + c], add2(make_float2(hi[2 * c], hi[2 * c + 1]),
+                                                     make_float2(lo[2 * c], lo[2 * c + 1])));
       }
       tc_fence_before();
       if (i + 1 < count) put_weighted(i + 1);
@@ -337,15 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpMma) {  // ------------------------------------ products
     const uint32_t idesc_s = umma_idesc_bf16(128, 128, false);
     const uint32_t idesc_y = umma_idesc_bf16_ab(128, VT, false, true);
-    const uint32_t idesc_u = umma_idesc_bf16_ab(KP, VT, true, true);
+    const uint32_t idesc_u = umma_idesc_bf16_ab(KP, 2 * VT, true, true);
     const uint64_t dh = desc_mn(base + S::kH, KP), dw = desc_mn(base + S::kW, L);
     const bool leader = lane == 0;
-    // Step i: S of chunk i + 1 (its buffer was P's of chunk i - 1, which has been waited for), q H
-    // and P v of chunk i, U of chunk i + 1.
+    // Step i: S of chunk i + 1 into the buffer of P of chunk i - 1, q H and P v of chunk i, U of
+    // chunk i + 1.
     for (int i = -1; i < count; ++i) {
       const bool more = i + 1 < count;
       const uint32_t next = stage(i + 1);
       if (more) {  // S = q k^T
+        if (i > 0) wait(bar.y, i - 1);
         if (!wait(bar.full[(i + 1) % ST], (i + 1) / ST)) break;
         umma_steps<KP / 16, 2, 2, L * 8 - 8, L * 8 - 8>(leader, tmem + kColS + ((i + 1) & 1) * 128, desc_k(next),
                                                         desc_k(next + S::kQ), idesc_s, false);
@@ -361,16 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(bar.p, i)) break;
         tc_fence_after();
         const uint64_t dv = desc_mn(stage(i) + 2 * S::kQ, L);
-        umma4_ta_if<128>(leader, tmem + kColY2, tmem + kColP, dv, idesc_y, 0u);
-        umma4_ta_if<128>(leader, tmem + kColY2, tmem + kColP + 32, dv + 512, idesc_y, 1u);
+        const uint32_t tp = tmem + kColS + (i & 1) * 128;
+        umma4_ta_if<128>(leader, tmem + kColY2, tp, dv, idesc_y, 0u);
+        umma4_ta_if<128>(leader, tmem + kColY2, tp + 64, dv + 512, idesc_y, 1u);
         umma_commit_if(leader, &bar.y);
       }
-      if (more) {  // U = k^T (weighted v), high then low
+      if (more) {  // U = k^T (weighted v), high and low side by side
         if (!wait(bar.w, i + 1)) break;
         tc_fence_after();
         const uint64_t dk = desc_mn(next + S::kQ, L);
         umma_steps<L / 16, 128, 128>(leader, tmem + kColU, dk, dw, idesc_u, false);
-        umma_steps<L / 16, 128, 128>(leader, tmem + kColU, dk, dw + (S::kV >> 4), idesc_u, true);
         umma_commit_if(leader, &bar.u);
       }
     }
