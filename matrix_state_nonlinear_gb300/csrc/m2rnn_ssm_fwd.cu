@@ -8,7 +8,7 @@
 // One block walks the chunks of one (batch, head) pair and one tile of 64 value columns.  Its warps
 // hand each other work through mbarriers, so that several chunks are in flight at once:
 //   8 warps   P from S (a quarter of the tokens and half the columns each);
-//   4 warps   y from Y1, Y2 and v;
+//   8 warps   y from Y1, Y2 and v (half the columns each);
 //   8 warps   the state, float32 in registers, and the weighted v (half the columns each);
 //   1 warp    issues the products;  1 warp  the loads (TMA);  2 warps  the gates, every other chunk.
 //  * S is decayed in float32 and rounded to bf16 in tensor memory, the first operand of P v; H is
@@ -30,8 +30,7 @@ namespace {
 constexpr int L = kTokens;
 constexpr int VT = kSsmColumns;
 // First warp of each kind.
-constexpr int kWarpY = 8, kWarpState = 12, kWarpMma = 20, kWarpLoad = 21,
-              kWarpGate = 22, kWarps = 24;
+constexpr int kWarpY = 8, kWarpState = 16, kWarpMma = 24, kWarpLoad = 25, kWarpGate = 26, kWarps = 28;
 constexpr int kThreads = 32 * kWarps;
 
 // Tensor memory columns.  S has two buffers, and P takes the place of its S: the 64 columns of
@@ -53,12 +52,14 @@ struct Smem {
   static_assert(kBytes <= 227 * 1024 && sizeof(ChunkGates) % 16 == 0, "");
 };
 
-// Per-chunk barriers complete once a chunk and no waiter is ever two chunks behind: each is filled
-// only after its waiters have passed the chunk before.  Stages and gate slots have one each.
+// A barrier's next phase completes only after every waiter has passed the phase before (a waiter
+// two phases behind would mistake one for the other).  Where a chunk's work may run that far
+// ahead there is a barrier for every buffer, stage or slot.
 struct Bars {
-  uint64_t full[3], empty[3];    // tiles of a stage: loaded; done with (by the warps of y)
-  uint64_t gate[4], gate_free[4];
-  uint64_t s, p, q, y, y_free, u, w, h;  // S, P, q H, P v done; Y read; U, weighted v, H done
+  uint64_t full[3], empty[3];      // tiles of a stage: loaded; done with (by the warps of y)
+  uint64_t gate[4], gate_free[4];  // gates of a chunk: written; done with (by y and the state)
+  uint64_t s[2], p[2];             // S, P, by buffer
+  uint64_t q, y, y_free, u, w, h;  // q H, P v done; Y read; U, weighted v, H done
   uint32_t tmem;
   int abort;
 };
@@ -91,10 +92,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const size_t plane = (size_t)p.K * p.V;
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 4);
-    for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 4);
-    mbar_init(&bar.s, 1), mbar_init(&bar.p, 8), mbar_init(&bar.q, 1), mbar_init(&bar.y, 1);
-    mbar_init(&bar.y_free, 4), mbar_init(&bar.u, 1), mbar_init(&bar.w, 8), mbar_init(&bar.h, 8);
+    for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 16);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.s[i], 1), mbar_init(&bar.p[i], 8);
+    mbar_init(&bar.q, 1), mbar_init(&bar.y, 1);
+    mbar_init(&bar.y_free, 8), mbar_init(&bar.u, 1), mbar_init(&bar.w, 8), mbar_init(&bar.h, 8);
     bar.abort = 0;
     fence_mbar_init();
   }
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2;
     for (int i = 0; i < count; ++i) {
       wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.s, i)) break;
+      if (!wait(bar.s[i & 1], i >> 1)) break;
       tc_fence_after();
       const ChunkGates& G = gates[i & 3];
       const float cum = G.cum[row];
@@ -166,9 +168,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(&bar.p, lane);
+      warp_arrive(&bar.p[i & 1], lane);
     }
   } else if (warp < kWarpState) {  // ----------------------------------- y
+    const int half = (warp - kWarpY) >> 2;
+    const long long ystride = (long long)p.N * p.V;
     for (int i = 0; i < count; ++i) {
       wait(bar.gate[i & 3], i >> 2);
       if (!wait(bar.y, i)) break;
@@ -177,53 +181,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 e2 = make_float2(e, e);
       const uint32_t tq = stage(i), tv = stage(i) + 2 * S::kQ;
 #pragma unroll 1
-      for (int x = 0; x < 4; ++x) {  // 16 columns at a time, out through this token's row of q
+      for (int x = 2 * half; x < 2 * half + 2; ++x) {  // 16 columns at a time, out through this token's row of q
         float y1[16], y2[16];
         tmem_ld16_nowait(t_lane + kColY1 + 16 * x, y1);
         tmem_ld16_nowait(t_lane + kColY2 + 16 * x, y2);
-        float2 v[2][4];
-        unpack8(ld_shared_v4(Tile<VT>::at(tv, row, 2 * x)), v[0]);
-        unpack8(ld_shared_v4(Tile<VT>::at(tv, row, 2 * x + 1)), v[1]);
+        const uint4 va = ld_shared_v4(Tile<VT>::at(tv, row, 2 * x)), vb = ld_shared_v4(Tile<VT>::at(tv, row, 2 * x + 1));
+        const float4* w4 = reinterpret_cast<const float4*>(wr + 16 * x);
         tmem_wait_ld();
-        if (x == 3) {
+        if (x & 1) {
           tc_fence_before();
           warp_arrive(&bar.y_free, lane);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          float2 v[4];
           uint32_t o[4];
-          const float4 w0 = *reinterpret_cast<const float4*>(wr + 16 * x + 8 * c);
-          const float4 w1 = *reinterpret_cast<const float4*>(wr + 16 * x + 8 * c + 4);
+          unpack8(c ? vb : va, v);
+          const float4 w0 = w4[2 * c], w1 = w4[2 * c + 1];
           const float2 w[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
                                make_float2(w1.z, w1.w)};
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const int k = 8 * c + 2 * z;
-            const float2 r =
-                fma2(w[z], v[c][z], fma2(e2, make_float2(y1[k], y1[k + 1]), make_float2(y2[k], y2[k + 1])));
+            const float2 r = fma2(w[z], v[z], fma2(e2, make_float2(y1[k], y1[k + 1]), make_float2(y2[k], y2[k + 1])));
             o[z] = pack_bf16x2(r.x, r.y);
           }
           st_shared_v4(Tile<VT>::at(tq, row, 2 * x + c), make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
       __syncwarp();
-      const long long t0 = (long long)(first + i) * L + 32 * quarter;
-      uint16_t* yg = p.y + ((b * p.T + t0) * p.N + n) * p.V + v0;
-      const long long ystride = (long long)p.N * p.V;
-      if (vec) {
-        const int ch = lane & 7, left = ch * 8 < vw ? (int)min(32LL, p.T - t0) : 0;
-        uint16_t* to = yg + (lane >> 3) * ystride + ch * 8;
-#pragma unroll 2
-        for (int x = 0; x < 8; ++x) {
-          const int r = (lane >> 3) + 4 * x;
-          if (r < left) *reinterpret_cast<uint4*>(to) = ld_shared_v4(Tile<VT>::at(tq, 32 * quarter + r, ch));
-          to += 4 * ystride;
+      const int t0 = (first + i) * L + 32 * quarter, left = min(32, p.T - t0), col0 = 32 * half;
+      uint16_t* yg = p.y + ((b * p.T + t0) * p.N + n) * p.V + v0 + col0;
+      if (vec) {  // 64 contiguous bytes of eight tokens at a time
+        const int ch = lane & 3, most = col0 + ch * 8 < vw ? left : 0;
+        uint16_t* to = yg + (lane >> 2) * ystride + ch * 8;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = (lane >> 2) + 8 * x;
+          if (r < most) *reinterpret_cast<uint4*>(to) = ld_shared_v4(Tile<VT>::at(tq, 32 * quarter + r, 4 * half + ch));
+          to += 8 * ystride;
         }
       } else {
-        for (int x = lane; x < 32 * VT; x += 32) {
-          const int r = x / VT, col = x % VT;
-          if (t0 + r < p.T && col < vw) {
-            const uint32_t u = ld_shared_u32(Tile<VT>::at(tq, 32 * quarter + r, col >> 3) + (col & 6) * 2);
+        for (int x = lane; x < 32 * 32; x += 32) {
+          const int r = x >> 5, col = x & 31;
+          if (r < left && col0 + col < vw) {
+            const uint32_t u = ld_shared_u32(Tile<VT>::at(tq, 32 * quarter + r, 4 * half + (col >> 3)) + (col & 6) * 2);
             yg[r * ystride + col] = (uint16_t)(col & 1 ? u >> 16 : u);
           }
         }
@@ -325,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                      make_float2(lo[2 * c], lo[2 * c + 1])));
       }
       tc_fence_before();
+      warp_arrive(&bar.gate_free[i & 3], lane);
       if (i + 1 < count) put_weighted(i + 1);
       if (!wait(bar.q, i)) break;  // q H of this chunk still reads the state's tile
       put_state(i + 1);
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(bar.full[(i + 1) % ST], (i + 1) / ST)) break;
         umma_steps<KP / 16, 2, 2, L * 8 - 8, L * 8 - 8>(leader, tmem + kColS + ((i + 1) & 1) * 128, desc_k(next),
                                                         desc_k(next + S::kQ), idesc_s, false);
-        umma_commit_if(leader, &bar.s);
+        umma_commit_if(leader, &bar.s[(i + 1) & 1]);
       }
       if (i >= 0) {
         wait(bar.h, i);
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         umma_steps<KP / 16, 2, 128, L * 8 - 8>(leader, tmem + kColY1, desc_k(stage(i)), dh, idesc_y, false);
         umma_commit_if(leader, &bar.q);
-        if (!wait(bar.p, i)) break;
+        if (!wait(bar.p[i & 1], i >> 1)) break;
         tc_fence_after();
         const uint64_t dv = desc_mn(stage(i) + 2 * S::kQ, L);
         const uint32_t tp = tmem + kColS + (i & 1) * 128;
