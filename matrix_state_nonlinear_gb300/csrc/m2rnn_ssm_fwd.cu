@@ -7,9 +7,9 @@
 // lane: S = q k^T, Y1 = q H, Y2 = P v (P = S decayed and masked), U = k^T (weighted v).
 // One block walks the chunks of one (batch, head) pair and one tile of 64 value columns.  Its warps
 // hand each other work through mbarriers, so that several chunks are in flight at once:
-//   8 warps   P from S (a quarter of the tokens and half the columns each);
+//   8 warps   P from S and the weighted v (a quarter of the tokens and half the columns each);
 //   8 warps   y from Y1, Y2 and v (half the columns each);
-//   8 warps   the state, float32 in registers, and the weighted v (half the columns each);
+//   8 warps   the state, float32 in registers (half the columns each);
 //   1 warp    issues the products;  1 warp  the loads (TMA);  2 warps  the gates, every other chunk.
 //  * S is decayed in float32 and rounded to bf16 in tensor memory, the first operand of P v; H is
 //    rounded to bf16 as an operand; y is bf16.  The state itself is float32 and takes U with float32
@@ -59,7 +59,8 @@ struct Bars {
   uint64_t full[3], empty[3];      // tiles of a stage: loaded; done with (by the warps of y)
   uint64_t gate[4], gate_free[4];  // gates of a chunk: written; done with (by y and the state)
   uint64_t s[2], p[2];             // S, P, by buffer
-  uint64_t q, y, y_free, u, w, h;  // q H, P v done; Y read; U, weighted v, H done
+  uint64_t q, y, y_free;           // q H, P v done; Y read
+  uint64_t u, u_free, w, h;        // U done, read; weighted v, H done
   uint32_t tmem;
   int abort;
 };
@@ -96,7 +97,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 16);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.s[i], 1), mbar_init(&bar.p[i], 8);
     mbar_init(&bar.q, 1), mbar_init(&bar.y, 1);
-    mbar_init(&bar.y_free, 8), mbar_init(&bar.u, 1), mbar_init(&bar.w, 8), mbar_init(&bar.h, 8);
+    mbar_init(&bar.y_free, 8), mbar_init(&bar.u, 1), mbar_init(&bar.u_free, 8);
+    mbar_init(&bar.w, 8), mbar_init(&bar.h, 8);
     bar.abort = 0;
     fence_mbar_init();
   }
@@ -117,7 +119,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kWarpY) {  // ------------------------------------------- P from S
     const int half = warp >> 2;
-    for (int i = 0; i < count; ++i) {
+    // Half a token's v of chunk i, weighted, as two bf16 values.
+    auto put_weighted = [&](int i) {
+      if (i > 0) wait(bar.u, i - 1);  // the product that read it
+      wait(bar.gate[i & 3], i >> 2);
+      if (!wait(bar.full[i % ST], i / ST)) return;
+      const float w = gates[i & 3].wk[row];
+      const float2 w2 = make_float2(w, w);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t at = Tile<VT>::at(0, row, 4 * half + c);
+        float2 f[4];
+        uint32_t hi[4], lo[4];
+        unpack8(ld_shared_v4(stage(i) + 2 * S::kQ + at), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16x2(mul2(f[e], w2), hi[e], lo[e]);
+        st_shared_v4(base + S::kW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_shared_v4(base + S::kW + S::kV + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bar.w, lane);
+    };
+    if (count > 0) put_weighted(0);
+    for (int i = 0; i < count && ok; ++i) {
       wait(bar.gate[i & 3], i >> 2);
       if (!wait(bar.s[i & 1], i >> 1)) break;
       tc_fence_after();
@@ -169,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(&bar.p[i & 1], lane);
+      if (i + 1 < count) put_weighted(i + 1);
     }
   } else if (warp < kWarpState) {  // ----------------------------------- y
     const int half = (warp - kWarpY) >> 2;
@@ -286,31 +311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    // Half a token's v of chunk i, weighted, as two bf16 values.
-    auto put_weighted = [&](int i) {
-      wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.full[i % ST], i / ST)) return;
-      const float w = gates[i & 3].wk[row];
-      const float2 w2 = make_float2(w, w);
-#pragma unroll 1
-      for (int c = 0; c < HC / 8; ++c) {
-        const uint32_t at = Tile<VT>::at(0, row, hcol / 8 + c);
-        float2 f[4];
-        uint32_t hi[4], lo[4];
-        unpack8(ld_shared_v4(stage(i) + 2 * S::kQ + at), f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split_bf16x2(mul2(f[e], w2), hi[e], lo[e]);
-        st_shared_v4(base + S::kW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        st_shared_v4(base + S::kW + S::kV + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-      }
-      fence_proxy_async_smem();
-      warp_arrive(&bar.w, lane);
-    };
     put_state(0);
     fence_proxy_async_smem();
     warp_arrive(&bar.h, lane);
-    if (count > 0) put_weighted(0);
     for (int i = 0; i < count; ++i) {
+      wait(bar.gate[i & 3], i >> 2);
       if (!wait(bar.u, i)) break;
       tc_fence_after();
       const float e = exp2_approx(gates[i & 3].total);
@@ -327,8 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                      make_float2(lo[2 * c], lo[2 * c + 1])));
       }
       tc_fence_before();
-      warp_arrive(&bar.gate_free[i & 3], lane);
-      if (i + 1 < count) put_weighted(i + 1);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.u_free);
+        mbar_arrive(&bar.gate_free[i & 3]);
+      }
       if (!wait(bar.q, i)) break;  // q H of this chunk still reads the state's tile
       put_state(i + 1);
       fence_proxy_async_smem();
@@ -374,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_if(leader, &bar.y);
       }
       if (more) {  // U = k^T (weighted v), high and low side by side
+        if (i >= 0) wait(bar.u_free, i);
         if (!wait(bar.w, i + 1)) break;
         tc_fence_after();
         const uint64_t dk = desc_mn(next + S::kQ, L);
