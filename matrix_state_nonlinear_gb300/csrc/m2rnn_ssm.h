@@ -48,27 +48,36 @@ struct SsmBackwardProblem {
 
 __host__ __device__ inline int ssm_chunks(int T) { return (T + kSsmChunk - 1) / kSsmChunk; }
 
-// How a pair's chunks are cut: `segments` of `per` chunks, side by side in the main launch, and
-// each into `fine` pieces of `piece` chunks for the launch that finds their starting states.
+// A pair's chunks are cut into `segments` of `per` chunks that run side by side.
 struct SsmCut {
-  int segments, per, fine, piece;
+  int segments, per;
 };
 SsmCut ssm_cut(int B, int T, int N, int V);
-int ssm_pieces(const SsmCut& c, int T);
-size_t ssm_segment_floats(const SsmCut& c, int B, int T, int N, int K, int V);
-struct SegmentProblem {
-  const uint16_t *x, *y;  // k and v, or q and dy
+size_t ssm_segment_floats(const SsmCut& c, int B, int N, int K, int V);
+
+// The state's sums alone (m2rnn_ssm_state.cu).
+struct StateProblem {
+  const uint16_t *x, *y;  // k and v, or, backwards, q and dy
   const uint16_t* a;
   const float *alpha, *beta;
-  const float* start;  // the first state (the last state's gradient), or null
   Strides sx, sy, sa;
   int B, T, N, Nqk, K, V;
-  float* state;  // [pairs][pieces][K][V], then [pairs][pieces]: ssm_segment_floats
-  int pieces;    // set by the launch, as is decay
-  float* decay;
+  const float* from;        // the first state (backwards: the last one's gradient), or null
+  const float* from_state;  // or every segment's, [pairs][segments][K][V]
+  float* to;                // the last state (backwards: the first one's gradient), or null
+  uint16_t* kept;           // backwards: G after every chunk, [pairs][chunks][2 (high, low)][K][V]
+  const uint16_t* Hs;       // with it: the forward's states,
+  float* dots;              // and <G, H> after every chunk, [pairs][chunks][tiles of V][8 parts]
+  int* status;
+  int pieces, per, first_piece;  // set by the launches, as are
+  float *to_state, *decay;
 };
-cudaError_t launch_ssm_segments(SegmentProblem p, const SsmCut& c, bool reverse, bool vec,
+// Every segment's starting state (backwards: its last state's gradient) into ws,
+// ssm_segment_floats.
+cudaError_t launch_ssm_segments(StateProblem p, const SsmCut& c, bool reverse, bool vec, float* ws,
                                 cudaStream_t stream);
+// The backward's first pass: kept, dots and `to`, from `from` or from_state.
+cudaError_t launch_ssm_state_gradients(StateProblem p, const SsmCut& c, bool vec, cudaStream_t stream);
 
 size_t ssm_forward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V);
 size_t ssm_backward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V);

@@ -19,7 +19,7 @@
 //  * Only H -> q H and U -> H follow the sequence; S and U of the next chunk are issued before this
 //    chunk's P v, so that P never waits for the tensor cores' latency.
 // Where the pairs are fewer than the SMs, segments of a sequence run side by side
-// (m2rnn_ssm_seg.cu).
+// (m2rnn_ssm_state.cu).
 #include <mutex>
 
 #include "m2rnn_ssm_tc.cuh"
@@ -69,8 +69,7 @@ static_assert(sizeof(Bars) <= 256, "");
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, SsmProblem p, SsmCut cut, int pieces, bool tma,
-                       bool vec) {
+                       const __grid_constant__ CUtensorMap map_v, SsmProblem p, SsmCut cut, bool tma, bool vec) {
   using S = Smem<KP>;
   constexpr int ST = S::kStages, PANELS = KP / 64;
   extern __shared__ unsigned char smem_raw[];
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int HC = VT / 2;  // this thread's columns, from hcol
     const int hcol = HC * ((warp - kWarpState) >> 2);
     float2 H[HC / 2];
-    const float* src = cut.segments > 1 ? p.ws + ((size_t)pair * pieces + seg * cut.fine) * plane
+    const float* src = cut.segments > 1 ? p.ws + ((size_t)pair * cut.segments + seg) * plane
                        : p.H0           ? p.H0 + pair * plane
                                         : nullptr;
     auto first_state = [&](int c) {
@@ -470,14 +469,14 @@ cudaError_t run(const SsmProblem& p, const SsmCut& cut, bool vec, cudaStream_t s
                    token_map(enc, &mv, p.v, p.V, p.N, p.T, p.B, p.sv);
   const unsigned units = (unsigned)((long long)p.B * p.N * ((p.V + VT - 1) / VT));
   ssm_forward_kernel<KP><<<dim3(units, cut.segments), kThreads, Smem<KP>::kBytes, stream>>>(
-      mq, mk, mv, p, cut, ssm_pieces(cut, p.T), tma, vec);
+      mq, mk, mv, p, cut, tma, vec);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t ssm_forward_workspace_bytes(int B, int T, int N, int, int K, int V) {
-  return sizeof(float) * ssm_segment_floats(ssm_cut(B, T, N, V), B, T, N, K, V);
+  return sizeof(float) * ssm_segment_floats(ssm_cut(B, T, N, V), B, N, K, V);
 }
 
 cudaError_t launch_ssm_forward(const SsmProblem& p, cudaStream_t stream) {
@@ -485,8 +484,9 @@ cudaError_t launch_ssm_forward(const SsmProblem& p, cudaStream_t stream) {
                    aligned_to(p.y, 16);
   const SsmCut cut = ssm_cut(p.B, p.T, p.N, p.V);
   if (cut.segments > 1) {
-    SegmentProblem s{p.k, p.v, p.a, p.alpha, p.beta, p.H0, p.sk, p.sv, p.sa, p.B, p.T, p.N, p.Nqk, p.K, p.V, p.ws};
-    const cudaError_t err = launch_ssm_segments(s, cut, false, vec, stream);
+    StateProblem s{p.k, p.v, p.a, p.alpha, p.beta, p.sk, p.sv, p.sa, p.B, p.T, p.N, p.Nqk, p.K, p.V, p.H0};
+    s.status = p.status;
+    const cudaError_t err = launch_ssm_segments(s, cut, false, vec, p.ws, stream);
     if (err != cudaSuccess) return err;
   }
   return p.K <= 64 ? run<64>(p, cut, vec, stream) : run<128>(p, cut, vec, stream);

@@ -1,0 +1,413 @@
+// m2rnn_ssm_state.cu — the scan's states alone: from tokens to the state, forwards, or to the
+// state's gradient, backwards.
+//
+//   forwards:   H <- exp(c_127) H + sum_s k_s (exp(c_127 - c_s) d_s v_s)^T      (reads k, v)
+//   backwards:  G <- exp(c_127) G + sum_t q_t (exp(c_t) dy_t)^T                 (reads q, dy)
+// over chunks of 128 tokens (c: sum of log f over the chunk).  Two uses:
+//  * pieces: where there are fewer (batch, head) pairs than SMs, a pair's sequence is cut into
+//    pieces, each piece's own state from zero found side by side, and a second launch chains them
+//    into the state before (after) each; the main kernels start there;
+//  * the backward's first pass: G after every chunk, kept for the second as two bf16 values each,
+//    with <G, H> there, the sum that the gates' gradients start from.
+// Products on the 5th-generation tensor cores: one of 128 x 16 steps per chunk, the weighted y in
+// two bf16 values (17 bits) side by side as its second operand.  Bound by the traffic of x and y,
+// 2 (K + V) bytes a token and head; warps by role as in the forward kernel.
+#include <mutex>
+
+#include "m2rnn_ssm_tc.cuh"
+
+namespace m2rnn {
+namespace {
+
+constexpr int L = kTokens;
+constexpr int VT = kSsmColumns;
+constexpr int kWarpState = 8, kWarpMma = 16, kWarpLoad = 17, kWarpGate = 18, kWarps = 20;  // 0..7: weights
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTmemCols = 128;
+
+struct alignas(16) Weights {
+  float w[L];
+  float l[L];   // scratch of the gates
+  float total;  // log2 of the chunk's decay
+};
+
+template <int KP>
+struct Smem {
+  static constexpr int kStages = 3;
+  static constexpr int kX = L * KP * 2, kY = L * VT * 2;
+  static constexpr int kStage = kX + kY;
+  static constexpr int kW = kStages * kStage;  // weighted y, high and low
+  static constexpr int kWeights = kW + 2 * kY;
+  static constexpr int kBars = kWeights + 4 * (int)sizeof(Weights);
+  static constexpr int kBytes = kBars + 256 + 1024;
+};
+
+struct Bars {
+  uint64_t full[3], empty[3];
+  uint64_t gate[4], gate_free[4];
+  uint64_t u, u_free, w;  // U done, read; weighted y written
+  uint32_t tmem;
+  int abort;
+};
+
+template <int KP, bool REVERSE>
+__global__ void __launch_bounds__(kThreads, 1)
+    ssm_state_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y,
+                     StateProblem p, bool tma, bool vec) {
+  using S = Smem<KP>;
+  constexpr int ST = S::kStages, PANELS = KP / 64;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t base = smem_u32(smem);
+  Weights* weights = reinterpret_cast<Weights*>(smem + S::kWeights);
+  Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
+  volatile int* abort = &bar.abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int vtiles = (p.V + VT - 1) / VT;
+  const int vt = blockIdx.x % vtiles, piece = blockIdx.y + p.first_piece;
+  const long long pair = blockIdx.x / vtiles;
+  const int n = (int)(pair % p.N);
+  const long long b = pair / p.N;
+  const int head = (int)((long long)n * p.Nqk / p.N);
+  const int chunks = ssm_chunks(p.T);
+  const int first = piece * p.per, count = min(chunks, first + p.per) - first;
+  const int v0 = vt * VT, vw = min(VT, p.V - v0);
+  const size_t plane = (size_t)p.K * p.V;
+  auto chunk_at = [&](int i) { return REVERSE ? first + count - 1 - i : first + i; };
+
+  if (tid == 0) {
+    for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 8);
+    mbar_init(&bar.u, 1), mbar_init(&bar.u_free, 8), mbar_init(&bar.w, 8);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&bar.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  auto stage = [&](int i) { return base + i % ST * S::kStage; };
+  const int quarter = warp & 3, row = 32 * quarter + lane, half = (warp >> 2) & 1;
+  const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
+  bool ok = true;
+  auto wait = [&](uint64_t& b, int i) {
+    if (ok) ok = warp_wait(&b, (uint32_t)i & 1u, abort);
+    return ok;
+  };
+
+  if (warp < kWarpState) {  // --------------------------------------- weighted y
+    for (int i = 0; i < count; ++i) {
+      if (i > 0) wait(bar.u, i - 1);  // the product that read the one before
+      wait(bar.gate[i & 3], i >> 2);
+      if (!wait(bar.full[i % ST], i / ST)) break;
+      const float w = weights[i & 3].w[row];
+      const float2 w2 = make_float2(w, w);
+#pragma unroll 2
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t at = Tile<VT>::at(0, row, 4 * half + c);
+        float2 f[4];
+        uint32_t hi[4], lo[4];
+        unpack8(ld_shared_v4(stage(i) + S::kX + at), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16x2(mul2(f[e], w2), hi[e], lo[e]);
+        st_shared_v4(base + S::kW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_shared_v4(base + S::kW + S::kY + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&bar.w, lane);
+    }
+  } else if (warp < kWarpMma) {  // ---------------------------------- the state
+    // This thread's row and half of the columns.  With K <= 64 the product has 64 rows, 16 in each
+    // quarter's first lanes.
+    constexpr int HC = VT / 2;
+    const int hcol = HC * half;
+    const int hrow = KP > 64 ? row : 16 * quarter + lane;
+    const bool has_row = (KP > 64 || lane < 16) && hrow < p.K;
+    const size_t at = (size_t)hrow * p.V + v0 + hcol;  // within [K][V]
+    const float* src = p.from_state ? p.from_state + ((size_t)pair * p.pieces + piece) * plane
+                       : p.from     ? p.from + pair * plane
+                                    : nullptr;
+    float2 H[HC / 2];
+    auto given = [&](int c) { return src && has_row && hcol + c < vw ? src[at + c] : 0.f; };
+#pragma unroll
+    for (int c = 0; c < HC / 2; ++c) H[c] = make_float2(given(2 * c), given(2 * c + 1));
+    float decay = 0.f;
+    for (int i = 0; i <= count; ++i) {
+      // Where states are kept: the one before chunk i (of this order), and <it, Hs there>.
+      if (REVERSE && p.kept && i < count) {
+        const int chunk = chunk_at(i);
+        float dot = 0.f;
+        if (has_row) {
+          uint16_t* to = p.kept + ((size_t)pair * chunks + chunk) * 2 * plane + at;
+          const uint16_t* hs = p.Hs + ((size_t)pair * (chunks + 1) + chunk + 1) * 2 * plane + at;
+          float2 d2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < HC / 8; ++c) {
+            if (hcol + 8 * c >= vw) break;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_bf16x2(H[4 * c + e], hi[e], lo[e]);
+            if (vec) {
+              float2 x[4], y[4];
+              unpack8(*reinterpret_cast<const uint4*>(hs + 8 * c), x);
+              unpack8(*reinterpret_cast<const uint4*>(hs + plane + 8 * c), y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d2 = fma2(H[4 * c + e], add2(x[e], y[e]), d2);
+              *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (hcol + 8 * c + e < vw) {
+                  const int k = 8 * c + e;
+                  const float h = bf16_to_f(hs[k]) + bf16_to_f(hs[plane + k]);
+                  dot = fmaf(e & 1 ? H[k / 2].y : H[k / 2].x, h, dot);
+                  to[k] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
+                  to[plane + k] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
+                }
+            }
+          }
+          dot += d2.x + d2.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+        if (lane == 0) p.dots[(((size_t)pair * chunks + chunk) * vtiles + vt) * 8 + warp - kWarpState] = dot;
+      }
+      if (i == count) break;
+      wait(bar.gate[i & 3], i >> 2);
+      if (!wait(bar.u, i)) break;
+      tc_fence_after();
+      const float total = weights[i & 3].total;
+      decay += total;
+      const float e = exp2_approx(total);
+      const float2 e2 = make_float2(e, e);
+#pragma unroll
+      for (int x = 0; x < HC / 16; ++x) {
+        float hi[16], lo[16];
+        tmem_ld16_nowait(t_lane + hcol + 16 * x, hi);
+        tmem_ld16_nowait(t_lane + VT + hcol + 16 * x, lo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          H[8 * x + c] = fma2(e2, H[8 * x + c], add2(make_float2(hi[2 * c], hi[2 * c + 1]),
+                                                     make_float2(lo[2 * c], lo[2 * c + 1])));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.u_free);
+        mbar_arrive(&bar.gate_free[i & 3]);
+      }
+    }
+    if (ok) {
+      if (p.decay && vt == 0 && warp == kWarpState && lane == 0) p.decay[pair * p.pieces + piece] = decay;
+      float* dst = p.to_state                         ? p.to_state + ((size_t)pair * p.pieces + piece) * plane
+                   : p.to && (REVERSE ? first == 0 : first + count == chunks) ? p.to + pair * plane
+                                                                              : nullptr;
+      if (dst && has_row) {
+#pragma unroll
+        for (int c = 0; c < HC; ++c)
+          if (hcol + c < vw) dst[at + c] = c & 1 ? H[c / 2].y : H[c / 2].x;
+      }
+    }
+  } else if (warp == kWarpMma) {  // --------------------------------- products
+    const uint32_t idesc = umma_idesc_bf16_ab(KP, 2 * VT, true, true);
+    const uint64_t dw = desc_mn(base + S::kW, L);
+    const bool leader = lane == 0;
+    for (int i = 0; i < count; ++i) {
+      if (i > 0) wait(bar.u_free, i - 1);
+      wait(bar.full[i % ST], i / ST);
+      if (!wait(bar.w, i)) break;
+      tc_fence_after();
+      umma_steps<L / 16, 128, 128>(leader, tmem, desc_mn(stage(i), L), dw, idesc, false);
+      umma_commit_if(leader, &bar.u);
+      umma_commit_if(leader, &bar.empty[i % ST]);
+    }
+  } else if (warp == kWarpLoad) {  // -------------------------------- loads
+    for (int i = 0; i < count; ++i) {
+      if (i >= ST && !wait(bar.empty[i % ST], i / ST - 1)) break;
+      const int t0 = chunk_at(i) * L;
+      if (tma) {
+        if (lane == 0) {
+          uint64_t* full = &bar.full[i % ST];
+          unsigned char* to = smem + i % ST * S::kStage;
+          mbar_arrive_expect_tx(full, S::kStage);
+#pragma unroll
+          for (int x = 0; x < PANELS; ++x)
+            tma_load_4d(to + panel(x, L), &map_x, full, 64 * x, head, t0, (int)b);
+          tma_load_4d(to + S::kX, &map_y, full, v0, n, t0, (int)b);
+        }
+        __syncwarp();
+      } else {
+        const int rows = min(L, p.T - t0);
+        const uint16_t* x0 = p.x + b * p.sx.batch + t0 * p.sx.token + (long long)head * p.K;
+        for (int x = 0; x < PANELS; ++x)
+          copy_tokens(stage(i) + panel(x, L), x0 + 64 * x, p.sx.token, rows, p.K - 64 * x, lane);
+        copy_tokens(stage(i) + S::kX, p.y + b * p.sy.batch + t0 * p.sy.token + (long long)n * p.V + v0, p.sy.token,
+                    rows, vw, lane);
+        fence_proxy_async_smem();
+        warp_arrive(&bar.full[i % ST], lane);
+      }
+    }
+    if (!ok && tma)  // given up: whatever was started here arrives before the block ends
+      for (int s = 0; s < ST; ++s)
+        for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
+  } else {  // ------------------------------------------------------- gates
+    const uint16_t* ag = p.a + b * p.sa.batch + n;
+    const float alpha = p.alpha[n], beta = p.beta[n];
+    auto logit = [&](int i, int e) {
+      const long long t = i < count ? (long long)chunk_at(i) * L + 32 * e + lane : p.T;
+      return t < p.T ? bf16_to_f(ag[t * p.sa.token]) : -INFINITY;
+    };
+    int i = warp - kWarpGate;
+    float4 a = make_float4(logit(i, 0), logit(i, 1), logit(i, 2), logit(i, 3));
+    for (; i < count; i += 2) {
+      const float4 ahead = make_float4(logit(i + 2, 0), logit(i + 2, 1), logit(i + 2, 2), logit(i + 2, 3));
+      if (i >= 4 && !wait(bar.gate_free[i & 3], (i >> 2) - 1)) break;
+      Weights& o = weights[i & 3];
+#pragma unroll 1
+      for (int e = 0; e < 4; ++e) {
+        const float2 g = ssm_gate(e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w, alpha, beta);
+        o.w[32 * e + lane] = g.x;
+        o.l[32 * e + lane] = g.y * kLog2e;
+      }
+      __syncwarp();
+      const float4 d = reinterpret_cast<const float4*>(o.w)[lane], c = reinterpret_cast<const float4*>(o.l)[lane];
+      // Sums of log2 f up to each token (backwards) or after it (forwards), over the four tokens of
+      // the lane and the lanes before (after).
+      float mine = c.x + c.y + c.z + c.w, run = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const float x = REVERSE ? __shfl_up_sync(~0u, run, s) : __shfl_down_sync(~0u, run, s);
+        if (REVERSE ? lane >= s : lane + s < 32) run += x;
+      }
+      if (lane == (REVERSE ? 31 : 0)) o.total = run;
+      float rest = REVERSE ? __shfl_up_sync(~0u, run, 1) : __shfl_down_sync(~0u, run, 1);
+      if (lane == (REVERSE ? 0 : 31)) rest = 0.f;
+      float4 w;
+      if (REVERSE) {
+        const float c1 = c.x + c.y, c2 = c1 + c.z;
+        w = make_float4(exp2_approx(rest + c.x), exp2_approx(rest + c1), exp2_approx(rest + c2), exp2_approx(rest + (c2 + c.w)));
+      } else {
+        const float r1 = c.w + c.z, r0 = r1 + c.y;
+        w = make_float4(d.x * exp2_approx(rest + r0), d.y * exp2_approx(rest + r1), d.z * exp2_approx(rest + c.w),
+                        d.w * exp2_approx(rest));
+      }
+      reinterpret_cast<float4*>(o.w)[lane] = w;
+      warp_arrive(&bar.gate[i & 3], lane);
+      a = ahead;
+    }
+  }
+  if (!ok && lane == 0) {
+    *abort = 1;
+    atomicExch(p.status, kStatusTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// state[piece] from the piece's own sum to the state before it (after it, with `reverse`), in
+// place: the chain starts at `from` and takes in a piece's decay and sum after it is written.
+__global__ void __launch_bounds__(256)
+    ssm_join_kernel(const float* __restrict__ from, float* __restrict__ state, const float* __restrict__ decays,
+                    int pieces, int kv, int reverse) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  const long long pair = blockIdx.y;
+  if (i >= kv) return;
+  float h = from ? from[(size_t)pair * kv + i] : 0.f;
+  float* s = state + (size_t)pair * pieces * kv + i;
+  const float* d = decays + pair * pieces;
+  constexpr int kAhead = 8;  // pieces loaded at once
+  for (int j = 0; j < pieces; j += kAhead) {
+    float own[kAhead], decay[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (j + u + 1 < pieces) {
+        const int at = reverse ? pieces - 1 - j - u : j + u;
+        own[u] = s[(size_t)at * kv];
+        decay[u] = d[at];
+      }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = reverse ? pieces - 1 - j - u : j + u;
+      if (j + u < pieces) s[(size_t)at * kv] = h;
+      if (j + u + 1 < pieces) h = fmaf(exp2_approx(decay[u]), h, own[u]);
+    }
+  }
+}
+
+template <int KP, bool REVERSE>
+cudaError_t run(const StateProblem& p, int blocks_y, bool vec, cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(ssm_state_kernel<KP, REVERSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<KP>::kBytes);
+  });
+  if (attr != cudaSuccess) return attr;
+  const EncodeTiledFn enc = tensor_map_encoder();
+  CUtensorMap mx{}, my{};
+  const bool tma = vec && enc && p.T > 0 && token_map(enc, &mx, p.x, p.K, p.Nqk, p.T, p.B, p.sx) &&
+                   token_map(enc, &my, p.y, p.V, p.N, p.T, p.B, p.sy);
+  const unsigned units = (unsigned)((long long)p.B * p.N * ((p.V + VT - 1) / VT));
+  ssm_state_kernel<KP, REVERSE><<<dim3(units, blocks_y), kThreads, Smem<KP>::kBytes, stream>>>(mx, my, p, tma, vec);
+  return cudaGetLastError();
+}
+
+cudaError_t run_any(const StateProblem& p, int blocks_y, bool reverse, bool vec, cudaStream_t stream) {
+  if (p.K <= 64) return reverse ? run<64, true>(p, blocks_y, vec, stream) : run<64, false>(p, blocks_y, vec, stream);
+  return reverse ? run<128, true>(p, blocks_y, vec, stream) : run<128, false>(p, blocks_y, vec, stream);
+}
+
+}  // namespace
+
+// Whole segments for every SM at most, of at least two chunks.
+SsmCut ssm_cut(int B, int T, int N, int V) {
+  constexpr int kSms = 152;
+  const long long units = (long long)B * N * ((V + VT - 1) / VT);
+  const int chunks = ssm_chunks(T);
+  SsmCut c{1, chunks > 0 ? chunks : 1};
+  long long want = kSms / units;
+  if (want > chunks / 2) want = chunks / 2;
+  if (want < 2) return c;
+  c.per = (int)((chunks + want - 1) / want);
+  c.segments = (chunks + c.per - 1) / c.per;
+  return c;
+}
+
+size_t ssm_segment_floats(const SsmCut& c, int B, int N, int K, int V) {
+  return c.segments > 1 ? (size_t)B * N * c.segments * ((size_t)K * V + 1) : 0;
+}
+
+cudaError_t launch_ssm_segments(StateProblem p, const SsmCut& c, bool reverse, bool vec, float* ws,
+                                cudaStream_t stream) {
+  const long long pairs = (long long)p.B * p.N;
+  const int kv = p.K * p.V;
+  const float* from = p.from;
+  p.from = nullptr;
+  p.from_state = nullptr;
+  p.kept = nullptr;
+  p.pieces = c.segments;
+  p.per = c.per;
+  p.first_piece = reverse ? 1 : 0;  // the last piece of the order ends the sequence: not needed
+  p.to_state = ws;
+  p.decay = ws + (size_t)pairs * c.segments * kv;
+  const cudaError_t err = run_any(p, c.segments - 1, reverse, vec, stream);
+  if (err != cudaSuccess) return err;
+  ssm_join_kernel<<<dim3((kv + 255) / 256, (unsigned)pairs), 256, 0, stream>>>(from, ws, p.decay, c.segments, kv,
+                                                                               reverse);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ssm_state_gradients(StateProblem p, const SsmCut& c, bool vec, cudaStream_t stream) {
+  p.pieces = c.segments;
+  p.per = c.per;
+  p.first_piece = 0;
+  p.to_state = nullptr;
+  p.decay = nullptr;
+  return run_any(p, c.segments, true, vec, stream);
+}
+
+}  // namespace m2rnn
