@@ -1,178 +1,831 @@
-// m2rnn_ssm_bwd.cu — gradients of the selective scan, token by token (see include/m2rnn.h).
+// m2rnn_ssm_bwd.cu — gradients of the selective scan (see include/m2rnn.h).
 //
-// One block per (batch, head) pair walks the chunks in reverse: it recomputes the chunk's states
-// from the kept one into the workspace, then scans its tokens in reverse with the state's
-// gradient in shared memory.  Per-head dq, dk and per-pair parameter sums go to the workspace
-// and are added in a fixed order.
-#include "m2rnn_ssm.h"
+// Two passes over chunks of 128 tokens.  The first (m2rnn_ssm_state.cu) runs the state's gradient
+// backwards, G <- exp(c_127) G + sum_t exp(c_t) q_t dy_t^T, and keeps it after every chunk.  With G
+// there and the state H before the chunk (kept by the forward), chunks are independent; the second
+// pass, here, takes them in any order.  With P_ts = exp(c_t - c_s) d_s (q_t . k_s) and dS_ts the
+// same of (dy_t . v_s), s <= t:
+//   dq = dS k + (exp(c) dy) H^T              dk = dS^T q + (w v) G^T,   w_s = exp(c_127 - c_s) d_s
+//   dv = P^T dy + w (k G) + w_r dy
+// and for the gate, with E_ts = P_ts (dy_t . v_s) over s < t,
+//   row_t = sum_s E_ts + exp(c_t) (q_t H) . dy_t,   col_s = sum_t E_ts + w_s (k_s G) . v_s,
+//   g_t = <G, H>_end + sum_{u >= t} (row_u - col_u)      (g_t = dL/dlog f_t)
+//   da = sigmoid (col + E_tt) / d - alpha sigmoid g,   dalpha = -sum d g,   dbeta = sum da
+// (<G, H> at a chunk's start replaces the first token's g: there is no sum behind it).
+//
+// Precision: the outputs dq, dk, dv are bf16 and so are the operands of their products (P, dS,
+// exp(c) dy, w v, H, G).  The gate's gradient ends in float32 sums over all tokens: E is float32
+// from float32 scores, and q H, k G take H and G as two bf16 values each.
+//
+// One block is resident per SM (shared memory) and walks steps: one (head, value tile) of one
+// chunk.  Heads that share q and k are consecutive steps of one item, whose dq and dk add up in
+// tensor memory; items of many heads may be split (float32 parts, added in a fixed order).
+// Sixteen warps do each phase together (a row, i.e. token, per lane; 16 or 32 columns per warp),
+// four others issue products, load, make gates, and finish the gate's gradient.
+#include <mutex>
+
+#include "m2rnn_ssm_tc.cuh"
 
 namespace m2rnn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int L = kTokens;
+constexpr int VT = kSsmColumns;
+constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpGate = 18, kWarps = 20;  // 0..15: element-wise; 19: the gate's gradient
+constexpr int kThreads = 32 * kWarps;
 
+// Tensor memory columns: q H and then P^T dy in the place of S, k G in the place of dP.
+constexpr int kColDq = 0, kColDk = 128, kColS = 256, kColDp = 384, kTmemCols = 512;
+
+struct alignas(16) Sums {  // of a head's chunk, per token; parts by column group or quarter
+  float row[4][L], row_state[4][L], col[4][L], col_state[4][L], diag[L];
+};
+
+template <int KP>
+struct Smem {
+  static constexpr int kTile = L * 128;            // 128 rows of 64 values
+  static constexpr int kQ = 0, kK = kQ + L * KP * 2;
+  static constexpr int kV = kK + L * KP * 2, kDy = kV + kTile;
+  static constexpr int kState = kDy + kTile;       // H, later G: high, low
+  static constexpr int kScaled = kState + 2 * KP * VT * 2;  // exp(c) dy, later w v
+  static constexpr int kP = kScaled + kTile, kDs = kP + 2 * kTile;
+  static constexpr int kGates = kDs + 2 * kTile;
+  static constexpr int kSums = kGates + 2 * (int)sizeof(ChunkGates);
+  static constexpr int kBars = kSums + (int)sizeof(Sums);
+  static constexpr int kBytes = kBars + 256 + 1024;  // and slack to align the tiles
+  static_assert(kBytes <= 227 * 1024, "");
+};
+
+// One phase per step (per item: qk, acc_free; per head: sums, sums_free); every barrier's next
+// phase needs its waiters to have passed the one before.
+struct Bars {
+  uint64_t qk, vd, h, g;            // tiles loaded
+  uint64_t step_free;               // v, dy, and the accumulators of the step read
+  uint64_t scaled1, scaled2;        // exp(c) dy, w v written
+  uint64_t s, pds, hd, q_read, gd, done;  // S, dP done; P, dS written; q H done, read; k G done; P^T dy done
+  uint64_t acc_free;                // dq, dk read
+  uint64_t gate[2], gate_free[2];
+  uint64_t sums, sums_free;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "");
+
+// The work of one block: items blockIdx.x, + gridDim.x, ...; an item is a chunk of a batch row and
+// q/k head, for `heads` of its heads, each for every value tile.
+struct Plan {
+  int chunks, vtiles, rep, splits, per_split;
+  long long items;
+};
 struct Workspace {
-  float *hist, *dq, *dk, *par;  // [pairs][65][K][V], [B,T,N,K] x 2, [pairs][2 + V]
+  float *segments, *dots, *par, *dqp, *dkp;
+  uint16_t* G;
   size_t floats;
 };
-Workspace carve(float* ws, int B, int T, int N, int K, int V) {
-  const size_t pairs = (size_t)B * N, kv = (size_t)K * V, tok = (size_t)B * T * N * K;
+
+// Position in a block's list of steps.
+struct Cursor {
+  long long item;
+  int b, group, chunk, split, head, last_head, vt;
+  int item_no, head_no;
+  __device__ bool start(const Plan& plan, int nqk) {
+    item = blockIdx.x, item_no = 0, head_no = 0;
+    return open(plan, nqk);
+  }
+  __device__ bool open(const Plan& plan, int nqk) {
+    if (item >= plan.items) return false;
+    long long x = item;
+    split = (int)(x % plan.splits), x /= plan.splits;
+    chunk = (int)(x % plan.chunks), x /= plan.chunks;
+    group = (int)(x % nqk);
+    b = (int)(x / nqk);
+    head = group * plan.rep + split * plan.per_split;
+    last_head = min(head + plan.per_split, (group + 1) * plan.rep) - 1;
+    vt = 0;
+    return true;
+  }
+  __device__ bool first(const Plan& plan) const { return vt == 0 && head == group * plan.rep + split * plan.per_split; }
+  __device__ bool head_end(const Plan& plan) const { return vt == plan.vtiles - 1; }
+  __device__ bool last(const Plan& plan) const { return head_end(plan) && head == last_head; }
+  __device__ bool next(const Plan& plan, int nqk) {
+    if (++vt < plan.vtiles) return true;
+    vt = 0;
+    ++head_no;
+    if (++head <= last_head) return true;
+    ++item_no;
+    item += gridDim.x;
+    return open(plan, nqk);
+  }
+};
+
+template <int KP>
+__global__ void __launch_bounds__(kThreads, 1)
+    ssm_backward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dy,
+                        const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_g,
+                        SsmBackwardProblem p, Plan plan, Workspace w, bool tma, bool vec) {
+  using S = Smem<KP>;
+  constexpr int PANELS = KP / 64;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t base = smem_u32(smem);
+  ChunkGates* gates = reinterpret_cast<ChunkGates*>(smem + S::kGates);
+  Sums& sums = *reinterpret_cast<Sums*>(smem + S::kSums);
+  Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
+  volatile int* abort = &bar.abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const size_t plane = (size_t)p.K * p.V;
+  if (tid == 0) {
+    mbar_init(&bar.qk, 1), mbar_init(&bar.vd, 1), mbar_init(&bar.h, 1), mbar_init(&bar.g, 1);
+    mbar_init(&bar.step_free, 16), mbar_init(&bar.scaled1, 16), mbar_init(&bar.scaled2, 16);
+    mbar_init(&bar.s, 1), mbar_init(&bar.pds, 16), mbar_init(&bar.hd, 1), mbar_init(&bar.q_read, 16);
+    mbar_init(&bar.gd, 1), mbar_init(&bar.done, 1), mbar_init(&bar.acc_free, 16);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 16);
+    mbar_init(&bar.sums, 16), mbar_init(&bar.sums_free, 1);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(&bar.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  bool ok = true;  // uniform in the warp
+  auto wait = [&](uint64_t& b, int i) {
+    if (ok) ok = warp_wait(&b, (uint32_t)i & 1u, abort);
+    return ok;
+  };
+  Cursor at;
+  bool more = at.start(plan, p.Nqk);
+
+  if (warp < kWarpMma) {  // ------------------------------------------ element-wise
+    const int quarter = warp & 3, group = warp >> 2, row = 32 * quarter + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
+    const uint32_t tv = base + S::kV, td = base + S::kDy;
+    const int c0 = 16 * group;  // this warp's 16 of the 64 value columns
+    for (int j = 0; more; ++j) {
+      const int v0 = at.vt * VT, vw = min(VT, p.V - v0);
+      const long long t = (long long)at.chunk * L + row;
+      if (at.vt == 0 && at.head_no > 0) wait(bar.sums_free, at.head_no - 1);
+      wait(bar.gate[j & 1], j >> 1);
+      if (!wait(bar.vd, j)) break;
+      const ChunkGates& G = gates[j & 1];
+      const float cum = G.cum[row], wk = G.wk[row];
+      const float et = exp2_approx(cum);
+      // exp(c) dy as an operand (and below w v, in the same place).
+      auto put_scaled = [&](uint32_t from, float f, uint64_t& ready) {
+        const float2 f2 = make_float2(f, f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t a = Tile<VT>::at(0, row, 2 * group + c);
+          float2 x[4];
+          uint32_t o[4];
+          unpack8(ld_shared_v4(from + a), x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = mul2(x[e], f2);
+            o[e] = pack_bf16x2(y.x, y.y);
+          }
+          st_shared_v4(base + S::kScaled + a, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&ready, lane);
+      };
+      put_scaled(td, et, bar.scaled1);
+
+      // P and dS from S and dP: block `group` of 32 columns against the quarter's own 32 rows.
+      if (!wait(bar.s, j)) break;
+      tc_fence_after();
+      {
+        const uint32_t tp = base + S::kP + (group >> 1) * S::kTile, ts = base + S::kDs + (group >> 1) * S::kTile;
+        const int ch = 4 * (group & 1);  // the block's first 16-byte chunk of a row
+        float rows = 0.f, diag = 0.f;
+        if (group > quarter) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            st_shared_v4(Tile<64>::at(tp, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
+            st_shared_v4(Tile<64>::at(ts, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
+          }
+        } else {
+          uint32_t po[2][8], so[2][8];
+          const float u = exp2_approx(cum - G.cum[32 * group + 31]);
+          const float2 u2 = make_float2(u, u);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {  // 16 columns at a time
+            float sc[16], dp[16], e[16];
+            tmem_ld16_nowait(t_lane + kColS + 32 * group + 16 * x, sc);
+            tmem_ld16_nowait(t_lane + kColDp + 32 * group + 16 * x, dp);
+            tmem_wait_ld();
+            if (group < quarter) {
+              const float4* w4 = reinterpret_cast<const float4*>(G.wd + 32 * group + 16 * x);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int z = 0; z < 8; ++z) {
+                const float4 wv = w4[z >> 1];
+                const float2 m = mul2(u2, z & 1 ? make_float2(wv.z, wv.w) : make_float2(wv.x, wv.y));
+                const float2 d = make_float2(dp[2 * z], dp[2 * z + 1]);
+                const float2 pv = mul2(make_float2(sc[2 * z], sc[2 * z + 1]), m), sv = mul2(d, m), ev = mul2(pv, d);
+                sum = add2(sum, ev);
+                e[2 * z] = ev.x, e[2 * z + 1] = ev.y;
+                po[x][z] = pack_bf16x2(pv.x, pv.y);
+                so[x][z] = pack_bf16x2(sv.x, sv.y);
+              }
+              rows += sum.x + sum.y;
+            } else {
+#pragma unroll
+              for (int z = 0; z < 8; ++z) {
+                float pv[2], sv[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int k = 2 * z + y, col = 16 * x + k;
+                  const float m = col <= lane ? exp2_approx(cum - G.diag[32 * group + col]) : 0.f;
+                  pv[y] = col <= lane ? sc[k] * m : 0.f;
+                  sv[y] = col <= lane ? dp[k] * m : 0.f;
+                  const float ev = pv[y] * dp[k];
+                  if (col == lane) diag = ev;
+                  e[k] = col < lane ? ev : 0.f;
+                  rows += e[k];
+                }
+                po[x][z] = pack_bf16x2(pv[0], pv[1]);
+                so[x][z] = pack_bf16x2(sv[0], sv[1]);
+              }
+            }
+            // Column sums over the warp's 32 rows: E through this block's own place in the tile of P
+            // (then of dS), read back four columns and four rows per lane, then across eight lanes.
+            const uint32_t scratch = x ? ts : tp;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              st_shared_v4(Tile<64>::at(scratch, row, ch + c),
+                           make_uint4(__float_as_uint(e[4 * c]), __float_as_uint(e[4 * c + 1]),
+                                      __float_as_uint(e[4 * c + 2]), __float_as_uint(e[4 * c + 3])));
+            __syncwarp();
+            float2 a01 = make_float2(0.f, 0.f), a23 = a01;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint4 q = ld_shared_v4(Tile<64>::at(scratch, 32 * quarter + (lane >> 2) + 8 * r, ch + (lane & 3)));
+              a01 = add2(a01, make_float2(__uint_as_float(q.x), __uint_as_float(q.y)));
+              a23 = add2(a23, make_float2(__uint_as_float(q.z), __uint_as_float(q.w)));
+            }
+            const bool up = lane & 16, mid = lane & 8;
+            float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
+            k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
+            k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
+            float k = mid ? k1 : k0;
+            k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
+            k += __shfl_xor_sync(~0u, k, 4);
+            if (!(lane & 4)) {
+              float& to = sums.col[quarter][32 * group + 16 * x + 4 * (lane & 3) + (up ? 2 : 0) + (mid ? 1 : 0)];
+              to = at.vt ? to + k : k;
+            }
+            __syncwarp();
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              st_shared_v4(Tile<64>::at(tp, row, ch + 2 * x + c),
+                           make_uint4(po[x][4 * c], po[x][4 * c + 1], po[x][4 * c + 2], po[x][4 * c + 3]));
+              st_shared_v4(Tile<64>::at(ts, row, ch + 2 * x + c),
+                           make_uint4(so[x][4 * c], so[x][4 * c + 1], so[x][4 * c + 2], so[x][4 * c + 3]));
+            }
+          float& to = sums.row[group][row];
+          to = at.vt ? to + rows : rows;
+          if (group == quarter) sums.diag[row] = at.vt ? sums.diag[row] + diag : diag;
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      warp_arrive(&bar.pds, lane);
+
+      // dw_r of the chunk: four columns per warp, four tokens per lane.
+      {
+        float2 a01 = make_float2(0.f, 0.f), a23 = a01;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t a = Tile<VT>::at(0, lane + 32 * r, warp >> 1) + 8 * (warp & 1);
+          a01 = fma2(bf16x2_to_float2(ld_shared_u32(tv + a)), bf16x2_to_float2(ld_shared_u32(td + a)), a01);
+          a23 = fma2(bf16x2_to_float2(ld_shared_u32(tv + a + 4)), bf16x2_to_float2(ld_shared_u32(td + a + 4)), a23);
+        }
+        const bool up = lane & 16, mid = lane & 8;
+        float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
+        k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
+        k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
+        float k = mid ? k1 : k0;
+        k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) k += __shfl_xor_sync(~0u, k, o);
+        const int col = 4 * warp + (up ? 2 : 0) + (mid ? 1 : 0);
+        if ((lane & 7) == 0 && col < vw)
+          w.par[((size_t)(at.b * plan.chunks + at.chunk) * p.N + at.head) * (2 + p.V) + 2 + v0 + col] = k;
+      }
+
+      // The state's part of the row sums: exp(c) (q H) . dy.
+      if (!wait(bar.hd, j)) break;
+      tc_fence_after();
+      {
+        float hi[16], lo[16];
+        tmem_ld16_nowait(t_lane + kColS + c0, hi);
+        tmem_ld16_nowait(t_lane + kColS + VT + c0, lo);
+        float2 y[8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float2 x[4];
+          unpack8(ld_shared_v4(Tile<VT>::at(td, row, 2 * group + c)), x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[4 * c + e] = x[e];
+        }
+        tmem_wait_ld();
+        tc_fence_before();
+        warp_arrive(&bar.q_read, lane);
+        float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dot = fma2(add2(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])), y[e], dot);
+        float& to = sums.row_state[group][row];
+        const float r = et * (dot.x + dot.y);
+        to = at.vt ? to + r : r;
+      }
+      put_scaled(tv, wk, bar.scaled2);
+
+      // k G: its part of the column sums, and of dv.
+      float2 x[8];
+      if (!wait(bar.gd, j)) break;
+      tc_fence_after();
+      {
+        float hi[16], lo[16];
+        tmem_ld16_nowait(t_lane + kColDp + c0, hi);
+        tmem_ld16_nowait(t_lane + kColDp + VT + c0, lo);
+        float2 y[8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float2 f[4];
+          unpack8(ld_shared_v4(Tile<VT>::at(tv, row, 2 * group + c)), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[4 * c + e] = f[e];
+        }
+        tmem_wait_ld();
+        const float2 w2 = make_float2(wk, wk);
+        float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = mul2(w2, add2(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])));
+          dot = fma2(x[e], y[e], dot);
+        }
+        float& to = sums.col_state[group][row];
+        to = at.vt ? to + (dot.x + dot.y) : dot.x + dot.y;
+      }
+      if (at.head_end(plan)) warp_arrive(&bar.sums, lane);
+
+      // dv = P^T dy + w (k G) + w_r dy.
+      if (!wait(bar.done, j)) break;
+      tc_fence_after();
+      {
+        float a[16];
+        tmem_ld16_nowait(t_lane + kColS + c0, a);
+        float2 y[8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float2 f[4];
+          unpack8(ld_shared_v4(Tile<VT>::at(td, row, 2 * group + c)), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[4 * c + e] = f[e];
+        }
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.step_free);
+          mbar_arrive(&bar.gate_free[j & 1]);
+        }
+        const float* wr = p.w_r + (size_t)at.head * p.V + v0 + c0;
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 w2 = make_float2(c0 + 2 * e < vw ? wr[2 * e] : 0.f, c0 + 2 * e + 1 < vw ? wr[2 * e + 1] : 0.f);
+          const float2 r = fma2(w2, y[e], add2(make_float2(a[2 * e], a[2 * e + 1]), x[e]));
+          o[e] = pack_bf16x2(r.x, r.y);
+        }
+        if (t < p.T) {
+          uint16_t* to = p.dv + (((size_t)at.b * p.T + t) * p.N + at.head) * p.V + v0 + c0;
+          if (vec) {
+            if (c0 < vw) *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c0 + 8 < vw) *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (c0 + e < vw) to[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+          }
+        }
+      }
+
+      __syncwarp();
+
+      // dq, dk of the item.
+      if (at.last(plan)) {
+        constexpr int KC = KP / 4;  // columns per warp
+        const size_t to = ((size_t)at.b * p.T + t) * p.Nqk + at.group;
+#pragma unroll 1
+        for (int c = 0; c < 2 * KC; c += 16) {
+          const bool is_k = c >= KC;
+          const int col = KC * group + (is_k ? c - KC : c);
+          float a[16];
+          tmem_ld16_nowait(t_lane + (is_k ? kColDk : kColDq) + col, a);
+          tmem_wait_ld();
+          if (t >= p.T) {
+          } else if (plan.splits > 1) {
+            float* f = (is_k ? w.dkp : w.dqp) + ((size_t)at.split * p.B * p.T * p.Nqk + to) * p.K + col;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (col + e < p.K) f[e] = a[e];
+          } else {
+            uint16_t* f = (is_k ? p.dk : p.dq) + to * p.K + col;
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
+            if (vec) {
+              if (col < p.K) *reinterpret_cast<uint4*>(f) = make_uint4(o[0], o[1], o[2], o[3]);
+              if (col + 8 < p.K) *reinterpret_cast<uint4*>(f + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (col + e < p.K) f[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        warp_arrive(&bar.acc_free, lane);
+      }
+      more = at.next(plan, p.Nqk);
+    }
+  } else if (warp == kWarpMma) {  // ---------------------------------- products
+    const uint32_t id_ss = umma_idesc_bf16(128, 128, false);                   // both K-major
+    const uint32_t id_st = umma_idesc_bf16_ab(128, 128, false, true);          // a state, high and low
+    const uint32_t id_k = umma_idesc_bf16(128, KP, false);
+    const uint32_t id_dq = umma_idesc_bf16_ab(128, KP, false, true), id_dk = umma_idesc_bf16_ab(128, KP, true, true);
+    const uint32_t id_dv = umma_idesc_bf16_ab(128, VT, true, true);
+    const uint32_t q = base + S::kQ, k = base + S::kK, v = base + S::kV, dy = base + S::kDy, st = base + S::kState;
+    const uint32_t sc = base + S::kScaled, tp = base + S::kP, ts = base + S::kDs;
+    constexpr int PANEL = L * 8 - 8;  // to the next panel of 64 columns, K-major
+    const bool leader = lane == 0;
+    for (int j = 0; more; ++j) {
+      const bool first = at.first(plan);
+      if (first) wait(bar.qk, at.item_no);
+      if (j > 0) wait(bar.step_free, j - 1);
+      if (!wait(bar.vd, j)) break;
+      tc_fence_after();
+      umma_steps<KP / 16, 2, 2, PANEL, PANEL>(leader, tmem + kColS, desc_k(q), desc_k(k), id_ss, false);
+      umma_steps<4, 2, 2>(leader, tmem + kColDp, desc_k(dy), desc_k(v), id_ss, false);
+      umma_commit_if(leader, &bar.s);
+      if (first && at.item_no > 0) wait(bar.acc_free, at.item_no - 1);
+      wait(bar.h, j);
+      if (!wait(bar.scaled1, j)) break;
+      tc_fence_after();
+      umma_steps<4, 2, 2>(leader, tmem + kColDq, desc_k(sc), desc_k(st), id_k, !first);
+      if (!wait(bar.pds, j)) break;
+      tc_fence_after();
+      umma_steps<KP / 16, 2, 128, PANEL>(leader, tmem + kColS, desc_k(q), desc_mn(st, KP), id_st, false);
+      umma_commit_if(leader, &bar.hd);
+      umma_steps<L / 16, 2, 128, PANEL>(leader, tmem + kColDq, desc_k(ts), desc_mn(k, L), id_dq, true);
+      umma_steps<L / 16, 128, 128>(leader, tmem + kColDk, desc_mn(ts, L), desc_mn(q, L), id_dk, !first);
+      wait(bar.g, j);
+      if (!wait(bar.scaled2, j)) break;
+      tc_fence_after();
+      umma_steps<KP / 16, 2, 128, PANEL>(leader, tmem + kColDp, desc_k(k), desc_mn(st, KP), id_st, false);
+      umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st), id_k, true);
+      umma_commit_if(leader, &bar.gd);
+      if (!wait(bar.q_read, j)) break;
+      tc_fence_after();
+      umma_steps<L / 16, 128, 128>(leader, tmem + kColS, desc_mn(tp, L), desc_mn(dy, L), id_dv, false);
+      umma_commit_if(leader, &bar.done);
+      more = at.next(plan, p.Nqk);
+    }
+  } else if (warp == kWarpLoad) {  // --------------------------------- loads
+    for (int j = 0; more; ++j) {
+      const int t0 = at.chunk * L, rows = min(L, p.T - t0), v0 = at.vt * VT, vw = min(VT, p.V - v0);
+      const long long pair = (long long)at.b * p.N + at.head;
+      if (at.first(plan)) {
+        if (j > 0 && !wait(bar.done, j - 1)) break;
+        if (tma) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar.qk, 2 * L * KP * 2);
+#pragma unroll
+            for (int x = 0; x < PANELS; ++x) {
+              tma_load_4d(smem + S::kQ + panel(x, L), &map_q, &bar.qk, 64 * x, at.group, t0, at.b);
+              tma_load_4d(smem + S::kK + panel(x, L), &map_k, &bar.qk, 64 * x, at.group, t0, at.b);
+            }
+          }
+        } else {
+          for (int x = 0; x < PANELS; ++x) {
+            copy_tokens(base + S::kQ + panel(x, L), p.q + at.b * p.sq.batch + t0 * p.sq.token + (long long)at.group * p.K + 64 * x,
+                        p.sq.token, rows, p.K - 64 * x, lane);
+            copy_tokens(base + S::kK + panel(x, L), p.k + at.b * p.sk.batch + t0 * p.sk.token + (long long)at.group * p.K + 64 * x,
+                        p.sk.token, rows, p.K - 64 * x, lane);
+          }
+          fence_proxy_async_smem();
+          warp_arrive(&bar.qk, lane);
+        }
+      }
+      if (j > 0 && !wait(bar.step_free, j - 1)) break;
+      if (tma) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.vd, 2 * S::kTile);
+          tma_load_4d(smem + S::kV, &map_v, &bar.vd, v0, at.head, t0, at.b);
+          tma_load_4d(smem + S::kDy, &map_dy, &bar.vd, v0, at.head, t0, at.b);
+        }
+      } else {
+        copy_tokens(base + S::kV, p.v + at.b * p.sv.batch + t0 * p.sv.token + (long long)at.head * p.V + v0, p.sv.token,
+                    rows, vw, lane);
+        copy_tokens(base + S::kDy, p.dy + (((size_t)at.b * p.T + t0) * p.N + at.head) * p.V + v0, (long long)p.N * p.V,
+                    rows, vw, lane);
+        fence_proxy_async_smem();
+        warp_arrive(&bar.vd, lane);
+      }
+      // H once the products with the step before's G are done, G once those with H are.
+#pragma unroll 1
+      for (int s = 0; s < 2; ++s) {
+        if (s == 0 && j > 0 && !wait(bar.gd, j - 1)) break;
+        if (s == 1 && !wait(bar.hd, j)) break;
+        uint64_t* full = s ? &bar.g : &bar.h;
+        if (tma) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(full, 2 * KP * VT * 2);
+            for (int x = 0; x < 2; ++x)
+              tma_load_4d(smem + S::kState + x * KP * VT * 2, s ? &map_g : &map_h, full, v0, 0, 2 * at.chunk + x, (int)pair);
+          }
+        } else {
+          const uint16_t* src = s ? w.G + ((size_t)pair * plan.chunks + at.chunk) * 2 * plane
+                                  : p.Hs + ((size_t)pair * (plan.chunks + 1) + at.chunk) * 2 * plane;
+          for (int x = 0; x < 2; ++x)
+            for (int id = lane; id < KP * 64; id += 32) {
+              const int r = id >> 6, c = id & 63;
+              st_shared_u16(Tile<64>::at(base + S::kState + x * KP * VT * 2, r, c >> 3) + (c & 7) * 2,
+                            r < p.K && c < vw ? src[x * plane + (size_t)r * p.V + v0 + c] : (uint16_t)0);
+            }
+          fence_proxy_async_smem();
+          warp_arrive(full, lane);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      more = at.next(plan, p.Nqk);
+    }
+    // Given up: whatever was started here arrives before the block ends (waits for what was not
+    // started run out).
+    if (!ok && tma) {
+      uint64_t* all[4] = {&bar.qk, &bar.vd, &bar.h, &bar.g};
+      for (int s = 0; s < 4; ++s)
+        for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(all[s], phase, kWaitLimitCycles / 64);
+    }
+  } else if (warp == kWarpGate) {  // --------------------------------- gates
+    for (int j = 0; more; ++j) {
+      const uint16_t* ag = p.a + at.b * p.sa.batch + at.head;
+      const long long t0 = (long long)at.chunk * L + lane;
+      const int last = p.T;
+      float4 a;
+      a.x = t0 < last ? bf16_to_f(ag[t0 * p.sa.token]) : -INFINITY;
+      a.y = t0 + 32 < last ? bf16_to_f(ag[(t0 + 32) * p.sa.token]) : -INFINITY;
+      a.z = t0 + 64 < last ? bf16_to_f(ag[(t0 + 64) * p.sa.token]) : -INFINITY;
+      a.w = t0 + 96 < last ? bf16_to_f(ag[(t0 + 96) * p.sa.token]) : -INFINITY;
+      const float alpha = p.alpha[at.head], beta = p.beta[at.head];
+      if (j >= 2 && !wait(bar.gate_free[j & 1], (j >> 1) - 1)) break;
+      put_chunk_gates(
+          gates[j & 1], [&](int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }, alpha, beta, lane);
+      warp_arrive(&bar.gate[j & 1], lane);
+      more = at.next(plan, p.Nqk);
+    }
+  } else {  // -------------------------------------------------------- the gate's gradient
+    while (more) {
+      if (at.head_end(plan)) {
+        if (!wait(bar.sums, at.head_no)) break;
+        const long long pair = (long long)at.b * p.N + at.head;
+        const float alpha = p.alpha[at.head], beta = p.beta[at.head];
+        const float* dots = w.dots + ((size_t)pair * (plan.chunks + 1) + at.chunk) * plan.vtiles * 8;
+        float end = 0.f, begin = 0.f;
+        for (int i = 0; i < plan.vtiles * 8; ++i) begin += dots[i], end += dots[plan.vtiles * 8 + i];
+        // Tokens 4 lane .. 4 lane + 3: row - col, then its sums over the later tokens.
+        float diff[4], full[4], g[4];
+        const int block = lane >> 3;  // of 32 tokens
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 4 * lane + e;
+          float r = 0.f, c = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r += sums.row_state[i][t] + (i <= block ? sums.row[i][t] : 0.f);
+            c += sums.col_state[i][t] + (i >= block ? sums.col[i][t] : 0.f);
+          }
+          diff[e] = r - c;
+          full[e] = c + sums.diag[t];
+        }
+        warp_arrive(&bar.sums_free, lane);
+        g[3] = diff[3], g[2] = diff[2] + g[3], g[1] = diff[1] + g[2], g[0] = diff[0] + g[1];
+        float run = g[0];
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+          const float y = __shfl_down_sync(~0u, run, s);
+          if (lane + s < 32) run += y;
+        }
+        float after = __shfl_down_sync(~0u, run, 1);
+        if (lane == 31) after = 0.f;
+        float dalpha = 0.f, dbeta = 0.f;
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          const long long t = (long long)at.chunk * L + 4 * lane + e;
+          if (t >= p.T) break;
+          const float gt = 4 * lane + e == 0 ? begin : end + (after + (e == 0 ? g[0] : e == 1 ? g[1] : e == 2 ? g[2] : g[3]));
+          const float a = bf16_to_f(p.a[at.b * p.sa.batch + t * p.sa.token + at.head]);
+          const float x = a + beta, ex = expf(-fabsf(x));
+          const float sig = x >= 0.f ? 1.f / (1.f + ex) : ex / (1.f + ex);
+          const float d = ssm_gate(a, alpha, beta).x;
+          const float da = sigmoid_over_softplus(x) * (e == 0 ? full[0] : e == 1 ? full[1] : e == 2 ? full[2] : full[3]) -
+                           alpha * sig * gt;
+          p.da[((size_t)at.b * p.T + t) * p.N + at.head] = f_to_bf16(da);
+          dalpha -= d * gt;
+          dbeta += da;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          dalpha += __shfl_xor_sync(~0u, dalpha, o);
+          dbeta += __shfl_xor_sync(~0u, dbeta, o);
+        }
+        if (lane == 0) {
+          float* par = w.par + ((size_t)(at.b * plan.chunks + at.chunk) * p.N + at.head) * (2 + p.V);
+          par[0] = dalpha, par[1] = dbeta;
+        }
+      }
+      more = at.next(plan, p.Nqk);
+    }
+  }
+  if (!ok && lane == 0) {
+    *abort = 1;
+    atomicExch(p.status, kStatusTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// dq, dk: the splits' parts added in order.
+__global__ void __launch_bounds__(256)
+    sum_splits_kernel(const float* __restrict__ dqp, const float* __restrict__ dkp, uint16_t* __restrict__ dq,
+                      uint16_t* __restrict__ dk, int splits, long long n) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float a = 0.f, b = 0.f;
+  for (int s = 0; s < splits; ++s) a += dqp[s * n + i], b += dkp[s * n + i];
+  dq[i] = f_to_bf16(a);
+  dk[i] = f_to_bf16(b);
+}
+
+// Sums over the batch's chunks of the parts [rows][N][2 + V]: 32 columns by 32 slices of rows per
+// block, the slices added in order.
+__global__ void __launch_bounds__(1024)
+    sum_params_kernel(const float* __restrict__ par, float* __restrict__ dalpha, float* __restrict__ dbeta,
+                      float* __restrict__ dw_r, int rows, int N, int V) {
+  __shared__ float part[32][33];
+  const int width = N * (2 + V), c = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  if (c < width)
+    for (int r = threadIdx.y; r < rows; r += 32) s += par[(size_t)r * width + c];
+  part[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y || c >= width) return;
+  s = 0.f;
+  for (int i = 0; i < 32; ++i) s += part[i][threadIdx.x];
+  const int n = c / (2 + V), j = c % (2 + V);
+  if (j == 0)
+    dalpha[n] = s;
+  else if (j == 1)
+    dbeta[n] = s;
+  else
+    dw_r[(size_t)n * V + j - 2] = s;
+}
+
+constexpr int kSms = 152;
+
+// Splits of a group's heads: the fewest rounds of steps over the SMs, a split more only for a gain.
+Plan make_plan(int B, int T, int N, int Nqk, int V) {
+  Plan p;
+  p.chunks = ssm_chunks(T);
+  p.vtiles = (V + VT - 1) / VT;
+  p.rep = N / Nqk;
+  p.splits = 1;
+  p.per_split = p.rep;
+  const long long base = (long long)B * Nqk * p.chunks;
+  double best = 1e30;
+  for (int s = 1; s <= p.rep && s <= 16; ++s) {
+    const int per = (p.rep + s - 1) / s, used = (p.rep + per - 1) / per;
+    if (used != s) continue;
+    const double cost = (double)((base * s + kSms - 1) / kSms) * (per + 0.5);
+    if (cost < 0.97 * best) best = cost, p.splits = s, p.per_split = per;
+  }
+  p.items = base * p.splits;
+  return p;
+}
+
+Workspace carve(float* ws, const Plan& plan, int B, int T, int N, int Nqk, int K, int V) {
   Workspace w;
-  w.hist = ws;
-  w.dq = w.hist + pairs * (kSsmChunk + 1) * kv;
-  w.dk = w.dq + tok;
-  w.par = w.dk + tok;
-  w.floats = pairs * (kSsmChunk + 1) * kv + 2 * tok + pairs * (2 + V);
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += (n + 3) / 4 * 4;
+    return ws ? ws + here : nullptr;
+  };
+  const size_t pairs = (size_t)B * N;
+  w.G = reinterpret_cast<uint16_t*>(take(pairs * plan.chunks * K * V));
+  w.segments = take(ssm_segment_floats(ssm_cut(B, T, N, V), B, N, K, V));
+  w.dots = take(pairs * (plan.chunks + 1) * plan.vtiles * 8);
+  w.par = take((size_t)B * plan.chunks * N * (2 + V));
+  const size_t part = plan.splits > 1 ? (size_t)plan.splits * B * T * Nqk * K : 0;
+  w.dqp = take(part);
+  w.dkp = take(part);
+  w.floats = at;
   return w;
 }
 
-__device__ __forceinline__ float block_sum(float s) {
-  __shared__ float part[kThreads];
-  __syncthreads();
-  part[threadIdx.x] = s;
-  __syncthreads();
-  float t = 0.f;
-  for (int i = 0; i < kThreads; ++i) t += part[i];
-  return t;
+// Tensor map of kept states [pairs][states][2][K][V] in boxes of one plane of 64 columns.
+bool state_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base, int K, int V, long long planes,
+               long long pairs, int kp) {
+  const cuuint64_t dims[4] = {(cuuint64_t)V, (cuuint64_t)K, (cuuint64_t)planes, (cuuint64_t)pairs};
+  const cuuint64_t strides[3] = {(cuuint64_t)V * 2, (cuuint64_t)K * V * 2, (cuuint64_t)K * V * 2 * planes};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)kp, 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-__global__ void __launch_bounds__(kThreads) ssm_backward_kernel(SsmBackwardProblem p, Workspace w) {
-  extern __shared__ float G[];  // [K][V]
-  __shared__ float sk[128], sq[128], sv[128], sdy[128];
-  const long long pair = blockIdx.x;
-  const int n = (int)(pair % p.N), c = threadIdx.x, K = p.K, V = p.V;
-  const long long b = pair / p.N;
-  const int head = (int)((long long)n * p.Nqk / p.N);
-  const int chunks = ssm_chunks(p.T);
-  const size_t KV = (size_t)K * V;
-  const bool live = c < V, krow = c < K;
-  float* hist = w.hist + (size_t)pair * (kSsmChunk + 1) * KV;
-  const float alpha = p.alpha[n], beta = p.beta[n];
-  const float wr = live ? p.w_r[(size_t)n * V + c] : 0.f;
-  for (int i = 0; i < K && live; ++i)
-    G[i * V + c] = p.dH_T ? p.dH_T[pair * KV + (size_t)i * V + c] : 0.f;
-  auto token = [&](int t, bool dy) {
-    __syncthreads();
-    if (krow) {
-      sk[c] = bf16_to_f(p.k[b * p.sk.batch + t * p.sk.token + (size_t)head * K + c]);
-      sq[c] = bf16_to_f(p.q[b * p.sq.batch + t * p.sq.token + (size_t)head * K + c]);
-    }
-    if (live) {
-      sv[c] = bf16_to_f(p.v[b * p.sv.batch + t * p.sv.token + (size_t)n * V + c]);
-      if (dy) sdy[c] = bf16_to_f(p.dy[((b * p.T + t) * p.N + n) * V + c]);
-    }
-    __syncthreads();
-  };
-  float dalpha = 0.f, dbeta = 0.f, dwr = 0.f;
-  for (int chunk = chunks - 1; chunk >= 0; --chunk) {
-    const int t0 = chunk * kSsmChunk, t1 = min(p.T, t0 + kSsmChunk);
-    const uint16_t* s = p.Hs + ((size_t)pair * (chunks + 1) + chunk) * 2 * KV;
-    for (int i = 0; i < K && live; ++i)
-      hist[(size_t)i * V + c] =
-          bf16_to_f(s[(size_t)i * V + c]) + bf16_to_f(s[KV + (size_t)i * V + c]);
-    for (int t = t0; t < t1; ++t) {
-      token(t, false);
-      const float2 gate = ssm_gate(bf16_to_f(p.a[b * p.sa.batch + t * p.sa.token + n]), alpha, beta);
-      const float f = expf(gate.y);
-      const float* h = hist + (size_t)(t - t0) * KV;
-      for (int i = 0; i < K && live; ++i)
-        hist[(size_t)(t - t0 + 1) * KV + (size_t)i * V + c] =
-            fmaf(f, h[(size_t)i * V + c], gate.x * sk[i] * sv[c]);
-    }
-    for (int t = t1 - 1; t >= t0; --t) {
-      token(t, true);
-      const float x = bf16_to_f(p.a[b * p.sa.batch + t * p.sa.token + n]) + beta;
-      const float2 gate = ssm_gate(x - beta, alpha, beta);
-      const float d = gate.x, f = expf(gate.y);
-      const float* hb = hist + (size_t)(t - t0) * KV;
-      const float* ha = hb + KV;
-      float dv = 0.f, g = 0.f;
-      for (int i = 0; i < K && live; ++i) {
-        const float gi = fmaf(sq[i], sdy[c], G[i * V + c]);
-        G[i * V + c] = gi;
-        dv = fmaf(gi, sk[i], dv);
-        g = fmaf(gi, hb[(size_t)i * V + c], g);
-      }
-      g = f * block_sum(g);
-      const size_t at = ((size_t)(b * p.T + t) * p.N + n);
-      float kgv = 0.f;
-      if (krow) {
-        float dq = 0.f, gv = 0.f;
-        for (int j = 0; j < V; ++j) {
-          dq = fmaf(ha[(size_t)c * V + j], sdy[j], dq);
-          gv = fmaf(G[c * V + j], sv[j], gv);
-        }
-        w.dq[at * K + c] = dq;
-        w.dk[at * K + c] = d * gv;
-        kgv = sk[c] * gv;
-      }
-      kgv = block_sum(kgv);
-      const float sig = 1.f / (1.f + expf(-x));
-      const float da = sig * (kgv - alpha * g);
-      if (c == 0) p.da[at] = f_to_bf16(da);
-      dalpha -= d * g;
-      dbeta += da;
-      if (live) {
-        p.dv[at * V + c] = f_to_bf16(fmaf(wr, sdy[c], d * dv));
-        dwr = fmaf(sdy[c], sv[c], dwr);
-        for (int i = 0; i < K; ++i) G[i * V + c] *= f;
-      }
-    }
-    __syncthreads();
-  }
-  float* par = w.par + pair * (2 + V);
-  if (c == 0) par[0] = dalpha, par[1] = dbeta;
-  if (live) par[2 + c] = dwr;
-  for (int i = 0; i < K && live && p.dH0; ++i) p.dH0[pair * KV + (size_t)i * V + c] = G[i * V + c];
-}
-
-// dq, dk of one (token, q/k head): the sum over the heads that read it.
-__global__ void __launch_bounds__(256)
-    sum_heads_kernel(SsmBackwardProblem p, Workspace w) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (long long)p.B * p.T * p.Nqk * p.K) return;
-  const int rep = p.N / p.Nqk, k = (int)(i % p.K);
-  const long long at = i / p.K;  // (b, t, head)
-  float dq = 0.f, dk = 0.f;
-  for (int r = 0; r < rep; ++r) {
-    dq += w.dq[(at * rep + r) * p.K + k];
-    dk += w.dk[(at * rep + r) * p.K + k];
-  }
-  p.dq[i] = f_to_bf16(dq);
-  p.dk[i] = f_to_bf16(dk);
-}
-
-__global__ void __launch_bounds__(128) sum_params_kernel(SsmBackwardProblem p, const float* par) {
-  const int n = blockIdx.x;
-  for (int c = threadIdx.x; c < 2 + p.V; c += 128) {
-    float s = 0.f;
-    for (int b = 0; b < p.B && p.T > 0; ++b) s += par[((size_t)b * p.N + n) * (2 + p.V) + c];
-    if (c == 0)
-      p.dalpha[n] = s;
-    else if (c == 1)
-      p.dbeta[n] = s;
-    else
-      p.dw_r[(size_t)n * p.V + c - 2] = s;
-  }
+template <int KP>
+cudaError_t run(const SsmBackwardProblem& p, const Plan& plan, const Workspace& w, bool vec, cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(ssm_backward_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<KP>::kBytes);
+  });
+  if (attr != cudaSuccess) return attr;
+  const EncodeTiledFn enc = tensor_map_encoder();
+  CUtensorMap mq{}, mk{}, mv{}, md{}, mh{}, mg{};
+  const long long pairs = (long long)p.B * p.N;
+  const Strides dense{(long long)p.T * p.N * p.V, (long long)p.N * p.V};
+  const bool tma = vec && enc && token_map(enc, &mq, p.q, p.K, p.Nqk, p.T, p.B, p.sq) &&
+                   token_map(enc, &mk, p.k, p.K, p.Nqk, p.T, p.B, p.sk) &&
+                   token_map(enc, &mv, p.v, p.V, p.N, p.T, p.B, p.sv) &&
+                   token_map(enc, &md, p.dy, p.V, p.N, p.T, p.B, dense) &&
+                   state_map(enc, &mh, p.Hs, p.K, p.V, 2LL * (plan.chunks + 1), pairs, KP) &&
+                   state_map(enc, &mg, w.G, p.K, p.V, 2LL * plan.chunks, pairs, KP);
+  const unsigned blocks = (unsigned)(plan.items < kSms ? plan.items : kSms);
+  ssm_backward_kernel<KP>
+      <<<blocks, kThreads, Smem<KP>::kBytes, stream>>>(mq, mk, mv, md, mh, mg, p, plan, w, tma, vec);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t ssm_backward_workspace_bytes(int B, int T, int N, int, int K, int V) {
-  return sizeof(float) * carve(nullptr, B, T, N, K, V).floats;
+size_t ssm_backward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V) {
+  return T > 0 ? sizeof(float) * carve(nullptr, make_plan(B, T, N, Nqk, V), B, T, N, Nqk, K, V).floats : 0;
 }
 
 cudaError_t launch_ssm_backward(const SsmBackwardProblem& p, cudaStream_t stream) {
-  const Workspace w = carve(p.ws, p.B, p.T, p.N, p.K, p.V);
-  const int smem = (int)sizeof(float) * p.K * p.V;
-  cudaError_t err = cudaFuncSetAttribute(ssm_backward_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t err = cudaSuccess;
+  if (p.T == 0) {  // the final state is the first
+    const size_t bytes = sizeof(float) * p.B * p.N * p.K * p.V;
+    if (p.dH0 && p.dH_T && p.dH0 != p.dH_T)
+      err = cudaMemcpyAsync(p.dH0, p.dH_T, bytes, cudaMemcpyDeviceToDevice, stream);
+    else if (p.dH0 && !p.dH_T)
+      err = cudaMemsetAsync(p.dH0, 0, bytes, stream);
+    if (err == cudaSuccess) err = cudaMemsetAsync(p.dalpha, 0, sizeof(float) * p.N, stream);
+    if (err == cudaSuccess) err = cudaMemsetAsync(p.dbeta, 0, sizeof(float) * p.N, stream);
+    if (err == cudaSuccess) err = cudaMemsetAsync(p.dw_r, 0, sizeof(float) * p.N * p.V, stream);
+    return err;
+  }
+  const Plan plan = make_plan(p.B, p.T, p.N, p.Nqk, p.V);
+  const Workspace w = carve(p.ws, plan, p.B, p.T, p.N, p.Nqk, p.K, p.V);
+  const Strides dense{(long long)p.T * p.N * p.V, (long long)p.N * p.V};
+  const bool vec = rows_of_16(p.q, p.sq, p.K) && rows_of_16(p.k, p.sk, p.K) && rows_of_16(p.v, p.sv, p.V) &&
+                   rows_of_16(p.dy, dense, p.V) && aligned_to(p.dq, 16) && aligned_to(p.dk, 16) &&
+                   aligned_to(p.dv, 16);
+  StateProblem s{p.q, p.dy, p.a, p.alpha, p.beta, p.sq, dense, p.sa, p.B, p.T, p.N, p.Nqk, p.K, p.V, p.dH_T};
+  s.status = p.status;
+  const SsmCut cut = ssm_cut(p.B, p.T, p.N, p.V);
+  if (cut.segments > 1) {
+    err = launch_ssm_segments(s, cut, true, vec, w.segments, stream);
+    if (err != cudaSuccess) return err;
+    s.from_state = w.segments;
+  }
+  s.to = p.dH0, s.kept = w.G, s.Hs = p.Hs, s.dots = w.dots;
+  err = launch_ssm_state_gradients(s, cut, vec, stream);
   if (err != cudaSuccess) return err;
-  ssm_backward_kernel<<<(unsigned)((long long)p.B * p.N), kThreads, smem, stream>>>(p, w);
-  const long long n = (long long)p.B * p.T * p.Nqk * p.K;
-  if (n > 0)
-    sum_heads_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, w);
-  sum_params_kernel<<<p.N, 128, 0, stream>>>(p, w.par);
+  err = p.K <= 64 ? run<64>(p, plan, w, vec, stream) : run<128>(p, plan, w, vec, stream);
+  if (err != cudaSuccess) return err;
+  if (plan.splits > 1) {
+    const long long n = (long long)p.B * p.T * p.Nqk * p.K;
+    sum_splits_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(w.dqp, w.dkp, p.dq, p.dk, plan.splits, n);
+  }
+  const int width = p.N * (2 + p.V);
+  sum_params_kernel<<<(width + 31) / 32, dim3(32, 32), 0, stream>>>(w.par, p.dalpha, p.dbeta, p.dw_r, p.B * plan.chunks,
+                                                                   p.N, p.V);
   return cudaGetLastError();
 }
 

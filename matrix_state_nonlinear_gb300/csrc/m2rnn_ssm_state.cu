@@ -134,13 +134,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < HC / 2; ++c) H[c] = make_float2(given(2 * c), given(2 * c + 1));
     float decay = 0.f;
     for (int i = 0; i <= count; ++i) {
-      // Where states are kept: the one before chunk i (of this order), and <it, Hs there>.
-      if (REVERSE && p.kept && i < count) {
-        const int chunk = chunk_at(i);
+      // Where states are kept: the one before chunk i (of this order), and <it, Hs there>; at the
+      // sequence's start the latter alone.
+      if (REVERSE && p.kept && (i < count || first == 0)) {
+        const int at_state = i < count ? chunk_at(i) + 1 : 0;  // of the forward's states
         float dot = 0.f;
         if (has_row) {
-          uint16_t* to = p.kept + ((size_t)pair * chunks + chunk) * 2 * plane + at;
-          const uint16_t* hs = p.Hs + ((size_t)pair * (chunks + 1) + chunk + 1) * 2 * plane + at;
+          uint16_t* to = p.kept + ((size_t)pair * chunks + at_state - 1) * 2 * plane + at;
+          const uint16_t* hs = p.Hs + ((size_t)pair * (chunks + 1) + at_state) * 2 * plane + at;
           float2 d2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < HC / 8; ++c) {
@@ -154,8 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               unpack8(*reinterpret_cast<const uint4*>(hs + plane + 8 * c), y);
 #pragma unroll
               for (int e = 0; e < 4; ++e) d2 = fma2(H[4 * c + e], add2(x[e], y[e]), d2);
-              *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              if (i < count) {
+                *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              }
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -163,8 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int k = 8 * c + e;
                   const float h = bf16_to_f(hs[k]) + bf16_to_f(hs[plane + k]);
                   dot = fmaf(e & 1 ? H[k / 2].y : H[k / 2].x, h, dot);
-                  to[k] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
-                  to[plane + k] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
+                  if (i < count) {
+                    to[k] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
+                    to[plane + k] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
+                  }
                 }
             }
           }
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        if (lane == 0) p.dots[(((size_t)pair * chunks + chunk) * vtiles + vt) * 8 + warp - kWarpState] = dot;
+        if (lane == 0) p.dots[(((size_t)pair * (chunks + 1) + at_state) * vtiles + vt) * 8 + warp - kWarpState] = dot;
       }
       if (i == count) break;
       wait(bar.gate[i & 3], i >> 2);
