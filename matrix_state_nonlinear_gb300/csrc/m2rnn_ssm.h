@@ -67,7 +67,7 @@ struct StateProblem {
   float* to;                // the last state (backwards: the first one's gradient), or null
   uint16_t* kept;           // backwards: G after every chunk, [pairs][chunks][2 (high, low)][K][V]
   const uint16_t* Hs;       // with it: the forward's states,
-  float* dots;              // and <G, H> at each of them, [pairs][chunks + 1][tiles of V][8 parts]
+  float* dots;              // and <G, H before the chunk>, [pairs][chunks][tiles of V][8 parts]
   int* status;
   int pieces, per, first_piece;  // set by the launches, as are
   float *to_state, *decay;

@@ -8,14 +8,16 @@
 //   dq = dS k + (exp(c) dy) H^T              dk = dS^T q + (w v) G^T,   w_s = exp(c_127 - c_s) d_s
 //   dv = P^T dy + w (k G) + w_r dy
 // and for the gate, with E_ts = P_ts (dy_t . v_s) over s < t,
-//   row_t = sum_s E_ts + exp(c_t) (q_t H) . dy_t,   col_s = sum_t E_ts + w_s (k_s G) . v_s,
-//   g_t = <G, H>_end + sum_{u >= t} (row_u - col_u)      (g_t = dL/dlog f_t)
-//   da = sigmoid (col + E_tt) / d - alpha sigmoid g,   dalpha = -sum d g,   dbeta = sum da
-// (<G, H> at a chunk's start replaces the first token's g: there is no sum behind it).
+//   r_u = exp(c_u) (q_u H) . dy_u,   l_s = w_s (k_s G) . v_s,
+//   g_t = dL/dlog f_t = exp(c_127) <G, H> + sum_{u >= t} r_u + sum_{s < t} l_s + sum_{u >= t > s} E_us
+//   da = sigmoid (l + sum_u E_us + E_ss) / d - alpha sigmoid g,   dalpha = -sum d g,   dbeta = sum da
+// g sums what passes token t, from the states and tokens before it to those after.  The last sum is
+// sum_{s < t} (column sum s - row sum s): only E itself, float32 and the same in both, cancels.
 //
-// Precision: the outputs dq, dk, dv are bf16 and so are the operands of their products (P, dS,
-// exp(c) dy, w v, H, G).  The gate's gradient ends in float32 sums over all tokens: E is float32
-// from float32 scores, and q H, k G take H and G as two bf16 values each.
+// Precision: dq, dk, dv are bf16, and one operand of each of their products is rounded to bf16 (P,
+// dS, exp(c) dy, w v); H and G enter as two bf16 values each.  The gate's gradient ends in float32
+// sums over all tokens: E is float32 from float32 scores, and q H, k G are float32 but for the 17
+// bits of H and G.
 //
 // One block is resident per SM (shared memory) and walks steps: one (head, value tile) of one
 // chunk.  Heads that share q and k are consecutive steps of one item, whose dq and dk add up in
@@ -482,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(bar.scaled1, j)) break;
       tc_fence_after();
       umma_steps<4, 2, 2>(leader, tmem + kColDq, desc_k(sc), desc_k(st), id_k, !first);
+      umma_steps<4, 2, 2>(leader, tmem + kColDq, desc_k(sc), desc_k(st + KP * VT * 2), id_k, true);
       if (!wait(bar.pds, j)) break;
       tc_fence_after();
       umma_steps<KP / 16, 2, 128, PANEL>(leader, tmem + kColS, desc_k(q), desc_mn(st, KP), id_st, false);
@@ -493,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       umma_steps<KP / 16, 2, 128, PANEL>(leader, tmem + kColDp, desc_k(k), desc_mn(st, KP), id_st, false);
       umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st), id_k, true);
+      umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st + KP * VT * 2), id_k, true);
       umma_commit_if(leader, &bar.gd);
       if (!wait(bar.q_read, j)) break;
       tc_fence_after();
@@ -600,48 +604,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(bar.sums, at.head_no)) break;
         const long long pair = (long long)at.b * p.N + at.head;
         const float alpha = p.alpha[at.head], beta = p.beta[at.head];
-        const float* dots = w.dots + ((size_t)pair * (plan.chunks + 1) + at.chunk) * plan.vtiles * 8;
-        float end = 0.f, begin = 0.f;
-        for (int i = 0; i < plan.vtiles * 8; ++i) begin += dots[i], end += dots[plan.vtiles * 8 + i];
-        // Tokens 4 lane .. 4 lane + 3: row - col, then its sums over the later tokens.
-        float diff[4], full[4], g[4];
+        const float* dots = w.dots + ((size_t)pair * plan.chunks + at.chunk) * plan.vtiles * 8;
+        float across = 0.f;
+        for (int i = 0; i < plan.vtiles * 8; ++i) across += dots[i];
+        // Tokens 4 lane .. 4 lane + 3: r, l + (column - row sum of E), and da's own sum.
+        float r[4], l[4], full[4];
         const int block = lane >> 3;  // of 32 tokens
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = 4 * lane + e;
-          float r = 0.f, c = 0.f;
+          float rs = 0.f, ls = 0.f, row = 0.f, col = 0.f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            r += sums.row_state[i][t] + (i <= block ? sums.row[i][t] : 0.f);
-            c += sums.col_state[i][t] + (i >= block ? sums.col[i][t] : 0.f);
+            rs += sums.row_state[i][t];
+            ls += sums.col_state[i][t];
+            if (i <= block) row += sums.row[i][t];
+            if (i >= block) col += sums.col[i][t];
           }
-          diff[e] = r - c;
-          full[e] = c + sums.diag[t];
+          r[e] = rs;
+          l[e] = ls + (col - row);
+          full[e] = ls + col + sums.diag[t];
         }
         warp_arrive(&bar.sums_free, lane);
-        g[3] = diff[3], g[2] = diff[2] + g[3], g[1] = diff[1] + g[2], g[0] = diff[0] + g[1];
-        float run = g[0];
+        // Sums of r over this token and the later ones, of l over the earlier ones.
+        r[2] += r[3], r[1] += r[2], r[0] += r[1];
+        const float l0 = l[0], l1 = l0 + l[1], l2 = l1 + l[2];
+        float after = r[0], before = l2 + l[3], total = 0.f;
+        float4 d;
+        {
+          const long long t0 = (long long)at.chunk * L + 4 * lane;
+          const uint16_t* ag = p.a + at.b * p.sa.batch + at.head;
+          float* pd = &d.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 g = ssm_gate(t0 + e < p.T ? bf16_to_f(ag[(t0 + e) * p.sa.token]) : -INFINITY, alpha, beta);
+            pd[e] = g.x;
+            total += g.y;
+          }
+        }
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
-          const float y = __shfl_down_sync(~0u, run, s);
-          if (lane + s < 32) run += y;
+          const float x = __shfl_down_sync(~0u, after, s), y = __shfl_up_sync(~0u, before, s);
+          if (lane + s < 32) after += x;
+          if (lane >= s) before += y;
+          total += __shfl_xor_sync(~0u, total, s);
         }
-        float after = __shfl_down_sync(~0u, run, 1);
+        after = __shfl_down_sync(~0u, after, 1), before = __shfl_up_sync(~0u, before, 1);
         if (lane == 31) after = 0.f;
+        if (lane == 0) before = 0.f;
+        across *= exp2_approx(total * kLog2e);
+        const float4 g = make_float4(across + (after + r[0]) + before, across + (after + r[1]) + (before + l0),
+                                     across + (after + r[2]) + (before + l1), across + (after + r[3]) + (before + l2));
         float dalpha = 0.f, dbeta = 0.f;
 #pragma unroll 1
         for (int e = 0; e < 4; ++e) {
           const long long t = (long long)at.chunk * L + 4 * lane + e;
           if (t >= p.T) break;
-          const float gt = 4 * lane + e == 0 ? begin : end + (after + (e == 0 ? g[0] : e == 1 ? g[1] : e == 2 ? g[2] : g[3]));
-          const float a = bf16_to_f(p.a[at.b * p.sa.batch + t * p.sa.token + at.head]);
-          const float x = a + beta, ex = expf(-fabsf(x));
+          const float gt = e == 0 ? g.x : e == 1 ? g.y : e == 2 ? g.z : g.w;
+          const float x = bf16_to_f(p.a[at.b * p.sa.batch + t * p.sa.token + at.head]) + beta, ex = expf(-fabsf(x));
           const float sig = x >= 0.f ? 1.f / (1.f + ex) : ex / (1.f + ex);
-          const float d = ssm_gate(a, alpha, beta).x;
           const float da = sigmoid_over_softplus(x) * (e == 0 ? full[0] : e == 1 ? full[1] : e == 2 ? full[2] : full[3]) -
                            alpha * sig * gt;
           p.da[((size_t)at.b * p.T + t) * p.N + at.head] = f_to_bf16(da);
-          dalpha -= d * gt;
+          dalpha -= (e == 0 ? d.x : e == 1 ? d.y : e == 2 ? d.z : d.w) * gt;
           dbeta += da;
         }
 #pragma unroll
@@ -735,7 +760,7 @@ Workspace carve(float* ws, const Plan& plan, int B, int T, int N, int Nqk, int K
   const size_t pairs = (size_t)B * N;
   w.G = reinterpret_cast<uint16_t*>(take(pairs * plan.chunks * K * V));
   w.segments = take(ssm_segment_floats(ssm_cut(B, T, N, V), B, N, K, V));
-  w.dots = take(pairs * (plan.chunks + 1) * plan.vtiles * 8);
+  w.dots = take(pairs * plan.chunks * plan.vtiles * 8);
   w.par = take((size_t)B * plan.chunks * N * (2 + V));
   const size_t part = plan.splits > 1 ? (size_t)plan.splits * B * T * Nqk * K : 0;
   w.dqp = take(part);

@@ -8,7 +8,7 @@
 //    pieces, each piece's own state from zero found side by side, and a second launch chains them
 //    into the state before (after) each; the main kernels start there;
 //  * the backward's first pass: G after every chunk, kept for the second as two bf16 values each,
-//    with <G, H> there, the sum that the gates' gradients start from.
+//    with <G, H>, H the state before the chunk: what reaches across it.
 // Products on the 5th-generation tensor cores: one of 128 x 16 steps per chunk, the weighted y in
 // two bf16 values (17 bits) side by side as its second operand.  Bound by the traffic of x and y,
 // 2 (K + V) bytes a token and head; warps by role as in the forward kernel.
@@ -134,14 +134,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < HC / 2; ++c) H[c] = make_float2(given(2 * c), given(2 * c + 1));
     float decay = 0.f;
     for (int i = 0; i <= count; ++i) {
-      // Where states are kept: the one before chunk i (of this order), and <it, Hs there>; at the
-      // sequence's start the latter alone.
-      if (REVERSE && p.kept && (i < count || first == 0)) {
-        const int at_state = i < count ? chunk_at(i) + 1 : 0;  // of the forward's states
+      // Where states are kept: G after the chunk, and <G, H> with H before it.
+      if (REVERSE && p.kept && i < count) {
+        const int chunk = chunk_at(i);
         float dot = 0.f;
         if (has_row) {
-          uint16_t* to = p.kept + ((size_t)pair * chunks + at_state - 1) * 2 * plane + at;
-          const uint16_t* hs = p.Hs + ((size_t)pair * (chunks + 1) + at_state) * 2 * plane + at;
+          uint16_t* to = p.kept + ((size_t)pair * chunks + chunk) * 2 * plane + at;
+          const uint16_t* hs = p.Hs + ((size_t)pair * (chunks + 1) + chunk) * 2 * plane + at;
           float2 d2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int c = 0; c < HC / 8; ++c) {
@@ -155,10 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               unpack8(*reinterpret_cast<const uint4*>(hs + plane + 8 * c), y);
 #pragma unroll
               for (int e = 0; e < 4; ++e) d2 = fma2(H[4 * c + e], add2(x[e], y[e]), d2);
-              if (i < count) {
-                *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
+              *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -166,10 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const int k = 8 * c + e;
                   const float h = bf16_to_f(hs[k]) + bf16_to_f(hs[plane + k]);
                   dot = fmaf(e & 1 ? H[k / 2].y : H[k / 2].x, h, dot);
-                  if (i < count) {
-                    to[k] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
-                    to[plane + k] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
-                  }
+                  to[k] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
+                  to[plane + k] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
                 }
             }
           }
@@ -177,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        if (lane == 0) p.dots[(((size_t)pair * (chunks + 1) + at_state) * vtiles + vt) * 8 + warp - kWarpState] = dot;
+        if (lane == 0) p.dots[(((size_t)pair * chunks + chunk) * vtiles + vt) * 8 + warp - kWarpState] = dot;
       }
       if (i == count) break;
       wait(bar.gate[i & 3], i >> 2);
