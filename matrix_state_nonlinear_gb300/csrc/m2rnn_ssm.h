@@ -65,8 +65,9 @@ struct StateProblem {
   const float* from;        // the first state (backwards: the last one's gradient), or null
   const float* from_state;  // or every segment's, [pairs][segments][K][V]
   float* to;                // the last state (backwards: the first one's gradient), or null
-  uint16_t* kept;           // backwards: G after every chunk, [pairs][chunks][2 (high, low)][K][V]
-  const uint16_t* Hs;       // with it: the forward's states,
+  uint16_t* kept;           // the state before every chunk and the last, [pairs][chunks + 1][2 (high,
+                            // low)][K][V]; backwards: G after every chunk, [pairs][chunks][2][K][V]
+  const uint16_t* Hs;       // with that: the forward's states,
   float* dots;              // and <G, H before the chunk>, [pairs][chunks][tiles of V][8 parts]
   int* status;
   int pieces, per, first_piece;  // set by the launches, as are
@@ -76,8 +77,8 @@ struct StateProblem {
 // ssm_segment_floats.
 cudaError_t launch_ssm_segments(StateProblem p, const SsmCut& c, bool reverse, bool vec, float* ws,
                                 cudaStream_t stream);
-// The backward's first pass: kept, dots and `to`, from `from` or from_state.
-cudaError_t launch_ssm_state_gradients(StateProblem p, const SsmCut& c, bool vec, cudaStream_t stream);
+// kept (backwards: dots too) and `to`, from `from` or from_state.
+cudaError_t launch_ssm_kept_states(StateProblem p, const SsmCut& c, bool reverse, bool vec, cudaStream_t stream);
 
 size_t ssm_forward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V);
 size_t ssm_backward_workspace_bytes(int B, int T, int N, int Nqk, int K, int V);

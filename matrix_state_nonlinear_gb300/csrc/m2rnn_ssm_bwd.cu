@@ -23,7 +23,8 @@
 // chunk.  Heads that share q and k are consecutive steps of one item, whose dq and dk add up in
 // tensor memory; items of many heads may be split (float32 parts, added in a fixed order).
 // Sixteen warps do each phase together (a row, i.e. token, per lane; 16 or 32 columns per warp),
-// four others issue products, load, make gates, and finish the gate's gradient.
+// four others issue products, load, store, and finish the gate's gradient.  A small launch before
+// computes every chunk's gates, and outputs leave through shared memory, whole rows at a time.
 #include <mutex>
 
 #include "m2rnn_ssm_tc.cuh"
@@ -33,11 +34,18 @@ namespace {
 
 constexpr int L = kTokens;
 constexpr int VT = kSsmColumns;
-constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpGate = 18, kWarps = 20;  // 0..15: element-wise; 19: the gate's gradient
+constexpr int kWarpMma = 16, kWarpLoad = 17, kWarpStore = 18, kWarps = 20;  // 0..15: element-wise; 19: the gate's gradient
 constexpr int kThreads = 32 * kWarps;
 
 // Tensor memory columns: q H and then P^T dy in the place of S, k G in the place of dP.
 constexpr int kColDq = 0, kColDk = 128, kColS = 256, kColDp = 384, kTmemCols = 512;
+
+// A chunk's gates in memory: what the products need, and per token sigmoid / d, alpha sigmoid, d.
+struct alignas(16) BackwardGates {
+  ChunkGates g;
+  float rho[L], asig[L], d[L];
+};
+static_assert(sizeof(BackwardGates) % 16 == 0, "");
 
 struct alignas(16) Sums {  // of a head's chunk, per token; parts by column group or quarter
   float row[4][L], row_state[4][L], col[4][L], col_state[4][L], diag[L];
@@ -52,7 +60,7 @@ struct Smem {
   static constexpr int kScaled = kState + 2 * KP * VT * 2;  // exp(c) dy, later w v
   static constexpr int kP = kScaled + kTile, kDs = kP + 2 * kTile;
   static constexpr int kGates = kDs + 2 * kTile;
-  static constexpr int kSums = kGates + 2 * (int)sizeof(ChunkGates);
+  static constexpr int kSums = kGates + 2 * (int)sizeof(BackwardGates);
   static constexpr int kBars = kSums + (int)sizeof(Sums);
   static constexpr int kBytes = kBars + 256 + 1024;  // and slack to align the tiles
   static_assert(kBytes <= 227 * 1024, "");
@@ -68,6 +76,7 @@ struct Bars {
   uint64_t acc_free;                // dq, dk read
   uint64_t gate[2], gate_free[2];
   uint64_t sums, sums_free;
+  uint64_t out, out_free;           // outputs in shared memory, on their way
   uint32_t tmem;
   int abort;
 };
@@ -81,6 +90,7 @@ struct Plan {
 };
 struct Workspace {
   float *segments, *dots, *par, *dqp, *dkp;
+  BackwardGates* gates;
   uint16_t* G;
   size_t floats;
 };
@@ -125,13 +135,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     ssm_backward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_dy,
                         const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_g,
-                        SsmBackwardProblem p, Plan plan, Workspace w, bool tma, bool vec) {
+                        const __grid_constant__ CUtensorMap map_dq, const __grid_constant__ CUtensorMap map_dk,
+                        const __grid_constant__ CUtensorMap map_dv, SsmBackwardProblem p, Plan plan, Workspace w,
+                        bool tma) {
   using S = Smem<KP>;
   constexpr int PANELS = KP / 64;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t base = smem_u32(smem);
-  ChunkGates* gates = reinterpret_cast<ChunkGates*>(smem + S::kGates);
+  BackwardGates* gates = reinterpret_cast<BackwardGates*>(smem + S::kGates);
   Sums& sums = *reinterpret_cast<Sums*>(smem + S::kSums);
   Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
   volatile int* abort = &bar.abort;
@@ -142,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.step_free, 16), mbar_init(&bar.scaled1, 16), mbar_init(&bar.scaled2, 16);
     mbar_init(&bar.s, 1), mbar_init(&bar.pds, 16), mbar_init(&bar.hd, 1), mbar_init(&bar.q_read, 16);
     mbar_init(&bar.gd, 1), mbar_init(&bar.done, 1), mbar_init(&bar.acc_free, 16);
-    for (int i = 0; i < 2; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 16);
-    mbar_init(&bar.sums, 16), mbar_init(&bar.sums_free, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 17);
+    mbar_init(&bar.sums, 16), mbar_init(&bar.sums_free, 1), mbar_init(&bar.out, 16), mbar_init(&bar.out_free, 1);
     bar.abort = 0;
     fence_mbar_init();
   }
@@ -165,13 +177,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
     const uint32_t tv = base + S::kV, td = base + S::kDy;
     const int c0 = 16 * group;  // this warp's 16 of the 64 value columns
+    bool sent_all = false;  // the step before sent dq and dk too
     for (int j = 0; more; ++j) {
       const int v0 = at.vt * VT, vw = min(VT, p.V - v0);
-      const long long t = (long long)at.chunk * L + row;
       if (at.vt == 0 && at.head_no > 0) wait(bar.sums_free, at.head_no - 1);
+      if (sent_all) wait(bar.out_free, j - 1);  // (the place of the scaled operand)
       wait(bar.gate[j & 1], j >> 1);
       if (!wait(bar.vd, j)) break;
-      const ChunkGates& G = gates[j & 1];
+      const ChunkGates& G = gates[j & 1].g;
       const float cum = G.cum[row], wk = G.wk[row];
       const float et = exp2_approx(cum);
       // exp(c) dy as an operand (and below w v, in the same place).
@@ -196,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       put_scaled(td, et, bar.scaled1);
 
       // P and dS from S and dP: block `group` of 32 columns against the quarter's own 32 rows.
+      if (j > 0 && !sent_all) wait(bar.out_free, j - 1);  // (the places of P and dS)
       if (!wait(bar.s, j)) break;
       tc_fence_after();
       {
@@ -399,33 +413,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bar.step_free);
           mbar_arrive(&bar.gate_free[j & 1]);
         }
+        // dv leaves through the first half of P's tile.
         const float* wr = p.w_r + (size_t)at.head * p.V + v0 + c0;
-        uint32_t o[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 w2 = make_float2(c0 + 2 * e < vw ? wr[2 * e] : 0.f, c0 + 2 * e + 1 < vw ? wr[2 * e + 1] : 0.f);
-          const float2 r = fma2(w2, y[e], add2(make_float2(a[2 * e], a[2 * e + 1]), x[e]));
-          o[e] = pack_bf16x2(r.x, r.y);
-        }
-        if (t < p.T) {
-          uint16_t* to = p.dv + (((size_t)at.b * p.T + t) * p.N + at.head) * p.V + v0 + c0;
-          if (vec) {
-            if (c0 < vw) *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (c0 + 8 < vw) *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-          } else {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (c0 + e < vw) to[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
+          for (int z = 0; z < 4; ++z) {
+            const int e = 4 * c + z;
+            const float2 w2 = make_float2(c0 + 2 * e < vw ? wr[2 * e] : 0.f, c0 + 2 * e + 1 < vw ? wr[2 * e + 1] : 0.f);
+            const float2 r = fma2(w2, y[e], add2(make_float2(a[2 * e], a[2 * e + 1]), x[e]));
+            o[z] = pack_bf16x2(r.x, r.y);
           }
+          st_shared_v4(Tile<64>::at(base + S::kP, row, 2 * group + c), make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
 
-      __syncwarp();
-
-      // dq, dk of the item.
-      if (at.last(plan)) {
+      // dq, dk of the item: bf16 through dS's tile, and the other half of P's and the scaled
+      // operand's; parts of a split item float32, a token per lane.
+      sent_all = at.last(plan);
+      if (sent_all) {
         constexpr int KC = KP / 4;  // columns per warp
-        const size_t to = ((size_t)at.b * p.T + t) * p.Nqk + at.group;
 #pragma unroll 1
         for (int c = 0; c < 2 * KC; c += 16) {
           const bool is_k = c >= KC;
@@ -433,31 +441,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           float a[16];
           tmem_ld16_nowait(t_lane + (is_k ? kColDk : kColDq) + col, a);
           tmem_wait_ld();
-          if (t >= p.T) {
-          } else if (plan.splits > 1) {
-            float* f = (is_k ? w.dkp : w.dqp) + ((size_t)at.split * p.B * p.T * p.Nqk + to) * p.K + col;
+          if (plan.splits > 1) {
+            float* f = (is_k ? w.dkp : w.dqp) + ((size_t)at.item * KP + col) * L + row;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (col + e < p.K) f[e] = a[e];
+            for (int e = 0; e < 16; ++e) f[e * L] = a[e];
           } else {
-            uint16_t* f = (is_k ? p.dk : p.dq) + to * p.K + col;
-            uint32_t o[8];
+            const uint32_t to = is_k ? (col < 64 ? base + S::kP + S::kTile : base + S::kScaled)
+                                     : base + S::kDs + (col >> 6) * S::kTile;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = pack_bf16x2(a[2 * e], a[2 * e + 1]);
-            if (vec) {
-              if (col < p.K) *reinterpret_cast<uint4*>(f) = make_uint4(o[0], o[1], o[2], o[3]);
-              if (col + 8 < p.K) *reinterpret_cast<uint4*>(f + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (col + e < p.K) f[e] = (uint16_t)(o[e >> 1] >> (16 * (e & 1)));
-            }
+            for (int x = 0; x < 2; ++x)
+              st_shared_v4(Tile<64>::at(to, row, ((col & 63) >> 3) + x),
+                           make_uint4(pack_bf16x2(a[8 * x], a[8 * x + 1]), pack_bf16x2(a[8 * x + 2], a[8 * x + 3]),
+                                      pack_bf16x2(a[8 * x + 4], a[8 * x + 5]), pack_bf16x2(a[8 * x + 6], a[8 * x + 7])));
           }
-          __syncwarp();
         }
         tc_fence_before();
-        warp_arrive(&bar.acc_free, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.acc_free);
       }
+      fence_proxy_async_smem();
+      warp_arrive(&bar.out, lane);
       more = at.next(plan, p.Nqk);
     }
   } else if (warp == kWarpMma) {  // ---------------------------------- products
@@ -530,6 +533,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           warp_arrive(&bar.qk, lane);
         }
       }
+      if (j >= 2 && !wait(bar.gate_free[j & 1], (j >> 1) - 1)) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar.gate[j & 1], sizeof(BackwardGates));
+        bulk_load(base + S::kGates + (j & 1) * (uint32_t)sizeof(BackwardGates), w.gates + pair * plan.chunks + at.chunk,
+                  sizeof(BackwardGates), &bar.gate[j & 1]);
+      }
       if (j > 0 && !wait(bar.step_free, j - 1)) break;
       if (tma) {
         if (lane == 0) {
@@ -545,6 +554,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(&bar.vd, lane);
       }
+      // The next step's tiles on their way to L2: they are loaded late, when their places are free.
+      if (tma && lane == 0) {
+        Cursor to = at;
+        if (to.next(plan, p.Nqk)) {
+          const int pair_to = to.b * p.N + to.head;
+          tma_prefetch_4d(&map_v, to.vt * VT, to.head, to.chunk * L, to.b);
+          tma_prefetch_4d(&map_dy, to.vt * VT, to.head, to.chunk * L, to.b);
+          for (int x = 0; x < 2; ++x) {
+            tma_prefetch_4d(&map_h, to.vt * VT, 0, 2 * to.chunk + x, pair_to);
+            tma_prefetch_4d(&map_g, to.vt * VT, 0, 2 * to.chunk + x, pair_to);
+          }
+          if (to.first(plan))
+            for (int x = 0; x < PANELS; ++x) {
+              tma_prefetch_4d(&map_q, 64 * x, to.group, to.chunk * L, to.b);
+              tma_prefetch_4d(&map_k, 64 * x, to.group, to.chunk * L, to.b);
+            }
+        }
+      }
+      __syncwarp();
       // H once the products with the step before's G are done, G once those with H are.
 #pragma unroll 1
       for (int s = 0; s < 2; ++s) {
@@ -560,13 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const uint16_t* src = s ? w.G + ((size_t)pair * plan.chunks + at.chunk) * 2 * plane
                                   : p.Hs + ((size_t)pair * (plan.chunks + 1) + at.chunk) * 2 * plane;
-          for (int x = 0; x < 2; ++x)
-            for (int id = lane; id < KP * 64; id += 32) {
-              const int r = id >> 6, c = id & 63;
-              st_shared_u16(Tile<64>::at(base + S::kState + x * KP * VT * 2, r, c >> 3) + (c & 7) * 2,
-                            r < p.K && c < vw ? src[x * plane + (size_t)r * p.V + v0 + c] : (uint16_t)0);
-            }
-          fence_proxy_async_smem();
+          copy_state<KP>(base + S::kState, src + v0, p.K, p.V, vw, lane);
           warp_arrive(full, lane);
         }
         __syncwarp();
@@ -576,99 +598,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Given up: whatever was started here arrives before the block ends (waits for what was not
     // started run out).
-    if (!ok && tma) {
-      uint64_t* all[4] = {&bar.qk, &bar.vd, &bar.h, &bar.g};
-      for (int s = 0; s < 4; ++s)
+    if (!ok) {
+      uint64_t* all[6] = {&bar.gate[0], &bar.gate[1], &bar.qk, &bar.vd, &bar.h, &bar.g};
+      for (int s = 0; s < (tma ? 6 : 2); ++s)
         for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(all[s], phase, kWaitLimitCycles / 64);
     }
-  } else if (warp == kWarpGate) {  // --------------------------------- gates
+  } else if (warp == kWarpStore) {  // -------------------------------- stores
     for (int j = 0; more; ++j) {
-      const uint16_t* ag = p.a + at.b * p.sa.batch + at.head;
-      const long long t0 = (long long)at.chunk * L + lane;
-      const int last = p.T;
-      float4 a;
-      a.x = t0 < last ? bf16_to_f(ag[t0 * p.sa.token]) : -INFINITY;
-      a.y = t0 + 32 < last ? bf16_to_f(ag[(t0 + 32) * p.sa.token]) : -INFINITY;
-      a.z = t0 + 64 < last ? bf16_to_f(ag[(t0 + 64) * p.sa.token]) : -INFINITY;
-      a.w = t0 + 96 < last ? bf16_to_f(ag[(t0 + 96) * p.sa.token]) : -INFINITY;
-      const float alpha = p.alpha[at.head], beta = p.beta[at.head];
-      if (j >= 2 && !wait(bar.gate_free[j & 1], (j >> 1) - 1)) break;
-      put_chunk_gates(
-          gates[j & 1], [&](int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }, alpha, beta, lane);
-      warp_arrive(&bar.gate[j & 1], lane);
+      if (!wait(bar.out, j)) break;
+      const int t0 = at.chunk * L, v0 = at.vt * VT;
+      const bool both = at.last(plan) && plan.splits == 1;
+      if (tma) {
+        tma_store_4d_if(lane == 0, &map_dv, base + S::kP, v0, at.head, t0, at.b);
+        if (both) {
+#pragma unroll
+          for (int x = 0; x < PANELS; ++x) {
+            tma_store_4d_if(lane == 0, &map_dq, base + S::kDs + x * S::kTile, 64 * x, at.group, t0, at.b);
+            tma_store_4d_if(lane == 0, &map_dk, x ? base + S::kScaled : base + S::kP + S::kTile, 64 * x, at.group, t0,
+                            at.b);
+          }
+        }
+        if (lane == 0) {
+          bulk_commit_group();
+          bulk_wait_group_read<0>();
+        }
+      } else {
+        const int rows = min(L, p.T - t0);
+        const size_t token = (size_t)at.b * p.T + t0;
+        copy_out(p.dv + (token * p.N + at.head) * p.V + v0, base + S::kP, (long long)p.N * p.V, rows, min(VT, p.V - v0),
+                 lane);
+        for (int x = 0; x < PANELS && both; ++x) {
+          const size_t to = (token * p.Nqk + at.group) * p.K + 64 * x;
+          copy_out(p.dq + to, base + S::kDs + x * S::kTile, (long long)p.Nqk * p.K, rows, p.K - 64 * x, lane);
+          copy_out(p.dk + to, x ? base + S::kScaled : base + S::kP + S::kTile, (long long)p.Nqk * p.K, rows, p.K - 64 * x,
+                   lane);
+        }
+      }
+      warp_arrive(&bar.out_free, lane);
       more = at.next(plan, p.Nqk);
     }
+    if (lane == 0) bulk_wait_group<0>();
   } else {  // -------------------------------------------------------- the gate's gradient
-    while (more) {
+    for (int j = 0; more; ++j) {
+      if (!wait(bar.gate[j & 1], j >> 1)) break;
       if (at.head_end(plan)) {
-        if (!wait(bar.sums, at.head_no)) break;
         const long long pair = (long long)at.b * p.N + at.head;
-        const float alpha = p.alpha[at.head], beta = p.beta[at.head];
+        const BackwardGates& G = gates[j & 1];
+        const float4 rho = reinterpret_cast<const float4*>(G.rho)[lane];
+        const float4 asig = reinterpret_cast<const float4*>(G.asig)[lane], d = reinterpret_cast<const float4*>(G.d)[lane];
         const float* dots = w.dots + ((size_t)pair * plan.chunks + at.chunk) * plan.vtiles * 8;
-        float across = 0.f;
-        for (int i = 0; i < plan.vtiles * 8; ++i) across += dots[i];
+        float across = lane < plan.vtiles * 8 ? dots[lane] * exp2_approx(G.g.total) : 0.f;  // at most 16 parts
+        if (!wait(bar.sums, at.head_no)) break;
         // Tokens 4 lane .. 4 lane + 3: r, l + (column - row sum of E), and da's own sum.
-        float r[4], l[4], full[4];
+        auto add = [](float4 a, const float* p, int lane) {
+          const float4 b = reinterpret_cast<const float4*>(p)[lane];
+          return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        };
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 r = zero, l = zero, row = zero, col = zero;
         const int block = lane >> 3;  // of 32 tokens
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = 4 * lane + e;
-          float rs = 0.f, ls = 0.f, row = 0.f, col = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            rs += sums.row_state[i][t];
-            ls += sums.col_state[i][t];
-            if (i <= block) row += sums.row[i][t];
-            if (i >= block) col += sums.col[i][t];
-          }
-          r[e] = rs;
-          l[e] = ls + (col - row);
-          full[e] = ls + col + sums.diag[t];
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          r = add(r, sums.row_state[i], lane);
+          l = add(l, sums.col_state[i], lane);
+          if (i <= block) row = add(row, sums.row[i], lane);
+          if (i >= block) col = add(col, sums.col[i], lane);
         }
+        float4 full = add(make_float4(l.x + col.x, l.y + col.y, l.z + col.z, l.w + col.w), sums.diag, lane);
         warp_arrive(&bar.sums_free, lane);
+        l = make_float4(l.x + (col.x - row.x), l.y + (col.y - row.y), l.z + (col.z - row.z), l.w + (col.w - row.w));
         // Sums of r over this token and the later ones, of l over the earlier ones.
-        r[2] += r[3], r[1] += r[2], r[0] += r[1];
-        const float l0 = l[0], l1 = l0 + l[1], l2 = l1 + l[2];
-        float after = r[0], before = l2 + l[3], total = 0.f;
-        float4 d;
-        {
-          const long long t0 = (long long)at.chunk * L + 4 * lane;
-          const uint16_t* ag = p.a + at.b * p.sa.batch + at.head;
-          float* pd = &d.x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 g = ssm_gate(t0 + e < p.T ? bf16_to_f(ag[(t0 + e) * p.sa.token]) : -INFINITY, alpha, beta);
-            pd[e] = g.x;
-            total += g.y;
-          }
-        }
+        r.z += r.w, r.y += r.z, r.x += r.y;
+        const float l1 = l.x + l.y, l2 = l1 + l.z;
+        float after = r.x, before = l2 + l.w;
 #pragma unroll
         for (int s = 1; s < 32; s <<= 1) {
           const float x = __shfl_down_sync(~0u, after, s), y = __shfl_up_sync(~0u, before, s);
           if (lane + s < 32) after += x;
           if (lane >= s) before += y;
-          total += __shfl_xor_sync(~0u, total, s);
+          across += __shfl_xor_sync(~0u, across, s);
         }
         after = __shfl_down_sync(~0u, after, 1), before = __shfl_up_sync(~0u, before, 1);
         if (lane == 31) after = 0.f;
         if (lane == 0) before = 0.f;
-        across *= exp2_approx(total * kLog2e);
-        const float4 g = make_float4(across + (after + r[0]) + before, across + (after + r[1]) + (before + l0),
-                                     across + (after + r[2]) + (before + l1), across + (after + r[3]) + (before + l2));
-        float dalpha = 0.f, dbeta = 0.f;
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          const long long t = (long long)at.chunk * L + 4 * lane + e;
-          if (t >= p.T) break;
-          const float gt = e == 0 ? g.x : e == 1 ? g.y : e == 2 ? g.z : g.w;
-          const float x = bf16_to_f(p.a[at.b * p.sa.batch + t * p.sa.token + at.head]) + beta, ex = expf(-fabsf(x));
-          const float sig = x >= 0.f ? 1.f / (1.f + ex) : ex / (1.f + ex);
-          const float da = sigmoid_over_softplus(x) * (e == 0 ? full[0] : e == 1 ? full[1] : e == 2 ? full[2] : full[3]) -
-                           alpha * sig * gt;
-          p.da[((size_t)at.b * p.T + t) * p.N + at.head] = f_to_bf16(da);
-          dalpha -= (e == 0 ? d.x : e == 1 ? d.y : e == 2 ? d.z : d.w) * gt;
-          dbeta += da;
-        }
+        const float4 g = make_float4(across + (after + r.x) + before, across + (after + r.y) + (before + l.x),
+                                     across + (after + r.z) + (before + l1), across + (after + r.w) + (before + l2));
+        const float4 da = make_float4(rho.x * full.x - asig.x * g.x, rho.y * full.y - asig.y * g.y,
+                                      rho.z * full.z - asig.z * g.z, rho.w * full.w - asig.w * g.w);
+        // (tokens past the sequence: d = 0, and every sum of theirs)
+        float dalpha = -(d.x * g.x + d.y * g.y + d.z * g.z + d.w * g.w), dbeta = da.x + da.y + da.z + da.w;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           dalpha += __shfl_xor_sync(~0u, dalpha, o);
@@ -678,7 +696,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* par = w.par + ((size_t)(at.b * plan.chunks + at.chunk) * p.N + at.head) * (2 + p.V);
           par[0] = dalpha, par[1] = dbeta;
         }
+        const long long t = (long long)at.chunk * L + 4 * lane;
+        uint16_t* to = p.da + ((size_t)at.b * p.T + t) * p.N + at.head;
+        if (t < p.T) to[0] = f_to_bf16(da.x);
+        if (t + 1 < p.T) to[p.N] = f_to_bf16(da.y);
+        if (t + 2 < p.T) to[2 * (size_t)p.N] = f_to_bf16(da.z);
+        if (t + 3 < p.T) to[3 * (size_t)p.N] = f_to_bf16(da.w);
       }
+      warp_arrive(&bar.gate_free[j & 1], lane);
       more = at.next(plan, p.Nqk);
     }
   }
@@ -691,16 +716,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
 }
 
-// dq, dk: the splits' parts added in order.
+// Every chunk's gates: a warp per chunk of a (batch, head) pair.
+__global__ void __launch_bounds__(128)
+    ssm_gates_kernel(SsmBackwardProblem p, BackwardGates* __restrict__ out, long long pairs, int chunks) {
+  const int lane = threadIdx.x & 31;
+  const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (id >= pairs * chunks) return;
+  const long long pair = id / chunks;
+  const int n = (int)(pair % p.N);
+  const uint16_t* ag = p.a + pair / p.N * p.sa.batch + n;
+  const long long t0 = id % chunks * L + lane;
+  const float alpha = p.alpha[n], beta = p.beta[n];
+  float a[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) a[e] = t0 + 32 * e < p.T ? bf16_to_f(ag[(t0 + 32 * e) * p.sa.token]) : -INFINITY;
+  BackwardGates& o = out[id];
+  put_chunk_gates(
+      o.g, [&](int e) { return e == 0 ? a[0] : e == 1 ? a[1] : e == 2 ? a[2] : a[3]; }, alpha, beta, lane);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = a[e] + beta, ex = expf(-fabsf(x));
+    const float sig = x >= 0.f ? 1.f / (1.f + ex) : ex / (1.f + ex);
+    o.rho[32 * e + lane] = sigmoid_over_softplus(x);
+    o.asig[32 * e + lane] = alpha * sig;
+    o.d[32 * e + lane] = ssm_gate(a[e], alpha, beta).x;
+  }
+}
+
+// dq, dk: the splits' parts [item][column][token] added in order; a block per chunk of a batch row
+// and q/k head, 32 columns at a time through shared memory.
 __global__ void __launch_bounds__(256)
     sum_splits_kernel(const float* __restrict__ dqp, const float* __restrict__ dkp, uint16_t* __restrict__ dq,
-                      uint16_t* __restrict__ dk, int splits, long long n) {
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float a = 0.f, b = 0.f;
-  for (int s = 0; s < splits; ++s) a += dqp[s * n + i], b += dkp[s * n + i];
-  dq[i] = f_to_bf16(a);
-  dk[i] = f_to_bf16(b);
+                      uint16_t* __restrict__ dk, Plan plan, int T, int Nqk, int K, int kp) {
+  __shared__ float part[32][L + 1];
+  const long long first = (long long)blockIdx.x * plan.splits;
+  const int chunk = blockIdx.x % plan.chunks, group = blockIdx.x / plan.chunks % Nqk;
+  const long long b = blockIdx.x / plan.chunks / Nqk;
+  const float* src = blockIdx.y ? dkp : dqp;
+  uint16_t* dst = (blockIdx.y ? dk : dq) + ((b * T + (long long)chunk * L) * Nqk + group) * K;
+  const int rows = min(L, T - chunk * L);
+  for (int c0 = 0; c0 < K; c0 += 32) {
+    for (int id = threadIdx.x; id < 32 * L; id += 256) {
+      const int c = id / L, r = id % L;
+      float s = 0.f;
+      for (int i = 0; i < plan.splits; ++i) s += src[((first + i) * kp + c0 + c) * L + r];
+      part[c][r] = s;
+    }
+    __syncthreads();
+    for (int id = threadIdx.x; id < 32 * L; id += 256) {
+      const int r = id / 32, c = id % 32;
+      if (r < rows && c0 + c < K) dst[(long long)r * Nqk * K + c0 + c] = f_to_bf16(part[c][r]);
+    }
+    __syncthreads();
+  }
 }
 
 // Sums over the batch's chunks of the parts [rows][N][2 + V]: 32 columns by 32 slices of rows per
@@ -762,23 +830,12 @@ Workspace carve(float* ws, const Plan& plan, int B, int T, int N, int Nqk, int K
   w.segments = take(ssm_segment_floats(ssm_cut(B, T, N, V), B, N, K, V));
   w.dots = take(pairs * plan.chunks * plan.vtiles * 8);
   w.par = take((size_t)B * plan.chunks * N * (2 + V));
-  const size_t part = plan.splits > 1 ? (size_t)plan.splits * B * T * Nqk * K : 0;
+  w.gates = reinterpret_cast<BackwardGates*>(take(pairs * plan.chunks * (sizeof(BackwardGates) / 4)));
+  const size_t part = plan.splits > 1 ? (size_t)plan.items * (K <= 64 ? 64 : 128) * L : 0;
   w.dqp = take(part);
   w.dkp = take(part);
   w.floats = at;
   return w;
-}
-
-// Tensor map of kept states [pairs][states][2][K][V] in boxes of one plane of 64 columns.
-bool state_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base, int K, int V, long long planes,
-               long long pairs, int kp) {
-  const cuuint64_t dims[4] = {(cuuint64_t)V, (cuuint64_t)K, (cuuint64_t)planes, (cuuint64_t)pairs};
-  const cuuint64_t strides[3] = {(cuuint64_t)V * 2, (cuuint64_t)K * V * 2, (cuuint64_t)K * V * 2 * planes};
-  const cuuint32_t box[4] = {64u, (cuuint32_t)kp, 1u, 1u};
-  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KP>
@@ -791,18 +848,23 @@ cudaError_t run(const SsmBackwardProblem& p, const Plan& plan, const Workspace& 
   });
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
-  CUtensorMap mq{}, mk{}, mv{}, md{}, mh{}, mg{};
+  CUtensorMap mq{}, mk{}, mv{}, md{}, mh{}, mg{}, mdq{}, mdk{}, mdv{};
   const long long pairs = (long long)p.B * p.N;
   const Strides dense{(long long)p.T * p.N * p.V, (long long)p.N * p.V};
+  const Strides dense_k{(long long)p.T * p.Nqk * p.K, (long long)p.Nqk * p.K};
   const bool tma = vec && enc && token_map(enc, &mq, p.q, p.K, p.Nqk, p.T, p.B, p.sq) &&
                    token_map(enc, &mk, p.k, p.K, p.Nqk, p.T, p.B, p.sk) &&
                    token_map(enc, &mv, p.v, p.V, p.N, p.T, p.B, p.sv) &&
                    token_map(enc, &md, p.dy, p.V, p.N, p.T, p.B, dense) &&
                    state_map(enc, &mh, p.Hs, p.K, p.V, 2LL * (plan.chunks + 1), pairs, KP) &&
-                   state_map(enc, &mg, w.G, p.K, p.V, 2LL * plan.chunks, pairs, KP);
+                   state_map(enc, &mg, w.G, p.K, p.V, 2LL * plan.chunks, pairs, KP) &&
+                   token_map(enc, &mdq, p.dq, p.K, p.Nqk, p.T, p.B, dense_k) &&
+                   token_map(enc, &mdk, p.dk, p.K, p.Nqk, p.T, p.B, dense_k) &&
+                   token_map(enc, &mdv, p.dv, p.V, p.N, p.T, p.B, dense);
+  ssm_gates_kernel<<<(unsigned)((pairs * plan.chunks + 3) / 4), 128, 0, stream>>>(p, w.gates, pairs, plan.chunks);
   const unsigned blocks = (unsigned)(plan.items < kSms ? plan.items : kSms);
   ssm_backward_kernel<KP>
-      <<<blocks, kThreads, Smem<KP>::kBytes, stream>>>(mq, mk, mv, md, mh, mg, p, plan, w, tma, vec);
+      <<<blocks, kThreads, Smem<KP>::kBytes, stream>>>(mq, mk, mv, md, mh, mg, mdq, mdk, mdv, p, plan, w, tma);
   return cudaGetLastError();
 }
 
@@ -840,14 +902,13 @@ cudaError_t launch_ssm_backward(const SsmBackwardProblem& p, cudaStream_t stream
     s.from_state = w.segments;
   }
   s.to = p.dH0, s.kept = w.G, s.Hs = p.Hs, s.dots = w.dots;
-  err = launch_ssm_state_gradients(s, cut, vec, stream);
+  err = launch_ssm_kept_states(s, cut, true, vec, stream);
   if (err != cudaSuccess) return err;
   err = p.K <= 64 ? run<64>(p, plan, w, vec, stream) : run<128>(p, plan, w, vec, stream);
   if (err != cudaSuccess) return err;
-  if (plan.splits > 1) {
-    const long long n = (long long)p.B * p.T * p.Nqk * p.K;
-    sum_splits_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(w.dqp, w.dkp, p.dq, p.dk, plan.splits, n);
-  }
+  if (plan.splits > 1)
+    sum_splits_kernel<<<dim3((unsigned)(plan.items / plan.splits), 2), 256, 0, stream>>>(
+        w.dqp, w.dkp, p.dq, p.dk, plan, p.T, p.Nqk, p.K, p.K <= 64 ? 64 : 128);
   const int width = p.N * (2 + p.V);
   sum_params_kernel<<<(width + 31) / 32, dim3(32, 32), 0, stream>>>(w.par, p.dalpha, p.dbeta, p.dw_r, p.B * plan.chunks,
                                                                    p.N, p.V);

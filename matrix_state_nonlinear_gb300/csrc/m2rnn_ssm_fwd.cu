@@ -277,40 +277,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 #pragma unroll
     for (int c = 0; c < HC / 2; ++c) H[c] = make_float2(first_state(2 * c), first_state(2 * c + 1));
-    uint16_t* kept = p.Hs ? p.Hs + (size_t)pair * (chunks + 1) * 2 * plane + (size_t)hrow * p.V + v0 + hcol : nullptr;
-    // The state before chunk i as the bf16 operand and, where it is kept, as two bf16 values.
-    auto put_state = [&](int i) {
+    // The state as the next product's bf16 operand.
+    auto put_state = [&]() {
       if (KP <= 64 && lane >= 16) return;
-      const bool keep = kept && has_row && (i < count || first + count == chunks);
-      uint16_t* to = kept + (size_t)(first + i) * 2 * plane;
 #pragma unroll
       for (int c = 0; c < HC / 8; ++c) {
-        uint32_t hi[4], lo[4];
+        uint32_t hi[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) hi[e] = pack_bf16x2(H[4 * c + e].x, H[4 * c + e].y);
         st_shared_v4(Tile<VT>::at(base + S::kH, hrow, hcol / 8 + c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        if (!keep) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 r = sub2(H[4 * c + e], bf16x2_to_float2(hi[e]));
-          lo[e] = pack_bf16x2(r.x, r.y);
-        }
-        if (vec) {
-          if (hcol + 8 * c < vw) {
-            *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (hcol + 8 * c + e < vw) {
-              to[8 * c + e] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
-              to[plane + 8 * c + e] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
-            }
-        }
       }
     };
-    put_state(0);
+    put_state();
     fence_proxy_async_smem();
     warp_arrive(&bar.h, lane);
     for (int i = 0; i < count; ++i) {
@@ -337,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar.gate_free[i & 3]);
       }
       if (!wait(bar.q, i)) break;  // q H of this chunk still reads the state's tile
-      put_state(i + 1);
+      put_state();
       fence_proxy_async_smem();
       warp_arrive(&bar.h, lane);
     }
@@ -483,10 +461,18 @@ cudaError_t launch_ssm_forward(const SsmProblem& p, cudaStream_t stream) {
   const bool vec = rows_of_16(p.q, p.sq, p.K) && rows_of_16(p.k, p.sk, p.K) && rows_of_16(p.v, p.sv, p.V) &&
                    aligned_to(p.y, 16);
   const SsmCut cut = ssm_cut(p.B, p.T, p.N, p.V);
-  if (cut.segments > 1) {
+  if (cut.segments > 1 || p.Hs) {
     StateProblem s{p.k, p.v, p.a, p.alpha, p.beta, p.sk, p.sv, p.sa, p.B, p.T, p.N, p.Nqk, p.K, p.V, p.H0};
     s.status = p.status;
-    const cudaError_t err = launch_ssm_segments(s, cut, false, vec, p.ws, stream);
+    cudaError_t err = cudaSuccess;
+    if (cut.segments > 1) {
+      err = launch_ssm_segments(s, cut, false, vec, p.ws, stream);
+      s.from_state = p.ws;
+    }
+    if (err == cudaSuccess && p.Hs) {
+      s.kept = p.Hs;
+      err = launch_ssm_kept_states(s, cut, false, vec && aligned_to(p.Hs, 16), stream);
+    }
     if (err != cudaSuccess) return err;
   }
   return p.K <= 64 ? run<64>(p, cut, vec, stream) : run<128>(p, cut, vec, stream);

@@ -7,8 +7,9 @@
 //  * pieces: where there are fewer (batch, head) pairs than SMs, a pair's sequence is cut into
 //    pieces, each piece's own state from zero found side by side, and a second launch chains them
 //    into the state before (after) each; the main kernels start there;
-//  * the backward's first pass: G after every chunk, kept for the second as two bf16 values each,
-//    with <G, H>, H the state before the chunk: what reaches across it.
+//  * a training step's states: H before every chunk for the backward; and the backward's first
+//    pass, G after every chunk, with <G, H>, H the state before the chunk: what reaches across it.
+//    Kept as two bf16 values each, through shared memory so that whole rows leave at once.
 // Products on the 5th-generation tensor cores: one of 128 x 16 steps per chunk, the weighted y in
 // two bf16 values (17 bits) side by side as its second operand.  Bound by the traffic of x and y,
 // 2 (K + V) bytes a token and head; warps by role as in the forward kernel.
@@ -31,13 +32,15 @@ struct alignas(16) Weights {
   float total;  // log2 of the chunk's decay
 };
 
-template <int KP>
+template <int KP, bool KEEP>
 struct Smem {
-  static constexpr int kStages = 3;
+  static constexpr int kStages = KEEP && KP > 64 ? 2 : 3;
   static constexpr int kX = L * KP * 2, kY = L * VT * 2;
   static constexpr int kStage = kX + kY;
   static constexpr int kW = kStages * kStage;  // weighted y, high and low
-  static constexpr int kWeights = kW + 2 * kY;
+  static constexpr int kKept = kW + 2 * kY;  // a state on its way out, high and low; and H on its way in
+  static constexpr int kHs = kKept + (KEEP ? 2 * KP * VT * 2 : 0);
+  static constexpr int kWeights = kHs + (KEEP ? 2 * KP * VT * 2 : 0);
   static constexpr int kBars = kWeights + 4 * (int)sizeof(Weights);
   static constexpr int kBytes = kBars + 256 + 1024;
 };
@@ -46,15 +49,17 @@ struct Bars {
   uint64_t full[3], empty[3];
   uint64_t gate[4], gate_free[4];
   uint64_t u, u_free, w;  // U done, read; weighted y written
+  uint64_t put, put_free, hs, hs_free;  // kept state written, on its way; H loaded, read
   uint32_t tmem;
   int abort;
 };
 
-template <int KP, bool REVERSE>
+template <int KP, bool REVERSE, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_state_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y,
-                     StateProblem p, bool tma, bool vec) {
-  using S = Smem<KP>;
+                     const __grid_constant__ CUtensorMap map_kept, const __grid_constant__ CUtensorMap map_hs,
+                     StateProblem p, bool tma) {
+  using S = Smem<KP, KEEP>;
   constexpr int ST = S::kStages, PANELS = KP / 64;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -79,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 8);
     mbar_init(&bar.u, 1), mbar_init(&bar.u_free, 8), mbar_init(&bar.w, 8);
+    mbar_init(&bar.put, 8), mbar_init(&bar.put_free, 1), mbar_init(&bar.hs, 1), mbar_init(&bar.hs_free, 8);
     bar.abort = 0;
     fence_mbar_init();
   }
@@ -134,45 +140,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < HC / 2; ++c) H[c] = make_float2(given(2 * c), given(2 * c + 1));
     float decay = 0.f;
     for (int i = 0; i <= count; ++i) {
-      // Where states are kept: G after the chunk, and <G, H> with H before it.
-      if (REVERSE && p.kept && i < count) {
-        const int chunk = chunk_at(i);
-        float dot = 0.f;
-        if (has_row) {
-          uint16_t* to = p.kept + ((size_t)pair * chunks + chunk) * 2 * plane + at;
-          const uint16_t* hs = p.Hs + ((size_t)pair * (chunks + 1) + chunk) * 2 * plane + at;
-          float2 d2 = make_float2(0.f, 0.f);
+      // The state before chunk i (of this order; forwards, the last state too) to its tile;
+      // backwards its product with H as well.
+      if (KEEP && (i < count || (!REVERSE && first + count == chunks))) {
+        if (i > 0 && !wait(bar.put_free, i - 1)) break;
+        if (REVERSE && !wait(bar.hs, i)) break;
+        float2 d2 = make_float2(0.f, 0.f);
+        if (KP > 64 || lane < 16) {
 #pragma unroll
           for (int c = 0; c < HC / 8; ++c) {
-            if (hcol + 8 * c >= vw) break;
+            const uint32_t o = Tile<VT>::at(0, hrow, hcol / 8 + c);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) split_bf16x2(H[4 * c + e], hi[e], lo[e]);
-            if (vec) {
+            st_shared_v4(base + S::kKept + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            st_shared_v4(base + S::kKept + KP * VT * 2 + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+            if (REVERSE) {
               float2 x[4], y[4];
-              unpack8(*reinterpret_cast<const uint4*>(hs + 8 * c), x);
-              unpack8(*reinterpret_cast<const uint4*>(hs + plane + 8 * c), y);
+              unpack8(ld_shared_v4(base + S::kHs + o), x);
+              unpack8(ld_shared_v4(base + S::kHs + KP * VT * 2 + o), y);
 #pragma unroll
               for (int e = 0; e < 4; ++e) d2 = fma2(H[4 * c + e], add2(x[e], y[e]), d2);
-              *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(to + plane + 8 * c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (hcol + 8 * c + e < vw) {
-                  const int k = 8 * c + e;
-                  const float h = bf16_to_f(hs[k]) + bf16_to_f(hs[plane + k]);
-                  dot = fmaf(e & 1 ? H[k / 2].y : H[k / 2].x, h, dot);
-                  to[k] = (uint16_t)(hi[e >> 1] >> (16 * (e & 1)));
-                  to[plane + k] = (uint16_t)(lo[e >> 1] >> (16 * (e & 1)));
-                }
             }
           }
-          dot += d2.x + d2.y;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.put);
+          if (REVERSE) mbar_arrive(&bar.hs_free);
+        }
+        if (REVERSE) {
+          float dot = d2.x + d2.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        if (lane == 0) p.dots[(((size_t)pair * chunks + chunk) * vtiles + vt) * 8 + warp - kWarpState] = dot;
+          for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+          if (lane == 0) p.dots[(((size_t)pair * chunks + chunk_at(i)) * vtiles + vt) * 8 + warp - kWarpState] = dot;
+        }
       }
       if (i == count) break;
       wait(bar.gate[i & 3], i >> 2);
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok) {
-      if (p.decay && vt == 0 && warp == kWarpState && lane == 0) p.decay[pair * p.pieces + piece] = decay;
+      if (!KEEP && p.decay && vt == 0 && warp == kWarpState && lane == 0) p.decay[pair * p.pieces + piece] = decay;
       float* dst = p.to_state                         ? p.to_state + ((size_t)pair * p.pieces + piece) * plane
                    : p.to && (REVERSE ? first == 0 : first + count == chunks) ? p.to + pair * plane
                                                                               : nullptr;
@@ -215,6 +218,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = umma_idesc_bf16_ab(KP, 2 * VT, true, true);
     const uint64_t dw = desc_mn(base + S::kW, L);
     const bool leader = lane == 0;
+    // A kept state to memory, state `chunk` of the sequence forwards, after chunk `chunk` backwards.
+    auto send = [&](int i) {
+      if (!wait(bar.put, i)) return false;
+      const int chunk = REVERSE ? chunk_at(i) : first + i;
+      if (tma) {
+        for (int x = 0; x < 2; ++x)
+          tma_store_4d_if(leader, &map_kept, base + S::kKept + x * KP * VT * 2, v0, 0, 2 * chunk + x, (int)pair);
+        if (leader) {
+          bulk_commit_group();
+          bulk_wait_group_read<0>();
+        }
+      } else {
+        uint16_t* to = p.kept + ((size_t)pair * (REVERSE ? chunks : chunks + 1) + chunk) * 2 * plane + v0;
+        for (int id = lane; id < 2 * KP * VT; id += 32) {
+          const int x = id / (KP * VT), r = id / VT % KP, c = id % VT;
+          if (r < p.K && c < vw) {
+            const uint32_t u = ld_shared_u32(Tile<VT>::at(base + S::kKept + x * KP * VT * 2, r, c >> 3) + (c & 6) * 2);
+            to[x * plane + (size_t)r * p.V + c] = (uint16_t)(c & 1 ? u >> 16 : u);
+          }
+        }
+      }
+      warp_arrive(&bar.put_free, lane);
+      return true;
+    };
     for (int i = 0; i < count; ++i) {
       if (i > 0) wait(bar.u_free, i - 1);
       wait(bar.full[i % ST], i / ST);
@@ -223,7 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_steps<L / 16, 128, 128>(leader, tmem, desc_mn(stage(i), L), dw, idesc, false);
       umma_commit_if(leader, &bar.u);
       umma_commit_if(leader, &bar.empty[i % ST]);
+      if (KEEP && !send(i)) break;
     }
+    if (KEEP && ok && !REVERSE && first + count == chunks) send(count);
+    if (KEEP && leader) bulk_wait_group<0>();
   } else if (warp == kWarpLoad) {  // -------------------------------- loads
     for (int i = 0; i < count; ++i) {
       if (i >= ST && !wait(bar.empty[i % ST], i / ST - 1)) break;
@@ -249,7 +279,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(&bar.full[i % ST], lane);
       }
+      if (KEEP && REVERSE) {
+        if (i > 0 && !wait(bar.hs_free, i - 1)) break;
+        if (tma) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar.hs, 2 * KP * VT * 2);
+            for (int x = 0; x < 2; ++x)
+              tma_load_4d(smem + S::kHs + x * KP * VT * 2, &map_hs, &bar.hs, v0, 0, 2 * chunk_at(i) + x, (int)pair);
+          }
+          __syncwarp();
+        } else {
+          copy_state<KP>(base + S::kHs, p.Hs + ((size_t)pair * (chunks + 1) + chunk_at(i)) * 2 * plane + v0, p.K, p.V, vw,
+                         lane);
+          warp_arrive(&bar.hs, lane);
+        }
+      }
     }
+    if (!ok && tma && KEEP && REVERSE)
+      for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.hs, phase, kWaitLimitCycles / 64);
     if (!ok && tma)  // given up: whatever was started here arrives before the block ends
       for (int s = 0; s < ST; ++s)
         for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
@@ -338,27 +385,32 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int KP, bool REVERSE>
+template <int KP, bool REVERSE, bool KEEP>
 cudaError_t run(const StateProblem& p, int blocks_y, bool vec, cudaStream_t stream) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(ssm_state_kernel<KP, REVERSE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<KP>::kBytes);
+    attr = cudaFuncSetAttribute(ssm_state_kernel<KP, REVERSE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<KP, KEEP>::kBytes);
   });
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
-  CUtensorMap mx{}, my{};
-  const bool tma = vec && enc && p.T > 0 && token_map(enc, &mx, p.x, p.K, p.Nqk, p.T, p.B, p.sx) &&
-                   token_map(enc, &my, p.y, p.V, p.N, p.T, p.B, p.sy);
-  const unsigned units = (unsigned)((long long)p.B * p.N * ((p.V + VT - 1) / VT));
-  ssm_state_kernel<KP, REVERSE><<<dim3(units, blocks_y), kThreads, Smem<KP>::kBytes, stream>>>(mx, my, p, tma, vec);
+  CUtensorMap mx{}, my{}, mk{}, mh{};
+  const long long pairs = (long long)p.B * p.N, chunks = ssm_chunks(p.T);
+  bool tma = vec && enc && p.T > 0 && token_map(enc, &mx, p.x, p.K, p.Nqk, p.T, p.B, p.sx) &&
+             token_map(enc, &my, p.y, p.V, p.N, p.T, p.B, p.sy);
+  if (KEEP)
+    tma = tma && state_map(enc, &mk, p.kept, p.K, p.V, 2 * (REVERSE ? chunks : chunks + 1), pairs, KP) &&
+          (!REVERSE || state_map(enc, &mh, p.Hs, p.K, p.V, 2 * (chunks + 1), pairs, KP));
+  const unsigned units = (unsigned)(pairs * ((p.V + VT - 1) / VT));
+  ssm_state_kernel<KP, REVERSE, KEEP>
+      <<<dim3(units, blocks_y), kThreads, Smem<KP, KEEP>::kBytes, stream>>>(mx, my, mk, mh, p, tma);
   return cudaGetLastError();
 }
 
-cudaError_t run_any(const StateProblem& p, int blocks_y, bool reverse, bool vec, cudaStream_t stream) {
-  if (p.K <= 64) return reverse ? run<64, true>(p, blocks_y, vec, stream) : run<64, false>(p, blocks_y, vec, stream);
-  return reverse ? run<128, true>(p, blocks_y, vec, stream) : run<128, false>(p, blocks_y, vec, stream);
+template <bool REVERSE, bool KEEP>
+cudaError_t run_any(const StateProblem& p, int blocks_y, bool vec, cudaStream_t stream) {
+  return p.K <= 64 ? run<64, REVERSE, KEEP>(p, blocks_y, vec, stream) : run<128, REVERSE, KEEP>(p, blocks_y, vec, stream);
 }
 
 }  // namespace
@@ -394,20 +446,21 @@ cudaError_t launch_ssm_segments(StateProblem p, const SsmCut& c, bool reverse, b
   p.first_piece = reverse ? 1 : 0;  // the last piece of the order ends the sequence: not needed
   p.to_state = ws;
   p.decay = ws + (size_t)pairs * c.segments * kv;
-  const cudaError_t err = run_any(p, c.segments - 1, reverse, vec, stream);
+  const cudaError_t err = reverse ? run_any<true, false>(p, c.segments - 1, vec, stream)
+                                  : run_any<false, false>(p, c.segments - 1, vec, stream);
   if (err != cudaSuccess) return err;
   ssm_join_kernel<<<dim3((kv + 255) / 256, (unsigned)pairs), 256, 0, stream>>>(from, ws, p.decay, c.segments, kv,
                                                                                reverse);
   return cudaGetLastError();
 }
 
-cudaError_t launch_ssm_state_gradients(StateProblem p, const SsmCut& c, bool vec, cudaStream_t stream) {
+cudaError_t launch_ssm_kept_states(StateProblem p, const SsmCut& c, bool reverse, bool vec, cudaStream_t stream) {
   p.pieces = c.segments;
   p.per = c.per;
   p.first_piece = 0;
   p.to_state = nullptr;
   p.decay = nullptr;
-  return run_any(p, c.segments, true, vec, stream);
+  return reverse ? run_any<true, true>(p, c.segments, vec, stream) : run_any<false, true>(p, c.segments, vec, stream);
 }
 
 }  // namespace m2rnn

@@ -72,6 +72,21 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+// Copies `bytes` (a multiple of 16) of consecutive memory into shared memory; completion as
+// transaction bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// Starts the fetch of a box into L2, where a later load will find it.
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
 // Tensor map of a bf16 operand [B][T][heads][width] with free token and batch strides, in boxes of
 // 128 tokens by 64 columns of one head, 128-byte swizzled; what lies outside is read as zero.
 inline bool token_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base, int width, int heads, int T, int B,
@@ -96,6 +111,38 @@ __device__ __forceinline__ void copy_tokens(uint32_t tile, const uint16_t* src, 
 }
 
 constexpr int kTokens = kSsmChunk;  // 128: a chunk is one row of every product per token
+
+// Tensor map of kept states [pairs][planes][K][V] in boxes of kp rows of 64 columns of one plane.
+inline bool state_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base, int K, int V, long long planes,
+                      long long pairs, int kp) {
+  const cuuint64_t dims[4] = {(cuuint64_t)V, (cuuint64_t)K, (cuuint64_t)planes, (cuuint64_t)pairs};
+  const cuuint64_t strides[3] = {(cuuint64_t)V * 2, (cuuint64_t)K * V * 2, (cuuint64_t)K * V * 2 * planes};
+  const cuuint32_t box[4] = {64u, (cuuint32_t)kp, 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// A state's two planes [K][V] into two tiles of KP rows, by one warp, value by value.
+template <int KP>
+__device__ __forceinline__ void copy_state(uint32_t tile, const uint16_t* src, int K, int V, int width, int lane) {
+  for (int id = lane; id < 2 * KP * 64; id += 32) {
+    const int x = id / (KP * 64), r = id / 64 % KP, c = id % 64;
+    st_shared_u16(Tile<64>::at(tile + x * KP * 128, r, c >> 3) + (c & 7) * 2,
+                  r < K && c < width ? src[((size_t)x * K + r) * V + c] : (uint16_t)0);
+  }
+  fence_proxy_async_smem();
+}
+// One warp copies tokens of a swizzled tile to memory, value by value: row r to dst + r * stride.
+__device__ __forceinline__ void copy_out(uint16_t* dst, uint32_t tile, long long stride, int rows, int width, int lane) {
+  for (int id = lane; id < kSsmChunk * 64; id += 32) {
+    const int r = id >> 6, c = id & 63;
+    if (r < rows && c < width) {
+      const uint32_t u = ld_shared_u32(Tile<64>::at(tile, r, c >> 3) + (c & 6) * 2);
+      dst[r * stride + c] = (uint16_t)(c & 1 ? u >> 16 : u);
+    }
+  }
+}
 
 // What the products of a chunk need of its gates, per token.  Blocks are of 32 tokens.
 struct alignas(16) ChunkGates {
