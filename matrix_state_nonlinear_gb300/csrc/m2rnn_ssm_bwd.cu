@@ -248,23 +248,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               rows += sum.x + sum.y;
             } else {
+              // (a masked pair has decay 2^-infinity)
+              const float4* w4 = reinterpret_cast<const float4*>(G.diag + 32 * group + 16 * x);
+              const int own = lane - 16 * x;  // the token's own column of these
+              float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
               for (int z = 0; z < 8; ++z) {
-                float pv[2], sv[2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const int k = 2 * z + y, col = 16 * x + k;
-                  const float m = col <= lane ? exp2_approx(cum - G.diag[32 * group + col]) : 0.f;
-                  pv[y] = col <= lane ? sc[k] * m : 0.f;
-                  sv[y] = col <= lane ? dp[k] * m : 0.f;
-                  const float ev = pv[y] * dp[k];
-                  if (col == lane) diag = ev;
-                  e[k] = col < lane ? ev : 0.f;
-                  rows += e[k];
-                }
-                po[x][z] = pack_bf16x2(pv[0], pv[1]);
-                so[x][z] = pack_bf16x2(sv[0], sv[1]);
+                const float4 wv = w4[z >> 1];
+                const float x0 = cum - (z & 1 ? wv.z : wv.x), x1 = cum - (z & 1 ? wv.w : wv.y);
+                const float2 m = make_float2(exp2_approx(2 * z <= own ? x0 : -INFINITY),
+                                             exp2_approx(2 * z + 1 <= own ? x1 : -INFINITY));
+                const float2 d = make_float2(dp[2 * z], dp[2 * z + 1]);
+                const float2 pv = mul2(make_float2(sc[2 * z], sc[2 * z + 1]), m), sv = mul2(d, m);
+                float2 ev = mul2(pv, d);
+                diag = 2 * z == own ? ev.x : 2 * z + 1 == own ? ev.y : diag;
+                ev.x = 2 * z == own ? 0.f : ev.x;
+                ev.y = 2 * z + 1 == own ? 0.f : ev.y;
+                sum = add2(sum, ev);
+                e[2 * z] = ev.x, e[2 * z + 1] = ev.y;
+                po[x][z] = pack_bf16x2(pv.x, pv.y);
+                so[x][z] = pack_bf16x2(sv.x, sv.y);
               }
+              rows += sum.x + sum.y;
             }
             // Column sums over the warp's 32 rows: E through this block's own place in the tile of P
             // (then of dS), read back four columns and four rows per lane, then across eight lanes.
@@ -744,7 +749,7 @@ __global__ void __launch_bounds__(128)
 }
 
 // dq, dk: the splits' parts [item][column][token] added in order; a block per chunk of a batch row
-// and q/k head, 32 columns at a time through shared memory.
+// and q/k head and 32 columns, which turn through shared memory.
 __global__ void __launch_bounds__(256)
     sum_splits_kernel(const float* __restrict__ dqp, const float* __restrict__ dkp, uint16_t* __restrict__ dq,
                       uint16_t* __restrict__ dk, Plan plan, int T, int Nqk, int K, int kp) {
@@ -755,19 +760,18 @@ __global__ void __launch_bounds__(256)
   const float* src = blockIdx.y ? dkp : dqp;
   uint16_t* dst = (blockIdx.y ? dk : dq) + ((b * T + (long long)chunk * L) * Nqk + group) * K;
   const int rows = min(L, T - chunk * L);
-  for (int c0 = 0; c0 < K; c0 += 32) {
-    for (int id = threadIdx.x; id < 32 * L; id += 256) {
-      const int c = id / L, r = id % L;
-      float s = 0.f;
-      for (int i = 0; i < plan.splits; ++i) s += src[((first + i) * kp + c0 + c) * L + r];
-      part[c][r] = s;
-    }
-    __syncthreads();
-    for (int id = threadIdx.x; id < 32 * L; id += 256) {
-      const int r = id / 32, c = id % 32;
-      if (r < rows && c0 + c < K) dst[(long long)r * Nqk * K + c0 + c] = f_to_bf16(part[c][r]);
-    }
-    __syncthreads();
+  const int c0 = 32 * blockIdx.z;
+#pragma unroll 4
+  for (int id = threadIdx.x; id < 32 * L; id += 256) {
+    const int c = id / L, r = id % L;
+    float s = 0.f;
+    for (int i = 0; i < plan.splits; ++i) s += src[((first + i) * kp + c0 + c) * L + r];
+    part[c][r] = s;
+  }
+  __syncthreads();
+  for (int id = threadIdx.x; id < 32 * L; id += 256) {
+    const int r = id / 32, c = id % 32;
+    if (r < rows && c0 + c < K) dst[(long long)r * Nqk * K + c0 + c] = f_to_bf16(part[c][r]);
   }
 }
 
@@ -907,7 +911,7 @@ cudaError_t launch_ssm_backward(const SsmBackwardProblem& p, cudaStream_t stream
   err = p.K <= 64 ? run<64>(p, plan, w, vec, stream) : run<128>(p, plan, w, vec, stream);
   if (err != cudaSuccess) return err;
   if (plan.splits > 1)
-    sum_splits_kernel<<<dim3((unsigned)(plan.items / plan.splits), 2), 256, 0, stream>>>(
+    sum_splits_kernel<<<dim3((unsigned)(plan.items / plan.splits), 2, (p.K + 31) / 32), 256, 0, stream>>>(
         w.dqp, w.dkp, p.dq, p.dk, plan, p.T, p.Nqk, p.K, p.K <= 64 ? 64 : 128);
   const int width = p.N * (2 + p.V);
   sum_params_kernel<<<(width + 31) / 32, dim3(32, 32), 0, stream>>>(w.par, p.dalpha, p.dbeta, p.dw_r, p.B * plan.chunks,
