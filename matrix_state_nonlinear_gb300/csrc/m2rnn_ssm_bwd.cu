@@ -70,7 +70,7 @@ struct Smem {
 // phase needs its waiters to have passed the one before.
 struct Bars {
   uint64_t qk, vd, h, g;            // tiles loaded
-  uint64_t step_free;               // v, dy, and the accumulators of the step read
+  uint64_t step_free, vd_read;      // the step's accumulators, v and dy read
   uint64_t scaled1, scaled2;        // exp(c) dy, w v written
   uint64_t s, pds, hd, q_read, gd, done;  // S, dP done; P, dS written; q H done, read; k G done; P^T dy done
   uint64_t acc_free;                // dq, dk read
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const size_t plane = (size_t)p.K * p.V;
   if (tid == 0) {
     mbar_init(&bar.qk, 1), mbar_init(&bar.vd, 1), mbar_init(&bar.h, 1), mbar_init(&bar.g, 1);
-    mbar_init(&bar.step_free, 16), mbar_init(&bar.scaled1, 16), mbar_init(&bar.scaled2, 16);
+    mbar_init(&bar.step_free, 16), mbar_init(&bar.vd_read, 16), mbar_init(&bar.scaled1, 16), mbar_init(&bar.scaled2, 16);
     mbar_init(&bar.s, 1), mbar_init(&bar.pds, 16), mbar_init(&bar.hd, 1), mbar_init(&bar.q_read, 16);
     mbar_init(&bar.gd, 1), mbar_init(&bar.done, 1), mbar_init(&bar.acc_free, 16);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 17);
@@ -188,14 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float cum = G.cum[row], wk = G.wk[row];
       const float et = exp2_approx(cum);
       // exp(c) dy as an operand (and below w v, in the same place).
-      auto put_scaled = [&](uint32_t from, float f, uint64_t& ready) {
+      auto put_scaled = [&](const uint4 (&from)[2], float f, uint64_t& ready) {
         const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint32_t a = Tile<VT>::at(0, row, 2 * group + c);
           float2 x[4];
           uint32_t o[4];
-          unpack8(ld_shared_v4(from + a), x);
+          unpack8(from[c], x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 y = mul2(x[e], f2);
@@ -206,113 +206,116 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         warp_arrive(&ready, lane);
       };
-      put_scaled(td, et, bar.scaled1);
+      {
+        const uint4 dr[2] = {ld_shared_v4(Tile<VT>::at(td, row, 2 * group)),
+                             ld_shared_v4(Tile<VT>::at(td, row, 2 * group + 1))};
+        put_scaled(dr, et, bar.scaled1);
+      }
 
-      // P and dS from S and dP: block `group` of 32 columns against the quarter's own 32 rows.
+      // P and dS from S and dP, 16 columns at a time: pieces `group` and 7 - group of eight, so that
+      // no warp of a quarter has both of the masked ones.
       if (j > 0 && !sent_all) wait(bar.out_free, j - 1);  // (the places of P and dS)
       if (!wait(bar.s, j)) break;
       tc_fence_after();
       {
-        const uint32_t tp = base + S::kP + (group >> 1) * S::kTile, ts = base + S::kDs + (group >> 1) * S::kTile;
-        const int ch = 4 * (group & 1);  // the block's first 16-byte chunk of a row
         float rows = 0.f, diag = 0.f;
-        if (group > quarter) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            st_shared_v4(Tile<64>::at(tp, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
-            st_shared_v4(Tile<64>::at(ts, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
-          }
-        } else {
-          uint32_t po[2][8], so[2][8];
-          const float u = exp2_approx(cum - G.cum[32 * group + 31]);
-          const float2 u2 = make_float2(u, u);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {  // 16 columns at a time
-            float sc[16], dp[16], e[16];
-            tmem_ld16_nowait(t_lane + kColS + 32 * group + 16 * x, sc);
-            tmem_ld16_nowait(t_lane + kColDp + 32 * group + 16 * x, dp);
-            tmem_wait_ld();
-            if (group < quarter) {
-              const float4* w4 = reinterpret_cast<const float4*>(G.wd + 32 * group + 16 * x);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int z = 0; z < 8; ++z) {
-                const float4 wv = w4[z >> 1];
-                const float2 m = mul2(u2, z & 1 ? make_float2(wv.z, wv.w) : make_float2(wv.x, wv.y));
-                const float2 d = make_float2(dp[2 * z], dp[2 * z + 1]);
-                const float2 pv = mul2(make_float2(sc[2 * z], sc[2 * z + 1]), m), sv = mul2(d, m), ev = mul2(pv, d);
-                sum = add2(sum, ev);
-                e[2 * z] = ev.x, e[2 * z + 1] = ev.y;
-                po[x][z] = pack_bf16x2(pv.x, pv.y);
-                so[x][z] = pack_bf16x2(sv.x, sv.y);
-              }
-              rows += sum.x + sum.y;
-            } else {
-              // (a masked pair has decay 2^-infinity)
-              const float4* w4 = reinterpret_cast<const float4*>(G.diag + 32 * group + 16 * x);
-              const int own = lane - 16 * x;  // the token's own column of these
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int z = 0; z < 8; ++z) {
-                const float4 wv = w4[z >> 1];
-                const float x0 = cum - (z & 1 ? wv.z : wv.x), x1 = cum - (z & 1 ? wv.w : wv.y);
-                const float2 m = make_float2(exp2_approx(2 * z <= own ? x0 : -INFINITY),
-                                             exp2_approx(2 * z + 1 <= own ? x1 : -INFINITY));
-                const float2 d = make_float2(dp[2 * z], dp[2 * z + 1]);
-                const float2 pv = mul2(make_float2(sc[2 * z], sc[2 * z + 1]), m), sv = mul2(d, m);
-                float2 ev = mul2(pv, d);
-                diag = 2 * z == own ? ev.x : 2 * z + 1 == own ? ev.y : diag;
-                ev.x = 2 * z == own ? 0.f : ev.x;
-                ev.y = 2 * z + 1 == own ? 0.f : ev.y;
-                sum = add2(sum, ev);
-                e[2 * z] = ev.x, e[2 * z + 1] = ev.y;
-                po[x][z] = pack_bf16x2(pv.x, pv.y);
-                so[x][z] = pack_bf16x2(sv.x, sv.y);
-              }
-              rows += sum.x + sum.y;
-            }
-            // Column sums over the warp's 32 rows: E through this block's own place in the tile of P
-            // (then of dS), read back four columns and four rows per lane, then across eight lanes.
-            const uint32_t scratch = x ? ts : tp;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              st_shared_v4(Tile<64>::at(scratch, row, ch + c),
-                           make_uint4(__float_as_uint(e[4 * c]), __float_as_uint(e[4 * c + 1]),
-                                      __float_as_uint(e[4 * c + 2]), __float_as_uint(e[4 * c + 3])));
-            __syncwarp();
-            float2 a01 = make_float2(0.f, 0.f), a23 = a01;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint4 q = ld_shared_v4(Tile<64>::at(scratch, 32 * quarter + (lane >> 2) + 8 * r, ch + (lane & 3)));
-              a01 = add2(a01, make_float2(__uint_as_float(q.x), __uint_as_float(q.y)));
-              a23 = add2(a23, make_float2(__uint_as_float(q.z), __uint_as_float(q.w)));
-            }
-            const bool up = lane & 16, mid = lane & 8;
-            float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
-            k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
-            k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
-            float k = mid ? k1 : k0;
-            k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
-            k += __shfl_xor_sync(~0u, k, 4);
-            if (!(lane & 4)) {
-              float& to = sums.col[quarter][32 * group + 16 * x + 4 * (lane & 3) + (up ? 2 : 0) + (mid ? 1 : 0)];
-              to = at.vt ? to + k : k;
-            }
-            __syncwarp();
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int piece = x ? 7 - group : group, block = piece >> 1, ch = 2 * (piece & 3);
+          const uint32_t tp = base + S::kP + (piece >> 2) * S::kTile, ts = base + S::kDs + (piece >> 2) * S::kTile;
+          if (block > quarter) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              st_shared_v4(Tile<64>::at(tp, row, ch + 2 * x + c),
-                           make_uint4(po[x][4 * c], po[x][4 * c + 1], po[x][4 * c + 2], po[x][4 * c + 3]));
-              st_shared_v4(Tile<64>::at(ts, row, ch + 2 * x + c),
-                           make_uint4(so[x][4 * c], so[x][4 * c + 1], so[x][4 * c + 2], so[x][4 * c + 3]));
+              st_shared_v4(Tile<64>::at(tp, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
+              st_shared_v4(Tile<64>::at(ts, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
             }
-          float& to = sums.row[group][row];
-          to = at.vt ? to + rows : rows;
-          if (group == quarter) sums.diag[row] = at.vt ? sums.diag[row] + diag : diag;
+            continue;
+          }
+          float sc[16], dp[16];
+          uint32_t po[8], so[8];
+          tmem_ld16_nowait(t_lane + kColS + 16 * piece, sc);
+          tmem_ld16_nowait(t_lane + kColDp + 16 * piece, dp);
+          float2 m[8];
+          int own = -1;  // the token's own column of these
+          if (block < quarter) {
+            const float u = exp2_approx(cum - G.cum[32 * block + 31]);
+            const float2 u2 = make_float2(u, u);
+            const float4* w4 = reinterpret_cast<const float4*>(G.wd + 16 * piece);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float4 wv = w4[z];
+              m[2 * z] = mul2(u2, make_float2(wv.x, wv.y));
+              m[2 * z + 1] = mul2(u2, make_float2(wv.z, wv.w));
+            }
+          } else {  // a masked pair has decay 2^-infinity
+            own = lane - 16 * (piece & 1);
+            const float4* w4 = reinterpret_cast<const float4*>(G.diag + 16 * piece);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float4 wv = w4[z];
+              m[2 * z] = make_float2(exp2_approx(4 * z <= own ? cum - wv.x : -INFINITY),
+                                     exp2_approx(4 * z + 1 <= own ? cum - wv.y : -INFINITY));
+              m[2 * z + 1] = make_float2(exp2_approx(4 * z + 2 <= own ? cum - wv.z : -INFINITY),
+                                         exp2_approx(4 * z + 3 <= own ? cum - wv.w : -INFINITY));
+            }
+          }
+          tmem_ready(sc, dp);
+          // E (into sc) = P dP.
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            const float2 d = make_float2(dp[2 * z], dp[2 * z + 1]);
+            const float2 pv = mul2(make_float2(sc[2 * z], sc[2 * z + 1]), m[z]), sv = mul2(d, m[z]);
+            float2 ev = mul2(pv, d);
+            po[z] = pack_bf16x2(pv.x, pv.y);
+            so[z] = pack_bf16x2(sv.x, sv.y);
+            if (block == quarter) {
+              diag = 2 * z == own ? ev.x : 2 * z + 1 == own ? ev.y : diag;
+              ev.x = 2 * z == own ? 0.f : ev.x;
+              ev.y = 2 * z + 1 == own ? 0.f : ev.y;
+            }
+            sum = add2(sum, ev);
+            sc[2 * z] = ev.x, sc[2 * z + 1] = ev.y;
+          }
+          rows += sum.x + sum.y;
+          // Column sums over the warp's 32 rows: E through this piece's own place in the tiles of P
+          // (columns 0 .. 7) and dS, read back four columns and four rows per lane, then across
+          // eight lanes.
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_shared_v4(Tile<64>::at(c < 2 ? tp : ts, row, ch + (c & 1)),
+                         make_uint4(__float_as_uint(sc[4 * c]), __float_as_uint(sc[4 * c + 1]),
+                                    __float_as_uint(sc[4 * c + 2]), __float_as_uint(sc[4 * c + 3])));
+          __syncwarp();
+          float2 a01 = make_float2(0.f, 0.f), a23 = a01;
+          const uint32_t from = lane & 2 ? ts : tp;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint4 q = ld_shared_v4(Tile<64>::at(from, 32 * quarter + (lane >> 2) + 8 * r, ch + (lane & 1)));
+            a01 = add2(a01, make_float2(__uint_as_float(q.x), __uint_as_float(q.y)));
+            a23 = add2(a23, make_float2(__uint_as_float(q.z), __uint_as_float(q.w)));
+          }
+          const bool up = lane & 16, mid = lane & 8;
+          float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
+          k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
+          k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
+          float k = mid ? k1 : k0;
+          k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
+          k += __shfl_xor_sync(~0u, k, 4);
+          if (!(lane & 4)) {
+            float& to = sums.col[quarter][16 * piece + 4 * (lane & 3) + (up ? 2 : 0) + (mid ? 1 : 0)];
+            to = at.vt ? to + k : k;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            st_shared_v4(Tile<64>::at(tp, row, ch + c), make_uint4(po[4 * c], po[4 * c + 1], po[4 * c + 2], po[4 * c + 3]));
+            st_shared_v4(Tile<64>::at(ts, row, ch + c), make_uint4(so[4 * c], so[4 * c + 1], so[4 * c + 2], so[4 * c + 3]));
+          }
+          if (own >= 0 && own < 16) sums.diag[row] = at.vt ? sums.diag[row] + diag : diag;
         }
+        float& to = sums.row[group][row];
+        to = at.vt ? to + rows : rows;
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -340,6 +343,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           w.par[((size_t)(at.b * plan.chunks + at.chunk) * p.N + at.head) * (2 + p.V) + 2 + v0 + col] = k;
       }
 
+      // This token's v and dy, 16 columns: from here on their tiles are the products' alone.
+      uint4 vr[2], dr[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        vr[c] = ld_shared_v4(Tile<VT>::at(tv, row, 2 * group + c));
+        dr[c] = ld_shared_v4(Tile<VT>::at(td, row, 2 * group + c));
+      }
+      warp_arrive(&bar.vd_read, lane);
+
       // The state's part of the row sums: exp(c) (q H) . dy.
       if (!wait(bar.hd, j)) break;
       tc_fence_after();
@@ -351,11 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float2 x[4];
-          unpack8(ld_shared_v4(Tile<VT>::at(td, row, 2 * group + c)), x);
+          unpack8(dr[c], x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[4 * c + e] = x[e];
         }
-        tmem_wait_ld();
+        tmem_ready(hi, lo);
         tc_fence_before();
         warp_arrive(&bar.q_read, lane);
         float2 dot = make_float2(0.f, 0.f);
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float r = et * (dot.x + dot.y);
         to = at.vt ? to + r : r;
       }
-      put_scaled(tv, wk, bar.scaled2);
+      put_scaled(vr, wk, bar.scaled2);
 
       // k G: its part of the column sums, and of dv.
       float2 x[8];
@@ -380,11 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float2 f[4];
-          unpack8(ld_shared_v4(Tile<VT>::at(tv, row, 2 * group + c)), f);
+          unpack8(vr[c], f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[4 * c + e] = f[e];
         }
-        tmem_wait_ld();
+        tmem_ready(hi, lo);
         const float2 w2 = make_float2(wk, wk);
         float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
@@ -407,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float2 f[4];
-          unpack8(ld_shared_v4(Tile<VT>::at(td, row, 2 * group + c)), f);
+          unpack8(dr[c], f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[4 * c + e] = f[e];
         }
-        tmem_wait_ld();
+        tmem_ready(a);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int col = KC * group + (is_k ? c - KC : c);
           float a[16];
           tmem_ld16_nowait(t_lane + (is_k ? kColDk : kColDq) + col, a);
-          tmem_wait_ld();
+          tmem_ready(a);
           if (plan.splits > 1) {
             float* f = (is_k ? w.dkp : w.dqp) + ((size_t)at.item * KP + col) * L + row;
 #pragma unroll
@@ -544,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_load(base + S::kGates + (j & 1) * (uint32_t)sizeof(BackwardGates), w.gates + pair * plan.chunks + at.chunk,
                   sizeof(BackwardGates), &bar.gate[j & 1]);
       }
-      if (j > 0 && !wait(bar.step_free, j - 1)) break;
+      if (j > 0) wait(bar.vd_read, j - 1);
+      if (j > 0 && !wait(bar.done, j - 1)) break;
       if (tma) {
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar.vd, 2 * S::kTile);
@@ -666,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           r = add(r, sums.row_state[i], lane);
           l = add(l, sums.col_state[i], lane);
-          if (i <= block) row = add(row, sums.row[i], lane);
+          row = add(row, sums.row[i], lane);
           if (i >= block) col = add(col, sums.col[i], lane);
         }
         float4 full = add(make_float4(l.x + col.x, l.y + col.y, l.z + col.z, l.w + col.w), sums.diag, lane);

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float u = exp2_approx(cum - G.cum[32 * cb + 31]);
             const float2 u2 = make_float2(u, u);
             const float4* w = reinterpret_cast<const float4*>(G.wd + col);
-            tmem_wait_ld();
+            tmem_ready(s);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float4 wv = w[e];
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
             const float4* w = reinterpret_cast<const float4*>(G.diag + col);
-            tmem_wait_ld();
+            tmem_ready(s);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float4 wv = w[e];
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16_nowait(t_lane + kColY2 + 16 * x, y2);
         const uint4 va = ld_shared_v4(Tile<VT>::at(tv, row, 2 * x)), vb = ld_shared_v4(Tile<VT>::at(tv, row, 2 * x + 1));
         const float4* w4 = reinterpret_cast<const float4*>(wr + 16 * x);
-        tmem_wait_ld();
+        tmem_ready(y1, y2);
         if (x & 1) {
           tc_fence_before();
           warp_arrive(&bar.y_free, lane);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float hi[16], lo[16];
         tmem_ld16_nowait(t_lane + kColU + hcol + 16 * x, hi);
         tmem_ld16_nowait(t_lane + kColU + VT + hcol + 16 * x, lo);
-        tmem_wait_ld();
+        tmem_ready(hi, lo);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           H[8 * x + c] = fma2(e2, H[8 * x + c], add2(make_float2(hi[2 * c], hi[2 * c + 1]),
@@ -382,6 +382,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(at + S::kQ + panel(x, L), &map_k, full, 64 * x, head, t0, (int)b);
           }
           tma_load_4d(at + 2 * S::kQ, &map_v, full, v0, n, t0, (int)b);
+          if (i + 2 < count) {  // on its way to L2, before its place is free
+            const int t2 = t0 + 2 * L;
+#pragma unroll
+            for (int x = 0; x < PANELS; ++x) {
+              tma_prefetch_4d(&map_q, 64 * x, head, t2, (int)b);
+              tma_prefetch_4d(&map_k, 64 * x, head, t2, (int)b);
+            }
+            tma_prefetch_4d(&map_v, v0, n, t2, (int)b);
+          }
         }
         __syncwarp();
       } else {

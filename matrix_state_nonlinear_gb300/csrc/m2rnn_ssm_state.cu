@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float hi[16], lo[16];
         tmem_ld16_nowait(t_lane + hcol + 16 * x, hi);
         tmem_ld16_nowait(t_lane + VT + hcol + 16 * x, lo);
-        tmem_wait_ld();
+        tmem_ready(hi, lo);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           H[8 * x + c] = fma2(e2, H[8 * x + c], add2(make_float2(hi[2 * c], hi[2 * c + 1]),
@@ -227,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_store_4d_if(leader, &map_kept, base + S::kKept + x * KP * VT * 2, v0, 0, 2 * chunk + x, (int)pair);
         if (leader) {
           bulk_commit_group();
-          bulk_wait_group_read<0>();
         }
       } else {
         uint16_t* to = p.kept + ((size_t)pair * (REVERSE ? chunks : chunks + 1) + chunk) * 2 * plane + v0;
@@ -239,8 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      warp_arrive(&bar.put_free, lane);
       return true;
+    };
+    auto sent = [&]() {  // its tile may be written again
+      if (leader) bulk_wait_group_read<0>();
+      warp_arrive(&bar.put_free, lane);
     };
     for (int i = 0; i < count; ++i) {
       if (i > 0) wait(bar.u_free, i - 1);
@@ -250,9 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_steps<L / 16, 128, 128>(leader, tmem, desc_mn(stage(i), L), dw, idesc, false);
       umma_commit_if(leader, &bar.u);
       umma_commit_if(leader, &bar.empty[i % ST]);
+      if (KEEP && i > 0) sent();  // while the product runs
       if (KEEP && !send(i)) break;
     }
-    if (KEEP && ok && !REVERSE && first + count == chunks) send(count);
+    if (KEEP && ok && !REVERSE && first + count == chunks) {
+      if (count > 0) sent();
+      send(count);
+    }
     if (KEEP && leader) bulk_wait_group<0>();
   } else if (warp == kWarpLoad) {  // -------------------------------- loads
     for (int i = 0; i < count; ++i) {
@@ -267,6 +273,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < PANELS; ++x)
             tma_load_4d(to + panel(x, L), &map_x, full, 64 * x, head, t0, (int)b);
           tma_load_4d(to + S::kX, &map_y, full, v0, n, t0, (int)b);
+          if (i + 2 < count) {  // on its way to L2, before its place is free
+            const int t2 = chunk_at(i + 2) * L;
+#pragma unroll
+            for (int x = 0; x < PANELS; ++x) tma_prefetch_4d(&map_x, 64 * x, head, t2, (int)b);
+            tma_prefetch_4d(&map_y, v0, n, t2, (int)b);
+            if (KEEP && REVERSE)
+              for (int x = 0; x < 2; ++x) tma_prefetch_4d(&map_hs, v0, 0, 2 * chunk_at(i + 2) + x, (int)pair);
+          }
         }
         __syncwarp();
       } else {

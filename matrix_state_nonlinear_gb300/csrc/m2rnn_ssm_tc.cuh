@@ -47,6 +47,18 @@ __device__ __forceinline__ void umma4_ta_if(bool pred, uint32_t d, uint32_t a, u
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return umma_desc(tile, 16, 1024, 2); }
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int rows) { return umma_desc(tile, rows * 128, 1024, 2); }
 
+// Waits for the warp's loads from tensor memory into v...  The empty statements tie every later use
+// of the registers to the wait: without them the compiler may move arithmetic on them before it.
+template <int N>
+__device__ __forceinline__ void tie(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+template <typename... V>
+__device__ __forceinline__ void tmem_ready(V&... v) {
+  tmem_wait_ld();
+  (tie(v), ...);
+}
 // Thread i of a warp writes 8 consecutive columns of tensor-memory lane i of the warp's quarter.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
