@@ -10,7 +10,8 @@
 //   8 warps   P from S and the weighted v (a quarter of the tokens and half the columns each);
 //   8 warps   y from Y1, Y2 and v (half the columns each);
 //   8 warps   the state, float32 in registers (half the columns each);
-//   1 warp    issues the products;  1 warp  the loads (TMA);  2 warps  the gates, every other chunk.
+//   2 warps   issue the products: S and P v; q H and U;
+//   2 warps   load the tiles (TMA) and compute the gates of every other chunk.
 //  * S is decayed in float32 and rounded to bf16 in tensor memory, the first operand of P v; H is
 //    rounded to bf16 as an operand; y is bf16.  The state itself is float32 and takes U with float32
 //    weights: the weighted v enters as two bf16 values (17 bits), two products.
@@ -30,7 +31,7 @@ namespace {
 constexpr int L = kTokens;
 constexpr int VT = kSsmColumns;
 // First warp of each kind.
-constexpr int kWarpY = 8, kWarpState = 16, kWarpMma = 24, kWarpLoad = 25, kWarpGate = 26, kWarps = 28;
+constexpr int kWarpY = 8, kWarpState = 16, kWarpMma = 24, kWarpLoad = 26, kWarps = 28;
 constexpr int kThreads = 32 * kWarps;
 
 // Tensor memory columns.  S has two buffers, and P takes the place of its S: the 64 columns of
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 8);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 16);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.s[i], 1), mbar_init(&bar.p[i], 8);
-    mbar_init(&bar.q, 1), mbar_init(&bar.y, 1);
+    mbar_init(&bar.q, 1), mbar_init(&bar.y, 2);
     mbar_init(&bar.y_free, 8), mbar_init(&bar.u, 1), mbar_init(&bar.u_free, 8);
     mbar_init(&bar.w, 8), mbar_init(&bar.h, 8);
     bar.abort = 0;
@@ -325,31 +326,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < HC; ++c)
         if (hcol + c < vw) dst[c] = c & 1 ? H[c / 2].y : H[c / 2].x;
     }
-  } else if (warp == kWarpMma) {  // ------------------------------------ products
-    const uint32_t idesc_s = umma_idesc_bf16(128, 128, false);
+  } else if (warp < kWarpLoad) {  // ------------------------------------ products
     const uint32_t idesc_y = umma_idesc_bf16_ab(128, VT, false, true);
-    const uint32_t idesc_u = umma_idesc_bf16_ab(KP, 2 * VT, true, true);
-    const uint64_t dh = desc_mn(base + S::kH, KP), dw = desc_mn(base + S::kW, L);
     const bool leader = lane == 0;
-    // Step i: S of chunk i + 1 into the buffer of P of chunk i - 1, q H and P v of chunk i, U of
-    // chunk i + 1.
-    for (int i = -1; i < count; ++i) {
-      const bool more = i + 1 < count;
-      const uint32_t next = stage(i + 1);
-      if (more) {  // S = q k^T
+    if (warp == kWarpMma) {
+      // S of chunk i + 1 into the buffer of P of chunk i - 1, then P v of chunk i.
+      const uint32_t idesc_s = umma_idesc_bf16(128, 128, false);
+      for (int i = -1; i < count; ++i) {
+        const uint32_t next = stage(i + 1);
         if (i > 0) wait(bar.y, i - 1);
-        if (!wait(bar.full[(i + 1) % ST], (i + 1) / ST)) break;
-        umma_steps<KP / 16, 2, 2, L * 8 - 8, L * 8 - 8>(leader, tmem + kColS + ((i + 1) & 1) * 128, desc_k(next),
-                                                        desc_k(next + S::kQ), idesc_s, false);
-        umma_commit_if(leader, &bar.s[(i + 1) & 1]);
-      }
-      if (i >= 0) {
-        wait(bar.h, i);
+        if (i + 1 < count) {
+          if (!wait(bar.full[(i + 1) % ST], (i + 1) / ST)) break;
+          umma_steps<KP / 16, 2, 2, L * 8 - 8, L * 8 - 8>(leader, tmem + kColS + ((i + 1) & 1) * 128, desc_k(next),
+                                                          desc_k(next + S::kQ), idesc_s, false);
+          umma_commit_if(leader, &bar.s[(i + 1) & 1]);
+        }
+        if (i < 0) continue;
         if (i > 0) wait(bar.y_free, i - 1);
-        if (!ok) break;
-        tc_fence_after();
-        umma_steps<KP / 16, 2, 128, L * 8 - 8>(leader, tmem + kColY1, desc_k(stage(i)), dh, idesc_y, false);
-        umma_commit_if(leader, &bar.q);
         if (!wait(bar.p[i & 1], i >> 1)) break;
         tc_fence_after();
         const uint64_t dv = desc_mn(stage(i) + 2 * S::kQ, L);
@@ -358,61 +351,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma4_ta_if<128>(leader, tmem + kColY2, tp + 64, dv + 512, idesc_y, 1u);
         umma_commit_if(leader, &bar.y);
       }
-      if (more) {  // U = k^T (weighted v), high and low side by side
-        if (i >= 0) wait(bar.u_free, i);
-        if (!wait(bar.w, i + 1)) break;
+    } else {
+      // U of chunk i (k^T times the weighted v, high and low side by side), then q H.
+      const uint32_t idesc_u = umma_idesc_bf16_ab(KP, 2 * VT, true, true);
+      const uint64_t dh = desc_mn(base + S::kH, KP), dw = desc_mn(base + S::kW, L);
+      for (int i = 0; i < count; ++i) {
+        wait(bar.full[i % ST], i / ST);
+        if (i > 0) wait(bar.u_free, i - 1);
+        if (!wait(bar.w, i)) break;
         tc_fence_after();
-        const uint64_t dk = desc_mn(next + S::kQ, L);
-        umma_steps<L / 16, 128, 128>(leader, tmem + kColU, dk, dw, idesc_u, false);
+        umma_steps<L / 16, 128, 128>(leader, tmem + kColU, desc_mn(stage(i) + S::kQ, L), dw, idesc_u, false);
         umma_commit_if(leader, &bar.u);
+        if (i > 0) wait(bar.y_free, i - 1);
+        if (!wait(bar.h, i)) break;
+        tc_fence_after();
+        umma_steps<KP / 16, 2, 128, L * 8 - 8>(leader, tmem + kColY1, desc_k(stage(i)), dh, idesc_y, false);
+        umma_commit_if(leader, &bar.q);
+        umma_commit_if(leader, &bar.y);
       }
     }
-  } else if (warp == kWarpLoad) {  // ----------------------------------- loads
-    for (int i = 0; i < count; ++i) {
-      if (i >= ST && !wait(bar.empty[i % ST], i / ST - 1)) break;
-      const int t0 = (first + i) * L;
-      if (tma) {
-        if (lane == 0) {
-          uint64_t* full = &bar.full[i % ST];
-          unsigned char* at = smem + i % ST * S::kStage;
-          mbar_arrive_expect_tx(full, S::kStage);
-#pragma unroll
-          for (int x = 0; x < PANELS; ++x) {
-            tma_load_4d(at + panel(x, L), &map_q, full, 64 * x, head, t0, (int)b);
-            tma_load_4d(at + S::kQ + panel(x, L), &map_k, full, 64 * x, head, t0, (int)b);
-          }
-          tma_load_4d(at + 2 * S::kQ, &map_v, full, v0, n, t0, (int)b);
-          if (i + 2 < count) {  // on its way to L2, before its place is free
-            const int t2 = t0 + 2 * L;
-#pragma unroll
-            for (int x = 0; x < PANELS; ++x) {
-              tma_prefetch_4d(&map_q, 64 * x, head, t2, (int)b);
-              tma_prefetch_4d(&map_k, 64 * x, head, t2, (int)b);
-            }
-            tma_prefetch_4d(&map_v, v0, n, t2, (int)b);
-          }
-        }
-        __syncwarp();
-      } else {
-        const int rows = min(L, p.T - t0);
-        const uint16_t* q = p.q + b * p.sq.batch + t0 * p.sq.token + (long long)head * p.K;
-        const uint16_t* k = p.k + b * p.sk.batch + t0 * p.sk.token + (long long)head * p.K;
-        const uint16_t* v = p.v + b * p.sv.batch + t0 * p.sv.token + (long long)n * p.V + v0;
-        for (int x = 0; x < PANELS; ++x) {
-          copy_tokens(stage(i) + panel(x, L), q + 64 * x, p.sq.token, rows, p.K - 64 * x, lane);
-          copy_tokens(stage(i) + S::kQ + panel(x, L), k + 64 * x, p.sk.token, rows, p.K - 64 * x, lane);
-        }
-        copy_tokens(stage(i) + 2 * S::kQ, v, p.sv.token, rows, vw, lane);
-        fence_proxy_async_smem();
-        warp_arrive(&bar.full[i % ST], lane);
-      }
-    }
-    // Given up: whatever was started here arrives before the block ends (a stage's load that was
-    // not started times out, one of an earlier chunk has long arrived).
-    if (!ok && tma)
-      for (int s = 0; s < ST; ++s)
-        for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
-  } else {  // ---------------------------------------------------------- gates
+  } else {  // ---------------------------------------------------------- gates and loads
     const uint16_t* ag = p.a + b * p.sa.batch + n;
     const float alpha = p.alpha[n], beta = p.beta[n];
     // Token 32 e + lane of a chunk, loaded two chunks ahead.
@@ -420,16 +378,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long t = (long long)(first + i) * L + 32 * e + lane;
       return i < count && t < p.T ? bf16_to_f(ag[t * p.sa.token]) : -INFINITY;
     };
-    int i = warp - kWarpGate;
+    int i = warp - kWarpLoad;
     float4 a = make_float4(logit(i, 0), logit(i, 1), logit(i, 2), logit(i, 3));
     for (; i < count; i += 2) {
       const float4 ahead = make_float4(logit(i + 2, 0), logit(i + 2, 1), logit(i + 2, 2), logit(i + 2, 3));
+      auto load = [&]() {
+        if (i >= ST && !wait(bar.empty[i % ST], i / ST - 1)) return;
+        const int t0 = (first + i) * L;
+        if (tma) {
+          if (lane == 0) {
+            uint64_t* full = &bar.full[i % ST];
+            unsigned char* at = smem + i % ST * S::kStage;
+            mbar_arrive_expect_tx(full, S::kStage);
+#pragma unroll
+            for (int x = 0; x < PANELS; ++x) {
+              tma_load_4d(at + panel(x, L), &map_q, full, 64 * x, head, t0, (int)b);
+              tma_load_4d(at + S::kQ + panel(x, L), &map_k, full, 64 * x, head, t0, (int)b);
+            }
+            tma_load_4d(at + 2 * S::kQ, &map_v, full, v0, n, t0, (int)b);
+            if (i + 2 < count) {  // on its way to L2, before its place is free
+              const int t2 = t0 + 2 * L;
+#pragma unroll
+              for (int x = 0; x < PANELS; ++x) {
+                tma_prefetch_4d(&map_q, 64 * x, head, t2, (int)b);
+                tma_prefetch_4d(&map_k, 64 * x, head, t2, (int)b);
+              }
+              tma_prefetch_4d(&map_v, v0, n, t2, (int)b);
+            }
+          }
+          __syncwarp();
+        } else {
+          const int rows = min(L, p.T - t0);
+          const uint16_t* q = p.q + b * p.sq.batch + t0 * p.sq.token + (long long)head * p.K;
+          const uint16_t* k = p.k + b * p.sk.batch + t0 * p.sk.token + (long long)head * p.K;
+          const uint16_t* v = p.v + b * p.sv.batch + t0 * p.sv.token + (long long)n * p.V + v0;
+          for (int x = 0; x < PANELS; ++x) {
+            copy_tokens(stage(i) + panel(x, L), q + 64 * x, p.sq.token, rows, p.K - 64 * x, lane);
+            copy_tokens(stage(i) + S::kQ + panel(x, L), k + 64 * x, p.sk.token, rows, p.K - 64 * x, lane);
+          }
+          copy_tokens(stage(i) + 2 * S::kQ, v, p.sv.token, rows, vw, lane);
+          fence_proxy_async_smem();
+          warp_arrive(&bar.full[i % ST], lane);
+        }
+      };
+      // The first chunks' tiles before their gates, later ones' after: their places are taken still.
+      if (i < ST) load();
       if (i >= 4 && !wait(bar.gate_free[i & 3], (i >> 2) - 1)) break;
       put_chunk_gates(
           gates[i & 3], [&](int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }, alpha, beta, lane);
       warp_arrive(&bar.gate[i & 3], lane);
       a = ahead;
+      if (i >= ST) load();
+      if (!ok) break;
     }
+    // Given up: whatever was started here arrives before the block ends (a stage's load that was
+    // not started times out, one of an earlier chunk has long arrived).
+    if (!ok && tma)
+      for (int s = 0; s < ST; ++s)
+        for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
   }
   if (!ok && lane == 0) {
     *abort = 1;
