@@ -6,9 +6,10 @@
 //   dX[t] = sum_j w[j] dpre[t+3-j],  dw[j] = sum_{b,t} dpre[t] X[t-3+j],  dbias = sum dpre
 //
 // Memory-bound: the forward reads and writes every element once (4 bytes an element), the
-// backward reads two and writes one (6 bytes).  A thread owns kVec neighbouring channels over a
-// stretch of tokens and slides a window of three tokens through registers; eight tokens are
-// loaded ahead of their arithmetic so that enough bytes are in flight.
+// backward reads two and writes one (6 bytes).  A thread owns four neighbouring channels (8-byte
+// accesses, arithmetic in pairs) over a stretch of tokens; eight (four) tokens are loaded at once
+// and joined to the last three in registers, so that enough bytes are in flight and the window
+// moves once per group of tokens.  The three tokens that stretches share are re-read, from L2.
 #include "m2rnn_ssm.h"
 #include "ptx_util.cuh"
 
@@ -19,69 +20,58 @@ constexpr int kTaps = 4;
 constexpr int kHist = kTaps - 1;
 constexpr int kThreads = 128;
 
+// VEC channels (4 or 1) of one token: raw, and as float pairs (one pair of which half is used).
 template <int VEC>
-struct Raw;  // VEC bf16 values as loaded
+struct Chan;
 template <>
-struct Raw<8> {
-  uint4 u;
+struct Chan<4> {
+  using Raw = uint2;
+  static constexpr int P = 2;
+  __device__ static void unpack(uint2 u, float2 (&f)[2]) {
+    f[0] = bf16x2_to_float2(u.x), f[1] = bf16x2_to_float2(u.y);
+  }
+  __device__ static uint2 pack(const float2 (&f)[2]) {
+    return make_uint2(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y));
+  }
 };
 template <>
-struct Raw<4> {
-  uint2 u;
+struct Chan<1> {
+  using Raw = uint16_t;
+  static constexpr int P = 1;
+  __device__ static void unpack(uint16_t u, float2 (&f)[1]) { f[0] = make_float2(bf16_to_f(u), 0.f); }
+  __device__ static uint16_t pack(const float2 (&f)[1]) { return f_to_bf16(f[0].x); }
 };
-template <>
-struct Raw<1> {
-  uint16_t u;
-};
-
-template <int VEC>
-__device__ __forceinline__ Raw<VEC> load_raw(const uint16_t* p) {
-  return *reinterpret_cast<const Raw<VEC>*>(p);
-}
-__device__ __forceinline__ void unpack(const Raw<8>& r, float (&f)[8]) {
-  f[0] = bf16_lo(r.u.x), f[1] = bf16_hi(r.u.x), f[2] = bf16_lo(r.u.y), f[3] = bf16_hi(r.u.y);
-  f[4] = bf16_lo(r.u.z), f[5] = bf16_hi(r.u.z), f[6] = bf16_lo(r.u.w), f[7] = bf16_hi(r.u.w);
-}
-__device__ __forceinline__ void unpack(const Raw<4>& r, float (&f)[4]) {
-  f[0] = bf16_lo(r.u.x), f[1] = bf16_hi(r.u.x), f[2] = bf16_lo(r.u.y), f[3] = bf16_hi(r.u.y);
-}
-__device__ __forceinline__ void unpack(const Raw<1>& r, float (&f)[1]) { f[0] = bf16_to_f(r.u); }
-__device__ __forceinline__ void store_vec(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ void store_vec(uint16_t* p, const float (&f)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-__device__ __forceinline__ void store_vec(uint16_t* p, const float (&f)[1]) { *p = f_to_bf16(f[0]); }
 
 // sigmoid with the fast exponential: relative error a few 2^-22, below the bf16 rounding of
 // every result but the sums dw and dbias, where it stays below 1e-6 of them.
-__device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-
-// X[t] of one batch row: the window for t in [-3, -1], x after that.
-template <int VEC>
-__device__ __forceinline__ void load_x(const uint16_t* xb, const uint16_t* win, long long x_token,
-                                       int C, int t, float (&f)[VEC]) {
-  if (t >= 0) {
-    unpack(load_raw<VEC>(xb + t * x_token), f);
-  } else if (win) {
-    unpack(load_raw<VEC>(win + (long long)(t + kHist) * C), f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = 0.f;
-  }
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  return make_float2(__fdividef(1.f, 1.f + __expf(-x.x)), __fdividef(1.f, 1.f + __expf(-x.y)));
 }
 
+// A thread's channels: taps as pairs, bias.
 template <int VEC>
-__device__ __forceinline__ void load_taps(const float* w, const float* bias, int c0,
-                                          float (&wt)[VEC][kTaps], float (&bs)[VEC]) {
+struct Taps {
+  static constexpr int P = Chan<VEC>::P;
+  float2 w[kTaps][P], b[P];
+  __device__ __forceinline__ void load(const float* wp, const float* bias, int c0) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    const float4 u = *reinterpret_cast<const float4*>(w + (size_t)(c0 + i) * kTaps);
-    wt[i][0] = u.x, wt[i][1] = u.y, wt[i][2] = u.z, wt[i][3] = u.w;
-    bs[i] = bias ? bias[c0 + i] : 0.f;
+    for (int i = 0; i < P; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(wp + (size_t)(c0 + 2 * i) * kTaps);
+      const float4 y = VEC > 1 ? *reinterpret_cast<const float4*>(wp + (size_t)(c0 + 2 * i + 1) * kTaps) : x;
+      w[0][i] = make_float2(x.x, y.x), w[1][i] = make_float2(x.y, y.y);
+      w[2][i] = make_float2(x.z, y.z), w[3][i] = make_float2(x.w, y.w);
+      b[i] = bias ? make_float2(bias[c0 + 2 * i], VEC > 1 ? bias[c0 + 2 * i + 1] : 0.f) : make_float2(0.f, 0.f);
+    }
   }
+};
+
+// X[t] of one batch row: the window for t in [-3, -1], x after that; zeros past the sequence.
+template <int VEC>
+__device__ __forceinline__ typename Chan<VEC>::Raw load_x(const uint16_t* xb, const uint16_t* win, long long x_token,
+                                                          int C, int T, int t) {
+  using Raw = typename Chan<VEC>::Raw;
+  const uint16_t* p = t >= 0 ? xb + t * x_token : win + (long long)(t + kHist) * C;
+  return t < T && (t >= 0 || win) ? *reinterpret_cast<const Raw*>(p) : Raw{};
 }
 
 // Forward: one thread, VEC channels, `span` tokens of one batch row.  The thread of the first
@@ -91,50 +81,59 @@ template <int VEC>
 __global__ void __launch_bounds__(kThreads)
     conv_window_kernel(ConvProblem p, uint16_t* __restrict__ out, uint16_t* window_out, int span,
                        int groups, int stretches) {
+  using Ch = Chan<VEC>;
+  using Raw = typename Ch::Raw;
+  constexpr int P = Ch::P, U = 8;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int c0 = VEC * (int)(id % groups);
   const int stretch = (int)(id / groups % stretches);
   const long long b = id / groups / stretches;
   if (b >= p.B) return;
-  float wt[VEC][kTaps], bs[VEC];
-  load_taps<VEC>(p.w, p.bias, c0, wt, bs);
   const uint16_t* xb = p.x + b * p.sx.batch + c0;
   const uint16_t* win = p.window_in ? p.window_in + b * kHist * p.C + c0 : nullptr;
   uint16_t* ob = out + b * p.T * p.C + c0;
   const int t0 = stretch * span, t1 = min(p.T, t0 + span);
-  float h[kHist][VEC];  // X[t-3], X[t-2], X[t-1]
+  float2 x[U + kHist][P];  // X[t - 3], ...
 #pragma unroll
-  for (int j = 0; j < kHist; ++j) load_x<VEC>(xb, win, p.sx.token, p.C, t0 - kHist + j, h[j]);
+  for (int j = 0; j < kHist; ++j) Ch::unpack(load_x<VEC>(xb, win, p.sx.token, p.C, p.T, t0 - kHist + j), x[j]);
   if (stretch == 0 && window_out) {
-    float f[kHist][VEC];
+    Raw f[kHist];
 #pragma unroll
-    for (int j = 0; j < kHist; ++j) load_x<VEC>(xb, win, p.sx.token, p.C, p.T - kHist + j, f[j]);
+    for (int j = 0; j < kHist; ++j) f[j] = load_x<VEC>(xb, win, p.sx.token, p.C, p.T, p.T - kHist + j);
 #pragma unroll
-    for (int j = 0; j < kHist; ++j) store_vec(window_out + (b * kHist + j) * p.C + c0, f[j]);
+    for (int j = 0; j < kHist; ++j) *reinterpret_cast<Raw*>(window_out + (b * kHist + j) * p.C + c0) = f[j];
   }
-  constexpr int kAhead = 8;
-  for (int t = t0; t < t1; t += kAhead) {
-    Raw<VEC> raw[kAhead];
+  Taps<VEC> w;
+  w.load(p.w, p.bias, c0);
+  Raw raw[U];
+  auto fetch = [&](int t) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t + u < t1) raw[u] = load_raw<VEC>(xb + (t + u) * p.sx.token);
+    for (int u = 0; u < U; ++u)
+      if (t + u < t1) raw[u] = *reinterpret_cast<const Raw*>(xb + (t + u) * p.sx.token);
+  };
+  fetch(t0);
+  for (int t = t0; t < t1; t += U) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < U; ++u) Ch::unpack(raw[u], x[kHist + u]);
+    fetch(t + U);  // while these are computed
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       if (t + u >= t1) break;
-      float x[VEC], o[VEC];
-      unpack(raw[u], x);
+      float2 o[P];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        float s = bs[i];
-        s = fmaf(wt[i][0], h[0][i], s);
-        s = fmaf(wt[i][1], h[1][i], s);
-        s = fmaf(wt[i][2], h[2][i], s);
-        s = fmaf(wt[i][3], x[i], s);
-        o[i] = s * sigmoid_f(s);
-        h[0][i] = h[1][i], h[1][i] = h[2][i], h[2][i] = x[i];
+      for (int i = 0; i < P; ++i) {
+        float2 s = fma2(w.w[0][i], x[u][i], w.b[i]);
+        s = fma2(w.w[1][i], x[u + 1][i], s);
+        s = fma2(w.w[2][i], x[u + 2][i], s);
+        s = fma2(w.w[3][i], x[u + 3][i], s);
+        o[i] = mul2(s, sigmoid2(s));
       }
-      store_vec(ob + (long long)(t + u) * p.C, o);
+      *reinterpret_cast<Raw*>(ob + (long long)(t + u) * p.C) = Ch::pack(o);
     }
+#pragma unroll
+    for (int j = 0; j < kHist; ++j)
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[j][i] = x[U + j][i];
   }
 }
 
@@ -146,98 +145,105 @@ __global__ void __launch_bounds__(kThreads)
     conv_backward_kernel(ConvProblem p, const uint16_t* __restrict__ dout,
                          uint16_t* __restrict__ dx, uint16_t* __restrict__ dwindow,
                          float* __restrict__ part, int span, int groups, int stretches) {
+  using Ch = Chan<VEC>;
+  using Raw = typename Ch::Raw;
+  constexpr int P = Ch::P, U = 4;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int c0 = VEC * (int)(id % groups);
   const int stretch = (int)(id / groups % stretches);
   const long long b = id / groups / stretches;
   if (b >= p.B) return;
-  float wt[VEC][kTaps], bs[VEC];
-  load_taps<VEC>(p.w, p.bias, c0, wt, bs);
   const uint16_t* xb = p.x + b * p.sx.batch + c0;
   const uint16_t* win = p.window_in ? p.window_in + b * kHist * p.C + c0 : nullptr;
   const uint16_t* gb = dout + b * p.T * p.C + c0;
   uint16_t* dxb = dx + b * p.T * p.C + c0;
   const int t0 = stretch * span, t1 = min(p.T, t0 + span);
-  float h[kHist][VEC], e[kHist][VEC];  // X[t-3..t-1], dpre[t-3..t-1] (zero before the stretch)
-  float dw[VEC][kTaps], db[VEC];
+  const float2 zero = make_float2(0.f, 0.f);
+  float2 x[U + kHist][P], e[U + kHist][P];  // X[t - 3] ..., dpre[t - 3] ... (zero before the stretch)
+  float2 dw[kTaps][P], db[P];
 #pragma unroll
   for (int j = 0; j < kHist; ++j) {
-    load_x<VEC>(xb, win, p.sx.token, p.C, t0 - kHist + j, h[j]);
+    Ch::unpack(load_x<VEC>(xb, win, p.sx.token, p.C, p.T, t0 - kHist + j), x[j]);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) e[j][i] = 0.f;
+    for (int i = 0; i < P; ++i) e[j][i] = zero;
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    db[i] = zero;
+#pragma unroll
+    for (int j = 0; j < kTaps; ++j) dw[j][i] = zero;
+  }
+  Taps<VEC> w;
+  w.load(p.w, p.bias, c0);
+  const int tend = t1 + kHist, most = min(p.T, tend);
+  Raw xr[U], gr[U];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + u < most) {
+        xr[u] = *reinterpret_cast<const Raw*>(xb + (t + u) * p.sx.token);
+        gr[u] = *reinterpret_cast<const Raw*>(gb + (long long)(t + u) * p.C);
+      } else {
+        xr[u] = gr[u] = Raw{};
+      }
+  };
+  fetch(t0);
+  for (int t = t0; t < tend; t += U) {
+    float2 g[U][P];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Ch::unpack(xr[u], x[kHist + u]);
+      Ch::unpack(gr[u], g[u]);
+    }
+    fetch(t + U);  // while these are computed
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool mine = t + u < t1;
+      // At token t + u, dX[t + u - 3] is complete.  (dout is zero past the sequence, so dpre is.)
+      float2 o[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        float2 s = fma2(w.w[0][i], x[u][i], w.b[i]);
+        s = fma2(w.w[1][i], x[u + 1][i], s);
+        s = fma2(w.w[2][i], x[u + 2][i], s);
+        s = fma2(w.w[3][i], x[u + 3][i], s);
+        const float2 sig = sigmoid2(s), one = make_float2(1.f, 1.f);
+        // sigma (1 + s (1 - sigma)); where sigma is 0, s may be -infinity: no slope
+        const float2 slope = mul2(sig, fma2(s, sub2(one, sig), one));
+        const float2 d = mul2(g[u][i], make_float2(sig.x > 0.f ? slope.x : 0.f, sig.y > 0.f ? slope.y : 0.f));
+        const float2 m = mine ? d : zero;
+        db[i] = add2(db[i], m);
+        dw[0][i] = fma2(m, x[u][i], dw[0][i]);
+        dw[1][i] = fma2(m, x[u + 1][i], dw[1][i]);
+        dw[2][i] = fma2(m, x[u + 2][i], dw[2][i]);
+        dw[3][i] = fma2(m, x[u + 3][i], dw[3][i]);
+        e[kHist + u][i] = d;
+        o[i] = fma2(w.w[3][i], e[u][i],
+                    fma2(w.w[2][i], e[u + 1][i], fma2(w.w[1][i], e[u + 2][i], mul2(w.w[0][i], d))));
+      }
+      const int at = t + u - kHist;
+      if (at >= t0 && at < t1)
+        *reinterpret_cast<Raw*>(dxb + (long long)at * p.C) = Ch::pack(o);
+      else if (at < 0 && stretch == 0 && dwindow)  // the window's own tokens
+        *reinterpret_cast<Raw*>(dwindow + (b * kHist + at + kHist) * p.C + c0) = Ch::pack(o);
+    }
+#pragma unroll
+    for (int j = 0; j < kHist; ++j)
+#pragma unroll
+      for (int i = 0; i < P; ++i) x[j][i] = x[U + j][i], e[j][i] = e[U + j][i];
+  }
+  float* row = part + ((b * stretches + stretch) * p.C + c0) * (kTaps + 1);
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    db[i] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kTaps; ++j) dw[i][j] = 0.f;
-  }
-  // At token t, dX[t-3] is complete: from dpre[t-3..t].  It is this thread's for t - 3 >= t0, or
-  // the window's for t - 3 < 0.
-  constexpr int kAhead = 4;
-  const int tend = t1 + kHist;
-  for (int t = t0; t < tend; t += kAhead) {
-    Raw<VEC> xr[kAhead], gr[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t + u < tend && t + u < p.T) {
-        xr[u] = load_raw<VEC>(xb + (t + u) * p.sx.token);
-        gr[u] = load_raw<VEC>(gb + (long long)(t + u) * p.C);
-      }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int tt = t + u;
-      if (tt >= tend) break;
-      float x[VEC], g[VEC], o[VEC];
-      if (tt < p.T) {
-        unpack(xr[u], x);
-        unpack(gr[u], g);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = g[i] = 0.f;
-      }
-      const bool mine = tt < t1;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        float s = bs[i];
-        s = fmaf(wt[i][0], h[0][i], s);
-        s = fmaf(wt[i][1], h[1][i], s);
-        s = fmaf(wt[i][2], h[2][i], s);
-        s = fmaf(wt[i][3], x[i], s);
-        const float sig = sigmoid_f(s);
-        const float d = tt < p.T ? g[i] * (sig * fmaf(s, 1.f - sig, 1.f)) : 0.f;
-        if (mine) {
-          db[i] += d;
-          dw[i][0] = fmaf(d, h[0][i], dw[i][0]);
-          dw[i][1] = fmaf(d, h[1][i], dw[i][1]);
-          dw[i][2] = fmaf(d, h[2][i], dw[i][2]);
-          dw[i][3] = fmaf(d, x[i], dw[i][3]);
-        }
-        o[i] = fmaf(wt[i][3], e[0][i],
-                    fmaf(wt[i][2], e[1][i], fmaf(wt[i][1], e[2][i], wt[i][0] * d)));
-        h[0][i] = h[1][i], h[1][i] = h[2][i], h[2][i] = x[i];
-        e[0][i] = e[1][i], e[1][i] = e[2][i], e[2][i] = d;
-      }
-      if (tt - kHist >= t0)
-        store_vec(dxb + (long long)(tt - kHist) * p.C, o);
-      else if (stretch == 0 && dwindow)  // tt < 3 in the first stretch: the window's own tokens
-        store_vec(dwindow + (b * kHist + tt) * p.C + c0, o);
-    }
-  }
-  if (part) {
-    float* row = part + ((b * stretches + stretch) * p.C + c0) * (kTaps + 1);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-      for (int j = 0; j < kTaps; ++j) row[i * (kTaps + 1) + j] = dw[i][j];
-      row[i * (kTaps + 1) + kTaps] = db[i];
-    }
+    for (int j = 0; j < kTaps; ++j) row[i * (kTaps + 1) + j] = i & 1 ? dw[j][i / 2].y : dw[j][i / 2].x;
+    row[i * (kTaps + 1) + kTaps] = i & 1 ? db[i / 2].y : db[i / 2].x;
   }
 }
 
-// Column sums of `count` rows of `width` floats, in a fixed order: 32 columns by 8 row slices
+// Column sums of `count` rows of `width` floats, in a fixed order: 32 columns by 32 row slices
 // per block, the slices added at the end.
-constexpr int kSumSlices = 8;
+constexpr int kSumSlices = 32;
 template <typename Put>
 __device__ __forceinline__ void column_sums(const float* src, int count, int width, int pitch,
                                             Put put) {
@@ -250,7 +256,6 @@ __device__ __forceinline__ void column_sums(const float* src, int count, int wid
   __syncthreads();
   if (threadIdx.y == 0 && c < width) {
     float t = 0.f;
-#pragma unroll
     for (int j = 0; j < kSumSlices; ++j) t += part[j][threadIdx.x];
     put(c, t);
   }
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(32 * kSumSlices)
 // Tokens per thread: long stretches re-read little (three tokens each) and sum more in
 // registers, short ones give a short prompt enough threads.
 int conv_span(int B, int T, int C, int vec) {
-  int span = 64;
+  int span = 128;
   while (span > 8 && (long long)B * ((T + span - 1) / span) * (C / vec) < 152LL * 1024) span /= 2;
   return span;
 }
@@ -330,8 +335,8 @@ cudaError_t launch_sum_rows(const float* src, float* dst0, float* dst1, int coun
 
 cudaError_t launch_conv_window(const ConvProblem& p, uint16_t* out, uint16_t* window_out,
                                cudaStream_t stream) {
-  if (rows_aligned(p, 8) && aligned_to(out, 16) && aligned_to(window_out, 16))
-    return run_forward<8>(p, out, window_out, stream);
+  if (rows_aligned(p, 4) && aligned_to(out, 8) && aligned_to(window_out, 8))
+    return run_forward<4>(p, out, window_out, stream);
   return run_forward<1>(p, out, window_out, stream);
 }
 

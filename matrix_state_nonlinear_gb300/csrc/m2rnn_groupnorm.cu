@@ -22,6 +22,36 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
+// VEC values as loaded, so that a load can be started ahead of its use.
+template <typename Y, int VEC>
+struct Raw {
+  uint4 u[VEC == 8 && sizeof(Y) == 4 ? 2 : 1];
+  __device__ __forceinline__ void load(const Y* p) {
+    if constexpr (VEC == 8) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(Y) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else if constexpr (sizeof(Y) == 4) {
+      u[0].x = __float_as_uint(*p);
+    } else {
+      u[0].x = *p;
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+    if constexpr (VEC == 8 && sizeof(Y) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(u[i].x), f[4 * i + 1] = __uint_as_float(u[i].y);
+        f[4 * i + 2] = __uint_as_float(u[i].z), f[4 * i + 3] = __uint_as_float(u[i].w);
+      }
+    } else if constexpr (VEC == 8) {
+      f[0] = bf16_lo(u[0].x), f[1] = bf16_hi(u[0].x), f[2] = bf16_lo(u[0].y), f[3] = bf16_hi(u[0].y);
+      f[4] = bf16_lo(u[0].z), f[5] = bf16_hi(u[0].z), f[6] = bf16_lo(u[0].w), f[7] = bf16_hi(u[0].w);
+    } else {
+      f[0] = sizeof(Y) == 4 ? __uint_as_float(u[0].x) : bf16_to_f((uint16_t)u[0].x);
+    }
+  }
+};
+
 // VEC values at p, as floats.
 template <int VEC>
 __device__ __forceinline__ void load_vals(const uint16_t* p, float (&f)[VEC]) {
@@ -81,23 +111,15 @@ __device__ __forceinline__ float team_sum(float s, int team) {
   }
 }
 
-// The group's values in registers, centred and scaled: z = n; returns inv.
-template <typename Y, int VEC, bool BLOCK, int R>
-__device__ __forceinline__ float load_normalised(const Y* y, bool live, int lane, int team, int chunks,
-                                                 int E, float eps, float (&z)[R][VEC]) {
+// Centres and scales a group's values (zeros outside it): z becomes n; returns inv.
+template <int VEC, bool BLOCK, int R>
+__device__ __forceinline__ float normalise(bool live, int lane, int team, int chunks, int E, float eps,
+                                           float (&z)[R][VEC]) {
   float s = 0.f;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int c = lane + r * team;
-    if (live && c < chunks) {
-      load_vals<VEC>(y + (size_t)c * VEC, z[r]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) z[r][i] = 0.f;
-    }
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) s += z[r][i];
-  }
   const float mean = team_sum<BLOCK>(s, team) / (float)E;
   s = 0.f;
 #pragma unroll
@@ -117,49 +139,79 @@ __device__ __forceinline__ float load_normalised(const Y* y, bool live, int lane
   return inv;
 }
 
-template <typename Y, int VEC, bool BLOCK, int R>
+// A team takes UNITS groups, `apart` units from one to the next, all loaded before the first is
+// computed.
+template <typename Y, int VEC, bool BLOCK, int R, int UNITS>
 __global__ void __launch_bounds__(kThreads)
-    groupnorm_kernel(NormProblem p, uint16_t* __restrict__ out, int team, int chunks) {
+    groupnorm_kernel(NormProblem p, uint16_t* __restrict__ out, int team, int chunks, long long apart) {
   const int E = p.D / p.groups;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (team - 1);
-  const long long unit = BLOCK ? blockIdx.x
-                               : ((long long)blockIdx.x * kThreads + threadIdx.x) / team;
-  const bool live = unit < p.rows * p.groups;
-  const int g = (int)(unit % p.groups);
-  const size_t at = live ? (size_t)(unit / p.groups) * p.D + (size_t)g * E : 0;
-  float z[R][VEC];
-  load_normalised<Y, VEC, BLOCK, R>(static_cast<const Y*>(p.y) + at, live, lane, team, chunks, E,
-                                    p.eps, z);
-  if (!live) return;
+  const long long first = BLOCK ? blockIdx.x
+                                : ((long long)blockIdx.x * kThreads + threadIdx.x) / team;
+  Raw<Y, VEC> y[UNITS][R];
+  Raw<uint16_t, VEC> x[UNITS][R];
+  size_t at[UNITS];
+  bool live[UNITS];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int c = lane + r * team;
-    if (c >= chunks) break;
-    const size_t e = (size_t)c * VEC;
-    float w[VEC], b[VEC], o[VEC];
-    load_vals<VEC>(p.w + (size_t)g * E + e, w);
-    if (p.bias) load_vals<VEC>(p.bias + (size_t)g * E + e, b);
+  for (int u = 0; u < UNITS; ++u) {
+    const long long unit = first + u * apart;
+    live[u] = first < apart && unit < p.rows * p.groups;
+    at[u] = live[u] ? (size_t)(unit / p.groups) * p.D + (size_t)(unit % p.groups) * E : 0;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = fmaf(w[i], z[r][i], p.bias ? b[i] : 0.f);
-    if (p.g) {
-      float x[VEC];
-      load_vals<VEC>(p.g + at + e, x);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) o[i] *= x[i] * sigmoid_f(x[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) o[i] *= sigmoid_f(o[i]);
+    for (int r = 0; r < R; ++r) {
+      const int c = lane + r * team;
+      if (live[u] && c < chunks) {
+        y[u][r].load(static_cast<const Y*>(p.y) + at[u] + (size_t)c * VEC);
+        if (p.g) x[u][r].load(p.g + at[u] + (size_t)c * VEC);
+      }
     }
-    store_vals<VEC>(out + at + e, o);
+  }
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const int g = (int)((first + u * apart) % p.groups);
+    float z[R][VEC];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (live[u] && lane + r * team < chunks) {
+        y[u][r].get(z[r]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) z[r][i] = 0.f;
+      }
+    }
+    normalise<VEC, BLOCK, R>(live[u], lane, team, chunks, E, p.eps, z);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = lane + r * team;
+      if (!live[u] || c >= chunks) break;
+      const size_t e = (size_t)c * VEC;
+      float w[VEC], b[VEC], o[VEC];
+      load_vals<VEC>(p.w + (size_t)g * E + e, w);
+      if (p.bias) load_vals<VEC>(p.bias + (size_t)g * E + e, b);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] = fmaf(w[i], z[r][i], p.bias ? b[i] : 0.f);
+      if (p.g) {
+        float gx[VEC];
+        x[u][r].get(gx);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] *= gx[i] * sigmoid_f(gx[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] *= sigmoid_f(o[i]);
+      }
+      store_vals<VEC>(out + at[u] + e, o);
+    }
   }
 }
 
-// Team t of `slots * groups` teams takes group t % groups of rows t / groups, + slots, ...
+// Team t of `slots * groups` teams takes group t % groups of rows t / groups, + slots, ...; the next
+// row is loaded while one is computed.
 template <typename Y, int VEC, bool BLOCK, int R>
 __global__ void __launch_bounds__(kThreads)
     groupnorm_backward_kernel(NormProblem p, const uint16_t* __restrict__ dout, Y* __restrict__ dy,
                               uint16_t* __restrict__ dg, float* __restrict__ part, int team,
                               int chunks, int slots) {
+  constexpr bool kAhead = R * VEC <= 16;  // as far as registers go
   const int E = p.D / p.groups;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (team - 1);
   const long long t = BLOCK ? blockIdx.x
@@ -173,36 +225,60 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) dw[r][i] = db[r][i] = 0.f;
   const long long steps = (p.rows + slots - 1) / slots;  // the same for every thread
+  Raw<Y, VEC> yr[R];
+  Raw<uint16_t, VEC> dr[R], xr[R];
+  auto load = [&](long long s) {
+    const long long row = slot + s * slots;
+    if (!has || row >= p.rows) return;
+    const size_t at = (size_t)row * p.D + (size_t)g * E;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = lane + r * team;
+      if (c >= chunks) break;
+      yr[r].load(static_cast<const Y*>(p.y) + at + (size_t)c * VEC);
+      dr[r].load(dout + at + (size_t)c * VEC);
+      if (p.g) xr[r].load(p.g + at + (size_t)c * VEC);
+    }
+  };
+  if (kAhead) load(0);
   for (long long s = 0; s < steps; ++s) {
     const long long row = slot + s * slots;
     const bool live = has && row < p.rows;
     const size_t at = live ? (size_t)row * p.D + (size_t)g * E : 0;
-    float z[R][VEC], dn[R][VEC];
-    const float inv = load_normalised<Y, VEC, BLOCK, R>(static_cast<const Y*>(p.y) + at, live, lane,
-                                                        team, chunks, E, p.eps, z);
+    if (!kAhead) load(s);
+    float z[R][VEC], dn[R][VEC], gx[kAhead ? R : 1][VEC];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (live && lane + r * team < chunks) {
+        yr[r].get(z[r]);
+        dr[r].get(dn[r]);
+        if (kAhead && p.g) xr[r].get(gx[kAhead ? r : 0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) z[r][i] = dn[r][i] = 0.f;
+      }
+    }
+    if (kAhead) load(s + 1);
+    const float inv = normalise<VEC, BLOCK, R>(live, lane, team, chunks, E, p.eps, z);
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int c = lane + r * team;
-      if (!live || c >= chunks) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) dn[r][i] = 0.f;
-        continue;
-      }
+      if (!live || c >= chunks) continue;
       const size_t e = (size_t)c * VEC;
-      float w[VEC], b[VEC], d[VEC];
+      float w[VEC], b[VEC], x[VEC];
       load_vals<VEC>(p.w + (size_t)g * E + e, w);
       if (p.bias) load_vals<VEC>(p.bias + (size_t)g * E + e, b);
-      load_vals<VEC>(dout + at + e, d);
       if (p.g) {
-        float x[VEC], o[VEC];
-        load_vals<VEC>(p.g + at + e, x);
+        if (!kAhead) xr[r].get(x);
+        float o[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-          const float sig = sigmoid_f(x[i]);
+          const float xi = kAhead ? gx[kAhead ? r : 0][i] : x[i];
+          const float sig = sigmoid_f(xi);
           const float pn = fmaf(w[i], z[r][i], p.bias ? b[i] : 0.f);
-          o[i] = d[i] * pn * (sig * fmaf(x[i], 1.f - sig, 1.f));
-          dn[r][i] = d[i] * (x[i] * sig);
+          o[i] = dn[r][i] * pn * (sig * fmaf(xi, 1.f - sig, 1.f));
+          dn[r][i] *= xi * sig;
         }
         store_vals<VEC>(dg + at + e, o);
       } else {
@@ -210,7 +286,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int i = 0; i < VEC; ++i) {
           const float pn = fmaf(w[i], z[r][i], p.bias ? b[i] : 0.f);
           const float sig = sigmoid_f(pn);
-          dn[r][i] = d[i] * (sig * fmaf(pn, 1.f - sig, 1.f));
+          dn[r][i] *= sig * fmaf(pn, 1.f - sig, 1.f);
         }
       }
 #pragma unroll
@@ -270,7 +346,7 @@ bool vec_ok(const NormProblem& p) {
 // Rows in flight of the backward: enough teams for every SM, few enough partial sums.
 int backward_slots(long long rows, int D, int groups) {
   const Shape s = shape_of(D / groups, (D / groups) % 8 == 0);
-  long long teams = 152LL * 6 * (s.block ? 1 : kThreads / s.team);
+  long long teams = 152LL * 4 * (s.block ? 1 : kThreads / s.team);
   long long slots = teams / groups;
   if (slots < 1) slots = 1;
   return (int)(slots < rows ? slots : rows > 0 ? rows : 1);
@@ -304,10 +380,19 @@ template <typename Y>
 cudaError_t forward_typed(const NormProblem& p, uint16_t* out, const Shape& s, cudaStream_t stream) {
   const long long units = p.rows * p.groups;
   const long long per_block = s.block ? 1 : kThreads / s.team;
-  const unsigned blocks = (unsigned)((units + per_block - 1) / per_block);
   return with_shape(s, [&](auto vec, auto block, auto r) {
-    groupnorm_kernel<Y, decltype(vec)::value, decltype(block)::value != 0, decltype(r)::value>
-        <<<blocks, kThreads, 0, stream>>>(p, out, s.team, s.chunks);
+    constexpr int V = decltype(vec)::value, R = decltype(r)::value;
+    constexpr bool B = decltype(block)::value != 0;
+    // Several units per team where there are enough of them to fill the GPU all the same.
+    constexpr int U = R * V <= 8 ? 4 : R * V <= 16 ? 2 : 1;
+    if (U > 1 && units >= 152LL * 8 * per_block * U) {
+      const long long apart = (units + U - 1) / U;
+      groupnorm_kernel<Y, V, B, R, U>
+          <<<(unsigned)((apart + per_block - 1) / per_block), kThreads, 0, stream>>>(p, out, s.team, s.chunks, apart);
+    } else {
+      groupnorm_kernel<Y, V, B, R, 1>
+          <<<(unsigned)((units + per_block - 1) / per_block), kThreads, 0, stream>>>(p, out, s.team, s.chunks, units);
+    }
     return cudaGetLastError();
   });
 }
