@@ -42,12 +42,6 @@ struct Chan<1> {
   __device__ static uint16_t pack(const float2 (&f)[1]) { return f_to_bf16(f[0].x); }
 };
 
-// sigmoid with the fast exponential: relative error a few 2^-22, below the bf16 rounding of
-// every result but the sums dw and dbias, where it stays below 1e-6 of them.
-__device__ __forceinline__ float2 sigmoid2(float2 x) {
-  return make_float2(__fdividef(1.f, 1.f + __expf(-x.x)), __fdividef(1.f, 1.f + __expf(-x.y)));
-}
-
 // A thread's channels: taps as pairs, bias.
 template <int VEC>
 struct Taps {
@@ -91,8 +85,8 @@ __global__ void __launch_bounds__(kThreads)
   if (b >= p.B) return;
   const uint16_t* xb = p.x + b * p.sx.batch + c0;
   const uint16_t* win = p.window_in ? p.window_in + b * kHist * p.C + c0 : nullptr;
-  uint16_t* ob = out + b * p.T * p.C + c0;
   const int t0 = stretch * span, t1 = min(p.T, t0 + span);
+  uint16_t* ob = out + (b * p.T + t0) * p.C + c0;
   float2 x[U + kHist][P];  // X[t - 3], ...
 #pragma unroll
   for (int j = 0; j < kHist; ++j) Ch::unpack(load_x<VEC>(xb, win, p.sx.token, p.C, p.T, t0 - kHist + j), x[j]);
@@ -106,10 +100,11 @@ __global__ void __launch_bounds__(kThreads)
   Taps<VEC> w;
   w.load(p.w, p.bias, c0);
   Raw raw[U];
+  const uint16_t* next = xb + t0 * p.sx.token;
   auto fetch = [&](int t) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < t1) raw[u] = *reinterpret_cast<const Raw*>(xb + (t + u) * p.sx.token);
+    for (int u = 0; u < U; ++u, next += p.sx.token)
+      if (t + u < t1) raw[u] = *reinterpret_cast<const Raw*>(next);
   };
   fetch(t0);
   for (int t = t0; t < t1; t += U) {
@@ -117,7 +112,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int u = 0; u < U; ++u) Ch::unpack(raw[u], x[kHist + u]);
     fetch(t + U);  // while these are computed
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u, ob += p.C) {
       if (t + u >= t1) break;
       float2 o[P];
 #pragma unroll
@@ -128,7 +123,7 @@ __global__ void __launch_bounds__(kThreads)
         s = fma2(w.w[3][i], x[u + 3][i], s);
         o[i] = mul2(s, sigmoid2(s));
       }
-      *reinterpret_cast<Raw*>(ob + (long long)(t + u) * p.C) = Ch::pack(o);
+      *reinterpret_cast<Raw*>(ob) = Ch::pack(o);
     }
 #pragma unroll
     for (int j = 0; j < kHist; ++j)
@@ -136,6 +131,11 @@ __global__ void __launch_bounds__(kThreads)
       for (int i = 0; i < P; ++i) x[j][i] = x[U + j][i];
   }
 }
+
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
 
 // Backward: one thread, VEC channels, `span` tokens of one batch row.  dX[t] needs dpre up to
 // t + 3, so the thread runs three tokens past its stretch; only its own tokens enter dw, dbias.
@@ -155,8 +155,6 @@ __global__ void __launch_bounds__(kThreads)
   if (b >= p.B) return;
   const uint16_t* xb = p.x + b * p.sx.batch + c0;
   const uint16_t* win = p.window_in ? p.window_in + b * kHist * p.C + c0 : nullptr;
-  const uint16_t* gb = dout + b * p.T * p.C + c0;
-  uint16_t* dxb = dx + b * p.T * p.C + c0;
   const int t0 = stretch * span, t1 = min(p.T, t0 + span);
   const float2 zero = make_float2(0.f, 0.f);
   float2 x[U + kHist][P], e[U + kHist][P];  // X[t - 3] ..., dpre[t - 3] ... (zero before the stretch)
@@ -175,31 +173,35 @@ __global__ void __launch_bounds__(kThreads)
   }
   Taps<VEC> w;
   w.load(p.w, p.bias, c0);
-  const int tend = t1 + kHist, most = min(p.T, tend);
+  const int most = min(p.T, t1 + kHist);
+  const uint16_t *nx = xb + t0 * p.sx.token, *ng = dout + (b * p.T + t0) * p.C + c0;
+  uint16_t* dxt = dx + (b * p.T + t0 - kHist) * p.C + c0;
   Raw xr[U], gr[U];
   auto fetch = [&](int t) {
+    const bool full = t + U <= most;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < most) {
-        xr[u] = *reinterpret_cast<const Raw*>(xb + (t + u) * p.sx.token);
-        gr[u] = *reinterpret_cast<const Raw*>(gb + (long long)(t + u) * p.C);
+    for (int u = 0; u < U; ++u, nx += p.sx.token, ng += p.C) {
+      if (full || t + u < most) {
+        xr[u] = *reinterpret_cast<const Raw*>(nx);
+        gr[u] = *reinterpret_cast<const Raw*>(ng);
       } else {
         xr[u] = gr[u] = Raw{};
       }
+    }
   };
-  fetch(t0);
-  for (int t = t0; t < tend; t += U) {
+  // Tokens t .. t + 3; token t + u completes dX[t + u - 3].  The stretch's own groups (a stretch is
+  // a multiple of four tokens, but for the sequence's end, past which dout and so dpre is zero)
+  // enter dw and dbias, the one after them does not.
+  auto group = [&](int t, auto own) {
     float2 g[U][P];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Ch::unpack(xr[u], x[kHist + u]);
       Ch::unpack(gr[u], g[u]);
     }
-    fetch(t + U);  // while these are computed
+    if (own.value) fetch(t + U);  // while these are computed
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool mine = t + u < t1;
-      // At token t + u, dX[t + u - 3] is complete.  (dout is zero past the sequence, so dpre is.)
+    for (int u = 0; u < U; ++u, dxt += p.C) {
       float2 o[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -208,30 +210,35 @@ __global__ void __launch_bounds__(kThreads)
         s = fma2(w.w[2][i], x[u + 2][i], s);
         s = fma2(w.w[3][i], x[u + 3][i], s);
         const float2 sig = sigmoid2(s), one = make_float2(1.f, 1.f);
-        // sigma (1 + s (1 - sigma)); where sigma is 0, s may be -infinity: no slope
-        const float2 slope = mul2(sig, fma2(s, sub2(one, sig), one));
-        const float2 d = mul2(g[u][i], make_float2(sig.x > 0.f ? slope.x : 0.f, sig.y > 0.f ? slope.y : 0.f));
-        const float2 m = mine ? d : zero;
-        db[i] = add2(db[i], m);
-        dw[0][i] = fma2(m, x[u][i], dw[0][i]);
-        dw[1][i] = fma2(m, x[u + 1][i], dw[1][i]);
-        dw[2][i] = fma2(m, x[u + 2][i], dw[2][i]);
-        dw[3][i] = fma2(m, x[u + 3][i], dw[3][i]);
+        // sigma (1 + s (1 - sigma)); s kept finite where sigma is 0
+        s = make_float2(fmaxf(s.x, -1e4f), fmaxf(s.y, -1e4f));
+        const float2 d = mul2(g[u][i], mul2(sig, fma2(s, sub2(one, sig), one)));
+        if (own.value) {
+          db[i] = add2(db[i], d);
+          dw[0][i] = fma2(d, x[u][i], dw[0][i]);
+          dw[1][i] = fma2(d, x[u + 1][i], dw[1][i]);
+          dw[2][i] = fma2(d, x[u + 2][i], dw[2][i]);
+          dw[3][i] = fma2(d, x[u + 3][i], dw[3][i]);
+        }
         e[kHist + u][i] = d;
         o[i] = fma2(w.w[3][i], e[u][i],
                     fma2(w.w[2][i], e[u + 1][i], fma2(w.w[1][i], e[u + 2][i], mul2(w.w[0][i], d))));
       }
       const int at = t + u - kHist;
-      if (at >= t0 && at < t1)
-        *reinterpret_cast<Raw*>(dxb + (long long)at * p.C) = Ch::pack(o);
-      else if (at < 0 && stretch == 0 && dwindow)  // the window's own tokens
-        *reinterpret_cast<Raw*>(dwindow + (b * kHist + at + kHist) * p.C + c0) = Ch::pack(o);
+      if (own.value ? u == kHist || t > t0 : at < t1)
+        *reinterpret_cast<Raw*>(dxt) = Ch::pack(o);
+      else if (own.value && stretch == 0 && dwindow)  // the window's own tokens
+        *reinterpret_cast<Raw*>(dwindow + (b * kHist + u) * p.C + c0) = Ch::pack(o);
     }
 #pragma unroll
     for (int j = 0; j < kHist; ++j)
 #pragma unroll
       for (int i = 0; i < P; ++i) x[j][i] = x[U + j][i], e[j][i] = e[U + j][i];
-  }
+  };
+  fetch(t0);
+  int t = t0;
+  for (; t < t1; t += U) group(t, Flag<true>{});
+  group(t, Flag<false>{});
   float* row = part + ((b * stretches + stretch) * p.C + c0) * (kTaps + 1);
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {

@@ -220,6 +220,20 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t u) {
 }
 
 // m16n8k16 bf16 MMA on an accumulator held as two float2 (rows g and g + 8).
+// 1 / (1 + e^-x) of two values: relative error a few 2^-22 (one exponential and one reciprocal
+// unit operation each, results below 2^-126 flushed to zero; the plain intrinsics spend four
+// more operations on those).
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 s = mul2(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(s.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(s.y));
+  e = add2(e, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
+}
+
 __device__ __forceinline__ void mma2(float2 (&d)[2], const uint32_t (&a)[4], uint32_t b0,
                                      uint32_t b1) {
   asm volatile(
