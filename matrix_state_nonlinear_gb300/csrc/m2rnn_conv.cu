@@ -132,6 +132,12 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Eight bytes to shared memory, asynchronously; zeros without `in`.
+__device__ __forceinline__ void copy8(void* dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 8 : 0)
+               : "memory");
+}
+
 template <bool V>
 struct Flag {
   static constexpr bool value = V;
@@ -141,7 +147,7 @@ struct Flag {
 // t + 3, so the thread runs three tokens past its stretch; only its own tokens enter dw, dbias.
 // The partial sums of each (batch row, stretch) go to `part` [rows][C][5].
 template <int VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     conv_backward_kernel(ConvProblem p, const uint16_t* __restrict__ dout,
                          uint16_t* __restrict__ dx, uint16_t* __restrict__ dwindow,
                          float* __restrict__ part, int span, int groups, int stretches) {
@@ -176,17 +182,38 @@ __global__ void __launch_bounds__(kThreads)
   const int most = min(p.T, t1 + kHist);
   const uint16_t *nx = xb + t0 * p.sx.token, *ng = dout + (b * p.T + t0) * p.C + c0;
   uint16_t* dxt = dx + (b * p.T + t0 - kHist) * p.C + c0;
+  // Loads ahead of their use: four channels by asynchronous copies to the thread's own slots of
+  // shared memory, three groups of tokens ahead (no other thread reads them, so nothing but the
+  // copies themselves is waited for); one channel to registers, one group ahead.
+  constexpr int S = VEC == 4 ? 4 : 1, kAhead = VEC == 4 ? S - 1 : 1;
+  __shared__ Raw slots[VEC == 4 ? S : 1][U][2][VEC == 4 ? kThreads : 1];
   Raw xr[U], gr[U];
+  int head = 0, tail = 0;
   auto fetch = [&](int t) {
-    const bool full = t + U <= most;
 #pragma unroll
     for (int u = 0; u < U; ++u, nx += p.sx.token, ng += p.C) {
-      if (full || t + u < most) {
+      const bool in = t + u < most;
+      if constexpr (VEC == 4) {
+        copy8(&slots[head][u][0][threadIdx.x], in ? nx : xb, in);
+        copy8(&slots[head][u][1][threadIdx.x], in ? ng : dout, in);
+      } else if (in) {
         xr[u] = *reinterpret_cast<const Raw*>(nx);
         gr[u] = *reinterpret_cast<const Raw*>(ng);
       } else {
         xr[u] = gr[u] = Raw{};
       }
+    }
+    if constexpr (VEC == 4) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      head = (head + 1) % S;
+    }
+  };
+  auto take = [&]() {
+    if constexpr (VEC == 4) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+#pragma unroll
+      for (int u = 0; u < U; ++u) xr[u] = slots[tail][u][0][threadIdx.x], gr[u] = slots[tail][u][1][threadIdx.x];
+      tail = (tail + 1) % S;
     }
   };
   // Tokens t .. t + 3; token t + u completes dX[t + u - 3].  The stretch's own groups (a stretch is
@@ -194,12 +221,13 @@ __global__ void __launch_bounds__(kThreads)
   // enter dw and dbias, the one after them does not.
   auto group = [&](int t, auto own) {
     float2 g[U][P];
+    take();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       Ch::unpack(xr[u], x[kHist + u]);
       Ch::unpack(gr[u], g[u]);
     }
-    if (own.value) fetch(t + U);  // while these are computed
+    if (own.value) fetch(t + kAhead * U);  // while these are computed
 #pragma unroll
     for (int u = 0; u < U; ++u, dxt += p.C) {
       float2 o[P];
@@ -235,10 +263,12 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int i = 0; i < P; ++i) x[j][i] = x[U + j][i], e[j][i] = e[U + j][i];
   };
-  fetch(t0);
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) fetch(t0 + s * U);
   int t = t0;
   for (; t < t1; t += U) group(t, Flag<true>{});
   group(t, Flag<false>{});
+  if constexpr (VEC == 4) asm volatile("cp.async.wait_all;" ::: "memory");
   float* row = part + ((b * stretches + stretch) * p.C + c0) * (kTaps + 1);
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
