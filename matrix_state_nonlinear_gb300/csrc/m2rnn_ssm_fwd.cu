@@ -19,6 +19,11 @@
 //    factors of at most one: one exponential per row and block instead of one per score.
 //  * Only H -> q H and U -> H follow the sequence; S and U of the next chunk are issued before this
 //    chunk's P v, so that P never waits for the tensor cores' latency.
+//  * q and k have their own stages, free as soon as the products have read them: with K = 128 only two
+//    fit, and held until y was out they left the loads in the open (222 -> 165 us for 4 sequences of
+//    8192 tokens and 32 heads).  y leaves through v's place.
+//  * The warps run five different programs, together near the instruction cache's size, so each is
+//    kept short: waits that do not succeed at once share one function, loads have one site each.
 // Where the pairs are fewer than the SMs, segments of a sequence run side by side
 // (m2rnn_ssm_state.cu).
 #include <mutex>
@@ -41,15 +46,16 @@ constexpr int kColS = 0, kColY1 = 256, kColY2 = 320, kColU = 384, kTmemCols = 51
 
 template <int KP>
 struct Smem {
-  static constexpr int kStages = KP <= 64 ? 3 : 2;
+  static constexpr int kStages = KP <= 64 ? 3 : 2, kStagesV = KP <= 64 ? 4 : 2;
   static constexpr int kQ = L * KP * 2, kV = L * VT * 2;
-  static constexpr int kStage = 2 * kQ + kV;
-  static constexpr int kW = kStages * kStage;  // weighted v, high and low
+  static constexpr int kStage = 2 * kQ;  // q and k
+  static constexpr int kVs = kStages * kStage;
+  static constexpr int kW = kVs + kStagesV * kV;  // weighted v, high and low
   static constexpr int kH = kW + 2 * kV;
   static constexpr int kGates = kH + KP * VT * 2;
   static constexpr int kWr = kGates + 4 * (int)sizeof(ChunkGates);
   static constexpr int kBars = kWr + VT * 4;
-  static constexpr int kBytes = kBars + 256 + 1024;  // and slack to align the tiles
+  static constexpr int kBytes = kBars + 320 + 1024;  // and slack to align the tiles
   static_assert(kBytes <= 227 * 1024 && sizeof(ChunkGates) % 16 == 0, "");
 };
 
@@ -57,22 +63,23 @@ struct Smem {
 // two phases behind would mistake one for the other).  Where a chunk's work may run that far
 // ahead there is a barrier for every buffer, stage or slot.
 struct Bars {
-  uint64_t full[3], empty[3];      // tiles of a stage: loaded; done with (by the warps of y)
+  uint64_t full[3], empty[3];      // q and k of a stage: loaded; done with (S, q H and U are)
+  uint64_t vfull[4], vempty[4];    // v of a stage: loaded; done with (by the warps of y)
   uint64_t gate[4], gate_free[4];  // gates of a chunk: written; done with (by y and the state)
   uint64_t s[2], p[2];             // S, P, by buffer
-  uint64_t q, y, y_free;           // q H, P v done; Y read
+  uint64_t y, y_free;              // q H and P v done; Y read
   uint64_t u, u_free, w, h;        // U done, read; weighted v, H done
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 256, "");
+static_assert(sizeof(Bars) <= 320, "");
 
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                        const __grid_constant__ CUtensorMap map_v, SsmProblem p, SsmCut cut, bool tma, bool vec) {
   using S = Smem<KP>;
-  constexpr int ST = S::kStages, PANELS = KP / 64;
+  constexpr int ST = S::kStages, SV = S::kStagesV, PANELS = KP / 64;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t base = smem_u32(smem);
@@ -93,10 +100,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const size_t plane = (size_t)p.K * p.V;
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 8);
+    for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.vfull[i], 1), mbar_init(&bar.vempty[i], 8);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 16);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.s[i], 1), mbar_init(&bar.p[i], 8);
-    mbar_init(&bar.q, 1), mbar_init(&bar.y, 2);
+    mbar_init(&bar.y, 2);
     mbar_init(&bar.y_free, 8), mbar_init(&bar.u, 1), mbar_init(&bar.u_free, 8);
     mbar_init(&bar.w, 8), mbar_init(&bar.h, 8);
     bar.abort = 0;
@@ -109,6 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
   auto stage = [&](int i) { return base + i % ST * S::kStage; };
+  auto vstage = [&](int i) { return base + S::kVs + i % SV * S::kV; };
   const int quarter = warp & 3, row = 32 * quarter + lane;  // token of the chunk, tensor-memory lane
   const uint32_t t_lane = tmem + ((uint32_t)(32 * quarter) << 16);
   bool ok = true;  // uniform in the warp
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto put_weighted = [&](int i) {
       if (i > 0) wait(bar.u, i - 1);  // the product that read it
       wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.full[i % ST], i / ST)) return;
+      if (!wait(bar.vfull[i % SV], i / SV)) return;
       const float w = gates[i & 3].wk[row];
       const float2 w2 = make_float2(w, w);
 #pragma unroll 1
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = Tile<VT>::at(0, row, 4 * half + c);
         float2 f[4];
         uint32_t hi[4], lo[4];
-        unpack8(ld_shared_v4(stage(i) + 2 * S::kQ + at), f);
+        unpack8(ld_shared_v4(vstage(i) + at), f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) split_bf16x2(mul2(f[e], w2), hi[e], lo[e]);
         st_shared_v4(base + S::kW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
@@ -204,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float e = exp2_approx(gates[i & 3].cum[row]);
       const float2 e2 = make_float2(e, e);
-      const uint32_t tq = stage(i), tv = stage(i) + 2 * S::kQ;
+      const uint32_t tv = vstage(i);
 #pragma unroll 1
-      for (int x = 2 * half; x < 2 * half + 2; ++x) {  // 16 columns at a time, out through this token's row of q
+      for (int x = 2 * half; x < 2 * half + 2; ++x) {  // 16 columns at a time, in place of this token's v
         float y1[16], y2[16];
         tmem_ld16_nowait(t_lane + kColY1 + 16 * x, y1);
         tmem_ld16_nowait(t_lane + kColY2 + 16 * x, y2);
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 r = fma2(w[z], v[z], fma2(e2, make_float2(y1[k], y1[k + 1]), make_float2(y2[k], y2[k + 1])));
             o[z] = pack_bf16x2(r.x, r.y);
           }
-          st_shared_v4(Tile<VT>::at(tq, row, 2 * x + c), make_uint4(o[0], o[1], o[2], o[3]));
+          st_shared_v4(Tile<VT>::at(tv, row, 2 * x + c), make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
       __syncwarp();
@@ -243,14 +252,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int r = (lane >> 2) + 8 * x;
-          if (r < most) *reinterpret_cast<uint4*>(to) = ld_shared_v4(Tile<VT>::at(tq, 32 * quarter + r, 4 * half + ch));
+          if (r < most) *reinterpret_cast<uint4*>(to) = ld_shared_v4(Tile<VT>::at(tv, 32 * quarter + r, 4 * half + ch));
           to += 8 * ystride;
         }
       } else {
         for (int x = lane; x < 32 * 32; x += 32) {
           const int r = x >> 5, col = x & 31;
           if (r < left && col0 + col < vw) {
-            const uint32_t u = ld_shared_u32(Tile<VT>::at(tq, 32 * quarter + r, 4 * half + (col >> 3)) + (col & 6) * 2);
+            const uint32_t u = ld_shared_u32(Tile<VT>::at(tv, 32 * quarter + r, 4 * half + (col >> 3)) + (col & 6) * 2);
             yg[r * ystride + col] = (uint16_t)(col & 1 ? u >> 16 : u);
           }
         }
@@ -258,11 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();  // the rows are the next load's
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&bar.empty[i % ST]);
+        mbar_arrive(&bar.vempty[i % SV]);
         mbar_arrive(&bar.gate_free[i & 3]);
       }
     }
-  } else if (warp < kWarpMma) {  // ------------------------------------- the state, weighted v
+  } else if (warp < kWarpMma) {  // ------------------------------------- the state
     // This thread's row of the state.  With K <= 64 the product has 64 rows, 16 in each quarter's
     // first lanes.
     const int hrow = KP > 64 ? row : 16 * quarter + lane;
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar.u_free);
         mbar_arrive(&bar.gate_free[i & 3]);
       }
-      if (!wait(bar.q, i)) break;  // q H of this chunk still reads the state's tile
+      if (!wait(bar.empty[i % ST], i / ST)) break;  // q H of this chunk still reads the state's tile
       put_state();
       fence_proxy_async_smem();
       warp_arrive(&bar.h, lane);
@@ -343,9 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (i < 0) continue;
         if (i > 0) wait(bar.y_free, i - 1);
+        wait(bar.vfull[i % SV], i / SV);
         if (!wait(bar.p[i & 1], i >> 1)) break;
         tc_fence_after();
-        const uint64_t dv = desc_mn(stage(i) + 2 * S::kQ, L);
+        const uint64_t dv = desc_mn(vstage(i), L);
         const uint32_t tp = tmem + kColS + (i & 1) * 128;
         umma4_ta_if<128>(leader, tmem + kColY2, tp, dv, idesc_y, 0u);
         umma4_ta_if<128>(leader, tmem + kColY2, tp + 64, dv + 512, idesc_y, 1u);
@@ -363,10 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_steps<L / 16, 128, 128>(leader, tmem + kColU, desc_mn(stage(i) + S::kQ, L), dw, idesc_u, false);
         umma_commit_if(leader, &bar.u);
         if (i > 0) wait(bar.y_free, i - 1);
+        wait(bar.s[i & 1], i >> 1);  // so that the stage is done with when q H is
         if (!wait(bar.h, i)) break;
         tc_fence_after();
         umma_steps<KP / 16, 2, 128, L * 8 - 8>(leader, tmem + kColY1, desc_k(stage(i)), dh, idesc_y, false);
-        umma_commit_if(leader, &bar.q);
+        umma_commit_if(leader, &bar.empty[i % ST]);
         umma_commit_if(leader, &bar.y);
       }
     }
@@ -382,60 +393,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     float4 a = make_float4(logit(i, 0), logit(i, 1), logit(i, 2), logit(i, 3));
     for (; i < count; i += 2) {
       const float4 ahead = make_float4(logit(i + 2, 0), logit(i + 2, 1), logit(i + 2, 2), logit(i + 2, 3));
-      auto load = [&]() {
-        if (i >= ST && !wait(bar.empty[i % ST], i / ST - 1)) return;
-        const int t0 = (first + i) * L;
-        if (tma) {
-          if (lane == 0) {
-            uint64_t* full = &bar.full[i % ST];
-            unsigned char* at = smem + i % ST * S::kStage;
-            mbar_arrive_expect_tx(full, S::kStage);
-#pragma unroll
-            for (int x = 0; x < PANELS; ++x) {
-              tma_load_4d(at + panel(x, L), &map_q, full, 64 * x, head, t0, (int)b);
-              tma_load_4d(at + S::kQ + panel(x, L), &map_k, full, 64 * x, head, t0, (int)b);
-            }
-            tma_load_4d(at + 2 * S::kQ, &map_v, full, v0, n, t0, (int)b);
-            if (i + 2 < count) {  // on its way to L2, before its place is free
-              const int t2 = t0 + 2 * L;
-#pragma unroll
-              for (int x = 0; x < PANELS; ++x) {
-                tma_prefetch_4d(&map_q, 64 * x, head, t2, (int)b);
-                tma_prefetch_4d(&map_k, 64 * x, head, t2, (int)b);
-              }
-              tma_prefetch_4d(&map_v, v0, n, t2, (int)b);
-            }
-          }
-          __syncwarp();
-        } else {
-          const int rows = min(L, p.T - t0);
-          const uint16_t* q = p.q + b * p.sq.batch + t0 * p.sq.token + (long long)head * p.K;
-          const uint16_t* k = p.k + b * p.sk.batch + t0 * p.sk.token + (long long)head * p.K;
-          const uint16_t* v = p.v + b * p.sv.batch + t0 * p.sv.token + (long long)n * p.V + v0;
+      const int t0 = (first + i) * L, s = i % ST, sv = i % SV, rows = min(L, p.T - t0);
+      // q and k of a stage are free once the products have read them, v when y has left its place.
+      if (i >= ST && !wait(bar.empty[s], i / ST - 1)) break;
+      if (tma) {
+        if (lane == 0) {
+          unsigned char* to = smem + s * S::kStage;
+          mbar_arrive_expect_tx(&bar.full[s], 2 * S::kQ);
+#pragma unroll 1
           for (int x = 0; x < PANELS; ++x) {
-            copy_tokens(stage(i) + panel(x, L), q + 64 * x, p.sq.token, rows, p.K - 64 * x, lane);
-            copy_tokens(stage(i) + S::kQ + panel(x, L), k + 64 * x, p.sk.token, rows, p.K - 64 * x, lane);
+            tma_load_4d(to + panel(x, L), &map_q, &bar.full[s], 64 * x, head, t0, (int)b);
+            tma_load_4d(to + S::kQ + panel(x, L), &map_k, &bar.full[s], 64 * x, head, t0, (int)b);
           }
-          copy_tokens(stage(i) + 2 * S::kQ, v, p.sv.token, rows, vw, lane);
-          fence_proxy_async_smem();
-          warp_arrive(&bar.full[i % ST], lane);
         }
-      };
-      // The first chunks' tiles before their gates, later ones' after: their places are taken still.
-      if (i < ST) load();
+        __syncwarp();
+      } else {
+        const uint16_t* q = p.q + b * p.sq.batch + t0 * p.sq.token + (long long)head * p.K;
+        const uint16_t* k = p.k + b * p.sk.batch + t0 * p.sk.token + (long long)head * p.K;
+#pragma unroll 1
+        for (int x = 0; x < 2 * PANELS; ++x) {
+          const int half = x / PANELS, c = x % PANELS;
+          copy_tokens(stage(i) + half * S::kQ + panel(c, L), (half ? k : q) + 64 * c,
+                      half ? p.sk.token : p.sq.token, rows, p.K - 64 * c, lane);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&bar.full[s], lane);
+      }
       if (i >= 4 && !wait(bar.gate_free[i & 3], (i >> 2) - 1)) break;
       put_chunk_gates(
           gates[i & 3], [&](int e) { return e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w; }, alpha, beta, lane);
       warp_arrive(&bar.gate[i & 3], lane);
       a = ahead;
-      if (i >= ST) load();
-      if (!ok) break;
+      if (i >= SV && !wait(bar.vempty[sv], i / SV - 1)) break;
+      if (tma) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar.vfull[sv], S::kV);
+          tma_load_4d(smem + S::kVs + sv * S::kV, &map_v, &bar.vfull[sv], v0, n, t0, (int)b);
+          if (i + 2 < count) {  // on its way to L2, before its place is free
+            const int t2 = t0 + 2 * L;
+#pragma unroll 1
+            for (int x = 0; x < PANELS; ++x) {
+              tma_prefetch_4d(&map_q, 64 * x, head, t2, (int)b);
+              tma_prefetch_4d(&map_k, 64 * x, head, t2, (int)b);
+            }
+            tma_prefetch_4d(&map_v, v0, n, t2, (int)b);
+          }
+        }
+        __syncwarp();
+      } else {
+        copy_tokens(vstage(i), p.v + b * p.sv.batch + t0 * p.sv.token + (long long)n * p.V + v0, p.sv.token, rows, vw,
+                    lane);
+        fence_proxy_async_smem();
+        warp_arrive(&bar.vfull[sv], lane);
+      }
     }
     // Given up: whatever was started here arrives before the block ends (a stage's load that was
     // not started times out, one of an earlier chunk has long arrived).
     if (!ok && tma)
-      for (int s = 0; s < ST; ++s)
-        for (int phase = 0; phase < 2; ++phase) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
+#pragma unroll 1
+      for (int phase = 0; phase < 2; ++phase) {
+#pragma unroll 1
+        for (int s = 0; s < ST; ++s) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
+#pragma unroll 1
+        for (int s = 0; s < SV; ++s) mbar_wait_bounded(&bar.vfull[s], phase, kWaitLimitCycles / 64);
+      }
   }
   if (!ok && lane == 0) {
     *abort = 1;

@@ -75,8 +75,25 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
 
 // A whole warp waits for the phase of `bar` with the given parity; false, for every lane, where the
 // wait ran out or another warp has given up.
+// The wait in full: one copy for all the warps' programs, which compete for the instruction cache.
+static __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volatile int* abort) {
+  const uint32_t start = (uint32_t)clock();
+  uint32_t done;
+  do {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (!done && (*abort || (uint32_t)clock() - start > (uint32_t)kWaitLimitCycles)) break;
+  } while (!done);
+  return __all_sync(~0u, done != 0);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(~0u, wait_or_abort(bar, parity, kWaitLimitCycles, abort));
+  if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_long(smem_u32(bar), parity, abort);
 }
 // One arrival for the warp, after its lanes' earlier work.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -113,7 +130,7 @@ inline bool token_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // The same box by one warp, value by value, for operands that a tensor map cannot describe.
-__device__ __forceinline__ void copy_tokens(uint32_t tile, const uint16_t* src, long long stride, int rows, int width,
+static __device__ __noinline__ void copy_tokens(uint32_t tile, const uint16_t* src, long long stride, int rows, int width,
                                             int lane) {
   for (int id = lane; id < kSsmChunk * 64; id += 32) {
     const int r = id >> 6, c = id & 63;
