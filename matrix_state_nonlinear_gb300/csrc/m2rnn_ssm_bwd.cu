@@ -61,9 +61,10 @@ struct Smem {
   static constexpr int kP = kScaled + kTile, kDs = kP + 2 * kTile;
   static constexpr int kGates = kDs + 2 * kTile;
   static constexpr int kSums = kGates + 2 * (int)sizeof(BackwardGates);
-  static constexpr int kBars = kSums + (int)sizeof(Sums);
+  static constexpr int kWr = kSums + (int)sizeof(Sums);
+  static constexpr int kBars = kWr + 16 * 16 * 4;
   static constexpr int kBytes = kBars + 256 + 1024;  // and slack to align the tiles
-  static_assert(kBytes <= 227 * 1024, "");
+  static_assert(kBytes <= 227 * 1024 && kWr % 16 == 0, "");
 };
 
 // One phase per step (per item: qk, acc_free; per head: sums, sums_free); every barrier's next
@@ -72,7 +73,7 @@ struct Bars {
   uint64_t qk, vd, h, g;            // tiles loaded
   uint64_t step_free, vd_read;      // the step's accumulators, v and dy read
   uint64_t scaled1, scaled2;        // exp(c) dy, w v written
-  uint64_t s, pds, hd, q_read, gd, done;  // S, dP done; P, dS written; q H done, read; k G done; P^T dy done
+  uint64_t s, pds, hd, q_read, gd, done;  // S, dP done; P, dS written; q H done, read; k G, P^T dy done; all done
   uint64_t acc_free;                // dq, dk read
   uint64_t gate[2], gate_free[2];
   uint64_t sums, sums_free;
@@ -106,7 +107,7 @@ struct Cursor {
   }
   __device__ bool open(const Plan& plan, int nqk) {
     if (item >= plan.items) return false;
-    long long x = item;
+    uint32_t x = (uint32_t)item;
     split = (int)(x % plan.splits), x /= plan.splits;
     chunk = (int)(x % plan.chunks), x /= plan.chunks;
     group = (int)(x % nqk);
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   BackwardGates* gates = reinterpret_cast<BackwardGates*>(smem + S::kGates);
   Sums& sums = *reinterpret_cast<Sums*>(smem + S::kSums);
   Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
+  float (*wr)[16] = reinterpret_cast<float (*)[16]>(smem + S::kWr);  // w_r, 16 columns per warp
   volatile int* abort = &bar.abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t plane = (size_t)p.K * p.V;
@@ -181,12 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; more; ++j) {
       const int v0 = at.vt * VT, vw = min(VT, p.V - v0);
       if (at.vt == 0 && at.head_no > 0) wait(bar.sums_free, at.head_no - 1);
-      if (sent_all) wait(bar.out_free, j - 1);  // (the place of the scaled operand)
+      if (j > 0) wait(bar.done, j - 1);         // (the scaled operand's place is read no more,
+      if (sent_all) wait(bar.out_free, j - 1);  // nor does dk leave through it)
       wait(bar.gate[j & 1], j >> 1);
       if (!wait(bar.vd, j)) break;
       const ChunkGates& G = gates[j & 1].g;
       const float cum = G.cum[row], wk = G.wk[row];
       const float et = exp2_approx(cum);
+      const float wl = lane < 16 && c0 + lane < vw ? p.w_r[(size_t)at.head * p.V + v0 + c0 + lane] : 0.f;
       // exp(c) dy as an operand (and below w v, in the same place).
       auto put_scaled = [&](const uint4 (&from)[2], float f, uint64_t& ready) {
         const float2 f2 = make_float2(f, f);
@@ -321,25 +325,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       warp_arrive(&bar.pds, lane);
 
-      // dw_r of the chunk: four columns per warp, four tokens per lane.
-      {
-        float2 a01 = make_float2(0.f, 0.f), a23 = a01;
+      // dw_r of the chunk: eight columns, four tokens per lane, by the quarters with the fewest scores.
+      if (quarter < 2) {
+        const int piece = 2 * group + quarter;
+        float2 s[4] = {};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint32_t a = Tile<VT>::at(0, lane + 32 * r, warp >> 1) + 8 * (warp & 1);
-          a01 = fma2(bf16x2_to_float2(ld_shared_u32(tv + a)), bf16x2_to_float2(ld_shared_u32(td + a)), a01);
-          a23 = fma2(bf16x2_to_float2(ld_shared_u32(tv + a + 4)), bf16x2_to_float2(ld_shared_u32(td + a + 4)), a23);
-        }
-        const bool up = lane & 16, mid = lane & 8;
-        float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
-        k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
-        k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
-        float k = mid ? k1 : k0;
-        k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
+          const uint32_t a = Tile<VT>::at(0, lane + 32 * r, piece);
+          float2 x[4], y[4];
+          unpack8(ld_shared_v4(tv + a), x);
+          unpack8(ld_shared_v4(td + a), y);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) k += __shfl_xor_sync(~0u, k, o);
-        const int col = 4 * warp + (up ? 2 : 0) + (mid ? 1 : 0);
-        if ((lane & 7) == 0 && col < vw)
+          for (int e = 0; e < 4; ++e) s[e] = fma2(x[e], y[e], s[e]);
+        }
+        const bool up = lane & 16, mid = lane & 8, low = lane & 4;
+        float2 h0 = up ? s[2] : s[0], h1 = up ? s[3] : s[1];
+        const float2 g0 = up ? s[0] : s[2], g1 = up ? s[1] : s[3];
+        h0.x += __shfl_xor_sync(~0u, g0.x, 16), h0.y += __shfl_xor_sync(~0u, g0.y, 16);
+        h1.x += __shfl_xor_sync(~0u, g1.x, 16), h1.y += __shfl_xor_sync(~0u, g1.y, 16);
+        float2 h = mid ? h1 : h0;
+        const float2 g = mid ? h0 : h1;
+        h.x += __shfl_xor_sync(~0u, g.x, 8), h.y += __shfl_xor_sync(~0u, g.y, 8);
+        float k = (low ? h.y : h.x) + __shfl_xor_sync(~0u, low ? h.x : h.y, 4);
+        k += __shfl_xor_sync(~0u, k, 2);
+        k += __shfl_xor_sync(~0u, k, 1);
+        const int col = 8 * piece + (up ? 4 : 0) + (mid ? 2 : 0) + (low ? 1 : 0);
+        if ((lane & 3) == 0 && col < vw)
           w.par[((size_t)(at.b * plan.chunks + at.chunk) * p.N + at.head) * (2 + p.V) + 2 + v0 + col] = k;
       }
 
@@ -378,78 +389,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float r = et * (dot.x + dot.y);
         to = at.vt ? to + r : r;
       }
+      if (lane < 16) wr[warp][lane] = wl;
       put_scaled(vr, wk, bar.scaled2);
 
-      // k G: its part of the column sums, and of dv.
-      float2 x[8];
+      // k G: its part of the column sums, and dv = P^T dy + w (k G) + w_r dy, which leaves through the
+      // first half of P's tile.
       if (!wait(bar.gd, j)) break;
       tc_fence_after();
-      {
-        float hi[16], lo[16];
-        tmem_ld16_nowait(t_lane + kColDp + c0, hi);
-        tmem_ld16_nowait(t_lane + kColDp + VT + c0, lo);
-        float2 y[8];
+      float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float2 f[4];
-          unpack8(vr[c], f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[4 * c + e] = f[e];
-        }
-        tmem_ready(hi, lo);
+      for (int c = 0; c < 2; ++c) {
+        float hi[8], lo[8], a[8];
+        tmem_ld8_nowait(t_lane + kColDp + c0 + 8 * c, hi);
+        tmem_ld8_nowait(t_lane + kColDp + VT + c0 + 8 * c, lo);
+        tmem_ld8_nowait(t_lane + kColS + c0 + 8 * c, a);
+        float2 x[4], y[4];
+        uint32_t o[4];
+        unpack8(vr[c], x);
+        unpack8(dr[c], y);
+        tmem_ready(hi, lo, a);
         const float2 w2 = make_float2(wk, wk);
-        float2 dot = make_float2(0.f, 0.f);
+        const float4 w0 = reinterpret_cast<const float4*>(wr[warp])[2 * c], w1 = reinterpret_cast<const float4*>(wr[warp])[2 * c + 1];
+        const float2 u[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y), make_float2(w1.z, w1.w)};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = mul2(w2, add2(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])));
-          dot = fma2(x[e], y[e], dot);
+        for (int e = 0; e < 4; ++e) {
+          const float2 kg = mul2(w2, add2(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])));
+          dot = fma2(kg, x[e], dot);
+          const float2 r = fma2(u[e], y[e], add2(make_float2(a[2 * e], a[2 * e + 1]), kg));
+          o[e] = pack_bf16x2(r.x, r.y);
         }
+        st_shared_v4(Tile<64>::at(base + S::kP, row, 2 * group + c), make_uint4(o[0], o[1], o[2], o[3]));
+      }
+      {
         float& to = sums.col_state[group][row];
         to = at.vt ? to + (dot.x + dot.y) : dot.x + dot.y;
       }
-      if (at.head_end(plan)) warp_arrive(&bar.sums, lane);
-
-      // dv = P^T dy + w (k G) + w_r dy.
-      if (!wait(bar.done, j)) break;
-      tc_fence_after();
-      {
-        float a[16];
-        tmem_ld16_nowait(t_lane + kColS + c0, a);
-        float2 y[8];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float2 f[4];
-          unpack8(dr[c], f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[4 * c + e] = f[e];
-        }
-        tmem_ready(a);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.step_free);
-          mbar_arrive(&bar.gate_free[j & 1]);
-        }
-        // dv leaves through the first half of P's tile.
-        const float* wr = p.w_r + (size_t)at.head * p.V + v0 + c0;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t o[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int e = 4 * c + z;
-            const float2 w2 = make_float2(c0 + 2 * e < vw ? wr[2 * e] : 0.f, c0 + 2 * e + 1 < vw ? wr[2 * e + 1] : 0.f);
-            const float2 r = fma2(w2, y[e], add2(make_float2(a[2 * e], a[2 * e + 1]), x[e]));
-            o[z] = pack_bf16x2(r.x, r.y);
-          }
-          st_shared_v4(Tile<64>::at(base + S::kP, row, 2 * group + c), make_uint4(o[0], o[1], o[2], o[3]));
-        }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar.step_free);
+        mbar_arrive(&bar.gate_free[j & 1]);
+        if (at.head_end(plan)) mbar_arrive(&bar.sums);
       }
 
       // dq, dk of the item: bf16 through dS's tile, and the other half of P's and the scaled
       // operand's; parts of a split item float32, a token per lane.
       sent_all = at.last(plan);
       if (sent_all) {
+        if (!wait(bar.done, j)) break;
+        tc_fence_after();
         constexpr int KC = KP / 4;  // columns per warp
 #pragma unroll 1
         for (int c = 0; c < 2 * KC; c += 16) {
@@ -511,16 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit_if(leader, &bar.hd);
       umma_steps<L / 16, 2, 128, PANEL>(leader, tmem + kColDq, desc_k(ts), desc_mn(k, L), id_dq, true);
       umma_steps<L / 16, 128, 128>(leader, tmem + kColDk, desc_mn(ts, L), desc_mn(q, L), id_dk, !first);
-      wait(bar.g, j);
-      if (!wait(bar.scaled2, j)) break;
-      tc_fence_after();
-      umma_steps<KP / 16, 2, 128, PANEL>(leader, tmem + kColDp, desc_k(k), desc_mn(st, KP), id_st, false);
-      umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st), id_k, true);
-      umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st + KP * VT * 2), id_k, true);
-      umma_commit_if(leader, &bar.gd);
       if (!wait(bar.q_read, j)) break;
       tc_fence_after();
       umma_steps<L / 16, 128, 128>(leader, tmem + kColS, desc_mn(tp, L), desc_mn(dy, L), id_dv, false);
+      if (!wait(bar.g, j)) break;
+      umma_steps<KP / 16, 2, 128, PANEL>(leader, tmem + kColDp, desc_k(k), desc_mn(st, KP), id_st, false);
+      umma_commit_if(leader, &bar.gd);
+      if (!wait(bar.scaled2, j)) break;
+      tc_fence_after();
+      umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st), id_k, true);
+      umma_steps<4, 2, 2>(leader, tmem + kColDk, desc_k(sc), desc_k(st + KP * VT * 2), id_k, true);
       umma_commit_if(leader, &bar.done);
       more = at.next(plan, p.Nqk);
     }
@@ -557,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   sizeof(BackwardGates), &bar.gate[j & 1]);
       }
       if (j > 0) wait(bar.vd_read, j - 1);
-      if (j > 0 && !wait(bar.done, j - 1)) break;
+      if (j > 0 && !wait(bar.gd, j - 1)) break;
       if (tma) {
         if (lane == 0) {
           mbar_arrive_expect_tx(&bar.vd, 2 * S::kTile);
@@ -594,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // H once the products with the step before's G are done, G once those with H are.
 #pragma unroll 1
       for (int s = 0; s < 2; ++s) {
-        if (s == 0 && j > 0 && !wait(bar.gd, j - 1)) break;
+        if (s == 0 && j > 0 && !wait(bar.done, j - 1)) break;
         if (s == 1 && !wait(bar.hd, j)) break;
         uint64_t* full = s ? &bar.g : &bar.h;
         if (tma) {
@@ -905,6 +893,7 @@ cudaError_t launch_ssm_backward(const SsmBackwardProblem& p, cudaStream_t stream
     return err;
   }
   const Plan plan = make_plan(p.B, p.T, p.N, p.Nqk, p.V);
+  if (plan.items > 0x7fffffffLL) return cudaErrorInvalidValue;  // (thousands of gigabytes of k and v)
   const Workspace w = carve(p.ws, plan, p.B, p.T, p.N, p.Nqk, p.K, p.V);
   const Strides dense{(long long)p.T * p.N * p.V, (long long)p.N * p.V};
   const bool vec = rows_of_16(p.q, p.sq, p.K) && rows_of_16(p.k, p.sk, p.K) && rows_of_16(p.v, p.sv, p.V) &&

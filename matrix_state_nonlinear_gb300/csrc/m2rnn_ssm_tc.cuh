@@ -18,7 +18,7 @@ __device__ __forceinline__ constexpr int panel(int i, int rows) { return i * row
 // A_PANEL, B_PANEL the further advance after every fourth (16-byte units).
 template <int STEPS, int A_STEP, int B_STEP, int A_PANEL = 0, int B_PANEL = 0>
 __device__ __forceinline__ void umma_steps(bool pred, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < STEPS / 4; ++i)
     umma4_if<A_STEP, B_STEP>(pred, d, a + i * (4 * A_STEP + A_PANEL), b + i * (4 * B_STEP + B_PANEL), idesc,
                              i > 0 || accumulate ? 1u : 0u);
@@ -58,6 +58,12 @@ template <typename... V>
 __device__ __forceinline__ void tmem_ready(V&... v) {
   tmem_wait_ld();
   (tie(v), ...);
+}
+// Thread i of a warp loads 8 consecutive columns of tensor-memory lane i of the warp's quarter.
+__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr));
 }
 // Thread i of a warp writes 8 consecutive columns of tensor-memory lane i of the warp's quarter.
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
