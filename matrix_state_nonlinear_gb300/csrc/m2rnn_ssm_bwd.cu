@@ -762,12 +762,21 @@ __global__ void __launch_bounds__(256)
   uint16_t* dst = (blockIdx.y ? dk : dq) + ((b * T + (long long)chunk * L) * Nqk + group) * K;
   const int rows = min(L, T - chunk * L);
   const int c0 = 32 * blockIdx.z;
-#pragma unroll 4
-  for (int id = threadIdx.x; id < 32 * L; id += 256) {
-    const int c = id / L, r = id % L;
-    float s = 0.f;
-    for (int i = 0; i < plan.splits; ++i) s += src[((first + i) * kp + c0 + c) * L + r];
-    part[c][r] = s;
+  float4 s[4];  // 32 columns of 32 times four tokens, four of these per thread
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < plan.splits; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = 8 * e + threadIdx.x / 32;
+      const float4 x = reinterpret_cast<const float4*>(src + ((first + i) * kp + c0 + c) * L)[threadIdx.x % 32];
+      s[e].x += x.x, s[e].y += x.y, s[e].z += x.z, s[e].w += x.w;
+    }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float* to = &part[8 * e + threadIdx.x / 32][4 * (threadIdx.x % 32)];
+    to[0] = s[e].x, to[1] = s[e].y, to[2] = s[e].z, to[3] = s[e].w;
   }
   __syncthreads();
   for (int id = threadIdx.x; id < 32 * L; id += 256) {
