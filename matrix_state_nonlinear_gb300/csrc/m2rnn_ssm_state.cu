@@ -24,7 +24,7 @@ constexpr int L = kTokens;
 constexpr int VT = kSsmColumns;
 constexpr int kWarpState = 8, kWarpMma = 16, kWarpLoad = 17, kWarpGate = 18, kWarps = 20;  // 0..7: weights
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTmemCols = 128;
+constexpr int kTmemCols = 256;  // two products
 
 struct alignas(16) Weights {
   float w[L];
@@ -32,23 +32,27 @@ struct alignas(16) Weights {
   float total;  // log2 of the chunk's decay
 };
 
-template <int KP, bool KEEP>
+template <int KP, bool REVERSE, bool KEEP>
 struct Smem {
   static constexpr int kStages = KEEP && KP > 64 ? 2 : 3;
+  // Weighted y of two chunks, so that weighing and the product overlap: 142 -> 112 us for pieces of
+  // 65536 tokens of 16 heads, K = 64, V = 128.  (Backwards with K = 128 there is no room beside H; the traffic of the states bounds that one.)
+  static constexpr int kW2 = KEEP && REVERSE && KP > 64 ? 1 : 2;
   static constexpr int kX = L * KP * 2, kY = L * VT * 2;
   static constexpr int kStage = kX + kY;
   static constexpr int kW = kStages * kStage;  // weighted y, high and low
-  static constexpr int kKept = kW + 2 * kY;  // a state on its way out, high and low; and H on its way in
+  static constexpr int kKept = kW + kW2 * 2 * kY;  // a state on its way out, high and low; and H on its way in
   static constexpr int kHs = kKept + (KEEP ? 2 * KP * VT * 2 : 0);
-  static constexpr int kWeights = kHs + (KEEP ? 2 * KP * VT * 2 : 0);
+  static constexpr int kWeights = kHs + (KEEP && REVERSE ? 2 * KP * VT * 2 : 0);
   static constexpr int kBars = kWeights + 4 * (int)sizeof(Weights);
   static constexpr int kBytes = kBars + 256 + 1024;
+  static_assert(kBytes <= 227 * 1024, "");
 };
 
 struct Bars {
   uint64_t full[3], empty[3];
   uint64_t gate[4], gate_free[4];
-  uint64_t u, u_free, w;  // U done, read; weighted y written
+  uint64_t u[2], u_free[2], w[2];  // U done, read; weighted y written
   uint64_t put, put_free, hs, hs_free;  // kept state written, on its way; H loaded, read
   uint32_t tmem;
   int abort;
@@ -59,8 +63,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ssm_state_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y,
                      const __grid_constant__ CUtensorMap map_kept, const __grid_constant__ CUtensorMap map_hs,
                      StateProblem p, bool tma) {
-  using S = Smem<KP, KEEP>;
-  constexpr int ST = S::kStages, PANELS = KP / 64;
+  using S = Smem<KP, REVERSE, KEEP>;
+  constexpr int ST = S::kStages, WB = S::kW2, PANELS = KP / 64;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t base = smem_u32(smem);
@@ -83,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 3; ++i) mbar_init(&bar.full[i], 1), mbar_init(&bar.empty[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 8);
-    mbar_init(&bar.u, 1), mbar_init(&bar.u_free, 8), mbar_init(&bar.w, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar.u[i], 1), mbar_init(&bar.u_free[i], 8), mbar_init(&bar.w[i], 8);
     mbar_init(&bar.put, 8), mbar_init(&bar.put_free, 1), mbar_init(&bar.hs, 1), mbar_init(&bar.hs_free, 8);
     bar.abort = 0;
     fence_mbar_init();
@@ -104,11 +108,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kWarpState) {  // --------------------------------------- weighted y
     for (int i = 0; i < count; ++i) {
-      if (i > 0) wait(bar.u, i - 1);  // the product that read the one before
+      if (i >= WB) wait(bar.u[i % WB], i / WB - 1);  // the product that read the place's last
       wait(bar.gate[i & 3], i >> 2);
       if (!wait(bar.full[i % ST], i / ST)) break;
       const float w = weights[i & 3].w[row];
       const float2 w2 = make_float2(w, w);
+      const uint32_t to = base + S::kW + i % WB * 2 * S::kY;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
         const uint32_t at = Tile<VT>::at(0, row, 4 * half + c);
@@ -117,11 +122,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack8(ld_shared_v4(stage(i) + S::kX + at), f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) split_bf16x2(mul2(f[e], w2), hi[e], lo[e]);
-        st_shared_v4(base + S::kW + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        st_shared_v4(base + S::kW + S::kY + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        st_shared_v4(to + at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_shared_v4(to + S::kY + at, make_uint4(lo[0], lo[1], lo[2], lo[3]));
       }
       fence_proxy_async_smem();
-      warp_arrive(&bar.w, lane);
+      warp_arrive(&bar.w[i % WB], lane);
     }
   } else if (warp < kWarpMma) {  // ---------------------------------- the state
     // This thread's row and half of the columns.  With K <= 64 the product has 64 rows, 16 in each
@@ -179,17 +184,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (i == count) break;
       wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.u, i)) break;
+      if (!wait(bar.u[i % WB], i / WB)) break;
       tc_fence_after();
       const float total = weights[i & 3].total;
       decay += total;
       const float e = exp2_approx(total);
       const float2 e2 = make_float2(e, e);
+      const uint32_t tu = t_lane + i % WB * 2 * VT + hcol;
 #pragma unroll
       for (int x = 0; x < HC / 16; ++x) {
         float hi[16], lo[16];
-        tmem_ld16_nowait(t_lane + hcol + 16 * x, hi);
-        tmem_ld16_nowait(t_lane + VT + hcol + 16 * x, lo);
+        tmem_ld16_nowait(tu + 16 * x, hi);
+        tmem_ld16_nowait(tu + VT + 16 * x, lo);
         tmem_ready(hi, lo);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&bar.u_free);
+        mbar_arrive(&bar.u_free[i % WB]);
         mbar_arrive(&bar.gate_free[i & 3]);
       }
     }
@@ -216,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpMma) {  // --------------------------------- products
     const uint32_t idesc = umma_idesc_bf16_ab(KP, 2 * VT, true, true);
-    const uint64_t dw = desc_mn(base + S::kW, L);
     const bool leader = lane == 0;
     // A kept state to memory, state `chunk` of the sequence forwards, after chunk `chunk` backwards.
     auto send = [&](int i) {
@@ -245,12 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&bar.put_free, lane);
     };
     for (int i = 0; i < count; ++i) {
-      if (i > 0) wait(bar.u_free, i - 1);
+      if (i >= WB) wait(bar.u_free[i % WB], i / WB - 1);
       wait(bar.full[i % ST], i / ST);
-      if (!wait(bar.w, i)) break;
+      if (!wait(bar.w[i % WB], i / WB)) break;
       tc_fence_after();
-      umma_steps<L / 16, 128, 128>(leader, tmem, desc_mn(stage(i), L), dw, idesc, false);
-      umma_commit_if(leader, &bar.u);
+      umma_steps<L / 16, 128, 128>(leader, tmem + i % WB * 2 * VT, desc_mn(stage(i), L),
+                                   desc_mn(base + S::kW + i % WB * 2 * S::kY, L), idesc, false);
+      umma_commit_if(leader, &bar.u[i % WB]);
       umma_commit_if(leader, &bar.empty[i % ST]);
       if (KEEP && i > 0) sent();  // while the product runs
       if (KEEP && !send(i)) break;
@@ -405,7 +411,7 @@ cudaError_t run(const StateProblem& p, int blocks_y, bool vec, cudaStream_t stre
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
     attr = cudaFuncSetAttribute(ssm_state_kernel<KP, REVERSE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<KP, KEEP>::kBytes);
+                                Smem<KP, REVERSE, KEEP>::kBytes);
   });
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
@@ -418,7 +424,7 @@ cudaError_t run(const StateProblem& p, int blocks_y, bool vec, cudaStream_t stre
           (!REVERSE || state_map(enc, &mh, p.Hs, p.K, p.V, 2 * (chunks + 1), pairs, KP));
   const unsigned units = (unsigned)(pairs * ((p.V + VT - 1) / VT));
   ssm_state_kernel<KP, REVERSE, KEEP>
-      <<<dim3(units, blocks_y), kThreads, Smem<KP, KEEP>::kBytes, stream>>>(mx, my, mk, mh, p, tma);
+      <<<dim3(units, blocks_y), kThreads, Smem<KP, REVERSE, KEEP>::kBytes, stream>>>(mx, my, mk, mh, p, tma);
   return cudaGetLastError();
 }
 
