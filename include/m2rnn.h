@@ -382,6 +382,10 @@ m2rnn_status m2rnn_conv_silu_backward_bf16(const uint16_t* x, const float* w, co
  * 1 <= K, V <= 128 (UNSUPPORTED above), B, N >= 1, T >= 0.  a = -infinity makes a token
  * inert (d = 0, f = 1); a token with a large enough a resets the state (f = 0).
  * The state and every sum are float32; the operands of the tensor-core products are bf16.
+ * q, k, v (and dy below) have to be finite: tokens are taken in chunks of 128 and what lies
+ * behind the causal mask is multiplied by zero, so an infinity or NaN reaches every token of
+ * its chunk, earlier ones too, and all later ones.  Operands of K, V % 8 == 0 values with
+ * 16-byte aligned pointers and strides are loaded in tiles; any others value by value, slowly.
  * m2rnn_ssm_forward_bf16 with Hs != NULL also keeps what the backward reads:
  *   Hs    m2rnn_ssm_states_bytes(...) bytes, 16-byte aligned: the state before every chunk
  *         of 128 tokens and the final one, each value as the sum of two bf16 values.

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const uint32_t a = Tile<VT>::at(0, row, 2 * group + c);
+          const uint32_t a = tile_at(0, row, 2 * group + c);
           float2 x[4];
           uint32_t o[4];
           unpack8(from[c], x);
@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&ready, lane);
       };
       {
-        const uint4 dr[2] = {ld_shared_v4(Tile<VT>::at(td, row, 2 * group)),
-                             ld_shared_v4(Tile<VT>::at(td, row, 2 * group + 1))};
+        const uint4 dr[2] = {ld_shared_v4(tile_at(td, row, 2 * group)),
+                             ld_shared_v4(tile_at(td, row, 2 * group + 1))};
         put_scaled(dr, et, bar.scaled1);
       }
 
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (block > quarter) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              st_shared_v4(Tile<64>::at(tp, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
-              st_shared_v4(Tile<64>::at(ts, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
+              st_shared_v4(tile_at(tp, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
+              st_shared_v4(tile_at(ts, row, ch + c), make_uint4(0u, 0u, 0u, 0u));
             }
             continue;
           }
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // eight lanes.
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            st_shared_v4(Tile<64>::at(c < 2 ? tp : ts, row, ch + (c & 1)),
+            st_shared_v4(tile_at(c < 2 ? tp : ts, row, ch + (c & 1)),
                          make_uint4(__float_as_uint(sc[4 * c]), __float_as_uint(sc[4 * c + 1]),
                                     __float_as_uint(sc[4 * c + 2]), __float_as_uint(sc[4 * c + 3])));
           __syncwarp();
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t from = lane & 2 ? ts : tp;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const uint4 q = ld_shared_v4(Tile<64>::at(from, 32 * quarter + (lane >> 2) + 8 * r, ch + (lane & 1)));
+            const uint4 q = ld_shared_v4(tile_at(from, 32 * quarter + (lane >> 2) + 8 * r, ch + (lane & 1)));
             a01 = add2(a01, make_float2(__uint_as_float(q.x), __uint_as_float(q.y)));
             a23 = add2(a23, make_float2(__uint_as_float(q.z), __uint_as_float(q.w)));
           }
@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            st_shared_v4(Tile<64>::at(tp, row, ch + c), make_uint4(po[4 * c], po[4 * c + 1], po[4 * c + 2], po[4 * c + 3]));
-            st_shared_v4(Tile<64>::at(ts, row, ch + c), make_uint4(so[4 * c], so[4 * c + 1], so[4 * c + 2], so[4 * c + 3]));
+            st_shared_v4(tile_at(tp, row, ch + c), make_uint4(po[4 * c], po[4 * c + 1], po[4 * c + 2], po[4 * c + 3]));
+            st_shared_v4(tile_at(ts, row, ch + c), make_uint4(so[4 * c], so[4 * c + 1], so[4 * c + 2], so[4 * c + 3]));
           }
           if (own >= 0 && own < 16) sums.diag[row] = at.vt ? sums.diag[row] + diag : diag;
         }
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 s[4] = {};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint32_t a = Tile<VT>::at(0, lane + 32 * r, piece);
+          const uint32_t a = tile_at(0, lane + 32 * r, piece);
           float2 x[4], y[4];
           unpack8(ld_shared_v4(tv + a), x);
           unpack8(ld_shared_v4(td + a), y);
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 vr[2], dr[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        vr[c] = ld_shared_v4(Tile<VT>::at(tv, row, 2 * group + c));
-        dr[c] = ld_shared_v4(Tile<VT>::at(td, row, 2 * group + c));
+        vr[c] = ld_shared_v4(tile_at(tv, row, 2 * group + c));
+        dr[c] = ld_shared_v4(tile_at(td, row, 2 * group + c));
       }
       warp_arrive(&bar.vd_read, lane);
 
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 r = fma2(u[e], y[e], add2(make_float2(a[2 * e], a[2 * e + 1]), kg));
           o[e] = pack_bf16x2(r.x, r.y);
         }
-        st_shared_v4(Tile<64>::at(base + S::kP, row, 2 * group + c), make_uint4(o[0], o[1], o[2], o[3]));
+        st_shared_v4(tile_at(base + S::kP, row, 2 * group + c), make_uint4(o[0], o[1], o[2], o[3]));
       }
       {
         float& to = sums.col_state[group][row];
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : base + S::kDs + (col >> 6) * S::kTile;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              st_shared_v4(Tile<64>::at(to, row, ((col & 63) >> 3) + x),
+              st_shared_v4(tile_at(to, row, ((col & 63) >> 3) + x),
                            make_uint4(pack_bf16x2(a[8 * x], a[8 * x + 1]), pack_bf16x2(a[8 * x + 2], a[8 * x + 3]),
                                       pack_bf16x2(a[8 * x + 4], a[8 * x + 5]), pack_bf16x2(a[8 * x + 6], a[8 * x + 7])));
           }

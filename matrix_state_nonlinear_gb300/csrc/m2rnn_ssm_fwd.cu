@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 w2 = make_float2(w, w);
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        const uint32_t at = Tile<VT>::at(0, row, 4 * half + c);
+        const uint32_t at = tile_at(0, row, 4 * half + c);
         float2 f[4];
         uint32_t hi[4], lo[4];
         unpack8(ld_shared_v4(vstage(i) + at), f);
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float y1[16], y2[16];
         tmem_ld16_nowait(t_lane + kColY1 + 16 * x, y1);
         tmem_ld16_nowait(t_lane + kColY2 + 16 * x, y2);
-        const uint4 va = ld_shared_v4(Tile<VT>::at(tv, row, 2 * x)), vb = ld_shared_v4(Tile<VT>::at(tv, row, 2 * x + 1));
+        const uint4 va = ld_shared_v4(tile_at(tv, row, 2 * x)), vb = ld_shared_v4(tile_at(tv, row, 2 * x + 1));
         const float4* w4 = reinterpret_cast<const float4*>(wr + 16 * x);
         tmem_ready(y1, y2);
         if (x & 1) {
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 r = fma2(w[z], v[z], fma2(e2, make_float2(y1[k], y1[k + 1]), make_float2(y2[k], y2[k + 1])));
             o[z] = pack_bf16x2(r.x, r.y);
           }
-          st_shared_v4(Tile<VT>::at(tv, row, 2 * x + c), make_uint4(o[0], o[1], o[2], o[3]));
+          st_shared_v4(tile_at(tv, row, 2 * x + c), make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
       __syncwarp();
@@ -252,14 +252,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int r = (lane >> 2) + 8 * x;
-          if (r < most) *reinterpret_cast<uint4*>(to) = ld_shared_v4(Tile<VT>::at(tv, 32 * quarter + r, 4 * half + ch));
+          if (r < most) *reinterpret_cast<uint4*>(to) = ld_shared_v4(tile_at(tv, 32 * quarter + r, 4 * half + ch));
           to += 8 * ystride;
         }
       } else {
         for (int x = lane; x < 32 * 32; x += 32) {
           const int r = x >> 5, col = x & 31;
           if (r < left && col0 + col < vw) {
-            const uint32_t u = ld_shared_u32(Tile<VT>::at(tv, 32 * quarter + r, 4 * half + (col >> 3)) + (col & 6) * 2);
+            const uint32_t u = ld_shared_u32(tile_at(tv, 32 * quarter + r, 4 * half + (col >> 3)) + (col & 6) * 2);
             yg[r * ystride + col] = (uint16_t)(col & 1 ? u >> 16 : u);
           }
         }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t hi[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) hi[e] = pack_bf16x2(H[4 * c + e].x, H[4 * c + e].y);
-        st_shared_v4(Tile<VT>::at(base + S::kH, hrow, hcol / 8 + c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        st_shared_v4(tile_at(base + S::kH, hrow, hcol / 8 + c), make_uint4(hi[0], hi[1], hi[2], hi[3]));
       }
     };
     put_state();

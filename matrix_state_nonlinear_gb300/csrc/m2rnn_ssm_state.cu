@@ -36,7 +36,8 @@ template <int KP, bool REVERSE, bool KEEP>
 struct Smem {
   static constexpr int kStages = KEEP && KP > 64 ? 2 : 3;
   // Weighted y of two chunks, so that weighing and the product overlap: 142 -> 112 us for pieces of
-  // 65536 tokens of 16 heads, K = 64, V = 128.  (Backwards with K = 128 there is no room beside H; the traffic of the states bounds that one.)
+  // 65536 tokens of 16 heads, K = 64, V = 128.  (Backwards with K = 128 there is no room beside H; the
+  // traffic of the states bounds that one.)
   static constexpr int kW2 = KEEP && REVERSE && KP > 64 ? 1 : 2;
   static constexpr int kX = L * KP * 2, kY = L * VT * 2;
   static constexpr int kStage = kX + kY;
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t to = base + S::kW + i % WB * 2 * S::kY;
 #pragma unroll 2
       for (int c = 0; c < 4; ++c) {
-        const uint32_t at = Tile<VT>::at(0, row, 4 * half + c);
+        const uint32_t at = tile_at(0, row, 4 * half + c);
         float2 f[4];
         uint32_t hi[4], lo[4];
         unpack8(ld_shared_v4(stage(i) + S::kX + at), f);
@@ -154,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (KP > 64 || lane < 16) {
 #pragma unroll
           for (int c = 0; c < HC / 8; ++c) {
-            const uint32_t o = Tile<VT>::at(0, hrow, hcol / 8 + c);
+            const uint32_t o = tile_at(0, hrow, hcol / 8 + c);
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) split_bf16x2(H[4 * c + e], hi[e], lo[e]);
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int id = lane; id < 2 * KP * VT; id += 32) {
           const int x = id / (KP * VT), r = id / VT % KP, c = id % VT;
           if (r < p.K && c < vw) {
-            const uint32_t u = ld_shared_u32(Tile<VT>::at(base + S::kKept + x * KP * VT * 2, r, c >> 3) + (c & 6) * 2);
+            const uint32_t u = ld_shared_u32(tile_at(base + S::kKept + x * KP * VT * 2, r, c >> 3) + (c & 6) * 2);
             to[x * plane + (size_t)r * p.V + c] = (uint16_t)(c & 1 ? u >> 16 : u);
           }
         }

@@ -1,14 +1,52 @@
 // m2rnn_ssm_tc.cuh — shared by the scan's kernels on the 5th-generation tensor cores.
 //
-// Operand tiles are bf16 in rows of 64 values (128 bytes), 128-byte swizzled (Tile<64>), a wider
+// Operand tiles are bf16 in rows of 64 values (128 bytes), 128-byte swizzled (tile_at), a wider
 // operand as panels of 64 columns.  An operand whose rows are the product's M (or N) is read
 // K-major; one whose rows are the product's summed index is read MN-major.
 #pragma once
 
 #include "m2rnn_internal.h"
-#include "m2rnn_ssm_mma.cuh"
+#include "m2rnn_ssm.h"
+#include "ptx_util.cuh"
 
 namespace m2rnn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Shared address of 16-byte chunk `chunk` of row `row` of a tile of rows of 64 bf16 values: chunks are
+// permuted within a row as the 128-byte swizzle has them.
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int row, int chunk) {
+  return tile + row * 128 + ((chunk ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t a, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+// 2^x, at most 2 ulp off.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x, y) as bf16 pairs hi + lo: hi is the rounding to bf16, lo that of the remainder, so that
+// hi + lo is within 2^-17 of each value (2^-18 of its binade) and two bf16 products give nearly
+// a float32 one.
+__device__ __forceinline__ void split_bf16x2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x.x, x.y);
+  const float2 r = sub2(x, bf16x2_to_float2(hi));
+  lo = pack_bf16x2(r.x, r.y);
+}
 
 // Byte offset of panel `i` of a tile of `rows` rows.
 __device__ __forceinline__ constexpr int panel(int i, int rows) { return i * rows * 128; }
@@ -140,7 +178,7 @@ static __device__ __noinline__ void copy_tokens(uint32_t tile, const uint16_t* s
                                             int lane) {
   for (int id = lane; id < kSsmChunk * 64; id += 32) {
     const int r = id >> 6, c = id & 63;
-    st_shared_u16(Tile<64>::at(tile, r, c >> 3) + (c & 7) * 2,
+    st_shared_u16(tile_at(tile, r, c >> 3) + (c & 7) * 2,
                   r < rows && c < width ? src[r * stride + c] : (uint16_t)0);
   }
 }
@@ -163,7 +201,7 @@ template <int KP>
 __device__ __forceinline__ void copy_state(uint32_t tile, const uint16_t* src, int K, int V, int width, int lane) {
   for (int id = lane; id < 2 * KP * 64; id += 32) {
     const int x = id / (KP * 64), r = id / 64 % KP, c = id % 64;
-    st_shared_u16(Tile<64>::at(tile + x * KP * 128, r, c >> 3) + (c & 7) * 2,
+    st_shared_u16(tile_at(tile + x * KP * 128, r, c >> 3) + (c & 7) * 2,
                   r < K && c < width ? src[((size_t)x * K + r) * V + c] : (uint16_t)0);
   }
   fence_proxy_async_smem();
@@ -173,7 +211,7 @@ __device__ __forceinline__ void copy_out(uint16_t* dst, uint32_t tile, long long
   for (int id = lane; id < kSsmChunk * 64; id += 32) {
     const int r = id >> 6, c = id & 63;
     if (r < rows && c < width) {
-      const uint32_t u = ld_shared_u32(Tile<64>::at(tile, r, c >> 3) + (c & 6) * 2);
+      const uint32_t u = ld_shared_u32(tile_at(tile, r, c >> 3) + (c & 6) * 2);
       dst[r * stride + c] = (uint16_t)(c & 1 ? u >> 16 : u);
     }
   }

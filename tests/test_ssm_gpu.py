@@ -8,7 +8,7 @@ Tolerances, derived from the arithmetic:
    roundings per term at most, and one on the result: 2^-8 (|want| + A), A the sum of the terms'
    magnitudes (the oracle on absolute inputs).
  * float32 results (states, dH0, parameter gradients): states are carried in float32 and enter
-   products as two bf16 values (2^-17 of each term), gates are float32 sums over at most 64
+   products as two bf16 values (2^-17 of each term), gates are float32 sums over at most 128
    tokens: 2^-14 A.  da: the same before its own rounding, with sums over a chunk's tokens:
    2^-8 |want| + 2^-10 max A.
 """
@@ -340,3 +340,83 @@ def test_norm_unaligned_and_empty():
     assert pkg.gate_groupnorm(y[:0], None, w, None, 2).shape == (0, 64)
     g = pkg.gate_groupnorm_backward(y[:0], None, w, None, y[:0], 2)
     assert float(g["dw"].abs().max()) == 0.0
+
+
+# ---------------------------------------------------------------- chunk edges, shared heads, many rows
+# Lengths around the scan's chunks of 128 tokens, many heads on one q and k (whose gradients are summed
+# over parts), more pairs than SMs, widths on either side of a tile of 64.
+EDGES = [(1, 127, 2, 1, 64, 64), (2, 128, 2, 2, 128, 64), (1, 255, 3, 1, 64, 128), (1, 256, 2, 1, 128, 128),
+         (1, 257, 2, 1, 40, 72), (1, 385, 6, 2, 65, 65), (1, 700, 40, 1, 64, 64), (2, 513, 5, 1, 128, 64),
+         (4, 130, 48, 3, 64, 64), (1, 1, 160, 160, 128, 128)]
+
+
+@pytest.mark.parametrize("shape", EDGES)
+@pytest.mark.parametrize("ends", [False, True])
+def test_scan_chunk_edges(shape, ends):
+    test_scan_forward(shape, ends, not ends)
+    test_scan_backward(shape, ends, not ends)
+    assert pkg.stream_status() == 0
+
+
+def test_scan_long_decays_between_chunks():
+    """Decays of one token from none to complete (f from 1 to 0), over chunks and pieces."""
+    s = scan_case(1, 1500, 2, 1, 64, 64, seed=101)
+    s["a"] = (rand((1, 1500, 2), 102, 12.0, torch.float32)).to(BF16)
+    check_forward(s, *pkg.ssm_forward(s))
+
+
+def test_norm_many_rows():
+    """Enough short groups for two rows a team, an odd number of them."""
+    test_norm(4867, 1024, 16, False, True, True)
+
+
+def test_conv_long_stretches():
+    """Stretches of several tens of tokens a thread, the last cut inside a group of loads."""
+    test_conv_window((3, 4099, 256), True, True, 8)
+    test_conv_backward((3, 4099, 256), True, 8)
+
+
+def block_f64(block, x):
+    """The example's block from its formulas, in double precision on the CPU, with autograd."""
+    p = {n: t.detach().double().cpu().requires_grad_() for n, t in block.p.items()}
+    x = x.double().cpu().requires_grad_()
+    N, G, K, V, C = block.N, block.G, block.K, block.V, block.C
+    B, T, _ = x.shape
+    z = x @ p["w_in"].T
+    gate, u, a = z[..., :N * V], z[..., N * V:N * V + C], z[..., N * V + C:N * V + C + N]
+    X = torch.cat([u.new_zeros(B, 3, C), u], 1)
+    c = torch.nn.functional.silu(p["conv_b"] + sum(X[:, j:j + T] * p["conv_w"][:, j] for j in range(4)))
+    v = c[..., :N * V].unflatten(-1, (N, V))
+    k, q = (t.unflatten(-1, (G, K)).repeat_interleave(N // G, 2) for t in c[..., N * V:].chunk(2, -1))
+    d = torch.nn.functional.softplus(a + p["beta"])
+    f = torch.exp(-p["alpha"] * d)
+    H, ys = x.new_zeros(B, N, K, V), []
+    for t in range(T):
+        H = f[:, t, :, None, None] * H + (d[:, t, :, None] * k[:, t])[..., None] * v[:, t, :, None]
+        ys.append((H * q[:, t, ..., None]).sum(-2) + p["w_r"] * v[:, t])
+    n = torch.nn.functional.layer_norm(torch.stack(ys, 1), (V,), eps=1e-5).flatten(2)
+    return ((n * p["norm_w"] + p["norm_b"]) * torch.nn.functional.silu(gate)) @ p["w_out"].T, p, x
+
+
+def test_block_gradients():
+    """The three operators together, forward and backward, against double precision.  At most eight
+    intermediates between a parameter and its gradient are bf16 (2^-9 of each value), and no stage
+    here more than doubles a relative error: 8 x 2 x 2^-9 = 2^-5 of the gradient's norm."""
+    from examples.ssm_block import Block
+    block, x, dout = Block(seed=3), rand((2, 200, 256), 130), rand((2, 200, 256), 131)
+    out, g = block.train(x, dout)
+    want, p, x64 = block_f64(block, x)
+    (want * dout.double().cpu()).sum().backward()
+    grads = dict({n: t.grad for n, t in p.items()}, x=x64.grad)
+    assert float((out.double().cpu() - want).norm()) <= 2.0 ** -5 * float(want.norm())
+    for n, ref in grads.items():
+        assert float((g[n].double().cpu() - ref).norm()) <= 2.0 ** -5 * float(ref.norm()), n
+
+
+def test_block_example():
+    """Prompts in parts and tokens agree with one call: outputs are bf16 of sums of 384 products of
+    values that each call rounds alike but for the chunks' cuts, 2^-7 at most, within 2^-5 of the
+    largest; and steps of a thousandth of each parameter along its gradient lower the loss."""
+    from examples.ssm_block import check
+    split, losses = check()
+    assert split < 2.0 ** -5 and all(b < a for a, b in zip(losses, losses[1:])), (split, losses)
