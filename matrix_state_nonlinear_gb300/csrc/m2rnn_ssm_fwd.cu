@@ -156,8 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (count > 0) put_weighted(0);
     for (int i = 0; i < count && ok; ++i) {
-      wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.s[i & 1], i >> 1)) break;
+      if (!wait(bar.s[i & 1], i >> 1)) break;  // (the gates were waited for with v)
       tc_fence_after();
       const ChunkGates& G = gates[i & 3];
       const float cum = G.cum[row];
@@ -213,8 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - kWarpY) >> 2;
     const long long ystride = (long long)p.N * p.V;
     for (int i = 0; i < count; ++i) {
-      wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.y, i)) break;
+      if (!wait(bar.y, i)) break;  // (P's warps had the gates)
       tc_fence_after();
       const float e = exp2_approx(gates[i & 3].cum[row]);
       const float2 e2 = make_float2(e, e);
@@ -307,8 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_proxy_async_smem();
     warp_arrive(&bar.h, lane);
     for (int i = 0; i < count; ++i) {
-      wait(bar.gate[i & 3], i >> 2);
-      if (!wait(bar.u, i)) break;
+      if (!wait(bar.u, i)) break;  // (weighing v took the gates)
       tc_fence_after();
       const float e = exp2_approx(gates[i & 3].total);
       const float2 e2 = make_float2(e, e);

@@ -408,7 +408,7 @@ def test_block_gradients():
     want, p, x64 = block_f64(block, x)
     (want * dout.double().cpu()).sum().backward()
     grads = dict({n: t.grad for n, t in p.items()}, x=x64.grad)
-    assert float((out.double().cpu() - want).norm()) <= 2.0 ** -5 * float(want.norm())
+    assert float((out.double().cpu() - want.detach()).norm()) <= 2.0 ** -5 * float(want.detach().norm())
     for n, ref in grads.items():
         assert float((g[n].double().cpu() - ref).norm()) <= 2.0 ** -5 * float(ref.norm()), n
 
