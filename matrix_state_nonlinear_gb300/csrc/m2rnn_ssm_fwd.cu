@@ -23,13 +23,14 @@
 //    fit, and held until y was out they left the loads in the open (222 -> 165 us for 4 sequences of
 //    8192 tokens and 32 heads).  y leaves through v's place.
 //  * The warps run five different programs, together near the instruction cache's size, so each is
-//    kept short: waits that do not succeed at once share one function, loads have one site each.
+//    kept short: waits that do not succeed at once share one function, loads have one site each, and
+//    P's loop of four is unrolled by two (240 us for 8 x 16384; by one 247, by four 287).
 // Where the pairs are fewer than the SMs, segments of a sequence run side by side
 // (m2rnn_ssm_state.cu).
-// Measured: 265 us for 8 x 16384 tokens of 16 heads, K = V = 64 (4.1 TB/s, 60 % of a copy), 263 us for
-// 65536 tokens of 16 heads, V = 128, after their segments' states, 162 us for 4 x 8192 tokens of 32
+// Measured: 240 us for 8 x 16384 tokens of 16 heads, K = V = 64 (4.5 TB/s, 66 % of a copy), 239 us for
+// 65536 tokens of 16 heads, V = 128, after their segments' states, 150 us for 4 x 8192 tokens of 32
 // heads, K = 128.  Bound by instruction issue (58 % of the slots; a chunk is 9700 warp instructions,
-// about 4100 cycles with K = 64): S has to be decayed and v weighted element by element.  Weighing v in
+// about 3700 cycles with K = 64): S has to be decayed and v weighted element by element.  Weighing v in
 // the state's warps took 287 us or more instead of 265, in four of the eight warps 290 instead of 282.
 #include <mutex>
 
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(bar.vfull[i % SV], i / SV)) return;
       const float w = gates[i & 3].wk[row];
       const float2 w2 = make_float2(w, w);
-#pragma unroll 1
+#pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t at = tile_at(0, row, 4 * half + c);
         float2 f[4];
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float cum = G.cum[row];
       const uint32_t ts = t_lane + kColS + (i & 1) * 128;
       // Block cb of 32 columns against the quarter's own block of 32 rows, 16 columns at a time.
-#pragma unroll 1
+#pragma unroll 2
       for (int x = 0; x < 4; ++x) {
         const int cb = 2 * half + (x >> 1), col = 32 * cb + 16 * (x & 1);
         uint32_t out[8];
