@@ -31,7 +31,8 @@
 // 65536 tokens of 16 heads, V = 128, after their segments' states, 150 us for 4 x 8192 tokens of 32
 // heads, K = 128.  Bound by instruction issue (58 % of the slots; a chunk is 9700 warp instructions,
 // about 3700 cycles with K = 64): S has to be decayed and v weighted element by element.  Weighing v in
-// the state's warps took 287 us or more instead of 265, in four of the eight warps 290 instead of 282.
+// the state's warps took 287 us or more instead of 264, in four of the eight warps 290 instead of 282
+// (8 x 16384, before the loops were unrolled).
 #include <mutex>
 
 #include "m2rnn_ssm_tc.cuh"
