@@ -10,7 +10,8 @@
 // accesses, arithmetic in pairs) over a stretch of tokens; eight (four) tokens are loaded at once
 // and joined to the last three in registers, so that enough bytes are in flight and the window
 // moves once per group of tokens.  The three tokens that stretches share are re-read, from L2.
-// Measured, 8 x 8192 tokens of 2304 channels: forward 98 us (6.2 TB/s, 91 % of a copy), backward 169 us
+// Measured, 8 x 8192 tokens of 2304 channels: forward 95 us (6.3 TB/s, 93 % of a copy; stretches of 64
+// tokens, of 128 98 us), backward (of 128; of 64 175 us and 12 us for the sums) 169 us
 // (5.4 TB/s; with loads to registers, three blocks an SM, 202 us) and 8 us for the sums.
 #include "m2rnn_ssm.h"
 #include "ptx_util.cuh"
@@ -323,10 +324,9 @@ __global__ void __launch_bounds__(32 * kSumSlices)
   });
 }
 
-// Tokens per thread: long stretches re-read little (three tokens each) and sum more in
+// Tokens per thread, `span` at most: long stretches re-read little (three tokens each) and sum more in
 // registers, short ones give a short prompt enough threads.
-int conv_span(int B, int T, int C, int vec) {
-  int span = 128;
+int conv_span(int B, int T, int C, int vec, int span) {
   while (span > 8 && (long long)B * ((T + span - 1) / span) * (C / vec) < 152LL * 1024) span /= 2;
   return span;
 }
@@ -338,12 +338,12 @@ bool rows_aligned(const ConvProblem& p, int vec) {
 }
 
 // Stretches of the backward; a fixed rule of the sizes, so that the workspace can be sized.
-int backward_span(int B, int T, int C) { return conv_span(B, T, C, 4); }
+int backward_span(int B, int T, int C) { return conv_span(B, T, C, 4, 128); }
 
 template <int VEC>
 cudaError_t run_forward(const ConvProblem& p, uint16_t* out, uint16_t* window_out,
                         cudaStream_t stream) {
-  const int span = conv_span(p.B, p.T, p.C, VEC);
+  const int span = conv_span(p.B, p.T, p.C, VEC, 64);
   const int groups = p.C / VEC, stretches = p.T > 0 ? (p.T + span - 1) / span : 1;
   const long long threads = (long long)groups * stretches * p.B;
   conv_window_kernel<VEC><<<(unsigned)((threads + kThreads - 1) / kThreads), kThreads, 0, stream>>>(

@@ -10,13 +10,13 @@
 // team of lanes takes one group of one row: each lane holds its share in registers, so y is read
 // once, and mean and variance are two exact passes over registers (the variance of the centred
 // values; no sum of squares is subtracted).  A team is 8, 16 or 32 lanes of a warp, or the whole
-// block for groups of more than 32 lanes' registers.  Short groups' forward loads two rows per team
+// block for groups of more than 32 lanes' registers.  Short groups' forward loads three rows per team
 // before it computes the first; the backward keeps a team on the same channels for many rows,
 // the next row loaded while one is computed, so that dw and db add up in registers and one row
 // of partial sums per team goes to memory.  All arithmetic is on pairs: at one value an
 // instruction both directions were bound by instruction issue (206 and 354 us).
-// Measured, 131072 rows of 16 groups of 64, bf16 with a gate: forward 139 us (5.8 TB/s, 85 % of a copy),
-// backward 228 us (5.9 TB/s) and 7 us for the sums.
+// Measured, 131072 rows of 16 groups of 64, bf16 with a gate: forward 136 us (5.9 TB/s, 87 % of a copy),
+// backward 228 us (5.9 TB/s) and 6 us for the sums.
 #include "m2rnn_ssm.h"
 #include "ptx_util.cuh"
 
@@ -370,10 +370,11 @@ bool vec_ok(const NormProblem& p) {
          aligned_to(p.w, 16) && aligned_to(p.bias, 16);
 }
 
-// Rows in flight of the backward: enough teams for every SM, few enough partial sums.
+// Rows in flight of the backward: two blocks of teams for every SM, as many as its registers let
+// reside (234 us for 131072 rows of 16 x 64 with the sums; four 239, eight 246).
 int backward_slots(long long rows, int D, int groups) {
   const Shape s = shape_of(D / groups, (D / groups) % 8 == 0);
-  long long teams = 152LL * 4 * (kThreads / s.width());
+  long long teams = 152LL * 2 * (kThreads / s.width());
   long long slots = teams / groups;
   if (slots < 1) slots = 1;
   return (int)(slots < rows ? slots : rows > 0 ? rows : 1);
@@ -409,9 +410,10 @@ cudaError_t forward_typed(const NormProblem& p, uint16_t* out, const Shape& s, c
   const long long units = p.rows * p.groups, per_block = kThreads / s.width();
   return with_shape(s, [&](auto vec, auto team, auto r) {
     constexpr int V = decltype(vec)::value, G = decltype(team)::value, R = decltype(r)::value;
-    // Several units per team where there are enough of them to fill the GPU all the same.
-    constexpr int U = R * V == 8 ? 2 : 1;
-    const bool many = U > 1 && units >= 152LL * 8 * per_block * U;
+    // Three units per team where that still fills the GPU (131072 rows of 16 x 64: 136 us; by two 140, by
+    // one 164).
+    constexpr int U = R * V == 8 ? 3 : 1;
+    const bool many = U > 1 && units >= 152LL * 4 * per_block * U;
     const long long apart = many ? ((p.rows + U - 1) / U) * p.groups : units;
     const unsigned blocks = (unsigned)((apart + per_block - 1) / per_block);
     if (many)
