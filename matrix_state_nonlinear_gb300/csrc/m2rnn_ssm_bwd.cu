@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const size_t plane = (size_t)p.K * p.V;
   if (tid == 0) {
     mbar_init(&bar.qk, 1), mbar_init(&bar.vd, 1), mbar_init(&bar.h, 1), mbar_init(&bar.g, 1);
-    mbar_init(&bar.step_free, 16), mbar_init(&bar.vd_read, 16), mbar_init(&bar.scaled1, 16), mbar_init(&bar.scaled2, 16);
+    mbar_init(&bar.step_free, 16), mbar_init(&bar.vd_read, 16);
+    mbar_init(&bar.scaled1, 16), mbar_init(&bar.scaled2, 16);
     mbar_init(&bar.s, 1), mbar_init(&bar.pds, 16), mbar_init(&bar.hd, 1), mbar_init(&bar.q_read, 16);
     mbar_init(&bar.gd, 1), mbar_init(&bar.done, 1), mbar_init(&bar.acc_free, 16);
     for (int i = 0; i < 2; ++i) mbar_init(&bar.gate[i], 1), mbar_init(&bar.gate_free[i], 17);
@@ -414,8 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack8(dr[c], y);
         tmem_ready(hi, lo, a);
         const float2 w2 = make_float2(wk, wk);
-        const float4 w0 = reinterpret_cast<const float4*>(wr[warp])[2 * c], w1 = reinterpret_cast<const float4*>(wr[warp])[2 * c + 1];
-        const float2 u[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y), make_float2(w1.z, w1.w)};
+        const float4 w0 = reinterpret_cast<const float4*>(wr[warp])[2 * c];
+        const float4 w1 = reinterpret_cast<const float4*>(wr[warp])[2 * c + 1];
+        const float2 u[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
+                             make_float2(w1.z, w1.w)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 kg = mul2(w2, add2(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])));
@@ -534,10 +537,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           for (int x = 0; x < PANELS; ++x) {
-            copy_tokens(base + S::kQ + panel(x, L), p.q + at.b * p.sq.batch + t0 * p.sq.token + (long long)at.group * p.K + 64 * x,
-                        p.sq.token, rows, p.K - 64 * x, lane);
-            copy_tokens(base + S::kK + panel(x, L), p.k + at.b * p.sk.batch + t0 * p.sk.token + (long long)at.group * p.K + 64 * x,
-                        p.sk.token, rows, p.K - 64 * x, lane);
+            copy_tokens(base + S::kQ + panel(x, L),
+                        p.q + at.b * p.sq.batch + t0 * p.sq.token + (long long)at.group * p.K + 64 * x, p.sq.token, rows, p.K - 64 * x, lane);
+            copy_tokens(base + S::kK + panel(x, L),
+                        p.k + at.b * p.sk.batch + t0 * p.sk.token + (long long)at.group * p.K + 64 * x, p.sk.token, rows, p.K - 64 * x, lane);
           }
           fence_proxy_async_smem();
           warp_arrive(&bar.qk, lane);

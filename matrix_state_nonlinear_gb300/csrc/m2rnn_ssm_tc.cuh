@@ -55,7 +55,8 @@ __device__ __forceinline__ constexpr int panel(int i, int rows) { return i * row
 // `pred` holds; a and b describe the first step, A_STEP and B_STEP are their advance per step and
 // A_PANEL, B_PANEL the further advance after every fourth (16-byte units).
 template <int STEPS, int A_STEP, int B_STEP, int A_PANEL = 0, int B_PANEL = 0>
-__device__ __forceinline__ void umma_steps(bool pred, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void umma_steps(bool pred, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           bool accumulate) {
 #pragma unroll 1
   for (int i = 0; i < STEPS / 4; ++i)
     umma4_if<A_STEP, B_STEP>(pred, d, a + i * (4 * A_STEP + A_PANEL), b + i * (4 * B_STEP + B_PANEL), idesc,
@@ -174,8 +175,8 @@ inline bool token_map(EncodeTiledFn enc, CUtensorMap* map, const uint16_t* base,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // The same box by one warp, value by value, for operands that a tensor map cannot describe.
-static __device__ __noinline__ void copy_tokens(uint32_t tile, const uint16_t* src, long long stride, int rows, int width,
-                                            int lane) {
+static __device__ __noinline__ void copy_tokens(uint32_t tile, const uint16_t* src, long long stride, int rows,
+                                                int width, int lane) {
   for (int id = lane; id < kSsmChunk * 64; id += 32) {
     const int r = id >> 6, c = id & 63;
     st_shared_u16(tile_at(tile, r, c >> 3) + (c & 7) * 2,

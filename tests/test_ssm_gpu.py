@@ -420,3 +420,29 @@ def test_block_example():
     from examples.ssm_block import check
     split, losses = check()
     assert split < 2.0 ** -5 and all(b < a for a, b in zip(losses, losses[1:])), (split, losses)
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 values: their ends against calls on the ends alone.  Conv and norm do
+    not look back that far, so they give the same bits; the scan's cut is on a chunk, and only the pieces
+    of the sequence, and with them float32 roundings of the state, differ: a bf16 rounding apart."""
+    T, C = 1_100_000, 2048
+    tail = T - (T - 12_000) // 128 * 128  # the cut is at a chunk's edge
+    x = torch.randn(1, T, C, device=DEV, dtype=BF16)
+    w, b = rand((C, 4), 1, 0.6, torch.float32), rand((C,), 2, 0.3, torch.float32)
+    last = x[:, -tail:].contiguous()
+    out, window = pkg.conv_silu_window(x, w, b)
+    end, _ = pkg.conv_silu_window(last, w, b, x[:, -tail - 3:-tail].contiguous())
+    assert torch.equal(out[:, -tail:], end) and torch.equal(window, x[:, -3:])
+    y = pkg.gate_groupnorm(x[0], out[0], b.abs() + 0.5, None, 32)
+    assert torch.equal(y[-tail:], pkg.gate_groupnorm(last[0], end[0], b.abs() + 0.5, None, 32))
+    del out, y
+    s = scan_case(1, T, 32, 1, 64, 1, seed=140, h0=False)
+    s.update(v=x.view(1, T, 32, 64), w_r=rand((32, 64), 141, 1.0, torch.float32))
+    cut = lambda lo, hi: {n: t[:, lo:hi] if n in ("q", "k", "v", "a") else t for n, t in s.items()}  # noqa: E731
+    y, H = pkg.ssm_forward(s)
+    before = pkg.ssm_forward(cut(0, T - tail))[1]
+    end, H_end = pkg.ssm_forward(dict(cut(T - tail, T), H0=before))
+    assert float((y[:, -tail:].float() - end.float()).abs().max()) <= 2.0 ** -7 * float(end.float().abs().max())
+    assert float((H - H_end).abs().max()) <= 2.0 ** -14 * float(H.abs().max())
+    assert pkg.stream_status() == 0
