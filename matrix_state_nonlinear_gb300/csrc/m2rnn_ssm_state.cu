@@ -12,8 +12,8 @@
 //    Kept as two bf16 values each, through shared memory so that whole rows leave at once.
 // Products on the 5th-generation tensor cores: one of 128 x 16 steps per chunk, the weighted y in
 // two bf16 values (17 bits) side by side as its second operand; warps by role as in the forward kernel.
-// Measured: 112 us for pieces of 65536 tokens of 16 heads, K = 64, V = 128 (weighing y in its eight warps
-// bounds it; sixteen, at 72 registers, took 111 us and the kept states longer); kept states of 4 x 8192
+// Measured: 87 us for the pieces of 65536 tokens of 16 heads, K = 64, V = 128 (weighing y in its eight warps
+// bounds it; sixteen, at 72 registers, took as long and the kept states longer); kept states of 4 x 8192
 // tokens of 32 heads, K = 128, V = 64: H 85 us (0.4 GB, 4.7 TB/s), G with <G, H> 136 us (0.67 GB,
 // 4.9 TB/s), near the memory's rate.
 #include <mutex>
@@ -38,7 +38,7 @@ struct alignas(16) Weights {
 template <int KP, bool REVERSE, bool KEEP>
 struct Smem {
   static constexpr int kStages = KEEP && KP > 64 ? 2 : 3;
-  // Weighted y of two chunks, so that weighing and the product overlap: 142 -> 112 us for pieces of
+  // Weighted y of two chunks, so that weighing and the product overlap: 142 -> 112 us for three pieces of
   // 65536 tokens of 16 heads, K = 64, V = 128.  (Backwards with K = 128 there is no room beside H; the
   // traffic of the states bounds that one.)
   static constexpr int kW2 = KEEP && REVERSE && KP > 64 ? 1 : 2;
@@ -379,32 +379,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
 }
 
-// state[piece] from the piece's own sum to the state before it (after it, with `reverse`), in
-// place: the chain starts at `from` and takes in a piece's decay and sum after it is written.
+// starts[segment]: the state before each segment of `sub` pieces (after it, with `reverse`), from the pieces'
+// own sums and decays, chained from `from` on.
 __global__ void __launch_bounds__(256)
-    ssm_join_kernel(const float* __restrict__ from, float* __restrict__ state, const float* __restrict__ decays,
-                    int pieces, int kv, int reverse) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
+    ssm_join_kernel(const float* __restrict__ from, const float* __restrict__ state, const float* __restrict__ decays,
+                    float* __restrict__ starts, int segments, int sub, int kv, int reverse) {
+  const int i = blockIdx.x * 256 + threadIdx.x, pieces = segments * sub, used = pieces - sub + 1;
   const long long pair = blockIdx.y;
   if (i >= kv) return;
   float h = from ? from[(size_t)pair * kv + i] : 0.f;
-  float* s = state + (size_t)pair * pieces * kv + i;
+  const float* s = state + (size_t)pair * pieces * kv + i;
   const float* d = decays + pair * pieces;
+  float* to = starts + (size_t)pair * segments * kv + i;
   constexpr int kAhead = 8;  // pieces loaded at once
-  for (int j = 0; j < pieces; j += kAhead) {
+  for (int j = 0; j < used; j += kAhead) {
     float own[kAhead], decay[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (j + u + 1 < pieces) {
+      if (j + u + 1 < used) {
         const int at = reverse ? pieces - 1 - j - u : j + u;
         own[u] = s[(size_t)at * kv];
         decay[u] = d[at];
       }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int at = reverse ? pieces - 1 - j - u : j + u;
-      if (j + u < pieces) s[(size_t)at * kv] = h;
-      if (j + u + 1 < pieces) h = fmaf(exp2_approx(decay[u]), h, own[u]);
+      if (j + u < used && (j + u) % sub == 0) {
+        const int segment = (j + u) / sub;
+        to[(size_t)(reverse ? segments - 1 - segment : segment) * kv] = h;
+      }
+      if (j + u + 1 < used) h = fmaf(exp2_approx(decay[u]), h, own[u]);
     }
   }
 }
@@ -439,22 +442,42 @@ cudaError_t run_any(const StateProblem& p, int blocks_y, bool vec, cudaStream_t 
 
 }  // namespace
 
-// Whole segments for every SM at most, of at least two chunks.
+constexpr int kSms = 152;
+static long long cut_units(int B, int N, int V) { return (long long)B * N * ((V + VT - 1) / VT); }
+
+// Pieces of a segment for the launch that finds the segments' states: as many as make the fewest rounds
+// of chunks (and three for a piece's start and end) over the SMs.  65536 tokens and 32 pairs and tiles:
+// three segments' states in nine pieces, 288 blocks of 43 chunks (87 us), not 96 of 128 (112 us).
+static int pieces_of(int segments, int per, long long units, bool whole) {
+  long long best = 0;
+  int sub = 1;
+  for (int s = 1; s <= 8 && s <= per; ++s) {
+    if (whole && per % s != 0) continue;
+    const long long rounds = (units * (segments - 1) * s + kSms - 1) / kSms, cost = rounds * ((per + s - 1) / s + 3);
+    if (best == 0 || cost < best) best = cost, sub = s;
+  }
+  return sub;
+}
+
+// Whole segments for every SM at most, of at least two chunks and a multiple of their pieces.
 SsmCut ssm_cut(int B, int T, int N, int V) {
-  constexpr int kSms = 152;
-  const long long units = (long long)B * N * ((V + VT - 1) / VT);
+  const long long units = cut_units(B, N, V);
   const int chunks = ssm_chunks(T);
   SsmCut c{1, chunks > 0 ? chunks : 1};
   long long want = kSms / units;
   if (want > chunks / 2) want = chunks / 2;
   if (want < 2) return c;
   c.per = (int)((chunks + want - 1) / want);
+  const int sub = pieces_of((int)want, c.per, units, false);
+  c.per = (c.per + sub - 1) / sub * sub;
   c.segments = (chunks + c.per - 1) / c.per;
   return c;
 }
 
 size_t ssm_segment_floats(const SsmCut& c, int B, int N, int K, int V) {
-  return c.segments > 1 ? (size_t)B * N * c.segments * ((size_t)K * V + 1) : 0;
+  if (c.segments <= 1) return 0;
+  const size_t state = (size_t)K * V;
+  return (size_t)B * N * c.segments * (state + pieces_of(c.segments, c.per, cut_units(B, N, V), true) * (state + 1));
 }
 
 cudaError_t launch_ssm_segments(StateProblem p, const SsmCut& c, bool reverse, bool vec, float* ws,
@@ -465,16 +488,17 @@ cudaError_t launch_ssm_segments(StateProblem p, const SsmCut& c, bool reverse, b
   p.from = nullptr;
   p.from_state = nullptr;
   p.kept = nullptr;
-  p.pieces = c.segments;
-  p.per = c.per;
-  p.first_piece = reverse ? 1 : 0;  // the last piece of the order ends the sequence: not needed
-  p.to_state = ws;
-  p.decay = ws + (size_t)pairs * c.segments * kv;
-  const cudaError_t err = reverse ? run_any<true, false>(p, c.segments - 1, vec, stream)
-                                  : run_any<false, false>(p, c.segments - 1, vec, stream);
+  const int sub = pieces_of(c.segments, c.per, cut_units(p.B, p.N, p.V), true);
+  p.pieces = c.segments * sub;
+  p.per = c.per / sub;
+  p.first_piece = reverse ? sub : 0;  // the last segment of the order ends the sequence: not needed
+  p.to_state = ws + (size_t)pairs * c.segments * kv;
+  p.decay = p.to_state + (size_t)pairs * p.pieces * kv;
+  const cudaError_t err = reverse ? run_any<true, false>(p, (c.segments - 1) * sub, vec, stream)
+                                  : run_any<false, false>(p, (c.segments - 1) * sub, vec, stream);
   if (err != cudaSuccess) return err;
-  ssm_join_kernel<<<dim3((kv + 255) / 256, (unsigned)pairs), 256, 0, stream>>>(from, ws, p.decay, c.segments, kv,
-                                                                               reverse);
+  ssm_join_kernel<<<dim3((kv + 255) / 256, (unsigned)pairs), 256, 0, stream>>>(from, p.to_state, p.decay, ws,
+                                                                               c.segments, sub, kv, reverse);
   return cudaGetLastError();
 }
 

@@ -358,6 +358,15 @@ def test_scan_chunk_edges(shape, ends):
     assert pkg.stream_status() == 0
 
 
+@pytest.mark.parametrize("shape", [(1, 1100, 2, 1, 64, 64), (1, 4217, 4, 2, 64, 64), (1, 2600, 3, 1, 128, 128)])
+def test_scan_segments_of_several_pieces(shape):
+    """Few pairs: segments whose states are found in three or four pieces each, the last segment shorter
+    than its pieces."""
+    test_scan_forward(shape, True, False)
+    test_scan_backward(shape, True, False)
+    assert pkg.stream_status() == 0
+
+
 def test_scan_long_decays_between_chunks():
     """Decays of one token from none to complete (f from 1 to 0), over chunks and pieces."""
     s = scan_case(1, 1500, 2, 1, 64, 64, seed=101)
