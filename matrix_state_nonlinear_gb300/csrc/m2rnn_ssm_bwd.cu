@@ -30,8 +30,6 @@
 // bounds it: 378 us for 4 x 8192 tokens of 32 heads on one q and k, K = 128, V = 64 (13600 cycles a step,
 // the tensor cores busy 30 %), 34 us for 4 x 2048 of 8 heads, K = V = 64.  A small launch before
 // computes every chunk's gates, and outputs leave through shared memory, whole rows at a time.
-#include <mutex>
-
 #include "m2rnn_ssm_tc.cuh"
 
 namespace m2rnn {
@@ -862,12 +860,9 @@ Workspace carve(float* ws, const Plan& plan, int B, int T, int N, int Nqk, int K
 
 template <int KP>
 cudaError_t run(const SsmBackwardProblem& p, const Plan& plan, const Workspace& w, bool vec, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(ssm_backward_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<KP>::kBytes);
-  });
+  // At every launch: the attribute belongs to the current device.
+  const cudaError_t attr =
+      cudaFuncSetAttribute(ssm_backward_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<KP>::kBytes);
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
   CUtensorMap mq{}, mk{}, mv{}, md{}, mh{}, mg{}, mdq{}, mdk{}, mdv{};

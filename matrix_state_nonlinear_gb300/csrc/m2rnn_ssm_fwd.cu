@@ -33,8 +33,6 @@
 // about 3700 cycles with K = 64): S has to be decayed and v weighted element by element.  Weighing v in
 // the state's warps took 287 us or more instead of 264, in four of the eight warps 290 instead of 282
 // (8 x 16384, before the loops were unrolled).
-#include <mutex>
-
 #include "m2rnn_ssm_tc.cuh"
 
 namespace m2rnn {
@@ -473,12 +471,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int KP>
 cudaError_t run(const SsmProblem& p, const SsmCut& cut, bool vec, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(ssm_forward_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<KP>::kBytes);
-  });
+  // At every launch: the attribute belongs to the current device.
+  const cudaError_t attr =
+      cudaFuncSetAttribute(ssm_forward_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<KP>::kBytes);
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
   CUtensorMap mq{}, mk{}, mv{};

@@ -16,8 +16,6 @@
 // bounds it; sixteen, at 72 registers, took as long and the kept states longer); kept states of 4 x 8192
 // tokens of 32 heads, K = 128, V = 64: H 85 us (0.4 GB, 4.7 TB/s), G with <G, H> 136 us (0.67 GB,
 // 4.9 TB/s), near the memory's rate.
-#include <mutex>
-
 #include "m2rnn_ssm_tc.cuh"
 
 namespace m2rnn {
@@ -414,12 +412,10 @@ __global__ void __launch_bounds__(256)
 
 template <int KP, bool REVERSE, bool KEEP>
 cudaError_t run(const StateProblem& p, int blocks_y, bool vec, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(ssm_state_kernel<KP, REVERSE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Smem<KP, REVERSE, KEEP>::kBytes);
-  });
+  // At every launch: the attribute belongs to the current device.
+  const cudaError_t attr =
+      cudaFuncSetAttribute(ssm_state_kernel<KP, REVERSE, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Smem<KP, REVERSE, KEEP>::kBytes);
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
   CUtensorMap mx{}, my{}, mk{}, mh{};
