@@ -3,7 +3,8 @@ window, the selective scan and the gated group norm (see include/m2rnn.h for the
 
 As in the rest of the package, the functions check and marshal arguments, allocate outputs and
 workspaces as torch memory when they are not given, and run on the current CUDA stream unless
-the keyword ``stream`` names another.  A token's kernels take a few microseconds, so the checks
+the keyword ``stream`` names another.  The tensors have to be on the current device (the stream's
+device, where one is named).  A token's kernels take a few microseconds, so the checks
 are one pass over each tensor's attributes and the error messages are made only on failure.
 """
 from __future__ import annotations
@@ -30,10 +31,14 @@ def _on_stream(f):
 
 
 def _device(t):
-    """The CUDA device index of a tensor; refuses host tensors."""
+    """The CUDA device index of a tensor; refuses host tensors, and tensors of another device than
+    the current one, on which the kernels would launch."""
     if not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
-    return t.get_device()
+    dev, current = t.get_device(), torch._C._cuda_getDevice()
+    if dev != current:
+        raise ValueError(f"inputs are on cuda:{dev}, the current device is cuda:{current}")
+    return dev
 
 
 def _refuse(t, name, dtype, shape, dev):
