@@ -135,6 +135,18 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _device(t):
+    """The device of a tensor; refuses host tensors, and tensors of another device than the current
+    one, on which the kernels would launch."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    current = torch._C._cuda_getDevice()
+    if dev.index != current:
+        raise ValueError(f"inputs are on {dev}, the current device is cuda:{current}")
+    return dev
+
+
 def _check(t, name, dtype, shape, dev):
     if t is None:
         return
@@ -153,11 +165,9 @@ def _marshal(q, k, v, a, alpha, beta, W, w_r, H0, y, H_T, opdtype):
 
     q and k may have N heads or a single head shared by all heads of v.
     """
-    if q.device.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    dev = _device(q)
     B, T, Nqk, K = q.shape
     N, V = v.shape[2], v.shape[3]
-    dev = q.device
     if Nqk not in (1, N):
         raise ValueError(f"q, k must have 1 or {N} heads, got {Nqk}")
     for t, name, dt, shp in [(q, "q", opdtype, (B, T, Nqk, K)), (k, "k", opdtype, (B, T, Nqk, K)),
@@ -382,9 +392,7 @@ def m2rnn_decode_step(q, k, v, a, alpha, beta, W, w_r, H_in, H_out=None, y=None,
     lib = load_library()
     B, Nqk, K = q.shape
     N, V = v.shape[1], v.shape[2]
-    dev = q.device
-    if q.device.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    dev = _device(q)
     for t, name, dt, shp in [(q, "q", torch.bfloat16, (B, Nqk, K)),
                              (k, "k", torch.bfloat16, (B, Nqk, K)),
                              (v, "v", torch.bfloat16, (B, N, V)), (a, "a", torch.bfloat16, (B, N)),
@@ -418,10 +426,8 @@ def conv_silu(x, w, bias=None, out=None, stream=None):
     """SiLU(causal depthwise Conv1D, kernel 4) over time: x [B, T, C] bf16, w [C, 4] float32,
     bias [C] float32 or None.  Returns out [B, T, C] bf16."""
     lib = load_library()
-    if x.device.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    dev = _device(x)
     B, T, C = x.shape
-    dev = x.device
     _check(x, "x", torch.bfloat16, (B, T, C), dev)
     _check(w, "w", torch.float32, (C, 4), dev)
     _check(bias, "bias", torch.float32, (C,), dev)
@@ -439,11 +445,9 @@ def gate_rmsnorm(y, g_pre, w_norm, eps=1e-6, out=None, stream=None):
     """RMSNorm(y ⊙ SiLU(g_pre)) over the last axis: y [..., D] float32, g_pre [..., D] bf16,
     w_norm [D] float32.  Returns out [..., D] bf16."""
     lib = load_library()
-    if y.device.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
+    dev = _device(y)
     D = y.shape[-1]
     rows = y.numel() // D if D else 0
-    dev = y.device
     _check(y, "y", torch.float32, tuple(y.shape), dev)
     _check(g_pre, "g_pre", torch.bfloat16, tuple(y.shape), dev)
     _check(w_norm, "w_norm", torch.float32, (D,), dev)
