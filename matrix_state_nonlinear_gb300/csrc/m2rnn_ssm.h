@@ -134,8 +134,8 @@ inline bool rows_of_16(const void* p, const Strides& s, int width) {
 
 #ifdef __CUDACC__
 // The gate of one token: d = softplus(x), log f = -alpha d, x = a + beta.  log f is held at
-// -105 and above: exp(-105) is zero in float32 already, and a bounded sum over a chunk keeps
-// the differences between its later tokens accurate after a token that resets the state.
+// -105 and above: exp(-105) is zero in float32 already, and the sums over a chunk of 128 tokens
+// are bounded (ChunkGates).
 __device__ __forceinline__ float2 ssm_gate(float a, float alpha, float beta) {
   const float x = a + beta;
   const float d = fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));

@@ -134,6 +134,15 @@ struct Cursor {
   }
 };
 
+// log2 of the weights of a token's sixteen columns from `col` on, where its block's tokens differ in hi.  Few
+// blocks do: apart from the usual code, which does not fit the instruction cache as it is.
+static __device__ __noinline__ void wide_exponents(const ChunkGates& G, int row, int col, float2 (&x)[8]) {
+  const float hi = G.hi[row], lo = G.lo[row];
+  for (int z = 0; z < 8; ++z)
+    x[z] = make_float2((hi - G.hi[col + 2 * z]) + (lo - G.diag[col + 2 * z]),
+                       (hi - G.hi[col + 2 * z + 1]) + (lo - G.diag[col + 2 * z + 1]));
+}
+
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_backward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -192,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(bar.gate[j & 1], j >> 1);
       if (!wait(bar.vd, j)) break;
       const ChunkGates& G = gates[j & 1].g;
-      const float cum = G.cum[row], wk = G.wk[row];
-      const float et = exp2_approx(cum);
+      const float cum = G.hi[row] + G.lo[row], wk = G.wk[row];  // (hi counts between blocks alone)
+      const float et = exp2_approx(cum + G.span[quarter][0]);
       const float wl = lane < 16 && c0 + lane < vw ? p.w_r[(size_t)at.head * p.V + v0 + c0 + lane] : 0.f;
       // exp(c) dy as an operand (and below w v, in the same place).
       auto put_scaled = [&](const uint4 (&from)[2], float f, uint64_t& ready) {
@@ -241,12 +250,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float sc[16], dp[16];
           uint32_t po[8], so[8];
+          float2 m[8];
           tmem_ld16_nowait(t_lane + kColS + 16 * piece, sc);
           tmem_ld16_nowait(t_lane + kColDp + 16 * piece, dp);
-          float2 m[8];
           int own = -1;  // the token's own column of these
           if (block < quarter) {
-            const float u = exp2_approx(cum - G.cum[32 * block + 31]);
+            const float u = exp2_approx(cum + G.span[quarter][block + 1]);
             const float2 u2 = make_float2(u, u);
             const float4* w4 = reinterpret_cast<const float4*>(G.wd + 16 * piece);
 #pragma unroll
@@ -261,11 +270,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               const float4 wv = w4[z];
-              m[2 * z] = make_float2(exp2_approx(4 * z <= own ? cum - wv.x : -INFINITY),
-                                     exp2_approx(4 * z + 1 <= own ? cum - wv.y : -INFINITY));
-              m[2 * z + 1] = make_float2(exp2_approx(4 * z + 2 <= own ? cum - wv.z : -INFINITY),
-                                         exp2_approx(4 * z + 3 <= own ? cum - wv.w : -INFINITY));
+              m[2 * z] = make_float2(cum - wv.x, cum - wv.y);
+              m[2 * z + 1] = make_float2(cum - wv.z, cum - wv.w);
             }
+            if (G.wide(quarter)) {
+              tmem_ready(sc, dp);  // no load may be in flight across the call
+              float2 x[8];
+              wide_exponents(G, row, 16 * piece, x);
+#pragma unroll
+              for (int z = 0; z < 8; ++z) m[z] = x[z];
+            }
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              m[z] = make_float2(exp2_approx(2 * z <= own ? m[z].x : -INFINITY),
+                                 exp2_approx(2 * z + 1 <= own ? m[z].y : -INFINITY));
           }
           tmem_ready(sc, dp);
           // E (into sc) = P dP.
@@ -659,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4 rho = reinterpret_cast<const float4*>(G.rho)[lane];
         const float4 asig = reinterpret_cast<const float4*>(G.asig)[lane], d = reinterpret_cast<const float4*>(G.d)[lane];
         const float* dots = w.dots + ((size_t)pair * plan.chunks + at.chunk) * plan.vtiles * 8;
-        float across = lane < plan.vtiles * 8 ? dots[lane] * exp2_approx(G.g.total) : 0.f;  // at most 16 parts
+        float across = lane < plan.vtiles * 8 ? dots[lane] * exp2_approx(G.g.total()) : 0.f;  // at most 16 parts
         if (!wait(bar.sums, at.head_no)) break;
         // Tokens 4 lane .. 4 lane + 3: r, l + (column - row sum of E), and da's own sum.
         auto add = [](float4 a, const float* p, int lane) {

@@ -16,7 +16,8 @@
 //    rounded to bf16 as an operand; y is bf16.  The state itself is float32 and takes U with float32
 //    weights: the weighted v enters as two bf16 values (17 bits), two products.
 //  * exp(c_t - c_s) is split at the end of s's block of 32, exp(c_t - c_end) exp(c_end - c_s), two
-//    factors of at most one: one exponential per row and block instead of one per score.
+//    factors of at most one: one exponential per row and block instead of one per score.  No sum in an
+//    exponent runs over more than a block, and where one is large it is kept in two parts (ChunkGates).
 //  * Only H -> q H and U -> H follow the sequence; S and U of the next chunk are issued before this
 //    chunk's P v, so that P never waits for the tensor cores' latency.
 //  * q and k have their own stages, free as soon as the products have read them: with K = 128 only two
@@ -78,6 +79,35 @@ struct Bars {
   int abort;
 };
 static_assert(sizeof(Bars) <= 320, "");
+
+// P from S for the half of the columns with the rows' own block, where that block's tokens differ in hi: as
+// below, but its weights are taken part by part.  Few blocks decay so far; inside the usual loop, which is
+// at the edge of the instruction cache, the same cost every block 255 to 290 us instead of 246 (8 x 16384).
+static __device__ __noinline__ void put_wide_scores(uint32_t ts, const ChunkGates& G, int row, int half) {
+  const int quarter = row >> 5;
+  const float hi = G.hi[row], lo = G.lo[row];
+#pragma unroll 1
+  for (int x = 0; x < 4; ++x) {
+    const int cb = 2 * half + (x >> 1), col = 32 * cb + 16 * (x & 1);
+    float s[16];
+    uint32_t out[8];
+    tmem_ld16_nowait(ts + col, s);
+    tmem_ready(s);
+    const float u = cb < quarter ? exp2_approx((hi + lo) + G.span[quarter][cb + 1]) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float q[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int k = 2 * e + z;
+        const float m = cb < quarter ? u * G.wd[col + k] : exp2_approx((hi - G.hi[col + k]) + (lo - G.diag[col + k]));
+        q[z] = col + k <= row ? s[k] * m : 0.f;
+      }
+      out[e] = pack_bf16x2(q[0], q[1]);
+    }
+    tmem_st8(ts + 64 * half + 8 * x, out);
+  }
+}
 
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -156,52 +186,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (count > 0) put_weighted(0);
     for (int i = 0; i < count && ok; ++i) {
-      if (!wait(bar.s[i & 1], i >> 1)) break;  // (the gates were waited for with v)
+      const ChunkGates& G = gates[i & 3];  // (waited for with v)
+      const float own = G.hi[row] + G.lo[row];
+      const bool wide = half == quarter >> 1 && G.wide(quarter);
+      if (!wait(bar.s[i & 1], i >> 1)) break;
       tc_fence_after();
-      const ChunkGates& G = gates[i & 3];
-      const float cum = G.cum[row];
       const uint32_t ts = t_lane + kColS + (i & 1) * 128;
       // Block cb of 32 columns against the quarter's own block of 32 rows, 16 columns at a time.
+      if (wide) {
+        put_wide_scores(ts, G, row, half);
+      } else {
 #pragma unroll 2
-      for (int x = 0; x < 4; ++x) {
-        const int cb = 2 * half + (x >> 1), col = 32 * cb + 16 * (x & 1);
-        uint32_t out[8];
-        if (cb > quarter) {
+        for (int x = 0; x < 4; ++x) {
+          const int cb = 2 * half + (x >> 1), col = 32 * cb + 16 * (x & 1);
+          uint32_t out[8];
+          if (cb > quarter) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) out[e] = 0u;
-        } else {
-          float s[16];
-          tmem_ld16_nowait(ts + col, s);
-          if (cb < quarter) {
-            const float u = exp2_approx(cum - G.cum[32 * cb + 31]);
-            const float2 u2 = make_float2(u, u);
-            const float4* w = reinterpret_cast<const float4*>(G.wd + col);
-            tmem_ready(s);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 wv = w[e];
-              const float2 a = mul2(make_float2(s[4 * e], s[4 * e + 1]), mul2(u2, make_float2(wv.x, wv.y)));
-              const float2 c = mul2(make_float2(s[4 * e + 2], s[4 * e + 3]), mul2(u2, make_float2(wv.z, wv.w)));
-              out[2 * e] = pack_bf16x2(a.x, a.y);
-              out[2 * e + 1] = pack_bf16x2(c.x, c.y);
-            }
+            for (int e = 0; e < 8; ++e) out[e] = 0u;
           } else {
-            const float4* w = reinterpret_cast<const float4*>(G.diag + col);
-            tmem_ready(s);
+            float s[16];
+            tmem_ld16_nowait(ts + col, s);
+            if (cb < quarter) {
+              const float u = exp2_approx(own + G.span[quarter][cb + 1]);
+              const float2 u2 = make_float2(u, u);
+              const float4* w = reinterpret_cast<const float4*>(G.wd + col);
+              tmem_ready(s);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 wv = w[e];
-              const float m[4] = {exp2_approx(cum - wv.x), exp2_approx(cum - wv.y), exp2_approx(cum - wv.z),
-                                  exp2_approx(cum - wv.w)};
-              float q[4];
+              for (int e = 0; e < 4; ++e) {
+                const float4 wv = w[e];
+                const float2 a = mul2(make_float2(s[4 * e], s[4 * e + 1]), mul2(u2, make_float2(wv.x, wv.y)));
+                const float2 c = mul2(make_float2(s[4 * e + 2], s[4 * e + 3]), mul2(u2, make_float2(wv.z, wv.w)));
+                out[2 * e] = pack_bf16x2(a.x, a.y);
+                out[2 * e + 1] = pack_bf16x2(c.x, c.y);
+              }
+            } else {
+              const float4* w = reinterpret_cast<const float4*>(G.diag + col);
+              tmem_ready(s);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) q[z] = 16 * (x & 1) + 4 * e + z <= lane ? s[4 * e + z] * m[z] : 0.f;
-              out[2 * e] = pack_bf16x2(q[0], q[1]);
-              out[2 * e + 1] = pack_bf16x2(q[2], q[3]);
+              for (int e = 0; e < 4; ++e) {
+                const float4 wv = w[e];
+                const float m[4] = {exp2_approx(own - wv.x), exp2_approx(own - wv.y), exp2_approx(own - wv.z),
+                                    exp2_approx(own - wv.w)};
+                float q[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) q[z] = 16 * (x & 1) + 4 * e + z <= lane ? s[4 * e + z] * m[z] : 0.f;
+                out[2 * e] = pack_bf16x2(q[0], q[1]);
+                out[2 * e + 1] = pack_bf16x2(q[2], q[3]);
+              }
             }
           }
+          tmem_st8(ts + 64 * half + 8 * x, out);
         }
-        tmem_st8(ts + 64 * half + 8 * x, out);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -214,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < count; ++i) {
       if (!wait(bar.y, i)) break;  // (P's warps had the gates)
       tc_fence_after();
-      const float e = exp2_approx(gates[i & 3].cum[row]);
+      const float e = exp2_approx(gates[i & 3].from_start(row));
       const float2 e2 = make_float2(e, e);
       const uint32_t tv = vstage(i);
 #pragma unroll 1
@@ -307,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < count; ++i) {
       if (!wait(bar.u, i)) break;  // (weighing v took the gates)
       tc_fence_after();
-      const float e = exp2_approx(gates[i & 3].total);
+      const float e = exp2_approx(gates[i & 3].total());
       const float2 e2 = make_float2(e, e);
 #pragma unroll
       for (int x = 0; x < HC / 16; ++x) {

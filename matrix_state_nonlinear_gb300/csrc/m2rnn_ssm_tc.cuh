@@ -218,53 +218,83 @@ __device__ __forceinline__ void copy_out(uint16_t* dst, uint32_t tile, long long
   }
 }
 
-// What the products of a chunk need of its gates, per token.  Blocks are of 32 tokens.
+// What the products of a chunk need of its gates.  Blocks are of 32 tokens; B_t is log2 of the decay from
+// the start of a token's block to the token, its own included.
+//
+// Between tokens s < t of two blocks the weight exp(c_t - c_s) d_s is 2^(B_t + span of the blocks between)
+// wd_s, within a block it is 2^(B_t - B_s) d_s.  B is kept as hi + lo.  Where a block decays by 2^-256 or
+// more in all, hi sums each token's log2 f rounded to a multiple of 2^-8, exactly (a block's sum is below
+// 2^13, as log f is held at -105 and above), and lo the rests, which stay below 1/16: B_t - B_s taken part
+// by part is then as exact as a sum over the tokens from s to t alone.  In one float it would lose 2^-24 of
+// B itself, 3e-4 of a weight between the last tokens of a block whose others forget the state (and 1.7e-3
+// summed from the chunk's start).  In any other block, nearly every one, hi is zero and lo is B, within
+// 2^-16 of a weight, and the usual path needs lo alone.
 struct alignas(16) ChunkGates {
-  float cum[kTokens];   // log2 of the decay from the chunk's start, the token's own included
-  float diag[kTokens];  // cum - log2 d: d exp(c_t - c_s) is 2^(cum_t - diag_s)
+  float hi[kTokens], lo[kTokens];
+  float diag[kTokens];  // lo - log2 d: d exp(c_t - c_s) is 2^((hi_t - hi_s) + (lo_t - diag_s)) within a block
   float wd[kTokens];    // d times the decay from the token to the end of its block
   float wk[kTokens];    // d times the decay from the token to the chunk's end
-  float total;          // log2 of the whole chunk's decay
+  float span[5][4];     // [i][j], j <= i: log2 of the decay of blocks j .. i - 1
+  __device__ __forceinline__ float total() const { return span[4][0]; }  // log2 of the whole chunk's decay
+  // log2 of the decay from the chunk's start to a token, its own included.
+  __device__ __forceinline__ float from_start(int t) const { return (hi[t] + lo[t]) + span[t >> 5][0]; }
+  // Whether a block's tokens differ in hi (which, like B, only falls or only rises).
+  __device__ __forceinline__ bool wide(int block) const { return hi[32 * block + 31] != 0.f; }
 };
 
 // One warp fills a chunk's gates; `logits` gives the logit of a token of the chunk (-infinity past
 // the sequence).  Each token's own values first (in o's arrays), then lane l sums over tokens
-// 4 l .. 4 l + 3 and the lanes before and after: sums over later tokens run from the end, so that
-// they are exact near zero.  The loop is kept short on purpose: the block's warps run different
-// code, and what does not fit the instruction cache stalls them all.
+// 4 l .. 4 l + 3 and the lanes before.  The loop is kept short on purpose: the block's warps run
+// different code, and what does not fit the instruction cache stalls them all.
 template <typename Logits>
 __device__ __forceinline__ void put_chunk_gates(ChunkGates& o, Logits logits, float alpha, float beta, int lane) {
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const int t = 32 * i + lane;
     const float2 g = ssm_gate(logits(i), alpha, beta);
+    const float c = g.y * kLog2e, h = (c + 49152.f) - 49152.f;  // 1.5 * 2^15: one ulp is 2^-8
     o.wd[t] = g.x;
-    o.cum[t] = g.y * kLog2e;
+    o.hi[t] = h;
+    o.lo[t] = c - h;
     o.diag[t] = log2f(g.x);
   }
   __syncwarp();
-  const float4 d = reinterpret_cast<const float4*>(o.wd)[lane], c = reinterpret_cast<const float4*>(o.cum)[lane];
-  float4 ld = reinterpret_cast<const float4*>(o.diag)[lane];
-  const float c1 = c.x + c.y, c2 = c1 + c.z, c3 = c2 + c.w, r2 = c.w, r1 = r2 + c.z, r0 = r1 + c.y;
-  float before = c3, after = r0 + c.x;
+  float4 h = reinterpret_cast<const float4*>(o.hi)[lane], l = reinterpret_cast<const float4*>(o.lo)[lane];
+  h.y += h.x, h.z += h.y, h.w += h.z;
+  l.y += l.x, l.z += l.y, l.w += l.z;
+  float sh = h.w, sl = l.w;  // over the block's lanes up to this one
 #pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const float x = __shfl_up_sync(~0u, before, s), y = __shfl_down_sync(~0u, after, s);
-    if (lane >= s) before += x;
-    if (lane + s < 32) after += y;
+  for (int s = 1; s < 8; s <<= 1) {
+    const float x = __shfl_up_sync(~0u, sh, s, 8), y = __shfl_up_sync(~0u, sl, s, 8);
+    if ((lane & 7) >= s) sh += x, sl += y;
   }
-  if (lane == 31) o.total = before;
-  float pre = __shfl_up_sync(~0u, before, 1), post = __shfl_down_sync(~0u, after, 1);
-  if (lane == 0) pre = 0.f;
-  if (lane == 31) post = 0.f;
-  const float4 x = make_float4(pre + c.x, pre + c1, pre + c2, pre + c3);
-  const float end = __shfl_sync(~0u, x.w, lane | 7);
-  reinterpret_cast<float4*>(o.cum)[lane] = x;
-  reinterpret_cast<float4*>(o.diag)[lane] = make_float4(x.x - ld.x, x.y - ld.y, x.z - ld.z, x.w - ld.w);
-  reinterpret_cast<float4*>(o.wd)[lane] = make_float4(d.x * exp2_approx(end - x.x), d.y * exp2_approx(end - x.y),
-                                                      d.z * exp2_approx(end - x.z), d.w * exp2_approx(end - x.w));
-  reinterpret_cast<float4*>(o.wk)[lane] = make_float4(d.x * exp2_approx(post + r0), d.y * exp2_approx(post + r1),
-                                                      d.z * exp2_approx(post + r2), d.w * exp2_approx(post));
+  const float eh = __shfl_sync(~0u, sh, 7, 8), el = __shfl_sync(~0u, sl, 7, 8);  // over the block
+  sh -= h.w, sl -= l.w;  // before the lane
+  h = make_float4(sh + h.x, sh + h.y, sh + h.z, sh + h.w);
+  l = make_float4(sl + l.x, sl + l.y, sl + l.z, sl + l.w);
+  const float4 d = reinterpret_cast<const float4*>(o.wd)[lane], ld = reinterpret_cast<const float4*>(o.diag)[lane];
+  const float4 wd = make_float4(d.x * exp2_approx((eh - h.x) + (el - l.x)), d.y * exp2_approx((eh - h.y) + (el - l.y)),
+                                d.z * exp2_approx((eh - h.z) + (el - l.z)), d.w * exp2_approx((eh - h.w) + (el - l.w)));
+  reinterpret_cast<float4*>(o.wd)[lane] = wd;
+  if (fabsf(eh) < 256.f) {
+    l = make_float4(l.x + h.x, l.y + h.y, l.z + h.z, l.w + h.w);
+    h = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  reinterpret_cast<float4*>(o.hi)[lane] = h;
+  reinterpret_cast<float4*>(o.lo)[lane] = l;
+  reinterpret_cast<float4*>(o.diag)[lane] = make_float4(l.x - ld.x, l.y - ld.y, l.z - ld.z, l.w - ld.w);
+  // Sums over whole blocks: of the later ones for wk, and span[i][j] by lane 4 i + j.
+  const uint32_t later = 14u << (lane >> 3), part = ((1u << (lane >> 2)) - 1u) & (15u << (lane & 3));
+  float tail = 0.f, span = 0.f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const float x = __shfl_sync(~0u, eh + el, 8 * b);
+    if (later >> b & 1) tail += x;
+    if (part >> b & 1) span += x;
+  }
+  const float e = exp2_approx(tail);
+  reinterpret_cast<float4*>(o.wk)[lane] = make_float4(e * wd.x, e * wd.y, e * wd.z, e * wd.w);
+  if (lane < 20) o.span[0][lane] = span;
 }
 
 // Eight bf16 values as four float2.
