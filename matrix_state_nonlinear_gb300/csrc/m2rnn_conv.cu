@@ -50,16 +50,11 @@ template <int VEC>
 struct Taps {
   static constexpr int P = Chan<VEC>::P;
   float2 w[kTaps][P], b[P];
-  // A channel's taps: one load, or four where the taps are not 16-byte aligned (views into a flat buffer).
-  __device__ __forceinline__ static float4 taps_of(const float* w, bool aligned) {
-    return aligned ? *reinterpret_cast<const float4*>(w) : make_float4(w[0], w[1], w[2], w[3]);
-  }
-  __device__ __forceinline__ void load(const ConvProblem& p, int c0) {
-    const float *wp = p.w, *bias = p.bias;
+  __device__ __forceinline__ void load(const float* wp, const float* bias, int c0) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const float4 x = taps_of(wp + (size_t)(c0 + 2 * i) * kTaps, p.w_aligned);
-      const float4 y = VEC > 1 ? taps_of(wp + (size_t)(c0 + 2 * i + 1) * kTaps, p.w_aligned) : x;
+      const float4 x = *reinterpret_cast<const float4*>(wp + (size_t)(c0 + 2 * i) * kTaps);
+      const float4 y = VEC > 1 ? *reinterpret_cast<const float4*>(wp + (size_t)(c0 + 2 * i + 1) * kTaps) : x;
       w[0][i] = make_float2(x.x, y.x), w[1][i] = make_float2(x.y, y.y);
       w[2][i] = make_float2(x.z, y.z), w[3][i] = make_float2(x.w, y.w);
       b[i] = bias ? make_float2(bias[c0 + 2 * i], VEC > 1 ? bias[c0 + 2 * i + 1] : 0.f) : make_float2(0.f, 0.f);
@@ -106,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < kHist; ++j) *reinterpret_cast<Raw*>(window_out + (b * kHist + j) * p.C + c0) = f[j];
   }
   Taps<VEC> w;
-  w.load(p, c0);
+  w.load(p.w, p.bias, c0);
   Raw raw[U];
   const uint16_t* next = xb + t0 * p.sx.token;
   auto fetch = [&](int t) {
@@ -186,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     for (int j = 0; j < kTaps; ++j) dw[j][i] = zero;
   }
   Taps<VEC> w;
-  w.load(p, c0);
+  w.load(p.w, p.bias, c0);
   const int most = min(p.T, t1 + kHist);
   const uint16_t *nx = xb + t0 * p.sx.token, *ng = dout + (b * p.T + t0) * p.C + c0;
   uint16_t* dxt = dx + (b * p.T + t0 - kHist) * p.C + c0;

@@ -95,7 +95,6 @@ struct ConvProblem {
   const uint16_t* window_in;
   int B, T, C;
   Strides sx;
-  bool w_aligned;  // to 16 bytes
 };
 cudaError_t launch_conv_window(const ConvProblem& p, uint16_t* out, uint16_t* window_out,
                                cudaStream_t stream);

@@ -40,8 +40,9 @@ m2rnn_status m2rnn_conv_silu_window_bf16(const uint16_t* x, const float* w, cons
                                          long long x_batch, long long x_token, void* stream) {
   if (B < 1 || T < 0 || C < 1 || !w || x_batch < 0 || x_token < 0) return M2RNN_ERR_INVALID_ARG;
   if (T > 0 && (!x || !out)) return M2RNN_ERR_INVALID_ARG;
+  if (!aligned_to(w, 16)) return M2RNN_ERR_INVALID_ARG;
   if ((long long)B * C > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
-  const ConvProblem p{x, w, bias, window_in, B, T, C, {x_batch, x_token}, aligned_to(w, 16)};
+  const ConvProblem p{x, w, bias, window_in, B, T, C, {x_batch, x_token}};
   return done(launch_conv_window(p, out, window_out, static_cast<cudaStream_t>(stream)));
 }
 
@@ -59,11 +60,11 @@ m2rnn_status m2rnn_conv_silu_backward_bf16(const uint16_t* x, const float* w, co
   if (B < 1 || T < 0 || C < 1 || !w || !dw || x_batch < 0 || x_token < 0)
     return M2RNN_ERR_INVALID_ARG;
   if (T > 0 && (!x || !dout || !dx || !workspace)) return M2RNN_ERR_INVALID_ARG;
-  if (!aligned_to(workspace, 16)) return M2RNN_ERR_INVALID_ARG;
+  if (!aligned_to(w, 16) || !aligned_to(workspace, 16)) return M2RNN_ERR_INVALID_ARG;
   if ((long long)B * C > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
   if (workspace_bytes < m2rnn_conv_silu_backward_workspace_bytes(B, T, C))
     return M2RNN_ERR_INVALID_ARG;
-  const ConvProblem p{x, w, bias, window_in, B, T, C, {x_batch, x_token}, aligned_to(w, 16)};
+  const ConvProblem p{x, w, bias, window_in, B, T, C, {x_batch, x_token}};
   return done(launch_conv_backward(p, dout, dx, dw, dbias, dwindow, static_cast<float*>(workspace),
                                    static_cast<cudaStream_t>(stream)));
 }
