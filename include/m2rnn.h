@@ -344,6 +344,10 @@ m2rnn_status m2rnn_forward_conv_bf16(const uint16_t* xq, const uint16_t* xk, con
  * and their width) are contiguous, so slices of a wider projection or conv output can be
  * passed without a copy.  All other tensors are dense.
  *
+ * Sizes.  Tensors may hold more than 2^31 values; T <= 2^31 - 128, and B C (conv), B N
+ * (scan) < 2^31.  The backwards count their sums in 32 bits: 5 C and 2 D (norm) and
+ * N (2 + V) <= 2^31 - 32.  UNSUPPORTED above.
+ *
  * m2rnn_conv_silu_window_bf16: m2rnn_conv_silu_bf16 continuing an earlier call.
  *   out[b,t,c] = SiLU(bias[c] + sum_{j=0..3} w[c][j] * X[b, t-3+j, c])
  *   with X[b, -3..-1] = window_in[b] (NULL: zeros) and X[b, t >= 0] = x[b, t].

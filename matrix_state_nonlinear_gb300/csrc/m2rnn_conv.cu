@@ -379,9 +379,12 @@ cudaError_t launch_conv_window(const ConvProblem& p, uint16_t* out, uint16_t* wi
   return run_forward<1>(p, out, window_out, stream);
 }
 
-size_t conv_backward_workspace_floats(int B, int T, int C) {
+long long conv_backward_rows(int B, int T, int C) {
   const int span = backward_span(B, T, C);
-  return (size_t)B * ((T + span - 1) / span) * C * (kTaps + 1);
+  return (long long)B * ((T + span - 1) / span);
+}
+size_t conv_backward_workspace_floats(int B, int T, int C) {
+  return (size_t)conv_backward_rows(B, T, C) * C * (kTaps + 1);
 }
 
 cudaError_t launch_conv_backward(const ConvProblem& p, const uint16_t* dout, uint16_t* dx,
@@ -394,8 +397,7 @@ cudaError_t launch_conv_backward(const ConvProblem& p, const uint16_t* dout, uin
   } else {
     const bool vec = rows_aligned(p, 4) && aligned_to(dout, 8) && aligned_to(dx, 8) &&
                      aligned_to(dwindow, 8);
-    const int span = backward_span(p.B, p.T, p.C);
-    count = p.B * ((p.T + span - 1) / span);
+    count = (int)conv_backward_rows(p.B, p.T, p.C);
     err = vec ? run_backward<4>(p, dout, dx, dwindow, ws, stream)
               : run_backward<1>(p, dout, dx, dwindow, ws, stream);
   }

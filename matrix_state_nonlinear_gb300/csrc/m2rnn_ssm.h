@@ -12,6 +12,9 @@ namespace m2rnn {
 constexpr int kSsmChunk = 128;   // tokens per chunk of the scan
 constexpr int kSsmColumns = 64;  // value columns per block of the scan
 
+// Tokens of a sequence at most: counts of them are rounded up to stretches of 128 in 32 bits.
+constexpr int kMaxTokens = 0x7fffffff - 127;
+
 // Batch and token strides of one bf16 operand, in elements.
 struct Strides {
   long long batch, token;
@@ -99,6 +102,7 @@ struct ConvProblem {
 cudaError_t launch_conv_window(const ConvProblem& p, uint16_t* out, uint16_t* window_out,
                                cudaStream_t stream);
 size_t conv_backward_workspace_floats(int B, int T, int C);
+long long conv_backward_rows(int B, int T, int C);  // of partial sums, 5 C floats each
 cudaError_t launch_conv_backward(const ConvProblem& p, const uint16_t* dout, uint16_t* dx,
                                  float* dw, float* dbias, uint16_t* dwindow, float* ws,
                                  cudaStream_t stream);

@@ -13,7 +13,28 @@ m2rnn_status done(cudaError_t e) { return e == cudaSuccess ? M2RNN_OK : M2RNN_ER
 m2rnn_status ssm_sizes(int B, int T, int N, int Nqk, int K, int V) {
   if (B < 1 || T < 0 || N < 1 || Nqk < 1 || K < 1 || V < 1 || N % Nqk != 0)
     return M2RNN_ERR_INVALID_ARG;
-  if (K > 128 || V > 128 || (long long)B * N > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
+  if (K > 128 || V > 128 || T > kMaxTokens || (long long)B * N > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
+  return M2RNN_OK;
+}
+// The backward's too: its sums over parameters count N (2 + V) of them in 32 bits, 32 per block.
+m2rnn_status ssm_backward_sizes(int B, int T, int N, int Nqk, int K, int V) {
+  const m2rnn_status st = ssm_sizes(B, T, N, Nqk, K, V);
+  return st == M2RNN_OK && (long long)N * (2 + V) > 0x7fffffffLL - 31 ? M2RNN_ERR_UNSUPPORTED : st;
+}
+
+// Sizes of the convolution; its backward counts 5 C sums, 32 per block, and their rows in 32 bits.
+m2rnn_status conv_sizes(int B, int T, int C, bool backward) {
+  if (B < 1 || T < 0 || C < 1) return M2RNN_ERR_INVALID_ARG;
+  if (T > kMaxTokens || (long long)B * C > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
+  if (backward && (5LL * C > 0x7fffffffLL - 31 || conv_backward_rows(B, T, C) > 0x7fffffffLL))
+    return M2RNN_ERR_UNSUPPORTED;
+  return M2RNN_OK;
+}
+
+// Sizes of the norm; its backward counts 2 D sums, 32 per block, in 32 bits.
+m2rnn_status norm_sizes(long long rows, int D, int groups, bool backward) {
+  if (rows < 0 || D < 1 || groups < 1 || D % groups != 0) return M2RNN_ERR_INVALID_ARG;
+  if (D / groups > kNormMaxGroup || (backward && 2LL * D > 0x7fffffffLL - 31)) return M2RNN_ERR_UNSUPPORTED;
   return M2RNN_OK;
 }
 
@@ -38,16 +59,17 @@ m2rnn_status m2rnn_conv_silu_window_bf16(const uint16_t* x, const float* w, cons
                                          const uint16_t* window_in, uint16_t* out,
                                          uint16_t* window_out, int B, int T, int C,
                                          long long x_batch, long long x_token, void* stream) {
-  if (B < 1 || T < 0 || C < 1 || !w || x_batch < 0 || x_token < 0) return M2RNN_ERR_INVALID_ARG;
+  const m2rnn_status st = conv_sizes(B, T, C, false);
+  if (st != M2RNN_OK) return st;
+  if (!w || x_batch < 0 || x_token < 0) return M2RNN_ERR_INVALID_ARG;
   if (T > 0 && (!x || !out)) return M2RNN_ERR_INVALID_ARG;
   if (!aligned_to(w, 16)) return M2RNN_ERR_INVALID_ARG;
-  if ((long long)B * C > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
   const ConvProblem p{x, w, bias, window_in, B, T, C, {x_batch, x_token}};
   return done(launch_conv_window(p, out, window_out, static_cast<cudaStream_t>(stream)));
 }
 
 size_t m2rnn_conv_silu_backward_workspace_bytes(int B, int T, int C) {
-  if (B < 1 || T < 0 || C < 1) return 0;
+  if (conv_sizes(B, T, C, true) != M2RNN_OK) return 0;
   return sizeof(float) * conv_backward_workspace_floats(B, T, C);
 }
 
@@ -57,11 +79,11 @@ m2rnn_status m2rnn_conv_silu_backward_bf16(const uint16_t* x, const float* w, co
                                            uint16_t* dwindow, int B, int T, int C,
                                            long long x_batch, long long x_token, void* workspace,
                                            size_t workspace_bytes, void* stream) {
-  if (B < 1 || T < 0 || C < 1 || !w || !dw || x_batch < 0 || x_token < 0)
-    return M2RNN_ERR_INVALID_ARG;
+  const m2rnn_status st = conv_sizes(B, T, C, true);
+  if (st != M2RNN_OK) return st;
+  if (!w || !dw || x_batch < 0 || x_token < 0) return M2RNN_ERR_INVALID_ARG;
   if (T > 0 && (!x || !dout || !dx || !workspace)) return M2RNN_ERR_INVALID_ARG;
   if (!aligned_to(w, 16) || !aligned_to(workspace, 16)) return M2RNN_ERR_INVALID_ARG;
-  if ((long long)B * C > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
   if (workspace_bytes < m2rnn_conv_silu_backward_workspace_bytes(B, T, C))
     return M2RNN_ERR_INVALID_ARG;
   const ConvProblem p{x, w, bias, window_in, B, T, C, {x_batch, x_token}};
@@ -75,7 +97,7 @@ size_t m2rnn_ssm_states_bytes(int B, int T, int N, int K, int V) {
 }
 
 size_t m2rnn_ssm_workspace_bytes(int B, int T, int N, int Nqk, int K, int V, int backward) {
-  if (ssm_sizes(B, T, N, Nqk, K, V) != M2RNN_OK) return 0;
+  if ((backward ? ssm_backward_sizes(B, T, N, Nqk, K, V) : ssm_sizes(B, T, N, Nqk, K, V)) != M2RNN_OK) return 0;
   return backward ? ssm_backward_workspace_bytes(B, T, N, Nqk, K, V)
                   : ssm_forward_workspace_bytes(B, T, N, Nqk, K, V);
 }
@@ -112,7 +134,7 @@ m2rnn_status m2rnn_ssm_backward_bf16(const uint16_t* q, const uint16_t* k, const
                                      float* dH0, const long long* strides, int B, int T, int N,
                                      int Nqk, int K, int V, void* workspace,
                                      size_t workspace_bytes, void* stream) {
-  const m2rnn_status st = ssm_sizes(B, T, N, Nqk, K, V);
+  const m2rnn_status st = ssm_backward_sizes(B, T, N, Nqk, K, V);
   if (st != M2RNN_OK) return st;
   if (!alpha || !beta || !w_r || !dalpha || !dbeta || !dw_r) return M2RNN_ERR_INVALID_ARG;
   if (T > 0 && (!q || !k || !v || !a || !Hs || !dy || !dq || !dk || !dv || !da))
@@ -147,9 +169,9 @@ m2rnn_status m2rnn_ssm_step_bf16(const uint16_t* q, const uint16_t* k, const uin
 m2rnn_status m2rnn_gate_groupnorm(const void* y, int y_f32, const uint16_t* g_pre, const float* w,
                                   const float* bias, float eps, uint16_t* out, long long rows,
                                   int D, int groups, void* stream) {
-  if (rows < 0 || D < 1 || groups < 1 || D % groups != 0 || !(eps >= 0.f) || !w)
-    return M2RNN_ERR_INVALID_ARG;
-  if (D / groups > kNormMaxGroup) return M2RNN_ERR_UNSUPPORTED;
+  const m2rnn_status st = norm_sizes(rows, D, groups, false);
+  if (st != M2RNN_OK) return st;
+  if (!(eps >= 0.f) || !w) return M2RNN_ERR_INVALID_ARG;
   if (rows == 0) return M2RNN_OK;
   if (!y || !out) return M2RNN_ERR_INVALID_ARG;
   const NormProblem p{y, y_f32 != 0, g_pre, w, bias, eps, rows, D, groups};
@@ -157,7 +179,7 @@ m2rnn_status m2rnn_gate_groupnorm(const void* y, int y_f32, const uint16_t* g_pr
 }
 
 size_t m2rnn_gate_groupnorm_backward_workspace_bytes(long long rows, int D, int groups) {
-  if (rows < 0 || D < 1 || groups < 1 || D % groups != 0 || D / groups > kNormMaxGroup) return 0;
+  if (norm_sizes(rows, D, groups, true) != M2RNN_OK) return 0;
   return sizeof(float) * groupnorm_backward_workspace_floats(rows, D, groups);
 }
 
@@ -167,9 +189,9 @@ m2rnn_status m2rnn_gate_groupnorm_backward(const void* y, int y_f32, const uint1
                                            float* dw, float* dbias, long long rows, int D,
                                            int groups, void* workspace, size_t workspace_bytes,
                                            void* stream) {
-  if (rows < 0 || D < 1 || groups < 1 || D % groups != 0 || !(eps >= 0.f) || !w || !dw)
-    return M2RNN_ERR_INVALID_ARG;
-  if (D / groups > kNormMaxGroup) return M2RNN_ERR_UNSUPPORTED;
+  const m2rnn_status st = norm_sizes(rows, D, groups, true);
+  if (st != M2RNN_OK) return st;
+  if (!(eps >= 0.f) || !w || !dw) return M2RNN_ERR_INVALID_ARG;
   if (rows > 0 && (!y || !dout || !dy || !workspace || (g_pre != nullptr) != (dg_pre != nullptr)))
     return M2RNN_ERR_INVALID_ARG;
   if (!aligned_to(workspace, 16) ||

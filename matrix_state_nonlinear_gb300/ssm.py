@@ -94,6 +94,13 @@ def _raise(st, where):
     raise M2RNNError(st, where)
 
 
+def _sizes(*n):
+    """Sizes that the library takes as 32-bit integers; ctypes would cut larger ones down."""
+    if max(n) > 0x7fffffff:
+        raise ValueError(f"sizes of 2^31 and above are not supported: {n}")
+    return n
+
+
 # ---------------------------------------------------------------- short causal convolution
 @_on_stream
 def conv_silu_window(x, w, bias=None, window=None, out=None, window_out=None):
@@ -103,6 +110,7 @@ def conv_silu_window(x, w, bias=None, window=None, out=None, window_out=None):
     window after x (may be ``window`` itself: in place)."""
     dev = _device(x)
     B, T, C = shape = x.shape
+    _sizes(B, T, C)
     xp, xb, xt = _tokens(x, "x", shape, dev)
     if out is None:
         out = x.new_empty(shape)
@@ -123,6 +131,7 @@ def conv_silu_step(x, w, bias, window, window_out=None, out=None):
     unless ``window_out`` is given.  Returns (out [B, C] bf16, window_out)."""
     dev = _device(x)
     B, C = shape = x.shape
+    _sizes(B, C)
     if x.dtype is not BF16 or (x.stride(1) != 1 and C > 1):
         _refuse(x, "x", BF16, shape, dev)
     if out is None:
@@ -144,6 +153,7 @@ def conv_silu_backward(x, w, bias, dout, window=None, grads=None, workspace=None
     float32, dwindow [B, 3, C] bf16 (``grads`` may supply any of them preallocated)."""
     dev = _device(x)
     B, T, C = shape = x.shape
+    _sizes(B, T, C)
     xp, xb, xt = _tokens(x, "x", shape, dev)
     g = dict(grads or {})
     ptrs = []
@@ -173,6 +183,7 @@ def _ssm_args(inputs):
     dev = _device(q)
     B, T, G, K = shape = q.shape
     N, V = v.shape[2:]
+    _sizes(B, T, G, K, N, V)
     if G < 1 or N % G:
         raise ValueError(f"q, k must have a number of heads that divides {N}, got {G}")
     qp, qb, qt = _tokens(q, "q", shape, dev)
@@ -186,11 +197,11 @@ def _ssm_args(inputs):
 
 
 def ssm_states_bytes(B, T, N, K, V) -> int:
-    return int(load_library().m2rnn_ssm_states_bytes(B, T, N, K, V))
+    return int(load_library().m2rnn_ssm_states_bytes(*_sizes(B, T, N, K, V)))
 
 
 def ssm_workspace_bytes(B, T, N, Nqk, K, V, backward=False) -> int:
-    return int(load_library().m2rnn_ssm_workspace_bytes(B, T, N, Nqk, K, V, int(backward)))
+    return int(load_library().m2rnn_ssm_workspace_bytes(*_sizes(B, T, N, Nqk, K, V), int(backward)))
 
 
 def _ssm_run(inputs, y, H_T, Hs, keep, workspace):
@@ -269,6 +280,7 @@ def ssm_step(q, k, v, a, alpha, beta, w_r, H_in, H_out=None, y=None):
     dev = _device(q)
     B, G, K = q.shape
     N, V = v.shape[1:]
+    _sizes(B, G, K, N, V)
     if G < 1 or N % G:
         raise ValueError(f"q, k must have a number of heads that divides {N}, got {G}")
     state = (B, N, K, V)
@@ -294,6 +306,7 @@ def _norm_args(y, g_pre, w, bias, groups):
     dev = _device(y)
     shape = y.shape
     D = shape[-1]
+    _sizes(D, groups)
     if y.dtype not in (F32, BF16):
         raise TypeError(f"y: expected {F32} or {BF16}, got {y.dtype}")
     if groups < 1 or D % groups:
