@@ -353,10 +353,10 @@ m2rnn_status m2rnn_forward_conv_bf16(const uint16_t* xq, const uint16_t* xk, con
  *   with X[b, -3..-1] = window_in[b] (NULL: zeros) and X[b, t >= 0] = x[b, t].
  *   x [B, T, C] bf16 with strides (x_batch, x_token); window_in, window_out [B, 3, C] bf16:
  *   the last three inputs, oldest first (window_out NULL: not written; window_out ==
- *   window_in updates in place); out [B, T, C] bf16 dense; w [C, 4], bias [C] (or NULL)
- *   float32.  T = 1 is the single-token form.  T = 0 copies the window.  Any C >= 1; rows
- *   of C % 4 == 0 channels with every bf16 pointer and stride 8-byte aligned run on
- *   8-byte accesses.
+ *   window_in updates in place); out [B, T, C] bf16 dense; w [C, 4] float32 (16-byte
+ *   aligned, else INVALID_ARG); bias [C] float32 or NULL (none).  T = 1 is the single-token
+ *   form.  T = 0 copies the window.  Any C >= 1; rows of C % 4 == 0 channels with every bf16
+ *   pointer and stride 8-byte aligned run on 8-byte accesses.
  * m2rnn_conv_silu_backward_bf16: its gradients, given dout [B, T, C] bf16 (dense):
  *   dx [B, T, C] bf16 (dense), dw [C, 4], dbias [C] float32 (NULL: not written),
  *   dwindow [B, 3, C] bf16 (NULL: not written).  The workspace (16-byte aligned, at least

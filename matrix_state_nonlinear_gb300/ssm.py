@@ -102,12 +102,19 @@ def _sizes(*n):
 
 
 # ---------------------------------------------------------------- short causal convolution
+def _taps(w, C, dev):
+    p = _ptr(w, "w", F32, (C, 4), dev)
+    if p is not None and p % 16:
+        raise ValueError("w: must be 16-byte aligned (a view into a larger buffer may not be; copy it once)")
+    return p
+
+
 @_on_stream
 def conv_silu_window(x, w, bias=None, window=None, out=None, window_out=None):
     """``conv_silu`` continuing an earlier call: x [B, T, C] bf16 (batch and token strides
-    free), w [C, 4] and bias [C] float32, window [B, 3, C] bf16 the last three inputs before
-    x, oldest first (None: zeros).  Returns (out [B, T, C] bf16, window_out [B, 3, C]), the
-    window after x (may be ``window`` itself: in place)."""
+    free), w [C, 4] (16-byte aligned) and bias [C] float32, window [B, 3, C] bf16 the last three
+    inputs before x, oldest first (None: zeros).  Returns (out [B, T, C] bf16, window_out
+    [B, 3, C]), the window after x (may be ``window`` itself: in place)."""
     dev = _device(x)
     B, T, C = shape = x.shape
     _sizes(B, T, C)
@@ -117,7 +124,7 @@ def conv_silu_window(x, w, bias=None, window=None, out=None, window_out=None):
     if window_out is None:
         window_out = x.new_empty((B, 3, C))
     st = load_library().m2rnn_conv_silu_window_bf16(
-        xp, _ptr(w, "w", F32, (C, 4), dev), _ptr(bias, "bias", F32, (C,), dev),
+        xp, _taps(w, C, dev), _ptr(bias, "bias", F32, (C,), dev),
         _ptr(window, "window", BF16, (B, 3, C), dev), _ptr(out, "out", BF16, shape, dev),
         _ptr(window_out, "window_out", BF16, (B, 3, C), dev), B, T, C, xb, xt, _stream(dev))
     if st != OK:
@@ -139,7 +146,7 @@ def conv_silu_step(x, w, bias, window, window_out=None, out=None):
     if window_out is None:
         window_out = window
     st = load_library().m2rnn_conv_silu_window_bf16(
-        x.data_ptr(), _ptr(w, "w", F32, (C, 4), dev), _ptr(bias, "bias", F32, (C,), dev),
+        x.data_ptr(), _taps(w, C, dev), _ptr(bias, "bias", F32, (C,), dev),
         _ptr(window, "window", BF16, (B, 3, C), dev), _ptr(out, "out", BF16, shape, dev),
         _ptr(window_out, "window_out", BF16, (B, 3, C), dev), B, 1, C, x.stride(0), C, _stream(dev))
     if st != OK:
@@ -165,7 +172,7 @@ def conv_silu_backward(x, w, bias, dout, window=None, grads=None, workspace=None
     lib = load_library()
     ws, wp, wb = _workspace(workspace, lib.m2rnn_conv_silu_backward_workspace_bytes(B, T, C), x)
     st = lib.m2rnn_conv_silu_backward_bf16(
-        xp, _ptr(w, "w", F32, (C, 4), dev), _ptr(bias, "bias", F32, (C,), dev),
+        xp, _taps(w, C, dev), _ptr(bias, "bias", F32, (C,), dev),
         _ptr(window, "window", BF16, (B, 3, C), dev), _ptr(dout, "dout", BF16, shape, dev), *ptrs,
         B, T, C, xb, xt, wp, wb, _stream(dev))
     if st != OK:

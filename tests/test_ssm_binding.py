@@ -124,3 +124,17 @@ def test_a_stream_of_another_device_is_refused(library, name):
         calls(0)[name](stream=stream)
     with pytest.raises(Reached):  # the stream's own device, whichever is current
         calls(1)[name](stream=stream)
+
+
+@pytest.mark.parametrize("offset", [4, 8, 12])
+def test_taps_off_16_bytes_are_refused_by_name(library, offset):
+    """As a view into a flat buffer of parameters may have them."""
+    class At(Fake):
+        def data_ptr(self):
+            return (1 << 20) + offset
+    w, x, win = At(0, 8, 4, dtype=torch.float32), Fake(0, 2, 5, 8), Fake(0, 2, 3, 8)
+    for call in (lambda: pkg.conv_silu_window(x, w, None, win, out=x, window_out=win),
+                 lambda: pkg.conv_silu_step(Fake(0, 2, 8), w, None, win, out=Fake(0, 2, 8)),
+                 lambda: pkg.conv_silu_backward(x, w, None, x, win, workspace=x)):
+        with pytest.raises(ValueError, match="w: must be 16-byte aligned"):
+            call()
