@@ -134,8 +134,8 @@ def conv_silu_window(x, w, bias=None, window=None, out=None, window_out=None):
 
 @_on_stream
 def conv_silu_step(x, w, bias, window, window_out=None, out=None):
-    """One token: x [B, C] bf16 (batch stride free), window [B, 3, C] bf16, updated in place
-    unless ``window_out`` is given.  Returns (out [B, C] bf16, window_out)."""
+    """One token: x [B, C] bf16 (batch stride free), window [B, 3, C] bf16 (None: zeros), updated
+    in place unless ``window_out`` is given.  Returns (out [B, C] bf16, window_out)."""
     dev = _device(x)
     B, C = shape = x.shape
     _sizes(B, C)
@@ -144,7 +144,7 @@ def conv_silu_step(x, w, bias, window, window_out=None, out=None):
     if out is None:
         out = x.new_empty(shape)
     if window_out is None:
-        window_out = window
+        window_out = x.new_empty((B, 3, C)) if window is None else window
     st = load_library().m2rnn_conv_silu_window_bf16(
         x.data_ptr(), _taps(w, C, dev), _ptr(bias, "bias", F32, (C,), dev),
         _ptr(window, "window", BF16, (B, 3, C), dev), _ptr(out, "out", BF16, shape, dev),

@@ -138,3 +138,11 @@ def test_taps_off_16_bytes_are_refused_by_name(library, offset):
                  lambda: pkg.conv_silu_backward(x, w, None, x, win, workspace=x)):
         with pytest.raises(ValueError, match="w: must be 16-byte aligned"):
             call()
+
+
+def test_a_first_token_gets_a_window(library):
+    """conv_silu_step without a window starts from zeros and returns the one after the token."""
+    with pytest.raises(Reached) as e:
+        pkg.conv_silu_step(Fake(0, 2, 8), Fake(0, 8, 4, dtype=torch.float32), None, None, out=Fake(0, 2, 8))
+    _, args = e.value.args
+    assert args[3] is None and args[5] is not None
