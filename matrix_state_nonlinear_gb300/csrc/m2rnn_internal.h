@@ -104,14 +104,14 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The driver's tensor-map encoder (null when it cannot be resolved).
+EncodeTiledFn tensor_map_encoder();
+
 // fp32 SIMT path (any 1 <= K, V <= 128).
 cudaError_t launch_fwd_f32(const Problem& p, cudaStream_t stream);
 
 // bf16 warp-MMA path: K % 16 == 0, K <= 128, V in {16, 32, 64, 128}.
 bool mma_rowwarp_supports(int K, int V);
-// The driver's tensor-map encoder (null when it cannot be resolved).
-EncodeTiledFn tensor_map_encoder();
-
 cudaError_t launch_fwd_bf16_mma_rowwarp(const Problem& p, EncodeTiledFn enc, cudaStream_t stream);
 
 // bf16 software-pipelined warp-MMA path with a producer warp: K % 16 == 0,

@@ -118,9 +118,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
                : "memory");
 }
 
-// A whole warp waits for the phase of `bar` with the given parity; false, for every lane, where the
-// wait ran out or another warp has given up.
-// The wait in full: one copy for all the warps' programs, which compete for the instruction cache.
+// warp_wait in full: one copy for all the warps' programs, which compete for the instruction cache.
 static __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volatile int* abort) {
   const uint32_t start = (uint32_t)clock();
   uint32_t done;
@@ -136,6 +134,8 @@ static __device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity
   } while (!done);
   return __all_sync(~0u, done != 0);
 }
+// A whole warp waits for the phase of `bar` with the given parity; false, for every lane, where the
+// wait ran out or another warp has given up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
   return warp_wait_long(smem_u32(bar), parity, abort);

@@ -219,10 +219,9 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t u) {
   return make_float2(bf16_lo(u), bf16_hi(u));
 }
 
-// m16n8k16 bf16 MMA on an accumulator held as two float2 (rows g and g + 8).
-// 1 / (1 + e^-x) of two values: relative error a few 2^-22 (one exponential and one reciprocal
-// unit operation each, results below 2^-126 flushed to zero; the plain intrinsics spend four
-// more operations on those).
+// 1 / (1 + e^-x) of two values, one exponential and one reciprocal unit operation each.  Relative
+// error at most about (2 + |x| / 3) 2^-22: the units' own, and for negative x the rounding of
+// x log2(e) in the exponent.  Results below 2^-126 are flushed to zero.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
   const float2 s = mul2(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
   float2 e, r;
@@ -234,6 +233,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 x) {
   return r;
 }
 
+// m16n8k16 bf16 MMA on an accumulator held as two float2 (rows g and g + 8).
 __device__ __forceinline__ void mma2(float2 (&d)[2], const uint32_t (&a)[4], uint32_t b0,
                                      uint32_t b1) {
   asm volatile(
