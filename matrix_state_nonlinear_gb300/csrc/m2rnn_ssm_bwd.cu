@@ -11,8 +11,10 @@
 //   r_u = exp(c_u) (q_u H) . dy_u,   l_s = w_s (k_s G) . v_s,
 //   g_t = dL/dlog f_t = exp(c_127) <G, H> + sum_{u >= t} r_u + sum_{s < t} l_s + sum_{u >= t > s} E_us
 //   da = sigmoid (l + sum_u E_us + E_ss) / d - alpha sigmoid g,   dalpha = -sum d g,   dbeta = sum da
-// g sums what passes token t, from the states and tokens before it to those after.  The last sum is
-// sum_{s < t} (column sum s - row sum s): only E itself, float32 and the same in both, cancels.
+// g sums what passes token t, from the states and tokens before it to those after, and nothing else: every
+// term has f_t in it.  (The last sum is also that of column s less row s over s < t, at 24 us less of 846.
+// But what cancels there leaves 2^-24 of the chunk's larger E at the tokens that forget everything, where d
+// is large: dalpha, which weighs g by d, was up to 2^-12 of its terms off.)
 //
 // Precision: dq, dk, dv are bf16, and one operand of each of their products is rounded to bf16 (P,
 // dS, exp(c) dy, w v); H and G enter as two bf16 values each.  The gate's gradient ends in float32
@@ -50,8 +52,14 @@ struct alignas(16) BackwardGates {
 };
 static_assert(sizeof(BackwardGates) % 16 == 0, "");
 
-struct alignas(16) Sums {  // of a head's chunk, per token; parts by column group or quarter
-  float row[4][L], row_state[4][L], col[4][L], col_state[4][L], diag[L];
+// Sums over a head's chunk, per token; parts by column group or quarter.
+struct alignas(16) Sums {
+  float row[4][L];   // E of a row over the blocks before its own
+  float first[L];    // and over the first 16 columns of its own
+  float col[4][L];   // E of a column over the rows of a later block; [its own block]: E over the pairs of the
+                     // column's piece of 16 and block that its token separates
+  float own[L];      // E of a column over the rows of its own block, its own included
+  float row_state[4][L], col_state[4][L];
 };
 
 template <int KP>
@@ -65,7 +73,7 @@ struct Smem {
   static constexpr int kGates = kDs + 2 * kTile;
   static constexpr int kSums = kGates + 2 * (int)sizeof(BackwardGates);
   static constexpr int kWr = kSums + (int)sizeof(Sums);
-  static constexpr int kBars = kWr + 16 * 16 * 4;
+  static constexpr int kBars = kWr + 4 * 16 * 4;
   static constexpr int kBytes = kBars + 256 + 1024;  // and slack to align the tiles
   static_assert(kBytes <= 227 * 1024 && kWr % 16 == 0, "");
 };
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   BackwardGates* gates = reinterpret_cast<BackwardGates*>(smem + S::kGates);
   Sums& sums = *reinterpret_cast<Sums*>(smem + S::kSums);
   Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
-  float (*wr)[16] = reinterpret_cast<float (*)[16]>(smem + S::kWr);  // w_r, 16 columns per warp
+  float (*wr)[16] = reinterpret_cast<float (*)[16]>(smem + S::kWr);  // w_r, 16 columns per group of warps
   volatile int* abort = &bar.abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t plane = (size_t)p.K * p.V;
@@ -195,7 +203,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool sent_all = false;  // the step before sent dq and dk too
     for (int j = 0; more; ++j) {
       const int v0 = at.vt * VT, vw = min(VT, p.V - v0);
-      if (at.vt == 0 && at.head_no > 0) wait(bar.sums_free, at.head_no - 1);
       if (j > 0) wait(bar.done, j - 1);         // (the scaled operand's place is read no more,
       if (sent_all) wait(bar.out_free, j - 1);  // nor does dk leave through it)
       wait(bar.gate[j & 1], j >> 1);
@@ -232,10 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P and dS from S and dP, 16 columns at a time: pieces `group` and 7 - group of eight, so that
       // no warp of a quarter has both of the masked ones.
       if (j > 0 && !sent_all) wait(bar.out_free, j - 1);  // (the places of P and dS)
+      if (at.vt == 0 && at.head_no > 0) wait(bar.sums_free, at.head_no - 1);
       if (!wait(bar.s, j)) break;
       tc_fence_after();
       {
-        float rows = 0.f, diag = 0.f;
+        float rows = 0.f;
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
           const int piece = x ? 7 - group : group, block = piece >> 1, ch = 2 * (piece & 3);
@@ -295,15 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 ev = mul2(pv, d);
             po[z] = pack_bf16x2(pv.x, pv.y);
             so[z] = pack_bf16x2(sv.x, sv.y);
-            if (block == quarter) {
-              diag = 2 * z == own ? ev.x : 2 * z + 1 == own ? ev.y : diag;
-              ev.x = 2 * z == own ? 0.f : ev.x;
-              ev.y = 2 * z + 1 == own ? 0.f : ev.y;
-            }
             sum = add2(sum, ev);
             sc[2 * z] = ev.x, sc[2 * z + 1] = ev.y;
           }
-          rows += sum.x + sum.y;
           // Column sums over the warp's 32 rows: E through this piece's own place in the tiles of P
           // (columns 0 .. 7) and dS, read back four columns and four rows per lane, then across
           // eight lanes.
@@ -313,24 +315,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                          make_uint4(__float_as_uint(sc[4 * c]), __float_as_uint(sc[4 * c + 1]),
                                     __float_as_uint(sc[4 * c + 2]), __float_as_uint(sc[4 * c + 3])));
           __syncwarp();
-          float2 a01 = make_float2(0.f, 0.f), a23 = a01;
+          const bool up = lane & 16, mid = lane & 8;
+          // To the lanes without bit 2 of each column's four.
+          auto to_columns = [&](float* to, float2 a01, float2 a23) {
+            float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
+            k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
+            k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
+            float k = mid ? k1 : k0;
+            k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
+            k += __shfl_xor_sync(~0u, k, 4);
+            to += 16 * piece + 4 * (lane & 3) + (up ? 2 : 0) + (mid ? 1 : 0);
+            if (!(lane & 4)) *to = at.vt ? *to + k : k;
+          };
+          float2 a01 = make_float2(0.f, 0.f), a23 = a01, b01 = a01, b23 = a01;
           const uint32_t from = lane & 2 ? ts : tp;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const uint4 q = ld_shared_v4(tile_at(from, 32 * quarter + (lane >> 2) + 8 * r, ch + (lane & 1)));
-            a01 = add2(a01, make_float2(__uint_as_float(q.x), __uint_as_float(q.y)));
-            a23 = add2(a23, make_float2(__uint_as_float(q.z), __uint_as_float(q.w)));
+            const int u = (lane >> 2) + 8 * r;
+            const uint4 q = ld_shared_v4(tile_at(from, 32 * quarter + u, ch + (lane & 1)));
+            float2 e0 = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+            float2 e1 = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+            a01 = add2(a01, e0);
+            a23 = add2(a23, e1);
+            if (block == quarter) {
+              // In the rows' own block also, for column t and row u >= t, E over the piece's columns before
+              // t (u's own left out): what passes t within the piece.  At the fourth lane the row's sum.
+              const int n = u - 16 * (piece & 1) - 4 * (lane & 3);  // this lane's columns before u
+              e0.x = n > 0 ? e0.x : 0.f, e0.y = n > 1 ? e0.y : 0.f;
+              e1.x = n > 2 ? e1.x : 0.f, e1.y = n > 3 ? e1.y : 0.f;
+              const float p2 = e0.x + e0.y, p3 = p2 + e1.x;
+              float run = p3 + e1.y;
+              float x = __shfl_up_sync(~0u, run, 1, 4);
+              if (lane & 3) run += x;
+              x = __shfl_up_sync(~0u, run, 2, 4);
+              if (lane & 2) run += x;
+              x = __shfl_up_sync(~0u, run, 1, 4);
+              if ((lane & 3) == 0) x = 0.f;
+              b01.x += n >= 0 ? x : 0.f, b01.y += n >= 1 ? x + e0.x : 0.f;
+              b23.x += n >= 2 ? x + p2 : 0.f, b23.y += n >= 3 ? x + p3 : 0.f;
+              if ((lane & 3) == 3 && !(piece & 1)) {
+                float& to = sums.first[32 * quarter + u];
+                to = at.vt ? to + run : run;
+              }
+            }
           }
-          const bool up = lane & 16, mid = lane & 8;
-          float k0 = up ? a23.x : a01.x, k1 = up ? a23.y : a01.y;
-          k0 += __shfl_xor_sync(~0u, up ? a01.x : a23.x, 16);
-          k1 += __shfl_xor_sync(~0u, up ? a01.y : a23.y, 16);
-          float k = mid ? k1 : k0;
-          k += __shfl_xor_sync(~0u, mid ? k0 : k1, 8);
-          k += __shfl_xor_sync(~0u, k, 4);
-          if (!(lane & 4)) {
-            float& to = sums.col[quarter][16 * piece + 4 * (lane & 3) + (up ? 2 : 0) + (mid ? 1 : 0)];
-            to = at.vt ? to + k : k;
+          if (block == quarter) {
+            to_columns(sums.own, a01, a23);
+            to_columns(sums.col[quarter], b01, b23);
+          } else {
+            to_columns(sums.col[quarter], a01, a23);
+            rows += sum.x + sum.y;
           }
           __syncwarp();
 #pragma unroll
@@ -338,7 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(tile_at(tp, row, ch + c), make_uint4(po[4 * c], po[4 * c + 1], po[4 * c + 2], po[4 * c + 3]));
             st_shared_v4(tile_at(ts, row, ch + c), make_uint4(so[4 * c], so[4 * c + 1], so[4 * c + 2], so[4 * c + 3]));
           }
-          if (own >= 0 && own < 16) sums.diag[row] = at.vt ? sums.diag[row] + diag : diag;
         }
         float& to = sums.row[group][row];
         to = at.vt ? to + rows : rows;
@@ -411,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float r = et * (dot.x + dot.y);
         to = at.vt ? to + r : r;
       }
-      if (lane < 16) wr[warp][lane] = wl;
+      if (lane < 16) wr[group][lane] = wl;  // (every warp has read the step before's)
       put_scaled(vr, wk, bar.scaled2);
 
       // k G: its part of the column sums, and dv = P^T dy + w (k G) + w_r dy, which leaves through the
@@ -431,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         unpack8(dr[c], y);
         tmem_ready(hi, lo, a);
         const float2 w2 = make_float2(wk, wk);
-        const float4 w0 = reinterpret_cast<const float4*>(wr[warp])[2 * c];
-        const float4 w1 = reinterpret_cast<const float4*>(wr[warp])[2 * c + 1];
+        const float4 w0 = reinterpret_cast<const float4*>(wr[group])[2 * c];
+        const float4 w1 = reinterpret_cast<const float4*>(wr[group])[2 * c + 1];
         const float2 u[4] = {make_float2(w0.x, w0.y), make_float2(w0.z, w0.w), make_float2(w1.x, w1.y),
                              make_float2(w1.z, w1.w)};
 #pragma unroll
@@ -679,24 +712,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* dots = w.dots + ((size_t)pair * plan.chunks + at.chunk) * plan.vtiles * 8;
         float across = lane < plan.vtiles * 8 ? dots[lane] * exp2_approx(G.g.total()) : 0.f;  // at most 16 parts
         if (!wait(bar.sums, at.head_no)) break;
-        // Tokens 4 lane .. 4 lane + 3: r, l + (column - row sum of E), and da's own sum.
+        // Tokens 4 lane .. 4 lane + 3: r, l, da's own sum, and `pass`, E over all pairs that the token
+        // separates: later one in a later block, by column (in the loop); both in its block's 16 columns, as
+        // summed above; later one in its block, earlier one before these columns, by row.
         auto add = [](float4 a, const float* p, int lane) {
           const float4 b = reinterpret_cast<const float4*>(p)[lane];
           return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
         };
         const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 r = zero, l = zero, row = zero, col = zero;
         const int block = lane >> 3;  // of 32 tokens
+        float4 r = zero, l = zero, full = add(zero, sums.own, lane), a = zero;
+        float4 pass = add(zero, sums.col[block], lane);
+        const float4 b = lane & 4 ? add(zero, sums.first, lane) : zero;
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           r = add(r, sums.row_state[i], lane);
           l = add(l, sums.col_state[i], lane);
-          row = add(row, sums.row[i], lane);
-          if (i >= block) col = add(col, sums.col[i], lane);
+          a = add(a, sums.row[i], lane);
+          const float4 c = i > block ? add(zero, sums.col[i], lane) : zero;
+          const float c1 = c.x + c.y, c2 = c1 + c.z;
+          float left = c2 + c.w;
+#pragma unroll
+          for (int s = 1; s < 32; s <<= 1) {
+            const float x = __shfl_up_sync(~0u, left, s);
+            if (lane >= s) left += x;
+          }
+          left = __shfl_up_sync(~0u, left, 1);
+          if (i > block) {
+            if (lane == 0) left = 0.f;
+            full = make_float4(full.x + c.x, full.y + c.y, full.z + c.z, full.w + c.w);
+            pass = make_float4(pass.x + left, pass.y + (left + c.x), pass.z + (left + c1), pass.w + (left + c2));
+          }
         }
-        float4 full = add(make_float4(l.x + col.x, l.y + col.y, l.z + col.z, l.w + col.w), sums.diag, lane);
         warp_arrive(&bar.sums_free, lane);
-        l = make_float4(l.x + (col.x - row.x), l.y + (col.y - row.y), l.z + (col.z - row.z), l.w + (col.w - row.w));
+        full = make_float4(full.x + l.x, full.y + l.y, full.z + l.z, full.w + l.w);
+        {
+          a.z += a.w, a.y += a.z, a.x += a.y;
+          const float b2 = b.z + b.w, b1 = b.y + b2;
+          float ra = a.x, rb = b.x + b1;  // over the block's lanes from this one on
+#pragma unroll
+          for (int s = 1; s < 8; s <<= 1) {
+            const float x = __shfl_down_sync(~0u, ra, s, 8), y = __shfl_down_sync(~0u, rb, s, 8);
+            if ((lane & 7) + s < 8) ra += x, rb += y;
+          }
+          ra = __shfl_down_sync(~0u, ra, 1, 8), rb = __shfl_down_sync(~0u, rb, 1, 8);
+          if ((lane & 7) == 7) ra = rb = 0.f;
+          if (!(lane & 4)) rb = 0.f;  // (tokens of the first 16 columns)
+          const float rest = ra + rb;
+          pass = make_float4(pass.x + (a.x + (b.x + b1) + rest), pass.y + (a.y + b1 + rest), pass.z + (a.z + b2 + rest),
+                             pass.w + (a.w + b.w + rest));
+        }
         // Sums of r over this token and the later ones, of l over the earlier ones.
         r.z += r.w, r.y += r.z, r.x += r.y;
         const float l1 = l.x + l.y, l2 = l1 + l.z;
@@ -711,8 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         after = __shfl_down_sync(~0u, after, 1), before = __shfl_up_sync(~0u, before, 1);
         if (lane == 31) after = 0.f;
         if (lane == 0) before = 0.f;
-        const float4 g = make_float4(across + (after + r.x) + before, across + (after + r.y) + (before + l.x),
-                                     across + (after + r.z) + (before + l1), across + (after + r.w) + (before + l2));
+        const float4 g = make_float4(across + (after + r.x) + before + pass.x, across + (after + r.y) + (before + l.x) + pass.y,
+                                     across + (after + r.z) + (before + l1) + pass.z,
+                                     across + (after + r.w) + (before + l2) + pass.w);
         const float4 da = make_float4(rho.x * full.x - asig.x * g.x, rho.y * full.y - asig.y * g.y,
                                       rho.z * full.z - asig.z * g.z, rho.w * full.w - asig.w * g.w);
         // (tokens past the sequence: d = 0, and every sum of theirs)

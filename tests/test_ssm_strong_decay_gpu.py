@@ -97,3 +97,18 @@ def test_inert_and_resetting_tokens_gate_gradients():
     s["a"][:, 64] = s["a"][:, 100] = 200.0
     s["k"][:, 64] = s["k"][:, 100] = 0
     check_backward(s, rand((1, 150, 2, 64), 71))
+
+
+@pytest.mark.parametrize("shape", [(2, 128, 8, 1, 128, 24), (1, 85, 16, 16, 64, 64), (1, 400, 6, 2, 40, 72)])
+@pytest.mark.parametrize("alpha", [0.5, 1.0, 2.0])
+def test_large_steps_among_small_ones(shape, alpha):
+    """d from 0 to 35, so that what a chunk's slow tokens leave in a sum would count many times over at its
+    fast ones, whose own gradient of log f is next to nothing.  dalpha weighs that gradient by d."""
+    B, T, N, _, _, V = shape
+    s = scan_case(*shape, seed=230, h0=False)
+    s.update({n: s[n].abs() for n in ("q", "k", "v")})
+    s["a"] = (10.0 + 8.0 * rand((B, T, N), 231, 1.0, torch.float32)).to(BF16)
+    s["alpha"], s["beta"] = torch.full_like(s["alpha"], alpha), torch.zeros_like(s["beta"])
+    check_forward(s, *pkg.ssm_forward(s))
+    check_backward(s, rand((B, T, N, V), 232))
+    check_backward(s, rand((B, T, N, V), 233).abs())
