@@ -3,8 +3,10 @@ gated norm, projection; as a prompt, as single tokens that continue it, and as a
 
     python examples/ssm_block.py
 
-Between the projections (plain matrix products) nothing is copied: the convolution reads a slice
-of the input projection, the scan slices of the convolution's output.
+Between the projections (plain matrix products) the convolution reads a slice of the input projection
+and the scan of a prompt slices of the convolution's output, without copies.  What the operators take
+dense is copied: the norm's gate, a single token's v, k, q and a, and, in training, dv, dk and dq side
+by side for the convolution's backward.
 """
 from __future__ import annotations
 

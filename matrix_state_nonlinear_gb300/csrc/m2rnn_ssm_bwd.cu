@@ -12,9 +12,9 @@
 //   g_t = dL/dlog f_t = exp(c_127) <G, H> + sum_{u >= t} r_u + sum_{s < t} l_s + sum_{u >= t > s} E_us
 //   da = sigmoid (l + sum_u E_us + E_ss) / d - alpha sigmoid g,   dalpha = -sum d g,   dbeta = sum da
 // g sums what passes token t, from the states and tokens before it to those after, and nothing else: every
-// term has f_t in it.  (The last sum is also that of column s less row s over s < t, at 24 us less of 846.
-// But what cancels there leaves 2^-24 of the chunk's larger E at the tokens that forget everything, where d
-// is large: dalpha, which weighs g by d, was up to 2^-12 of its terms off.)
+// term has f_t in it.  (The last sum is also that of column s less row s over s < t, 31 us cheaper for the
+// step below.  But what cancels there leaves 2^-24 of the chunk's larger E at the tokens that forget
+// everything, where d is large: dalpha, which weighs g by d, was up to 2^-12 of its terms off.)
 //
 // Precision: dq, dk, dv are bf16, and one operand of each of their products is rounded to bf16 (P,
 // dS, exp(c) dy, w v); H and G enter as two bf16 values each.  The gate's gradient ends in float32
@@ -29,8 +29,8 @@
 // Sixteen warps do each phase together (a row, i.e. token, per lane; 16 or 32 columns per warp),
 // four others issue products, load, store, and finish the gate's gradient.  K = 128 fills tensor memory
 // (S, dP, dq, dk) and shared memory, so a step's phases follow one another and that chain is what
-// bounds it: 378 us for 4 x 8192 tokens of 32 heads on one q and k, K = 128, V = 64 (13600 cycles a step,
-// the tensor cores busy 30 %), 34 us for 4 x 2048 of 8 heads, K = V = 64.  A small launch before
+// bounds it: 423 us for 4 x 8192 tokens of 32 heads on one q and k, K = 128, V = 64 (15100 cycles a step,
+// the tensor cores busy 27 %), 37 us for 4 x 2048 of 8 heads, K = V = 64.  A small launch before
 // computes every chunk's gates, and outputs leave through shared memory, whole rows at a time.
 #include "m2rnn_ssm_tc.cuh"
 

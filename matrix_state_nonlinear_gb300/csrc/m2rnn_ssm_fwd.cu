@@ -25,15 +25,16 @@
 //    8192 tokens and 32 heads).  y leaves through v's place.
 //  * The warps run five different programs, together near the instruction cache's size, so each is
 //    kept short: waits that do not succeed at once share one function, loads have one site each, and
-//    P's loop of four is unrolled by two (240 us for 8 x 16384; by one 247, by four 287).
+//    P's loop of four is unrolled by two (246 us for 8 x 16384; by one 256, by four, before the weights were taken
+//    by block, 287 instead of 240).
 // Where the pairs are fewer than the SMs, segments of a sequence run side by side
 // (m2rnn_ssm_state.cu).
-// Measured: 240 us for 8 x 16384 tokens of 16 heads, K = V = 64 (4.5 TB/s, 66 % of a copy), 239 us for
-// 65536 tokens of 16 heads, V = 128, after their segments' states, 150 us for 4 x 8192 tokens of 32
-// heads, K = 128.  Bound by instruction issue (58 % of the slots; a chunk is 9700 warp instructions,
-// about 3700 cycles with K = 64): S has to be decayed and v weighted element by element.  Weighing v in
-// the state's warps took 287 us or more instead of 264, in four of the eight warps 290 instead of 282
-// (8 x 16384, before the loops were unrolled).
+// Measured: 246 us for 8 x 16384 tokens of 16 heads, K = V = 64 (4.4 TB/s, 65 % of a copy), 244 us for
+// 65536 tokens of 16 heads, V = 128, after their segments' states, 152 us for 4 x 8192 tokens of 32
+// heads, K = 128.  A chunk is 8700 warp instructions and about 3800 cycles with K = 64; they issue in 58 %
+// of the slots.  The warps of P bound it, which decay S and weigh v element by element, and the waits
+// between roles.  Weighing v in the state's warps took 287 us or more instead of 264, in four of the eight
+// warps 290 instead of 282 (8 x 16384, before the loops were unrolled).
 #include "m2rnn_ssm_tc.cuh"
 
 namespace m2rnn {
