@@ -457,6 +457,86 @@ m2rnn_status m2rnn_gate_groupnorm_backward(const void* y, int y_f32, const uint1
                                            int groups, void* workspace, size_t workspace_bytes,
                                            void* stream);
 
+/*
+ * What stands around a block in a stack: the residual's addition with the RMS norm in front of a
+ * block, the projections in 8 bits, and the clipping of a training step's gradients.
+ *
+ * Residual RMS norm.  Each of `rows` rows of D channels:
+ *   h = stream_in + x  (rounded to the stream's type; x NULL: h = stream_in)
+ *   out = h / sqrt(mean(h^2) + eps) ⊙ w
+ * x bf16; stream_in and h bf16 or float32 (stream_f32 != 0); w [D] float32.  x_row and stream_row are the
+ * elements from one row to the next; h and out [rows, D] are dense.  h may be NULL without x (not written)
+ * and may be stream_in itself (in place) where that is dense.  The norm is taken of the rounded h, in
+ * float32: |h| above 1e19 overflows its square (out is 0 there).  D <= 16384 (UNSUPPORTED above).
+ * A row that holds an infinity or a NaN gives NaN, in its own row only.  Rows of D % 8 == 0 channels with
+ * 16-byte aligned pointers and rows run on 16-byte accesses.
+ * m2rnn_add_rmsnorm: out bf16.  m2rnn_add_rmsnorm_fp8: out in 8 bits (see below), q [rows, D] with q_row
+ *   bytes from row to row (q and q_row multiples of 16) and scales [rows, ceil(D / 128)], dense.
+ * m2rnn_add_rmsnorm_backward: with dout [rows, D] bf16 and dh [rows, D] of the stream's type (the gradient
+ *   that reaches h by the stream; NULL: none), g = dout ⊙ w and r = 1 / sqrt(mean(h^2) + eps):
+ *     d = dh + r g - h r^3 mean(g ⊙ h),   dw = sum over rows of dout ⊙ h r
+ *   dx (bf16) and dresidual (of the stream's type) are both d; either may be NULL, not both.  dx or
+ *   dresidual may be dh itself where the types agree.  All dense.  The workspace (16-byte aligned) holds
+ *   partial sums, added in a fixed order.
+ */
+m2rnn_status m2rnn_add_rmsnorm(const uint16_t* x, long long x_row, const void* stream_in,
+                               int stream_f32, long long stream_row, const float* w, float eps,
+                               void* h, uint16_t* out, long long rows, int D, void* stream);
+m2rnn_status m2rnn_add_rmsnorm_fp8(const uint16_t* x, long long x_row, const void* stream_in,
+                                   int stream_f32, long long stream_row, const float* w, float eps,
+                                   void* h, uint8_t* q, long long q_row, uint8_t* scales,
+                                   long long rows, int D, void* stream);
+size_t m2rnn_add_rmsnorm_backward_workspace_bytes(long long rows, int D);
+m2rnn_status m2rnn_add_rmsnorm_backward(const void* h, int stream_f32, const float* w, float eps,
+                                        const uint16_t* dout, const void* dh, uint16_t* dx,
+                                        void* dresidual, float* dw, long long rows, int D,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 8 bits: e4m3 values q and, for each 128 consecutive values of a row (the last block may be shorter), one
+ * scale s, a power of two kept as its exponent plus 127 in a byte (e8m0); a value stands for q s.  s is the
+ * least power of two with max |value| / s <= 448, 2^-126 at the least; q is value / s rounded to the
+ * nearest, ties to even.  A block that holds an infinity or a NaN gets the scale NaN (255) and NaNs.
+ * Rows start q_row bytes apart; q and q_row are multiples of 16.  Scales are dense.
+ * m2rnn_quantise_fp8: x [rows, D] bf16 or float32 (x_f32 != 0), x_row elements from row to row ->
+ *   q [rows, D], scales [rows, ceil(D / 128)].
+ * m2rnn_quantise_weight_fp8: w [N, K], one scale for each 128 x 128 block -> q [N, K],
+ *   scales [ceil(N / 128), ceil(K / 128)].
+ * m2rnn_linear_fp8: out[m, n] = sum_k x[m, k] w[n, k] of such values, x [M, K] with a scale for each 128
+ *   of a row, w [N, K] with one for each 128 x 128 block; out [M, N] bf16 or float32 (out_f32 != 0), dense.
+ *   Sums are float32 on the tensor cores.  A NaN of x spoils its row of out, one of w its column; a scale
+ *   of w that is NaN spoils the columns of its block.  N rows of out that are multiples of 16 bytes at a
+ *   16-byte aligned address are written 16 bytes at a time.
+ */
+m2rnn_status m2rnn_quantise_fp8(const void* x, int x_f32, long long x_row, uint8_t* q,
+                                long long q_row, uint8_t* scales, long long rows, int D,
+                                void* stream);
+m2rnn_status m2rnn_quantise_weight_fp8(const void* w, int w_f32, long long w_row, uint8_t* q,
+                                       long long q_row, uint8_t* scales, int N, int K,
+                                       void* stream);
+m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* x_scales,
+                              const uint8_t* w, long long w_row, const uint8_t* w_scales, void* out,
+                              int out_f32, long long M, int N, int K, void* stream);
+
+/*
+ * The global norm of `count` gradients, and their clipping:
+ *   norm = sqrt(sum of all values squared),   out[i] = grads[i] min(1, max_norm / norm)
+ * grads[i] holds values[i] values (0 is allowed), float32 (is_f32[i] != 0) or bf16, anywhere on a
+ * boundary of its type; out[i] is grads[i] itself (in place) or memory apart.  These four arrays are host
+ * memory, read during the call.  norm: one float32 on the device.  out NULL: the norm alone (max_norm is
+ * not read).  Values that hold an infinity or a NaN are not clipped: they stay as they are, and norm says
+ * so.  A norm of finite values above float32's range reads as infinite too, but does clip.
+ * INVALID_ARG where something that is written shares memory with another gradient or output, or max_norm
+ * is negative, infinite or NaN; UNSUPPORTED above 2^40 values.  Squares are summed in 64 bits above a few
+ * of them, in a fixed order, and also where they leave float32's range.  The workspace (16-byte aligned,
+ * at least m2rnn_grad_norm_workspace_bytes) is overwritten.
+ */
+size_t m2rnn_grad_norm_workspace_bytes(int count);
+m2rnn_status m2rnn_clip_grad_norm(const void* const* grads, void* const* out,
+                                  const long long* values, const unsigned char* is_f32, int count,
+                                  float max_norm, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Name of a bf16 kernel variant (NULL for an unknown id).  Id 0 is "auto". */
 const char* m2rnn_variant_name(int variant);
 

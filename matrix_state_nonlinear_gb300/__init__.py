@@ -12,3 +12,5 @@ from .m2rnn import (M2RNNError, backward_workspace_bytes, conv_silu, gate_rmsnor
 from .ssm import (conv_silu_backward, conv_silu_step, conv_silu_window, gate_groupnorm,  # noqa: F401
                   gate_groupnorm_backward, ssm_backward, ssm_forward, ssm_forward_train,
                   ssm_states_bytes, ssm_step, ssm_workspace_bytes)
+from .layer import (add_rmsnorm, add_rmsnorm_backward, add_rmsnorm_fp8, clip_grad_norm,  # noqa: F401
+                    grad_norm, linear_fp8, quantise_fp8, quantise_weight_fp8)

@@ -1,0 +1,373 @@
+// m2rnn_addnorm.cu — the residual's addition with the RMS norm in front of a block, its 8-bit form and
+// its backward.
+//
+//   h = stream + x (rounded to the stream's type),  inv = 1 / sqrt(mean(h^2) + eps),  out = h inv w
+// Backward, with g = dout w and dh the gradient that arrives at h from behind:
+//   d = dh + inv g - h inv^3 mean(g h)  (dx and dresidual),  dw = sum over rows of dout h inv
+//
+// Memory-bound.  A block takes one row, held in registers in chunks of 8 channels per thread, so that
+// every input is read once; the norm is taken of h as the stream's type holds it, which is what the
+// next layer and the backward read.  In 8 bits, 16 neighbouring threads hold the 128 channels of a scale.
+#include "m2rnn_layer.h"
+#include "ptx_util.cuh"
+
+namespace m2rnn {
+namespace {
+
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+
+// Eight values as loaded, so that a load can be started ahead of its use.  Without VEC they lie at any
+// address and `n` of them exist; the others are zero.
+template <typename T, bool VEC>
+struct Raw8 {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4)
+          v[i] = i < n ? __float_as_uint(p[i]) : 0u;
+        else
+          v[i] = i < n ? p[i] : 0u;
+      }
+      if constexpr (sizeof(T) == 4) {
+        u[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        u[sizeof(T) / 2 - 1] = make_uint4(v[4], v[5], v[6], v[7]);
+      } else {
+        u[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[2 * i] = make_float2(__uint_as_float(u[i].x), __uint_as_float(u[i].y));
+        f[2 * i + 1] = make_float2(__uint_as_float(u[i].z), __uint_as_float(u[i].w));
+      }
+    } else {
+      f[0] = bf16x2_to_float2(u[0].x), f[1] = bf16x2_to_float2(u[0].y);
+      f[2] = bf16x2_to_float2(u[0].z), f[3] = bf16x2_to_float2(u[0].w);
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[4]) {  // rounded to T
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        u[i] = make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y), __float_as_uint(f[2 * i + 1].x),
+                          __float_as_uint(f[2 * i + 1].y));
+    } else {
+      u[0] = make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                        pack_bf16x2(f[3].x, f[3].y));
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int n) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+    } else {
+      const uint4 a = u[0], b = u[sizeof(T) / 2 - 1];
+      const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          if (i < n) p[i] = __uint_as_float(v[i]);
+        } else {
+          if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+        }
+      }
+    }
+  }
+};
+
+// Sums of two values over the block, for every thread.  `turn` (0, 1, 0, ...) chooses the scratch, so that
+// one barrier a sum is enough.
+__device__ __forceinline__ float2 block_sum(float2 s, int turn) {
+  __shared__ float2 part[2][16];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    s = add2(s, make_float2(__shfl_xor_sync(~0u, s.x, o), __shfl_xor_sync(~0u, s.y, o)));
+  const int warps = blockDim.x >> 5;
+  if (warps > 1) {
+    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = part[turn][0];
+    for (int w = 1; w < warps; ++w) s = add2(s, part[turn][w]);
+  }
+  return s;
+}
+
+// Channels of chunk c.
+__device__ __forceinline__ int chunk_width(int c, int D) { return min(8, D - 8 * c); }
+
+template <typename T, bool FP8, bool VEC, int R>
+__global__ void __launch_bounds__(512)
+    add_rmsnorm_kernel(AddNormProblem p, uint16_t* __restrict__ out, uint8_t* __restrict__ q, long long q_row,
+                       uint8_t* __restrict__ scales) {
+  const int T_ = blockDim.x, chunks = (p.D + 7) / 8;
+  const float inv_d = 1.f / (float)p.D;
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const T* stream = static_cast<const T*>(p.stream) + row * p.stream_row;
+    const uint16_t* x = p.x ? p.x + row * p.x_row : nullptr;
+    float2 h[R][4], s = pair(0.f);
+    Raw8<T, VEC> a[R];
+    Raw8<uint16_t, VEC> b[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = threadIdx.x + r * T_;
+      if (c < chunks) {
+        a[r].load(stream + 8 * c, chunk_width(c, p.D));
+        if (x) b[r].load(x + 8 * c, chunk_width(c, p.D));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = threadIdx.x + r * T_;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[r][i] = pair(0.f);
+      if (c < chunks) {
+        a[r].get(h[r]);
+        if (x) {
+          float2 v[4];
+          b[r].get(v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[r][i] = add2(h[r][i], v[i]);
+          a[r].set(h[r]);
+          if (sizeof(T) == 2) a[r].get(h[r]);
+        }
+        if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D + 8 * c, chunk_width(c, p.D));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fma2(h[r][i], h[r][i], s);
+    }
+    const float inv = rsqrtf(block_sum(make_float2(s.x + s.y, 0.f), turn).x * inv_d + p.eps);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = threadIdx.x + r * T_;
+      if (c < chunks) {
+        Raw8<float, VEC> u;
+        float2 w[4];
+        u.load(p.w + 8 * c, chunk_width(c, p.D));
+        u.get(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[r][i] = mul2(mul2(h[r][i], pair(inv)), w[i]);
+      }
+      if constexpr (FP8) {
+        uint32_t top = 0;  // of |values| as bits, which order them and put NaN above all
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = max(top, max(__float_as_uint(h[r][i].x) & 0x7fffffffu, __float_as_uint(h[r][i].y) & 0x7fffffffu));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+        const uint32_t e = scale_exponent(top);
+        const float2 by = pair(inverse_scale(e));
+        if (c < chunks && (c & 15) == 0) scales[row * scale_blocks(p.D) + (c >> 4)] = (uint8_t)e;
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = mul2(h[r][i], by);
+          v[i] = pack_e4m3x2(y.x, y.y);
+        }
+        const uint2 u = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+        uint8_t* to = q + row * q_row + 8 * c;
+        const int n = chunk_width(c, p.D);  // none or fewer behind the last chunk
+        if (VEC ? c < chunks : n == 8) {
+          *reinterpret_cast<uint2*>(to) = u;
+        } else if (!VEC) {
+#pragma unroll
+          for (int i = 0; i < 7; ++i)
+            if (i < n) to[i] = (uint8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
+        }
+      } else if (c < chunks) {
+        Raw8<uint16_t, VEC> o;
+        o.set(h[r]);
+        o.store(out + row * p.D + 8 * c, chunk_width(c, p.D));
+      }
+    }
+  }
+}
+
+// Block b takes rows b, + blocks, ..., the next row loaded while one is computed; its channels' part of dw
+// adds up in registers and goes to row b of `part`.
+template <typename T, bool VEC, int R>
+__global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(AddNormBackwardProblem p, float* __restrict__ part) {
+  const int T_ = blockDim.x, chunks = (p.D + 7) / 8;
+  const float inv_d = 1.f / (float)p.D;
+  float2 dw[R][4], w[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int c = threadIdx.x + r * T_;
+    Raw8<float, VEC> u;
+    if (c < chunks) u.load(p.w + 8 * c, chunk_width(c, p.D)), u.get(w[r]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dw[r][i] = pair(0.f);
+      if (c >= chunks) w[r][i] = pair(0.f);
+    }
+  }
+  Raw8<T, VEC> hr[R], er[R];
+  Raw8<uint16_t, VEC> dr[R];
+  auto load = [&](long long row) {
+    if (row >= p.rows) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = threadIdx.x + r * T_;
+      if (c < chunks) {
+        const long long at = row * p.D + 8 * c;
+        const int n = chunk_width(c, p.D);
+        hr[r].load(static_cast<const T*>(p.h) + at, n);
+        dr[r].load(p.dout + at, n);
+        if (p.dh) er[r].load(static_cast<const T*>(p.dh) + at, n);
+      }
+    }
+  };
+  load(blockIdx.x);
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    float2 h[R][4], d[R][4], e[R][4], s1 = pair(0.f), s2 = pair(0.f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[r][i] = d[r][i] = e[r][i] = pair(0.f);
+      if (threadIdx.x + r * T_ < chunks) {
+        hr[r].get(h[r]);
+        dr[r].get(d[r]);
+        if (p.dh) er[r].get(e[r]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s1 = fma2(h[r][i], h[r][i], s1);
+        s2 = fma2(mul2(d[r][i], w[r][i]), h[r][i], s2);
+      }
+    }
+    load(row + gridDim.x);
+    const float2 sum = block_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
+    const float inv = rsqrtf(sum.x * inv_d + p.eps);
+    const float2 iv = pair(inv), back = pair(-inv * inv * inv * (sum.y * inv_d));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int c = threadIdx.x + r * T_;
+      const int n = chunk_width(c, p.D);
+      const long long at = row * p.D + 8 * c;
+      float2 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dw[r][i] = fma2(d[r][i], mul2(h[r][i], iv), dw[r][i]);
+        o[i] = add2(fma2(h[r][i], back, mul2(mul2(d[r][i], w[r][i]), iv)), e[r][i]);
+      }
+      if (c < chunks && p.dx) {
+        Raw8<uint16_t, VEC> u;
+        u.set(o);
+        u.store(p.dx + at, n);
+      }
+      if (c < chunks && p.dresidual) {
+        Raw8<T, VEC> u;
+        u.set(o);
+        u.store(static_cast<T*>(p.dresidual) + at, n);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int c = threadIdx.x + r * T_;
+    Raw8<float, VEC> u;
+    u.set(dw[r]);
+    if (c < chunks) u.store(part + (long long)blockIdx.x * p.D + 8 * c, chunk_width(c, p.D));
+  }
+}
+
+// Threads of a row's block for R chunks per thread.
+int threads_for(int D, int R) {
+  const int chunks = (D + 7) / 8;
+  return ((chunks + R - 1) / R + 31) / 32 * 32;
+}
+// Chunks per thread, the fewest from `least` on whose block has at most 512 threads.
+int chunks_each(int D, int least) {
+  int R = least;
+  while (threads_for(D, R) > 512) R *= 2;
+  return R;
+}
+
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+template <typename F>
+cudaError_t with_chunks(int R, F f) {
+  return R == 1 ? f(Int<1>{}) : R == 2 ? f(Int<2>{}) : f(Int<4>{});
+}
+
+template <typename T, bool FP8, bool VEC>
+cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
+                    cudaStream_t stream) {
+  const int R = chunks_each(p.D, p.rows >= 152 * 16 ? 4 : 1);
+  return with_chunks(R, [&](auto r) {
+    constexpr int N = decltype(r)::value;
+    const unsigned blocks = (unsigned)(p.rows < 0x7fffffff ? p.rows : 0x7fffffff);
+    add_rmsnorm_kernel<T, FP8, VEC, N><<<blocks, threads_for(p.D, N), 0, stream>>>(p, out, q, q_row, scales);
+    return cudaGetLastError();
+  });
+}
+
+bool rows_of_8(const void* p, long long row, size_t size) { return aligned_to(p, 16) && row * size % 16 == 0; }
+
+bool vec_ok(const AddNormProblem& p) {
+  const size_t size = p.stream_f32 ? 4 : 2;
+  return p.D % 8 == 0 && aligned_to(p.w, 16) && rows_of_8(p.stream, p.stream_row, size) &&
+         (!p.x || rows_of_8(p.x, p.x_row, 2)) && aligned_to(p.h, 16);
+}
+
+template <bool FP8>
+cudaError_t dispatch(const AddNormProblem& p, bool vec, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
+                     cudaStream_t stream) {
+  if (p.stream_f32)
+    return vec ? forward<float, FP8, true>(p, out, q, q_row, scales, stream)
+               : forward<float, FP8, false>(p, out, q, q_row, scales, stream);
+  return vec ? forward<uint16_t, FP8, true>(p, out, q, q_row, scales, stream)
+             : forward<uint16_t, FP8, false>(p, out, q, q_row, scales, stream);
+}
+
+int backward_blocks(long long rows, int D) {
+  const long long most = 152LL * 4;
+  (void)D;
+  return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const AddNormProblem& p, uint16_t* out, cudaStream_t stream) {
+  return dispatch<false>(p, vec_ok(p) && aligned_to(out, 16), out, nullptr, 0, nullptr, stream);
+}
+cudaError_t launch_add_rmsnorm_fp8(const AddNormProblem& p, uint8_t* q, long long q_row, uint8_t* scales,
+                                   cudaStream_t stream) {
+  return dispatch<true>(p, vec_ok(p), nullptr, q, q_row, scales, stream);
+}
+
+size_t add_rmsnorm_backward_workspace_floats(long long rows, int D) { return (size_t)backward_blocks(rows, D) * D; }
+
+cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStream_t stream) {
+  if (p.rows == 0) return cudaMemsetAsync(p.dw, 0, sizeof(float) * p.D, stream);
+  const bool vec = p.D % 8 == 0 && aligned_to(p.w, 16) && aligned_to(p.h, 16) && aligned_to(p.dout, 16) &&
+                   aligned_to(p.dh, 16) && aligned_to(p.dx, 16) && aligned_to(p.dresidual, 16);
+  const int blocks = backward_blocks(p.rows, p.D);
+  const cudaError_t err = with_chunks(chunks_each(p.D, 1), [&](auto r) {
+    constexpr int R = decltype(r)::value;
+    auto go = [&](auto kernel) {
+      kernel<<<blocks, threads_for(p.D, R), 0, stream>>>(p, p.ws);
+      return cudaGetLastError();
+    };
+    if (p.stream_f32)
+      return vec ? go(add_rmsnorm_backward_kernel<float, true, R>) : go(add_rmsnorm_backward_kernel<float, false, R>);
+    return vec ? go(add_rmsnorm_backward_kernel<uint16_t, true, R>)
+               : go(add_rmsnorm_backward_kernel<uint16_t, false, R>);
+  });
+  if (err != cudaSuccess) return err;
+  return launch_sum_rows(p.ws, p.dw, nullptr, blocks, p.D, p.D, p.D, stream);
+}
+
+}  // namespace m2rnn

@@ -1,0 +1,283 @@
+"""Binding of what stands around a block in a stack: the residual's addition with its RMS norm, the
+projections in 8 bits, and the clipping of a step's gradients (see include/m2rnn.h for the formulas).
+
+Checks, allocation, streams and devices are as in the selective block's binding: outputs and workspaces
+are torch memory, made when they are not given, and the calls run on the current CUDA stream unless the
+keyword ``stream`` names another.
+
+8-bit tensors are float8_e4m3fn with one float8_e8m0fnu scale (a power of two) for each 128 channels, for
+weights for each 128 x 128.  Their rows start on 16-byte boundaries; what is made here is laid out so.
+"""
+from __future__ import annotations
+
+from array import array
+
+import torch
+
+from .m2rnn import OK, load_library
+from .ssm import BF16, F32, _device, _on_stream, _ptr, _raise, _refuse, _sizes, _stream, _workspace
+
+FP8, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _rows(t, name, dtype, shape, dev):
+    """The address of a tensor [..., D] of this type and shape whose rows lie one stride apart, each
+    contiguous, and that stride in elements."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, dtype, shape, dev)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    s = t.stride()
+    if t.numel() == 0:
+        return t.data_ptr(), shape[-1]
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    row = count = None  # from row to row; rows so far
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if row is None:
+            row, count = s[i], shape[i]
+        elif s[i] == row * count:
+            count *= shape[i]
+        else:
+            raise ValueError(f"{name}: rows must lie one stride apart")
+    return t.data_ptr(), shape[-1] if row is None else row
+
+
+def _byte_rows(t, name, shape, dev):
+    """The same for e4m3 values, whose rows start on 16-byte boundaries."""
+    p, row = _rows(t, name, FP8, shape, dev)
+    if t.numel() == shape[-1]:  # a single row: nothing lies behind it
+        row = (shape[-1] + 15) // 16 * 16
+    if p % 16 or row % 16:
+        raise ValueError(f"{name}: rows must start on 16-byte boundaries, {row} bytes apart from address {p:#x} they do not "
+                         "(the package's own 8-bit tensors do)")
+    return p, row
+
+
+def _new_bytes(like, shape):
+    """An e4m3 tensor whose rows start on 16-byte boundaries."""
+    D = shape[-1]
+    return torch.empty((*shape[:-1], (D + 15) // 16 * 16), dtype=FP8, device=like.device)[..., :D]
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+# ---------------------------------------------------------------- residual RMS norm
+def _norm_args(x, residual, w, h):
+    """Checks the norm's inputs: (h, sizes, addresses up to eps, address of h)."""
+    dev = _device(x)
+    shape = x.shape
+    D = shape[-1]
+    if residual is None:
+        if x.dtype not in (F32, BF16):
+            raise TypeError(f"x: expected {F32} or {BF16}, got {x.dtype}")
+        sp, row = _rows(x, "x", x.dtype, shape, dev)
+        args, kind, hp = (None, 0, sp, int(x.dtype is F32), row), x.dtype, None
+        if h is not None:
+            raise ValueError("h: without a residual it is x")
+        h = x
+    else:
+        kind = residual.dtype
+        if kind not in (F32, BF16):
+            raise TypeError(f"residual: expected {F32} or {BF16}, got {kind}")
+        xp, x_row = _rows(x, "x", BF16, shape, dev)
+        sp, row = _rows(residual, "residual", kind, shape, dev)
+        if h is None:
+            h = torch.empty(shape, dtype=kind, device=x.device)
+        hp = _ptr(h, "h", kind, shape, dev)
+        args = (xp, x_row, sp, int(kind is F32), row)
+    return dev, h, (x.numel() // D if D else 0, D), (*args, _ptr(w, "w", F32, (D,), dev)), hp
+
+
+@_on_stream
+def add_rmsnorm(x, residual, w, eps=1e-5, out=None, h=None):
+    """RMS norm of a residual stream: h = residual + x in the residual's type, out = h /
+    sqrt(mean(h^2) + eps) times w.  x [..., D] bf16, residual [..., D] bf16 or float32 (rows of both may lie
+    a wider stride apart), w [D] float32; residual None: h is x, bf16 or float32.  ``h`` may be the residual
+    itself (in place).  Returns (out [..., D] bf16, h)."""
+    dev, h, size, args, hp = _norm_args(x, residual, w, h)
+    if out is None:
+        out = torch.empty(x.shape, dtype=BF16, device=x.device)
+    st = load_library().m2rnn_add_rmsnorm(*args, eps, hp, _ptr(out, "out", BF16, x.shape, dev), *size, _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_add_rmsnorm")
+    return out, h
+
+
+@_on_stream
+def add_rmsnorm_fp8(x, residual, w, eps=1e-5, out=None, scales=None, h=None):
+    """``add_rmsnorm`` with its result in 8 bits, for ``linear_fp8``.  Returns (out [..., D] float8_e4m3fn,
+    scales [..., ceil(D / 128)] float8_e8m0fnu, h)."""
+    dev, h, size, args, hp = _norm_args(x, residual, w, h)
+    shape = x.shape
+    if out is None:
+        out = _new_bytes(x, shape)
+    blocks = (*shape[:-1], _blocks(shape[-1]))
+    if scales is None:
+        scales = torch.empty(blocks, dtype=E8M0, device=x.device)
+    st = load_library().m2rnn_add_rmsnorm_fp8(*args, eps, hp, *_byte_rows(out, "out", shape, dev),
+                                              _ptr(scales, "scales", E8M0, blocks, dev), *size, _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_add_rmsnorm_fp8")
+    return out, scales, h
+
+
+@_on_stream
+def add_rmsnorm_backward(h, w, dout, dh=None, eps=1e-5, grads=None, workspace=None):
+    """Gradients of ``add_rmsnorm`` from its h: dout [..., D] bf16 the gradient of out, dh (of h's type,
+    optional) the one that reaches h by the stream.  Returns a dict dx [..., D] bf16, dresidual [..., D] of h's
+    type (the same tensor as dx for a bf16 stream), dw [D] float32 (``grads`` may supply any of them
+    preallocated)."""
+    dev = _device(h)
+    shape, kind = h.shape, h.dtype
+    D = shape[-1]
+    if kind not in (F32, BF16):
+        raise TypeError(f"h: expected {F32} or {BF16}, got {kind}")
+    g = dict(grads or {})
+    if g.get("dx") is None:
+        g["dx"] = torch.empty(shape, dtype=BF16, device=h.device)
+    if g.get("dresidual") is None:
+        g["dresidual"] = g["dx"] if kind is BF16 else torch.empty(shape, dtype=kind, device=h.device)
+    if g.get("dw") is None:
+        g["dw"] = torch.empty(D, dtype=F32, device=h.device)
+    dx, dr = _ptr(g["dx"], "dx", BF16, shape, dev), _ptr(g["dresidual"], "dresidual", kind, shape, dev)
+    rows = h.numel() // D if D else 0
+    lib = load_library()
+    ws, wp, wb = _workspace(workspace, lib.m2rnn_add_rmsnorm_backward_workspace_bytes(rows, D), h)
+    st = lib.m2rnn_add_rmsnorm_backward(
+        _ptr(h, "h", kind, shape, dev), int(kind is F32), _ptr(w, "w", F32, (D,), dev), eps,
+        _ptr(dout, "dout", BF16, shape, dev), _ptr(dh, "dh", kind, shape, dev), dx, None if dr == dx else dr,
+        _ptr(g["dw"], "dw", F32, (D,), dev), rows, D, wp, wb, _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_add_rmsnorm_backward")
+    return g
+
+
+# ---------------------------------------------------------------- 8-bit projections
+def _source(x, name):
+    if x.dtype not in (F32, BF16):
+        raise TypeError(f"{name}: expected {F32} or {BF16}, got {x.dtype}")
+    return x.dtype is F32
+
+
+@_on_stream
+def quantise_fp8(x, out=None, scales=None):
+    """x [..., D] bf16 or float32 in 8 bits with a scale for each 128 channels: (out [..., D]
+    float8_e4m3fn, scales [..., ceil(D / 128)] float8_e8m0fnu)."""
+    dev, shape, f32 = _device(x), x.shape, _source(x, "x")
+    D = shape[-1]
+    _sizes(D)
+    if out is None:
+        out = _new_bytes(x, shape)
+    blocks = (*shape[:-1], _blocks(D))
+    if scales is None:
+        scales = torch.empty(blocks, dtype=E8M0, device=x.device)
+    xp, row = _rows(x, "x", x.dtype, shape, dev)
+    st = load_library().m2rnn_quantise_fp8(xp, int(f32), row, *_byte_rows(out, "out", shape, dev),
+                                           _ptr(scales, "scales", E8M0, blocks, dev), x.numel() // D if D else 0, D,
+                                           _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_quantise_fp8")
+    return out, scales
+
+
+@_on_stream
+def quantise_weight_fp8(w, out=None, scales=None):
+    """A projection's weight w [N, K] (out, in) bf16 or float32 in 8 bits with a scale for each 128 x 128:
+    (out [N, K] float8_e4m3fn, scales [ceil(N / 128), ceil(K / 128)] float8_e8m0fnu)."""
+    dev, f32 = _device(w), _source(w, "w")
+    N, K = shape = w.shape
+    _sizes(N, K)
+    if out is None:
+        out = _new_bytes(w, shape)
+    blocks = (_blocks(N), _blocks(K))
+    if scales is None:
+        scales = torch.empty(blocks, dtype=E8M0, device=w.device)
+    wp, row = _rows(w, "w", w.dtype, shape, dev)
+    st = load_library().m2rnn_quantise_weight_fp8(wp, int(f32), row, *_byte_rows(out, "out", shape, dev),
+                                                  _ptr(scales, "scales", E8M0, blocks, dev), N, K, _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_quantise_weight_fp8")
+    return out, scales
+
+
+@_on_stream
+def linear_fp8(x, x_scales, w, w_scales, out=None, out_dtype=BF16):
+    """Projection in 8 bits: out = x w^T with float32 sums.  x [..., K] and x_scales from
+    ``add_rmsnorm_fp8`` or ``quantise_fp8``, or x bf16 or float32 with x_scales None (quantised here, the same
+    values); w [N, K] and w_scales from ``quantise_weight_fp8``.  Returns out [..., N], bf16 or float32."""
+    dev = _device(x)
+    if x_scales is None:
+        x, x_scales = quantise_fp8(x)
+    shape = x.shape
+    K = shape[-1]
+    N = w.shape[0]
+    _sizes(N, K)
+    if out is None:
+        out = torch.empty((*shape[:-1], N), dtype=out_dtype, device=x.device)
+    if out.dtype not in (F32, BF16):
+        raise TypeError(f"out: expected {F32} or {BF16}, got {out.dtype}")
+    st = load_library().m2rnn_linear_fp8(
+        *_byte_rows(x, "x", shape, dev), _ptr(x_scales, "x_scales", E8M0, (*shape[:-1], _blocks(K)), dev),
+        *_byte_rows(w, "w", (N, K), dev), _ptr(w_scales, "w_scales", E8M0, (_blocks(N), _blocks(K)), dev),
+        _ptr(out, "out", out.dtype, (*shape[:-1], N), dev), int(out.dtype is F32), x.numel() // K if K else 0, N, K,
+        _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_linear_fp8")
+    return out
+
+
+# ---------------------------------------------------------------- gradients
+def _gradients(grads, out, max_norm, norm, workspace):
+    grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
+    if not grads:
+        raise ValueError("grads: at least one tensor")
+    dev = _device(grads[0])
+    n = len(grads)
+    ptrs, sizes, kinds = array("Q"), array("q"), bytearray(n)
+    for i, t in enumerate(grads):
+        kind = t.dtype
+        if kind is F32:
+            kinds[i] = 1
+        elif kind is not BF16:
+            raise TypeError(f"grads[{i}]: expected {F32} or {BF16}, got {kind}")
+        if t.get_device() != dev or not t.is_contiguous():
+            _refuse(t, f"grads[{i}]", kind, t.shape, dev)
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel())
+    to = ptrs if out is None else None
+    if out is not None and out is not False:
+        out = list(out.values()) if isinstance(out, dict) else list(out)
+        if len(out) != n:
+            raise ValueError(f"out: {len(out)} tensors for {n} gradients")
+        to = array("Q", [_ptr(o, "out", t.dtype, t.shape, dev) for o, t in zip(out, grads)])
+    if norm is None:
+        norm = torch.empty((), dtype=F32, device=grads[0].device)
+    lib = load_library()
+    ws, wp, wb = _workspace(workspace, lib.m2rnn_grad_norm_workspace_bytes(n), grads[0])
+    kinds = array("B", kinds)
+    st = lib.m2rnn_clip_grad_norm(ptrs.buffer_info()[0], None if to is None else to.buffer_info()[0],
+                                  sizes.buffer_info()[0], kinds.buffer_info()[0], n, max_norm,
+                                  _ptr(norm, "norm", F32, (), dev), wp, wb, _stream(dev))
+    if st != OK:
+        _raise(st, "m2rnn_clip_grad_norm")
+    return norm
+
+
+@_on_stream
+def grad_norm(grads, norm=None, workspace=None):
+    """The norm of all values of grads (a sequence or dict of contiguous float32 and bf16 tensors)
+    together: a float32 scalar on the device."""
+    return _gradients(grads, False, 0.0, norm, workspace)
+
+
+@_on_stream
+def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None):
+    """Scales grads (a sequence or dict of contiguous float32 and bf16 tensors, none of which share memory)
+    by min(1, max_norm / norm), in place, or into the tensors ``out``.  Returns the norm before that, a
+    float32 scalar on the device.  Where a value is infinite or NaN the norm is, and nothing is scaled."""
+    return _gradients(grads, out, max_norm, norm, workspace)
