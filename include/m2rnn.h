@@ -507,6 +507,9 @@ m2rnn_status m2rnn_add_rmsnorm_backward(const void* h, int stream_f32, const flo
  *   Sums are float32 on the tensor cores.  A NaN of x spoils its row of out, one of w its column; a scale
  *   of w that is NaN spoils the columns of its block.  N rows of out that are multiples of 16 bytes at a
  *   16-byte aligned address are written 16 bytes at a time.
+ * m2rnn_linear_quantise_fp8: the same with x [M, K] bf16 or float32 (x_f32 != 0), x_row elements from row to
+ *   row, as m2rnn_quantise_fp8 makes it 8 bits; up to 16 rows of bf16 within the product's own launch.  The
+ *   workspace (16-byte aligned; NULL where its size is 0) is overwritten.
  */
 m2rnn_status m2rnn_quantise_fp8(const void* x, int x_f32, long long x_row, uint8_t* q,
                                 long long q_row, uint8_t* scales, long long rows, int D,
@@ -517,6 +520,11 @@ m2rnn_status m2rnn_quantise_weight_fp8(const void* w, int w_f32, long long w_row
 m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* x_scales,
                               const uint8_t* w, long long w_row, const uint8_t* w_scales, void* out,
                               int out_f32, long long M, int N, int K, void* stream);
+size_t m2rnn_linear_quantise_workspace_bytes(int x_f32, long long M, int K);
+m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row, const uint8_t* w,
+                                       long long w_row, const uint8_t* w_scales, void* out,
+                                       int out_f32, long long M, int N, int K, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /*
  * The global norm of `count` gradients, and their clipping:

@@ -1,0 +1,87 @@
+// m2rnn_fp8_tc.cuh — 8-bit operands on the 5th-generation tensor cores, shared by the kernels of the
+// projection: tensor maps, block-scaled products, scales in tensor memory.
+//
+// A stage holds 128 bytes of K, one scale block, of each row of both operands, 128-byte swizzled.  A
+// product takes its scales from tensor memory, one byte of a 32-bit word per row, which its instruction
+// names: a word holds the scales of four blocks one after the other, as they lie in memory, so that scales are
+// brought once in four stages (once a stage, each byte four times, they took longer than the products: 1040 us
+// instead of 365 for 16384 x 4096 x 8192).  Words of rows 32 c .. 32 c + 31 of 128 are in column c, the same in
+// each of the four quarters of the lanes.  They get there by a copy of 512 bytes of shared memory, line r
+// holding the words of rows r, r + 32, r + 64, r + 96.
+#pragma once
+
+#include "m2rnn_internal.h"
+#include "m2rnn_layer.h"
+#include "m2rnn_ssm_tc.cuh"
+
+namespace m2rnn {
+
+constexpr int kBlockK = 128;  // bytes of K per stage
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Instruction descriptor of kind::mxf8f6f4: e4m3 A and B (0), both K-major, scales of type e8m0 (bit 23),
+// byte `which` of each scale word (bits 4 and 5 for B's, 29 and 30 for A's).
+__host__ __device__ constexpr uint32_t idesc_fp8(int M, int N, uint32_t which) {
+  return (which << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (which << 29);
+}
+// D (+)= (A sa)(B sb)^T over 32 values of K.
+__device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) { return umma_desc(smem, 0, 128, 0); }
+// Scales of 128 rows into 4 columns of tensor memory.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(scale_desc(smem)) : "memory");
+}
+
+constexpr int kQuad = 4;  // scale blocks, and stages, to a word
+
+// Scale words of ROWS rows per lane, each of the four blocks from i on, loaded one word ahead of their use:
+// loads first, then whatever waits for them.
+template <int ROWS>
+struct ScaleWords {
+  const uint8_t* row[ROWS];
+  bool live[ROWS];
+  bool words;  // rows and their starts are whole words
+  int blocks;  // of a row
+  uint32_t next[ROWS][kQuad];
+  __device__ __forceinline__ void fetch(int i) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (words) {
+        next[r][0] = live[r] ? *reinterpret_cast<const uint32_t*>(row[r] + i) : 0x7f7f7f7fu;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kQuad; ++j) next[r][j] = live[r] && i + j < blocks ? row[r][i + j] : 0x7fu;
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t word(int r) const {
+    return words ? next[r][0] : next[r][0] | next[r][1] << 8 | next[r][2] << 16 | next[r][3] << 24;
+  }
+};
+
+// Tensor map of rows of K bytes in boxes of `rows` rows of 128 bytes, 128-byte swizzled; what lies outside
+// is read as zero.
+inline bool byte_map(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* base, long long K, long long rows, long long row,
+                     int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row};
+  const cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows}, estr[2] = {1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace m2rnn

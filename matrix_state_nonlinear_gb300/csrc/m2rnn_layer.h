@@ -59,14 +59,17 @@ cudaError_t launch_quantise_weight(const void* w, bool f32, long long w_row, uin
 
 struct LinearProblem {
   const uint8_t *x, *x_scales;  // [M, K], [M, scale_blocks(K)]
+  const uint16_t* raw;          // or, for up to kRawRows tokens, x as bf16, x_row elements from row to row
   const uint8_t *w, *w_scales;  // [N, K], [scale_blocks(N), scale_blocks(K)]
-  long long x_row, w_row;       // bytes from row to row, multiples of 16
+  long long x_row, w_row;       // from row to row; bytes are multiples of 16
   void* out;                    // [M, N] bf16 or float32
   bool out_f32;
   int M, N, K;
   int* status;
 };
+constexpr int kRawRows = 16;
 cudaError_t launch_linear_fp8(const LinearProblem& p, cudaStream_t stream);
+cudaError_t launch_linear_pair(const LinearProblem& p, cudaStream_t stream);  // many tokens
 
 // The norm of `count` tensors (with `out`: their scaling to at most max_norm).
 struct GradProblem {

@@ -111,21 +111,58 @@ m2rnn_status m2rnn_quantise_weight_fp8(const void* w, int w_f32, long long w_row
   return done(launch_quantise_weight(w, w_f32 != 0, w_row, q, q_row, scales, N, K, static_cast<cudaStream_t>(stream)));
 }
 
-m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* x_scales, const uint8_t* w,
-                              long long w_row, const uint8_t* w_scales, void* out, int out_f32, long long M, int N,
-                              int K, void* stream) {
+// Sizes of a product and its weights.  Rows are tensor-map coordinates and the tiles, of 128 x 16 at the
+// least, a grid, both in 31 bits; a tensor map's stride has 40.
+static m2rnn_status linear_checks(const uint8_t* w, long long w_row, const uint8_t* w_scales, const void* out,
+                                  long long M, int N, int K) {
   if (M < 0 || N < 1 || K < 1) return M2RNN_ERR_INVALID_ARG;
-  // Rows are tensor-map coordinates, and the tiles of 128 x 16 a grid, both in 31 bits.
   if (M > 0x7fffff00LL || N > 0x7fffff00 || K > 0x7fffff00 || ((M + 15) / 16) * ((N + 127LL) / 128) > 0x7fffffffLL)
     return M2RNN_ERR_UNSUPPORTED;
   if (M == 0) return M2RNN_OK;
-  if (!x || !x_scales || !w || !w_scales || !out || !byte_rows(x, x_row, K) || !byte_rows(w, w_row, K))
-    return M2RNN_ERR_INVALID_ARG;
-  if (x_row >= 1LL << 40 || w_row >= 1LL << 40) return M2RNN_ERR_UNSUPPORTED;  // a tensor map's stride
+  if (!w || !w_scales || !out || !byte_rows(w, w_row, K)) return M2RNN_ERR_INVALID_ARG;
+  return w_row >= 1LL << 40 ? M2RNN_ERR_UNSUPPORTED : M2RNN_OK;
+}
+
+m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* x_scales, const uint8_t* w,
+                              long long w_row, const uint8_t* w_scales, void* out, int out_f32, long long M, int N,
+                              int K, void* stream) {
+  const m2rnn_status st = linear_checks(w, w_row, w_scales, out, M, N, K);
+  if (st != M2RNN_OK || M == 0) return st;
+  if (!x || !x_scales || !byte_rows(x, x_row, K)) return M2RNN_ERR_INVALID_ARG;
+  if (x_row >= 1LL << 40) return M2RNN_ERR_UNSUPPORTED;
   int* status = device_status();
   if (!status) return M2RNN_ERR_CUDA;
-  const LinearProblem p{x, x_scales, w, w_scales, x_row, w_row, out, out_f32 != 0, (int)M, N, K, status};
+  const LinearProblem p{x, x_scales, nullptr, w, w_scales, x_row, w_row, out, out_f32 != 0, (int)M, N, K, status};
   return done(launch_linear_fp8(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t m2rnn_linear_quantise_workspace_bytes(int x_f32, long long M, int K) {
+  if (M < 1 || M > 0x7fffff00LL || K < 1 || (M <= kRawRows && !x_f32)) return 0;
+  return (size_t)M * ((K + 15LL) / 16 * 16 + scale_blocks(K));
+}
+
+m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row, const uint8_t* w, long long w_row,
+                                       const uint8_t* w_scales, void* out, int out_f32, long long M, int N, int K,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  m2rnn_status st = linear_checks(w, w_row, w_scales, out, M, N, K);
+  if (st != M2RNN_OK || M == 0) return st;
+  if (!x || x_row < 0) return M2RNN_ERR_INVALID_ARG;
+  int* status = device_status();
+  if (!status) return M2RNN_ERR_CUDA;
+  const auto at = static_cast<cudaStream_t>(stream);
+  LinearProblem p{nullptr, nullptr, nullptr, w, w_scales, x_row, w_row, out, out_f32 != 0, (int)M, N, K, status};
+  const size_t need = m2rnn_linear_quantise_workspace_bytes(x_f32, M, K);
+  if (need > 0) {
+    if (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need) return M2RNN_ERR_INVALID_ARG;
+    p.x_row = (K + 15LL) / 16 * 16;
+    uint8_t *q = static_cast<uint8_t*>(workspace), *scales = q + M * p.x_row;
+    st = done(launch_quantise_rows(x, x_f32 != 0, x_row, q, p.x_row, scales, M, K, at));
+    if (st != M2RNN_OK) return st;
+    p.x = q, p.x_scales = scales;
+  } else {
+    p.raw = static_cast<const uint16_t*>(x);
+  }
+  return done(launch_linear_fp8(p, at));
 }
 
 size_t m2rnn_grad_norm_workspace_bytes(int count) { return count >= 0 ? grad_norm_workspace_bytes(count) : 0; }

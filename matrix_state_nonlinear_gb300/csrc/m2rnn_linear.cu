@@ -4,174 +4,231 @@
 //
 // The scales are powers of two, so the tensor cores apply them exactly (kind::mxf8f6f4) and the sum over
 // all of K stays in one float32 accumulator in tensor memory.
-#include "m2rnn_internal.h"
-#include "m2rnn_layer.h"
-#include "m2rnn_ssm_tc.cuh"
+//
+// This kernel takes few and middling numbers of tokens and is bound by the weights' way from memory, and
+// below a few megabytes by latency.  A block takes 128 channels (the product's rows, so that the weights fill
+// the tensor core however few tokens there are) by NT tokens.  Where that gives fewer blocks than SMs, a
+// cluster of up to 8 blocks shares a tile, each with a stretch of K, and adds up its parts through
+// distributed shared memory, in the order of K.  Up to 16 tokens of bf16 are quantised on the way in, by the
+// warps that later write the results.
+#include "m2rnn_fp8_tc.cuh"
 
 namespace m2rnn {
 namespace {
 
-constexpr int MT = 128;  // output channels of a tile: the product's rows (tensor-memory lanes)
-constexpr int KB = 128;  // bytes of K per stage: one scale block
+constexpr int MT = 128;  // channels of a tile
 constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kThreads = 224;
-
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Instruction descriptor of kind::mxf8f6f4: e4m3 A and B (0), both K-major, scales of type e8m0 (bit 23),
-// the first byte of each scale word.
-__host__ __device__ constexpr uint32_t idesc_fp8(int M, int N) {
-  return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
-}
-// D (+)= (A sa)(B sb)^T over 32 values of K.
-__device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-      : "memory");
-}
-// Scales of 128 rows into 4 columns of tensor memory: word c of 16-byte line r is that of row 32 c + r.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(umma_desc(smem, 0, 128, 0))
-               : "memory");
-}
 
 template <int NT>
 struct Smem {
-  static constexpr int kStages = 5;
-  static constexpr int kA = MT * KB, kB = NT * KB, kStage = kA + kB;
-  static constexpr int kScales = kStages * kStage, kScaleStage = 1024;
-  static constexpr int kBytes = kScales + kStages * kScaleStage + 1024;  // 1024: to align the first stage
+  static constexpr int kStages = NT <= 32 ? 8 : NT == 64 ? 7 : 6;
+  static constexpr int kA = MT * kBlockK, kB = NT * kBlockK, kStage = kA + kB;
+  static constexpr int kScaleStages = 4, kScaleStage = 1024;  // words of the channels and the tokens
+  static constexpr int kScales = kStages * kStage;
+  static constexpr int kBytes = kScales + kScaleStages * kScaleStage + 1024;  // 1024: to align the first stage
+  static constexpr int kColScale = NT;                                   // two sets of 4 + 4 columns
+  static constexpr int kTmemCols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT <= 64 ? 128 : 256;
 };
-template <int S>
+template <int S, int Q>
 struct Bars {
-  uint64_t full[S], empty[S], done;
+  uint64_t full[S], empty[S], scale_full[Q], scale_empty[Q], done;
   uint32_t tmem;
   int abort;
 };
 
-template <int NT, typename Out>
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Eight bf16 values of a row from k on, zeros behind its K values.
+__device__ __forceinline__ uint4 load_raw(const uint16_t* row, int k, int K, bool vec) {
+  if (vec && k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = k + i < K ? row[k + i] : 0u;
+  return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
+template <int NT, bool RAW, typename Out>
 __global__ void __launch_bounds__(kThreads)
     linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LinearProblem p,
-                  int token_tiles, bool vec) {
+                  int token_tiles, int split, bool raw_vec, bool vec) {
   using S = Smem<NT>;
-  constexpr int ST = S::kStages;
+  constexpr int ST = S::kStages, SQ = S::kScaleStages;
   extern __shared__ unsigned char raw[];
-  __shared__ Bars<ST> bar;
-  unsigned char* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  const uint32_t base = smem_u32(smem);
+  __shared__ Bars<ST, SQ> bar;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = (int)(blockIdx.x / token_tiles) * MT, m0 = (int)(blockIdx.x % token_tiles) * NT;
-  const int blocks = scale_blocks(p.K);
+  const int tile = blockIdx.x / split, rank = blockIdx.x % split;  // a cluster is a tile's blocks
+  const int n0 = tile / token_tiles * MT, m0 = tile % token_tiles * NT;
+  const int all = scale_blocks(p.K), begin = (int)((long long)all * rank / split),
+            end = (int)((long long)all * (rank + 1) / split);
   volatile int* abort = &bar.abort;
-  constexpr int kTmemCols = 256, kColScale = NT;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&bar.full[s], 2), mbar_init(&bar.empty[s], 1);
+    for (int s = 0; s < ST; ++s) mbar_init(&bar.full[s], RAW ? 1 + kEpilogueWarps : 1), mbar_init(&bar.empty[s], 1);
+    for (int s = 0; s < SQ; ++s)
+      mbar_init(&bar.scale_full[s], RAW ? 1 + kEpilogueWarps : 1), mbar_init(&bar.scale_empty[s], 1);
     mbar_init(&bar.done, 1);
     bar.abort = 0;
     fence_mbar_init();
   }
-  if (warp == kWarpMma) tmem_alloc(&bar.tmem, kTmemCols);
+  if (warp == kWarpMma) tmem_alloc(&bar.tmem, S::kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
   bool ok = true;
+  // Step i (from begin) is stage (i - begin) % ST, its turn (i - begin) / ST.
+  auto stage_free = [&](int g) {
+    if (g >= ST) ok = warp_wait(&bar.empty[g % ST], (uint32_t)(g / ST - 1) & 1u, abort);
+    return ok;
+  };
+  // Its scales are byte (i - begin) % 4 of word (i - begin) / 4.
+  auto scales_free = [&](int h) {
+    if (h >= SQ) ok = warp_wait(&bar.scale_empty[h % SQ], (uint32_t)(h / SQ - 1) & 1u, abort);
+    return ok;
+  };
 
   if (warp == kWarpLoad) {
-    for (int i = 0; i < blocks; ++i) {
-      const int s = i % ST;
-      if (i >= ST && !(ok = warp_wait(&bar.empty[s], (uint32_t)(i / ST - 1) & 1u, abort))) break;
+    for (int g = 0; g < end - begin && stage_free(g); ++g) {
       if (lane == 0) {
-        unsigned char* to = smem + s * S::kStage;
-        mbar_arrive_expect_tx(&bar.full[s], S::kStage);
-        tma_load_2d(to, &map_w, &bar.full[s], i * KB, n0);
-        tma_load_2d(to + S::kA, &map_x, &bar.full[s], i * KB, m0);
+        const int s = g % ST, k = (begin + g) * kBlockK;
+        const uint32_t to = base + s * S::kStage;
+        mbar_arrive_expect_tx(&bar.full[s], RAW ? S::kA : S::kStage);
+        tma_load_2d(to, &map_w, &bar.full[s], k, n0);
+        if (!RAW) tma_load_2d(to + S::kA, &map_x, &bar.full[s], k, m0);
       }
       __syncwarp();
     }
   } else if (warp == kWarpScale) {
-    const uint8_t* sw = p.w_scales + (size_t)(n0 / KB) * blocks;
-    for (int i = 0; i < blocks; ++i) {
-      const int s = i % ST;
-      uint32_t u[4];
+    constexpr int R = (NT + 31) / 32;
+    ScaleWords<1> w;
+    ScaleWords<R> x;
+    w.blocks = x.blocks = all;
+    w.row[0] = p.w_scales + (size_t)(n0 / kScaleBlock) * all;
+    w.live[0] = true;
+    const bool words = all % kQuad == 0 && begin % kQuad == 0;
+    w.words = words && reinterpret_cast<uintptr_t>(p.w_scales) % kQuad == 0;
+    x.words = words && reinterpret_cast<uintptr_t>(p.x_scales) % kQuad == 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int m = m0 + 32 * c + lane;
-        u[c] = (32 * c < NT && m < p.M ? p.x_scales[(size_t)m * blocks + i] : 127u) * 0x01010101u;
-      }
-      const uint32_t v = sw[i] * 0x01010101u;
-      if (i >= ST && !(ok = warp_wait(&bar.empty[s], (uint32_t)(i / ST - 1) & 1u, abort))) break;
-      const uint32_t to = base + S::kScales + s * S::kScaleStage;
-      st_shared_v4(to + lane * 16, make_uint4(v, v, v, v));
-      st_shared_v4(to + 512 + lane * 16, make_uint4(u[0], u[1], u[2], u[3]));
+    for (int c = 0; c < R; ++c) {
+      const int m = m0 + 32 * c + lane;
+      x.live[c] = !RAW && m < p.M && 32 * c + lane < NT;
+      x.row[c] = RAW ? nullptr : p.x_scales + (size_t)m * all;
+    }
+    w.fetch(begin), x.fetch(begin);
+    for (int i = begin, h = 0; i < end; i += kQuad, ++h) {
+      uint32_t u[R];
+      const uint32_t v = w.word(0);
+#pragma unroll
+      for (int c = 0; c < R; ++c) u[c] = x.word(c);
+      if (i + kQuad < end) w.fetch(i + kQuad), x.fetch(i + kQuad);
+      if (!scales_free(h)) break;
+      const uint32_t to = base + S::kScales + h % SQ * S::kScaleStage + lane * 16;
+      st_shared_v4(to, make_uint4(v, v, v, v));
+      if (!RAW) st_shared_v4(to + 512, make_uint4(u[0], u[R > 1 ? 1 : 0], u[R > 2 ? 2 : 0], u[R > 3 ? 3 : 0]));
       fence_proxy_async_smem();
-      warp_arrive(&bar.full[s], lane);
+      warp_arrive(&bar.scale_full[h % SQ], lane);
     }
   } else if (warp == kWarpMma) {
-    constexpr uint32_t idesc = idesc_fp8(MT, NT);
-    for (int i = 0; i < blocks; ++i) {
-      const int s = i % ST;
-      if (!(ok = warp_wait(&bar.full[s], (uint32_t)(i / ST) & 1u, abort))) break;
+    uint32_t sa = 0;
+    for (int g = 0; g < end - begin; ++g) {
+      const int s = g % ST, h = g / kQuad;
+      if (g % kQuad == 0) {
+        if (!(ok = warp_wait(&bar.scale_full[h % SQ], (uint32_t)(h / SQ) & 1u, abort))) break;
+        tc_fence_after();
+        sa = tmem + S::kColScale + 8 * (h & 1);
+        if (lane == 0) {
+          const uint32_t scales = base + S::kScales + h % SQ * S::kScaleStage;
+          copy_scales(sa, scales);
+          copy_scales(sa + 4, scales + 512);
+          umma_commit(&bar.scale_empty[h % SQ]);
+        }
+      }
+      if (!(ok = warp_wait(&bar.full[s], (uint32_t)(g / ST) & 1u, abort))) break;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t at = base + s * S::kStage, scales = base + S::kScales + s * S::kScaleStage;
-        const uint32_t sa = tmem + kColScale + 8 * s, sb = sa + 4;
-        copy_scales(sa, scales);
-        copy_scales(sb, scales + 512);
+        const uint32_t at = base + s * S::kStage, idesc = idesc_fp8(MT, NT, g % kQuad);
         const uint64_t a = desc_k(at), b = desc_k(at + S::kA);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_fp8(tmem, a + 2 * k, b + 2 * k, idesc, sa, sb, i > 0 || k > 0);
+        for (int k = 0; k < 4; ++k) umma_fp8(tmem, a + 2 * k, b + 2 * k, idesc, sa, sa + 4, g > 0 || k > 0);
         umma_commit(&bar.empty[s]);
-        if (i == blocks - 1) umma_commit(&bar.done);
+        if (g == end - begin - 1) umma_commit(&bar.done);
       }
       __syncwarp();
     }
   } else {
-    ok = warp_wait(&bar.done, 0, abort);
+    if constexpr (RAW) {
+      // 16 threads take 128 values of a row, eight each; rows r and r + 8, four steps ahead.
+      const int r = threadIdx.x >> 4, piece = threadIdx.x & 15;
+      uint4 next[4][2];
+      auto fetch = [&](int i0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool live = i0 + j < end && r + 8 * h < p.M;
+            next[j][h] = live ? load_raw(p.raw + (r + 8 * h) * p.x_row, (i0 + j) * kBlockK + piece * 8, p.K, raw_vec)
+                              : make_uint4(0, 0, 0, 0);
+          }
+      };
+      fetch(begin);
+      for (int i0 = begin; i0 < end && ok; i0 += 4) {
+        uint4 now[4][2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) now[j][0] = next[j][0], now[j][1] = next[j][1];
+        if (i0 + 4 < end) fetch(i0 + 4);
+        const int h = (i0 - begin) / kQuad;
+        if (!scales_free(h)) break;
+        const uint32_t scales = base + S::kScales + h % SQ * S::kScaleStage + 512;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (i0 + j >= end || !ok || !stage_free(i0 + j - begin)) continue;
+          const int s = (i0 + j - begin) % ST;
+          const uint32_t to = base + s * S::kStage + S::kA;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u[4] = {now[j][h].x, now[j][h].y, now[j][h].z, now[j][h].w};
+            uint32_t top = 0, q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max(top, max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+            const uint32_t e = scale_exponent(top);
+            const float by = inverse_scale(e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = pack_e4m3x2(bf16_lo(u[i]) * by, bf16_hi(u[i]) * by);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(tile_at(to, r + 8 * h, piece >> 1) + (piece & 1) * 8),
+                         "r"(q[0] | q[1] << 16), "r"(q[2] | q[3] << 16)
+                         : "memory");
+            if (piece == 0)
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (r + 8 * h) * 16 + j), "r"(e) : "memory");
+          }
+          fence_proxy_async_smem();
+          warp_arrive(&bar.full[s], lane);
+        }
+        if (ok) warp_arrive(&bar.scale_full[h % SQ], lane);
+      }
+    }
+    if (ok) ok = warp_wait(&bar.done, 0, abort);
     tc_fence_after();
-    // Lane = channel: a tile row by row (token) through the stages, which every product has left.
-    Out* tile = reinterpret_cast<Out*>(smem);
+    // A lane is a channel: the tile goes row by row (token) into the stages, which every product has left.
     if (ok) {
+      constexpr int C = NT < 16 ? NT : 16;
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 16) {
-        float v[16];
+      for (int c = 0; c < NT; c += C) {
+        float v[C];
         tmem_ld16_nowait(tmem + ((uint32_t)(32 * warp) << 16) + c, v);
         tmem_ready(v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          Out* to = tile + (c + j) * MT + 32 * warp + lane;
-          if constexpr (sizeof(Out) == 4)
-            *to = v[j];
-          else
-            *to = f_to_bf16(v[j]);
-        }
-      }
-    }
-    named_bar_sync(1, 32 * kEpilogueWarps);
-    if (ok) {
-      const int rows = min(NT, p.M - m0), width = min(MT, p.N - n0);
-      Out* out = static_cast<Out*>(p.out) + (size_t)m0 * p.N + n0;
-      if (vec) {
-        constexpr int V = 16 / sizeof(Out), L = MT / V;  // values per access, accesses per row
-        for (int id = threadIdx.x; id < rows * L; id += 32 * kEpilogueWarps) {
-          const int r = id / L, c = id % L * V;
-          if (c < width)
-            *reinterpret_cast<uint4*>(out + (size_t)r * p.N + c) = *reinterpret_cast<const uint4*>(tile + r * MT + c);
-        }
-      } else {
-        for (int id = threadIdx.x; id < rows * MT; id += 32 * kEpilogueWarps) {
-          const int r = id / MT, c = id % MT;
-          if (c < width) out[(size_t)r * p.N + c] = tile[r * MT + c];
-        }
+        for (int j = 0; j < C; ++j)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + j) * MT + 32 * warp + lane) * 4), "f"(v[j]) : "memory");
       }
     }
   }
@@ -185,41 +242,96 @@ __global__ void __launch_bounds__(kThreads)
       for (int s = 0; s < ST; ++s) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kWarpMma) tmem_dealloc(tmem, S::kTmemCols);
+  if (split > 1) cluster_sync_all();
+  if (!*abort) {
+    // This block's share of the tile's tokens, four channels a thread.
+    const int first = NT * rank / split, rows = min(NT * (rank + 1) / split, p.M - m0) - first;
+    Out* out = static_cast<Out*>(p.out) + (long long)(m0 + first) * p.N + n0;
+    for (int id = threadIdx.x; id < rows * (MT / 4); id += kThreads) {
+      const int r = id / (MT / 4), c = id % (MT / 4) * 4, n = p.N - n0 - c;
+      if (n <= 0) continue;
+      const uint32_t at = base + ((first + r) * MT + c) * 4;
+      float4 v;
+      if (split == 1) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+      } else {
+        v = ld_cluster_v4(mapa_shared(at, 0));
+        for (int s = 1; s < split; ++s) {
+          const float4 u = ld_cluster_v4(mapa_shared(at, s));
+          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+      }
+      Out* to = out + (long long)r * p.N + c;
+      if constexpr (sizeof(Out) == 4) {
+        if (vec) {
+          *reinterpret_cast<float4*>(to) = v;
+        } else {
+          to[0] = v.x;
+          if (n > 1) to[1] = v.y;
+          if (n > 2) to[2] = v.z;
+          if (n > 3) to[3] = v.w;
+        }
+      } else {
+        if (vec) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        } else {
+          to[0] = f_to_bf16(v.x);
+          if (n > 1) to[1] = f_to_bf16(v.y);
+          if (n > 2) to[2] = f_to_bf16(v.z);
+          if (n > 3) to[3] = f_to_bf16(v.w);
+        }
+      }
+    }
+  }
+  if (split > 1) cluster_sync_all();  // no part of this block's tile is read any more
 }
 
-// Tensor map of rows of K bytes in boxes of `rows` rows of 128 bytes, 128-byte swizzled; what lies outside
-// is read as zero.
-bool byte_map(EncodeTiledFn enc, CUtensorMap* map, const uint8_t* base, long long K, long long rows, long long row,
-              int box_rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row};
-  const cuuint32_t box[2] = {(cuuint32_t)KB, (cuuint32_t)box_rows}, estr[2] = {1u, 1u};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int NT, typename Out>
+template <int NT, bool RAW, typename Out>
 cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   using S = Smem<NT>;
+  auto* kernel = linear_kernel<NT, RAW, Out>;
   // At every launch: the attribute belongs to the current device.
-  const cudaError_t attr =
-      cudaFuncSetAttribute(linear_kernel<NT, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (attr != cudaSuccess) return attr;
   const EncodeTiledFn enc = tensor_map_encoder();
   CUtensorMap mw{}, mx{};
-  if (!enc || !byte_map(enc, &mw, p.w, p.K, p.N, p.w_row, MT) || !byte_map(enc, &mx, p.x, p.K, p.M, p.x_row, NT))
+  if (!enc || !byte_map(enc, &mw, p.w, p.K, p.N, p.w_row, MT) ||
+      (!RAW && !byte_map(enc, &mx, p.x, p.K, p.M, p.x_row, NT)))
     return cudaErrorNotSupported;
-  const long long tokens = (p.M + NT - 1) / NT, channels = (p.N + MT - 1) / MT;
-  const bool vec = p.N % (16 / (int)sizeof(Out)) == 0 && aligned_to(p.out, 16);
-  linear_kernel<NT, Out><<<(unsigned)(tokens * channels), kThreads, S::kBytes, stream>>>(mw, mx, p, (int)tokens, vec);
-  return cudaGetLastError();
+  const long long tokens = (p.M + NT - 1) / NT, tiles = tokens * ((p.N + MT - 1) / MT);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 152 && split * 2 <= scale_blocks(p.K)) split *= 2;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(tiles * split));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = S::kBytes;
+  c.stream = stream;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)split, a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  const bool raw_vec = RAW && aligned_to(p.raw, 16) && p.x_row % 8 == 0;
+  const bool vec = p.N % 4 == 0 && aligned_to(p.out, 4 * sizeof(Out));
+  return cudaLaunchKernelEx(&c, kernel, mw, mx, p, (int)tokens, split, raw_vec, vec);
+}
+
+template <typename Out>
+cudaError_t dispatch(const LinearProblem& p, cudaStream_t stream) {
+  if (p.raw) return run<16, true, Out>(p, stream);
+  if (p.M <= 16) return run<16, false, Out>(p, stream);
+  if (p.M <= 32) return run<32, false, Out>(p, stream);
+  if (p.M <= 64) return run<64, false, Out>(p, stream);
+  return run<128, false, Out>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_fp8(const LinearProblem& p, cudaStream_t stream) {
-  return p.out_f32 ? run<128, float>(p, stream) : run<128, uint16_t>(p, stream);
+  const long long pairs = ((p.M + 255LL) / 256) * ((p.N + 255LL) / 256);
+  if (pairs >= 64 && !p.raw) return launch_linear_pair(p, stream);
+  return p.out_f32 ? dispatch<float>(p, stream) : dispatch<uint16_t>(p, stream);
 }
 
 }  // namespace m2rnn

@@ -1,0 +1,297 @@
+// m2rnn_linear_pair.cu — the 8-bit projection of many tokens: tiles of 256 tokens by 256 channels on pairs
+// of SMs.
+//
+// Bound by the tensor cores.  A pair (a cluster of two blocks) shares each tile's operands: every block loads
+// 128 rows of tokens and 128 of weights a stage and the product, issued by the first block, reads both
+// blocks' shared memory, so that a stage's 32 KB feed 512 cycles of an SM's tensor core (a 128 x 256 tile
+// of one SM would load 48).  Block r's accumulators hold tokens 128 r .. of the tile, a token per lane, all 256
+// channels, and leave by 16-byte stores of eight channels a thread.  Blocks stay on their SM and take tiles
+// in turn; the next tile's products run while the last one's results leave.  Two buffers of 256 columns and
+// the scales would need 536 columns of tensor memory, so the buffers overlap in 32 columns, which are read
+// first: the next tile starts as soon as these are out.
+#include "m2rnn_fp8_tc.cuh"
+
+namespace m2rnn {
+namespace {
+
+constexpr int kRows = 128;                // rows of each operand per block and stage
+constexpr int kTile = 2 * kRows;          // tokens and channels of a tile
+constexpr int kStages = 6;
+constexpr int kOperand = kRows * kBlockK, kStage = 2 * kOperand;
+constexpr int kScaleStages = 4, kScaleStage = 512 + 1024;  // words of 128 tokens and 256 channels
+constexpr int kScales = kStages * kStage;
+constexpr int kSmemBytes = kScales + kScaleStages * kScaleStage + 1024;  // 1024: to align the first stage
+constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kThreads = 224;
+constexpr int kTmemCols = 512, kColSecond = 224, kColScale = 480;  // scales: two sets of 4 + 8 columns
+constexpr int kGroup = 8;                 // token tiles that share a run of channel tiles
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages], scale_full[kScaleStages], scale_empty[kScaleStages], done[2], early;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void umma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+      : "memory");
+}
+// The same copy in both blocks, each from its own shared memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t smem) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(scale_desc(smem)) : "memory");
+}
+// The barrier of both blocks completes when every product issued so far is done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A load whose bytes count on a barrier (cluster address) that may be the other block's.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+// A whole warp waits for arrivals that may come from the other block.
+__device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(~0u, mbar_wait_cluster(bar, parity, kWaitLimitCycles, abort));
+}
+
+// Tile t of the raster: runs of kGroup token tiles by all channel tiles, so that the tiles in flight share
+// their operands in L2.
+__device__ __forceinline__ int2 tile_at_index(int t, int token_tiles, int channel_tiles) {
+  const int run = t / (kGroup * channel_tiles), first = run * kGroup, wide = min(kGroup, token_tiles - first);
+  const int in = t - run * kGroup * channel_tiles;
+  return make_int2(first + in % wide, in / wide);
+}
+
+template <typename Out>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                       LinearProblem p, int token_tiles, int channel_tiles, bool vec) {
+  extern __shared__ unsigned char raw[];
+  __shared__ Bars bar;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int blocks = scale_blocks(p.K), tiles = token_tiles * channel_tiles;
+  volatile int* abort = &bar.abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&bar.full[s], 1), mbar_init(&bar.empty[s], 1);
+    for (int s = 0; s < kScaleStages; ++s) mbar_init(&bar.scale_full[s], 2), mbar_init(&bar.scale_empty[s], 1);
+    mbar_init(&bar.done[0], 1), mbar_init(&bar.done[1], 1);
+    mbar_init(&bar.early, 2 * kEpilogueWarps);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar.tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the other block's barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  bool ok = true;
+  // Steps are counted over all tiles: step g is stage g % kStages, its turn g / kStages.
+  auto free_stage = [&](int g) {
+    if (g >= kStages) ok = warp_wait(&bar.empty[g % kStages], (uint32_t)(g / kStages - 1) & 1u, abort);
+    return ok;
+  };
+
+  if (warp == kWarpLoad) {
+    int g = 0;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const int2 at = tile_at_index(t, token_tiles, channel_tiles);
+      for (int i = 0; i < blocks && free_stage(g); ++i, ++g) {
+        if (lane == 0) {
+          const int s = g % kStages;
+          const uint32_t to = base + s * kStage, full = mapa_shared(smem_u32(&bar.full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kStage);
+          tma_load_2d_pair(to, &map_x, full, i * kBlockK, at.x * kTile + rank * kRows);
+          tma_load_2d_pair(to + kOperand, &map_w, full, i * kBlockK, at.y * kTile + rank * kRows);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == kWarpScale) {
+    // Words are counted over all tiles as the steps are: word h is slot h % kScaleStages.
+    ScaleWords<4> x;
+    ScaleWords<2> w;
+    x.blocks = w.blocks = blocks;
+    x.words = blocks % kQuad == 0 && reinterpret_cast<uintptr_t>(p.x_scales) % kQuad == 0;
+    w.words = blocks % kQuad == 0 && reinterpret_cast<uintptr_t>(p.w_scales) % kQuad == 0;
+    auto aim = [&](int t) {
+      const int2 at = tile_at_index(t, token_tiles, channel_tiles);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int m = at.x * kTile + rank * kRows + 32 * c + lane;
+        x.live[c] = m < p.M;
+        x.row[c] = p.x_scales + (size_t)m * blocks;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int n = at.y * 2 + c;
+        w.live[c] = (long long)n * kScaleBlock < p.N;
+        w.row[c] = p.w_scales + (size_t)n * blocks;
+      }
+      x.fetch(0), w.fetch(0);
+    };
+    if (pair < tiles) aim(pair);
+    int h = 0;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      for (int i = 0; i < blocks; i += kQuad, ++h) {
+        const uint4 u = make_uint4(x.word(0), x.word(1), x.word(2), x.word(3));
+        const uint32_t v0 = w.word(0), v1 = w.word(1);
+        if (i + kQuad < blocks)
+          x.fetch(i + kQuad), w.fetch(i + kQuad);
+        else if (t + pairs < tiles)
+          aim(t + pairs);
+        const int s = h % kScaleStages;
+        if (h >= kScaleStages && !(ok = warp_wait(&bar.scale_empty[s], (uint32_t)(h / kScaleStages - 1) & 1u, abort))) break;
+        const uint32_t to = base + kScales + s * kScaleStage + lane * 16;
+        st_shared_v4(to, u);
+        st_shared_v4(to + 512, make_uint4(v0, v0, v0, v0));
+        st_shared_v4(to + 1024, make_uint4(v1, v1, v1, v1));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.scale_full[s]), 0));
+      }
+    }
+  } else if (warp == kWarpMma) {
+    int g = 0, h = 0, n = 0;
+    for (int t = pair; rank == 0 && t < tiles && ok; t += pairs, ++n) {
+      if (n > 0 && !(ok = pair_wait(&bar.early, (uint32_t)(n - 1) & 1u, abort))) break;
+      const uint32_t d = tmem + (n & 1 ? kColSecond : 0);
+      uint32_t sa = 0;
+      for (int i = 0; i < blocks; ++i, ++g) {
+        const int s = g % kStages;
+        if (i % kQuad == 0) {
+          const int hs = h % kScaleStages;
+          if (!(ok = pair_wait(&bar.scale_full[hs], (uint32_t)(h / kScaleStages) & 1u, abort))) break;
+          tc_fence_after();
+          sa = tmem + kColScale + 12 * (h & 1);
+          if (lane == 0) {
+            const uint32_t scales = base + kScales + hs * kScaleStage;
+            copy_scales_pair(sa, scales);
+            copy_scales_pair(sa + 4, scales + 512);
+            copy_scales_pair(sa + 8, scales + 1024);
+            commit_pair(&bar.scale_empty[hs]);
+          }
+          ++h;
+        }
+        if (!(ok = pair_wait(&bar.full[s], (uint32_t)(g / kStages) & 1u, abort))) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t at = base + s * kStage, idesc = idesc_fp8(kTile, kTile, i % kQuad);
+          const uint64_t a = desc_k(at), b = desc_k(at + kOperand);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_fp8_pair(d, a + 2 * k, b + 2 * k, idesc, sa, sa + 4, i > 0 || k > 0);
+          commit_pair(&bar.empty[s]);
+          if (i == blocks - 1) commit_pair(&bar.done[n & 1]);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    int n = 0;
+    for (int t = pair; t < tiles; t += pairs, ++n) {
+      const int2 at = tile_at_index(t, token_tiles, channel_tiles);
+      if (!(ok = warp_wait(&bar.done[n & 1], (uint32_t)(n >> 1) & 1u, abort))) break;
+      tc_fence_after();
+      const long long m = (long long)at.x * kTile + rank * kRows + 32 * warp + lane;
+      const uint32_t from = tmem + ((uint32_t)(32 * warp) << 16) + (n & 1 ? kColSecond : 0);
+      Out* out = static_cast<Out*>(p.out) + m * p.N;
+#pragma unroll 1
+      for (int j = 0; j < kTile / 32; ++j) {
+        const int c = n & 1 ? j : (j + kTile / 32 - 1) % (kTile / 32);  // the columns that both buffers have first
+        float v[32];
+        tmem_ld16_nowait(from + 32 * c, v);
+        tmem_ld16_nowait(from + 32 * c + 16, v + 16);
+        tmem_ready(v);
+        if (j == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.early), 0));
+        }
+        const int n0 = at.y * kTile + 32 * c;
+        if (m >= p.M || n0 >= p.N) continue;
+        if (vec) {
+          constexpr int V = 16 / sizeof(Out);
+#pragma unroll
+          for (int k = 0; k < 32; k += V) {
+            if (n0 + k >= p.N) break;
+            uint4 u;
+            if constexpr (sizeof(Out) == 4)
+              u = make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]),
+                             __float_as_uint(v[k + 3]));
+            else
+              u = make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                             pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+            *reinterpret_cast<uint4*>(out + n0 + k) = u;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (n0 + k >= p.N) break;
+            if constexpr (sizeof(Out) == 4)
+              out[n0 + k] = v[k];
+            else
+              out[n0 + k] = f_to_bf16(v[k]);
+          }
+        }
+      }
+    }
+  }
+  if (!ok && lane == 0) {
+    *abort = 1;
+    atomicExch(p.status, kStatusTimeout);
+  }
+  // Given up: loads that were started, by either block, arrive before the pair ends.
+  if (!ok && warp == kWarpLoad && rank == 0)
+    for (int phase = 0; phase < 2; ++phase)
+      for (int s = 0; s < kStages; ++s) mbar_wait_bounded(&bar.full[s], phase, kWaitLimitCycles / 64);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // nothing of the other block reaches this one any more
+  if (warp == kWarpMma)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+template <typename Out>
+cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
+  // At every launch: the attribute belongs to the current device.
+  const cudaError_t attr =
+      cudaFuncSetAttribute(linear_pair_kernel<Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (attr != cudaSuccess) return attr;
+  const EncodeTiledFn enc = tensor_map_encoder();
+  CUtensorMap mw{}, mx{};
+  if (!enc || !byte_map(enc, &mw, p.w, p.K, p.N, p.w_row, kRows) || !byte_map(enc, &mx, p.x, p.K, p.M, p.x_row, kRows))
+    return cudaErrorNotSupported;
+  const int tokens = (p.M + kTile - 1) / kTile, channels = (p.N + kTile - 1) / kTile;
+  const long long tiles = (long long)tokens * channels;
+  const bool vec = p.N % (16 / (int)sizeof(Out)) == 0 && aligned_to(p.out, 16);
+  const unsigned pairs = (unsigned)(tiles < 76 ? tiles : 76);
+  linear_pair_kernel<Out><<<2 * pairs, kThreads, kSmemBytes, stream>>>(mx, mw, p, tokens, channels, vec);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_pair(const LinearProblem& p, cudaStream_t stream) {
+  return p.out_f32 ? run<float>(p, stream) : run<uint16_t>(p, stream);
+}
+
+}  // namespace m2rnn

@@ -206,26 +206,34 @@ def quantise_weight_fp8(w, out=None, scales=None):
 
 
 @_on_stream
-def linear_fp8(x, x_scales, w, w_scales, out=None, out_dtype=BF16):
+def linear_fp8(x, x_scales, w, w_scales, out=None, out_dtype=BF16, workspace=None):
     """Projection in 8 bits: out = x w^T with float32 sums.  x [..., K] and x_scales from
     ``add_rmsnorm_fp8`` or ``quantise_fp8``, or x bf16 or float32 with x_scales None (quantised here, the same
     values); w [N, K] and w_scales from ``quantise_weight_fp8``.  Returns out [..., N], bf16 or float32."""
     dev = _device(x)
-    if x_scales is None:
-        x, x_scales = quantise_fp8(x)
     shape = x.shape
     K = shape[-1]
     N = w.shape[0]
     _sizes(N, K)
+    wp, w_row = _byte_rows(w, "w", (N, K), dev)
+    ws = _ptr(w_scales, "w_scales", E8M0, (_blocks(N), _blocks(K)), dev)
+    to = (*shape[:-1], N)
     if out is None:
-        out = torch.empty((*shape[:-1], N), dtype=out_dtype, device=x.device)
-    if out.dtype not in (F32, BF16):
-        raise TypeError(f"out: expected {F32} or {BF16}, got {out.dtype}")
-    st = load_library().m2rnn_linear_fp8(
-        *_byte_rows(x, "x", shape, dev), _ptr(x_scales, "x_scales", E8M0, (*shape[:-1], _blocks(K)), dev),
-        *_byte_rows(w, "w", (N, K), dev), _ptr(w_scales, "w_scales", E8M0, (_blocks(N), _blocks(K)), dev),
-        _ptr(out, "out", out.dtype, (*shape[:-1], N), dev), int(out.dtype is F32), x.numel() // K if K else 0, N, K,
-        _stream(dev))
+        out = torch.empty(to, dtype=out_dtype, device=x.device)
+    kind = out.dtype
+    if kind is not BF16 and kind is not F32:
+        raise TypeError(f"out: expected {F32} or {BF16}, got {kind}")
+    op, M = _ptr(out, "out", kind, to, dev), x.numel() // K if K else 0
+    lib = load_library()
+    if x_scales is None:
+        f32 = _source(x, "x")
+        xp, row = _rows(x, "x", x.dtype, shape, dev)
+        space, sp, sb = _workspace(workspace, lib.m2rnn_linear_quantise_workspace_bytes(f32, M, K), x)
+        st = lib.m2rnn_linear_quantise_fp8(xp, f32, row, wp, w_row, ws, op, kind is F32, M, N, K, sp, sb, _stream(dev))
+    else:
+        xp, row = _byte_rows(x, "x", shape, dev)
+        sp = _ptr(x_scales, "x_scales", E8M0, (*shape[:-1], _blocks(K)), dev)
+        st = lib.m2rnn_linear_fp8(xp, row, sp, wp, w_row, ws, op, kind is F32, M, N, K, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_linear_fp8")
     return out

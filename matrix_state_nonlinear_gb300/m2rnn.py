@@ -67,6 +67,8 @@ SYMBOLS = {
     "m2rnn_quantise_fp8": (_I, [_P, _I, _L, _P, _L, _P, _L, _I, _P]),
     "m2rnn_quantise_weight_fp8": (_I, [_P, _I, _L, _P, _L, _P, _I, _I, _P]),
     "m2rnn_linear_fp8": (_I, [_P, _L, _P, _P, _L, _P, _P, _I, _L, _I, _I, _P]),
+    "m2rnn_linear_quantise_workspace_bytes": (ctypes.c_size_t, [_I, _L, _I]),
+    "m2rnn_linear_quantise_fp8": (_I, [_P, _I, _L, _P, _L, _P, _P, _I, _L, _I, _I, _P, ctypes.c_size_t, _P]),
     "m2rnn_grad_norm_workspace_bytes": (ctypes.c_size_t, [_I]),
     "m2rnn_clip_grad_norm": (_I, [_P] * 4 + [_I, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
 }
