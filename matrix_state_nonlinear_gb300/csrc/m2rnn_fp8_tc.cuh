@@ -31,19 +31,54 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 __host__ __device__ constexpr uint32_t idesc_fp8(int M, int N, uint32_t which) {
   return (which << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | (which << 29);
 }
-// D (+)= (A sa)(B sb)^T over 32 values of K.
-__device__ __forceinline__ void umma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-      : "memory");
+// D (+)= (A sa)(B sb)^T over the 128 values of K of a stage, in four steps of 32, issued where `pred` holds: a
+// whole warp runs the issuing loop, so that addresses and descriptors stay in uniform registers, and one
+// lane issues.  (From a branch that one lane takes, the four products took 280 cycles to issue and a commit 118,
+// of the 512 that the products themselves take.)  PAIR: across the two blocks of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void umma4_fp8_if(bool pred, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t sa, uint32_t sb, uint32_t accumulate_first) {
+#define M2RNN_FP8_STEP(group, p)                                                                                   \
+  "@q tcgen05.mma.cta_group::" group ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], " p ";\n\t"
+#define M2RNN_FP8_STEPS(group)                                                                                     \
+  "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t"                                                               \
+  "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\tsetp.ne.b32 t, %8, 0;\n\tmov.b64 a, %1;\n\tmov.b64 b, %2;\n\t" \
+  M2RNN_FP8_STEP(group, "p") "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t" M2RNN_FP8_STEP(group, "t")               \
+  "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t" M2RNN_FP8_STEP(group, "t")                                          \
+  "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t" M2RNN_FP8_STEP(group, "t") "}"
+  if constexpr (PAIR)
+    asm volatile(M2RNN_FP8_STEPS("2")::"r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb),
+                 "r"(accumulate_first), "r"((int)pred), "r"(1)
+                 : "memory");
+  else
+    asm volatile(M2RNN_FP8_STEPS("1")::"r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa), "r"(sb),
+                 "r"(accumulate_first), "r"((int)pred), "r"(1)
+                 : "memory");
+#undef M2RNN_FP8_STEPS
+#undef M2RNN_FP8_STEP
 }
-__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) { return umma_desc(smem, 0, 128, 0); }
-// Scales of 128 rows into 4 columns of tensor memory.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(scale_desc(smem)) : "memory");
+// Scales of 128 rows into 4 columns of tensor memory.  PAIR: the same copy in both blocks, each from its own
+// shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales_if(bool pred, uint32_t tmem, uint32_t smem) {
+  const uint64_t desc = umma_desc(smem, 0, 128, 0);
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(
+            tmem),
+        "l"(desc), "r"((int)pred)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(
+            tmem),
+        "l"(desc), "r"((int)pred)
+        : "memory");
+}
+// A converged warp waits for a phase; the usual case, a phase that is over, costs one poll and no vote.
+__device__ __forceinline__ bool issue_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return warp_wait_long(smem_u32(bar), parity, abort);
 }
 
 constexpr int kQuad = 4;  // scale blocks, and stages, to a word

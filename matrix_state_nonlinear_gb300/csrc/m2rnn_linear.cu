@@ -137,32 +137,29 @@ __global__ void __launch_bounds__(kThreads)
       warp_arrive(&bar.scale_full[h % SQ], lane);
     }
   } else if (warp == kWarpMma) {
-    uint32_t sa = 0;
-    for (int g = 0; g < end - begin; ++g) {
-      const int s = g % ST, h = g / kQuad;
-      if (g % kQuad == 0) {
-        if (!(ok = warp_wait(&bar.scale_full[h % SQ], (uint32_t)(h / SQ) & 1u, abort))) break;
-        tc_fence_after();
-        sa = tmem + S::kColScale + 8 * (h & 1);
-        if (lane == 0) {
-          const uint32_t scales = base + S::kScales + h % SQ * S::kScaleStage;
-          copy_scales(sa, scales);
-          copy_scales(sa + 4, scales + 512);
-          umma_commit(&bar.scale_empty[h % SQ]);
-        }
-      }
-      if (!(ok = warp_wait(&bar.full[s], (uint32_t)(g / ST) & 1u, abort))) break;
+    const bool leader = elect_one_sync();
+    int s = 0, hs = 0;
+    uint32_t turn = 0, scale_turn = 0;
+    for (int i0 = begin; i0 < end && ok; i0 += kQuad) {
+      if (!(ok = issue_wait(&bar.scale_full[hs], scale_turn, abort))) break;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t at = base + s * S::kStage, idesc = idesc_fp8(MT, NT, g % kQuad);
-        const uint64_t a = desc_k(at), b = desc_k(at + S::kA);
+      const uint32_t sa = tmem + S::kColScale + 8 * (hs & 1), scales = base + S::kScales + hs * S::kScaleStage;
+      copy_scales_if<false>(leader, sa, scales);
+      copy_scales_if<false>(leader, sa + 4, scales + 512);
+      umma_commit_if(leader, &bar.scale_empty[hs]);
+      if (++hs == SQ) hs = 0, scale_turn ^= 1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_fp8(tmem, a + 2 * k, b + 2 * k, idesc, sa, sa + 4, g > 0 || k > 0);
-        umma_commit(&bar.empty[s]);
-        if (g == end - begin - 1) umma_commit(&bar.done);
+      for (int j = 0; j < kQuad; ++j) {
+        if (i0 + j >= end || !(ok = issue_wait(&bar.full[s], turn, abort))) break;
+        tc_fence_after();
+        const uint32_t at = base + s * S::kStage;
+        umma4_fp8_if<false>(leader, tmem, desc_k(at), desc_k(at + S::kA), idesc_fp8(MT, NT, j), sa, sa + 4,
+                            i0 + j > begin);
+        umma_commit_if(leader, &bar.empty[s]);
+        if (++s == ST) s = 0, turn ^= 1;
       }
-      __syncwarp();
     }
+    if (ok) umma_commit_if(leader, &bar.done);
   } else {
     if constexpr (RAW) {
       // 16 threads take 128 values of a row, eight each; rows r and r + 8, four steps ahead.

@@ -31,24 +31,13 @@ struct Bars {
   int abort;
 };
 
-__device__ __forceinline__ void umma_fp8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
-                                              uint32_t accumulate) {
+// The barrier of both blocks completes when everything issued so far is done.
+__device__ __forceinline__ void commit_pair_if(bool pred, uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-      : "memory");
-}
-// The same copy in both blocks, each from its own shared memory.
-__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint32_t smem) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(scale_desc(smem)) : "memory");
-}
-// The barrier of both blocks completes when every product issued so far is done.
-__device__ __forceinline__ void commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)3), "r"((int)pred)
       : "memory");
 }
 // A load whose bytes count on a barrier (cluster address) that may be the other block's.
@@ -171,39 +160,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       }
     }
   } else if (warp == kWarpMma) {
-    int g = 0, h = 0, n = 0;
+    // Stage s and scale slot hs, with the parities of their turns.
+    const bool leader = elect_one_sync();
+    int s = 0, hs = 0, n = 0;
+    uint32_t turn = 0, scale_turn = 0;
     for (int t = pair; rank == 0 && t < tiles && ok; t += pairs, ++n) {
       if (n > 0 && !(ok = pair_wait(&bar.early, (uint32_t)(n - 1) & 1u, abort))) break;
       const uint32_t d = tmem + (n & 1 ? kColSecond : 0);
-      uint32_t sa = 0;
-      for (int i = 0; i < blocks; ++i, ++g) {
-        const int s = g % kStages;
-        if (i % kQuad == 0) {
-          const int hs = h % kScaleStages;
-          if (!(ok = pair_wait(&bar.scale_full[hs], (uint32_t)(h / kScaleStages) & 1u, abort))) break;
-          tc_fence_after();
-          sa = tmem + kColScale + 12 * (h & 1);
-          if (lane == 0) {
-            const uint32_t scales = base + kScales + hs * kScaleStage;
-            copy_scales_pair(sa, scales);
-            copy_scales_pair(sa + 4, scales + 512);
-            copy_scales_pair(sa + 8, scales + 1024);
-            commit_pair(&bar.scale_empty[hs]);
-          }
-          ++h;
-        }
-        if (!(ok = pair_wait(&bar.full[s], (uint32_t)(g / kStages) & 1u, abort))) break;
+      for (int i0 = 0; i0 < blocks && ok; i0 += kQuad) {
+        if (!(ok = pair_wait(&bar.scale_full[hs], scale_turn, abort))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t at = base + s * kStage, idesc = idesc_fp8(kTile, kTile, i % kQuad);
-          const uint64_t a = desc_k(at), b = desc_k(at + kOperand);
+        const uint32_t sa = tmem + kColScale + 12 * (hs & 1), scales = base + kScales + hs * kScaleStage;
+        copy_scales_if<true>(leader, sa, scales);
+        copy_scales_if<true>(leader, sa + 4, scales + 512);
+        copy_scales_if<true>(leader, sa + 8, scales + 1024);
+        commit_pair_if(leader, &bar.scale_empty[hs]);
+        if (++hs == kScaleStages) hs = 0, scale_turn ^= 1;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_fp8_pair(d, a + 2 * k, b + 2 * k, idesc, sa, sa + 4, i > 0 || k > 0);
-          commit_pair(&bar.empty[s]);
-          if (i == blocks - 1) commit_pair(&bar.done[n & 1]);
+        for (int j = 0; j < kQuad; ++j) {
+          if (i0 + j >= blocks || !(ok = issue_wait(&bar.full[s], turn, abort))) break;
+          tc_fence_after();
+          const uint32_t at = base + s * kStage;
+          umma4_fp8_if<true>(leader, d, desc_k(at), desc_k(at + kOperand), idesc_fp8(kTile, kTile, j), sa, sa + 4,
+                             i0 + j > 0);
+          commit_pair_if(leader, &bar.empty[s]);
+          if (++s == kStages) s = 0, turn ^= 1;
         }
-        __syncwarp();
       }
+      if (ok) commit_pair_if(leader, &bar.done[n & 1]);
     }
   } else {
     int n = 0;
@@ -227,31 +211,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.early), 0));
         }
         const int n0 = at.y * kTile + 32 * c;
-        if (m >= p.M || n0 >= p.N) continue;
-        if (vec) {
-          constexpr int V = 16 / sizeof(Out);
+        if (m < p.M && n0 < p.N) {
+          if (vec) {
+            constexpr int V = 16 / sizeof(Out);
 #pragma unroll
-          for (int k = 0; k < 32; k += V) {
-            if (n0 + k >= p.N) break;
-            uint4 u;
-            if constexpr (sizeof(Out) == 4)
-              u = make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]),
-                             __float_as_uint(v[k + 3]));
-            else
-              u = make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
-                             pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
-            *reinterpret_cast<uint4*>(out + n0 + k) = u;
-          }
-        } else {
+            for (int k = 0; k < 32; k += V) {
+              if (n0 + k >= p.N) break;
+              uint4 u;
+              if constexpr (sizeof(Out) == 4)
+                u = make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]),
+                               __float_as_uint(v[k + 3]));
+              else
+                u = make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                               pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+              *reinterpret_cast<uint4*>(out + n0 + k) = u;
+            }
+          } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            if (n0 + k >= p.N) break;
-            if constexpr (sizeof(Out) == 4)
-              out[n0 + k] = v[k];
-            else
-              out[n0 + k] = f_to_bf16(v[k]);
+            for (int k = 0; k < 32; ++k) {
+              if (n0 + k >= p.N) break;
+              if constexpr (sizeof(Out) == 4)
+                out[n0 + k] = v[k];
+              else
+                out[n0 + k] = f_to_bf16(v[k]);
+            }
           }
         }
+        __syncwarp();  // loads from tensor memory are the whole warp's
       }
     }
   }
