@@ -3,9 +3,9 @@
 //
 // A stage holds 128 bytes of K, one scale block, of each row of both operands, 128-byte swizzled.  A
 // product takes its scales from tensor memory, one byte of a 32-bit word per row, which its instruction
-// names: a word holds the scales of four blocks one after the other, as they lie in memory, so that scales are
-// brought once in four stages (once a stage, each byte four times, they took longer than the products: 1040 us
-// instead of 365 for 16384 x 4096 x 8192).  Words of rows 32 c .. 32 c + 31 of 128 are in column c, the same in
+// names: a word holds the scales of four blocks one after the other, as they lie in memory, and scales are brought
+// four words at a time, once in 16 stages (brought once a stage, each byte four times, they took longer than
+// the products: 1040 us for 16384 x 4096 x 8192).  Words of rows 32 c .. 32 c + 31 of 128 are in column c, the same in
 // each of the four quarters of the lanes.  They get there by a copy of 512 bytes of shared memory, line r
 // holding the words of rows r, r + 32, r + 64, r + 96.
 #pragma once
@@ -81,30 +81,38 @@ __device__ __forceinline__ bool issue_wait(uint64_t* bar, uint32_t parity, volat
   return warp_wait_long(smem_u32(bar), parity, abort);
 }
 
-constexpr int kQuad = 4;  // scale blocks, and stages, to a word
+constexpr int kQuad = 4;            // scale blocks, and stages, to a word
+constexpr int kGroup = 4 * kQuad;  // and to a group of words
 
-// Scale words of ROWS rows per lane, each of the four blocks from i on, loaded one word ahead of their use:
-// loads first, then whatever waits for them.
+// Groups of scale words of ROWS rows per lane: the 16 blocks from i on, loaded one group ahead of their use,
+// all loads before anything that waits for them.  Blocks behind a row's last get any scale: nothing uses them.
 template <int ROWS>
 struct ScaleWords {
   const uint8_t* row[ROWS];
   bool live[ROWS];
   bool words;  // rows and their starts are whole words
   int blocks;  // of a row
-  uint32_t next[ROWS][kQuad];
+  uint32_t next[ROWS][4];
   __device__ __forceinline__ void fetch(int i) {
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (words) {
-        next[r][0] = live[r] ? *reinterpret_cast<const uint32_t*>(row[r] + i) : 0x7f7f7f7fu;
-      } else {
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-        for (int j = 0; j < kQuad; ++j) next[r][j] = live[r] && i + j < blocks ? row[r][i + j] : 0x7fu;
+      for (int q = 0; q < 4; ++q) {
+        next[r][q] = 0x7f7f7f7fu;  // 1
+        if (words && live[r] && i + q * kQuad < blocks)
+          next[r][q] = *reinterpret_cast<const uint32_t*>(row[r] + i + q * kQuad);
       }
-    }
+    if (!words) fetch_bytes(i);
   }
-  __device__ __forceinline__ uint32_t word(int r) const {
-    return words ? next[r][0] : next[r][0] | next[r][1] << 8 | next[r][2] << 16 | next[r][3] << 24;
+  __device__ __forceinline__ void fetch_bytes(int i) {
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      uint32_t b[kGroup];
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) b[j] = live[r] && i + j < blocks ? row[r][i + j] : 0x7fu;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) next[r][q] = b[4 * q] | b[4 * q + 1] << 8 | b[4 * q + 2] << 16 | b[4 * q + 3] << 24;
+    }
   }
 };
 

@@ -123,18 +123,24 @@ __global__ void __launch_bounds__(kThreads)
       x.row[c] = RAW ? nullptr : p.x_scales + (size_t)m * all;
     }
     w.fetch(begin), x.fetch(begin);
-    for (int i = begin, h = 0; i < end; i += kQuad, ++h) {
-      uint32_t u[R];
-      const uint32_t v = w.word(0);
+    for (int i = begin, h = 0; i < end && ok; i += kGroup) {
+      uint32_t v[4], u[4][4];
 #pragma unroll
-      for (int c = 0; c < R; ++c) u[c] = x.word(c);
-      if (i + kQuad < end) w.fetch(i + kQuad), x.fetch(i + kQuad);
-      if (!scales_free(h)) break;
-      const uint32_t to = base + S::kScales + h % SQ * S::kScaleStage + lane * 16;
-      st_shared_v4(to, make_uint4(v, v, v, v));
-      if (!RAW) st_shared_v4(to + 512, make_uint4(u[0], u[R > 1 ? 1 : 0], u[R > 2 ? 2 : 0], u[R > 3 ? 3 : 0]));
-      fence_proxy_async_smem();
-      warp_arrive(&bar.scale_full[h % SQ], lane);
+      for (int q = 0; q < 4; ++q) {
+        v[q] = w.next[0][q];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[q][r] = x.next[r < R ? r : 0][q];
+      }
+      if (i + kGroup < end) w.fetch(i + kGroup), x.fetch(i + kGroup);
+#pragma unroll
+      for (int q = 0; q < 4; ++q, ++h) {
+        if (i + q * kQuad >= end || !scales_free(h)) break;
+        const uint32_t to = base + S::kScales + h % SQ * S::kScaleStage + lane * 16;
+        st_shared_v4(to, make_uint4(v[q], v[q], v[q], v[q]));
+        if (!RAW) st_shared_v4(to + 512, make_uint4(u[q][0], u[q][1], u[q][2], u[q][3]));
+        fence_proxy_async_smem();
+        warp_arrive(&bar.scale_full[h % SQ], lane);
+      }
     }
   } else if (warp == kWarpMma) {
     const bool leader = elect_one_sync();

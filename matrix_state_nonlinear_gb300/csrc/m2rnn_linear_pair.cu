@@ -5,7 +5,7 @@
 // 128 rows of tokens and 128 of weights a stage and the product, issued by the first block, reads both
 // blocks' shared memory, so that a stage's 32 KB feed 512 cycles of an SM's tensor core (a 128 x 256 tile
 // of one SM would load 48).  Block r's accumulators hold tokens 128 r .. of the tile, a token per lane, all 256
-// channels, and leave by 16-byte stores of eight channels a thread.  Blocks stay on their SM and take tiles
+// channels, and leave by 32-byte stores, a whole sector each.  Blocks stay on their SM and take tiles
 // in turn; the next tile's products run while the last one's results leave.  Two buffers of 256 columns and
 // the scales would need 536 columns of tensor memory, so the buffers overlap in 32 columns, which are read
 // first: the next tile starts as soon as these are out.
@@ -18,12 +18,12 @@ constexpr int kRows = 128;                // rows of each operand per block and 
 constexpr int kTile = 2 * kRows;          // tokens and channels of a tile
 constexpr int kStages = 6;
 constexpr int kOperand = kRows * kBlockK, kStage = 2 * kOperand;
-constexpr int kScaleStages = 4, kScaleStage = 512 + 1024;  // words of 128 tokens and 256 channels
+constexpr int kScaleStages = 3, kScaleWord = 512 + 1024, kScaleStage = 4 * kScaleWord;  // 128 tokens, 256 channels
 constexpr int kScales = kStages * kStage;
 constexpr int kSmemBytes = kScales + kScaleStages * kScaleStage + 1024;  // 1024: to align the first stage
 constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kThreads = 224;
 constexpr int kTmemCols = 512, kColSecond = 224, kColScale = 480;  // scales: two sets of 4 + 8 columns
-constexpr int kGroup = 8;                 // token tiles that share a run of channel tiles
+constexpr int kRun = 8;                   // token tiles that share a run of channel tiles
 
 struct Bars {
   uint64_t full[kStages], empty[kStages], scale_full[kScaleStages], scale_empty[kScaleStages], done[2], early;
@@ -54,11 +54,11 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(~0u, mbar_wait_cluster(bar, parity, kWaitLimitCycles, abort));
 }
 
-// Tile t of the raster: runs of kGroup token tiles by all channel tiles, so that the tiles in flight share
+// Tile t of the raster: runs of kRun token tiles by all channel tiles, so that the tiles in flight share
 // their operands in L2.
 __device__ __forceinline__ int2 tile_at_index(int t, int token_tiles, int channel_tiles) {
-  const int run = t / (kGroup * channel_tiles), first = run * kGroup, wide = min(kGroup, token_tiles - first);
-  const int in = t - run * kGroup * channel_tiles;
+  const int run = t / (kRun * channel_tiles), first = run * kRun, wide = min(kRun, token_tiles - first);
+  const int in = t - run * kRun * channel_tiles;
   return make_int2(first + in % wide, in / wide);
 }
 
@@ -116,7 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       }
     }
   } else if (warp == kWarpScale) {
-    // Words are counted over all tiles as the steps are: word h is slot h % kScaleStages.
+    // Groups are counted over all tiles as the steps are: group h is slot h % kScaleStages.
     ScaleWords<4> x;
     ScaleWords<2> w;
     x.blocks = w.blocks = blocks;
@@ -141,19 +141,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     if (pair < tiles) aim(pair);
     int h = 0;
     for (int t = pair; t < tiles && ok; t += pairs) {
-      for (int i = 0; i < blocks; i += kQuad, ++h) {
-        const uint4 u = make_uint4(x.word(0), x.word(1), x.word(2), x.word(3));
-        const uint32_t v0 = w.word(0), v1 = w.word(1);
-        if (i + kQuad < blocks)
-          x.fetch(i + kQuad), w.fetch(i + kQuad);
+      for (int i = 0; i < blocks; i += kGroup, ++h) {
+        uint32_t u[4][4], v[2][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) u[q][r] = x.next[r][q];
+          v[0][q] = w.next[0][q], v[1][q] = w.next[1][q];
+        }
+        if (i + kGroup < blocks)
+          x.fetch(i + kGroup), w.fetch(i + kGroup);
         else if (t + pairs < tiles)
           aim(t + pairs);
         const int s = h % kScaleStages;
         if (h >= kScaleStages && !(ok = warp_wait(&bar.scale_empty[s], (uint32_t)(h / kScaleStages - 1) & 1u, abort))) break;
         const uint32_t to = base + kScales + s * kScaleStage + lane * 16;
-        st_shared_v4(to, u);
-        st_shared_v4(to + 512, make_uint4(v0, v0, v0, v0));
-        st_shared_v4(to + 1024, make_uint4(v1, v1, v1, v1));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          st_shared_v4(to + q * kScaleWord, make_uint4(u[q][0], u[q][1], u[q][2], u[q][3]));
+          st_shared_v4(to + q * kScaleWord + 512, make_uint4(v[0][q], v[0][q], v[0][q], v[0][q]));
+          st_shared_v4(to + q * kScaleWord + 1024, make_uint4(v[1][q], v[1][q], v[1][q], v[1][q]));
+        }
+        // A release that other blocks see takes some 1800 cycles: once in 16 stages that passes unnoticed.
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.scale_full[s]), 0));
@@ -163,19 +172,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     // Stage s and scale slot hs, with the parities of their turns.
     const bool leader = elect_one_sync();
     int s = 0, hs = 0, n = 0;
-    uint32_t turn = 0, scale_turn = 0;
+    uint32_t turn = 0, scale_turn = 0, scales = 0;
     for (int t = pair; rank == 0 && t < tiles && ok; t += pairs, ++n) {
-      if (n > 0 && !(ok = pair_wait(&bar.early, (uint32_t)(n - 1) & 1u, abort))) break;
+      if (n > 0 && !(ok = warp_wait(&bar.early, (uint32_t)(n - 1) & 1u, abort))) break;
+      tc_fence_after();
       const uint32_t d = tmem + (n & 1 ? kColSecond : 0);
       for (int i0 = 0; i0 < blocks && ok; i0 += kQuad) {
-        if (!(ok = pair_wait(&bar.scale_full[hs], scale_turn, abort))) break;
-        tc_fence_after();
-        const uint32_t sa = tmem + kColScale + 12 * (hs & 1), scales = base + kScales + hs * kScaleStage;
+        if (i0 % kGroup == 0) {
+          if (!(ok = pair_wait(&bar.scale_full[hs], scale_turn, abort))) break;
+          tc_fence_after();
+          scales = base + kScales + hs * kScaleStage;
+        }
+        const uint32_t sa = tmem + kColScale + 12 * (i0 / kQuad & 1);
         copy_scales_if<true>(leader, sa, scales);
         copy_scales_if<true>(leader, sa + 4, scales + 512);
         copy_scales_if<true>(leader, sa + 8, scales + 1024);
-        commit_pair_if(leader, &bar.scale_empty[hs]);
-        if (++hs == kScaleStages) hs = 0, scale_turn ^= 1;
+        scales += kScaleWord;
+        if (i0 % kGroup == kGroup - kQuad || i0 + kQuad >= blocks) {
+          commit_pair_if(leader, &bar.scale_empty[hs]);
+          if (++hs == kScaleStages) hs = 0, scale_turn ^= 1;
+        }
 #pragma unroll
         for (int j = 0; j < kQuad; ++j) {
           if (i0 + j >= blocks || !(ok = issue_wait(&bar.full[s], turn, abort))) break;
@@ -208,23 +224,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         if (j == 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bar.early), 0));
+          // Nothing but these loads, which are complete, has to come before: a release that other blocks see would
+          // wait for the last tile's stores.
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(&bar.early), 0))
+                         : "memory");
         }
         const int n0 = at.y * kTile + 32 * c;
         if (m < p.M && n0 < p.N) {
           if (vec) {
-            constexpr int V = 16 / sizeof(Out);
+            constexpr int V = 32 / sizeof(Out);
 #pragma unroll
             for (int k = 0; k < 32; k += V) {
-              if (n0 + k >= p.N) break;
-              uint4 u;
-              if constexpr (sizeof(Out) == 4)
-                u = make_uint4(__float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]),
-                               __float_as_uint(v[k + 3]));
-              else
-                u = make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
-                               pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
-              *reinterpret_cast<uint4*>(out + n0 + k) = u;
+              uint32_t u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if constexpr (sizeof(Out) == 4)
+                  u[e] = __float_as_uint(v[k + e]);
+                else
+                  u[e] = pack_bf16x2(v[k + 2 * e], v[k + 2 * e + 1]);
+              }
+              if (n0 + k < p.N)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + n0 + k), "r"(u[0]),
+                             "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                             : "memory");
             }
           } else {
 #pragma unroll
@@ -268,7 +291,7 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
     return cudaErrorNotSupported;
   const int tokens = (p.M + kTile - 1) / kTile, channels = (p.N + kTile - 1) / kTile;
   const long long tiles = (long long)tokens * channels;
-  const bool vec = p.N % (16 / (int)sizeof(Out)) == 0 && aligned_to(p.out, 16);
+  const bool vec = p.N % (32 / (int)sizeof(Out)) == 0 && aligned_to(p.out, 32);
   const unsigned pairs = (unsigned)(tiles < 76 ? tiles : 76);
   linear_pair_kernel<Out><<<2 * pairs, kThreads, kSmemBytes, stream>>>(mx, mw, p, tokens, channels, vec);
   return cudaGetLastError();
