@@ -10,7 +10,7 @@
 // the tensor core however few tokens there are) by NT tokens.  Where that gives fewer blocks than SMs, a
 // cluster of up to 8 blocks shares a tile, each with a stretch of K, and adds up its parts through
 // distributed shared memory, in the order of K.  Up to 16 tokens of bf16 are quantised on the way in, by the
-// warps that later write the results.
+// warps that later write the results (32 tokens take 25 us that way, 13 with a launch before, 4096 x 8192).
 #include "m2rnn_fp8_tc.cuh"
 
 namespace m2rnn {
@@ -45,9 +45,9 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-// Eight bf16 values of a row from k on, zeros behind its K values.
-__device__ __forceinline__ uint4 load_raw(const uint16_t* row, int k, int K, bool vec) {
-  if (vec && k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
+// Eight bf16 values of a row from k on, zeros behind its K values.  The general case stays out of line: the
+// loop it would be unrolled into does not fit the instruction cache.
+__device__ __noinline__ uint4 load_any(const uint16_t* row, int k, int K) {
   uint32_t v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = k + i < K ? row[k + i] : 0u;
@@ -70,13 +70,24 @@ __global__ void __launch_bounds__(kThreads)
             end = (int)((long long)all * (rank + 1) / split);
   volatile int* abort = &bar.abort;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&bar.full[s], RAW ? 1 + kEpilogueWarps : 1), mbar_init(&bar.empty[s], 1);
+  const int steps = end - begin;
+  // Step g is stage g % ST, its turn g / ST; its scales are byte g % 4 of word g / 4.
+  auto load = [&](int g) {
+    const int s = g % ST, k = (begin + g) * kBlockK;
+    const uint32_t to = base + s * S::kStage;
+    mbar_arrive_expect_tx(&bar.full[s], RAW ? S::kA : S::kStage);
+    tma_load_2d(to, &map_w, &bar.full[s], k, n0);
+    if (!RAW) tma_load_2d(to + S::kA, &map_x, &bar.full[s], k, m0);
+  };
+  if (warp == kWarpLoad && lane == 0) {  // the first loads leave before anything else
+    for (int s = 0; s < ST; ++s) mbar_init(&bar.full[s], 1), mbar_init(&bar.empty[s], 1);
     for (int s = 0; s < SQ; ++s)
       mbar_init(&bar.scale_full[s], RAW ? 1 + kEpilogueWarps : 1), mbar_init(&bar.scale_empty[s], 1);
     mbar_init(&bar.done, 1);
     bar.abort = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    for (int g = 0; g < min(ST, steps); ++g) load(g);
   }
   if (warp == kWarpMma) tmem_alloc(&bar.tmem, S::kTmemCols);
   tc_fence_before();
@@ -84,26 +95,18 @@ __global__ void __launch_bounds__(kThreads)
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
   bool ok = true;
-  // Step i (from begin) is stage (i - begin) % ST, its turn (i - begin) / ST.
   auto stage_free = [&](int g) {
     if (g >= ST) ok = warp_wait(&bar.empty[g % ST], (uint32_t)(g / ST - 1) & 1u, abort);
     return ok;
   };
-  // Its scales are byte (i - begin) % 4 of word (i - begin) / 4.
   auto scales_free = [&](int h) {
     if (h >= SQ) ok = warp_wait(&bar.scale_empty[h % SQ], (uint32_t)(h / SQ - 1) & 1u, abort);
     return ok;
   };
 
   if (warp == kWarpLoad) {
-    for (int g = 0; g < end - begin && stage_free(g); ++g) {
-      if (lane == 0) {
-        const int s = g % ST, k = (begin + g) * kBlockK;
-        const uint32_t to = base + s * S::kStage;
-        mbar_arrive_expect_tx(&bar.full[s], RAW ? S::kA : S::kStage);
-        tma_load_2d(to, &map_w, &bar.full[s], k, n0);
-        if (!RAW) tma_load_2d(to + S::kA, &map_x, &bar.full[s], k, m0);
-      }
+    for (int g = ST; g < steps && stage_free(g); ++g) {
+      if (lane == 0) load(g);
       __syncwarp();
     }
   } else if (warp == kWarpScale) {
@@ -168,55 +171,70 @@ __global__ void __launch_bounds__(kThreads)
     if (ok) umma_commit_if(leader, &bar.done);
   } else {
     if constexpr (RAW) {
-      // 16 threads take 128 values of a row, eight each; rows r and r + 8, four steps ahead.
-      const int r = threadIdx.x >> 4, piece = threadIdx.x & 15;
-      uint4 next[4][2];
-      auto fetch = [&](int i0) {
+      // 16 threads take 128 values of a row, eight each, of rows r, r + 8, ...: a word's four steps at a time, the
+      // next four on their way.
+      constexpr int H = NT / 8;
+      const int r = threadIdx.x >> 4, piece = threadIdx.x & 15, rows = p.M - m0;
+      uint4 next[kQuad][H];
+      auto fetch = [&](int g0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kQuad; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool live = i0 + j < end && r + 8 * h < p.M;
-            next[j][h] = live ? load_raw(p.raw + (r + 8 * h) * p.x_row, (i0 + j) * kBlockK + piece * 8, p.K, raw_vec)
-                              : make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < H; ++h) {
+            const uint16_t* row = p.raw + (m0 + r + 8 * h) * p.x_row;
+            const int k = (begin + g0 + j) * kBlockK + piece * 8;
+            const bool live = g0 + j < steps && r + 8 * h < rows;
+            next[j][h] = make_uint4(0, 0, 0, 0);
+            if (raw_vec && live && k < p.K) next[j][h] = *reinterpret_cast<const uint4*>(row + k);
+            if (!raw_vec && live) next[j][h] = load_any(row, k, p.K);
           }
       };
-      fetch(begin);
-      for (int i0 = begin; i0 < end && ok; i0 += 4) {
-        uint4 now[4][2];
+      fetch(0);
+      for (int g0 = 0, w = 0; g0 < steps && scales_free(w); g0 += kQuad, ++w) {
+        const uint32_t scales = base + S::kScales + w % SQ * S::kScaleStage + 512;
+        uint4 word[kQuad][H];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) now[j][0] = next[j][0], now[j][1] = next[j][1];
-        if (i0 + 4 < end) fetch(i0 + 4);
-        const int h = (i0 - begin) / kQuad;
-        if (!scales_free(h)) break;
-        const uint32_t scales = base + S::kScales + h % SQ * S::kScaleStage + 512;
+        for (int j = 0; j < kQuad; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (i0 + j >= end || !ok || !stage_free(i0 + j - begin)) continue;
-          const int s = (i0 + j - begin) % ST;
-          const uint32_t to = base + s * S::kStage + S::kA;
+          for (int h = 0; h < H; ++h) word[j][h] = next[j][h];
+        if (g0 + kQuad < steps) fetch(g0 + kQuad);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t u[4] = {now[j][h].x, now[j][h].y, now[j][h].z, now[j][h].w};
-            uint32_t top = 0, q[4];
+        for (int j = 0; j < kQuad; ++j) {
+          if (g0 + j >= steps || !stage_free(g0 + j)) break;
+          const uint4(&now)[H] = word[j];
+          const uint32_t to = base + (g0 + j) % ST * S::kStage + S::kA;
+          uint32_t top[H];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = max(top, max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
+          for (int h = 0; h < H; ++h) {
+            const uint32_t u[4] = {now[h].x, now[h].y, now[h].z, now[h].w};
+            top[h] = 0;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-            const uint32_t e = scale_exponent(top);
+            for (int i = 0; i < 4; ++i) top[h] = max(top[h], max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              if (8 * h < rows) top[h] = max(top[h], __shfl_xor_sync(~0u, top[h], o));
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            if (8 * h >= rows) break;  // products of rows that are not there go nowhere
+            const uint32_t u[4] = {now[h].x, now[h].y, now[h].z, now[h].w}, e = scale_exponent(top[h]);
             const float by = inverse_scale(e);
+            uint32_t q[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = pack_e4m3x2(bf16_lo(u[i]) * by, bf16_hi(u[i]) * by);
             asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(tile_at(to, r + 8 * h, piece >> 1) + (piece & 1) * 8),
-                         "r"(q[0] | q[1] << 16), "r"(q[2] | q[3] << 16)
-                         : "memory");
+                         "r"(q[0] | q[1] << 16), "r"(q[2] | q[3] << 16));
+            // Row m's word is in line m % 32, word m / 32.
             if (piece == 0)
-              asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (r + 8 * h) * 16 + j), "r"(e) : "memory");
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (r + 8 * h) % 32 * 16 + (r + 8 * h) / 32 * 4 + j),
+                           "r"(e));
           }
-          fence_proxy_async_smem();
-          warp_arrive(&bar.full[s], lane);
         }
-        if (ok) warp_arrive(&bar.scale_full[h % SQ], lane);
+        if (!ok) break;
+        fence_proxy_async_smem();
+        warp_arrive(&bar.scale_full[w % SQ], lane);
       }
     }
     if (ok) ok = warp_wait(&bar.done, 0, abort);
@@ -303,8 +321,11 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
       (!RAW && !byte_map(enc, &mx, p.x, p.K, p.M, p.x_row, NT)))
     return cudaErrorNotSupported;
   const long long tokens = (p.M + NT - 1) / NT, tiles = tokens * ((p.N + MT - 1) / MT);
+  // As many blocks per tile as the SMs allow, each with a word of scales, four steps, at the least (64 and 128
+  // tokens, 2048 x 1024: 6.2 and 7.7 us; with two steps each 7.1 and 9.5, the parts' sum costs more than it
+  // saves; with the whole of K in a block 6.9 and 8.5, and 16.4 and 18.1 us instead of 7.5 and 9.0 for K = 8192).
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 152 && split * 2 <= scale_blocks(p.K)) split *= 2;
+  while (split < 8 && tiles * split * 2 <= 152 && split * 2 * kQuad <= scale_blocks(p.K)) split *= 2;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)(tiles * split));
   c.blockDim = dim3(kThreads);
@@ -315,7 +336,7 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   a.val.clusterDim.x = (unsigned)split, a.val.clusterDim.y = a.val.clusterDim.z = 1;
   c.attrs = &a;
   c.numAttrs = 1;
-  const bool raw_vec = RAW && aligned_to(p.raw, 16) && p.x_row % 8 == 0;
+  const bool raw_vec = RAW && aligned_to(p.raw, 16) && p.x_row % 8 == 0 && p.K % 8 == 0;
   const bool vec = p.N % 4 == 0 && aligned_to(p.out, 4 * sizeof(Out));
   return cudaLaunchKernelEx(&c, kernel, mw, mx, p, (int)tokens, split, raw_vec, vec);
 }

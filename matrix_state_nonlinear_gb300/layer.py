@@ -59,7 +59,12 @@ def _byte_rows(t, name, shape, dev):
 def _new_bytes(like, shape):
     """An e4m3 tensor whose rows start on 16-byte boundaries."""
     D = shape[-1]
-    return torch.empty((*shape[:-1], (D + 15) // 16 * 16), dtype=FP8, device=like.device)[..., :D]
+    if D % 16 == 0:
+        return torch.empty(shape, dtype=FP8, device=like.device)
+    row, strides = (D + 15) // 16 * 16, [1]
+    for n in reversed(shape[1:]):
+        strides.append(row if len(strides) == 1 else strides[-1] * n)
+    return torch.empty_strided(shape, strides[::-1], dtype=FP8, device=like.device)
 
 
 def _blocks(n):
