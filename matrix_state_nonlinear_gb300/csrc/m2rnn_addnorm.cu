@@ -192,10 +192,117 @@ __global__ void __launch_bounds__(512)
   }
 }
 
-// Block b takes rows b, + blocks, ..., the next row loaded while one is computed; its channels' part of dw
-// adds up in registers and goes to row b of `part`.
+// 16 bytes to shared memory without passing through registers, by way of L1 (SECTORS: where a thread's next
+// copy is the other half of the sector); a thread's own copies are complete once at most N of its later groups
+// are not.
+template <bool SECTORS>
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  if constexpr (SECTORS)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The rows of h, dout and dh that a block reads, on their way ahead of their use: kAhead rows in shared memory,
+// where each thread reads what it has copied itself (no barrier), or, at any alignment, one row in registers.
+// Four rows for a bf16 stream of up to 8192 channels; as many of a float32 one would leave room for half the
+// blocks on an SM (65536 x 2048: 417 us instead of 325 with two).
+template <typename T, int R>
+constexpr int kAhead = R * sizeof(T) <= 4 && sizeof(T) == 2 ? 4 : R * sizeof(T) <= 8 ? 2 : 1;
+template <typename T, int R>
+constexpr int kRingPerThread = kAhead<T, R> * (2 * (int)sizeof(T) / 2 + 1) * R * 16;  // bytes
 template <typename T, bool VEC, int R>
-__global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(AddNormBackwardProblem p, float* __restrict__ part) {
+struct RowStream {
+  static constexpr int kRows = VEC ? kAhead<T, R> : 1, kParts = sizeof(T) / 2;  // 16-byte pieces of eight values of the stream
+  const AddNormBackwardProblem& p;
+  const int chunks;
+  uint4* own;  // [kRows][kParts + 1 + kParts][R][threads]
+  int at = 0, to = 0;
+  Raw8<T, VEC> hr[R], er[R];
+  Raw8<uint16_t, VEC> dr[R];
+
+  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, int chunks_, uint4* smem)
+      : p(p_), chunks(chunks_), own(smem + threadIdx.x) {}
+  __device__ __forceinline__ uint4* slot(int stage, int part, int r) const {
+    return own + ((stage * (2 * kParts + 1) + part) * R + r) * blockDim.x;
+  }
+  __device__ __forceinline__ void start(long long row) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int c = threadIdx.x + r * blockDim.x;
+        if (c < chunks) {
+          const long long i = row * p.D + 8 * c;
+          const T *h = static_cast<const T*>(p.h) + i, *e = static_cast<const T*>(p.dh) + i;
+          if constexpr (VEC) {
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) copy16<kParts == 2>(smem_u32(slot(to, k, r)), reinterpret_cast<const uint4*>(h) + k);
+            copy16<false>(smem_u32(slot(to, kParts, r)), p.dout + i);
+            if (p.dh)
+#pragma unroll
+              for (int k = 0; k < kParts; ++k)
+                copy16<kParts == 2>(smem_u32(slot(to, kParts + 1 + k, r)), reinterpret_cast<const uint4*>(e) + k);
+          } else {
+            const int n = chunk_width(c, p.D);
+            hr[r].load(h, n);
+            dr[r].load(p.dout + i, n);
+            if (p.dh) er[r].load(e, n);
+          }
+        }
+      }
+    }
+    if constexpr (VEC) {
+      copies_commit();
+      to = to + 1 == kRows ? 0 : to + 1;
+    }
+  }
+  __device__ __forceinline__ void begin(long long row, long long step) {
+#pragma unroll
+    for (int i = 0; i < (VEC ? kRows - 1 : 1); ++i) start(row + i * step);
+  }
+  // The values of `row`, zeros behind the last channel; the next row that is not on its way yet starts.
+  __device__ __forceinline__ void next(long long row, long long step, float2 (&h)[R][4], float2 (&d)[R][4],
+                                       float2 (&e)[R][4]) {
+    if constexpr (VEC) {
+      start(row + (kRows - 1) * step);
+      copies_wait<kRows - 1>();
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[r][i] = d[r][i] = e[r][i] = pair(0.f);
+      if (threadIdx.x + r * blockDim.x < chunks) {
+        if constexpr (VEC) {
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) hr[r].u[k] = *slot(at, k, r);
+          dr[r].u[0] = *slot(at, kParts, r);
+          if (p.dh)
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) er[r].u[k] = *slot(at, kParts + 1 + k, r);
+        }
+        hr[r].get(h[r]);
+        dr[r].get(d[r]);
+        if (p.dh) er[r].get(e[r]);
+      }
+    }
+    if constexpr (VEC)
+      at = at + 1 == kRows ? 0 : at + 1;
+    else
+      start(row + step);
+  }
+};
+
+// Block b takes rows b, + blocks, ...; its channels' part of dw adds up in registers and goes to row b of
+// `part`.
+template <typename T, bool VEC, int R>
+__global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
+    add_rmsnorm_backward_kernel(AddNormBackwardProblem p, float* __restrict__ part) {
+  extern __shared__ uint4 ring[];
   const int T_ = blockDim.x, chunks = (p.D + 7) / 8;
   const float inv_d = 1.f / (float)p.D;
   float2 dw[R][4], w[R][4];
@@ -210,42 +317,19 @@ __global__ void __launch_bounds__(512) add_rmsnorm_backward_kernel(AddNormBackwa
       if (c >= chunks) w[r][i] = pair(0.f);
     }
   }
-  Raw8<T, VEC> hr[R], er[R];
-  Raw8<uint16_t, VEC> dr[R];
-  auto load = [&](long long row) {
-    if (row >= p.rows) return;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int c = threadIdx.x + r * T_;
-      if (c < chunks) {
-        const long long at = row * p.D + 8 * c;
-        const int n = chunk_width(c, p.D);
-        hr[r].load(static_cast<const T*>(p.h) + at, n);
-        dr[r].load(p.dout + at, n);
-        if (p.dh) er[r].load(static_cast<const T*>(p.dh) + at, n);
-      }
-    }
-  };
-  load(blockIdx.x);
+  RowStream<T, VEC, R> rows(p, chunks, ring);
+  rows.begin(blockIdx.x, gridDim.x);
   int turn = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     float2 h[R][4], d[R][4], e[R][4], s1 = pair(0.f), s2 = pair(0.f);
+    rows.next(row, gridDim.x, h, d, e);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[r][i] = d[r][i] = e[r][i] = pair(0.f);
-      if (threadIdx.x + r * T_ < chunks) {
-        hr[r].get(h[r]);
-        dr[r].get(d[r]);
-        if (p.dh) er[r].get(e[r]);
-      }
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s1 = fma2(h[r][i], h[r][i], s1);
         s2 = fma2(mul2(d[r][i], w[r][i]), h[r][i], s2);
       }
-    }
-    load(row + gridDim.x);
     const float2 sum = block_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
     const float inv = rsqrtf(sum.x * inv_d + p.eps);
     const float2 iv = pair(inv), back = pair(-inv * inv * inv * (sum.y * inv_d));
@@ -305,7 +389,9 @@ cudaError_t with_chunks(int R, F f) {
 template <typename T, bool FP8, bool VEC>
 cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
                     cudaStream_t stream) {
-  const int R = chunks_each(p.D, p.rows >= 152 * 16 ? 4 : 1);
+  // Few rows are spread as wide as they go; of many, two chunks a thread (65536 x 2048: 153 us; one chunk
+  // 169, four 158; 8191 x 4096 in 8 bits: 58, 65, 64).
+  const int R = chunks_each(p.D, p.rows >= 152 * 16 ? 2 : 1);
   return with_chunks(R, [&](auto r) {
     constexpr int N = decltype(r)::value;
     const unsigned blocks = (unsigned)(p.rows < 0x7fffffff ? p.rows : 0x7fffffff);
@@ -332,9 +418,9 @@ cudaError_t dispatch(const AddNormProblem& p, bool vec, uint16_t* out, uint8_t* 
              : forward<uint16_t, FP8, false>(p, out, q, q_row, scales, stream);
 }
 
+// Blocks of the backward: 1024 threads for every SM.
 int backward_blocks(long long rows, int D) {
-  const long long most = 152LL * 4;
-  (void)D;
+  const long long most = 152LL * (1024 / threads_for(D, chunks_each(D, 1)));
   return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
 }
 
@@ -358,7 +444,12 @@ cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStr
   const cudaError_t err = with_chunks(chunks_each(p.D, 1), [&](auto r) {
     constexpr int R = decltype(r)::value;
     auto go = [&](auto kernel) {
-      kernel<<<blocks, threads_for(p.D, R), 0, stream>>>(p, p.ws);
+      const int threads = threads_for(p.D, R);
+      const int bytes = vec ? threads * (p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>) : 0;
+      // At every launch: the attribute belongs to the current device.
+      const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (attr != cudaSuccess) return attr;
+      kernel<<<blocks, threads, bytes, stream>>>(p, p.ws);
       return cudaGetLastError();
     };
     if (p.stream_f32)

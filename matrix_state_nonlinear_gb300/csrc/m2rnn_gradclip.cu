@@ -4,11 +4,15 @@
 //   norm = sqrt(sum over all values of g^2),   out = g min(1, max_norm / norm)
 //
 // Memory-bound: the norm reads every value once, the scaling reads and writes it once.  The tensors are a
-// table in the launch's parameters (no copy to the device), cut into chunks that the blocks take in turn.  A
-// chunk's squares are summed in float32 per thread (16 or 32 of them), everything above in 64 bits, so the
-// result hardly depends on the number of values; sums that float32 cannot hold, because the values are very
-// large or very small, are taken again in 64 bits.  Every block's sum has a place of its own and all are
-// added in the same order by every block of the second launch: no atomics, the same bits every time.
+// table in the launch's parameters (no copy to the device).  Those of 64 KB and more are laid end to end in units
+// of 8 KB, of which every block takes an equal stretch, so that blocks end together however the tensors are cut;
+// the scaling takes each stretch from its end, which the norm read last and L2 still holds.  Smaller tensors,
+// each of which costs a block a whole turn whatever its size, go to the blocks one by one.
+// A thread's squares are summed in float32 for one part (32 or 64 of them) and then as a pair of floats, hi and
+// lo, that loses nothing; blocks' sums are 64-bit ones.  The result hardly depends on the number of values.  Sums
+// that float32 cannot hold, because the values are very large or very small, are taken again in 64 bits.
+// Every block's sum has a place of its own and all are added in the same order by every block of the second
+// launch: no atomics, the same bits every time.
 #include <math.h>
 
 #include "m2rnn_layer.h"
@@ -18,14 +22,14 @@ namespace m2rnn {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kVecs = 4;                             // 16-byte accesses of a thread per chunk
-constexpr int kChunkBytes = kThreads * kVecs * 16;   // 32 KB of a tensor
+constexpr int kUnitBytes = kThreads * 16;
+constexpr int kVecs = 8;  // units of one tensor that a block takes at once, 16 bytes a thread of each
 
-// One launch's tensors: entry i owns the chunks from first[i] to first[i + 1].
+// One launch's tensors: entry i < large owns the units from first[i] to first[i + 1], the others are small.
 template <int N>
 struct Table {
-  int count, chunks;
-  int first[N];
+  int count, large, units;
+  int first[N + 1];
   unsigned long long in[N], out[N], values[N];  // values: the number of them times two, plus one for float32
 };
 
@@ -33,26 +37,49 @@ struct Part {
   const unsigned char* in;
   unsigned char* out;
   bool f32;
-  long long values;  // of this part
+  long long values;  // of this part, 0 when there are no more
 };
 
-// Chunk c of the table.
-template <int N>
-__device__ __forceinline__ Part part_of(const Table<N>& t, int c) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.first[mid] <= c)
-      lo = mid;
-    else
-      hi = mid - 1;
+// A block's stretch of units in parts of up to kVecs units of one tensor, forwards or backwards, and then its
+// small tensors.
+template <int N, bool BACK>
+struct Stretch {
+  const Table<N>& t;
+  int from, to, entry, small;
+  __device__ __forceinline__ Stretch(const Table<N>& t_) : t(t_), small(t_.large + blockIdx.x) {
+    from = (int)((long long)t.units * blockIdx.x / gridDim.x), to = (int)((long long)t.units * (blockIdx.x + 1) / gridDim.x);
+    const int u = BACK ? to - 1 : from;
+    int lo = 0, hi = t.large - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.first[mid] <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    entry = lo;
   }
-  const bool f32 = t.values[lo] & 1;
-  const long long each = kChunkBytes / (f32 ? 4 : 2), at = (long long)(c - t.first[lo]) * each;
-  return Part{reinterpret_cast<const unsigned char*>(t.in[lo]) + at * (f32 ? 4 : 2),
-              reinterpret_cast<unsigned char*>(t.out[lo]) + at * (f32 ? 4 : 2), f32,
-              min(each, (long long)(t.values[lo] >> 1) - at)};
-}
+  __device__ __forceinline__ Part next() {
+    int i = entry, n = kVecs;
+    long long off = 0;  // in units
+    if (from >= to) {
+      i = small, small += gridDim.x;
+      if (i >= t.count) return Part{nullptr, nullptr, true, 0};
+    } else if (BACK) {
+      if (t.first[i] >= to) i = --entry;
+      const int at = max(max(from, t.first[i]), to - kVecs);
+      n = to - at, off = at - t.first[i], to = at;
+    } else {
+      if (t.first[i + 1] <= from) i = ++entry;
+      n = min(min(to, t.first[i + 1]) - from, kVecs), off = from - t.first[i], from += n;
+    }
+    const bool f32 = t.values[i] & 1;
+    const int size = f32 ? 4 : 2, each = kUnitBytes / size;
+    return Part{reinterpret_cast<const unsigned char*>(t.in[i]) + off * kUnitBytes,
+                reinterpret_cast<unsigned char*>(t.out[i]) + off * kUnitBytes, f32,
+                min((long long)n * each, (long long)(t.values[i] >> 1) - off * each)};
+  }
+};
 
 __device__ __forceinline__ float value(const Part& p, long long i) {
   return p.f32 ? reinterpret_cast<const float*>(p.in)[i] : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p.in)[i]);
@@ -91,7 +118,7 @@ __device__ __noinline__ double squares64(uint4 u, bool f32) {
   }
   return s;
 }
-// Whether a sum of at most 32 squares lost something to float32's range: above it, or so small that squares
+// Whether a sum of at most 64 squares lost something to float32's range: above it, or so small that squares
 // below 2^-126 count.
 __device__ __forceinline__ bool out_of_range(float s) { return !(s < INFINITY) || s < 0x1p-100f; }
 
@@ -114,21 +141,41 @@ __device__ __forceinline__ double block_sum(double s) {
   return total;
 }
 
+// The 16-byte accesses of a part: their number and the first.
+struct Vecs {
+  int head;
+  long long count;
+  const uint4* in;
+  uint4* out;
+};
+__device__ __forceinline__ Vecs vecs_of(const Part& p, bool any) {
+  const int size = p.f32 ? 4 : 2, head = any ? head_of(p) : 0;
+  return Vecs{head, any ? (p.values - head) * size / 16 : 0, reinterpret_cast<const uint4*>(p.in + head * size),
+              reinterpret_cast<uint4*>(p.out + head * size)};
+}
+__device__ __forceinline__ void load(const Vecs& v, uint4 (&u)[kVecs]) {
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int at = threadIdx.x + i * kThreads;
+    u[i] = at < v.count ? v.in[at] : make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads) sum_squares_kernel(const __grid_constant__ Table<N> t, double* sums) {
-  double sum = 0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const Part p = part_of(t, c);
-    const int head = head_of(p), size = p.f32 ? 4 : 2, per = 16 / size;
-    const long long vecs = (p.values - head) / per;
-    const uint4* v = reinterpret_cast<const uint4*>(p.in + head * size);
-    uint4 u[kVecs];
+  Stretch<N, false> stretch(t);
+  double rare = 0;
+  float hi = 0.f, lo = 0.f;
+  Part p = stretch.next();
+  Vecs v = vecs_of(p, true);
+  uint4 u[kVecs];
+  load(v, u);
+  while (p.values > 0) {
+    const Part q = stretch.next();
+    const Vecs w = vecs_of(q, true);
+    uint4 ahead[kVecs];
+    load(w, ahead);
     float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int at = threadIdx.x + i * kThreads;
-      u[i] = at < vecs ? v[at] : make_uint4(0, 0, 0, 0);
-    }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) s += squares(u[i], p.f32);
     if (out_of_range(s)) {
@@ -137,18 +184,23 @@ __global__ void __launch_bounds__(kThreads) sum_squares_kernel(const __grid_cons
       for (int i = 0; i < kVecs; ++i) any |= u[i].x | u[i].y | u[i].z | u[i].w;
       if (any & 0x7fff7fffu)
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) sum += squares64(u[i], p.f32);
-    } else {
-      sum += s;
+        for (int i = 0; i < kVecs; ++i) rare += squares64(u[i], p.f32);
+    } else {  // hi + lo += s, exactly but for the rounding of lo
+      const float sum = hi + s, back = sum - hi;
+      lo += (hi - (sum - back)) + (s - back);
+      hi = sum;
     }
     // The values around the 16-byte accesses: at most 7 before and 7 behind.
-    const long long edge = p.values - vecs * per;
-    if (threadIdx.x < edge) {
-      const double x = value(p, threadIdx.x < head ? threadIdx.x : vecs * per + threadIdx.x);
-      sum += x * x;
+    const long long inner = v.count * (p.f32 ? 4 : 8);
+    if (threadIdx.x < p.values - inner) {
+      const double x = value(p, threadIdx.x < v.head ? threadIdx.x : inner + threadIdx.x);
+      rare += x * x;
     }
+    p = q, v = w;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) u[i] = ahead[i];
   }
-  sum = block_sum(sum);
+  const double sum = block_sum(rare + ((double)hi + (double)lo));
   if (threadIdx.x == 0) sums[blockIdx.x] = sum;
 }
 
@@ -171,77 +223,87 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* sums, int 
   if (threadIdx.x == 0) *norm = (float)n;
 }
 
-// Chunks from the last to the first: the last ones read are still in L2.
 template <int N>
 __global__ void __launch_bounds__(kThreads)
     clip_kernel(const __grid_constant__ Table<N> t, const double* sums, int count, float max_norm, float* norm,
                 bool in_place) {
+  Stretch<N, true> stretch(t);
+  // Whether 16 bytes of a part lie the same way where they are read and written.
+  auto alike = [](const Part& p) { return (((uint32_t)(uintptr_t)p.in ^ (uint32_t)(uintptr_t)p.out) & 15u) == 0; };
+  Part p = stretch.next();
+  Vecs v = vecs_of(p, alike(p));
+  uint4 u[kVecs];
+  load(v, u);  // on its way while the sums are added
   const double n = norm_of(sums, count);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // A norm that is infinite or NaN clips nothing.
   const bool clips = n > max_norm && n < INFINITY;
   if (in_place && !clips) return;
   const float by = clips ? (float)(max_norm / n) : 1.f;
-  for (int c = t.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-    const Part p = part_of(t, c);
-    const int size = p.f32 ? 4 : 2, per = 16 / size;
-    const bool same = (((uint32_t)(uintptr_t)p.in ^ (uint32_t)(uintptr_t)p.out) & 15u) == 0;
-    const int head = same ? head_of(p) : 0;
-    const long long vecs = same ? (p.values - head) / per : 0;
-    const uint4* v = reinterpret_cast<const uint4*>(p.in + head * size);
-    uint4* o = reinterpret_cast<uint4*>(p.out + head * size);
-    uint4 u[kVecs];
+  const float2 b = make_float2(by, by);
+  while (p.values > 0) {
+    const Part q = stretch.next();
+    const Vecs w = vecs_of(q, alike(q));
+    uint4 ahead[kVecs];
+    load(w, ahead);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      const int at = threadIdx.x + i * kThreads;
-      if (at < vecs) u[i] = v[at];
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int at = threadIdx.x + i * kThreads;
-      if (at >= vecs) break;
-      const float2 b = make_float2(by, by);
-      uint32_t* w = &u[i].x;
+      uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
       if (p.f32) {
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-          const float2 x = mul2(make_float2(__uint_as_float(w[j]), __uint_as_float(w[j + 1])), b);
-          w[j] = __float_as_uint(x.x), w[j + 1] = __float_as_uint(x.y);
+          const float2 y = mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), b);
+          x[j] = __float_as_uint(y.x), x[j + 1] = __float_as_uint(y.y);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 x = mul2(bf16x2_to_float2(w[j]), b);
-          w[j] = pack_bf16x2(x.x, x.y);
+          const float2 y = mul2(bf16x2_to_float2(x[j]), b);
+          x[j] = pack_bf16x2(y.x, y.y);
         }
       }
-      o[at] = u[i];
+      const int at = threadIdx.x + i * kThreads;
+      if (at < v.count) v.out[at] = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    for (long long i = threadIdx.x; i < p.values - vecs * per; i += kThreads) {
-      const long long at = i < head ? i : vecs * per + i;
+    const long long inner = v.count * (p.f32 ? 4 : 8);
+    for (long long i = threadIdx.x; i < p.values - inner; i += kThreads) {
+      const long long at = i < v.head ? i : inner + i;
       put(p, at, value(p, at) * by);
     }
+    p = q, v = w;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) u[i] = ahead[i];
   }
 }
 
-constexpr int kSmall = 96, kLarge = 1000;  // tensors per launch: parameters of 2.7 and 28 KB
-constexpr int kBlocks = 152 * 4;
+constexpr int kSmall = 96, kMiddle = 320, kLarge = 1000;  // tensors per launch: parameters of 2.7, 9 and 28 KB
+// One block an SM with 8 accesses a thread on their way (384M bf16 values: 360 us, 5.6M float32: 15.5; two
+// blocks with four each 364 and 17.0, four 368 and 26.7).
+constexpr int kBlocks = 152;
 
 int launches(int count) { return (count + kLarge - 1) / kLarge; }
 
 template <int N>
 void fill(Table<N>& t, const GradProblem& p, int from, int count) {
-  t.count = 0, t.chunks = 0;
-  for (int i = from; i < from + count; ++i) {
-    if (p.values[i] == 0) continue;
-    const long long each = kChunkBytes / (p.f32[i] ? 4 : 2);
-    t.first[t.count] = t.chunks;
-    t.in[t.count] = reinterpret_cast<uintptr_t>(p.in[i]);
-    t.out[t.count] = reinterpret_cast<uintptr_t>(p.out ? p.out[i] : nullptr);
-    t.values[t.count] = (unsigned long long)p.values[i] * 2 + (p.f32[i] ? 1 : 0);
-    t.chunks += (int)((p.values[i] + each - 1) / each);
-    ++t.count;
+  t.count = t.large = t.units = 0;
+  for (int small = 0; small < 2; ++small) {
+    for (int i = from; i < from + count; ++i) {
+      const long long each = kUnitBytes / (p.f32[i] ? 4 : 2), units = (p.values[i] + each - 1) / each;
+      if (units == 0 || (units <= kVecs) != (small != 0)) continue;
+      t.first[t.count] = t.units;
+      t.in[t.count] = reinterpret_cast<uintptr_t>(p.in[i]);
+      t.out[t.count] = reinterpret_cast<uintptr_t>(p.out ? p.out[i] : nullptr);
+      t.values[t.count] = (unsigned long long)p.values[i] * 2 + (p.f32[i] ? 1 : 0);
+      if (!small) t.units += (int)units;
+      ++t.count;
+    }
+    if (!small) t.large = t.count, t.first[t.count] = t.units;
   }
+}
+template <int N>
+int blocks_of(const Table<N>& t) {
+  const int most = t.units + t.count - t.large;
+  return most < kBlocks ? (most > 0 ? most : 1) : kBlocks;
 }
 
 // Adds its blocks' number to `parts`.
@@ -249,8 +311,8 @@ template <int N>
 cudaError_t sum_squares(const GradProblem& p, int from, int count, double* sums, int* parts, cudaStream_t stream) {
   Table<N> t;
   fill(t, p, from, count);
-  if (t.chunks == 0) return cudaSuccess;
-  const int blocks = t.chunks < kBlocks ? t.chunks : kBlocks;
+  if (t.count == 0) return cudaSuccess;
+  const int blocks = blocks_of(t);
   sum_squares_kernel<N><<<blocks, kThreads, 0, stream>>>(t, sums + *parts);
   *parts += blocks;
   return cudaGetLastError();
@@ -260,8 +322,7 @@ cudaError_t clip(const GradProblem& p, int from, int count, const double* sums, 
                  cudaStream_t stream) {
   Table<N> t;
   fill(t, p, from, count);
-  const int blocks = t.chunks < kBlocks ? (t.chunks > 0 ? t.chunks : 1) : kBlocks;
-  clip_kernel<N><<<blocks, kThreads, 0, stream>>>(t, sums, parts, p.max_norm, from == 0 ? p.norm : nullptr, in_place);
+  clip_kernel<N><<<blocks_of(t), kThreads, 0, stream>>>(t, sums, parts, p.max_norm, from == 0 ? p.norm : nullptr, in_place);
   return cudaGetLastError();
 }
 
@@ -276,8 +337,9 @@ cudaError_t launch_grad_norm(const GradProblem& p, cudaStream_t stream) {
   cudaError_t err = cudaSuccess;
   for (int from = 0; from < p.count && err == cudaSuccess; from += kLarge) {
     const int n = p.count - from < kLarge ? p.count - from : kLarge;
-    err = n <= kSmall ? sum_squares<kSmall>(p, from, n, sums, &parts, stream)
-                      : sum_squares<kLarge>(p, from, n, sums, &parts, stream);
+    err = n <= kSmall    ? sum_squares<kSmall>(p, from, n, sums, &parts, stream)
+          : n <= kMiddle ? sum_squares<kMiddle>(p, from, n, sums, &parts, stream)
+                         : sum_squares<kLarge>(p, from, n, sums, &parts, stream);
   }
   if (err != cudaSuccess) return err;
   if (!p.out) {
@@ -288,8 +350,9 @@ cudaError_t launch_grad_norm(const GradProblem& p, cudaStream_t stream) {
   for (int i = 0; i < p.count; ++i) in_place = in_place && p.in[i] == p.out[i];
   for (int from = 0; from < p.count && err == cudaSuccess; from += kLarge) {
     const int n = p.count - from < kLarge ? p.count - from : kLarge;
-    err = n <= kSmall ? clip<kSmall>(p, from, n, sums, parts, in_place, stream)
-                      : clip<kLarge>(p, from, n, sums, parts, in_place, stream);
+    err = n <= kSmall    ? clip<kSmall>(p, from, n, sums, parts, in_place, stream)
+          : n <= kMiddle ? clip<kMiddle>(p, from, n, sums, parts, in_place, stream)
+                         : clip<kLarge>(p, from, n, sums, parts, in_place, stream);
   }
   return err;
 }

@@ -11,8 +11,8 @@ Tolerances, derived from the arithmetic (eps / 2 of a type: bf16 2^-8, e4m3 2^-4
    A scale may be the neighbouring power only where max / 448 is within 2^-17 of a power of two.
  * Products: 8-bit values multiply exactly; the tensor cores add 32 products to a float32 at a time, each
    addition within 2^-23 of the sum of magnitudes so far: 2^-23 (K / 32 + 2) A, A the sum of all terms' magnitudes.
- * The gradients' norm: 64-bit sums of float32 sums of at most 32 squares: 2^-21; clipped values 2^-22 more, and
-   their type's rounding.
+ * The gradients' norm: exact sums of float32 sums of at most 64 squares, in at most 12 roundings each: 12 2^-25 of
+   the norm, below 2^-21; clipped values 2^-22 more, and their type's rounding.
 """
 import numpy as np
 import pytest
