@@ -5,9 +5,12 @@
 // Backward, with g = dout w and dh the gradient that arrives at h from behind:
 //   d = dh + inv g - h inv^3 mean(g h)  (dx and dresidual),  dw = sum over rows of dout h inv
 //
-// Memory-bound.  A block takes one row, held in registers in chunks of 8 channels per thread, so that
-// every input is read once; the norm is taken of h as the stream's type holds it, which is what the
-// next layer and the backward read.  In 8 bits, 16 neighbouring threads hold the 128 channels of a scale.
+// Memory-bound.  A block takes one row, held in registers, eight channels of a thread to a chunk, so that every
+// input is read once; the norm is taken of h as the stream's type holds it, which is what the next layer and the
+// backward read.  Where everything is 16-byte aligned (VEC) the eight are consecutive, and in 8 bits 16
+// neighbouring threads hold the 128 channels of a scale.  Otherwise they lie a block's threads apart, so that a
+// warp's accesses are still of consecutive values, and the 128 are those of four warps.
+// Measured: 65536 x 2048, bf16: forward 153 us (7.0 TB/s, 1.03 of a copy's rate), backward 174 us with the sums.
 #include "m2rnn_layer.h"
 #include "ptx_util.cuh"
 
@@ -16,23 +19,28 @@ namespace {
 
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-// Eight values as loaded, so that a load can be started ahead of its use.  Without VEC they lie at any
-// address and `n` of them exist; the others are zero.
+// Chunk r of a thread's channels of a row of D, as loaded, so that a load can be started ahead of its use.
+// Channels that are not there are zero and are not stored.
 template <typename T, bool VEC>
 struct Raw8 {
   uint4 u[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, int n) {
+  // Without VEC: channel i of the chunk.
+  static __device__ __forceinline__ int channel(int r, int i) { return (8 * r + i) * blockDim.x + threadIdx.x; }
+  static __device__ __forceinline__ int first(int r) { return 8 * (threadIdx.x + r * blockDim.x); }
+  __device__ __forceinline__ void load(const T* row, int r, int D) {
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        u[i] = first(r) < D ? reinterpret_cast<const uint4*>(row + first(r))[i] : make_uint4(0, 0, 0, 0);
     } else {
       uint32_t v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        const int c = channel(r, i);
         if constexpr (sizeof(T) == 4)
-          v[i] = i < n ? __float_as_uint(p[i]) : 0u;
+          v[i] = c < D ? __float_as_uint(row[c]) : 0u;
         else
-          v[i] = i < n ? p[i] : 0u;
+          v[i] = c < D ? row[c] : 0u;
       }
       if constexpr (sizeof(T) == 4) {
         u[0] = make_uint4(v[0], v[1], v[2], v[3]);
@@ -65,19 +73,21 @@ struct Raw8 {
                         pack_bf16x2(f[3].x, f[3].y));
     }
   }
-  __device__ __forceinline__ void store(T* p, int n) const {
+  __device__ __forceinline__ void store(T* row, int r, int D) const {
     if constexpr (VEC) {
+      if (first(r) < D)
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + first(r))[i] = u[i];
     } else {
       const uint4 a = u[0], b = u[sizeof(T) / 2 - 1];
       const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        const int c = channel(r, i);
         if constexpr (sizeof(T) == 4) {
-          if (i < n) p[i] = __uint_as_float(v[i]);
+          if (c < D) row[c] = __uint_as_float(v[i]);
         } else {
-          if (i < n) p[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+          if (c < D) row[c] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
         }
       }
     }
@@ -101,14 +111,57 @@ __device__ __forceinline__ float2 block_sum(float2 s, int turn) {
   return s;
 }
 
-// Channels of chunk c.
-__device__ __forceinline__ int chunk_width(int c, int D) { return min(8, D - 8 * c); }
+// |values| as bits, which order them and put NaN above all.
+__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Chunk r of a row in 8 bits, VEC: 16 threads to a scale.
+__device__ __forceinline__ void store_fp8(const float2 (&v)[4], int r, int D, uint8_t* q, uint8_t* scales) {
+  uint32_t top = 0, b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(bits(v[i].x), bits(v[i].y)));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+  const uint32_t e = scale_exponent(top);
+  const float2 by = pair(inverse_scale(e));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = mul2(v[i], by);
+    b[i] = pack_e4m3x2(y.x, y.y);
+  }
+  const int c = 8 * (threadIdx.x + r * blockDim.x);
+  if (c >= D) return;
+  if (c % kScaleBlock == 0) scales[c / kScaleBlock] = (uint8_t)e;
+  *reinterpret_cast<uint2*>(q + c) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+}
+// A row in 8 bits without VEC: a block has a multiple of 128 threads, so that the 128 channels of a scale are
+// one value of each thread of four warps.
+template <int R>
+__device__ __forceinline__ void store_fp8_any(const float2 (&v)[R][4], int D, uint8_t* q, uint8_t* scales) {
+  __shared__ uint32_t tops[8 * R][16];
+  const int warp = threadIdx.x >> 5;
+  const float* value = &v[0][0].x;
+#pragma unroll
+  for (int i = 0; i < 8 * R; ++i) {
+    const uint32_t top = __reduce_max_sync(~0u, bits(value[i]));
+    if ((threadIdx.x & 31) == 0) tops[i][warp] = top;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8 * R; ++i) {
+    const uint32_t* t = &tops[i][warp & ~3];
+    const uint32_t e = scale_exponent(max(max(t[0], t[1]), max(t[2], t[3])));
+    const int c = i * blockDim.x + threadIdx.x;
+    if (c < D) {
+      if (c % kScaleBlock == 0) scales[c / kScaleBlock] = (uint8_t)e;
+      q[c] = (uint8_t)pack_e4m3x2(value[i] * inverse_scale(e), 0.f);
+    }
+  }
+}
 
 template <typename T, bool FP8, bool VEC, int R>
 __global__ void __launch_bounds__(512)
     add_rmsnorm_kernel(AddNormProblem p, uint16_t* __restrict__ out, uint8_t* __restrict__ q, long long q_row,
                        uint8_t* __restrict__ scales) {
-  const int T_ = blockDim.x, chunks = (p.D + 7) / 8;
   const float inv_d = 1.f / (float)p.D;
   int turn = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
@@ -119,76 +172,42 @@ __global__ void __launch_bounds__(512)
     Raw8<uint16_t, VEC> b[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int c = threadIdx.x + r * T_;
-      if (c < chunks) {
-        a[r].load(stream + 8 * c, chunk_width(c, p.D));
-        if (x) b[r].load(x + 8 * c, chunk_width(c, p.D));
-      }
+      a[r].load(stream, r, p.D);
+      if (x) b[r].load(x, r, p.D);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int c = threadIdx.x + r * T_;
+      a[r].get(h[r]);
+      if (x) {
+        float2 v[4];
+        b[r].get(v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[r][i] = pair(0.f);
-      if (c < chunks) {
-        a[r].get(h[r]);
-        if (x) {
-          float2 v[4];
-          b[r].get(v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[r][i] = add2(h[r][i], v[i]);
-          a[r].set(h[r]);
-          if (sizeof(T) == 2) a[r].get(h[r]);
-        }
-        if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D + 8 * c, chunk_width(c, p.D));
+        for (int i = 0; i < 4; ++i) h[r][i] = add2(h[r][i], v[i]);
+        a[r].set(h[r]);
+        if (sizeof(T) == 2) a[r].get(h[r]);
       }
+      if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D, r, p.D);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s = fma2(h[r][i], h[r][i], s);
     }
     const float inv = rsqrtf(block_sum(make_float2(s.x + s.y, 0.f), turn).x * inv_d + p.eps);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int c = threadIdx.x + r * T_;
-      if (c < chunks) {
-        Raw8<float, VEC> u;
-        float2 w[4];
-        u.load(p.w + 8 * c, chunk_width(c, p.D));
-        u.get(w);
+      Raw8<float, VEC> u;
+      float2 w[4];
+      u.load(p.w, r, p.D);
+      u.get(w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[r][i] = mul2(mul2(h[r][i], pair(inv)), w[i]);
-      }
-      if constexpr (FP8) {
-        uint32_t top = 0;  // of |values| as bits, which order them and put NaN above all
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          top = max(top, max(__float_as_uint(h[r][i].x) & 0x7fffffffu, __float_as_uint(h[r][i].y) & 0x7fffffffu));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-        const uint32_t e = scale_exponent(top);
-        const float2 by = pair(inverse_scale(e));
-        if (c < chunks && (c & 15) == 0) scales[row * scale_blocks(p.D) + (c >> 4)] = (uint8_t)e;
-        uint32_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = mul2(h[r][i], by);
-          v[i] = pack_e4m3x2(y.x, y.y);
-        }
-        const uint2 u = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-        uint8_t* to = q + row * q_row + 8 * c;
-        const int n = chunk_width(c, p.D);  // none or fewer behind the last chunk
-        if (VEC ? c < chunks : n == 8) {
-          *reinterpret_cast<uint2*>(to) = u;
-        } else if (!VEC) {
-#pragma unroll
-          for (int i = 0; i < 7; ++i)
-            if (i < n) to[i] = (uint8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
-        }
-      } else if (c < chunks) {
+      for (int i = 0; i < 4; ++i) h[r][i] = mul2(mul2(h[r][i], pair(inv)), w[i]);
+      if constexpr (FP8 && VEC) {
+        store_fp8(h[r], r, p.D, q + row * q_row, scales + row * scale_blocks(p.D));
+      } else if constexpr (!FP8) {
         Raw8<uint16_t, VEC> o;
         o.set(h[r]);
-        o.store(out + row * p.D + 8 * c, chunk_width(c, p.D));
+        o.store(out + row * p.D, r, p.D);
       }
     }
+    if constexpr (FP8 && !VEC) store_fp8_any<R>(h, p.D, q + row * q_row, scales + row * scale_blocks(p.D));
   }
 }
 
@@ -218,41 +237,39 @@ template <typename T, int R>
 constexpr int kRingPerThread = kAhead<T, R> * (2 * (int)sizeof(T) / 2 + 1) * R * 16;  // bytes
 template <typename T, bool VEC, int R>
 struct RowStream {
-  static constexpr int kRows = VEC ? kAhead<T, R> : 1, kParts = sizeof(T) / 2;  // 16-byte pieces of eight values of the stream
+  static constexpr int kRows = kAhead<T, R>, kParts = sizeof(T) / 2;  // 16-byte pieces of 8 values
   const AddNormBackwardProblem& p;
-  const int chunks;
   uint4* own;  // [kRows][kParts + 1 + kParts][R][threads]
   int at = 0, to = 0;
   Raw8<T, VEC> hr[R], er[R];
   Raw8<uint16_t, VEC> dr[R];
 
-  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, int chunks_, uint4* smem)
-      : p(p_), chunks(chunks_), own(smem + threadIdx.x) {}
+  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, uint4* smem) : p(p_), own(smem + threadIdx.x) {}
   __device__ __forceinline__ uint4* slot(int stage, int part, int r) const {
     return own + ((stage * (2 * kParts + 1) + part) * R + r) * blockDim.x;
   }
   __device__ __forceinline__ void start(long long row) {
     if (row < p.rows) {
+      const T *h = static_cast<const T*>(p.h) + row * p.D, *e = static_cast<const T*>(p.dh) + row * p.D;
+      const uint16_t* d = p.dout + row * p.D;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int c = threadIdx.x + r * blockDim.x;
-        if (c < chunks) {
-          const long long i = row * p.D + 8 * c;
-          const T *h = static_cast<const T*>(p.h) + i, *e = static_cast<const T*>(p.dh) + i;
-          if constexpr (VEC) {
+        if constexpr (VEC) {
+          const int c = Raw8<T, VEC>::first(r);
+          if (c < p.D) {
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) copy16<kParts == 2>(smem_u32(slot(to, k, r)), reinterpret_cast<const uint4*>(h) + k);
-            copy16<false>(smem_u32(slot(to, kParts, r)), p.dout + i);
+            for (int k = 0; k < kParts; ++k)
+              copy16<kParts == 2>(smem_u32(slot(to, k, r)), reinterpret_cast<const uint4*>(h + c) + k);
+            copy16<false>(smem_u32(slot(to, kParts, r)), d + c);
             if (p.dh)
 #pragma unroll
               for (int k = 0; k < kParts; ++k)
-                copy16<kParts == 2>(smem_u32(slot(to, kParts + 1 + k, r)), reinterpret_cast<const uint4*>(e) + k);
-          } else {
-            const int n = chunk_width(c, p.D);
-            hr[r].load(h, n);
-            dr[r].load(p.dout + i, n);
-            if (p.dh) er[r].load(e, n);
+                copy16<kParts == 2>(smem_u32(slot(to, kParts + 1 + k, r)), reinterpret_cast<const uint4*>(e + c) + k);
           }
+        } else {
+          hr[r].load(h, r, p.D);
+          dr[r].load(d, r, p.D);
+          if (p.dh) er[r].load(e, r, p.D);
         }
       }
     }
@@ -263,9 +280,12 @@ struct RowStream {
   }
   __device__ __forceinline__ void begin(long long row, long long step) {
 #pragma unroll
-    for (int i = 0; i < (VEC ? kRows - 1 : 1); ++i) start(row + i * step);
+    for (int i = 0; i < (VEC ? kRows - 1 : kParts / kParts); ++i) start(row + i * step);
   }
-  // The values of `row`, zeros behind the last channel; the next row that is not on its way yet starts.
+  // dh of the row at hand is taken before the sums where there is room to hold it across them (65536 x 2048
+  // float32: 317 us, 364 where it is taken after them; 4000 x 16384 bf16: 215 and 124).
+  static constexpr bool kEarly = VEC && R <= 2;
+  // h, dout and, if early, dh of `row`, zeros behind the last channel; a later row starts.
   __device__ __forceinline__ void next(long long row, long long step, float2 (&h)[R][4], float2 (&d)[R][4],
                                        float2 (&e)[R][4]) {
     if constexpr (VEC) {
@@ -276,20 +296,30 @@ struct RowStream {
     for (int r = 0; r < R; ++r) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[r][i] = d[r][i] = e[r][i] = pair(0.f);
-      if (threadIdx.x + r * blockDim.x < chunks) {
+      if (!VEC || Raw8<T, VEC>::first(r) < p.D) {
         if constexpr (VEC) {
 #pragma unroll
           for (int k = 0; k < kParts; ++k) hr[r].u[k] = *slot(at, k, r);
           dr[r].u[0] = *slot(at, kParts, r);
-          if (p.dh)
+          if (kEarly && p.dh)
 #pragma unroll
             for (int k = 0; k < kParts; ++k) er[r].u[k] = *slot(at, kParts + 1 + k, r);
         }
         hr[r].get(h[r]);
         dr[r].get(d[r]);
-        if (p.dh) er[r].get(e[r]);
+        if (kEarly && p.dh) er[r].get(e[r]);
       }
     }
+  }
+  // dh of chunk r, where it is late.
+  __device__ __forceinline__ void late(int r, float2 (&e)[4]) {
+    if (kEarly || !p.dh || (VEC && Raw8<T, VEC>::first(r) >= p.D)) return;
+    if constexpr (VEC)
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) er[r].u[k] = *slot(at, kParts + 1 + k, r);
+    er[r].get(e);
+  }
+  __device__ __forceinline__ void done(long long row, long long step) {
     if constexpr (VEC)
       at = at + 1 == kRows ? 0 : at + 1;
     else
@@ -303,77 +333,80 @@ template <typename T, bool VEC, int R>
 __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
     add_rmsnorm_backward_kernel(AddNormBackwardProblem p, float* __restrict__ part) {
   extern __shared__ uint4 ring[];
-  const int T_ = blockDim.x, chunks = (p.D + 7) / 8;
   const float inv_d = 1.f / (float)p.D;
-  float2 dw[R][4], w[R][4];
+  constexpr bool kKeep = R <= 2;  // the weight stays in registers where there is room for it
+  float2 dw[R][4], kept[kKeep ? R : 1][4];
+  auto weight = [&](int r, float2(&w)[4]) {
+    Raw8<float, VEC> u;
+    u.load(p.w, r, p.D);
+    u.get(w);
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = threadIdx.x + r * T_;
-    Raw8<float, VEC> u;
-    if (c < chunks) u.load(p.w + 8 * c, chunk_width(c, p.D)), u.get(w[r]);
+    if constexpr (kKeep) weight(r, kept[r]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dw[r][i] = pair(0.f);
-      if (c >= chunks) w[r][i] = pair(0.f);
-    }
+    for (int i = 0; i < 4; ++i) dw[r][i] = pair(0.f);
   }
-  RowStream<T, VEC, R> rows(p, chunks, ring);
+  RowStream<T, VEC, R> rows(p, ring);
   rows.begin(blockIdx.x, gridDim.x);
   int turn = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    float2 h[R][4], d[R][4], e[R][4], s1 = pair(0.f), s2 = pair(0.f);
+    float2 h[R][4], d[R][4], s1 = pair(0.f), s2 = pair(0.f);
+    float2 e[R][4];
     rows.next(row, gridDim.x, h, d, e);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      float2 w[4];
+      if constexpr (!kKeep) weight(r, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s1 = fma2(h[r][i], h[r][i], s1);
-        s2 = fma2(mul2(d[r][i], w[r][i]), h[r][i], s2);
+        s2 = fma2(mul2(d[r][i], kKeep ? kept[kKeep ? r : 0][i] : w[i]), h[r][i], s2);
       }
+    }
     const float2 sum = block_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
     const float inv = rsqrtf(sum.x * inv_d + p.eps);
     const float2 iv = pair(inv), back = pair(-inv * inv * inv * (sum.y * inv_d));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int c = threadIdx.x + r * T_;
-      const int n = chunk_width(c, p.D);
-      const long long at = row * p.D + 8 * c;
-      float2 o[4];
+      float2 o[4], w[4];
+      rows.late(r, e[r]);
+      if constexpr (!kKeep) weight(r, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         dw[r][i] = fma2(d[r][i], mul2(h[r][i], iv), dw[r][i]);
-        o[i] = add2(fma2(h[r][i], back, mul2(mul2(d[r][i], w[r][i]), iv)), e[r][i]);
+        o[i] = add2(fma2(h[r][i], back, mul2(mul2(d[r][i], kKeep ? kept[kKeep ? r : 0][i] : w[i]), iv)), e[r][i]);
       }
-      if (c < chunks && p.dx) {
+      if (p.dx) {
         Raw8<uint16_t, VEC> u;
         u.set(o);
-        u.store(p.dx + at, n);
+        u.store(p.dx + row * p.D, r, p.D);
       }
-      if (c < chunks && p.dresidual) {
+      if (p.dresidual) {
         Raw8<T, VEC> u;
         u.set(o);
-        u.store(static_cast<T*>(p.dresidual) + at, n);
+        u.store(static_cast<T*>(p.dresidual) + row * p.D, r, p.D);
       }
     }
+    rows.done(row, gridDim.x);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = threadIdx.x + r * T_;
     Raw8<float, VEC> u;
     u.set(dw[r]);
-    if (c < chunks) u.store(part + (long long)blockIdx.x * p.D + 8 * c, chunk_width(c, p.D));
+    u.store(part + (long long)blockIdx.x * p.D, r, p.D);
   }
 }
 
-// Threads of a row's block for R chunks per thread.
-int threads_for(int D, int R) {
-  const int chunks = (D + 7) / 8;
-  return ((chunks + R - 1) / R + 31) / 32 * 32;
+// Threads of a row's block for R chunks per thread: whole warps, without VEC four at a time.
+int threads_for(int D, int R, bool vec) {
+  const int chunks = (D + 7) / 8, whole = vec ? 32 : 128;
+  return ((chunks + R - 1) / R + whole - 1) / whole * whole;
 }
 // Chunks per thread, the fewest from `least` on whose block has at most 512 threads.
 int chunks_each(int D, int least) {
   int R = least;
-  while (threads_for(D, R) > 512) R *= 2;
+  while (threads_for(D, R, true) > 512) R *= 2;
   return R;
 }
 
@@ -391,11 +424,11 @@ cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long lon
                     cudaStream_t stream) {
   // Few rows are spread as wide as they go; of many, two chunks a thread (65536 x 2048: 153 us; one chunk
   // 169, four 158; 8191 x 4096 in 8 bits: 58, 65, 64).
-  const int R = chunks_each(p.D, p.rows >= 152 * 16 ? 2 : 1);
+  const int R = chunks_each(p.D, VEC && p.rows >= 152 * 16 ? 2 : 1);
   return with_chunks(R, [&](auto r) {
     constexpr int N = decltype(r)::value;
     const unsigned blocks = (unsigned)(p.rows < 0x7fffffff ? p.rows : 0x7fffffff);
-    add_rmsnorm_kernel<T, FP8, VEC, N><<<blocks, threads_for(p.D, N), 0, stream>>>(p, out, q, q_row, scales);
+    add_rmsnorm_kernel<T, FP8, VEC, N><<<blocks, threads_for(p.D, N, VEC), 0, stream>>>(p, out, q, q_row, scales);
     return cudaGetLastError();
   });
 }
@@ -418,9 +451,9 @@ cudaError_t dispatch(const AddNormProblem& p, bool vec, uint16_t* out, uint8_t* 
              : forward<uint16_t, FP8, false>(p, out, q, q_row, scales, stream);
 }
 
-// Blocks of the backward: 1024 threads for every SM.
+// Blocks of the backward, and rows of its sums: 1024 threads for every SM.
 int backward_blocks(long long rows, int D) {
-  const long long most = 152LL * (1024 / threads_for(D, chunks_each(D, 1)));
+  const long long most = 152LL * (1024 / threads_for(D, chunks_each(D, 1), true));
   return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
 }
 
@@ -444,7 +477,7 @@ cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStr
   const cudaError_t err = with_chunks(chunks_each(p.D, 1), [&](auto r) {
     constexpr int R = decltype(r)::value;
     auto go = [&](auto kernel) {
-      const int threads = threads_for(p.D, R);
+      const int threads = threads_for(p.D, R, vec);
       const int bytes = vec ? threads * (p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>) : 0;
       // At every launch: the attribute belongs to the current device.
       const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
