@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-constexpr int kSmall = 96, kMiddle = 320, kLarge = 1000;  // tensors per launch: parameters of 2.7, 9 and 28 KB
+constexpr int kSmall = 32, kMiddle = 320, kLarge = 1000;  // tensors per launch: parameters of 1, 9 and 28 KB
 // One block an SM with 8 accesses a thread on their way (384M bf16 values: 360 us, 5.6M float32: 15.5; two
 // blocks with four each 364 and 17.0, four 368 and 26.7).
 constexpr int kBlocks = 152;

@@ -147,13 +147,13 @@ m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row
   m2rnn_status st = linear_checks(w, w_row, w_scales, out, M, N, K);
   if (st != M2RNN_OK || M == 0) return st;
   if (!x || x_row < 0) return M2RNN_ERR_INVALID_ARG;
+  const size_t need = m2rnn_linear_quantise_workspace_bytes(x_f32, M, K);
+  if (need > 0 && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return M2RNN_ERR_INVALID_ARG;
   int* status = device_status();
   if (!status) return M2RNN_ERR_CUDA;
   const auto at = static_cast<cudaStream_t>(stream);
   LinearProblem p{nullptr, nullptr, nullptr, w, w_scales, x_row, w_row, out, out_f32 != 0, (int)M, N, K, status};
-  const size_t need = m2rnn_linear_quantise_workspace_bytes(x_f32, M, K);
   if (need > 0) {
-    if (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need) return M2RNN_ERR_INVALID_ARG;
     p.x_row = (K + 15LL) / 16 * 16;
     uint8_t *q = static_cast<uint8_t*>(workspace), *scales = q + M * p.x_row;
     st = done(launch_quantise_rows(x, x_f32 != 0, x_row, q, p.x_row, scales, M, K, at));

@@ -56,6 +56,13 @@ def _byte_rows(t, name, shape, dev):
     return p, row
 
 
+def _dense(like, dtype):
+    """A new dense tensor of the same shape (the like-form of empty is the cheapest)."""
+    if like.dtype is dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
+
+
 def _new_bytes(like, shape):
     """An e4m3 tensor whose rows start on 16-byte boundaries."""
     D = shape[-1]
@@ -92,7 +99,7 @@ def _norm_args(x, residual, w, h):
         xp, x_row = _rows(x, "x", BF16, shape, dev)
         sp, row = _rows(residual, "residual", kind, shape, dev)
         if h is None:
-            h = torch.empty(shape, dtype=kind, device=x.device)
+            h = _dense(residual, kind)
         hp = _ptr(h, "h", kind, shape, dev)
         args = (xp, x_row, sp, int(kind is F32), row)
     return dev, h, (x.numel() // D if D else 0, D), (*args, _ptr(w, "w", F32, (D,), dev)), hp
@@ -106,7 +113,7 @@ def add_rmsnorm(x, residual, w, eps=1e-5, out=None, h=None):
     itself (in place).  Returns (out [..., D] bf16, h)."""
     dev, h, size, args, hp = _norm_args(x, residual, w, h)
     if out is None:
-        out = torch.empty(x.shape, dtype=BF16, device=x.device)
+        out = _dense(x, BF16)
     st = load_library().m2rnn_add_rmsnorm(*args, eps, hp, _ptr(out, "out", BF16, x.shape, dev), *size, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_add_rmsnorm")
@@ -144,9 +151,9 @@ def add_rmsnorm_backward(h, w, dout, dh=None, eps=1e-5, grads=None, workspace=No
         raise TypeError(f"h: expected {F32} or {BF16}, got {kind}")
     g = dict(grads or {})
     if g.get("dx") is None:
-        g["dx"] = torch.empty(shape, dtype=BF16, device=h.device)
+        g["dx"] = _dense(h, BF16)
     if g.get("dresidual") is None:
-        g["dresidual"] = g["dx"] if kind is BF16 else torch.empty(shape, dtype=kind, device=h.device)
+        g["dresidual"] = g["dx"] if kind is BF16 else _dense(h, kind)
     if g.get("dw") is None:
         g["dw"] = torch.empty(D, dtype=F32, device=h.device)
     dx, dr = _ptr(g["dx"], "dx", BF16, shape, dev), _ptr(g["dresidual"], "dresidual", kind, shape, dev)
@@ -245,25 +252,28 @@ def linear_fp8(x, x_scales, w, w_scales, out=None, out_dtype=BF16, workspace=Non
 
 
 # ---------------------------------------------------------------- gradients
+_IS_F32 = {F32: 1, BF16: 0}
+
+
 def _gradients(grads, out, max_norm, norm, workspace):
     grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
     if not grads:
         raise ValueError("grads: at least one tensor")
     dev = _device(grads[0])
-    n = len(grads)
-    ptrs, sizes, kinds = array("Q"), array("q"), bytearray(n)
     for i, t in enumerate(grads):
-        kind = t.dtype
-        if kind is F32:
-            kinds[i] = 1
-        elif kind is not BF16:
-            raise TypeError(f"grads[{i}]: expected {F32} or {BF16}, got {kind}")
+        if t.dtype not in _IS_F32:
+            raise TypeError(f"grads[{i}]: expected {F32} or {BF16}, got {t.dtype}")
         if t.get_device() != dev or not t.is_contiguous():
-            _refuse(t, f"grads[{i}]", kind, t.shape, dev)
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
-    to = ptrs if out is None else None
-    if out is not None and out is not False:
+            _refuse(t, f"grads[{i}]", t.dtype, t.shape, dev)
+    n = len(grads)
+    ptrs = array("Q", [t.data_ptr() for t in grads])
+    sizes = array("q", [t.numel() for t in grads])
+    kinds = array("B", [_IS_F32[t.dtype] for t in grads])
+    if out is None:
+        to = ptrs
+    elif out is _NORM_ONLY:
+        to = None
+    else:
         out = list(out.values()) if isinstance(out, dict) else list(out)
         if len(out) != n:
             raise ValueError(f"out: {len(out)} tensors for {n} gradients")
@@ -272,7 +282,6 @@ def _gradients(grads, out, max_norm, norm, workspace):
         norm = torch.empty((), dtype=F32, device=grads[0].device)
     lib = load_library()
     ws, wp, wb = _workspace(workspace, lib.m2rnn_grad_norm_workspace_bytes(n), grads[0])
-    kinds = array("B", kinds)
     st = lib.m2rnn_clip_grad_norm(ptrs.buffer_info()[0], None if to is None else to.buffer_info()[0],
                                   sizes.buffer_info()[0], kinds.buffer_info()[0], n, max_norm,
                                   _ptr(norm, "norm", F32, (), dev), wp, wb, _stream(dev))
@@ -281,11 +290,14 @@ def _gradients(grads, out, max_norm, norm, workspace):
     return norm
 
 
+_NORM_ONLY = object()
+
+
 @_on_stream
 def grad_norm(grads, norm=None, workspace=None):
     """The norm of all values of grads (a sequence or dict of contiguous float32 and bf16 tensors)
     together: a float32 scalar on the device."""
-    return _gradients(grads, False, 0.0, norm, workspace)
+    return _gradients(grads, _NORM_ONLY, 0.0, norm, workspace)
 
 
 @_on_stream
