@@ -10,14 +10,18 @@
 // the tensor core however few tokens there are) by NT tokens.  Where that gives fewer blocks than SMs, a
 // cluster of up to 8 blocks shares a tile, each with a stretch of K, and adds up its parts through
 // distributed shared memory, in the order of K.  Up to 16 tokens of bf16 are quantised on the way in, by the
-// warps that later write the results (32 tokens take 25 us that way, 13 with a launch before, 4096 x 8192).
+// warps that later write the results and four more (64 tokens would take 26 us that way, 13 with a launch
+// before, 4096 x 8192: every block reads all rows).
 #include "m2rnn_fp8_tc.cuh"
 
 namespace m2rnn {
 namespace {
 
 constexpr int MT = 128;  // channels of a tile
-constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kThreads = 224;
+constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kWarps = 7;
+constexpr int kQuantWarps = 8;  // the epilogue's four and four more, behind the others
+template <bool RAW>
+constexpr int kThreads = 32 * (RAW ? kWarps + kQuantWarps - kEpilogueWarps : kWarps);
 
 template <int NT>
 struct Smem {
@@ -55,7 +59,7 @@ __device__ __noinline__ uint4 load_any(const uint16_t* row, int k, int K) {
 }
 
 template <int NT, bool RAW, typename Out>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads<RAW>)
     linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LinearProblem p,
                   int token_tiles, int split, bool raw_vec, bool vec) {
   using S = Smem<NT>;
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kThreads)
   if (warp == kWarpLoad && lane == 0) {  // the first loads leave before anything else
     for (int s = 0; s < ST; ++s) mbar_init(&bar.full[s], 1), mbar_init(&bar.empty[s], 1);
     for (int s = 0; s < SQ; ++s)
-      mbar_init(&bar.scale_full[s], RAW ? 1 + kEpilogueWarps : 1), mbar_init(&bar.scale_empty[s], 1);
+      mbar_init(&bar.scale_full[s], RAW ? 1 + kQuantWarps : 1), mbar_init(&bar.scale_empty[s], 1);
     mbar_init(&bar.done, 1);
     bar.abort = 0;
     fence_mbar_init();
@@ -169,74 +173,55 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     if (ok) umma_commit_if(leader, &bar.done);
-  } else {
+  } else {  // --------------- RAW: eight warps quantise
     if constexpr (RAW) {
-      // 16 threads take 128 values of a row, eight each, of rows r, r + 8, ...: a word's four steps at a time, the
-      // next four on their way.
-      constexpr int H = NT / 8;
-      const int r = threadIdx.x >> 4, piece = threadIdx.x & 15, rows = p.M - m0;
-      uint4 next[kQuad][H];
-      auto fetch = [&](int g0) {
-#pragma unroll
-        for (int j = 0; j < kQuad; ++j)
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const uint16_t* row = p.raw + (m0 + r + 8 * h) * p.x_row;
-            const int k = (begin + g0 + j) * kBlockK + piece * 8;
-            const bool live = g0 + j < steps && r + 8 * h < rows;
-            next[j][h] = make_uint4(0, 0, 0, 0);
-            if (raw_vec && live && k < p.K) next[j][h] = *reinterpret_cast<const uint4*>(row + k);
-            if (!raw_vec && live) next[j][h] = load_any(row, k, p.K);
-          }
+      // 16 threads take 128 values of a row, eight each.  A word's four steps are handed over at once, with their
+      // scales; as each is done, the one four steps on starts on its way.
+      static_assert(NT == 16 && kQuantWarps == 8, "a row for every 16 threads");
+      const int id = warp < kEpilogueWarps ? threadIdx.x : threadIdx.x - 32 * (kWarps - kEpilogueWarps);
+      const int r = id >> 4, piece = id & 15;
+      const bool live = m0 + r < p.M;  // products of rows that are not there go nowhere
+      const uint16_t* row = p.raw + (live ? (m0 + r) * p.x_row : 0);
+      uint4 word[kQuad];
+      auto fetch = [&](int g) {
+        const int k = (begin + g) * kBlockK + piece * 8;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (raw_vec && live && g < steps && k < p.K) u = *reinterpret_cast<const uint4*>(row + k);
+        if (!raw_vec && live && g < steps) u = load_any(row, k, p.K);
+        return u;
       };
-      fetch(0);
+#pragma unroll
+      for (int j = 0; j < kQuad; ++j) word[j] = fetch(j);
       for (int g0 = 0, w = 0; g0 < steps && scales_free(w); g0 += kQuad, ++w) {
         const uint32_t scales = base + S::kScales + w % SQ * S::kScaleStage + 512;
-        uint4 word[kQuad][H];
-#pragma unroll
-        for (int j = 0; j < kQuad; ++j)
-#pragma unroll
-          for (int h = 0; h < H; ++h) word[j][h] = next[j][h];
-        if (g0 + kQuad < steps) fetch(g0 + kQuad);
 #pragma unroll
         for (int j = 0; j < kQuad; ++j) {
           if (g0 + j >= steps || !stage_free(g0 + j)) break;
-          const uint4(&now)[H] = word[j];
           const uint32_t to = base + (g0 + j) % ST * S::kStage + S::kA;
-          uint32_t top[H];
+          const uint4 u = word[j];
+          // The largest |value|, two bf16 at a time.
+          uint32_t top = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
 #pragma unroll
-          for (int h = 0; h < H; ++h) {
-            const uint32_t u[4] = {now[h].x, now[h].y, now[h].z, now[h].w};
-            top[h] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[h] = max(top[h], max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
-          }
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-              if (8 * h < rows) top[h] = max(top[h], __shfl_xor_sync(~0u, top[h], o));
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            if (8 * h >= rows) break;  // products of rows that are not there go nowhere
-            const uint32_t u[4] = {now[h].x, now[h].y, now[h].z, now[h].w}, e = scale_exponent(top[h]);
-            const float by = inverse_scale(e);
-            uint32_t q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = pack_e4m3x2(bf16_lo(u[i]) * by, bf16_hi(u[i]) * by);
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(tile_at(to, r + 8 * h, piece >> 1) + (piece & 1) * 8),
-                         "r"(q[0] | q[1] << 16), "r"(q[2] | q[3] << 16));
-            // Row m's word is in line m % 32, word m / 32.
-            if (piece == 0)
-              asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + (r + 8 * h) % 32 * 16 + (r + 8 * h) / 32 * 4 + j),
-                           "r"(e));
-          }
+          for (int o = 8; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+          const uint32_t e = scale_exponent(max(top << 16, top & 0xffff0000u));
+          const float2 by = make_float2(inverse_scale(e), inverse_scale(e));
+          const float2 v0 = mul2(bf16x2_to_float2(u.x), by), v1 = mul2(bf16x2_to_float2(u.y), by);
+          const float2 v2 = mul2(bf16x2_to_float2(u.z), by), v3 = mul2(bf16x2_to_float2(u.w), by);
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(tile_at(to, r, piece >> 1) + (piece & 1) * 8),
+                       "r"(pack_e4m3x2(v0.x, v0.y) | pack_e4m3x2(v1.x, v1.y) << 16),
+                       "r"(pack_e4m3x2(v2.x, v2.y) | pack_e4m3x2(v3.x, v3.y) << 16)
+                       : "memory");
+          if (piece == 0)  // row r's word is the first of line r
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(scales + r * 16 + j), "r"(e) : "memory");
+          word[j] = fetch(g0 + j + kQuad);
         }
         if (!ok) break;
         fence_proxy_async_smem();
         warp_arrive(&bar.scale_full[w % SQ], lane);
       }
     }
+  }
+  if (warp < kEpilogueWarps) {
     if (ok) ok = warp_wait(&bar.done, 0, abort);
     tc_fence_after();
     // A lane is a channel: the tile goes row by row (token) into the stages, which every product has left.
@@ -269,7 +254,7 @@ __global__ void __launch_bounds__(kThreads)
     // This block's share of the tile's tokens, four channels a thread.
     const int first = NT * rank / split, rows = min(NT * (rank + 1) / split, p.M - m0) - first;
     Out* out = static_cast<Out*>(p.out) + (long long)(m0 + first) * p.N + n0;
-    for (int id = threadIdx.x; id < rows * (MT / 4); id += kThreads) {
+    for (int id = threadIdx.x; id < rows * (MT / 4); id += kThreads<RAW>) {
       const int r = id / (MT / 4), c = id % (MT / 4) * 4, n = p.N - n0 - c;
       if (n <= 0) continue;
       const uint32_t at = base + ((first + r) * MT + c) * 4;
@@ -328,7 +313,7 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   while (split < 8 && tiles * split * 2 <= 152 && split * 2 * kQuad <= scale_blocks(p.K)) split *= 2;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)(tiles * split));
-  c.blockDim = dim3(kThreads);
+  c.blockDim = dim3(kThreads<RAW>);
   c.dynamicSmemBytes = S::kBytes;
   c.stream = stream;
   cudaLaunchAttribute a{};
