@@ -66,6 +66,7 @@ struct LinearProblem {
   bool out_f32;
   int M, N, K;
   int* status;
+  bool follows = false;         // launched behind the quantising of x, which writes nothing else: may start early
 };
 constexpr int kRawRows = 16;
 cudaError_t launch_linear_fp8(const LinearProblem& p, cudaStream_t stream);
@@ -87,6 +88,8 @@ size_t grad_norm_workspace_bytes(int count);
 cudaError_t launch_grad_norm(const GradProblem& p, cudaStream_t stream);
 
 #ifdef __CUDACC__
+// A launch that `follows` may start from here on.
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 // The exponent (of 2, biased by 127) of the least power of two s with amax / s <= 448 = 1.75 * 2^8, 2^-126
 // at the least; 255, e8m0's NaN, where amax is infinite or NaN.  From amax's bits: s is
 // 2^(floor(log2 amax) - 8), or twice that where the leading digits are above 1.75.

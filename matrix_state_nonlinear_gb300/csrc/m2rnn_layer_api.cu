@@ -158,7 +158,7 @@ m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row
     uint8_t *q = static_cast<uint8_t*>(workspace), *scales = q + M * p.x_row;
     st = done(launch_quantise_rows(x, x_f32 != 0, x_row, q, p.x_row, scales, M, K, at));
     if (st != M2RNN_OK) return st;
-    p.x = q, p.x_scales = scales;
+    p.x = q, p.x_scales = scales, p.follows = true;
   } else {
     p.raw = static_cast<const uint16_t*>(x);
   }

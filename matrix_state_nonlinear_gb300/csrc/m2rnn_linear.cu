@@ -76,14 +76,17 @@ __global__ void __launch_bounds__(kThreads<RAW>)
 
   const int steps = end - begin;
   // Step g is stage g % ST, its turn g / ST; its scales are byte g % 4 of word g / 4.
-  auto load = [&](int g) {
-    const int s = g % ST, k = (begin + g) * kBlockK;
-    const uint32_t to = base + s * S::kStage;
+  auto load_w = [&](int g) {
+    const int s = g % ST;
     mbar_arrive_expect_tx(&bar.full[s], RAW ? S::kA : S::kStage);
-    tma_load_2d(to, &map_w, &bar.full[s], k, n0);
-    if (!RAW) tma_load_2d(to + S::kA, &map_x, &bar.full[s], k, m0);
+    tma_load_2d(base + s * S::kStage, &map_w, &bar.full[s], (begin + g) * kBlockK, n0);
   };
-  if (warp == kWarpLoad && lane == 0) {  // the first loads leave before anything else
+  auto load_x = [&](int g) {
+    const int s = g % ST;
+    if (!RAW) tma_load_2d(base + s * S::kStage + S::kA, &map_x, &bar.full[s], (begin + g) * kBlockK, m0);
+  };
+  // The first loads leave before anything else, those of the weights before the launch that writes x is over.
+  if (warp == kWarpLoad && lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&bar.full[s], 1), mbar_init(&bar.empty[s], 1);
     for (int s = 0; s < SQ; ++s)
       mbar_init(&bar.scale_full[s], RAW ? 1 + kQuantWarps : 1), mbar_init(&bar.scale_empty[s], 1);
@@ -91,7 +94,9 @@ __global__ void __launch_bounds__(kThreads<RAW>)
     bar.abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
-    for (int g = 0; g < min(ST, steps); ++g) load(g);
+    for (int g = 0; g < min(ST, steps); ++g) load_w(g);
+    wait_for_launch_before();
+    for (int g = 0; g < min(ST, steps); ++g) load_x(g);
   }
   if (warp == kWarpMma) tmem_alloc(&bar.tmem, S::kTmemCols);
   tc_fence_before();
@@ -110,7 +115,7 @@ __global__ void __launch_bounds__(kThreads<RAW>)
 
   if (warp == kWarpLoad) {
     for (int g = ST; g < steps && stage_free(g); ++g) {
-      if (lane == 0) load(g);
+      if (lane == 0) load_w(g), load_x(g);
       __syncwarp();
     }
   } else if (warp == kWarpScale) {
@@ -129,7 +134,9 @@ __global__ void __launch_bounds__(kThreads<RAW>)
       x.live[c] = !RAW && m < p.M && 32 * c + lane < NT;
       x.row[c] = RAW ? nullptr : p.x_scales + (size_t)m * all;
     }
-    w.fetch(begin), x.fetch(begin);
+    w.fetch(begin);
+    wait_for_launch_before();
+    x.fetch(begin);
     for (int i = begin, h = 0; i < end && ok; i += kGroup) {
       uint32_t v[4], u[4][4];
 #pragma unroll
@@ -316,11 +323,13 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   c.blockDim = dim3(kThreads<RAW>);
   c.dynamicSmemBytes = S::kBytes;
   c.stream = stream;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim.x = (unsigned)split, a.val.clusterDim.y = a.val.clusterDim.z = 1;
-  c.attrs = &a;
-  c.numAttrs = 1;
+  cudaLaunchAttribute a[2] = {};
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = (unsigned)split, a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[1].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = p.follows ? 2 : 1;
   const bool raw_vec = RAW && aligned_to(p.raw, 16) && p.x_row % 8 == 0 && p.K % 8 == 0;
   const bool vec = p.N % 4 == 0 && aligned_to(p.out, 4 * sizeof(Out));
   return cudaLaunchKernelEx(&c, kernel, mw, mx, p, (int)tokens, split, raw_vec, vec);

@@ -90,6 +90,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
   }
   tc_fence_before();
   __syncthreads();
+  wait_for_launch_before();
   cluster_sync_all();  // the other block's barriers are ready
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
@@ -293,8 +294,17 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   const long long tiles = (long long)tokens * channels;
   const bool vec = p.N % (32 / (int)sizeof(Out)) == 0 && aligned_to(p.out, 32);
   const unsigned pairs = (unsigned)(tiles < 76 ? tiles : 76);
-  linear_pair_kernel<Out><<<2 * pairs, kThreads, kSmemBytes, stream>>>(mx, mw, p, tokens, channels, vec);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(2 * pairs);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = kSmemBytes;
+  c.stream = stream;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = p.follows ? 1 : 0;
+  return cudaLaunchKernelEx(&c, linear_pair_kernel<Out>, mx, mw, p, tokens, channels, vec);
 }
 
 }  // namespace

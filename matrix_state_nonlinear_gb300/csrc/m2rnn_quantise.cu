@@ -79,6 +79,7 @@ template <typename T, typename Index>
 __global__ void __launch_bounds__(kThreads)
     quantise_rows_kernel(const T* __restrict__ x, long long x_row, uint8_t* __restrict__ q, long long q_row,
                          uint8_t* __restrict__ scales, Index units, int blocks, int D) {
+  let_next_launch_start();
   const Index unit = (Index)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
   const Index row = unit / (Index)blocks;
   const int b = (int)(unit - row * (Index)blocks), at = b * kScaleBlock + (threadIdx.x & 15) * 8;
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int EACH>
 __global__ void __launch_bounds__(kThreads) quantise_flat_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                                  uint8_t* __restrict__ scales, long long units) {
+  let_next_launch_start();
   const long long first = (long long)blockIdx.x * (EACH * kThreads / 16) + (threadIdx.x >> 4);
   const int piece = (threadIdx.x & 15) * 8;
   float v[EACH][8];
@@ -117,6 +119,7 @@ template <typename T, typename Index>
 __global__ void __launch_bounds__(kThreads)
     quantise_rows_any_kernel(const T* __restrict__ x, long long x_row, uint8_t* __restrict__ q, long long q_row,
                              uint8_t* __restrict__ scales, Index units, int blocks, int D) {
+  let_next_launch_start();
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
