@@ -8,8 +8,9 @@
 // This kernel takes few and middling numbers of tokens and is bound by the weights' way from memory, and
 // below a few megabytes by latency.  A block takes 128 channels (the product's rows, so that the weights fill
 // the tensor core however few tokens there are) by NT tokens.  Where that gives fewer blocks than SMs, a
-// cluster of up to 8 blocks shares a tile, each with a stretch of K, and adds up its parts through
-// distributed shared memory, in the order of K.  Up to 16 tokens of bf16 are quantised on the way in, by the
+// cluster of up to 8 blocks shares a tile, each with a stretch of K.  Every block then writes each of the
+// others' share of the tokens into that block's shared memory, and adds up its own share in the order of K: one
+// barrier of the cluster, nothing read from afar (which took 1.5 us longer for 64 tokens).  Up to 16 tokens of bf16 are quantised on the way in, by the
 // warps that later write the results and four more (64 tokens would take 26 us that way, 13 with a launch
 // before, 4096 x 8192: every block reads all rows).
 #include "m2rnn_fp8_tc.cuh"
@@ -23,13 +24,16 @@ constexpr int kQuantWarps = 8;  // the epilogue's four and four more, behind the
 template <bool RAW>
 constexpr int kThreads = 32 * (RAW ? kWarps + kQuantWarps - kEpilogueWarps : kWarps);
 
-template <int NT>
+template <int NT, bool SPLIT>
 struct Smem {
-  static constexpr int kStages = NT <= 32 ? 8 : NT == 64 ? 7 : 6;
+  static constexpr int kStages = NT <= 32 ? 8 : NT == 64 ? 7 : SPLIT ? 4 : 6;
   static constexpr int kA = MT * kBlockK, kB = NT * kBlockK, kStage = kA + kB;
   static constexpr int kScaleStages = 4, kScaleStage = 1024;  // words of the channels and the tokens
   static constexpr int kScales = kStages * kStage;
-  static constexpr int kBytes = kScales + kScaleStages * kScaleStage + 1024;  // 1024: to align the first stage
+  // The tile's parts that this block sums: [blocks of the cluster][its share of the tokens][channels] floats.  A
+  // block alone puts them where the stages were, which every product has left by then.
+  static constexpr int kEnd = kScales + kScaleStages * kScaleStage, kParts = SPLIT ? kEnd : 0;
+  static constexpr int kBytes = kEnd + (SPLIT ? NT * MT * 4 : 0) + 1024;  // 1024: to align the first stage
   static constexpr int kColScale = NT;                                   // two sets of 4 + 4 columns
   static constexpr int kTmemCols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT <= 64 ? 128 : 256;
 };
@@ -40,15 +44,6 @@ struct Bars {
   int abort;
 };
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // Eight bf16 values of a row from k on, zeros behind its K values.  The general case stays out of line: the
 // loop it would be unrolled into does not fit the instruction cache.
 __device__ __noinline__ uint4 load_any(const uint16_t* row, int k, int K) {
@@ -58,16 +53,17 @@ __device__ __noinline__ uint4 load_any(const uint16_t* row, int k, int K) {
   return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 
-template <int NT, bool RAW, typename Out>
+template <int NT, bool RAW, bool SPLIT, typename Out>
 __global__ void __launch_bounds__(kThreads<RAW>)
     linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, LinearProblem p,
-                  int token_tiles, int split, bool raw_vec, bool vec) {
-  using S = Smem<NT>;
+                  int token_tiles, int split_, bool raw_vec, bool vec) {
+  using S = Smem<NT, SPLIT>;
   constexpr int ST = S::kStages, SQ = S::kScaleStages;
   extern __shared__ unsigned char raw[];
   __shared__ Bars<ST, SQ> bar;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = SPLIT ? split_ : 1;
   const int tile = blockIdx.x / split, rank = blockIdx.x % split;  // a cluster is a tile's blocks
   const int n0 = tile / token_tiles * MT, m0 = tile % token_tiles * NT;
   const int all = scale_blocks(p.K), begin = (int)((long long)all * rank / split),
@@ -103,6 +99,10 @@ __global__ void __launch_bounds__(kThreads<RAW>)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
+  if (SPLIT) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block has started
+  auto others_started = [&] {
+    if (SPLIT) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  };
   bool ok = true;
   auto stage_free = [&](int g) {
     if (g >= ST) ok = warp_wait(&bar.empty[g % ST], (uint32_t)(g / ST - 1) & 1u, abort);
@@ -228,20 +228,28 @@ __global__ void __launch_bounds__(kThreads<RAW>)
       }
     }
   }
+  __syncwarp();
+  others_started();
+  const int share = NT / split, log_share = 31 - __clz(share);  // of the tile's tokens; powers of two
   if (warp < kEpilogueWarps) {
     if (ok) ok = warp_wait(&bar.done, 0, abort);
     tc_fence_after();
-    // A lane is a channel: the tile goes row by row (token) into the stages, which every product has left.
-    if (ok) {
-      constexpr int C = NT < 16 ? NT : 16;
+    if (ok) {  // a lane is a channel, a column a token
+      constexpr int C = 16;
 #pragma unroll 1
       for (int c = 0; c < NT; c += C) {
         float v[C];
         tmem_ld16_nowait(tmem + ((uint32_t)(32 * warp) << 16) + c, v);
         tmem_ready(v);
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c + j) * MT + 32 * warp + lane) * 4), "f"(v[j]) : "memory");
+        for (int j = 0; j < C; ++j) {
+          const int owner = (c + j) >> log_share, t = (c + j) & (share - 1);
+          const uint32_t to = base + S::kParts + ((rank * share + t) * MT + 32 * warp + lane) * 4;
+          if (SPLIT)
+            st_cluster_f32(mapa_shared(to, owner), v[j]);
+          else
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v[j]) : "memory");
+        }
       }
     }
   }
@@ -256,54 +264,47 @@ __global__ void __launch_bounds__(kThreads<RAW>)
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) tmem_dealloc(tmem, S::kTmemCols);
-  if (split > 1) cluster_sync_all();
-  if (!*abort) {
-    // This block's share of the tile's tokens, four channels a thread.
-    const int first = NT * rank / split, rows = min(NT * (rank + 1) / split, p.M - m0) - first;
-    Out* out = static_cast<Out*>(p.out) + (long long)(m0 + first) * p.N + n0;
-    for (int id = threadIdx.x; id < rows * (MT / 4); id += kThreads<RAW>) {
-      const int r = id / (MT / 4), c = id % (MT / 4) * 4, n = p.N - n0 - c;
-      if (n <= 0) continue;
-      const uint32_t at = base + ((first + r) * MT + c) * 4;
-      float4 v;
-      if (split == 1) {
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  if (SPLIT) cluster_sync_all();
+  if (*abort) return;
+  // This block's share, four channels a thread.
+  const int first = m0 + rank * share, rows = min(share, p.M - first);
+  Out* out = static_cast<Out*>(p.out) + (long long)first * p.N + n0;
+  for (int id = threadIdx.x; id < rows * (MT / 4); id += kThreads<RAW>) {
+    const int r = id / (MT / 4), c = id % (MT / 4) * 4, n = p.N - n0 - c;
+    if (n <= 0) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < split; ++s) {
+      const uint4 u = ld_shared_v4(base + S::kParts + ((s * share + r) * MT + c) * 4);
+      v.x += __uint_as_float(u.x), v.y += __uint_as_float(u.y);
+      v.z += __uint_as_float(u.z), v.w += __uint_as_float(u.w);
+    }
+    Out* to = out + (long long)r * p.N + c;
+    if constexpr (sizeof(Out) == 4) {
+      if (vec) {
+        *reinterpret_cast<float4*>(to) = v;
       } else {
-        v = ld_cluster_v4(mapa_shared(at, 0));
-        for (int s = 1; s < split; ++s) {
-          const float4 u = ld_cluster_v4(mapa_shared(at, s));
-          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        }
+        to[0] = v.x;
+        if (n > 1) to[1] = v.y;
+        if (n > 2) to[2] = v.z;
+        if (n > 3) to[3] = v.w;
       }
-      Out* to = out + (long long)r * p.N + c;
-      if constexpr (sizeof(Out) == 4) {
-        if (vec) {
-          *reinterpret_cast<float4*>(to) = v;
-        } else {
-          to[0] = v.x;
-          if (n > 1) to[1] = v.y;
-          if (n > 2) to[2] = v.z;
-          if (n > 3) to[3] = v.w;
-        }
+    } else {
+      if (vec) {
+        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
       } else {
-        if (vec) {
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        } else {
-          to[0] = f_to_bf16(v.x);
-          if (n > 1) to[1] = f_to_bf16(v.y);
-          if (n > 2) to[2] = f_to_bf16(v.z);
-          if (n > 3) to[3] = f_to_bf16(v.w);
-        }
+        to[0] = f_to_bf16(v.x);
+        if (n > 1) to[1] = f_to_bf16(v.y);
+        if (n > 2) to[2] = f_to_bf16(v.z);
+        if (n > 3) to[3] = f_to_bf16(v.w);
       }
     }
   }
-  if (split > 1) cluster_sync_all();  // no part of this block's tile is read any more
 }
 
-template <int NT, bool RAW, typename Out>
-cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
-  using S = Smem<NT>;
-  auto* kernel = linear_kernel<NT, RAW, Out>;
+template <int NT, bool RAW, bool SPLIT, typename Out>
+cudaError_t launch(const LinearProblem& p, int split, cudaStream_t stream) {
+  using S = Smem<NT, SPLIT>;
+  auto* kernel = linear_kernel<NT, RAW, SPLIT, Out>;
   // At every launch: the attribute belongs to the current device.
   const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (attr != cudaSuccess) return attr;
@@ -313,11 +314,6 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
       (!RAW && !byte_map(enc, &mx, p.x, p.K, p.M, p.x_row, NT)))
     return cudaErrorNotSupported;
   const long long tokens = (p.M + NT - 1) / NT, tiles = tokens * ((p.N + MT - 1) / MT);
-  // As many blocks per tile as the SMs allow, each with a word of scales, four steps, at the least (64 and 128
-  // tokens, 2048 x 1024: 6.2 and 7.7 us; with two steps each 7.1 and 9.5, the parts' sum costs more than it
-  // saves; with the whole of K in a block 6.9 and 8.5, and 16.4 and 18.1 us instead of 7.5 and 9.0 for K = 8192).
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 152 && split * 2 * kQuad <= scale_blocks(p.K)) split *= 2;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((unsigned)(tiles * split));
   c.blockDim = dim3(kThreads<RAW>);
@@ -333,6 +329,17 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   const bool raw_vec = RAW && aligned_to(p.raw, 16) && p.x_row % 8 == 0 && p.K % 8 == 0;
   const bool vec = p.N % 4 == 0 && aligned_to(p.out, 4 * sizeof(Out));
   return cudaLaunchKernelEx(&c, kernel, mw, mx, p, (int)tokens, split, raw_vec, vec);
+}
+
+template <int NT, bool RAW, typename Out>
+cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
+  // As many blocks per tile as the SMs allow, each with a word of scales, four steps, at the least (64 and 128
+  // tokens, 2048 x 1024: 5.8 and 7.7 us; with two steps each 7.1 and 9.5, the parts' sum costs more than it
+  // saves; with the whole of K in a block 6.9 and 8.5, and 16.4 and 18.1 us instead of 7.5 and 8.7 for K = 8192).
+  const long long tiles = (long long)((p.M + NT - 1) / NT) * ((p.N + MT - 1) / MT);
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 152 && split * 2 * kQuad <= scale_blocks(p.K)) split *= 2;
+  return split > 1 ? launch<NT, RAW, true, Out>(p, split, stream) : launch<NT, RAW, false, Out>(p, 1, stream);
 }
 
 template <typename Out>
