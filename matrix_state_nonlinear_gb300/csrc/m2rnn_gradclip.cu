@@ -163,6 +163,7 @@ __device__ __forceinline__ void load(const Vecs& v, uint4 (&u)[kVecs]) {
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) sum_squares_kernel(const __grid_constant__ Table<N> t, double* sums) {
+  let_next_launch_start();
   Stretch<N, false> stretch(t);
   double rare = 0;
   float hi = 0.f, lo = 0.f;
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(kThreads)
   Part p = stretch.next();
   Vecs v = vecs_of(p, alike(p));
   uint4 u[kVecs];
-  load(v, u);  // on its way while the sums are added
+  load(v, u);  // on its way while the last of the sums are made and added
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const double n = norm_of(sums, count);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   // A norm that is infinite or NaN clips nothing.
@@ -322,8 +324,18 @@ cudaError_t clip(const GradProblem& p, int from, int count, const double* sums, 
                  cudaStream_t stream) {
   Table<N> t;
   fill(t, p, from, count);
-  clip_kernel<N><<<blocks_of(t), kThreads, 0, stream>>>(t, sums, parts, p.max_norm, from == 0 ? p.norm : nullptr, in_place);
-  return cudaGetLastError();
+  // Starts while the launch that sums the squares ends, and waits for it before it reads sums or writes anything.
+  // Behind another of its kind (more tensors than a launch takes) it starts after that.
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks_of(t));
+  c.blockDim = dim3(kThreads);
+  c.stream = stream;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = from == 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, clip_kernel<N>, t, sums, parts, p.max_norm, from == 0 ? p.norm : nullptr, in_place);
 }
 
 }  // namespace
