@@ -5,8 +5,8 @@
 // Backward, with g = dout w and dh the gradient that arrives at h from behind:
 //   d = dh + inv g - h inv^3 mean(g h)  (dx and dresidual),  dw = sum over rows of dout h inv
 //
-// Memory-bound.  A block takes one row, held in registers, eight channels of a thread to a chunk, so that every
-// input is read once; the norm is taken of h as the stream's type holds it, which is what the next layer and the
+// Memory-bound.  A block takes one row (one of up to 256 or 512 channels half a warp or a warp of it, blockDim.y
+// rows a block), held in registers, eight channels of a thread to a chunk, so that every input is read once; the norm is taken of h as the stream's type holds it, which is what the next layer and the
 // backward read.  Where everything is 16-byte aligned (VEC) the eight are consecutive, and in 8 bits 16
 // neighbouring threads hold the 128 channels of a scale.  Otherwise they lie a block's threads apart, so that a
 // warp's accesses are still of consecutive values, and the 128 are those of four warps.
@@ -94,38 +94,54 @@ struct Raw8 {
   }
 };
 
-// Sums of two values over the block, for every thread.  `turn` (0, 1, 0, ...) chooses the scratch, so that
-// one barrier a sum is enough.
-__device__ __forceinline__ float2 block_sum(float2 s, int turn) {
-  __shared__ float2 part[2][16];
+__device__ __forceinline__ float across(float x, int lanes) { return x + __shfl_xor_sync(~0u, x, lanes); }
+__device__ __forceinline__ float2 across(float2 x, int lanes) {
+  return add2(x, make_float2(__shfl_xor_sync(~0u, x.x, lanes), __shfl_xor_sync(~0u, x.y, lanes)));
+}
+// Sum over the threads of a row, for each of them: of one value or two.  `turn` (0, 1, 0, ...) chooses the
+// scratch, so that one barrier a sum is enough.
+template <typename V>
+__device__ __forceinline__ V row_sum(V s, int turn) {
+  __shared__ V part[2][16];
+  if (blockDim.x > 16) s = across(s, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    s = add2(s, make_float2(__shfl_xor_sync(~0u, s.x, o), __shfl_xor_sync(~0u, s.y, o)));
-  const int warps = blockDim.x >> 5;
-  if (warps > 1) {
+  for (int o = 8; o > 0; o >>= 1) s = across(s, o);
+  if (blockDim.x > 32) {  // and then a row has the block for itself
+    const int warps = blockDim.x >> 5;
     if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = s;
     __syncthreads();
-    s = part[turn][0];
-    for (int w = 1; w < warps; ++w) s = add2(s, part[turn][w]);
+    if constexpr (sizeof(V) == 8) {  // shorter: no shuffles in a row (16384 x 8192: 161 us instead of 172)
+      s = part[turn][0];
+      for (int w = 1; w < warps; ++w) s = add2(s, part[turn][w]);
+    } else {  // fewer instructions
+      const int w = threadIdx.x & 15;
+      s = w < warps ? part[turn][w] : V{};
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s = across(s, o);
+    }
   }
   return s;
 }
 
-// |values| as bits, which order them and put NaN above all.
-__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The larger of two |values|, NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
 
-// Chunk r of a row in 8 bits, VEC: 16 threads to a scale.
-__device__ __forceinline__ void store_fp8(const float2 (&v)[4], int r, int D, uint8_t* q, uint8_t* scales) {
-  uint32_t top = 0, b[4];
+// Chunk r of a row in 8 bits, VEC: 16 threads to a scale.  v holds h w; the result is v inv.  The largest |v inv| is
+// the largest |v| times inv, rounding being monotonic, and the scale's inverse, a power of two, goes with inv.
+__device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r, int D, uint8_t* q, uint8_t* scales) {
+  float top = larger(larger(larger(v[0].x, v[0].y), larger(v[1].x, v[1].y)), larger(larger(v[2].x, v[2].y), larger(v[3].x, v[3].y)));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(bits(v[i].x), bits(v[i].y)));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-  const uint32_t e = scale_exponent(top);
+  for (int o = 8; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(~0u, top, o));
+  const uint32_t e = scale_exponent(__float_as_uint(top * inv) & 0x7fffffffu);
   const float2 by = pair(inverse_scale(e));
+  uint32_t b[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 y = mul2(v[i], by);
+    const float2 y = mul2(mul2(v[i], pair(inv)), by);
     b[i] = pack_e4m3x2(y.x, y.y);
   }
   const int c = 8 * (threadIdx.x + r * blockDim.x);
@@ -133,23 +149,35 @@ __device__ __forceinline__ void store_fp8(const float2 (&v)[4], int r, int D, ui
   if (c % kScaleBlock == 0) scales[c / kScaleBlock] = (uint8_t)e;
   *reinterpret_cast<uint2*>(q + c) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
 }
-// A row in 8 bits without VEC: a block has a multiple of 128 threads, so that the 128 channels of a scale are
-// one value of each thread of four warps.
+// |values| as bits, which order them and put NaN above all.
+__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// A row in 8 bits without VEC: a row has one warp, and the 128 channels of a scale are four values of each lane,
+// or a multiple of 128 threads, and they are one value of each thread of four warps.
 template <int R>
 __device__ __forceinline__ void store_fp8_any(const float2 (&v)[R][4], int D, uint8_t* q, uint8_t* scales) {
   __shared__ uint32_t tops[8 * R][16];
   const int warp = threadIdx.x >> 5;
   const float* value = &v[0][0].x;
+  const bool alone = blockDim.x == 32;
+  if (!alone) {
 #pragma unroll
-  for (int i = 0; i < 8 * R; ++i) {
-    const uint32_t top = __reduce_max_sync(~0u, bits(value[i]));
-    if ((threadIdx.x & 31) == 0) tops[i][warp] = top;
+    for (int i = 0; i < 8 * R; ++i) {
+      const uint32_t top = __reduce_max_sync(~0u, bits(value[i]));
+      if ((threadIdx.x & 31) == 0) tops[i][warp] = top;
+    }
+    __syncthreads();
   }
-  __syncthreads();
+  uint32_t e = 0;
 #pragma unroll
   for (int i = 0; i < 8 * R; ++i) {
-    const uint32_t* t = &tops[i][warp & ~3];
-    const uint32_t e = scale_exponent(max(max(t[0], t[1]), max(t[2], t[3])));
+    if (!alone) {
+      const uint32_t* t = &tops[i][warp & ~3];
+      e = scale_exponent(max(max(t[0], t[1]), max(t[2], t[3])));
+    } else if (i % 4 == 0) {
+      e = scale_exponent(__reduce_max_sync(
+          ~0u, max(max(bits(value[i]), bits(value[i + 1])), max(bits(value[i + 2]), bits(value[i + 3])))));
+    }
     const int c = i * blockDim.x + threadIdx.x;
     if (c < D) {
       if (c % kScaleBlock == 0) scales[c / kScaleBlock] = (uint8_t)e;
@@ -158,57 +186,60 @@ __device__ __forceinline__ void store_fp8_any(const float2 (&v)[R][4], int D, ui
   }
 }
 
+// Two blocks of 512 threads to an SM where a thread has one chunk (or two, VEC): left alone, the compiler takes
+// 128 registers for a chunk of eight separate channels.
 template <typename T, bool FP8, bool VEC, int R>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, R == 1 || (VEC && R == 2) ? 2 : 1)
     add_rmsnorm_kernel(AddNormProblem p, uint16_t* __restrict__ out, uint8_t* __restrict__ q, long long q_row,
                        uint8_t* __restrict__ scales) {
-  const float inv_d = 1.f / (float)p.D;
-  int turn = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    const T* stream = static_cast<const T*>(p.stream) + row * p.stream_row;
-    const uint16_t* x = p.x ? p.x + row * p.x_row : nullptr;
-    float2 h[R][4], s = pair(0.f);
-    Raw8<T, VEC> a[R];
-    Raw8<uint16_t, VEC> b[R];
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const int D = row < p.rows ? p.D : 0;  // behind the last row there are no channels
+  const T* stream = static_cast<const T*>(p.stream) + row * p.stream_row;
+  const uint16_t* x = p.x ? p.x + row * p.x_row : nullptr;
+  float2 h[R][4], s = pair(0.f);
+  Raw8<T, VEC> a[R];
+  Raw8<uint16_t, VEC> b[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      a[r].load(stream, r, p.D);
-      if (x) b[r].load(x, r, p.D);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      a[r].get(h[r]);
-      if (x) {
-        float2 v[4];
-        b[r].get(v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[r][i] = add2(h[r][i], v[i]);
-        a[r].set(h[r]);
-        if (sizeof(T) == 2) a[r].get(h[r]);
-      }
-      if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D, r, p.D);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = fma2(h[r][i], h[r][i], s);
-    }
-    const float inv = rsqrtf(block_sum(make_float2(s.x + s.y, 0.f), turn).x * inv_d + p.eps);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      Raw8<float, VEC> u;
-      float2 w[4];
-      u.load(p.w, r, p.D);
-      u.get(w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[r][i] = mul2(mul2(h[r][i], pair(inv)), w[i]);
-      if constexpr (FP8 && VEC) {
-        store_fp8(h[r], r, p.D, q + row * q_row, scales + row * scale_blocks(p.D));
-      } else if constexpr (!FP8) {
-        Raw8<uint16_t, VEC> o;
-        o.set(h[r]);
-        o.store(out + row * p.D, r, p.D);
-      }
-    }
-    if constexpr (FP8 && !VEC) store_fp8_any<R>(h, p.D, q + row * q_row, scales + row * scale_blocks(p.D));
+  for (int r = 0; r < R; ++r) {
+    a[r].load(stream, r, D);
+    if (x) b[r].load(x, r, D);
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    a[r].get(h[r]);
+    if (x) {
+      float2 v[4];
+      b[r].get(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[r][i] = add2(h[r][i], v[i]);
+      a[r].set(h[r]);
+      if (sizeof(T) == 2) a[r].get(h[r]);
+    }
+    if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D, r, D);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fma2(h[r][i], h[r][i], s);
+  }
+  const float inv = rsqrtf(row_sum(s.x + s.y, 0) * (1.f / (float)p.D) + p.eps);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    Raw8<float, VEC> u;
+    float2 w[4];
+    u.load(p.w, r, p.D);
+    u.get(w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[r][i] = mul2(h[r][i], w[i]);
+    if constexpr (!FP8 || !VEC)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[r][i] = mul2(h[r][i], pair(inv));
+    if constexpr (FP8 && VEC) {
+      store_fp8(h[r], inv, r, D, q + row * q_row, scales + row * scale_blocks(p.D));
+    } else if constexpr (!FP8) {
+      Raw8<uint16_t, VEC> o;
+      o.set(h[r]);
+      o.store(out + row * p.D, r, D);
+    }
+  }
+  if constexpr (FP8 && !VEC) store_fp8_any<R>(h, D, q + row * q_row, scales + row * scale_blocks(p.D));
 }
 
 // 16 bytes to shared memory without passing through registers, by way of L1 (SECTORS: where a thread's next
@@ -235,18 +266,18 @@ template <typename T, int R>
 constexpr int kAhead = R * sizeof(T) <= 4 && sizeof(T) == 2 ? 4 : R * sizeof(T) <= 8 ? 2 : 1;
 template <typename T, int R>
 constexpr int kRingPerThread = kAhead<T, R> * (2 * (int)sizeof(T) / 2 + 1) * R * 16;  // bytes
-template <typename T, bool VEC, int R>
+template <typename T, bool VEC, int R, bool MULTI>
 struct RowStream {
   static constexpr int kRows = kAhead<T, R>, kParts = sizeof(T) / 2;  // 16-byte pieces of 8 values
   const AddNormBackwardProblem& p;
-  uint4* own;  // [kRows][kParts + 1 + kParts][R][threads]
+  uint4* own;  // [kRows][kParts + 1 + kParts][R][threads of the block]
   int at = 0, to = 0;
   Raw8<T, VEC> hr[R], er[R];
   Raw8<uint16_t, VEC> dr[R];
 
-  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, uint4* smem) : p(p_), own(smem + threadIdx.x) {}
+  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, uint4* smem) : p(p_), own(smem + (MULTI ? threadIdx.y * blockDim.x : 0) + threadIdx.x) {}
   __device__ __forceinline__ uint4* slot(int stage, int part, int r) const {
-    return own + ((stage * (2 * kParts + 1) + part) * R + r) * blockDim.x;
+    return own + ((stage * (2 * kParts + 1) + part) * R + r) * (blockDim.x * (MULTI ? blockDim.y : 1));
   }
   __device__ __forceinline__ void start(long long row) {
     if (row < p.rows) {
@@ -285,8 +316,8 @@ struct RowStream {
   // dh of the row at hand is taken before the sums where there is room to hold it across them (65536 x 2048
   // float32: 317 us, 364 where it is taken after them; 4000 x 16384 bf16: 215 and 124).
   static constexpr bool kEarly = VEC && R <= 2;
-  // h, dout and, if early, dh of `row`, zeros behind the last channel; a later row starts.
-  __device__ __forceinline__ void next(long long row, long long step, float2 (&h)[R][4], float2 (&d)[R][4],
+  // h, dout and, if early, dh of `row`, zeros behind the last of its D channels; a later row starts.
+  __device__ __forceinline__ void next(long long row, int D, long long step, float2 (&h)[R][4], float2 (&d)[R][4],
                                        float2 (&e)[R][4]) {
     if constexpr (VEC) {
       start(row + (kRows - 1) * step);
@@ -296,7 +327,7 @@ struct RowStream {
     for (int r = 0; r < R; ++r) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[r][i] = d[r][i] = e[r][i] = pair(0.f);
-      if (!VEC || Raw8<T, VEC>::first(r) < p.D) {
+      if (VEC ? Raw8<T, VEC>::first(r) < D : D > 0) {
         if constexpr (VEC) {
 #pragma unroll
           for (int k = 0; k < kParts; ++k) hr[r].u[k] = *slot(at, k, r);
@@ -312,8 +343,8 @@ struct RowStream {
     }
   }
   // dh of chunk r, where it is late.
-  __device__ __forceinline__ void late(int r, float2 (&e)[4]) {
-    if (kEarly || !p.dh || (VEC && Raw8<T, VEC>::first(r) >= p.D)) return;
+  __device__ __forceinline__ void late(int r, int D, float2 (&e)[4]) {
+    if (kEarly || !p.dh || (VEC ? Raw8<T, VEC>::first(r) >= D : D == 0)) return;
     if constexpr (VEC)
 #pragma unroll
       for (int k = 0; k < kParts; ++k) er[r].u[k] = *slot(at, kParts + 1 + k, r);
@@ -327,9 +358,9 @@ struct RowStream {
   }
 };
 
-// Block b takes rows b, + blocks, ...; its channels' part of dw adds up in registers and goes to row b of
-// `part`.
-template <typename T, bool VEC, int R>
+// Block b takes rows b, + blocks, ... (MULTI: blockDim.y of them at once); its channels' part of dw adds up in
+// registers and goes to row b of `part`.
+template <typename T, bool VEC, int R, bool MULTI>
 __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
     add_rmsnorm_backward_kernel(AddNormBackwardProblem p, float* __restrict__ part) {
   extern __shared__ uint4 ring[];
@@ -347,13 +378,18 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[r][i] = pair(0.f);
   }
-  RowStream<T, VEC, R> rows(p, ring);
-  rows.begin(blockIdx.x, gridDim.x);
+  RowStream<T, VEC, R, MULTI> rows(p, ring);
+  const int at_once = MULTI ? blockDim.y : 1;
+  const long long step = (long long)gridDim.x * at_once;
+  long long row = (long long)blockIdx.x * at_once + (MULTI ? threadIdx.y : 0);
+  rows.begin(row, step);
   int turn = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+  // All threads of a block go round equally often; behind the last row there are no channels.
+  for (long long first = (long long)blockIdx.x * at_once; first < p.rows; first += step, row += step, turn ^= 1) {
+    const int D = !MULTI || row < p.rows ? p.D : 0;
     float2 h[R][4], d[R][4], s1 = pair(0.f), s2 = pair(0.f);
     float2 e[R][4];
-    rows.next(row, gridDim.x, h, d, e);
+    rows.next(row, D, step, h, d, e);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 w[4];
@@ -364,13 +400,13 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
         s2 = fma2(mul2(d[r][i], kKeep ? kept[kKeep ? r : 0][i] : w[i]), h[r][i], s2);
       }
     }
-    const float2 sum = block_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
-    const float inv = rsqrtf(sum.x * inv_d + p.eps);
+    const float2 sum = row_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
+    const float inv = !MULTI || D > 0 ? rsqrtf(sum.x * inv_d + p.eps) : 0.f;
     const float2 iv = pair(inv), back = pair(-inv * inv * inv * (sum.y * inv_d));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 o[4], w[4];
-      rows.late(r, e[r]);
+      rows.late(r, D, e[r]);
       if constexpr (!kKeep) weight(r, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -380,34 +416,56 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
       if (p.dx) {
         Raw8<uint16_t, VEC> u;
         u.set(o);
-        u.store(p.dx + row * p.D, r, p.D);
+        u.store(p.dx + row * p.D, r, D);
       }
       if (p.dresidual) {
         Raw8<T, VEC> u;
         u.set(o);
-        u.store(static_cast<T*>(p.dresidual) + row * p.D, r, p.D);
+        u.store(static_cast<T*>(p.dresidual) + row * p.D, r, D);
       }
     }
-    rows.done(row, gridDim.x);
+    rows.done(row, step);
+  }
+  float* to = part + (long long)blockIdx.x * p.D;
+  if (MULTI) {  // the block's rows at once add up first, in the rows' place
+    copies_wait<0>();
+    __syncthreads();
+    to = reinterpret_cast<float*>(ring) + threadIdx.y * p.D;
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     Raw8<float, VEC> u;
     u.set(dw[r]);
-    u.store(part + (long long)blockIdx.x * p.D, r, p.D);
+    u.store(to, r, p.D);
+  }
+  if (MULTI) {
+    __syncthreads();
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < p.D; c += blockDim.x * blockDim.y) {
+      float s = 0.f;
+      for (int y = 0; y < blockDim.y; ++y) s += reinterpret_cast<const float*>(ring)[y * p.D + c];
+      part[(long long)blockIdx.x * p.D + c] = s;
+    }
   }
 }
 
-// Threads of a row's block for R chunks per thread: whole warps, without VEC four at a time.
-int threads_for(int D, int R, bool vec) {
-  const int chunks = (D + 7) / 8, whole = vec ? 32 : 128;
-  return ((chunks + R - 1) / R + whole - 1) / whole * whole;
+// How rows are spread: chunks and threads per row, rows per block.
+struct Spread {
+  int R, threads, rows;
+  dim3 block() const { return dim3(threads, rows); }
+};
+// Threads of a row for R chunks each: half a warp, whole warps, or (8 bits, not VEC) a warp or four at a time.
+int threads_for(int D, int R, bool vec, bool fp8) {
+  const int n = ((D + 7) / 8 + R - 1) / R;
+  if (vec && n <= 16) return 16;
+  const int whole = !vec && fp8 && n > 32 ? 128 : 32;
+  return (n + whole - 1) / whole * whole;
 }
-// Chunks per thread, the fewest from `least` on whose block has at most 512 threads.
-int chunks_each(int D, int least) {
+// With `least` chunks a thread, or more where a row would have more than 512 threads.
+Spread spread_of(int D, int least, bool vec, bool fp8) {
   int R = least;
-  while (threads_for(D, R, true) > 512) R *= 2;
-  return R;
+  while (threads_for(D, R, vec, fp8) > 512) R *= 2;
+  const int threads = threads_for(D, R, vec, fp8);
+  return Spread{R, threads, threads <= 32 ? 256 / threads : 1};
 }
 
 template <int N>
@@ -422,13 +480,15 @@ cudaError_t with_chunks(int R, F f) {
 template <typename T, bool FP8, bool VEC>
 cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
                     cudaStream_t stream) {
-  // Few rows are spread as wide as they go; of many, two chunks a thread (65536 x 2048: 153 us; one chunk
+  // Few rows are spread as wide as they go; of many, a thread takes two chunks (65536 x 2048: 153 us; one chunk
   // 169, four 158; 8191 x 4096 in 8 bits: 58, 65, 64).
-  const int R = chunks_each(p.D, VEC && p.rows >= 152 * 16 ? 2 : 1);
-  return with_chunks(R, [&](auto r) {
-    constexpr int N = decltype(r)::value;
-    const unsigned blocks = (unsigned)(p.rows < 0x7fffffff ? p.rows : 0x7fffffff);
-    add_rmsnorm_kernel<T, FP8, VEC, N><<<blocks, threads_for(p.D, N, VEC), 0, stream>>>(p, out, q, q_row, scales);
+  const bool many = p.rows >= 152 * 16;
+  Spread s = spread_of(p.D, !many ? 1 : VEC ? 2 : 1, VEC, FP8);
+  if (!many) s.rows = s.threads < 32 ? 2 : 1;
+  return with_chunks(s.R, [&](auto r) {
+    const long long blocks = (p.rows + s.rows - 1) / s.rows;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;  // more than a terabyte
+    add_rmsnorm_kernel<T, FP8, VEC, decltype(r)::value><<<(unsigned)blocks, s.block(), 0, stream>>>(p, out, q, q_row, scales);
     return cudaGetLastError();
   });
 }
@@ -451,10 +511,12 @@ cudaError_t dispatch(const AddNormProblem& p, bool vec, uint16_t* out, uint8_t* 
              : forward<uint16_t, FP8, false>(p, out, q, q_row, scales, stream);
 }
 
-// Blocks of the backward, and rows of its sums: 1024 threads for every SM.
-int backward_blocks(long long rows, int D) {
-  const long long most = 152LL * (1024 / threads_for(D, chunks_each(D, 1), true));
-  return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+// The backward's spread (several rows a block only with a chunk per thread), and its blocks, which are the rows of its sums: 1024 threads for every SM.
+Spread backward_spread(int D, bool vec) { return spread_of(D, 1, vec, false); }
+int backward_blocks(long long rows, int D, bool vec) {
+  const Spread s = backward_spread(D, vec);
+  const long long most = 152LL * (1024 / (s.threads * s.rows)), all = (rows + s.rows - 1) / s.rows;
+  return (int)(all < most ? (all > 0 ? all : 1) : most);
 }
 
 }  // namespace
@@ -467,28 +529,42 @@ cudaError_t launch_add_rmsnorm_fp8(const AddNormProblem& p, uint8_t* q, long lon
   return dispatch<true>(p, vec_ok(p), nullptr, q, q_row, scales, stream);
 }
 
-size_t add_rmsnorm_backward_workspace_floats(long long rows, int D) { return (size_t)backward_blocks(rows, D) * D; }
+size_t add_rmsnorm_backward_workspace_floats(long long rows, int D) {
+  const int a = backward_blocks(rows, D, false), b = backward_blocks(rows, D, true);
+  return (size_t)(a > b ? a : b) * D;
+}
 
 cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStream_t stream) {
   if (p.rows == 0) return cudaMemsetAsync(p.dw, 0, sizeof(float) * p.D, stream);
   const bool vec = p.D % 8 == 0 && aligned_to(p.w, 16) && aligned_to(p.h, 16) && aligned_to(p.dout, 16) &&
                    aligned_to(p.dh, 16) && aligned_to(p.dx, 16) && aligned_to(p.dresidual, 16);
-  const int blocks = backward_blocks(p.rows, p.D);
-  const cudaError_t err = with_chunks(chunks_each(p.D, 1), [&](auto r) {
+  const int blocks = backward_blocks(p.rows, p.D, vec);
+  const Spread s = backward_spread(p.D, vec);
+  const cudaError_t err = with_chunks(s.R, [&](auto r) {
     constexpr int R = decltype(r)::value;
     auto go = [&](auto kernel) {
-      const int threads = threads_for(p.D, R, vec);
-      const int bytes = vec ? threads * (p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>) : 0;
+      const int ring = vec ? s.threads * s.rows * (p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>) : 0;
+      const int sums = s.rows > 1 ? s.rows * p.D * 4 : 0, bytes = ring > sums ? ring : sums;
       // At every launch: the attribute belongs to the current device.
       const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       if (attr != cudaSuccess) return attr;
-      kernel<<<blocks, threads, bytes, stream>>>(p, p.ws);
+      kernel<<<blocks, s.block(), bytes, stream>>>(p, p.ws);
       return cudaGetLastError();
     };
+    if constexpr (R == 1) {
+      if (s.rows > 1) {
+        if (p.stream_f32)
+          return vec ? go(add_rmsnorm_backward_kernel<float, true, 1, true>)
+                     : go(add_rmsnorm_backward_kernel<float, false, 1, true>);
+        return vec ? go(add_rmsnorm_backward_kernel<uint16_t, true, 1, true>)
+                   : go(add_rmsnorm_backward_kernel<uint16_t, false, 1, true>);
+      }
+    }
     if (p.stream_f32)
-      return vec ? go(add_rmsnorm_backward_kernel<float, true, R>) : go(add_rmsnorm_backward_kernel<float, false, R>);
-    return vec ? go(add_rmsnorm_backward_kernel<uint16_t, true, R>)
-               : go(add_rmsnorm_backward_kernel<uint16_t, false, R>);
+      return vec ? go(add_rmsnorm_backward_kernel<float, true, R, false>)
+                 : go(add_rmsnorm_backward_kernel<float, false, R, false>);
+    return vec ? go(add_rmsnorm_backward_kernel<uint16_t, true, R, false>)
+               : go(add_rmsnorm_backward_kernel<uint16_t, false, R, false>);
   });
   if (err != cudaSuccess) return err;
   return launch_sum_rows(p.ws, p.dw, nullptr, blocks, p.D, p.D, p.D, stream);

@@ -89,33 +89,62 @@ constexpr int kGroup = 4 * kQuad;  // and to a group of words
 
 // Groups of scale words of ROWS rows per lane: the 16 blocks from i on, loaded one group ahead of their use,
 // all loads before anything that waits for them.  Blocks behind a row's last get any scale: nothing uses them.
+// A row of `blocks` scales starts anywhere, so a word of it is made of two whole words of memory; only words
+// that hold a byte of the row are read, and of the tensor's first and last rows, before and behind which memory
+// may end, bytes.
 template <int ROWS>
 struct ScaleWords {
   const uint8_t* row[ROWS];
-  bool live[ROWS];
+  bool live[ROWS], edge[ROWS];
   bool words;  // rows and their starts are whole words
   int blocks;  // of a row
-  uint32_t next[ROWS][4];
-  __device__ __forceinline__ void fetch(int i) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        next[r][q] = 0x7f7f7f7fu;  // 1
-        if (words && live[r] && i + q * kQuad < blocks)
-          next[r][q] = *reinterpret_cast<const uint32_t*>(row[r] + i + q * kQuad);
-      }
-    if (!words) fetch_bytes(i);
+  uint32_t next[ROWS][4], over[ROWS];
+  // The tensor's row m of `rows`.
+  __device__ __forceinline__ void aim(int r, const uint8_t* scales, long long m, long long rows) {
+    live[r] = m < rows, edge[r] = m == 0 || m == rows - 1;
+    row[r] = scales + m * blocks;
   }
-  __device__ __forceinline__ void fetch_bytes(int i) {
+  __device__ __forceinline__ void fetch(int i) {
+    if (words) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          next[r][q] = 0x7f7f7f7fu;  // 1
+          if (live[r] && i + 4 * q < blocks) next[r][q] = *reinterpret_cast<const uint32_t*>(row[r] + i + 4 * q);
+        }
+      return;
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      uint32_t b[kGroup];
+      const int first = i - (int)(reinterpret_cast<uintptr_t>(row[r] + i) & 3u);  // from the row's start
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) b[j] = live[r] && i + j < blocks ? row[r][i + j] : 0x7fu;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) next[r][q] = b[4 * q] | b[4 * q + 1] << 8 | b[4 * q + 2] << 16 | b[4 * q + 3] << 24;
+      for (int q = 0; q < 5; ++q) {
+        uint32_t w = 0x7f7f7f7fu;
+        if (live[r] && first + 4 * q < blocks) {
+          if (!edge[r])
+            w = *reinterpret_cast<const uint32_t*>(row[r] + first + 4 * q);
+          else
+            w = edge_word(row[r] + first + 4 * q, -first - 4 * q, blocks - first - 4 * q);
+        }
+        if (q < 4)
+          next[r][q] = w;
+        else
+          over[r] = w;
+      }
     }
+  }
+  // The word's bytes from lo to hi.
+  static __device__ __noinline__ uint32_t edge_word(const uint8_t* p, int lo, int hi) {
+    uint32_t w = 0;
+    for (int j = max(lo, 0); j < min(hi, 4); ++j) w |= (uint32_t)p[j] << (8 * j);
+    return w;
+  }
+  // Word q of the group that was fetched from block i on.
+  __device__ __forceinline__ uint32_t word(int r, int q, int i) const {
+    if (words) return next[r][q];
+    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(row[r] + i) & 3u;
+    return __funnelshift_r(next[r][q], q < 3 ? next[r][q < 3 ? q + 1 : 0] : over[r], 8 * off);
   }
 };
 

@@ -138,7 +138,7 @@ m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* 
 
 size_t m2rnn_linear_quantise_workspace_bytes(int x_f32, long long M, int K) {
   if (M < 1 || M > 0x7fffff00LL || K < 1 || (M <= kRawRows && !x_f32)) return 0;
-  return (size_t)M * ((K + 15LL) / 16 * 16 + scale_blocks(K));
+  return (size_t)M * ((K + 15LL) / 16 * 16 + scale_blocks(K));  // q, then its scales
 }
 
 m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row, const uint8_t* w, long long w_row,

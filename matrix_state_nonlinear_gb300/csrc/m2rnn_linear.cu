@@ -123,17 +123,12 @@ __global__ void __launch_bounds__(kThreads<RAW>)
     ScaleWords<1> w;
     ScaleWords<R> x;
     w.blocks = x.blocks = all;
-    w.row[0] = p.w_scales + (size_t)(n0 / kScaleBlock) * all;
-    w.live[0] = true;
     const bool words = all % kQuad == 0 && begin % kQuad == 0;
     w.words = words && reinterpret_cast<uintptr_t>(p.w_scales) % kQuad == 0;
     x.words = words && reinterpret_cast<uintptr_t>(p.x_scales) % kQuad == 0;
+    w.aim(0, p.w_scales, n0 / kScaleBlock, scale_blocks(p.N));
 #pragma unroll
-    for (int c = 0; c < R; ++c) {
-      const int m = m0 + 32 * c + lane;
-      x.live[c] = !RAW && m < p.M && 32 * c + lane < NT;
-      x.row[c] = RAW ? nullptr : p.x_scales + (size_t)m * all;
-    }
+    for (int c = 0; c < R; ++c) x.aim(c, p.x_scales, m0 + 32 * c + lane, RAW ? 0 : p.M);
     w.fetch(begin);
     wait_for_launch_before();
     x.fetch(begin);
@@ -141,9 +136,9 @@ __global__ void __launch_bounds__(kThreads<RAW>)
       uint32_t v[4], u[4][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        v[q] = w.next[0][q];
+        v[q] = w.word(0, q, i);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) u[q][r] = x.next[r < R ? r : 0][q];
+        for (int r = 0; r < 4; ++r) u[q][r] = x.word(r < R ? r : 0, q, i);
       }
       if (i + kGroup < end) w.fetch(i + kGroup), x.fetch(i + kGroup);
 #pragma unroll

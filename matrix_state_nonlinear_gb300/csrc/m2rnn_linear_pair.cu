@@ -20,7 +20,9 @@ constexpr int kStages = 6;
 constexpr int kOperand = kRows * kBlockK, kStage = 2 * kOperand;
 constexpr int kScaleStages = 3, kScaleWord = 512 + 1024, kScaleStage = 4 * kScaleWord;  // 128 tokens, 256 channels
 constexpr int kScales = kStages * kStage;
-constexpr int kSmemBytes = kScales + kScaleStages * kScaleStage + 1024;  // 1024: to align the first stage
+constexpr int kTurn = kScales + kScaleStages * kScaleStage;  // 32 tokens by 32 channels for each epilogue warp
+constexpr int kTurnRow = 32 * 2 + 4, kTurnBytes = 32 * kTurnRow;  // of two bytes; 4: rows in different banks
+constexpr int kSmemBytes = kTurn + 4 * kTurnBytes + 1024;    // 1024: to align the first stage
 constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kThreads = 224;
 constexpr int kTmemCols = 512, kColSecond = 224, kColScale = 480;  // scales: two sets of 4 + 8 columns
 constexpr int kRun = 8;                   // token tiles that share a run of channel tiles
@@ -126,17 +128,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     auto aim = [&](int t) {
       const int2 at = tile_at_index(t, token_tiles, channel_tiles);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int m = at.x * kTile + rank * kRows + 32 * c + lane;
-        x.live[c] = m < p.M;
-        x.row[c] = p.x_scales + (size_t)m * blocks;
-      }
+      for (int c = 0; c < 4; ++c) x.aim(c, p.x_scales, (long long)at.x * kTile + rank * kRows + 32 * c + lane, p.M);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int n = at.y * 2 + c;
-        w.live[c] = (long long)n * kScaleBlock < p.N;
-        w.row[c] = p.w_scales + (size_t)n * blocks;
-      }
+      for (int c = 0; c < 2; ++c) w.aim(c, p.w_scales, at.y * 2 + c, scale_blocks(p.N));
       x.fetch(0), w.fetch(0);
     };
     if (pair < tiles) aim(pair);
@@ -147,8 +141,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) u[q][r] = x.next[r][q];
-          v[0][q] = w.next[0][q], v[1][q] = w.next[1][q];
+          for (int r = 0; r < 4; ++r) u[q][r] = x.word(r, q, i);
+          v[0][q] = w.word(0, q, i), v[1][q] = w.word(1, q, i);
         }
         if (i + kGroup < blocks)
           x.fetch(i + kGroup), w.fetch(i + kGroup);
@@ -232,32 +226,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
                          : "memory");
         }
         const int n0 = at.y * kTile + 32 * c;
-        if (m < p.M && n0 < p.N) {
-          if (vec) {
-            constexpr int V = 32 / sizeof(Out);
+        if (vec && m < p.M) {
+          constexpr int V = 32 / sizeof(Out);
 #pragma unroll
-            for (int k = 0; k < 32; k += V) {
-              uint32_t u[8];
+          for (int k = 0; k < 32; k += V) {
+            uint32_t u[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if constexpr (sizeof(Out) == 4)
-                  u[e] = __float_as_uint(v[k + e]);
-                else
-                  u[e] = pack_bf16x2(v[k + 2 * e], v[k + 2 * e + 1]);
-              }
-              if (n0 + k < p.N)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + n0 + k), "r"(u[0]),
-                             "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                             : "memory");
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              if (n0 + k >= p.N) break;
+            for (int e = 0; e < 8; ++e) {
               if constexpr (sizeof(Out) == 4)
-                out[n0 + k] = v[k];
+                u[e] = __float_as_uint(v[k + e]);
               else
-                out[n0 + k] = f_to_bf16(v[k]);
+                u[e] = pack_bf16x2(v[k + 2 * e], v[k + 2 * e + 1]);
+            }
+            if (n0 + k < p.N)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + n0 + k), "r"(u[0]),
+                           "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                           : "memory");
+          }
+        }
+        if (!vec) {
+          // Rows that do not start on whole sectors: turned in shared memory, so that a warp writes neighbouring channels
+          // of one token (of 32-bit results half of them at a time).
+          constexpr int W = 64 / sizeof(Out);
+          const uint32_t turn = base + kTurn + warp * kTurnBytes;
+          const long long m_first = m - lane;
+#pragma unroll
+          for (int half = 0; half < 32 / W; ++half) {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              uint32_t u;
+              if constexpr (sizeof(Out) == 4)
+                u = __float_as_uint(v[half * W + k]);
+              else
+                u = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(turn + lane * kTurnRow + 4 * k), "r"(u) : "memory");
+            }
+            __syncwarp();
+            const int k = lane % W, n = n0 + half * W + k;
+            Out* to = static_cast<Out*>(p.out) + m_first * p.N + n;
+#pragma unroll 4
+            for (int t = lane / W; t < 32; t += 32 / W) {
+              uint32_t u;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"((turn + t * kTurnRow + k * (int)sizeof(Out)) & ~3u));
+              if (m_first + t < p.M && n < p.N) {
+                if constexpr (sizeof(Out) == 4)
+                  to[(long long)t * p.N] = __uint_as_float(u);
+                else
+                  to[(long long)t * p.N] = (uint16_t)(k & 1 ? u >> 16 : u);
+              }
             }
           }
         }

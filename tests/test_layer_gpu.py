@@ -96,7 +96,7 @@ def test_quantise_infinities():
 # ---------------------------------------------------------------- residual norm
 # rows, D: one channel, odd widths, one and several threads' chunks, wide rows, many rows
 NORM = [(1, 1), (3, 7), (2, 8), (5, 129), (9, 1000), (4, 1001), (64, 2048), (3, 4104), (2, 8192), (2, 16384), (2, 16383),
-        (2600, 264), (2500, 2100)]
+        (2600, 264), (2500, 2100), (2701, 96), (5003, 128), (3001, 134), (2439, 505), (2433, 1001), (2600, 1032), (40, 200)]
 
 
 def norm_case(rows, D, f32, residual, seed=0, pad=0):
@@ -220,7 +220,7 @@ def test_norm_backward_repeats_and_empty():
 LINEAR = [(1, 1, 1), (1, 128, 128), (1, 2000, 1000), (2, 129, 127), (3, 8, 4096), (7, 256, 384), (16, 200, 144), (17, 130, 513),
           (33, 96, 2048), (64, 520, 640), (65, 128, 256), (100, 4384, 300), (127, 127, 127), (129, 257, 129), (200, 300, 1300),
           (255, 384, 96), (257, 136, 8192), (520, 1000, 520), (1021, 264, 200), (3, 5, 20000),
-          (2100, 2200, 300), (4000, 1300, 1280), (260, 16500, 2180)]
+          (2100, 2200, 300), (4000, 1300, 1280), (260, 16500, 2180), (2500, 2001, 700), (3000, 1158, 1821), (2049, 2052, 4000)]
 
 
 def linear_case(M, N, K, seed=0):
@@ -262,6 +262,24 @@ def test_linear_leaves_what_is_not_its_own():
     wide = torch.empty((M, 512), dtype=torch.uint8, device=DEV).fill_(0x7f).view(FP8)  # NaN around the values
     wide[:, 16:16 + K].copy_(args[0])
     assert torch.equal(pkg.linear_fp8(wide[:, 16:16 + K], *args[1:]), want)
+
+
+@pytest.mark.parametrize("K", [1300, 5000])
+@pytest.mark.parametrize("first", [1, 2, 3])
+def test_linear_of_some_tokens(K, first):
+    """Scales of an odd number to a row, from any row on: whatever lies around the part does not count."""
+    x, sx, w, sw = linear_case(300, 2100 if K == 1300 else 200, K, 3)
+    want = pkg.linear_fp8(x, sx, w, sw)
+    s = torch.full((302, sx.shape[1]), 255, dtype=torch.uint8, device=DEV).view(E8M0)  # NaN around it
+    s.view(torch.uint8)[1:301] = sx.view(torch.uint8)
+    for last in (300, 299, 270):
+        out = pkg.linear_fp8(x[first:last], s[1 + first:1 + last], w, sw)
+        assert torch.equal(out, want[first:last])
+    M = 2400  # and the pairs' kernel
+    x, sx, w, sw = linear_case(M, 2100, K, 4)
+    want = pkg.linear_fp8(x, sx, w, sw)
+    assert torch.equal(pkg.linear_fp8(x[first:], sx[first:], w, sw), want[first:])
+    assert torch.equal(pkg.linear_fp8(x[:-first], sx[:-first], w, sw), want[:-first])
 
 
 def test_linear_nan_stays_in_its_row_and_block():
