@@ -136,9 +136,12 @@ m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* 
   return done(launch_linear_fp8(p, static_cast<cudaStream_t>(stream)));
 }
 
+// Bytes from row to row of activations in the workspace: rows start on lines of the cache, short ones on 16 bytes.
+static long long quantised_row(int K) { return K > 128 ? (K + 127LL) / 128 * 128 : (K + 15LL) / 16 * 16; }
+
 size_t m2rnn_linear_quantise_workspace_bytes(int x_f32, long long M, int K) {
   if (M < 1 || M > 0x7fffff00LL || K < 1 || (M <= kRawRows && !x_f32)) return 0;
-  return (size_t)M * ((K + 15LL) / 16 * 16 + scale_blocks(K));  // q, then its scales
+  return (size_t)M * (quantised_row(K) + scale_blocks(K));  // q, then its scales
 }
 
 m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row, const uint8_t* w, long long w_row,
@@ -154,7 +157,7 @@ m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row
   const auto at = static_cast<cudaStream_t>(stream);
   LinearProblem p{nullptr, nullptr, nullptr, w, w_scales, x_row, w_row, out, out_f32 != 0, (int)M, N, K, status};
   if (need > 0) {
-    p.x_row = (K + 15LL) / 16 * 16;
+    p.x_row = quantised_row(K);
     uint8_t *q = static_cast<uint8_t*>(workspace), *scales = q + M * p.x_row;
     st = done(launch_quantise_rows(x, x_f32 != 0, x_row, q, p.x_row, scales, M, K, at));
     if (st != M2RNN_OK) return st;

@@ -26,14 +26,16 @@ constexpr int kThreads = 32 * (RAW ? kWarps + kQuantWarps - kEpilogueWarps : kWa
 
 template <int NT, bool SPLIT>
 struct Smem {
-  static constexpr int kStages = NT <= 32 ? 8 : NT == 64 ? 7 : SPLIT ? 4 : 6;
+  static constexpr int kStages = NT <= 32 ? 8 : NT == 64 ? 7 : 6;
   static constexpr int kA = MT * kBlockK, kB = NT * kBlockK, kStage = kA + kB;
   static constexpr int kScaleStages = 4, kScaleStage = 1024;  // words of the channels and the tokens
   static constexpr int kScales = kStages * kStage;
-  // The tile's parts that this block sums: [blocks of the cluster][its share of the tokens][channels] floats.  A
-  // block alone puts them where the stages were, which every product has left by then.
-  static constexpr int kEnd = kScales + kScaleStages * kScaleStage, kParts = SPLIT ? kEnd : 0;
-  static constexpr int kBytes = kEnd + (SPLIT ? NT * MT * 4 : 0) + 1024;  // 1024: to align the first stage
+  // The tile's parts that this block sums: [blocks of the cluster][its share of the tokens][channels] floats.  Those
+  // of a block alone, or of 128 tokens, which would leave room for four stages, lie where the stages were; then
+  // the cluster's blocks meet before they write there.
+  static constexpr bool kOver = !SPLIT || NT == 128;
+  static constexpr int kEnd = kScales + kScaleStages * kScaleStage, kParts = kOver ? 0 : kEnd;
+  static constexpr int kBytes = kEnd + (kOver ? 0 : (NT + 7) * MT * 4) + 1024;  // 1024: to align the first stage
   static constexpr int kColScale = NT;                                   // two sets of 4 + 4 columns
   static constexpr int kTmemCols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT <= 64 ? 128 : 256;
 };
@@ -66,8 +68,10 @@ __global__ void __launch_bounds__(kThreads<RAW>)
   const int split = SPLIT ? split_ : 1;
   const int tile = blockIdx.x / split, rank = blockIdx.x % split;  // a cluster is a tile's blocks
   const int n0 = tile / token_tiles * MT, m0 = tile % token_tiles * NT;
-  const int all = scale_blocks(p.K), begin = (int)((long long)all * rank / split),
-            end = (int)((long long)all * (rank + 1) / split);
+  // Stretches of K are of whole words of scales.
+  const int all = scale_blocks(p.K), quads = (all + kQuad - 1) / kQuad;
+  const int begin = kQuad * (int)((long long)quads * rank / split),
+            end = min(all, kQuad * (int)((long long)quads * (rank + 1) / split));
   volatile int* abort = &bar.abort;
 
   const int steps = end - begin;
@@ -99,10 +103,8 @@ __global__ void __launch_bounds__(kThreads<RAW>)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  if (SPLIT) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block has started
-  auto others_started = [&] {
-    if (SPLIT) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  };
+  constexpr bool kMeet = SPLIT && S::kOver;
+  if (SPLIT && !kMeet) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block has started
   bool ok = true;
   auto stage_free = [&](int g) {
     if (g >= ST) ok = warp_wait(&bar.empty[g % ST], (uint32_t)(g / ST - 1) & 1u, abort);
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kThreads<RAW>)
     ScaleWords<1> w;
     ScaleWords<R> x;
     w.blocks = x.blocks = all;
-    const bool words = all % kQuad == 0 && begin % kQuad == 0;
+    const bool words = all % kQuad == 0;
     w.words = words && reinterpret_cast<uintptr_t>(p.w_scales) % kQuad == 0;
     x.words = words && reinterpret_cast<uintptr_t>(p.x_scales) % kQuad == 0;
     w.aim(0, p.w_scales, n0 / kScaleBlock, scale_blocks(p.N));
@@ -224,13 +226,15 @@ __global__ void __launch_bounds__(kThreads<RAW>)
     }
   }
   __syncwarp();
-  others_started();
-  const int share = NT / split, log_share = 31 - __clz(share);  // of the tile's tokens; powers of two
+  if (SPLIT && !kMeet) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // and so have the others
+  if (warp < kEpilogueWarps && ok) ok = warp_wait(&bar.done, 0, abort);
+  if (kMeet) cluster_sync_all();
+  const int share = (NT + split - 1) / split;  // of the tile's tokens
   if (warp < kEpilogueWarps) {
-    if (ok) ok = warp_wait(&bar.done, 0, abort);
     tc_fence_after();
     if (ok) {  // a lane is a channel, a column a token
       constexpr int C = 16;
+      [[maybe_unused]] int owner = 0, t = 0;
 #pragma unroll 1
       for (int c = 0; c < NT; c += C) {
         float v[C];
@@ -238,12 +242,14 @@ __global__ void __launch_bounds__(kThreads<RAW>)
         tmem_ready(v);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          const int owner = (c + j) >> log_share, t = (c + j) & (share - 1);
-          const uint32_t to = base + S::kParts + ((rank * share + t) * MT + 32 * warp + lane) * 4;
-          if (SPLIT)
+          if constexpr (SPLIT) {
+            const uint32_t to = base + S::kParts + ((rank * share + t) * MT + 32 * warp + lane) * 4;
             st_cluster_f32(mapa_shared(to, owner), v[j]);
-          else
+            if (++t == share) t = 0, ++owner;
+          } else {
+            const uint32_t to = base + S::kParts + ((c + j) * MT + 32 * warp + lane) * 4;
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v[j]) : "memory");
+          }
         }
       }
     }
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(kThreads<RAW>)
   if (SPLIT) cluster_sync_all();
   if (*abort) return;
   // This block's share, four channels a thread.
-  const int first = m0 + rank * share, rows = min(share, p.M - first);
+  const int first = m0 + rank * share, rows = min(min(share, NT - rank * share), p.M - first);
   Out* out = static_cast<Out*>(p.out) + (long long)first * p.N + n0;
   for (int id = threadIdx.x; id < rows * (MT / 4); id += kThreads<RAW>) {
     const int r = id / (MT / 4), c = id % (MT / 4) * 4, n = p.N - n0 - c;
@@ -331,9 +337,15 @@ cudaError_t run(const LinearProblem& p, cudaStream_t stream) {
   // As many blocks per tile as the SMs allow, each with a word of scales, four steps, at the least (64 and 128
   // tokens, 2048 x 1024: 5.8 and 7.7 us; with two steps each 7.1 and 9.5, the parts' sum costs more than it
   // saves; with the whole of K in a block 6.9 and 8.5, and 16.4 and 18.1 us instead of 7.5 and 8.7 for K = 8192).
+  // A cluster's blocks lie within one of the GPU's graphics processing clusters, whose SMs do not divide evenly: no
+  // more than so many clusters run at once, and a tile too many costs the whole time again (50 tiles in threes:
+  // 30 us, in twos 23).
+  static constexpr int kBlocks[] = {8, 6, 4, 3, 2}, kClusters[] = {15, 22, 36, 46, 76};
   const long long tiles = (long long)((p.M + NT - 1) / NT) * ((p.N + MT - 1) / MT);
+  const int words = (scale_blocks(p.K) + kQuad - 1) / kQuad;
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 152 && split * 2 * kQuad <= scale_blocks(p.K)) split *= 2;
+  for (int i = 0; i < 5 && split == 1; ++i)
+    if (tiles <= kClusters[i] && kBlocks[i] <= words) split = kBlocks[i];
   return split > 1 ? launch<NT, RAW, true, Out>(p, split, stream) : launch<NT, RAW, false, Out>(p, 1, stream);
 }
 

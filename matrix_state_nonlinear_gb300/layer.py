@@ -64,11 +64,13 @@ def _dense(like, dtype):
 
 
 def _new_bytes(like, shape):
-    """An e4m3 tensor whose rows start on 16-byte boundaries."""
+    """An e4m3 tensor whose rows start on 16-byte boundaries, those of more than 128 values on 128-byte ones:
+    the product reads 128 bytes of a row at a time, which then lie in one line of the cache."""
     D = shape[-1]
-    if D % 16 == 0:
+    to = 128 if D > 128 else 16
+    if D % to == 0:
         return torch.empty(shape, dtype=FP8, device=like.device)
-    row, strides = (D + 15) // 16 * 16, [1]
+    row, strides = (D + to - 1) // to * to, [1]
     for n in reversed(shape[1:]):
         strides.append(row if len(strides) == 1 else strides[-1] * n)
     return torch.empty_strided(shape, strides[::-1], dtype=FP8, device=like.device)
