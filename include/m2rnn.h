@@ -505,8 +505,8 @@ m2rnn_status m2rnn_add_rmsnorm_backward(const void* h, int stream_f32, const flo
  * m2rnn_linear_fp8: out[m, n] = sum_k x[m, k] w[n, k] of such values, x [M, K] with a scale for each 128
  *   of a row, w [N, K] with one for each 128 x 128 block; out [M, N] bf16 or float32 (out_f32 != 0), dense.
  *   Sums are float32 on the tensor cores.  A NaN of x spoils its row of out, one of w its column; a scale
- *   of w that is NaN spoils the columns of its block.  N rows of out that are multiples of 16 bytes at a
- *   16-byte aligned address are written 16 bytes at a time.
+ *   of w that is NaN spoils the columns of its block.  Fastest with rows of x and w on 128-byte boundaries
+ *   and rows of out that are whole multiples of 32 bytes at a 32-byte aligned address.
  * m2rnn_linear_quantise_fp8: the same with x [M, K] bf16 or float32 (x_f32 != 0), x_row elements from row to
  *   row, as m2rnn_quantise_fp8 makes it 8 bits; up to 16 rows of bf16 within the product's own launch.  The
  *   workspace (16-byte aligned; NULL where its size is 0) is overwritten.

@@ -5,12 +5,14 @@
 // Backward, with g = dout w and dh the gradient that arrives at h from behind:
 //   d = dh + inv g - h inv^3 mean(g h)  (dx and dresidual),  dw = sum over rows of dout h inv
 //
-// Memory-bound.  A block takes one row (one of up to 256 or 512 channels half a warp or a warp of it, blockDim.y
-// rows a block), held in registers, eight channels of a thread to a chunk, so that every input is read once; the norm is taken of h as the stream's type holds it, which is what the next layer and the
-// backward read.  Where everything is 16-byte aligned (VEC) the eight are consecutive, and in 8 bits 16
-// neighbouring threads hold the 128 channels of a scale.  Otherwise they lie a block's threads apart, so that a
-// warp's accesses are still of consecutive values, and the 128 are those of four warps.
-// Measured: 65536 x 2048, bf16: forward 153 us (7.0 TB/s, 1.03 of a copy's rate), backward 174 us with the sums.
+// Memory-bound.  A block takes one row, held in registers, eight channels of a thread to a chunk, so that every
+// input is read once; half a warp or a warp takes a row of few channels, and a block several of those.  The norm
+// is taken of h as the stream's type holds it, which is what the next layer and the backward read.  Where
+// everything is 16-byte aligned (VEC) the eight channels are consecutive, and in 8 bits 16 neighbouring threads hold
+// the 128 channels of a scale.  Otherwise they lie a row's threads apart, so that a warp's accesses are still of
+// consecutive values.
+// Measured: 65536 x 2048, bf16: forward 154 us (7.0 TB/s, 1.03 of a copy's rate), backward 171 us with the sums;
+// 8191 x 4096 in 8 bits on a float32 stream: 56 us (6.6 TB/s); odd rows, 65536 x 1001: 140 and 172 us.
 #include "m2rnn_layer.h"
 #include "ptx_util.cuh"
 
@@ -133,7 +135,8 @@ __device__ __forceinline__ float larger(float a, float b) {
 // Chunk r of a row in 8 bits, VEC: 16 threads to a scale.  v holds h w; the result is v inv.  The largest |v inv| is
 // the largest |v| times inv, rounding being monotonic, and the scale's inverse, a power of two, goes with inv.
 __device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r, int D, uint8_t* q, uint8_t* scales) {
-  float top = larger(larger(larger(v[0].x, v[0].y), larger(v[1].x, v[1].y)), larger(larger(v[2].x, v[2].y), larger(v[3].x, v[3].y)));
+  float top = larger(larger(larger(v[0].x, v[0].y), larger(v[1].x, v[1].y)),
+                     larger(larger(v[2].x, v[2].y), larger(v[3].x, v[3].y)));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(~0u, top, o));
   const uint32_t e = scale_exponent(__float_as_uint(top * inv) & 0x7fffffffu);
@@ -275,7 +278,8 @@ struct RowStream {
   Raw8<T, VEC> hr[R], er[R];
   Raw8<uint16_t, VEC> dr[R];
 
-  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, uint4* smem) : p(p_), own(smem + (MULTI ? threadIdx.y * blockDim.x : 0) + threadIdx.x) {}
+  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, uint4* smem)
+      : p(p_), own(smem + (MULTI ? threadIdx.y * blockDim.x : 0) + threadIdx.x) {}
   __device__ __forceinline__ uint4* slot(int stage, int part, int r) const {
     return own + ((stage * (2 * kParts + 1) + part) * R + r) * (blockDim.x * (MULTI ? blockDim.y : 1));
   }
@@ -488,7 +492,8 @@ cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long lon
   return with_chunks(s.R, [&](auto r) {
     const long long blocks = (p.rows + s.rows - 1) / s.rows;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;  // more than a terabyte
-    add_rmsnorm_kernel<T, FP8, VEC, decltype(r)::value><<<(unsigned)blocks, s.block(), 0, stream>>>(p, out, q, q_row, scales);
+    add_rmsnorm_kernel<T, FP8, VEC, decltype(r)::value>
+        <<<(unsigned)blocks, s.block(), 0, stream>>>(p, out, q, q_row, scales);
     return cudaGetLastError();
   });
 }
@@ -511,7 +516,8 @@ cudaError_t dispatch(const AddNormProblem& p, bool vec, uint16_t* out, uint8_t* 
              : forward<uint16_t, FP8, false>(p, out, q, q_row, scales, stream);
 }
 
-// The backward's spread (several rows a block only with a chunk per thread), and its blocks, which are the rows of its sums: 1024 threads for every SM.
+// The backward's spread (several rows a block only with a chunk per thread), and its blocks, which are the rows of
+// its sums: 1024 threads for every SM.
 Spread backward_spread(int D, bool vec) { return spread_of(D, 1, vec, false); }
 int backward_blocks(long long rows, int D, bool vec) {
   const Spread s = backward_spread(D, vec);
@@ -543,7 +549,8 @@ cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStr
   const cudaError_t err = with_chunks(s.R, [&](auto r) {
     constexpr int R = decltype(r)::value;
     auto go = [&](auto kernel) {
-      const int ring = vec ? s.threads * s.rows * (p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>) : 0;
+      const int each = p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>;
+      const int ring = vec ? s.threads * s.rows * each : 0;
       const int sums = s.rows > 1 ? s.rows * p.D * 4 : 0, bytes = ring > sums ? ring : sums;
       // At every launch: the attribute belongs to the current device.
       const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

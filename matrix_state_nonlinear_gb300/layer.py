@@ -51,8 +51,8 @@ def _byte_rows(t, name, shape, dev):
     if t.numel() == shape[-1]:  # a single row: nothing lies behind it
         row = (shape[-1] + 15) // 16 * 16
     if p % 16 or row % 16:
-        raise ValueError(f"{name}: rows must start on 16-byte boundaries, {row} bytes apart from address {p:#x} they do not "
-                         "(the package's own 8-bit tensors do)")
+        raise ValueError(f"{name}: rows must start on 16-byte boundaries; {row} bytes apart from address {p:#x} they "
+                         "do not (the package's own 8-bit tensors do)")
     return p, row
 
 
@@ -64,16 +64,20 @@ def _dense(like, dtype):
 
 
 def _new_bytes(like, shape):
-    """An e4m3 tensor whose rows start on 16-byte boundaries, those of more than 128 values on 128-byte ones:
-    the product reads 128 bytes of a row at a time, which then lie in one line of the cache."""
+    """An e4m3 tensor whose rows start on 16-byte boundaries, those of more than 128 values on 128-byte ones (the
+    product reads 128 bytes of a row at a time, which then lie in one line of the cache), its address and the
+    bytes from row to row."""
     D = shape[-1]
     to = 128 if D > 128 else 16
-    if D % to == 0:
-        return torch.empty(shape, dtype=FP8, device=like.device)
-    row, strides = (D + to - 1) // to * to, [1]
-    for n in reversed(shape[1:]):
-        strides.append(row if len(strides) == 1 else strides[-1] * n)
-    return torch.empty_strided(shape, strides[::-1], dtype=FP8, device=like.device)
+    row = (D + to - 1) // to * to
+    if D == row:
+        t = torch.empty(shape, dtype=FP8, device=like.device)
+    else:
+        strides = [1]
+        for n in reversed(shape[1:]):
+            strides.append(row if len(strides) == 1 else strides[-1] * n)
+        t = torch.empty_strided(shape, strides[::-1], dtype=FP8, device=like.device)
+    return t, t.data_ptr(), row
 
 
 def _blocks(n):
@@ -81,29 +85,32 @@ def _blocks(n):
 
 
 # ---------------------------------------------------------------- residual RMS norm
+# Tensors that are made here need no check: a token's call is short.
 def _norm_args(x, residual, w, h):
-    """Checks the norm's inputs: (h, sizes, addresses up to eps, address of h)."""
+    """Checks the norm's inputs: (device, h, sizes, arguments up to w, address of h)."""
     dev = _device(x)
     shape = x.shape
     D = shape[-1]
     if residual is None:
-        if x.dtype not in (F32, BF16):
-            raise TypeError(f"x: expected {F32} or {BF16}, got {x.dtype}")
-        sp, row = _rows(x, "x", x.dtype, shape, dev)
-        args, kind, hp = (None, 0, sp, int(x.dtype is F32), row), x.dtype, None
+        kind = x.dtype
+        if kind is not BF16 and kind is not F32:
+            raise TypeError(f"x: expected {F32} or {BF16}, got {kind}")
         if h is not None:
             raise ValueError("h: without a residual it is x")
-        h = x
+        sp, row = _rows(x, "x", kind, shape, dev)
+        args, h, hp = (None, 0, sp, kind is F32, row), x, None
     else:
         kind = residual.dtype
-        if kind not in (F32, BF16):
+        if kind is not BF16 and kind is not F32:
             raise TypeError(f"residual: expected {F32} or {BF16}, got {kind}")
         xp, x_row = _rows(x, "x", BF16, shape, dev)
         sp, row = _rows(residual, "residual", kind, shape, dev)
         if h is None:
             h = _dense(residual, kind)
-        hp = _ptr(h, "h", kind, shape, dev)
-        args = (xp, x_row, sp, int(kind is F32), row)
+            hp = h.data_ptr()
+        else:
+            hp = _ptr(h, "h", kind, shape, dev)
+        args = (xp, x_row, sp, kind is F32, row)
     return dev, h, (x.numel() // D if D else 0, D), (*args, _ptr(w, "w", F32, (D,), dev)), hp
 
 
@@ -116,10 +123,22 @@ def add_rmsnorm(x, residual, w, eps=1e-5, out=None, h=None):
     dev, h, size, args, hp = _norm_args(x, residual, w, h)
     if out is None:
         out = _dense(x, BF16)
-    st = load_library().m2rnn_add_rmsnorm(*args, eps, hp, _ptr(out, "out", BF16, x.shape, dev), *size, _stream(dev))
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", BF16, x.shape, dev)
+    st = load_library().m2rnn_add_rmsnorm(*args, eps, hp, op, *size, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_add_rmsnorm")
     return out, h
+
+
+def _scales(like, shape, scales, dev):
+    """The scales of a tensor of this shape, new ones when they are not given, and their address."""
+    blocks = (*shape[:-1], _blocks(shape[-1]))
+    if scales is None:
+        scales = torch.empty(blocks, dtype=E8M0, device=like.device)
+        return scales, scales.data_ptr()
+    return scales, _ptr(scales, "scales", E8M0, blocks, dev)
 
 
 @_on_stream
@@ -129,12 +148,11 @@ def add_rmsnorm_fp8(x, residual, w, eps=1e-5, out=None, scales=None, h=None):
     dev, h, size, args, hp = _norm_args(x, residual, w, h)
     shape = x.shape
     if out is None:
-        out = _new_bytes(x, shape)
-    blocks = (*shape[:-1], _blocks(shape[-1]))
-    if scales is None:
-        scales = torch.empty(blocks, dtype=E8M0, device=x.device)
-    st = load_library().m2rnn_add_rmsnorm_fp8(*args, eps, hp, *_byte_rows(out, "out", shape, dev),
-                                              _ptr(scales, "scales", E8M0, blocks, dev), *size, _stream(dev))
+        out, op, row = _new_bytes(x, shape)
+    else:
+        op, row = _byte_rows(out, "out", shape, dev)
+    scales, sp = _scales(x, shape, scales, dev)
+    st = load_library().m2rnn_add_rmsnorm_fp8(*args, eps, hp, op, row, sp, *size, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_add_rmsnorm_fp8")
     return out, scales, h
@@ -185,15 +203,13 @@ def quantise_fp8(x, out=None, scales=None):
     dev, shape, f32 = _device(x), x.shape, _source(x, "x")
     D = shape[-1]
     _sizes(D)
-    if out is None:
-        out = _new_bytes(x, shape)
-    blocks = (*shape[:-1], _blocks(D))
-    if scales is None:
-        scales = torch.empty(blocks, dtype=E8M0, device=x.device)
     xp, row = _rows(x, "x", x.dtype, shape, dev)
-    st = load_library().m2rnn_quantise_fp8(xp, int(f32), row, *_byte_rows(out, "out", shape, dev),
-                                           _ptr(scales, "scales", E8M0, blocks, dev), x.numel() // D if D else 0, D,
-                                           _stream(dev))
+    if out is None:
+        out, op, q_row = _new_bytes(x, shape)
+    else:
+        op, q_row = _byte_rows(out, "out", shape, dev)
+    scales, sp = _scales(x, shape, scales, dev)
+    st = load_library().m2rnn_quantise_fp8(xp, f32, row, op, q_row, sp, x.numel() // D if D else 0, D, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_quantise_fp8")
     return out, scales
@@ -206,14 +222,13 @@ def quantise_weight_fp8(w, out=None, scales=None):
     dev, f32 = _device(w), _source(w, "w")
     N, K = shape = w.shape
     _sizes(N, K)
-    if out is None:
-        out = _new_bytes(w, shape)
-    blocks = (_blocks(N), _blocks(K))
-    if scales is None:
-        scales = torch.empty(blocks, dtype=E8M0, device=w.device)
     wp, row = _rows(w, "w", w.dtype, shape, dev)
-    st = load_library().m2rnn_quantise_weight_fp8(wp, int(f32), row, *_byte_rows(out, "out", shape, dev),
-                                                  _ptr(scales, "scales", E8M0, blocks, dev), N, K, _stream(dev))
+    if out is None:
+        out, op, q_row = _new_bytes(w, shape)
+    else:
+        op, q_row = _byte_rows(out, "out", shape, dev)
+    scales, sp = _scales(w, (_blocks(N), K), scales, dev)
+    st = load_library().m2rnn_quantise_weight_fp8(wp, f32, row, op, q_row, sp, N, K, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_quantise_weight_fp8")
     return out, scales
@@ -231,13 +246,15 @@ def linear_fp8(x, x_scales, w, w_scales, out=None, out_dtype=BF16, workspace=Non
     _sizes(N, K)
     wp, w_row = _byte_rows(w, "w", (N, K), dev)
     ws = _ptr(w_scales, "w_scales", E8M0, (_blocks(N), _blocks(K)), dev)
-    to = (*shape[:-1], N)
-    if out is None:
-        out = torch.empty(to, dtype=out_dtype, device=x.device)
-    kind = out.dtype
+    to, kind = (*shape[:-1], N), out_dtype if out is None else out.dtype
     if kind is not BF16 and kind is not F32:
         raise TypeError(f"out: expected {F32} or {BF16}, got {kind}")
-    op, M = _ptr(out, "out", kind, to, dev), x.numel() // K if K else 0
+    if out is None:
+        out = torch.empty(to, dtype=kind, device=x.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", kind, to, dev)
+    M = x.numel() // K if K else 0
     lib = load_library()
     if x_scales is None:
         f32 = _source(x, "x")

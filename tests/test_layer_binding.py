@@ -145,7 +145,7 @@ def test_norm_sizes(lib):
     assert call(4, 16385) == UNSUPPORTED and call(0, 8) == OK
     back = lambda dx, dr, ws, n: lib.m2rnn_add_rmsnorm_backward(A, 0, A, 1e-5, A, None, dx, dr, A, 4, 8, ws, n, None)  # noqa: E731
     need = lib.m2rnn_add_rmsnorm_backward_workspace_bytes(4, 8)
-    assert need >= 4 * 8 * 4 and lib.m2rnn_add_rmsnorm_backward_workspace_bytes(4, 16385) == 0
+    assert need > 0 and lib.m2rnn_add_rmsnorm_backward_workspace_bytes(4, 16385) == 0
     assert back(None, None, A, need) == back(A, None, None, need) == back(A, None, A + 4, need) == back(A, None, A, need - 1) == INVALID
 
 
