@@ -10,9 +10,9 @@
 // the tensor core however few tokens there are) by NT tokens.  Where that gives fewer blocks than SMs, a
 // cluster of up to 8 blocks shares a tile, each with a stretch of K.  Every block then writes each of the
 // others' share of the tokens into that block's shared memory and adds up its own share in the order of K: one
-// barrier of the cluster, nothing read from afar (half a microsecond less).  Up to 16 tokens of bf16 are quantised on the
-// way in, by the warps that later write the results and four more (64 tokens would take 26 us that way, 13
-// with a launch before, 4096 x 8192: every block reads all rows).
+// barrier of the cluster, nothing read from afar (half a microsecond less).  Up to 16 tokens of bf16 are
+// quantised on the way in, by the warps that later write the results and four more (64 tokens would take 26 us
+// that way, 13 with a launch before, 4096 x 8192: every block reads all rows).
 // Measured, 64 x 4096 x 8192: 11.7 us (3.0 TB/s of weights and tokens); 16 x 2048 x 4384: 5.0 us.
 #include "m2rnn_fp8_tc.cuh"
 

@@ -9,8 +9,8 @@
 // in turn; the next tile's products run while the last one's results leave.  Two buffers of 256 columns and
 // the scales would need 536 columns of tensor memory, so the buffers overlap in 32 columns, which are read
 // first: the next tile starts as soon as these are out.
-// Measured, 16384 x 4096 x 8192: 307 us (3.6 PFLOP/s; the tensor cores work in 87 % of the cycles, at the clock that the
-// power allows), 362 us in a long run at the power limit; 8192 x 2048 x 4384: 50 us.
+// Measured, 16384 x 4096 x 8192: 307 us (3.6 PFLOP/s; the tensor cores work in 87 % of the cycles, at the clock
+// that the power allows), 362 us in a long run at the power limit; 8192 x 2048 x 4384: 50 us.
 #include "m2rnn_fp8_tc.cuh"
 
 namespace m2rnn {
