@@ -123,9 +123,10 @@ __device__ __noinline__ double squares64(uint4 u, bool f32) {
   }
   return s;
 }
-// Whether a sum of at most 64 squares lost something to float32's range: above it, or so small that squares
-// below 2^-126 count.
-__device__ __forceinline__ bool out_of_range(float s) { return !(s < INFINITY) || s < 0x1p-100f; }
+// Whether a sum of at most 64 squares is near the ends of float32's range: so large that a thread's sums (fewer than
+// 2^20 of them for the most values that a call takes) could leave it together, or so small that squares below
+// 2^-126 count.
+__device__ __forceinline__ bool out_of_range(float s) { return !(s < 0x1p100f) || s < 0x1p-100f; }
 
 // Sum over the block, for every thread, in a fixed order.  Only one warp adds in 64 bits: an SM adds two
 // doubles a cycle, and 512 threads' shuffles and sums took 11 us of its time.

@@ -371,6 +371,15 @@ def test_clip_over_the_range(kind, scale):
     check_clip(grads, float(np.float32(most)), out, pkg.clip_grad_norm(grads, most, out=out))
 
 
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("scale", [2e18, 1e17])
+def test_clip_sums_that_leave_the_range_together(kind, scale):
+    """Squares whose sums over a part of a thread's values stay below 2^128, those over all of its values not."""
+    grads = tensors([12_000_001], 61, [kind], scale)
+    out = [torch.empty_like(g) for g in grads]
+    check_clip(grads, 1.0, out, pkg.clip_grad_norm(grads, 1.0, out=out))
+
+
 def test_clip_zero_and_not_finite():
     grads = tensors([100, 9], 70, [F32, BF16])
     before = [g.clone() for g in grads]
