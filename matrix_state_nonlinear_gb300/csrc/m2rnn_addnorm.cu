@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
     }
     const float2 sum = row_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
     const float inv = !MULTI || D > 0 ? rsqrtf(sum.x * inv_d + p.eps) : 0.f;
-    const float2 iv = pair(inv), back = pair(-inv * inv * inv * (sum.y * inv_d));
+    // In this order: inv^3 leaves float32 where |h| is above 1e13 or below 1e-13.
+    const float2 iv = pair(inv), back = pair(-(sum.y * inv_d * inv) * inv * inv);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 o[4], w[4];

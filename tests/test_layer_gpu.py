@@ -186,6 +186,36 @@ def test_norm_backward(rows, D, f32, with_dh):
     assert f32 or g["dresidual"] is g["dx"]
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -50, 2.0 ** 50])
+@pytest.mark.parametrize("D,f32", [(384, True), (1001, True), (520, False)])
+def test_norm_backward_over_the_range(scale, D, f32):
+    """Streams whose 1 / sqrt(mean(h^2)) has a cube outside float32; every result is inside."""
+    _, h, w = norm_case(40, D, f32, True, seed=36)
+    h, dout = h.contiguous() * scale, rand((40, D), 37)
+    g = pkg.add_rmsnorm_backward(h, w, dout, None, 0.0)
+    d, dw, size, wsize = ol.rmsnorm_backward(f64(h), f64(w), f64(dout), None, 0.0)
+    within(g["dx"], d, 2.0 ** -8 * np.abs(d) + 2.0 ** -16 * size, "dx")
+    within(g["dresidual"], d, (0 if f32 else 2.0 ** -8) * np.abs(d) + 2.0 ** -16 * size, "dresidual")
+    within(g["dw"], dw, 2.0 ** -15 * wsize, "dw")
+
+
+def test_norm_rows_of_one_infinity():
+    """An infinity leaves the rest of its row zero, in 8 bits but for its block, and other rows as they are."""
+    x, r, w = norm_case(4, 384, True, True)
+    want, _ = pkg.add_rmsnorm(x, r, w)
+    eight, scales, _ = pkg.add_rmsnorm_fp8(x, r, w)
+    r[2, 200] = float("inf")
+    out, _ = pkg.add_rmsnorm(x, r, w)
+    q, s, _ = pkg.add_rmsnorm_fp8(x, r, w)
+    rest = torch.arange(384, device=out.device) != 200
+    assert out[2, 200].isnan() and (out[2][rest] == 0).all()
+    assert s[2].float().isnan().tolist() == [False, True, False] and (q[2].float()[:128] == 0).all()
+    assert (q[2].float()[256:] == 0).all() and q[2].float()[128:256].isnan().all()
+    others = [0, 1, 3]
+    assert torch.equal(out[others], want[others]) and torch.equal(s[others].float(), scales[others].float())
+    assert torch.equal(q[others].float(), eight[others].float())
+
+
 def test_norm_backward_against_differences():
     """The gradients against central differences of the oracle at the same point."""
     rows, D, step = 4, 136, 1e-6
