@@ -312,6 +312,18 @@ def test_linear_of_some_tokens(K, first):
     assert torch.equal(pkg.linear_fp8(x[:-first], sx[:-first], w, sw), want[:-first])
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 264, 1000), (40, 264, 1000), (2100, 2200, 300)])
+@pytest.mark.parametrize("large", ["x", "w"])
+def test_linear_scales_far_apart(M, N, K, large):
+    """Activations and weights near opposite ends of float32, whose products are near one."""
+    up, down = 2.0 ** 112, 2.0 ** -112
+    x, w = rand((M, K), 80, up if large == "x" else down, F32), rand((N, K), 81, down if large == "x" else up, F32)
+    args = (*pkg.quantise_fp8(x), *pkg.quantise_weight_fp8(w))
+    check_linear(pkg.linear_fp8(*args, out_dtype=F32), *args)
+    x = x.to(BF16)
+    assert torch.equal(pkg.linear_fp8(x, None, *args[2:]), pkg.linear_fp8(*pkg.quantise_fp8(x), *args[2:]))
+
+
 def test_linear_nan_stays_in_its_row_and_block():
     M, N, K = 40, 300, 400
     x, sx, w, sw = linear_case(M, N, K, 8)
