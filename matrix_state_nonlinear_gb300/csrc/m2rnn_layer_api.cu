@@ -198,7 +198,8 @@ m2rnn_status m2rnn_clip_grad_norm(const void* const* grads, void* const* out, co
       r[n++] = Range{b, b + bytes, true};
       if (a != b) r[n++] = Range{a, a + bytes, false};
     }
-    std::sort(r.get(), r.get() + n, [](const Range& x, const Range& y) { return x.from < y.from; });
+    const auto before = [](const Range& x, const Range& y) { return x.from < y.from; };
+    if (!std::is_sorted(r.get(), r.get() + n, before)) std::sort(r.get(), r.get() + n, before);
     if (written_overlap(r.get(), n)) return M2RNN_ERR_INVALID_ARG;
   }
   const GradProblem p{grads, out, values, is_f32, count, max_norm, norm, workspace};

@@ -279,15 +279,18 @@ def _gradients(grads, out, max_norm, norm, workspace):
     if not grads:
         raise ValueError("grads: at least one tensor")
     dev = _device(grads[0])
-    for i, t in enumerate(grads):
-        if t.dtype not in _IS_F32:
-            raise TypeError(f"grads[{i}]: expected {F32} or {BF16}, got {t.dtype}")
-        if t.get_device() != dev or not t.is_contiguous():
-            _refuse(t, f"grads[{i}]", t.dtype, t.shape, dev)
+    # A pass over all tensors for each attribute: a fifth less than one loop's statements.
     n = len(grads)
+    kinds = [_IS_F32.get(t.dtype) for t in grads]
+    if None in kinds or {t.get_device() for t in grads} != {dev} or not all([t.is_contiguous() for t in grads]):
+        for i, t in enumerate(grads):
+            if t.dtype not in _IS_F32:
+                raise TypeError(f"grads[{i}]: expected {F32} or {BF16}, got {t.dtype}")
+            if t.get_device() != dev or not t.is_contiguous():
+                _refuse(t, f"grads[{i}]", t.dtype, t.shape, dev)
     ptrs = array("Q", [t.data_ptr() for t in grads])
     sizes = array("q", [t.numel() for t in grads])
-    kinds = array("B", [_IS_F32[t.dtype] for t in grads])
+    kinds = array("B", kinds)
     if out is None:
         to = ptrs
     elif out is _NORM_ONLY:
