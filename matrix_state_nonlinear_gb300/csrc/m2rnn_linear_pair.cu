@@ -22,8 +22,8 @@ constexpr int kStages = 6;
 constexpr int kOperand = kRows * kBlockK, kStage = 2 * kOperand;
 constexpr int kScaleStages = 3, kScaleWord = 512 + 1024, kScaleStage = 4 * kScaleWord;  // 128 tokens, 256 channels
 constexpr int kScales = kStages * kStage;
-constexpr int kTurn = kScales + kScaleStages * kScaleStage;  // 32 tokens by 32 channels for each epilogue warp
-constexpr int kTurnRow = 32 * 2 + 4, kTurnBytes = 32 * kTurnRow;  // of two bytes; 4: rows in different banks
+constexpr int kTurn = kScales + kScaleStages * kScaleStage;  // 32 tokens by 32 channels of two bytes for each epilogue warp
+constexpr int kTurnBytes = 32 * (32 * 2 + 4);
 constexpr int kSmemBytes = kTurn + 4 * kTurnBytes + 1024;    // 1024: to align the first stage
 constexpr int kEpilogueWarps = 4, kWarpLoad = 4, kWarpMma = 5, kWarpScale = 6, kThreads = 224;
 constexpr int kTmemCols = 512, kColSecond = 224, kColScale = 480;  // scales: two sets of 4 + 8 columns
@@ -66,8 +66,10 @@ __device__ __forceinline__ int2 tile_at_index(int t, int token_tiles, int channe
   return make_int2(first + in % wide, in / wide);
 }
 
+// One block to an SM, said to the compiler: left alone it keeps to 128 registers and spills (8192 x 4096 x 8192: 181
+// us instead of 172).
 template <typename Out>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                        LinearProblem p, int token_tiles, int channel_tiles, bool vec) {
   extern __shared__ unsigned char raw[];
@@ -248,35 +250,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           }
         }
         if (!vec) {
-          // Rows that do not start on whole sectors: turned in shared memory, so that a warp writes neighbouring channels
-          // of one token (of 32-bit results half of them at a time).
-          constexpr int W = 64 / sizeof(Out);
+          // Rows that do not start on whole sectors: turned in shared memory, so that a warp writes neighbouring
+          // channels of one token (of 32-bit results 16 tokens after the other 16, for want of room).
+          constexpr int kTokens = 64 / sizeof(Out), kRow = 32 * sizeof(Out) + 4;  // 4: rows in different banks
+          static_assert(kTokens * kRow <= kTurnBytes, "room");
           const uint32_t turn = base + kTurn + warp * kTurnBytes;
-          const long long m_first = m - lane;
 #pragma unroll
-          for (int half = 0; half < 32 / W; ++half) {
+          for (int part = 0; part < 32 / kTokens; ++part) {
             __syncwarp();
+            if (lane / kTokens == part)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              uint32_t u;
-              if constexpr (sizeof(Out) == 4)
-                u = __float_as_uint(v[half * W + k]);
-              else
-                u = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(turn + lane * kTurnRow + 4 * k), "r"(u) : "memory");
-            }
-            __syncwarp();
-            const int k = lane % W, n = n0 + half * W + k;
-            Out* to = static_cast<Out*>(p.out) + m_first * p.N + n;
-#pragma unroll 4
-            for (int t = lane / W; t < 32; t += 32 / W) {
-              uint32_t u;
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"((turn + t * kTurnRow + k * (int)sizeof(Out)) & ~3u));
-              if (m_first + t < p.M && n < p.N) {
+              for (int k = 0; k < 8 * (int)sizeof(Out); ++k) {
+                uint32_t u;
                 if constexpr (sizeof(Out) == 4)
-                  to[(long long)t * p.N] = __uint_as_float(u);
+                  u = __float_as_uint(v[k]);
                 else
-                  to[(long long)t * p.N] = (uint16_t)(k & 1 ? u >> 16 : u);
+                  u = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(turn + lane % kTokens * kRow + 4 * k), "r"(u) : "memory");
+              }
+            __syncwarp();
+            const long long first = m - lane + part * kTokens;
+            const int live = n0 + lane < p.N ? (int)max(0LL, min((long long)kTokens, p.M - first)) : 0;
+            Out* to = static_cast<Out*>(p.out) + first * p.N + n0 + lane;
+#pragma unroll 8
+            for (int t = 0; t < kTokens; ++t, to += p.N) {
+              uint32_t u;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"((turn + t * kRow + lane * (int)sizeof(Out)) & ~3u));
+              if (t < live) {
+                if constexpr (sizeof(Out) == 4)
+                  *to = __uint_as_float(u);
+                else
+                  *to = (uint16_t)(lane & 1 ? u >> 16 : u);
               }
             }
           }
