@@ -7,9 +7,9 @@
 //
 // Memory-bound.  A block takes one row, held in registers, eight channels of a thread to a chunk, so that every
 // input is read once; half a warp or a warp takes a row of few channels, and a block several of those.  The norm
-// is taken of h as the stream's type holds it, which is what the next layer and the backward read.  Where
-// everything is 16-byte aligned (VEC) the eight channels are consecutive, and in 8 bits 16 neighbouring threads hold
-// the 128 channels of a scale.  Otherwise they lie a row's threads apart, so that a warp's accesses are still of
+// is taken of h as the stream's type holds it, which is what the next layer and the backward read.  Chunks are
+// eight consecutive channels where memory allows 16-byte accesses (and in 8 bits 16 neighbouring threads hold the
+// 128 channels of a scale); otherwise they lie a row's threads apart, so that a warp's accesses are still of
 // consecutive values.
 // Measured: 65536 x 2048, bf16: forward 154 us (7.0 TB/s, 1.03 of a copy's rate), backward 171 us with the sums;
 // 8191 x 4096 in 8 bits on a float32 stream: 56 us (6.6 TB/s); odd rows, 65536 x 1001: 140 and 172 us.
@@ -19,38 +19,83 @@
 namespace m2rnn {
 namespace {
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-// Chunk r of a thread's channels of a row of D, as loaded, so that a load can be started ahead of its use.
+// How a row lies in memory.  kVec: every row of every tensor starts on 16 bytes.  kShift: rows of dense tensors, or
+// as good as, with a number of channels that is no multiple of 8, so that row m starts m D mod 8 = s values behind a
+// 16-byte boundary, in all tensors alike: a chunk is 16-byte aligned and its first channel is s below a multiple of
+// 8, the first and last chunk of a row hold neighbours' values, which read as zero (65536 x 1001: 140 us value by
+// value).  kAny: anything else, value by value.
+enum Access { kAny, kVec, kShift };
+// The places in a row that hold its channels, counted from its first chunk on: none where there is no row.
+// `last`: memory may end behind them.
+struct Span {
+  int lo, hi;
+  bool last;
+};
+__device__ __forceinline__ int shift_of(long long row, int D) { return (int)(row * D & 7); }
+
+// Chunk r of a thread's channels of a row, as loaded, so that a load can be started ahead of its use.
 // Channels that are not there are zero and are not stored.
-template <typename T, bool VEC>
+template <typename T, int A>
 struct Raw8 {
   uint4 u[sizeof(T) / 2];
-  // Without VEC: channel i of the chunk.
+  // kAny: channel i of the chunk.
   static __device__ __forceinline__ int channel(int r, int i) { return (8 * r + i) * blockDim.x + threadIdx.x; }
   static __device__ __forceinline__ int first(int r) { return 8 * (threadIdx.x + r * blockDim.x); }
-  __device__ __forceinline__ void load(const T* row, int r, int D) {
-    if constexpr (VEC) {
+  __device__ __forceinline__ void load(const T* row, int r, const Span& d) {
+    if constexpr (A == kAny) {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = channel(r, i) < d.hi ? bits_at(row, channel(r, i)) : 0u;
+      put(v);
+    } else if (A == kVec || first(r) + 8 <= d.hi || !d.last) {
 #pragma unroll
       for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-        u[i] = first(r) < D ? reinterpret_cast<const uint4*>(row + first(r))[i] : make_uint4(0, 0, 0, 0);
+        u[i] = first(r) < d.hi ? reinterpret_cast<const uint4*>(row + first(r))[i] : make_uint4(0, 0, 0, 0);
+      mask(r, d);
     } else {
       uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = channel(r, i);
-        if constexpr (sizeof(T) == 4)
-          v[i] = c < D ? __float_as_uint(row[c]) : 0u;
-        else
-          v[i] = c < D ? row[c] : 0u;
-      }
-      if constexpr (sizeof(T) == 4) {
-        u[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        u[sizeof(T) / 2 - 1] = make_uint4(v[4], v[5], v[6], v[7]);
-      } else {
-        u[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-      }
+      for (int i = 0; i < 8; ++i) v[i] = first(r) + i < d.hi ? bits_at(row, first(r) + i) : 0u;
+      put(v);
+      mask(r, d);
     }
+  }
+  // kShift: neighbours' values become zero.
+  __device__ __forceinline__ void mask(int r, const Span& d) {
+    if (A != kShift || (first(r) >= d.lo && first(r) + 8 <= d.hi)) return;
+    uint32_t v[8];
+    take(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (first(r) + i < d.lo || first(r) + i >= d.hi) v[i] = 0;
+    put(v);
+  }
+  static __device__ __forceinline__ uint32_t bits_at(const T* row, int c) {
+    if constexpr (sizeof(T) == 4)
+      return __float_as_uint(row[c]);
+    else
+      return row[c];
+  }
+  __device__ __forceinline__ void put(const uint32_t (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+      u[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      u[sizeof(T) / 2 - 1] = make_uint4(v[4], v[5], v[6], v[7]);
+    } else {
+      u[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+  }
+  __device__ __forceinline__ void take(uint32_t (&v)[8]) const {
+    const uint4 a = u[0], b = u[sizeof(T) / 2 - 1];
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = sizeof(T) == 4 ? w[i] : w[i / 2] >> (16 * (i & 1)) & 0xffffu;
   }
   __device__ __forceinline__ void get(float2 (&f)[4]) const {
     if constexpr (sizeof(T) == 4) {
@@ -75,26 +120,57 @@ struct Raw8 {
                         pack_bf16x2(f[3].x, f[3].y));
     }
   }
-  __device__ __forceinline__ void store(T* row, int r, int D) const {
-    if constexpr (VEC) {
-      if (first(r) < D)
+  __device__ __forceinline__ void store(T* row, int r, const Span& d) const {
+    if (A == kVec ? first(r) < d.hi : A == kShift && first(r) >= d.lo && first(r) + 8 <= d.hi) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + first(r))[i] = u[i];
-    } else {
-      const uint4 a = u[0], b = u[sizeof(T) / 2 - 1];
-      const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(row + first(r))[i] = u[i];
+    } else if (A != kVec && (A == kAny || first(r) < d.hi)) {
+      uint32_t v[8];
+      take(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = channel(r, i);
-        if constexpr (sizeof(T) == 4) {
-          if (c < D) row[c] = __uint_as_float(v[i]);
-        } else {
-          if (c < D) row[c] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
-        }
+        const int c = A == kAny ? channel(r, i) : first(r) + i;
+        if (c < d.lo || c >= d.hi) continue;
+        if constexpr (sizeof(T) == 4)
+          row[c] = __uint_as_float(v[i]);
+        else
+          row[c] = (uint16_t)v[i];
       }
     }
   }
 };
+// The weights of chunk r.  kShift: of two chunks of w, moved by the row's shift.
+template <int A>
+__device__ __forceinline__ void load_weight(const float* w, int r, const Span& d, int D, float2 (&f)[4]) {
+  if constexpr (A != kShift) {
+    Raw8<float, A> u;
+    u.load(w, r, Span{0, D, false});
+    u.get(f);
+  } else {
+    float v[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = Raw8<float, A>::first(r) + 8 * h - 8;
+      if (c >= 0 && c + 8 <= D) {
+        const float4 a = reinterpret_cast<const float4*>(w + c)[0], b = reinterpret_cast<const float4*>(w + c)[1];
+        v[8 * h] = a.x, v[8 * h + 1] = a.y, v[8 * h + 2] = a.z, v[8 * h + 3] = a.w;
+        v[8 * h + 4] = b.x, v[8 * h + 5] = b.y, v[8 * h + 6] = b.z, v[8 * h + 7] = b.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] = c + i >= 0 && c + i < D ? w[c + i] : 0.f;
+      }
+    }
+    // v[8 - lo] to the front, by powers of two.
+    const int k = 8 - d.lo;
+#pragma unroll
+    for (int b = 8; b > 0; b /= 2)
+      if (k & b)
+#pragma unroll
+        for (int i = 0; i < 7 + b && i + b < 16; ++i) v[i] = v[i + b];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+  }
+}
 
 __device__ __forceinline__ float across(float x, int lanes) { return x + __shfl_xor_sync(~0u, x, lanes); }
 __device__ __forceinline__ float2 across(float2 x, int lanes) {
@@ -132,7 +208,7 @@ __device__ __forceinline__ float larger(float a, float b) {
   return r;
 }
 
-// Chunk r of a row in 8 bits, VEC: 16 threads to a scale.  v holds h w; the result is v inv.  The largest |v inv| is
+// Chunk r of a row in 8 bits, kVec: 16 threads to a scale.  v holds h w; the result is v inv.  The largest |v inv| is
 // the largest |v| times inv, rounding being monotonic, and the scale's inverse, a power of two, goes with inv.
 __device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r, int D, uint8_t* q, uint8_t* scales) {
   float top = larger(larger(larger(v[0].x, v[0].y), larger(v[1].x, v[1].y)),
@@ -155,7 +231,7 @@ __device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r
 // |values| as bits, which order them and put NaN above all.
 __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// A row in 8 bits without VEC: a row has one warp, and the 128 channels of a scale are four values of each lane,
+// A row in 8 bits, kAny: a row has one warp, and the 128 channels of a scale are four values of each lane,
 // or a multiple of 128 threads, and they are one value of each thread of four warps.
 template <int R>
 __device__ __forceinline__ void store_fp8_any(const float2 (&v)[R][4], int D, uint8_t* q, uint8_t* scales) {
@@ -189,23 +265,24 @@ __device__ __forceinline__ void store_fp8_any(const float2 (&v)[R][4], int D, ui
   }
 }
 
-// Two blocks of 512 threads to an SM where a thread has one chunk (or two, VEC): left alone, the compiler takes
+// Two blocks of 512 threads to an SM where a thread has one chunk (or two, not kAny): left alone, the compiler takes
 // 128 registers for a chunk of eight separate channels.
-template <typename T, bool FP8, bool VEC, int R>
-__global__ void __launch_bounds__(512, R == 1 || (VEC && R == 2) ? 2 : 1)
+template <typename T, bool FP8, int A, int R>
+__global__ void __launch_bounds__(512, R == 1 || (A != kAny && R == 2) ? 2 : 1)
     add_rmsnorm_kernel(AddNormProblem p, uint16_t* __restrict__ out, uint8_t* __restrict__ q, long long q_row,
                        uint8_t* __restrict__ scales) {
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-  const int D = row < p.rows ? p.D : 0;  // behind the last row there are no channels
-  const T* stream = static_cast<const T*>(p.stream) + row * p.stream_row;
-  const uint16_t* x = p.x ? p.x + row * p.x_row : nullptr;
+  const int lo = A == kShift ? shift_of(row, p.D) : 0;
+  const Span d{lo, row < p.rows ? lo + p.D : 0, row + 1 >= p.rows};  // behind the last row there are no channels
+  const T* stream = static_cast<const T*>(p.stream) + row * p.stream_row - lo;
+  const uint16_t* x = p.x ? p.x + row * p.x_row - lo : nullptr;
   float2 h[R][4], s = pair(0.f);
-  Raw8<T, VEC> a[R];
-  Raw8<uint16_t, VEC> b[R];
+  Raw8<T, A> a[R];
+  Raw8<uint16_t, A> b[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    a[r].load(stream, r, D);
-    if (x) b[r].load(x, r, D);
+    a[r].load(stream, r, d);
+    if (x) b[r].load(x, r, d);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -218,31 +295,29 @@ __global__ void __launch_bounds__(512, R == 1 || (VEC && R == 2) ? 2 : 1)
       a[r].set(h[r]);
       if (sizeof(T) == 2) a[r].get(h[r]);
     }
-    if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D, r, D);
+    if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D - lo, r, d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma2(h[r][i], h[r][i], s);
   }
   const float inv = rsqrtf(row_sum(s.x + s.y, 0) * (1.f / (float)p.D) + p.eps);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    Raw8<float, VEC> u;
     float2 w[4];
-    u.load(p.w, r, p.D);
-    u.get(w);
+    load_weight<A>(p.w, r, d, p.D, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[r][i] = mul2(h[r][i], w[i]);
-    if constexpr (!FP8 || !VEC)
+    if constexpr (!FP8 || A == kAny)
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[r][i] = mul2(h[r][i], pair(inv));
-    if constexpr (FP8 && VEC) {
-      store_fp8(h[r], inv, r, D, q + row * q_row, scales + row * scale_blocks(p.D));
+    if constexpr (FP8 && A == kVec) {
+      store_fp8(h[r], inv, r, d.hi, q + row * q_row, scales + row * scale_blocks(p.D));
     } else if constexpr (!FP8) {
-      Raw8<uint16_t, VEC> o;
+      Raw8<uint16_t, A> o;
       o.set(h[r]);
-      o.store(out + row * p.D, r, D);
+      o.store(out + row * p.D - lo, r, d);
     }
   }
-  if constexpr (FP8 && !VEC) store_fp8_any<R>(h, D, q + row * q_row, scales + row * scale_blocks(p.D));
+  if constexpr (FP8 && A == kAny) store_fp8_any<R>(h, d.hi, q + row * q_row, scales + row * scale_blocks(p.D));
 }
 
 // 16 bytes to shared memory without passing through registers, by way of L1 (SECTORS: where a thread's next
@@ -254,6 +329,13 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
   else
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <bool SECTORS>
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {  // and zeros behind them
+  if constexpr (SECTORS)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -269,61 +351,74 @@ template <typename T, int R>
 constexpr int kAhead = R * sizeof(T) <= 4 && sizeof(T) == 2 ? 4 : R * sizeof(T) <= 8 ? 2 : 1;
 template <typename T, int R>
 constexpr int kRingPerThread = kAhead<T, R> * (2 * (int)sizeof(T) / 2 + 1) * R * 16;  // bytes
-template <typename T, bool VEC, int R, bool MULTI>
+template <typename T, int A, int R, bool MULTI>
 struct RowStream {
   static constexpr int kRows = kAhead<T, R>, kParts = sizeof(T) / 2;  // 16-byte pieces of 8 values
   const AddNormBackwardProblem& p;
   uint4* own;  // [kRows][kParts + 1 + kParts][R][threads of the block]
+  const int lo;  // a thread's rows all have the same shift
   int at = 0, to = 0;
-  Raw8<T, VEC> hr[R], er[R];
-  Raw8<uint16_t, VEC> dr[R];
+  Raw8<T, A> hr[R], er[R];
+  Raw8<uint16_t, A> dr[R];
 
-  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, uint4* smem)
-      : p(p_), own(smem + (MULTI ? threadIdx.y * blockDim.x : 0) + threadIdx.x) {}
+  __device__ __forceinline__ RowStream(const AddNormBackwardProblem& p_, int lo_, uint4* smem)
+      : p(p_), own(smem + (MULTI ? threadIdx.y * blockDim.x : 0) + threadIdx.x), lo(lo_) {}
+  __device__ __forceinline__ Span span(long long row) const {
+    return Span{lo, row < p.rows ? lo + p.D : 0, row + 1 >= p.rows};
+  }
   __device__ __forceinline__ uint4* slot(int stage, int part, int r) const {
     return own + ((stage * (2 * kParts + 1) + part) * R + r) * (blockDim.x * (MULTI ? blockDim.y : 1));
   }
   __device__ __forceinline__ void start(long long row) {
     if (row < p.rows) {
-      const T *h = static_cast<const T*>(p.h) + row * p.D, *e = static_cast<const T*>(p.dh) + row * p.D;
-      const uint16_t* d = p.dout + row * p.D;
+      const Span s = span(row);
+      const T *h = static_cast<const T*>(p.h) + row * p.D - lo, *e = static_cast<const T*>(p.dh) + row * p.D - lo;
+      const uint16_t* d = p.dout + row * p.D - lo;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if constexpr (VEC) {
-          const int c = Raw8<T, VEC>::first(r);
-          if (c < p.D) {
+        if constexpr (A != kAny) {
+          const int c = Raw8<T, A>::first(r);
+          // Part k of `parts` of eight values: of the last row only what is there.
+          auto copy = [&](auto sectors, int part, const void* from, int k, int parts) {
+            const uint32_t at = smem_u32(slot(to, part, r));
+            const uint4* v = static_cast<const uint4*>(from) + k;
+            const int each = 8 / parts;
+            if (A == kShift && s.last)
+              copy16<decltype(sectors)::value>(at, v, max(0, min(each, s.hi - c - k * each)) * (16 / each));
+            else
+              copy16<decltype(sectors)::value>(at, v);
+          };
+          if (c < s.hi) {
 #pragma unroll
-            for (int k = 0; k < kParts; ++k)
-              copy16<kParts == 2>(smem_u32(slot(to, k, r)), reinterpret_cast<const uint4*>(h + c) + k);
-            copy16<false>(smem_u32(slot(to, kParts, r)), d + c);
+            for (int k = 0; k < kParts; ++k) copy(Int<kParts == 2>{}, k, h + c, k, kParts);
+            copy(Int<false>{}, kParts, d + c, 0, 1);
             if (p.dh)
 #pragma unroll
-              for (int k = 0; k < kParts; ++k)
-                copy16<kParts == 2>(smem_u32(slot(to, kParts + 1 + k, r)), reinterpret_cast<const uint4*>(e + c) + k);
+              for (int k = 0; k < kParts; ++k) copy(Int<kParts == 2>{}, kParts + 1 + k, e + c, k, kParts);
           }
         } else {
-          hr[r].load(h, r, p.D);
-          dr[r].load(d, r, p.D);
-          if (p.dh) er[r].load(e, r, p.D);
+          hr[r].load(h, r, s);
+          dr[r].load(d, r, s);
+          if (p.dh) er[r].load(e, r, s);
         }
       }
     }
-    if constexpr (VEC) {
+    if constexpr (A != kAny) {
       copies_commit();
       to = to + 1 == kRows ? 0 : to + 1;
     }
   }
   __device__ __forceinline__ void begin(long long row, long long step) {
 #pragma unroll
-    for (int i = 0; i < (VEC ? kRows - 1 : kParts / kParts); ++i) start(row + i * step);
+    for (int i = 0; i < (A != kAny ? kRows - 1 : kParts / kParts); ++i) start(row + i * step);
   }
   // dh of the row at hand is taken before the sums where there is room to hold it across them (65536 x 2048
   // float32: 317 us, 364 where it is taken after them; 4000 x 16384 bf16: 215 and 124).
-  static constexpr bool kEarly = VEC && R <= 2;
-  // h, dout and, if early, dh of `row`, zeros behind the last of its D channels; a later row starts.
-  __device__ __forceinline__ void next(long long row, int D, long long step, float2 (&h)[R][4], float2 (&d)[R][4],
-                                       float2 (&e)[R][4]) {
-    if constexpr (VEC) {
+  static constexpr bool kEarly = A != kAny && R <= 2;
+  // h, dout and, if early, dh of `row`, zeros where its span has no channels; a later row starts.
+  __device__ __forceinline__ void next(long long row, const Span& s, long long step, float2 (&h)[R][4],
+                                       float2 (&d)[R][4], float2 (&e)[R][4]) {
+    if constexpr (A != kAny) {
       start(row + (kRows - 1) * step);
       copies_wait<kRows - 1>();
     }
@@ -331,14 +426,15 @@ struct RowStream {
     for (int r = 0; r < R; ++r) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[r][i] = d[r][i] = e[r][i] = pair(0.f);
-      if (VEC ? Raw8<T, VEC>::first(r) < D : D > 0) {
-        if constexpr (VEC) {
+      if (A != kAny ? Raw8<T, A>::first(r) < s.hi : s.hi > 0) {
+        if constexpr (A != kAny) {
 #pragma unroll
           for (int k = 0; k < kParts; ++k) hr[r].u[k] = *slot(at, k, r);
           dr[r].u[0] = *slot(at, kParts, r);
           if (kEarly && p.dh)
 #pragma unroll
             for (int k = 0; k < kParts; ++k) er[r].u[k] = *slot(at, kParts + 1 + k, r);
+          hr[r].mask(r, s), dr[r].mask(r, s);  // of dh, neighbours' values change nothing
         }
         hr[r].get(h[r]);
         dr[r].get(d[r]);
@@ -347,15 +443,15 @@ struct RowStream {
     }
   }
   // dh of chunk r, where it is late.
-  __device__ __forceinline__ void late(int r, int D, float2 (&e)[4]) {
-    if (kEarly || !p.dh || (VEC ? Raw8<T, VEC>::first(r) >= D : D == 0)) return;
-    if constexpr (VEC)
+  __device__ __forceinline__ void late(int r, const Span& s, float2 (&e)[4]) {
+    if (kEarly || !p.dh || (A != kAny ? Raw8<T, A>::first(r) >= s.hi : s.hi == 0)) return;
+    if constexpr (A != kAny)
 #pragma unroll
       for (int k = 0; k < kParts; ++k) er[r].u[k] = *slot(at, kParts + 1 + k, r);
     er[r].get(e);
   }
   __device__ __forceinline__ void done(long long row, long long step) {
-    if constexpr (VEC)
+    if constexpr (A != kAny)
       at = at + 1 == kRows ? 0 : at + 1;
     else
       start(row + step);
@@ -364,36 +460,34 @@ struct RowStream {
 
 // Block b takes rows b, + blocks, ... (MULTI: blockDim.y of them at once); its channels' part of dw adds up in
 // registers and goes to row b of `part`.
-template <typename T, bool VEC, int R, bool MULTI>
+template <typename T, int A, int R, bool MULTI>
 __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
     add_rmsnorm_backward_kernel(AddNormBackwardProblem p, float* __restrict__ part) {
   extern __shared__ uint4 ring[];
   const float inv_d = 1.f / (float)p.D;
   constexpr bool kKeep = R <= 2;  // the weight stays in registers where there is room for it
   float2 dw[R][4], kept[kKeep ? R : 1][4];
-  auto weight = [&](int r, float2(&w)[4]) {
-    Raw8<float, VEC> u;
-    u.load(p.w, r, p.D);
-    u.get(w);
-  };
+  const int at_once = MULTI ? blockDim.y : 1;
+  const long long step = (long long)gridDim.x * at_once;
+  long long row = (long long)blockIdx.x * at_once + (MULTI ? threadIdx.y : 0);
+  // The shift of all of a thread's rows: more than one only where the grid is a multiple of 8.
+  const int lo = A == kShift ? shift_of(row, p.D) : 0;
+  auto weight = [&](int r, float2(&w)[4]) { load_weight<A>(p.w, r, Span{lo, lo + p.D, false}, p.D, w); };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if constexpr (kKeep) weight(r, kept[r]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[r][i] = pair(0.f);
   }
-  RowStream<T, VEC, R, MULTI> rows(p, ring);
-  const int at_once = MULTI ? blockDim.y : 1;
-  const long long step = (long long)gridDim.x * at_once;
-  long long row = (long long)blockIdx.x * at_once + (MULTI ? threadIdx.y : 0);
+  RowStream<T, A, R, MULTI> rows(p, lo, ring);
   rows.begin(row, step);
   int turn = 0;
   // All threads of a block go round equally often; behind the last row there are no channels.
   for (long long first = (long long)blockIdx.x * at_once; first < p.rows; first += step, row += step, turn ^= 1) {
-    const int D = !MULTI || row < p.rows ? p.D : 0;
+    const Span span = rows.span(row);
     float2 h[R][4], d[R][4], s1 = pair(0.f), s2 = pair(0.f);
     float2 e[R][4];
-    rows.next(row, D, step, h, d, e);
+    rows.next(row, span, step, h, d, e);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 w[4];
@@ -405,13 +499,13 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
       }
     }
     const float2 sum = row_sum(make_float2(s1.x + s1.y, s2.x + s2.y), turn);
-    const float inv = !MULTI || D > 0 ? rsqrtf(sum.x * inv_d + p.eps) : 0.f;
+    const float inv = !MULTI || span.hi > 0 ? rsqrtf(sum.x * inv_d + p.eps) : 0.f;
     // In this order: inv^3 leaves float32 where |h| is above 1e13 or below 1e-13.
     const float2 iv = pair(inv), back = pair(-(sum.y * inv_d * inv) * inv * inv);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float2 o[4], w[4];
-      rows.late(r, D, e[r]);
+      rows.late(r, span, e[r]);
       if constexpr (!kKeep) weight(r, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -419,14 +513,14 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
         o[i] = add2(fma2(h[r][i], back, mul2(mul2(d[r][i], kKeep ? kept[kKeep ? r : 0][i] : w[i]), iv)), e[r][i]);
       }
       if (p.dx) {
-        Raw8<uint16_t, VEC> u;
+        Raw8<uint16_t, A> u;
         u.set(o);
-        u.store(p.dx + row * p.D, r, D);
+        u.store(p.dx + row * p.D - lo, r, span);
       }
       if (p.dresidual) {
-        Raw8<T, VEC> u;
+        Raw8<T, A> u;
         u.set(o);
-        u.store(static_cast<T*>(p.dresidual) + row * p.D, r, D);
+        u.store(static_cast<T*>(p.dresidual) + row * p.D - lo, r, span);
       }
     }
     rows.done(row, step);
@@ -439,9 +533,18 @@ __global__ void __launch_bounds__(512, R == 1 ? 2 : 1)
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    Raw8<float, VEC> u;
-    u.set(dw[r]);
-    u.store(to, r, p.D);
+    if constexpr (A == kShift) {
+      const float* value = &dw[r][0].x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = Raw8<float, A>::first(r) + i - lo;
+        if (c >= 0 && c < p.D) to[c] = value[i];
+      }
+    } else {
+      Raw8<float, A> u;
+      u.set(dw[r]);
+      u.store(to, r, Span{0, p.D, false});
+    }
   }
   if (MULTI) {
     __syncthreads();
@@ -458,70 +561,70 @@ struct Spread {
   int R, threads, rows;
   dim3 block() const { return dim3(threads, rows); }
 };
-// Threads of a row for R chunks each: half a warp, whole warps, or (8 bits, not VEC) a warp or four at a time.
-int threads_for(int D, int R, bool vec, bool fp8) {
-  const int n = ((D + 7) / 8 + R - 1) / R;
-  if (vec && n <= 16) return 16;
-  const int whole = !vec && fp8 && n > 32 ? 128 : 32;
+// Threads of a row for R chunks each: half a warp, whole warps, or (8 bits, kAny) a warp or four at a time.
+int threads_for(int D, int R, Access a, bool fp8) {
+  const int n = ((D + (a == kShift ? 7 : 0) + 7) / 8 + R - 1) / R;
+  if (a != kAny && n <= 16) return 16;
+  const int whole = a == kAny && fp8 && n > 32 ? 128 : 32;
   return (n + whole - 1) / whole * whole;
 }
 // With `least` chunks a thread, or more where a row would have more than 512 threads.
-Spread spread_of(int D, int least, bool vec, bool fp8) {
+Spread spread_of(int D, int least, Access a, bool fp8) {
   int R = least;
-  while (threads_for(D, R, vec, fp8) > 512) R *= 2;
-  const int threads = threads_for(D, R, vec, fp8);
+  while (threads_for(D, R, a, fp8) > 512) R *= 2;
+  const int threads = threads_for(D, R, a, fp8);
   return Spread{R, threads, threads <= 32 ? 256 / threads : 1};
 }
 
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
 template <typename F>
 cudaError_t with_chunks(int R, F f) {
   return R == 1 ? f(Int<1>{}) : R == 2 ? f(Int<2>{}) : f(Int<4>{});
 }
 
-template <typename T, bool FP8, bool VEC>
+template <typename T, bool FP8, Access A>
 cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
                     cudaStream_t stream) {
   // Few rows are spread as wide as they go; of many, a thread takes two chunks (65536 x 2048: 153 us; one chunk
   // 169, four 158; 8191 x 4096 in 8 bits: 58, 65, 64).
   const bool many = p.rows >= 152 * 16;
-  Spread s = spread_of(p.D, !many ? 1 : VEC ? 2 : 1, VEC, FP8);
+  Spread s = spread_of(p.D, many && A != kAny ? 2 : 1, A, FP8);
   if (!many) s.rows = s.threads < 32 ? 2 : 1;
   return with_chunks(s.R, [&](auto r) {
     const long long blocks = (p.rows + s.rows - 1) / s.rows;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;  // more than a terabyte
-    add_rmsnorm_kernel<T, FP8, VEC, decltype(r)::value>
+    add_rmsnorm_kernel<T, FP8, A, decltype(r)::value>
         <<<(unsigned)blocks, s.block(), 0, stream>>>(p, out, q, q_row, scales);
     return cudaGetLastError();
   });
 }
 
-bool rows_of_8(const void* p, long long row, size_t size) { return aligned_to(p, 16) && row * size % 16 == 0; }
+// Whether rows of D values can be read as kShift: a chunk may reach up to 7 values into the next row.
+bool shift_ok(int D) { return D >= 8 && D + 7 <= kNormMaxRow; }
 
-bool vec_ok(const AddNormProblem& p) {
+// `rest`: whether what is particular to the call starts on 16 bytes.
+Access access_of(const AddNormProblem& p, bool rest) {
   const size_t size = p.stream_f32 ? 4 : 2;
-  return p.D % 8 == 0 && aligned_to(p.w, 16) && rows_of_8(p.stream, p.stream_row, size) &&
-         (!p.x || rows_of_8(p.x, p.x_row, 2)) && aligned_to(p.h, 16);
+  if (!rest || !aligned_to(p.w, 16) || !aligned_to(p.h, 16) || !aligned_to(p.stream, 16) || !aligned_to(p.x, 16))
+    return kAny;
+  if (p.D % 8 == 0) return p.stream_row * size % 16 == 0 && (!p.x || p.x_row % 8 == 0) ? kVec : kAny;
+  auto alike = [&](long long row) { return row >= p.D && (row - p.D) % 8 == 0; };
+  return shift_ok(p.D) && alike(p.stream_row) && (!p.x || alike(p.x_row)) ? kShift : kAny;
 }
 
-template <bool FP8>
-cudaError_t dispatch(const AddNormProblem& p, bool vec, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
+template <typename T, bool FP8>
+cudaError_t dispatch(const AddNormProblem& p, Access a, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
                      cudaStream_t stream) {
-  if (p.stream_f32)
-    return vec ? forward<float, FP8, true>(p, out, q, q_row, scales, stream)
-               : forward<float, FP8, false>(p, out, q, q_row, scales, stream);
-  return vec ? forward<uint16_t, FP8, true>(p, out, q, q_row, scales, stream)
-             : forward<uint16_t, FP8, false>(p, out, q, q_row, scales, stream);
+  if (a == kVec) return forward<T, FP8, kVec>(p, out, q, q_row, scales, stream);
+  if constexpr (!FP8)
+    if (a == kShift) return forward<T, FP8, kShift>(p, out, q, q_row, scales, stream);
+  return forward<T, FP8, kAny>(p, out, q, q_row, scales, stream);
 }
 
 // The backward's spread (several rows a block only with a chunk per thread), and its blocks, which are the rows of
 // its sums: 1024 threads for every SM.
-Spread backward_spread(int D, bool vec) { return spread_of(D, 1, vec, false); }
-int backward_blocks(long long rows, int D, bool vec) {
-  const Spread s = backward_spread(D, vec);
+Spread backward_spread(int D, Access a) { return spread_of(D, 1, a, false); }
+int backward_blocks(long long rows, int D, Access a) {
+  const Spread s = backward_spread(D, a);
   const long long most = 152LL * (1024 / (s.threads * s.rows)), all = (rows + s.rows - 1) / s.rows;
   return (int)(all < most ? (all > 0 ? all : 1) : most);
 }
@@ -529,29 +632,35 @@ int backward_blocks(long long rows, int D, bool vec) {
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const AddNormProblem& p, uint16_t* out, cudaStream_t stream) {
-  return dispatch<false>(p, vec_ok(p) && aligned_to(out, 16), out, nullptr, 0, nullptr, stream);
+  const Access a = access_of(p, aligned_to(out, 16));
+  return p.stream_f32 ? dispatch<float, false>(p, a, out, nullptr, 0, nullptr, stream)
+                      : dispatch<uint16_t, false>(p, a, out, nullptr, 0, nullptr, stream);
 }
 cudaError_t launch_add_rmsnorm_fp8(const AddNormProblem& p, uint8_t* q, long long q_row, uint8_t* scales,
                                    cudaStream_t stream) {
-  return dispatch<true>(p, vec_ok(p), nullptr, q, q_row, scales, stream);
+  const Access a = access_of(p, true);
+  return p.stream_f32 ? dispatch<float, true>(p, a, nullptr, q, q_row, scales, stream)
+                      : dispatch<uint16_t, true>(p, a, nullptr, q, q_row, scales, stream);
 }
 
 size_t add_rmsnorm_backward_workspace_floats(long long rows, int D) {
-  const int a = backward_blocks(rows, D, false), b = backward_blocks(rows, D, true);
+  const int a = backward_blocks(rows, D, kAny);
+  const int b = D % 8 == 0 ? backward_blocks(rows, D, kVec) : shift_ok(D) ? backward_blocks(rows, D, kShift) : 0;
   return (size_t)(a > b ? a : b) * D;
 }
 
 cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStream_t stream) {
   if (p.rows == 0) return cudaMemsetAsync(p.dw, 0, sizeof(float) * p.D, stream);
-  const bool vec = p.D % 8 == 0 && aligned_to(p.w, 16) && aligned_to(p.h, 16) && aligned_to(p.dout, 16) &&
-                   aligned_to(p.dh, 16) && aligned_to(p.dx, 16) && aligned_to(p.dresidual, 16);
-  const int blocks = backward_blocks(p.rows, p.D, vec);
-  const Spread s = backward_spread(p.D, vec);
+  const bool aligned = aligned_to(p.w, 16) && aligned_to(p.h, 16) && aligned_to(p.dout, 16) && aligned_to(p.dh, 16) &&
+                       aligned_to(p.dx, 16) && aligned_to(p.dresidual, 16);
+  const Access a = !aligned ? kAny : p.D % 8 == 0 ? kVec : shift_ok(p.D) ? kShift : kAny;
+  const int blocks = backward_blocks(p.rows, p.D, a);
+  const Spread s = backward_spread(p.D, a);
   const cudaError_t err = with_chunks(s.R, [&](auto r) {
     constexpr int R = decltype(r)::value;
     auto go = [&](auto kernel) {
       const int each = p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>;
-      const int ring = vec ? s.threads * s.rows * each : 0;
+      const int ring = a != kAny ? s.threads * s.rows * each : 0;
       const int sums = s.rows > 1 ? s.rows * p.D * 4 : 0, bytes = ring > sums ? ring : sums;
       // At every launch: the attribute belongs to the current device.
       const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -559,20 +668,16 @@ cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStr
       kernel<<<blocks, s.block(), bytes, stream>>>(p, p.ws);
       return cudaGetLastError();
     };
-    if constexpr (R == 1) {
-      if (s.rows > 1) {
-        if (p.stream_f32)
-          return vec ? go(add_rmsnorm_backward_kernel<float, true, 1, true>)
-                     : go(add_rmsnorm_backward_kernel<float, false, 1, true>);
-        return vec ? go(add_rmsnorm_backward_kernel<uint16_t, true, 1, true>)
-                   : go(add_rmsnorm_backward_kernel<uint16_t, false, 1, true>);
-      }
-    }
-    if (p.stream_f32)
-      return vec ? go(add_rmsnorm_backward_kernel<float, true, R, false>)
-                 : go(add_rmsnorm_backward_kernel<float, false, R, false>);
-    return vec ? go(add_rmsnorm_backward_kernel<uint16_t, true, R, false>)
-               : go(add_rmsnorm_backward_kernel<uint16_t, false, R, false>);
+    auto with = [&](auto access) {
+      constexpr int A = decltype(access)::value;
+      if constexpr (R == 1)
+        if (s.rows > 1)
+          return p.stream_f32 ? go(add_rmsnorm_backward_kernel<float, A, 1, true>)
+                              : go(add_rmsnorm_backward_kernel<uint16_t, A, 1, true>);
+      return p.stream_f32 ? go(add_rmsnorm_backward_kernel<float, A, R, false>)
+                          : go(add_rmsnorm_backward_kernel<uint16_t, A, R, false>);
+    };
+    return a == kVec ? with(Int<kVec>{}) : a == kShift ? with(Int<kShift>{}) : with(Int<kAny>{});
   });
   if (err != cudaSuccess) return err;
   return launch_sum_rows(p.ws, p.dw, nullptr, blocks, p.D, p.D, p.D, stream);

@@ -199,6 +199,36 @@ def test_norm_backward_over_the_range(scale, D, f32):
     within(g["dw"], dw, 2.0 ** -15 * wsize, "dw")
 
 
+@pytest.mark.parametrize("rows,D", [(3, 1001), (5, 9), (3000, 37), (2500, 1340), (2, 8), (17, 8187)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_rows_keep_to_themselves(rows, D, f32):
+    """Rows side by side at any offset: a row of NaN changes no other, and nothing around a result is written."""
+    _, h, w = norm_case(rows, D, f32, True, seed=90)
+    x, r, dout, dh = rand((rows, D), 91), h.contiguous(), rand((rows, D), 92), rand((rows, D), 93, 1.0, h.dtype)
+
+    def room(dtype):
+        flat = torch.full((rows * D + 64,), 7.0, dtype=dtype, device=DEV)
+        return flat, flat[32:32 + rows * D].view(rows, D)
+
+    def call(x, dout):
+        flats, places = zip(*(room(k) for k in (BF16, h.dtype, BF16, h.dtype)))
+        pkg.add_rmsnorm(x, r, w, out=places[0], h=places[1])
+        g = pkg.add_rmsnorm_backward(r, w, dout, dh, grads=dict(dx=places[2], dresidual=places[3]))
+        for flat in flats:
+            assert (flat[:32] == 7).all() and (flat[32 + rows * D:] == 7).all()
+        return (*places, g["dw"])
+
+    want = call(x, dout)
+    for bad in {0, rows // 2, rows - 1}:
+        y, d = x.clone(), dout.clone()
+        y[bad] = d[bad] = float("nan")
+        got = call(y, d)
+        rest = torch.arange(rows, device=DEV) != bad
+        for a, b in zip(got[:4], want[:4]):
+            assert torch.equal(a[rest], b[rest]) and a[bad].isnan().all()
+        assert got[4].isnan().all()
+
+
 def test_norm_rows_of_one_infinity():
     """An infinity leaves the rest of its row zero, in 8 bits but for its block, and other rows as they are."""
     x, r, w = norm_case(4, 384, True, True)
