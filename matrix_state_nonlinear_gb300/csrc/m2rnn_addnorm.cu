@@ -12,7 +12,8 @@
 // 128 channels of a scale); otherwise they lie a row's threads apart, so that a warp's accesses are still of
 // consecutive values.
 // Measured: 65536 x 2048, bf16: forward 154 us (7.0 TB/s, 1.03 of a copy's rate), backward 171 us with the sums;
-// 8191 x 4096 in 8 bits on a float32 stream: 56 us (6.6 TB/s); odd rows, 65536 x 1001: 140 and 172 us.
+// 8191 x 4096 in 8 bits on a float32 stream: 56 us (6.6 TB/s); 65536 rows of 1001: 102 and 107 us, of 1000 77 and
+// 105.
 #include "m2rnn_layer.h"
 #include "ptx_util.cuh"
 
@@ -29,8 +30,8 @@ __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 // How a row lies in memory.  kVec: every row of every tensor starts on 16 bytes.  kShift: rows of dense tensors, or
 // as good as, with a number of channels that is no multiple of 8, so that row m starts m D mod 8 = s values behind a
 // 16-byte boundary, in all tensors alike: a chunk is 16-byte aligned and its first channel is s below a multiple of
-// 8, the first and last chunk of a row hold neighbours' values, which read as zero (65536 x 1001: 140 us value by
-// value).  kAny: anything else, value by value.
+// 8, the first and last chunk of a row hold neighbours' values, which read as zero (65536 x 1001, bf16: forward
+// 102 us, 139 value by value, backward 107 and 172).  kAny: anything else, value by value.
 enum Access { kAny, kVec, kShift };
 // The places in a row that hold its channels, counted from its first chunk on: none where there is no row.
 // `last`: memory may end behind them.
@@ -139,7 +140,8 @@ struct Raw8 {
     }
   }
 };
-// The weights of chunk r.  kShift: of two chunks of w, moved by the row's shift.
+// The weights of chunk r.  kShift: of two chunks of w, by the row's shift (3000 x 9001, backward: 109 us; moved by
+// powers of two, 121).
 template <int A>
 __device__ __forceinline__ void load_weight(const float* w, int r, const Span& d, int D, float2 (&f)[4]) {
   if constexpr (A != kShift) {
@@ -160,15 +162,21 @@ __device__ __forceinline__ void load_weight(const float* w, int r, const Span& d
         for (int i = 0; i < 8; ++i) v[8 * h + i] = c + i >= 0 && c + i < D ? w[c + i] : 0.f;
       }
     }
-    // v[8 - lo] to the front, by powers of two.
-    const int k = 8 - d.lo;
+    auto pick = [&](auto shift) {
+      constexpr int from = 8 - decltype(shift)::value;
 #pragma unroll
-    for (int b = 8; b > 0; b /= 2)
-      if (k & b)
-#pragma unroll
-        for (int i = 0; i < 7 + b && i + b < 16; ++i) v[i] = v[i + b];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) f[i] = make_float2(v[from + 2 * i], v[from + 2 * i + 1]);
+    };
+    switch (d.lo) {
+      case 1: pick(Int<1>{}); break;
+      case 2: pick(Int<2>{}); break;
+      case 3: pick(Int<3>{}); break;
+      case 4: pick(Int<4>{}); break;
+      case 5: pick(Int<5>{}); break;
+      case 6: pick(Int<6>{}); break;
+      case 7: pick(Int<7>{}); break;
+      default: pick(Int<0>{});
+    }
   }
 }
 
