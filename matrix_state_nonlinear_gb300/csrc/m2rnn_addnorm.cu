@@ -589,13 +589,23 @@ cudaError_t with_chunks(int R, F f) {
   return R == 1 ? f(Int<1>{}) : R == 2 ? f(Int<2>{}) : f(Int<4>{});
 }
 
+// Chunks a thread of many rows (few are spread as wide as they go): two (65536 x 2048 bf16 with residual: 153 us,
+// with one 169, with four 158), of which a thread's loads are on their way together.  Four where they are of two
+// bytes a channel, or of four and the result of one, and rows are long: less of a block's time is then spent on
+// sums (16384 x 4096 bf16 without residual: in 8 bits 47 us instead of 54, in bf16 43 instead of 47; with residual,
+// in 8 bits, 71.7 instead of 73.1).  One where 16 threads hold the row so (498379 x 96 in 8 bits: 47 instead of 72).
+int chunks_of(const AddNormProblem& p, Access a, bool fp8) {
+  if (a == kAny || p.D + (a == kShift ? 7 : 0) <= 16 * 8) return 1;
+  const int read = (p.stream_f32 ? 4 : 2) + (p.x ? 2 : 0);
+  const bool four = fp8 ? p.D >= (read == 2 ? 512 : 4096) && read <= 4 : p.D >= 2048 && read == 2;
+  return a == kVec && four ? 4 : 2;
+}
+
 template <typename T, bool FP8, Access A>
 cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
                     cudaStream_t stream) {
-  // Few rows are spread as wide as they go; of many, a thread takes two chunks (65536 x 2048: 153 us; one chunk
-  // 169, four 158; 8191 x 4096 in 8 bits: 58, 65, 64).
   const bool many = p.rows >= 152 * 16;
-  Spread s = spread_of(p.D, many && A != kAny ? 2 : 1, A, FP8);
+  Spread s = spread_of(p.D, many ? chunks_of(p, A, FP8) : 1, A, FP8);
   if (!many) s.rows = s.threads < 32 ? 2 : 1;
   return with_chunks(s.R, [&](auto r) {
     const long long blocks = (p.rows + s.rows - 1) / s.rows;
