@@ -216,8 +216,9 @@ __device__ __forceinline__ float larger(float a, float b) {
   return r;
 }
 
-// Chunk r of a row in 8 bits, kVec: 16 threads to a scale.  v holds h w; the result is v inv.  The largest |v inv| is
+// Chunk r of a row in 8 bits: 16 threads to a scale, TAIL where the row's last chunk may be shorter.  v holds h w; the result is v inv.  The largest |v inv| is
 // the largest |v| times inv, rounding being monotonic, and the scale's inverse, a power of two, goes with inv.
+template <bool TAIL>
 __device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r, int D, uint8_t* q, uint8_t* scales) {
   float top = larger(larger(larger(v[0].x, v[0].y), larger(v[1].x, v[1].y)),
                      larger(larger(v[2].x, v[2].y), larger(v[3].x, v[3].y)));
@@ -234,8 +235,17 @@ __device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r
   const int c = 8 * (threadIdx.x + r * blockDim.x);
   if (c >= D) return;
   if (c % kScaleBlock == 0) scales[c / kScaleBlock] = (uint8_t)e;
-  *reinterpret_cast<uint2*>(q + c) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+  if (!TAIL || c + 8 <= D) {
+    *reinterpret_cast<uint2*>(q + c) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (c + i < D) q[c + i] = (uint8_t)(b[i / 2] >> (8 * (i & 1)));
+  }
 }
+// kShift in 8 bits: a row's values pass through shared memory, as scales and q follow the row.  Value c is at c +
+// c / 32, so that threads eight apart meet different banks (65536 x 1001, bf16: 108 us; value by value 196).
+__host__ __device__ constexpr int place_of(int c) { return c + c / 32; }
 // |values| as bits, which order them and put NaN above all.
 __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
@@ -284,6 +294,8 @@ __global__ void __launch_bounds__(512, R == 1 || (A != kAny && R == 2) ? 2 : 1)
   const Span d{lo, row < p.rows ? lo + p.D : 0, row + 1 >= p.rows};  // behind the last row there are no channels
   const T* stream = static_cast<const T*>(p.stream) + row * p.stream_row - lo;
   const uint16_t* x = p.x ? p.x + row * p.x_row - lo : nullptr;
+  extern __shared__ float turned[];
+  [[maybe_unused]] float* turn = turned + threadIdx.y * place_of(p.D + 31);
   float2 h[R][4], s = pair(0.f);
   Raw8<T, A> a[R];
   Raw8<uint16_t, A> b[R];
@@ -306,19 +318,36 @@ __global__ void __launch_bounds__(512, R == 1 || (A != kAny && R == 2) ? 2 : 1)
     if (p.h) a[r].store(static_cast<T*>(p.h) + row * p.D - lo, r, d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma2(h[r][i], h[r][i], s);
+    if constexpr (FP8 && A == kShift) {
+      const float* value = &h[r][0].x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = Raw8<T, A>::first(r) + i - lo;
+        if (c >= 0 && c < p.D) turn[place_of(c)] = value[i];
+      }
+    }
   }
+  if (FP8 && A == kShift) __syncwarp();  // wider rows pass the sum's barrier
   const float inv = rsqrtf(row_sum(s.x + s.y, 0) * (1.f / (float)p.D) + p.eps);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float2 w[4];
-    load_weight<A>(p.w, r, d, p.D, w);
+    if constexpr (FP8 && A == kShift) {
+      const int c = Raw8<T, A>::first(r);
+      float* value = &h[r][0].x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) value[i] = c + i < p.D && d.hi > 0 ? turn[place_of(c) + i] : 0.f;
+      load_weight<A>(p.w, r, Span{0, p.D, false}, p.D, w);
+    } else {
+      load_weight<A>(p.w, r, d, p.D, w);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[r][i] = mul2(h[r][i], w[i]);
-    if constexpr (!FP8 || A == kAny)
+    if constexpr (!FP8 || A == kAny)  // store_fp8 does it itself
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[r][i] = mul2(h[r][i], pair(inv));
-    if constexpr (FP8 && A == kVec) {
-      store_fp8(h[r], inv, r, d.hi, q + row * q_row, scales + row * scale_blocks(p.D));
+    if constexpr (FP8 && A != kAny) {
+      store_fp8<A == kShift>(h[r], inv, r, d.hi > 0 ? p.D : 0, q + row * q_row, scales + row * scale_blocks(p.D));
     } else if constexpr (!FP8) {
       Raw8<uint16_t, A> o;
       o.set(h[r]);
@@ -610,8 +639,13 @@ cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long lon
   return with_chunks(s.R, [&](auto r) {
     const long long blocks = (p.rows + s.rows - 1) / s.rows;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;  // more than a terabyte
-    add_rmsnorm_kernel<T, FP8, A, decltype(r)::value>
-        <<<(unsigned)blocks, s.block(), 0, stream>>>(p, out, q, q_row, scales);
+    auto* kernel = add_rmsnorm_kernel<T, FP8, A, decltype(r)::value>;
+    const int bytes = FP8 && A == kShift ? s.rows * place_of(p.D + 31) * (int)sizeof(float) : 0;
+    if (bytes > 0) {  // at every launch: the attribute belongs to the current device
+      const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (attr != cudaSuccess) return attr;
+    }
+    kernel<<<(unsigned)blocks, s.block(), bytes, stream>>>(p, out, q, q_row, scales);
     return cudaGetLastError();
   });
 }
@@ -633,8 +667,7 @@ template <typename T, bool FP8>
 cudaError_t dispatch(const AddNormProblem& p, Access a, uint16_t* out, uint8_t* q, long long q_row, uint8_t* scales,
                      cudaStream_t stream) {
   if (a == kVec) return forward<T, FP8, kVec>(p, out, q, q_row, scales, stream);
-  if constexpr (!FP8)
-    if (a == kShift) return forward<T, FP8, kShift>(p, out, q, q_row, scales, stream);
+  if (a == kShift) return forward<T, FP8, kShift>(p, out, q, q_row, scales, stream);
   return forward<T, FP8, kAny>(p, out, q, q_row, scales, stream);
 }
 

@@ -229,6 +229,31 @@ def test_norm_rows_keep_to_themselves(rows, D, f32):
         assert got[4].isnan().all()
 
 
+@pytest.mark.parametrize("rows,D", [(3, 1001), (5, 9), (3000, 37), (2500, 1340), (17, 8187), (40, 200)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_rows_in_8_bits_keep_to_themselves(rows, D, f32):
+    """The same in 8 bits: the bytes between rows stay as they were."""
+    _, h, w = norm_case(rows, D, f32, True, seed=95)
+    x, r, row = rand((rows, D), 96), h.contiguous(), (D + 15) // 16 * 16 + 16
+
+    def call(x):
+        flat = torch.full((rows + 1, row), 0x55, dtype=torch.uint8, device=DEV)
+        q, s, h = pkg.add_rmsnorm_fp8(x, r, w, out=flat.view(torch.float8_e4m3fn)[:rows, :D])
+        assert (flat[:rows, D:] == 0x55).all() and (flat[rows] == 0x55).all()
+        return q.view(torch.uint8), s.view(torch.uint8), h
+
+    want = call(x)
+    check_quantised(want[0].view(torch.float8_e4m3fn), want[1].view(torch.float8_e8m0fnu),
+                    ol.rmsnorm(f64(want[2]), f64(w), 1e-5))
+    for bad in {0, rows // 2, rows - 1}:
+        y = x.clone()
+        y[bad] = float("nan")
+        got = call(y)
+        rest = torch.arange(rows, device=DEV) != bad
+        assert all(torch.equal(a[rest], b[rest]) for a, b in zip(got, want))
+        assert (got[1][bad] == 255).all() and (got[0][bad] & 0x7f == 0x7f).all()
+
+
 def test_norm_rows_of_one_infinity():
     """An infinity leaves the rest of its row zero, in 8 bits but for its block, and other rows as they are."""
     x, r, w = norm_case(4, 384, True, True)
