@@ -58,6 +58,22 @@ def test_norm():
     assert ((g["dw"].double() - want).abs() <= 2.0 ** -13 * size).all()
 
 
+def test_norm_of_odd_rows():
+    """Rows that start anywhere; a multiple of 8 of them before the last 5000, which so start as they do alone."""
+    rows, D = (OVER // 2049 + 777) // 8 * 8, 2049
+    x, r, w = fill((rows, D), 6), fill((rows, D), 7), torch.rand(D, device=DEV) + 0.5
+    out, h = pkg.add_rmsnorm(x, r, w)
+    a, b = pkg.add_rmsnorm(tail(x), tail(r), w)
+    assert torch.equal(out[-5000:], a) and torch.equal(h[-5000:], b)
+    del out
+    q, s, h = pkg.add_rmsnorm_fp8(x, r, w, h=h)
+    a, c, _ = pkg.add_rmsnorm_fp8(tail(x), tail(r), w)
+    assert torch.equal(bits(q[-5000:]), bits(a)) and torch.equal(bits(s[-5000:]), bits(c))
+    del q, s
+    g = pkg.add_rmsnorm_backward(h, w, x, r)
+    assert torch.equal(g["dx"][-5000:], pkg.add_rmsnorm_backward(tail(h), w, tail(x), tail(r))["dx"])
+
+
 @pytest.mark.parametrize("D", [2048, 2047])
 def test_quantise(D):
     rows = OVER // D + 99
