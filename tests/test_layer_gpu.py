@@ -305,7 +305,8 @@ def test_norm_backward_repeats_and_empty():
 LINEAR = [(1, 1, 1), (1, 128, 128), (1, 2000, 1000), (2, 129, 127), (3, 8, 4096), (7, 256, 384), (16, 200, 144), (17, 130, 513),
           (33, 96, 2048), (64, 520, 640), (65, 128, 256), (100, 4384, 300), (127, 127, 127), (129, 257, 129), (200, 300, 1300),
           (255, 384, 96), (257, 136, 8192), (520, 1000, 520), (1021, 264, 200), (3, 5, 20000),
-          (20, 6400, 1700), (86, 6381, 1500), (100, 3200, 3000), (60, 2700, 2600), (9, 2500, 4100), (2100, 2200, 300), (4000, 1300, 1280), (260, 16500, 2180), (2500, 2001, 700), (3000, 1158, 1821), (2049, 2052, 4000)]
+          (20, 6400, 1700), (86, 6381, 1500), (100, 3200, 3000), (60, 2700, 2600), (9, 2500, 4100), (2100, 2200, 300), (4000, 1300, 1280), (260, 16500, 2180), (2500, 2001, 700), (3000, 1158, 1821), (2049, 2052, 4000),
+          (5000, 1000, 7), (20000, 100, 129), (19500, 1, 200), (2560, 1024, 640), (2432, 1024, 640), (129, 9800, 1040)]
 
 
 def linear_case(M, N, K, seed=0):
