@@ -470,7 +470,8 @@ m2rnn_status m2rnn_gate_groupnorm_backward(const void* y, int y_f32, const uint1
  * float32: |h| above 1e19 overflows its square (out is 0 there).  D <= 16384 (UNSUPPORTED above).
  * A NaN gives NaN in all of its row, an infinity in its channel (in 8 bits in its 128) and zeros in the rest of
  * the row; other rows are untouched.  16-byte aligned pointers run on 16-byte accesses where D % 8 == 0 and rows
- * are aligned so, or where the rows' distances are D or a multiple of 8 more.
+ * are aligned so, or where the rows' distances are D or a multiple of 8 more.  The order of a row's sum depends on
+ * the sizes and alignment of the call and, where D % 8 != 0, on the row's place; the same call gives the same bits.
  * m2rnn_add_rmsnorm: out bf16.  m2rnn_add_rmsnorm_fp8: out in 8 bits (see below), q [rows, D] with q_row
  *   bytes from row to row (q and q_row multiples of 16) and scales [rows, ceil(D / 128)], dense.
  * m2rnn_add_rmsnorm_backward: with dout [rows, D] bf16 and dh [rows, D] of the stream's type (the gradient

@@ -41,7 +41,11 @@ def test_norm():
     out, h = pkg.add_rmsnorm(x, r, w)
     a, b = pkg.add_rmsnorm(tail(x), tail(r), w)
     assert torch.equal(out[-5000:], a) and torch.equal(h[-5000:], b)
-    assert torch.equal(out[:100], pkg.add_rmsnorm(x[:100], r[:100], w)[0])
+    # Few rows are spread over more threads, whose sums of squares are in another order.  Both results are within
+    # 2^-8 + 2^-17 of the exact v (a rounding to bf16, float32 before it), so within 2^-7 + 2^-16 of v of each other,
+    # and |v| is at most 1 + 2^-7 of either: (2^-7 + 2^-16)(1 + 2^-7) < 2^-7 + 2^-13.
+    few = pkg.add_rmsnorm(x[:100], r[:100], w)[0].double()
+    assert ((out[:100].double() - few).abs() <= (2.0 ** -7 + 2.0 ** -13) * few.abs()).all()
     q, s, h = pkg.add_rmsnorm_fp8(x, r, w, h=h)
     a, c, _ = pkg.add_rmsnorm_fp8(tail(x), tail(r), w)
     assert torch.equal(bits(q[-5000:]), bits(a)) and torch.equal(bits(s[-5000:]), bits(c))
