@@ -169,21 +169,29 @@ def add_rmsnorm_backward(h, w, dout, dh=None, eps=1e-5, grads=None, workspace=No
     D = shape[-1]
     if kind not in (F32, BF16):
         raise TypeError(f"h: expected {F32} or {BF16}, got {kind}")
-    g = dict(grads or {})
+    hp = _ptr(h, "h", kind, shape, dev)
+    g = dict(grads) if grads else {}
     if g.get("dx") is None:
         g["dx"] = _dense(h, BF16)
+        dx = g["dx"].data_ptr()
+    else:
+        dx = _ptr(g["dx"], "dx", BF16, shape, dev)
     if g.get("dresidual") is None:
         g["dresidual"] = g["dx"] if kind is BF16 else _dense(h, kind)
+        dr = g["dresidual"].data_ptr()
+    else:
+        dr = _ptr(g["dresidual"], "dresidual", kind, shape, dev)
     if g.get("dw") is None:
         g["dw"] = torch.empty(D, dtype=F32, device=h.device)
-    dx, dr = _ptr(g["dx"], "dx", BF16, shape, dev), _ptr(g["dresidual"], "dresidual", kind, shape, dev)
+        dw = g["dw"].data_ptr()
+    else:
+        dw = _ptr(g["dw"], "dw", F32, (D,), dev)
     rows = h.numel() // D if D else 0
     lib = load_library()
     ws, wp, wb = _workspace(workspace, lib.m2rnn_add_rmsnorm_backward_workspace_bytes(rows, D), h)
     st = lib.m2rnn_add_rmsnorm_backward(
-        _ptr(h, "h", kind, shape, dev), int(kind is F32), _ptr(w, "w", F32, (D,), dev), eps,
-        _ptr(dout, "dout", BF16, shape, dev), _ptr(dh, "dh", kind, shape, dev), dx, None if dr == dx else dr,
-        _ptr(g["dw"], "dw", F32, (D,), dev), rows, D, wp, wb, _stream(dev))
+        hp, kind is F32, _ptr(w, "w", F32, (D,), dev), eps, _ptr(dout, "dout", BF16, shape, dev),
+        _ptr(dh, "dh", kind, shape, dev), dx, None if dr == dx else dr, dw, rows, D, wp, wb, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_add_rmsnorm_backward")
     return g
@@ -302,11 +310,14 @@ def _gradients(grads, out, max_norm, norm, workspace):
         to = array("Q", [_ptr(o, "out", t.dtype, t.shape, dev) for o, t in zip(out, grads)])
     if norm is None:
         norm = torch.empty((), dtype=F32, device=grads[0].device)
+        to_norm = norm.data_ptr()
+    else:
+        to_norm = _ptr(norm, "norm", F32, (), dev)
     lib = load_library()
     ws, wp, wb = _workspace(workspace, lib.m2rnn_grad_norm_workspace_bytes(n), grads[0])
     st = lib.m2rnn_clip_grad_norm(ptrs.buffer_info()[0], None if to is None else to.buffer_info()[0],
                                   sizes.buffer_info()[0], kinds.buffer_info()[0], n, max_norm,
-                                  _ptr(norm, "norm", F32, (), dev), wp, wb, _stream(dev))
+                                  to_norm, wp, wb, _stream(dev))
     if st != OK:
         _raise(st, "m2rnn_clip_grad_norm")
     return norm
