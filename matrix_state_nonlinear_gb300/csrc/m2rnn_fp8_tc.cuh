@@ -90,8 +90,8 @@ constexpr int kGroup = 4 * kQuad;  // and to a group of words
 // Groups of scale words of ROWS rows per lane: the 16 blocks from i on, loaded one group ahead of their use,
 // all loads before anything that waits for them.  Blocks behind a row's last get any scale: nothing uses them.
 // A row of `blocks` scales starts anywhere, so a word of it is made of two whole words of memory; only words
-// that hold a byte of the row are read, and of the tensor's last row (and its first, where that does not start on
-// a word), behind which memory may end, bytes: those in one call a row after all other loads, as a call waits for
+// that hold a byte of the row are read, and of the rows whose words hold bytes outside the tensor (at most three
+// at either end), where memory may end, bytes: those in one call a row after all other loads, as a call waits for
 // its result (3840 x 3840 x 1280: 22.8 us with a call for each of the first and last row's words, 18.6 so).
 template <int ROWS>
 struct ScaleWords {
@@ -102,7 +102,7 @@ struct ScaleWords {
   uint32_t next[ROWS][4], over[ROWS];
   // The tensor's row m of `rows`.
   __device__ __forceinline__ void aim(int r, const uint8_t* scales, long long m, long long rows) {
-    live[r] = m < rows, edge[r] = m == rows - 1 || (m == 0 && (reinterpret_cast<uintptr_t>(scales) & 3u));
+    live[r] = m < rows, edge[r] = live[r] && words_leave(scales, rows, blocks, m);
     row[r] = scales + m * blocks;
   }
   __device__ __forceinline__ void fetch(int i) {
@@ -118,7 +118,7 @@ struct ScaleWords {
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const int first = i - (int)(reinterpret_cast<uintptr_t>(row[r] + i) & 3u);  // from the row's start
+      const int first = word_start(row[r], i);
 #pragma unroll
       for (int q = 0; q < 5; ++q) {
         uint32_t w = 0x7f7f7f7fu;
@@ -132,7 +132,7 @@ struct ScaleWords {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
       if (edge[r]) {
-        const EdgeWords e = edge_words(row[r], i - (int)(reinterpret_cast<uintptr_t>(row[r] + i) & 3u), blocks);
+        const EdgeWords e = edge_words(row[r], word_start(row[r], i), blocks);
         next[r][0] = e.w[0], next[r][1] = e.w[1], next[r][2] = e.w[2], next[r][3] = e.w[3], over[r] = e.w[4];
       }
   }

@@ -57,6 +57,17 @@ cudaError_t launch_quantise_rows(const void* x, bool f32, long long x_row, uint8
 cudaError_t launch_quantise_weight(const void* w, bool f32, long long w_row, uint8_t* q, long long q_row,
                                    uint8_t* scales, int N, int K, cudaStream_t stream);
 
+// Rows of scales, `blocks` bytes each and one behind the other from any address on, are read as whole words of memory.
+// The block, of the row at `row`, that the word of block i starts with: i, or up to three less.
+__host__ __device__ inline int word_start(const uint8_t* row, int i) {
+  return i - (int)(reinterpret_cast<uintptr_t>(row + i) & 3u);
+}
+// Whether words of row m of `rows` hold bytes outside the tensor.
+__host__ __device__ inline bool words_leave(const uint8_t* scales, long long rows, int blocks, long long m) {
+  const uintptr_t from = reinterpret_cast<uintptr_t>(scales), row = from + m * blocks;
+  return (row & ~(uintptr_t)3) < from || ((row + blocks + 3) & ~(uintptr_t)3) > from + rows * blocks;
+}
+
 struct LinearProblem {
   const uint8_t *x, *x_scales;  // [M, K], [M, scale_blocks(K)]
   const uint16_t* raw;          // or, for up to kRawRows tokens, x as bf16, x_row elements from row to row
