@@ -641,8 +641,11 @@ cudaError_t forward(const AddNormProblem& p, uint16_t* out, uint8_t* q, long lon
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;  // more than a terabyte
     auto* kernel = add_rmsnorm_kernel<T, FP8, A, decltype(r)::value>;
     const int bytes = FP8 && A == kShift ? s.rows * place_of(p.D + 31) * (int)sizeof(float) : 0;
-    if (bytes > 0) {  // at every launch: the attribute belongs to the current device
-      const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if constexpr (FP8 && A == kShift) {
+      // At every launch, as the attribute belongs to the current device, and for the widest row, whatever this call's
+      // is: another thread's call may be between its attribute and its launch.  (Several rows a block: under 18 KB.)
+      constexpr int kMost = place_of(kNormMaxRow + 31) * (int)sizeof(float);
+      const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
       if (attr != cudaSuccess) return attr;
     }
     kernel<<<(unsigned)blocks, s.block(), bytes, stream>>>(p, out, q, q_row, scales);
@@ -711,10 +714,13 @@ cudaError_t launch_add_rmsnorm_backward(const AddNormBackwardProblem& p, cudaStr
     constexpr int R = decltype(r)::value;
     auto go = [&](auto kernel) {
       const int each = p.stream_f32 ? kRingPerThread<float, R> : kRingPerThread<uint16_t, R>;
+      constexpr int kMost = 512 * (kRingPerThread<float, R> > kRingPerThread<uint16_t, R> ? kRingPerThread<float, R>
+                                                                                          : kRingPerThread<uint16_t, R>);
       const int ring = a != kAny ? s.threads * s.rows * each : 0;
       const int sums = s.rows > 1 ? s.rows * p.D * 4 : 0, bytes = ring > sums ? ring : sums;
-      // At every launch: the attribute belongs to the current device.
-      const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      // At every launch, as the attribute belongs to the current device, and for the largest block, whatever this call's
+      // is: another thread's call may be between its attribute and its launch.  (Sums of several rows: 8 KB at most.)
+      const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
       if (attr != cudaSuccess) return attr;
       kernel<<<blocks, s.block(), bytes, stream>>>(p, p.ws);
       return cudaGetLastError();
