@@ -435,7 +435,7 @@ cudaError_t launch_vt_cache(const Problem& p, EncodeTiledFn enc, cudaStream_t st
   // Tc <= threads (one gate logit per thread and chunk), and the shared memory fits.
   int Tc = min(V <= 64 ? 64 : 32, 2 * Kp);
   SmemLayout L = make_layout(Kp, V, Tc, WREG);
-  while (L.total > 227 * 1024 && Tc > 8) {
+  while (L.total > kMostShared && Tc > 8) {
     Tc /= 2;
     L = make_layout(Kp, V, Tc, WREG);
   }
@@ -447,7 +447,7 @@ cudaError_t launch_vt_cache(const Problem& p, EncodeTiledFn enc, cudaStream_t st
     return cudaErrorInvalidValue;
   if (!make_map(enc, &mv, p.v, V, p.N, p.T, p.B, Tc)) return cudaErrorInvalidValue;
   auto kern = fwd_bf16_mma_rowwarp<VT, WREG, kCache, kRagged>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   if (err != cudaSuccess) return err;
   const unsigned grid = (unsigned)p.B * (unsigned)p.N;
   kern<<<grid, 2 * Kp, L.total, stream>>>(mq, mk, mv, (const uint16_t*)p.q, (const uint16_t*)p.k,

@@ -598,7 +598,7 @@ cudaError_t launch_pipe_vt(const Problem& p, EncodeTiledFn enc, cudaStream_t str
   const bool ring = p.Hs && VT == 4;
   int Tc = 64;
   PipeLayout L = pipe_layout(p.K, V, Tc, ring);
-  while (L.total > 227 * 1024 && Tc > 8) {
+  while (L.total > kMostShared && Tc > 8) {
     Tc /= 2;
     L = pipe_layout(p.K, V, Tc, ring);
   }
@@ -627,7 +627,7 @@ cudaError_t launch_pipe_vt(const Problem& p, EncodeTiledFn enc, cudaStream_t str
       return cudaErrorInvalidValue;
   }
   auto kern = p.Hs ? fwd_bf16_mma_pipe<VT, true> : fwd_bf16_mma_pipe<VT, false>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   if (err != cudaSuccess) return err;
   const unsigned grid = (unsigned)p.B * (unsigned)p.N;
   const int threads = 32 * (p.K / 16 + 1);

@@ -762,7 +762,7 @@ cudaError_t launch_r8(const Problem& p, EncodeTiledFn enc, cudaStream_t stream) 
     return cudaErrorInvalidValue;
   auto kern = fwd_bf16_r8<MT, CS, kConv>;
   cudaError_t err =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)CS * (unsigned)p.B * (unsigned)p.N, 1, 1);

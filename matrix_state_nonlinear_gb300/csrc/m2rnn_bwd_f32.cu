@@ -250,7 +250,7 @@ cudaError_t launch_simt(const BackwardProblem& p, cudaStream_t stream) {
   const size_t smem = sizeof(float) * ((size_t)p.V * p.V + (size_t)p.K * p.V + 2 * p.K +
                                        2 * p.V + 4 + kThreads / 32 + 1);
   cudaError_t err = cudaFuncSetAttribute(bwd_simt_kernel<Tin, Th>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   if (err != cudaSuccess) return err;
   const unsigned pairs = (unsigned)p.B * (unsigned)p.N;
   float* heads = p.ws + (size_t)p.B * p.N * backward_pair_floats(p.K, p.V);

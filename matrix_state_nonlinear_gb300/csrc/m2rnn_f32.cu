@@ -95,7 +95,7 @@ cudaError_t launch_fwd_f32(const Problem& p, cudaStream_t stream) {
   const size_t smem =
       sizeof(float) * ((size_t)p.V * p.V + 2ull * p.K * p.V + 2ull * (2 * p.K + p.V + 2));
   cudaError_t err =
-      cudaFuncSetAttribute(fwd_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      cudaFuncSetAttribute(fwd_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   if (err != cudaSuccess) return err;
   const unsigned grid = (unsigned)p.B * (unsigned)p.N;
   fwd_f32_kernel<<<grid, kThreads, smem, stream>>>(

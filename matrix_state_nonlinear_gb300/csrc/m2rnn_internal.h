@@ -19,6 +19,11 @@ constexpr long long kWaitLimitCycles = 2000000000LL;
 // Limit used by the forced-timeout test hook (about 0.5 ms).
 constexpr long long kDebugWaitLimitCycles = 1000000LL;
 
+// Shared memory of a block.  Launchers of kernels without static arrays whose dynamic ones depend on the call's
+// sizes set this as the kernel's limit: set to the call's own size, it could lie too low for another thread's call
+// that is between its attribute and its launch.
+constexpr int kMostShared = 227 * 1024;
+
 // Unique id of the calling thread's current CUDA context (cuCtxGetId), or false when no
 // context is current yet.  Device addresses of module symbols are cached per context id,
 // so a device reset (which ends the context and may reload the module elsewhere) makes

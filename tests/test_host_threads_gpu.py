@@ -102,7 +102,31 @@ static Call norm_fp8(int f32, int D) {
   float* w = reinterpret_cast<float*>(t + (3 << 20));
   return [=](cudaStream_t at) { return m2rnn_add_rmsnorm_fp8(nullptr, 0, t, f32, D, w, 1e-5f, nullptr, q, (D + 15) / 16 * 16, scales, 4, D, at); };
 }
-//MORE
+// The recurrence, one step for one head: n is K, or K and V.
+static Call forward_f32(int n) {
+  float *t = reinterpret_cast<float*>(room(4 << 20)), *y = reinterpret_cast<float*>(room(1 << 20));
+  return [=](cudaStream_t at) { return m2rnn_forward_f32(t, t, t, t, t, t, t, t, nullptr, y, nullptr, 1, 1, 1, n, n, at); };
+}
+static Call backward_f32(int n) {
+  const size_t ws = m2rnn_backward_workspace_bytes(1, 1, 1, 1, n, n);
+  float *t = reinterpret_cast<float*>(room(4 << 20)), *g = reinterpret_cast<float*>(room(1 << 20));
+  char* s = room(ws);
+  return [=](cudaStream_t at) {
+    float* o[9];
+    for (int i = 0; i < 9; ++i) o[i] = g + i * 16384;
+    return m2rnn_backward_f32(t, t, t, t, t, t, t, t, nullptr, t, t, nullptr, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7], nullptr,
+                              1, 1, 1, 1, n, n, s, ws, at);
+  };
+}
+static Call forward_bf16(int variant, int V, int n) {
+  char *t = room(4 << 20), *y = room(1 << 20);
+  const uint16_t* u = reinterpret_cast<uint16_t*>(t);
+  const float* f = reinterpret_cast<float*>(t);
+  float* o = reinterpret_cast<float*>(y);
+  return [=](cudaStream_t at) {
+    return m2rnn_forward_bf16_variant(u, u, u, u, f, f, u, f, nullptr, o, nullptr, 1, 8, 1, n, V, variant, at);
+  };
+}
 int main(int argc, char** argv) {
   if (argc < 4) return 2;
   const int times = std::atoi(argv[2]);
@@ -113,7 +137,10 @@ int main(int argc, char** argv) {
     if (!std::strcmp(argv[1], "norm_backward f32")) calls.push_back(norm_backward(1, n));
     if (!std::strcmp(argv[1], "norm_fp8 bf16")) calls.push_back(norm_fp8(0, n));
     if (!std::strcmp(argv[1], "norm_fp8 f32")) calls.push_back(norm_fp8(1, n));
-    //CASES
+    if (!std::strcmp(argv[1], "forward f32")) calls.push_back(forward_f32(n));
+    if (!std::strcmp(argv[1], "backward f32")) calls.push_back(backward_f32(n));
+    for (int v = 1; v < 10; ++v)
+      if (m2rnn_variant_name(v) && !std::strcmp(argv[1], m2rnn_variant_name(v))) calls.push_back(forward_bf16(v, 64, n));
   }
   std::vector<std::thread> threads;
   std::vector<int> refused(calls.size());
@@ -153,7 +180,9 @@ def program(tmp_path_factory):
 @pytest.mark.parametrize("call,sizes", [
     ("norm_backward bf16", (2048, 4096, 1024)), ("norm_backward f32", (2047, 4095, 1023)),
     ("norm_fp8 bf16", (9001, 16001, 12345)), ("norm_fp8 f32", (9001, 16001, 12345)),
+    ("forward f32", (128, 96, 16)), ("backward f32", (128, 96, 120)), ("mma_sync_rowwarp", (128, 64, 96)),
+    ("mma_sync_pipelined", (64, 48, 32)), ("mma_sync_rows8", (64, 32)),
 ])
 def test_no_launch_is_refused(program, call, sizes):
-    r = subprocess.run([program, call, "20000", *map(str, sizes)], capture_output=True, text=True, timeout=120)
+    r = subprocess.run([program, call, "20000" if call.startswith("norm") else "8000", *map(str, sizes)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
