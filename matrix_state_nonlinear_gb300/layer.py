@@ -91,6 +91,7 @@ def _norm_args(x, residual, w, h):
     dev = _device(x)
     shape = x.shape
     D = shape[-1]
+    _sizes(D)
     if residual is None:
         kind = x.dtype
         if kind is not BF16 and kind is not F32:
@@ -167,6 +168,7 @@ def add_rmsnorm_backward(h, w, dout, dh=None, eps=1e-5, grads=None, workspace=No
     dev = _device(h)
     shape, kind = h.shape, h.dtype
     D = shape[-1]
+    _sizes(D)
     if kind not in (F32, BF16):
         raise TypeError(f"h: expected {F32} or {BF16}, got {kind}")
     hp = _ptr(h, "h", kind, shape, dev)
