@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) sum_squares_kernel(const __grid_cons
       uint32_t any = 0;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) any |= u[i].x | u[i].y | u[i].z | u[i].w;
-      if (any & 0x7fff7fffu)
+      if (any & (p.f32 ? 0x7fffffffu : 0x7fff7fffu))  // any value but zeros, whatever their signs
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) rare += squares64(u[i], p.f32);
     } else {  // hi + lo += s, exactly but for the rounding of lo
