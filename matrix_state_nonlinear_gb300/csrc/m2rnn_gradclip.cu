@@ -123,6 +123,15 @@ __device__ __noinline__ double squares64(uint4 u, bool f32) {
   }
   return s;
 }
+// 16 bytes of values times `by`, in 64 bits.
+__device__ __noinline__ uint4 times64(uint4 u, bool f32, double by) {
+  uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = f32 ? __float_as_uint((float)(__uint_as_float(v[i]) * by))
+               : pack_bf16x2((float)(bf16_lo(v[i]) * by), (float)(bf16_hi(v[i]) * by));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
 // Whether a sum of at most 64 squares is near the ends of float32's range: so large that a thread's sums (fewer than
 // 2^20 of them for the most values that a call takes) could leave it together, or so small that squares below
 // 2^-126 count.
@@ -247,7 +256,10 @@ __global__ void __launch_bounds__(kThreads)
   // A norm that is infinite or NaN clips nothing.
   const bool clips = n > max_norm && n < INFINITY;
   if (in_place && !clips) return;
-  const float by = clips ? (float)(max_norm / n) : 1.f;
+  const double factor = clips ? max_norm / n : 1.0;
+  // Below 2^-126 float32 would hold the factor with few bits or none, and values of up to 2^128 need them.
+  const bool small = factor < 0x1p-126;
+  const float by = (float)factor;
   const float2 b = make_float2(by, by);
   while (p.values > 0) {
     const Part q = stretch.next();
@@ -257,7 +269,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      if (p.f32) {
+      if (small) {
+        const uint4 y = times64(u[i], p.f32, factor);
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+      } else if (p.f32) {
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           const float2 y = mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), b);
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(kThreads)
     const long long inner = v.count * (p.f32 ? 4 : 8);
     for (long long i = threadIdx.x; i < p.values - inner; i += kThreads) {
       const long long at = i < v.head ? i : inner + i;
-      put(p, at, value(p, at) * by);
+      put(p, at, small ? (float)(value(p, at) * factor) : value(p, at) * by);
     }
     p = q, v = w;
 #pragma unroll

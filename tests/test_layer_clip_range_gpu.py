@@ -21,3 +21,21 @@ def test_values_of_one_bit(bit, sign):
         most = 2.0 ** -149
         check_clip(grads, most, out, pkg.clip_grad_norm(grads, most, out=out))
         assert torch.equal(pkg.grad_norm(grads), pkg.clip_grad_norm(grads, 1.0))
+
+
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("most", [1e-3, 1e-12, 1e-30])
+@pytest.mark.parametrize("off", [0, 1])
+def test_factors_below_the_range(kind, most, off):
+    """max_norm / norm below 2^-126, where the clipped values are ordinary numbers; in whole accesses and beside them."""
+    most = float(np.float32(most))
+    grads = tensors([9000, 37, 50001], 80, [kind] * 3, 1e37)
+    grads[0][5] = 3e38
+    grads = [g[off:] for g in grads]
+    before = [g.clone() for g in grads]
+    out = [torch.empty_like(g) for g in grads]
+    norm = pkg.clip_grad_norm(grads, most, out=out)
+    assert most / 1e40 < 2.0 ** -126
+    check_clip(before, most, out, norm)
+    pkg.clip_grad_norm(grads, most)
+    assert all(torch.equal(a, b) for a, b in zip(grads, out))
