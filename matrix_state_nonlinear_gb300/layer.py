@@ -48,7 +48,7 @@ def _rows(t, name, dtype, shape, dev):
 def _byte_rows(t, name, shape, dev):
     """The same for e4m3 values, whose rows start on 16-byte boundaries."""
     p, row = _rows(t, name, FP8, shape, dev)
-    if t.numel() == shape[-1]:  # a single row: nothing lies behind it
+    if t.numel() <= shape[-1]:  # a single row, or none: nothing lies behind it
         row = (shape[-1] + 15) // 16 * 16
     if p % 16 or row % 16:
         raise ValueError(f"{name}: rows must start on 16-byte boundaries; {row} bytes apart from address {p:#x} they "

@@ -30,3 +30,16 @@ def test_rows_that_do_not_fit_32_bits_are_refused(stub, name):  # noqa: F811
         ROWS[name](16)
     with pytest.raises(ValueError, match="2\\^31"):
         ROWS[name](WIDE)
+
+
+def test_no_tokens_in_8_bits(stub):  # noqa: F811
+    """8-bit rows of any width where there are none: their strides say nothing."""
+    w, sw = t(128, 1008, dtype=FP8), t(1, 8, dtype=E8M0)
+    for x, s in (((0, 1000), (0, 8)), ((3, 0, 1000), (3, 0, 8))):
+        w.shape, w.is_contiguous, w.stride = torch.Size((128, 1000)), lambda: False, lambda: (1008, 1)
+        with pytest.raises(Reached):
+            pkg.linear_fp8(t(*x, dtype=FP8), t(*s, dtype=E8M0), w, sw, out=t(*x[:-1], 128))
+    with pytest.raises(Reached):
+        pkg.quantise_fp8(t(0, 1000), out=t(0, 1000, dtype=FP8), scales=t(0, 8, dtype=E8M0))
+    with pytest.raises(Reached):
+        pkg.add_rmsnorm_fp8(t(0, 1000), None, t(1000, dtype=F32), out=t(0, 1000, dtype=FP8), scales=t(0, 8, dtype=E8M0))
