@@ -285,7 +285,8 @@ _IS_F32 = {F32: 1, BF16: 0}
 
 
 def _gradients(grads, out, max_norm, norm, workspace):
-    grads = list(grads.values()) if isinstance(grads, dict) else list(grads)
+    names = grads if isinstance(grads, dict) else None
+    grads = list(grads.values()) if names is not None else list(grads)
     if not grads:
         raise ValueError("grads: at least one tensor")
     dev = _device(grads[0])
@@ -306,7 +307,12 @@ def _gradients(grads, out, max_norm, norm, workspace):
     elif out is _NORM_ONLY:
         to = None
     else:
-        out = list(out.values()) if isinstance(out, dict) else list(out)
+        if isinstance(out, dict) and names is not None:
+            if out.keys() != names.keys():
+                raise ValueError(f"out: {sorted(out.keys() ^ names.keys(), key=str)} on one side only")
+            out = [out[name] for name in names]
+        else:
+            out = list(out.values()) if isinstance(out, dict) else list(out)
         if len(out) != n:
             raise ValueError(f"out: {len(out)} tensors for {n} gradients")
         to = array("Q", [_ptr(o, "out", t.dtype, t.shape, dev) for o, t in zip(out, grads)])
@@ -338,6 +344,7 @@ def grad_norm(grads, norm=None, workspace=None):
 @_on_stream
 def clip_grad_norm(grads, max_norm, out=None, norm=None, workspace=None):
     """Scales grads (a sequence or dict of contiguous float32 and bf16 tensors, none of which share memory)
-    by min(1, max_norm / norm), in place, or into the tensors ``out``.  Returns the norm before that, a
-    float32 scalar on the device.  Where a value is infinite or NaN the norm is, and nothing is scaled."""
+    by min(1, max_norm / norm), in place, or into the tensors ``out`` (in the same order; where both are dicts,
+    those of the same names).  Returns the norm before that, a float32 scalar on the device.  Where a value is
+    infinite or NaN the norm is, and nothing is scaled."""
     return _gradients(grads, out, max_norm, norm, workspace)
