@@ -47,7 +47,7 @@ class Block:
                     H=torch.zeros(B, self.N, self.K, self.V, device=dev))
 
     def quantise(self):
-        """From now on prompts and tokens go through 8-bit copies of the projections."""
+        """From now on prompts and tokens go through 8-bit copies of the projections; training does not."""
         self.w8 = {n: m2.quantise_weight_fp8(self.p[n]) for n in ("w_in", "w_out")}
         return self
 
@@ -78,12 +78,17 @@ class Block:
 
     def prompt(self, x, cache):
         """x [B, T, D] bf16 -> [B, T, D]; the cache moves on by T tokens, in place."""
+        return self._out(self._mix(*self._project(x), cache))
+
+    def forward(self, x, cache):
+        """``prompt`` as ``train`` computes it: through the projections that it returns gradients of."""
+        return self._mix(*self._split(x @ self.p["w_in"].T), cache) @ self.p["w_out"].T
+
+    def _mix(self, gate, u, a, cache):
         p = self.p
-        gate, u, a = self._project(x)
         c, _ = m2.conv_silu_window(u, p["conv_w"], p["conv_b"], cache["window"], window_out=cache["window"])
         y, _ = m2.ssm_forward(self._scan_inputs(c, a, cache["H"]), H_T=cache["H"])
-        o = m2.gate_groupnorm(y.flatten(2), gate.contiguous(), p["norm_w"], p["norm_b"], self.N)
-        return self._out(o)
+        return m2.gate_groupnorm(y.flatten(2), gate.contiguous(), p["norm_w"], p["norm_b"], self.N)
 
     def token(self, x, cache):
         """x [B, D] bf16 -> [B, D]; the cache moves on by one token, in place."""
@@ -163,7 +168,7 @@ class Stack:
         for b, w in zip(self.blocks, self.norms):
             n, h = m2.add_rmsnorm(y, h, w)
             kept.append((n, h))
-            y = b.prompt(n, b.cache(x.shape[0]))
+            y = b.forward(n, b.cache(x.shape[0]))
         out, h = m2.add_rmsnorm(y, h, self.norms[-1])
         d = m2.add_rmsnorm_backward(h, self.norms[-1], dout)
         grads = {f"norm{len(self.blocks)}": d["dw"]}
