@@ -20,6 +20,8 @@ m2rnn_status row_sizes(long long rows, int D) {
   return D > kNormMaxRow ? M2RNN_ERR_UNSUPPORTED : M2RNN_OK;
 }
 
+size_t size_of(int f32) { return f32 ? 4 : 2; }
+
 // Rows of 8-bit values that start on 16-byte boundaries.
 bool byte_rows(const void* p, long long row, int width) {
   return aligned_to(p, 16) && row % 16 == 0 && row >= width;
@@ -52,6 +54,9 @@ static m2rnn_status add_norm_problem(const uint16_t* x, long long x_row, const v
   if (st != M2RNN_OK) return st;
   if (!(eps >= 0.f) || !w || x_row < 0 || stream_row < 0) return M2RNN_ERR_INVALID_ARG;
   if (rows > 0 && (!stream_in || (x && !h))) return M2RNN_ERR_INVALID_ARG;
+  const size_t size = size_of(stream_f32);
+  if (!aligned_to(x, 2) || !aligned_to(stream_in, size) || !aligned_to(w, 4) || !aligned_to(h, size))
+    return M2RNN_ERR_INVALID_ARG;
   *p = AddNormProblem{x, stream_in, x_row, stream_row, stream_f32 != 0, w, eps, h, rows, D};
   return M2RNN_OK;
 }
@@ -62,7 +67,7 @@ m2rnn_status m2rnn_add_rmsnorm(const uint16_t* x, long long x_row, const void* s
   AddNormProblem p;
   const m2rnn_status st = add_norm_problem(x, x_row, stream_in, stream_f32, stream_row, w, eps, h, rows, D, &p);
   if (st != M2RNN_OK || rows == 0) return st;
-  if (!out) return M2RNN_ERR_INVALID_ARG;
+  if (!out || !aligned_to(out, 2)) return M2RNN_ERR_INVALID_ARG;
   return done(launch_add_rmsnorm(p, out, static_cast<cudaStream_t>(stream)));
 }
 
@@ -89,6 +94,10 @@ m2rnn_status m2rnn_add_rmsnorm_backward(const void* h, int stream_f32, const flo
   if (rows > 0 && (!h || !dout || !workspace || (!dx && !dresidual))) return M2RNN_ERR_INVALID_ARG;
   if (!aligned_to(workspace, 16) || workspace_bytes < m2rnn_add_rmsnorm_backward_workspace_bytes(rows, D))
     return M2RNN_ERR_INVALID_ARG;
+  const size_t size = size_of(stream_f32);
+  if (!aligned_to(h, size) || !aligned_to(w, 4) || !aligned_to(dout, 2) || !aligned_to(dh, size) || !aligned_to(dx, 2) ||
+      !aligned_to(dresidual, size) || !aligned_to(dw, 4))
+    return M2RNN_ERR_INVALID_ARG;
   const AddNormBackwardProblem p{h,  stream_f32 != 0, w, eps, dout, dh, dx, dresidual, dw, rows,
                                  D,  static_cast<float*>(workspace)};
   return done(launch_add_rmsnorm_backward(p, static_cast<cudaStream_t>(stream)));
@@ -99,7 +108,7 @@ m2rnn_status m2rnn_quantise_fp8(const void* x, int x_f32, long long x_row, uint8
   if (rows < 0 || D < 1 || x_row < 0) return M2RNN_ERR_INVALID_ARG;
   if ((rows + 1) > 0x7ffffff0LL * 16 / scale_blocks(D)) return M2RNN_ERR_UNSUPPORTED;
   if (rows == 0) return M2RNN_OK;
-  if (!x || !q || !scales || !byte_rows(q, q_row, D)) return M2RNN_ERR_INVALID_ARG;
+  if (!x || !aligned_to(x, size_of(x_f32)) || !q || !scales || !byte_rows(q, q_row, D)) return M2RNN_ERR_INVALID_ARG;
   return done(launch_quantise_rows(x, x_f32 != 0, x_row, q, q_row, scales, rows, D, static_cast<cudaStream_t>(stream)));
 }
 
@@ -107,26 +116,27 @@ m2rnn_status m2rnn_quantise_weight_fp8(const void* w, int w_f32, long long w_row
                                        uint8_t* scales, int N, int K, void* stream) {
   if (N < 1 || K < 1 || w_row < 0) return M2RNN_ERR_INVALID_ARG;
   if ((long long)scale_blocks(N) * scale_blocks(K) > 0x7fffffffLL) return M2RNN_ERR_UNSUPPORTED;
-  if (!w || !q || !scales || !byte_rows(q, q_row, K)) return M2RNN_ERR_INVALID_ARG;
+  if (!w || !aligned_to(w, size_of(w_f32)) || !q || !scales || !byte_rows(q, q_row, K)) return M2RNN_ERR_INVALID_ARG;
   return done(launch_quantise_weight(w, w_f32 != 0, w_row, q, q_row, scales, N, K, static_cast<cudaStream_t>(stream)));
 }
 
 // Sizes of a product and its weights.  Rows are tensor-map coordinates and the tiles, of 128 x 16 at the
 // least, a grid, both in 31 bits; a tensor map's stride has 40.
 static m2rnn_status linear_checks(const uint8_t* w, long long w_row, const uint8_t* w_scales, const void* out,
-                                  long long M, int N, int K) {
+                                  int out_f32, long long M, int N, int K) {
   if (M < 0 || N < 1 || K < 1) return M2RNN_ERR_INVALID_ARG;
   if (M > 0x7fffff00LL || N > 0x7fffff00 || K > 0x7fffff00 || ((M + 15) / 16) * ((N + 127LL) / 128) > 0x7fffffffLL)
     return M2RNN_ERR_UNSUPPORTED;
   if (M == 0) return M2RNN_OK;
-  if (!w || !w_scales || !out || !byte_rows(w, w_row, K)) return M2RNN_ERR_INVALID_ARG;
+  if (!w || !w_scales || !out || !aligned_to(out, size_of(out_f32)) || !byte_rows(w, w_row, K))
+    return M2RNN_ERR_INVALID_ARG;
   return w_row >= 1LL << 40 ? M2RNN_ERR_UNSUPPORTED : M2RNN_OK;
 }
 
 m2rnn_status m2rnn_linear_fp8(const uint8_t* x, long long x_row, const uint8_t* x_scales, const uint8_t* w,
                               long long w_row, const uint8_t* w_scales, void* out, int out_f32, long long M, int N,
                               int K, void* stream) {
-  const m2rnn_status st = linear_checks(w, w_row, w_scales, out, M, N, K);
+  const m2rnn_status st = linear_checks(w, w_row, w_scales, out, out_f32, M, N, K);
   if (st != M2RNN_OK || M == 0) return st;
   if (!x || !x_scales || !byte_rows(x, x_row, K)) return M2RNN_ERR_INVALID_ARG;
   if (x_row >= 1LL << 40) return M2RNN_ERR_UNSUPPORTED;
@@ -147,9 +157,9 @@ size_t m2rnn_linear_quantise_workspace_bytes(int x_f32, long long M, int K) {
 m2rnn_status m2rnn_linear_quantise_fp8(const void* x, int x_f32, long long x_row, const uint8_t* w, long long w_row,
                                        const uint8_t* w_scales, void* out, int out_f32, long long M, int N, int K,
                                        void* workspace, size_t workspace_bytes, void* stream) {
-  m2rnn_status st = linear_checks(w, w_row, w_scales, out, M, N, K);
+  m2rnn_status st = linear_checks(w, w_row, w_scales, out, out_f32, M, N, K);
   if (st != M2RNN_OK || M == 0) return st;
-  if (!x || x_row < 0) return M2RNN_ERR_INVALID_ARG;
+  if (!x || x_row < 0 || !aligned_to(x, size_of(x_f32))) return M2RNN_ERR_INVALID_ARG;
   const size_t need = m2rnn_linear_quantise_workspace_bytes(x_f32, M, K);
   if (need > 0 && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < need)) return M2RNN_ERR_INVALID_ARG;
   int* status = device_status();
@@ -180,7 +190,7 @@ m2rnn_status m2rnn_clip_grad_norm(const void* const* grads, void* const* out, co
     return M2RNN_ERR_INVALID_ARG;
   long long total = 0;
   for (int i = 0; i < count; ++i) {
-    const size_t size = is_f32[i] ? 4 : 2;
+    const size_t size = size_of(is_f32[i]);
     if (values[i] < 0 || (values[i] > 0 && (!grads[i] || (out && !out[i])))) return M2RNN_ERR_INVALID_ARG;
     if (values[i] > 0 && (!aligned_to(grads[i], size) || (out && !aligned_to(out[i], size))))
       return M2RNN_ERR_INVALID_ARG;
