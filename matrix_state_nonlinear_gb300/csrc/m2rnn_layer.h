@@ -15,7 +15,8 @@
 namespace m2rnn {
 
 constexpr int kScaleBlock = 128;  // values that share a scale
-__host__ __device__ inline int scale_blocks(int n) { return (n + kScaleBlock - 1) / kScaleBlock; }
+// Of n >= 1 values, up to 2^31 - 1 of them.
+__host__ __device__ inline int scale_blocks(int n) { return (n - 1) / kScaleBlock + 1; }
 
 constexpr int kNormMaxRow = 16384;  // channels of a row of the norm
 
