@@ -183,7 +183,7 @@ size_t m2rnn_grad_norm_workspace_bytes(int count) { return count >= 0 ? grad_nor
 m2rnn_status m2rnn_clip_grad_norm(const void* const* grads, void* const* out, const long long* values,
                                   const unsigned char* is_f32, int count, float max_norm, float* norm, void* workspace,
                                   size_t workspace_bytes, void* stream) {
-  if (count < 0 || !norm) return M2RNN_ERR_INVALID_ARG;
+  if (count < 0 || !norm || !aligned_to(norm, 4)) return M2RNN_ERR_INVALID_ARG;
   if (out && !(max_norm >= 0.f && max_norm <= 3.402823466e38f)) return M2RNN_ERR_INVALID_ARG;
   if (count > 0 && (!grads || !values || !is_f32 || !workspace || !aligned_to(workspace, 16) ||
                     workspace_bytes < m2rnn_grad_norm_workspace_bytes(count)))

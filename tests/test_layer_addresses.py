@@ -1,5 +1,7 @@
 """C entries of the layer refuse addresses off their type's boundary, which a kernel would fault on.  No GPU: the
 addresses are never read."""
+import ctypes
+
 import pytest
 
 import __graft_entry__
@@ -47,10 +49,15 @@ def linear_quantise(lib, f32, **at):
     return lib.m2rnn_linear_quantise_fp8(a["x"], f32, 8, A, 16, A, a["out"], f32, 4, 8, 8, A, 1 << 20, None)
 
 
+def clip(lib, f32, **at):
+    kept = [ctypes.c_uint64(A), ctypes.c_uint64(A), ctypes.c_longlong(4), ctypes.c_ubyte(f32)]
+    return lib.m2rnn_clip_grad_norm(*map(ctypes.addressof, kept), 1, 1.0, at["norm"], A, 1 << 20, None)
+
+
 WIDE, HALF, FLOAT = "of the stream's type", "bf16", "float32"
 CALLS = [(norm, dict(x=HALF, stream=WIDE, w=FLOAT, h=WIDE, out=HALF)), (norm_fp8, dict(x=HALF, stream=WIDE, w=FLOAT, h=WIDE)),
          (backward, dict(h=WIDE, w=FLOAT, dout=HALF, dh=WIDE, dx=HALF, dresidual=WIDE, dw=FLOAT)), (quantise, dict(x=WIDE)),
-         (quantise_weight, dict(w=WIDE)), (linear, dict(out=WIDE)), (linear_quantise, dict(x=WIDE, out=WIDE))]
+         (quantise_weight, dict(w=WIDE)), (clip, dict(norm=FLOAT)), (linear, dict(out=WIDE)), (linear_quantise, dict(x=WIDE, out=WIDE))]
 
 
 @pytest.mark.parametrize("f32", [0, 1])
