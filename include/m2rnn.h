@@ -467,7 +467,8 @@ m2rnn_status m2rnn_gate_groupnorm_backward(const void* y, int y_f32, const uint1
  * x bf16; stream_in and h bf16 or float32 (stream_f32 != 0); w [D] float32.  x_row and stream_row are the
  * elements from one row to the next; h and out [rows, D] are dense.  h may be NULL without x (not written)
  * and may be stream_in itself (in place) where that is dense.  The norm is taken of the rounded h, in
- * float32: |h| above 1e19 overflows its square (out is 0 there).  D <= 16384 (UNSUPPORTED above).
+ * float32: |h| above 1e19 overflows its square (out is 0 there), and with eps = 0 a row whose values are all below
+ * 1e-19 loses digits of their squares.  D <= 16384 (UNSUPPORTED above).
  * A NaN gives NaN in all of its row, an infinity in its channel (in 8 bits in its 128) and zeros in the rest of
  * the row; other rows are untouched.  16-byte aligned pointers run on 16-byte accesses where D % 8 == 0 and rows
  * are aligned so, or where the rows' distances are D or a multiple of 8 more.  The order of a row's sum depends on
@@ -507,8 +508,9 @@ m2rnn_status m2rnn_add_rmsnorm_backward(const void* h, int stream_f32, const flo
  * m2rnn_linear_fp8: out[m, n] = sum_k x[m, k] w[n, k] of such values, x [M, K] with a scale for each 128
  *   of a row, w [N, K] with one for each 128 x 128 block; out [M, N] bf16 or float32 (out_f32 != 0), dense.
  *   Sums are float32 on the tensor cores.  A NaN of x spoils its row of out, one of w its column; a scale
- *   of w that is NaN spoils the columns of its block.  Fastest with rows of x and w on 128-byte boundaries
- *   and rows of out that are whole multiples of 32 bytes at a 32-byte aligned address.
+ *   of w that is NaN spoils the columns of its block.  A form for serving: it has no gradient.  Fastest with
+ *   rows of x and w on 128-byte boundaries and rows of out that are whole multiples of 32 bytes at a 32-byte
+ *   aligned address.
  * m2rnn_linear_quantise_fp8: the same with x [M, K] bf16 or float32 (x_f32 != 0), x_row elements from row to
  *   row, as m2rnn_quantise_fp8 makes it 8 bits; up to 16 rows of bf16 within the product's own launch.  The
  *   workspace (16-byte aligned; NULL where its size is 0) is overwritten.

@@ -12,8 +12,8 @@
 // 128 channels of a scale); otherwise they lie a row's threads apart, so that a warp's accesses are still of
 // consecutive values.
 // Measured: 65536 x 2048, bf16: forward 154 us (7.0 TB/s, 1.03 of a copy's rate), backward 171 us with the sums;
-// 8191 x 4096 in 8 bits on a float32 stream: 56 us (6.6 TB/s); 65536 rows of 1001: 102 and 107 us, of 1000 77 and
-// 105.
+// 8191 x 4096 in 8 bits on a float32 stream: 56 us (6.6 TB/s); 65536 bf16 rows of 1001: 102 and 107 us, of 1000 77
+// and 105; backward of wide rows, 3000 x 9001: 108 us (bf16) and 140 (float32).
 #include "m2rnn_layer.h"
 #include "ptx_util.cuh"
 
@@ -140,8 +140,8 @@ struct Raw8 {
     }
   }
 };
-// The weights of chunk r.  kShift: of two chunks of w, by the row's shift (3000 x 9001, backward: 109 us; moved by
-// powers of two, 121).
+// The weights of chunk r.  kShift: of two chunks of w, by the row's shift (3000 x 9001, bf16, backward: 109 us; moved
+// by powers of two, 121).
 template <int A>
 __device__ __forceinline__ void load_weight(const float* w, int r, const Span& d, int D, float2 (&f)[4]) {
   if constexpr (A != kShift) {
@@ -244,7 +244,8 @@ __device__ __forceinline__ void store_fp8(const float2 (&v)[4], float inv, int r
   }
 }
 // kShift in 8 bits: a row's values pass through shared memory, as scales and q follow the row.  Value c is at c +
-// c / 32, so that threads eight apart meet different banks (65536 x 1001, bf16: 108 us; value by value 196).
+// c / 32, so that threads eight apart meet different banks (65536 x 1001, bf16 with residual: 108 us; value by value
+// 196).
 __host__ __device__ constexpr int place_of(int c) { return c + c / 32; }
 // |values| as bits, which order them and put NaN above all.
 __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }

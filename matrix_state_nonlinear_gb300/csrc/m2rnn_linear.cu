@@ -13,7 +13,8 @@
 // barrier of the cluster, nothing read from afar (half a microsecond less).  Up to 16 tokens of bf16 are
 // quantised on the way in, by the warps that later write the results and four more (64 tokens would take 26 us
 // that way, 13 with a launch before, 4096 x 8192: every block reads all rows).
-// Measured, 64 x 4096 x 8192: 11.7 us (3.0 TB/s of weights and tokens); 16 x 2048 x 4384: 5.0 us.
+// Measured, weights from memory: 64 x 4096 x 8192: 11.3 us (3.1 TB/s of weights and tokens), 11.7 with the quantising;
+// 16 x 2048 x 4384: 6.8 us with it (5.3 alone with the weights in L2).
 #include "m2rnn_fp8_tc.cuh"
 
 namespace m2rnn {

@@ -2,7 +2,9 @@
 // blocks of 128 along a row, weights in blocks of 128 x 128.  Memory-bound: 16 neighbouring threads take
 // 128 values of a row, eight consecutive ones each, or, where rows do not start on 16-byte boundaries, a warp
 // does, its lanes on neighbouring values.
-// Measured, 16384 x 4096 bf16: 32 us (6.3 TB/s), 16384 x 4097: 61 us.
+// Measured, 16384 x 4096 bf16: 32 us (6.3 TB/s), 16384 x 4097: 60 us, bound by instructions there (a value a load
+// and a store); weights 8192 x 4096: float32 29 us (5.8 TB/s), bf16 46, where 90 registers leave room for 16 warps an
+// SM and they wait for memory.
 #include "m2rnn_layer.h"
 #include "ptx_util.cuh"
 

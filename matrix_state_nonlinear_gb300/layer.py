@@ -248,7 +248,8 @@ def quantise_weight_fp8(w, out=None, scales=None):
 def linear_fp8(x, x_scales, w, w_scales, out=None, out_dtype=BF16, workspace=None):
     """Projection in 8 bits: out = x w^T with float32 sums.  x [..., K] and x_scales from
     ``add_rmsnorm_fp8`` or ``quantise_fp8``, or x bf16 or float32 with x_scales None (quantised here, the same
-    values); w [N, K] and w_scales from ``quantise_weight_fp8``.  Returns out [..., N], bf16 or float32."""
+    values); w [N, K] and w_scales from ``quantise_weight_fp8``.  For serving: it has no gradient.  Returns out
+    [..., N], bf16 or float32."""
     dev = _device(x)
     shape = x.shape
     K = shape[-1]
